@@ -438,6 +438,156 @@ oscar_status oscar_paged_decode_attention(const oscar_paged_cache* c, const floa
                                           int num_splits, void* workspace, size_t ws_bytes,
                                           void* stream);
 
+/*
+ * ----------------------------------------------------------------------
+ * The 16-bit cache: unquantised keys and values (bf16 or fp16), for the
+ * layers that stay at full precision and for a prompt before it is packed.
+ * The pages have no counterpart; head_dim, the 32-token page, the block
+ * table and the grouping of query heads are those of the packed caches.
+ *
+ *  paged       (block_table set): k, v [n_pages][Hkv][32][128], weight
+ *              [n_pages][Hkv][32]; logical block j of sequence b (its tokens
+ *              32j .. 32j+31) is page block_table[b*max_blocks + j].  T_cap is
+ *              ignored.  Sequences may share pages for reading; a page whose
+ *              weight a call adds to belongs to one sequence.
+ *  contiguous  (block_table NULL): k, v [B][Hkv][T_cap][128] (the layout that
+ *              oscar_prefill_kv reads), weight [B][Hkv][T_cap].  max_blocks
+ *              and n_pages are ignored.
+ *  n_tok[b]    the tokens that sequence b holds; device memory.
+ *  weight      optional (NULL): the attention weight that each stored token
+ *              of each KV head has gathered, float32.
+ * k, v and weight are 16-byte aligned, arrays of 32-bit numbers 4-byte.  A
+ * cache has fewer than 2^31 - 128 rows of 128 elements and a sequence room for
+ * fewer tokens than that (else OSCAR_ERR_UNSUPPORTED).
+ *
+ * Ragged batches.  New tokens and their queries lie behind one another,
+ * token-major: sequence b's are rows start[b] .. start[b+1] - 1 of a tensor
+ * of `total` rows [total][heads][128], whose rows are `stride` elements apart
+ * (a multiple of 8; heads*128 when dense, more for a slice of a fused
+ * projection).  start: device int32 [B+1], not decreasing.  Rows that belong
+ * to no sequence are neither read nor written.
+ *
+ * Visibility.  A query at position p sees the tokens j <= p with
+ * window == 0, or j > p - window, or j < n_sink.  Tokens that a query does
+ * not see do not reach its output, whatever they hold (NaN, infinity).
+ *
+ * The device checks lengths (n_tok[b] in [0, capacity], and <= the host's
+ * max_tok where a call takes it), start and page ids: a bad one skips the
+ * access and is recorded in the status word (oscar_device_status); what the
+ * call writes for that sequence is then unspecified, but stays within the
+ * sequence's own rows.
+ * ----------------------------------------------------------------------
+ */
+#define OSCAR_KV16_BF16 0
+#define OSCAR_KV16_FP16 1
+
+typedef struct {
+  int B, Hkv;
+  int max_blocks;              /* paged: row length of block_table */
+  int n_pages;                 /* paged: pages in the pool */
+  int T_cap;                   /* contiguous: tokens per row */
+  int dtype;                   /* OSCAR_KV16_BF16 or OSCAR_KV16_FP16 */
+  uint16_t* k;
+  uint16_t* v;
+  float* weight;
+  const int32_t* block_table;  /* device [B][max_blocks] page ids (B * max_blocks < 2^31) */
+  int32_t* n_tok;              /* device [B] */
+} oscar_kv16_cache;
+
+/*
+ * Writes sequence b's new tokens to its positions pos0[b], pos0[b] + 1, ...
+ * and sets n_tok[b] = pos0[b] + their number (for every b, those without new
+ * tokens too): pos0[b] = its length appends, less takes back the tokens from
+ * there on (rejected drafts).  The written tokens' weights become 0.
+ *  k_new, v_new  [total][Hkv][128] in the cache's type, rows k_stride and
+ *                v_stride elements apart
+ *  pos0          device int32 [B], not c->n_tok (which the call writes)
+ * A sequence whose tokens would pass its capacity is not written and keeps its
+ * length (recorded in the status word).
+ */
+oscar_status oscar_kv16_write(const oscar_kv16_cache* c, const uint16_t* k_new,
+                              long long k_stride, const uint16_t* v_new, long long v_stride,
+                              const int32_t* start, const int32_t* pos0, int total, void* stream);
+
+/*
+ * Attention of every sequence's newest tokens: its queries start[b] ..
+ * start[b+1] - 1 are the last of its n_tok[b] tokens (already written), so
+ * query i stands at position n_tok[b] - (start[b+1] - start[b]) + i.
+ *  q    [total][Hq][128] in the cache's type, rows q_stride elements apart
+ *  out  [total][Hq][128], dense, the same type:
+ *       sum_j softmax_j(softmax_scale * q.k_j) v_j over the visible tokens
+ *  lse  float32 [total][Hq] or NULL: log sum_j exp(softmax_scale * q.k_j)
+ *       (a query that sees nothing: out 0, lse -inf)
+ *  max_tok  host bound on the n_tok[b]; plans the split of long caches over
+ *       several blocks when there are few queries
+ * window >= 0, n_sink >= 0.  workspace: oscar_kv16_attention_workspace_bytes
+ * of device memory (no initialisation; NULL if that is 0).  Calls that use
+ * one workspace must not overlap on the GPU.
+ */
+oscar_status oscar_kv16_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                  long long q_stride, const int32_t* start, int total, int Hq,
+                                  float softmax_scale, int max_tok, int window, int n_sink,
+                                  uint16_t* out, float* lse, void* workspace, size_t ws_bytes,
+                                  void* stream);
+size_t oscar_kv16_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, int total,
+                                            int max_tok, int window, int n_sink);
+
+/*
+ * The same for one query per sequence, that of its newest token (position
+ * n_tok[b] - 1), with the work split evenly over the tokens of the whole
+ * batch and joined: one launch (accumulate: two).
+ *  q    [B][Hq][128], rows q_stride elements apart;  out [B][Hq][128], dense
+ *       (a sequence without tokens gives zeros)
+ *  accumulate  1 adds to weight[j] of every visible token j of KV head h the
+ *       softmax probabilities it got from h's query heads (c->weight set)
+ * workspace: a decode workspace (see oscar_decode_attention: its header of
+ * OSCAR_DECODE_WS_HEADER_BYTES is zero before the first use and after every
+ * call) of oscar_kv16_decode_workspace_bytes bytes.  B*Hkv <= 65536,
+ * B <= 8192 and B*Hkv*ceil(max_tok/32) < 2^31 (else OSCAR_ERR_UNSUPPORTED).
+ */
+oscar_status oscar_kv16_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                         long long q_stride, int Hq, float softmax_scale,
+                                         int max_tok, int window, int n_sink, int accumulate,
+                                         uint16_t* out, void* workspace, size_t ws_bytes,
+                                         void* stream);
+size_t oscar_kv16_decode_workspace_bytes(const oscar_kv16_cache* c, int Hq, int max_tok,
+                                         int window, int n_sink, int accumulate);
+
+/*
+ * Adds to weight[j] of KV head h the probabilities that token j got from the
+ * last n_obs queries (0: all) of its sequence under h's query heads:
+ * weight[j] += sum_i exp(softmax_scale * q_i.k_j - lse_i).  q, start, total,
+ * the positions and the visibility are those of oscar_kv16_attention, lse is
+ * what it wrote.  No workspace; one order of summation, so the same inputs
+ * give the same bits.
+ */
+oscar_status oscar_kv16_accumulate(const oscar_kv16_cache* c, const uint16_t* q,
+                                   long long q_stride, const float* lse, const int32_t* start,
+                                   int total, int Hq, float softmax_scale, int max_tok,
+                                   int window, int n_sink, int n_obs, void* stream);
+
+/*
+ * Eviction by accumulated weight: for every (sequence, KV head) the first
+ * keep_first tokens, the last keep_recent and, of those between, the keep_top
+ * with the largest src->weight (equal weights: the lower position; a NaN
+ * counts as larger than any number) go to dst's positions 0, 1, ... in order
+ * of position, keys, values and (if dst->weight is set) weights; then
+ * dst->n_tok[b] = min(n_tok[b], keep), keep = keep_first + keep_recent +
+ * keep_top.  A sequence of at most keep tokens is copied whole.  src is left
+ * as it was.  Afterwards a token's position is its place among the kept ones.
+ *  kept  int32 [B][Hkv][keep] or NULL: the kept tokens' positions in src,
+ *        rising; -1 behind the last
+ *  max_tok  host bound on src's n_tok[b]
+ * dst has the B, Hkv and type of src, room for keep tokens a sequence (else
+ * OSCAR_ERR_CAPACITY), its blocks mapped, and no memory in common with src.
+ * workspace: oscar_kv16_evict_workspace_bytes of device memory.
+ */
+oscar_status oscar_kv16_evict(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
+                              int max_tok, int keep_first, int keep_recent, int keep_top,
+                              int32_t* kept, void* workspace, size_t ws_bytes, void* stream);
+size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok, int keep_first,
+                                        int keep_recent, int keep_top);
+
 /* Self-test of the bounded waits (failure detection; the pages have no
  * counterpart).  One CTA waits on an mbarrier that nothing arrives at,
  * gives up after `iterations` polls, records the wait-timeout bit in the

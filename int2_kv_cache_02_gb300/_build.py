@@ -20,7 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 
 LIBS = {
     "liboscar.so": ["rotate.cu", "quantize.cu", "decode_int2.cu", "decode_int2_pad.cu", "decode_bf16.cu",
-                    "combine.cu", "api.cu", "decode_static.cu"],
+                    "combine.cu", "api.cu", "decode_static.cu", "kv16_api.cu", "kv16_write.cu",
+                    "kv16_attention.cu", "kv16_decode.cu", "kv16_accumulate.cu", "kv16_evict.cu"],
     "liboscar_synth.so": ["synth.cu"],
 }
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -74,7 +75,7 @@ def build(force: bool = False, verbose: bool = False) -> dict[str, str]:
         paths[lib] = target
         if not force and not _stale(target, deps):
             continue
-        with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        with ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
             results = list(ex.map(_compile, srcs))
         with open(os.path.join(BUILD, lib + ".ptxas.log"), "w") as f:
             for (obj, log), src in zip(results, srcs):

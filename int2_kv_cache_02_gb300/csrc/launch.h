@@ -194,6 +194,45 @@ cudaError_t launch_prefill_kv(const uint16_t* k, const uint16_t* v, int in_T, in
                               int Hkv, int T_cap, int p0, int group, int bits, KeyScale ks,
                               uint8_t* packed, cudaStream_t s);
 
+// The 16-bit cache (oscar_kv16_cache) as the kernels take it.
+struct Kv16 {
+  uint16_t* k;
+  uint16_t* v;
+  float* weight;
+  const int32_t* table;   // nullptr: contiguous rows of T_cap tokens
+  int32_t* n_tok;
+  unsigned* status;
+  int B, Hkv, max_blocks, n_pages, T_cap;
+  int cap;                // tokens a sequence can hold
+  bool half;              // fp16 (else bf16)
+};
+// Queries of a call over a 16-bit cache: rows [start[b], start[b+1]) of q
+// belong to sequence b, or row b if start is nullptr (one query each).
+struct Kv16Query {
+  const uint16_t* q;
+  long long stride;       // elements between rows
+  const int32_t* start;
+  int total, Hq, max_tok, window, n_sink;
+  float scale_log2;       // softmax_scale * log2(e)
+};
+cudaError_t launch_kv16_write(const Kv16& c, const uint16_t* k_new, long long k_stride,
+                              const uint16_t* v_new, long long v_stride, const int32_t* start,
+                              const int32_t* pos0, int total, cudaStream_t s);
+// *launches: the kernels launched; kv16_*_ws_bytes: the workspace needed.
+cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* out, float* lse,
+                                  void* ws, int* launches, cudaStream_t s);
+size_t kv16_attention_ws_bytes(const Kv16& c, int Hq, int total, int max_tok, int window,
+                               int n_sink);
+cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
+                               void* ws, int* launches, cudaStream_t s);
+size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int n_sink,
+                            bool accumulate);
+cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const float* lse, int n_obs,
+                                   cudaStream_t s);
+cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int keep_first,
+                              int keep_recent, int keep_top, int32_t* kept, void* ws,
+                              cudaStream_t s);
+
 // One CTA polls an mbarrier nothing arrives at, `iterations` times, then
 // records kDevErrWaitTimeout in *status (self-test of the bounded waits).
 cudaError_t launch_wait_timeout_selftest(unsigned* status, unsigned iterations, cudaStream_t s);

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from ctypes import POINTER, c_float, c_int, c_size_t, c_uint, c_ulonglong, c_void_p
+from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_ulonglong, c_void_p
 
 import torch
 
@@ -48,6 +48,13 @@ class OscarPagedCacheStruct(ctypes.Structure):
                 ("bits", c_int)]
 
 
+class OscarKV16CacheStruct(ctypes.Structure):
+    _fields_ = [("B", c_int), ("Hkv", c_int), ("max_blocks", c_int), ("n_pages", c_int),
+                ("T_cap", c_int), ("dtype", c_int),
+                ("k", c_void_p), ("v", c_void_p), ("weight", c_void_p),
+                ("block_table", c_void_p), ("n_tok", c_void_p)]
+
+
 BLOCK_BYTES = 2752
 BLOCK_BYTES_INT4 = 4800
 # byte ranges of the fields of one 32-token block record (include/oscar.h)
@@ -59,6 +66,7 @@ RECORD_FIELDS_INT4 = {"k_codes": (0, 2048), "v_codes": (2048, 4096), "k_scale": 
                       "k_zero": (4352, 4608), "k_norm": (4608, 4672), "v_scale": (4672, 4736),
                       "v_zero": (4736, 4800)}
 PER_TOKEN_FIELDS = ("k_norm", "v_scale", "v_zero")
+_KV16_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def record_bytes(bits: int = 2) -> int:
@@ -72,6 +80,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     P = POINTER(OscarCacheStruct)
     PP = POINTER(OscarPagedCacheStruct)
+    P16 = POINTER(OscarKV16CacheStruct)
     sig = {
         "oscar_rotate_q": (c_int, [c_void_p, c_void_p, c_int, c_int, c_uint, c_void_p]),
         "oscar_rotate_scale_k": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
@@ -96,6 +105,23 @@ def _load() -> ctypes.CDLL:
         "oscar_bf16_decode_attention": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int,
                                                 c_int, c_int, c_int, c_float, c_void_p, c_int,
                                                 c_void_p, c_size_t, c_void_p]),
+        "oscar_kv16_write": (c_int, [P16, c_void_p, c_longlong, c_void_p, c_longlong, c_void_p,
+                                     c_void_p, c_int, c_void_p]),
+        "oscar_kv16_attention": (c_int, [P16, c_void_p, c_longlong, c_void_p, c_int, c_int,
+                                         c_float, c_int, c_int, c_int, c_void_p, c_void_p,
+                                         c_void_p, c_size_t, c_void_p]),
+        "oscar_kv16_attention_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int,
+                                                            c_int]),
+        "oscar_kv16_decode_attention": (c_int, [P16, c_void_p, c_longlong, c_int, c_float, c_int,
+                                                c_int, c_int, c_int, c_void_p, c_void_p,
+                                                c_size_t, c_void_p]),
+        "oscar_kv16_decode_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int,
+                                                         c_int]),
+        "oscar_kv16_accumulate": (c_int, [P16, c_void_p, c_longlong, c_void_p, c_void_p, c_int,
+                                          c_int, c_float, c_int, c_int, c_int, c_int, c_void_p]),
+        "oscar_kv16_evict": (c_int, [P16, P16, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                     c_size_t, c_void_p]),
+        "oscar_kv16_evict_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int]),
         "oscar_device_status": (c_int, [c_void_p]),
         "oscar_selftest_wait_timeout": (c_int, [c_uint, c_void_p]),
         "oscar_status_string": (ctypes.c_char_p, [c_int]),
@@ -207,7 +233,45 @@ class KVCache:
                    for n in ("packed", "k_res", "v_res", "k_res_norm"))
 
 
-class PagedKVCache:
+class _PagePool:
+    """Host-side page allocator of the paged caches: which pages are free, and
+    the block table's host copy beside the device's (self.block_table)."""
+
+    def _init_pool(self, B: int, max_blocks: int, n_pages: int):
+        self._free = list(range(n_pages))
+        self._table_host = [[-1] * max_blocks for _ in range(B)]
+
+    def map_blocks(self, b: int, n_blocks: int, order=None):
+        """Gives sequence b pages for its logical blocks 0..n_blocks-1 (those
+        not mapped yet), taking free pages in `order` (a permutation of page
+        ids, for tests) or in pool order."""
+        if order is not None:
+            free = set(self._free)
+            self._free = [p for p in order if p in free]
+        row = self._table_host[b]
+        for j in range(n_blocks):
+            if row[j] < 0:
+                if not self._free:
+                    raise OscarError(4, "PagedKVCache.map_blocks: page pool exhausted")
+                row[j] = self._free.pop(0)
+        self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
+
+    def page_of(self, b: int, block: int) -> int:
+        return self._table_host[b][block]
+
+    def release_blocks(self, b: int, n_blocks: int = 0):
+        """Takes back sequence b's pages behind its first n_blocks logical
+        blocks; they are free for any sequence from then on, so work that
+        reads them has to be queued before what writes them."""
+        row = self._table_host[b]
+        for j in range(n_blocks, len(row)):
+            if row[j] >= 0:
+                self._free.append(row[j])
+                row[j] = -1
+        self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
+
+
+class PagedKVCache(_PagePool):
     """Caller-owned device buffers of a paged cache (oscar_paged_cache):
     a pool of n_pages pages (each one 2752-byte record per KV head for 32
     tokens), the block table [B][max_blocks] (page ids, -1 = unmapped),
@@ -238,8 +302,7 @@ class PagedKVCache:
         for name in ("k_res", "v_res", "k_res_norm"):
             setattr(s, name, getattr(self, name).data_ptr())
         self.struct = s
-        self._free = list(range(n_pages))
-        self._table_host = [[-1] * max_blocks for _ in range(B)]
+        self._init_pool(B, max_blocks, n_pages)
 
     B = property(lambda self: self.struct.B)
     Hkv = property(lambda self: self.struct.Hkv)
@@ -250,24 +313,6 @@ class PagedKVCache:
     def ref(self):
         return ctypes.byref(self.struct)
 
-    def map_blocks(self, b: int, n_blocks: int, order=None):
-        """Gives sequence b pages for its logical blocks 0..n_blocks-1 (those
-        not mapped yet), taking free pages in `order` (a permutation of page
-        ids, for tests) or in pool order."""
-        if order is not None:
-            free = set(self._free)
-            self._free = [p for p in order if p in free]
-        row = self._table_host[b]
-        for j in range(n_blocks):
-            if row[j] < 0:
-                if not self._free:
-                    raise OscarError(4, "PagedKVCache.map_blocks: page pool exhausted")
-                row[j] = self._free.pop(0)
-        self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
-
-    def page_of(self, b: int, block: int) -> int:
-        return self._table_host[b][block]
-
     def record(self, b: int, h: int, block: int) -> torch.Tensor:
         """View of the 2752-byte record of (b, h, logical block)."""
         return self.pages[self.page_of(b, block), h]
@@ -275,6 +320,100 @@ class PagedKVCache:
     def lengths(self):
         """(n_packed, n_res) per sequence, read back from the device."""
         return self.n_packed_d.cpu().tolist(), self.n_res_d.cpu().tolist()
+
+
+class KV16Cache:
+    """A 16-bit cache (oscar_kv16_cache) over the caller's device tensors:
+
+    k, v         bf16 or fp16; paged [n_pages][Hkv][32][128] if block_table is
+                 given, else contiguous [B][Hkv][T_cap][128]
+    n_tok        int32 [B], the sequences' lengths
+    block_table  int32 [B][max_blocks], page ids
+    weight       optional float32, as k without its last dimension
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, n_tok: torch.Tensor,
+                 block_table: torch.Tensor | None = None, weight: torch.Tensor | None = None):
+        self.k, self.v, self.n_tok = k, v, n_tok
+        self.block_table, self.weight = block_table, weight
+        if k.dtype not in _KV16_DTYPES:
+            raise ValueError("the cache takes bfloat16 or float16 keys and values")
+        if k.dim() != 4 or k.shape[3] != D or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v: two tensors [..][Hkv][..][128] of one shape and type")
+        if block_table is not None and (block_table.dim() != 2 or k.shape[2] != G):
+            raise ValueError("a paged cache: block_table [B][max_blocks], k [n_pages][Hkv][32][128]")
+        if weight is not None and weight.shape != k.shape[:3]:
+            raise ValueError("weight: the shape of k without its last dimension")
+        self.B = int(k.shape[0] if block_table is None else block_table.shape[0])
+        self.Hkv, self.dtype, self.device = int(k.shape[1]), k.dtype, k.device
+        s = OscarKV16CacheStruct()
+        s.B, s.Hkv, s.dtype = self.B, self.Hkv, _KV16_DTYPES[k.dtype]
+        if block_table is None:
+            s.T_cap = k.shape[2]
+        else:
+            s.max_blocks, s.n_pages = block_table.shape[1], k.shape[0]
+        s.k, s.v = _ptr(k), self._mine(v, k.dtype, k.numel())
+        s.n_tok = self._mine(n_tok, torch.int32, self.B)
+        s.block_table = self._mine(block_table, torch.int32, None)
+        s.weight = self._mine(weight, torch.float32, k.numel() // D)
+        self.struct = s
+        self._ref = ctypes.byref(s)
+
+    def _mine(self, t: torch.Tensor | None, dtype: torch.dtype, n: int | None):
+        """Pointer of a dense tensor that goes with the cache."""
+        if t is None:
+            return None
+        if t.dtype != dtype or (n is not None and t.numel() != n):
+            raise ValueError(f"expected {n if n is not None else ''} {dtype} elements, "
+                             f"got {tuple(t.shape)} {t.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"tensor on {t.device}, cache on {self.device}")
+        return _ptr(t)
+
+    def _rows(self, t: torch.Tensor, heads: int, total: int | None = None):
+        """(pointer, row stride, rows) of a [rows][heads][128] tensor of the cache's
+        type, dense within a row."""
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != self.dtype:
+            raise ValueError(f"expected [rows][{heads}][{D}] of {self.dtype}, "
+                             f"got {tuple(t.shape)} {t.dtype}")
+        rows = t.shape[0]
+        if total is not None and rows != total:
+            raise ValueError(f"expected {total} rows, got {rows}")
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError(f"tensor on {t.device}, cache on {self.device}")
+        stride = t.stride()
+        if stride[2] != 1 or (heads > 1 and stride[1] != D):
+            raise ValueError("a row's heads have to lie densely one behind another")
+        return t.data_ptr(), (stride[0] if rows > 1 else heads * D), rows
+
+    def ref(self):
+        return self._ref
+
+    capacity = property(lambda self: self.struct.max_blocks * G if self.block_table is not None
+                        else self.struct.T_cap)
+
+    @staticmethod
+    def contiguous(B: int, Hkv: int, T_cap: int, dtype=torch.bfloat16, device=None,
+                   weights: bool = False) -> "KV16Cache":
+        """An empty contiguous cache with buffers of its own."""
+        dev = torch.device(device if device is not None else "cuda")
+        k, v = (torch.zeros((B, Hkv, T_cap, D), dtype=dtype, device=dev) for _ in range(2))
+        w = torch.zeros((B, Hkv, T_cap), dtype=torch.float32, device=dev) if weights else None
+        return KV16Cache(k, v, torch.zeros(B, dtype=torch.int32, device=dev), weight=w)
+
+
+class PagedKV16Cache(_PagePool, KV16Cache):
+    """A paged KV16Cache with buffers and a block table of its own; pages are
+    handed out as in PagedKVCache."""
+
+    def __init__(self, B: int, Hkv: int, max_blocks: int, n_pages: int, dtype=torch.bfloat16,
+                 device=None, weights: bool = False):
+        dev = torch.device(device if device is not None else "cuda")
+        k, v = (torch.zeros((n_pages, Hkv, G, D), dtype=dtype, device=dev) for _ in range(2))
+        w = torch.zeros((n_pages, Hkv, G), dtype=torch.float32, device=dev) if weights else None
+        KV16Cache.__init__(self, k, v, torch.zeros(B, dtype=torch.int32, device=dev),
+                           torch.full((B, max_blocks), -1, dtype=torch.int32, device=dev), w)
+        self._init_pool(B, max_blocks, n_pages)
 
 
 # ---------------------------------------------------------------------------
@@ -401,6 +540,119 @@ def bf16_decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, B: 
                                             _ptr(workspace),
                                             workspace.numel() * workspace.element_size(),
                                             _stream(stream)), "oscar_bf16_decode_attention")
+
+
+# ---- the 16-bit cache ------------------------------------------------------
+
+def _kv16_call(cache: KV16Cache, where: str, fn, args, stream):
+    """Calls the library with the cache's device current, on `stream` or that
+    device's current stream."""
+    if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
+        with torch.cuda.device(cache.device):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, _stream(stream))
+    if st != 0:
+        raise OscarError(st, where)
+
+
+def _bytes(workspace: torch.Tensor, cache: KV16Cache):
+    if workspace.device != cache.device:
+        raise ValueError(f"workspace on {workspace.device}, cache on {cache.device}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def kv16_write(cache: KV16Cache, k_new: torch.Tensor, v_new: torch.Tensor, start: torch.Tensor,
+               pos0: torch.Tensor, stream=None):
+    """New tokens into the cache: rows start[b] .. start[b+1] of k_new, v_new
+    [total][Hkv][128] (a row may be a slice of a wider one) go to sequence b's
+    positions pos0[b] .., and n_tok[b] = pos0[b] + their number."""
+    k, ks, total = cache._rows(k_new, cache.Hkv)
+    v, vs, _ = cache._rows(v_new, cache.Hkv, total)
+    _kv16_call(cache, "oscar_kv16_write", _lib.oscar_kv16_write,
+               (cache._ref, k, ks, v, vs, cache._mine(start, torch.int32, cache.B + 1),
+                cache._mine(pos0, torch.int32, cache.B), total), stream)
+
+
+def kv16_attention_workspace_bytes(cache: KV16Cache, Hq: int, total: int, max_tok: int,
+                                   window: int = 0, n_sink: int = 0) -> int:
+    return int(_lib.oscar_kv16_attention_workspace_bytes(cache._ref, Hq, total, max_tok, window,
+                                                         n_sink))
+
+
+def kv16_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor, softmax_scale: float,
+                   max_tok: int, out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+                   n_sink: int = 0, lse: torch.Tensor | None = None, stream=None):
+    """Causal attention of every sequence's newest tokens over its cached ones:
+    rows start[b] .. start[b+1] of q [total][Hq][128] are the queries of the
+    last tokens of sequence b (already in the cache).  With window > 0 a query
+    sees the last `window` tokens up to its own and the first n_sink.  out
+    [total][Hq][128]; lse float32 [total][Hq]: the logarithm of the sum of the
+    exponentials.  max_tok bounds the n_tok[b]."""
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    qp, qs, total = cache._rows(q, Hq)
+    w, wb = _bytes(workspace, cache)
+    _kv16_call(cache, "oscar_kv16_attention", _lib.oscar_kv16_attention,
+               (cache._ref, qp, qs, cache._mine(start, torch.int32, cache.B + 1), total, Hq,
+                softmax_scale, max_tok, window, n_sink,
+                cache._mine(out, cache.dtype, total * Hq * D),
+                cache._mine(lse, torch.float32, total * Hq), w, wb), stream)
+
+
+def kv16_decode_workspace_bytes(cache: KV16Cache, Hq: int, max_tok: int, window: int = 0,
+                                n_sink: int = 0, accumulate: bool = False) -> int:
+    return int(_lib.oscar_kv16_decode_workspace_bytes(cache._ref, Hq, max_tok, window, n_sink,
+                                                      int(accumulate)))
+
+
+def kv16_decode_attention(cache: KV16Cache, q: torch.Tensor, softmax_scale: float, max_tok: int,
+                          out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+                          n_sink: int = 0, accumulate: bool = False, stream=None):
+    """Attention of each sequence's newest token, q and out [B][Hq][128];
+    accumulate adds its probabilities to the weights of the tokens it sees.
+    The workspace comes zeroed from alloc_workspace."""
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    qp, qs, _ = cache._rows(q, Hq, cache.B)
+    w, wb = _bytes(workspace, cache)
+    _kv16_call(cache, "oscar_kv16_decode_attention", _lib.oscar_kv16_decode_attention,
+               (cache._ref, qp, qs, Hq, softmax_scale, max_tok, window, n_sink, int(accumulate),
+                cache._mine(out, cache.dtype, cache.B * Hq * D), w, wb), stream)
+
+
+def kv16_accumulate(cache: KV16Cache, q: torch.Tensor, lse: torch.Tensor, start: torch.Tensor,
+                    softmax_scale: float, max_tok: int, window: int = 0, n_sink: int = 0,
+                    n_obs: int = 0, stream=None):
+    """Adds to each cached token's weight the probabilities it got from the
+    last n_obs queries (0: all) of its sequence; q, start and the window as for
+    kv16_attention, lse as it wrote it."""
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    qp, qs, total = cache._rows(q, Hq)
+    _kv16_call(cache, "oscar_kv16_accumulate", _lib.oscar_kv16_accumulate,
+               (cache._ref, qp, qs, cache._mine(lse, torch.float32, total * Hq),
+                cache._mine(start, torch.int32, cache.B + 1), total, Hq, softmax_scale, max_tok,
+                window, n_sink, n_obs), stream)
+
+
+def kv16_evict_workspace_bytes(src: KV16Cache, max_tok: int, keep_first: int, keep_recent: int,
+                               keep_top: int) -> int:
+    return int(_lib.oscar_kv16_evict_workspace_bytes(src._ref, max_tok, keep_first, keep_recent,
+                                                     keep_top))
+
+
+def kv16_evict(src: KV16Cache, dst: KV16Cache, max_tok: int, keep_first: int, keep_recent: int,
+               keep_top: int, workspace: torch.Tensor, kept: torch.Tensor | None = None,
+               stream=None):
+    """The first keep_first, the last keep_recent and the keep_top heaviest
+    tokens between them, per (sequence, KV head), into dst in order of
+    position.  kept int32 [B][Hkv][keep]: their positions in src, -1 behind the
+    last.  Sequences of at most keep tokens are copied whole."""
+    if dst.device != src.device:
+        raise ValueError(f"source on {src.device}, destination on {dst.device}")
+    keep = keep_first + keep_recent + keep_top
+    w, wb = _bytes(workspace, src)
+    _kv16_call(src, "oscar_kv16_evict", _lib.oscar_kv16_evict,
+               (src._ref, dst._ref, max_tok, keep_first, keep_recent, keep_top,
+                src._mine(kept, torch.int32, src.B * src.Hkv * keep), w, wb), stream)
 
 
 def selftest_wait_timeout(iterations: int = 256, stream=None):

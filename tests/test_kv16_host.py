@@ -1,0 +1,195 @@
+"""Host-side checks of the 16-bit cache's calls: bad arguments are refused
+before anything is launched, workspace sizes, the page allocator.  No kernel
+runs here; the cases pass made-up device addresses and are skipped where a GPU
+is present, so that a hole in the checks can never become a launch."""
+import ctypes
+
+import pytest
+import torch
+
+from int2_kv_cache_02_gb300 import _build
+
+no_gpu_only = pytest.mark.skipif(torch.cuda.is_available(),
+                                 reason="fake-pointer validation runs only without a GPU")
+FAKE = 0x7F0000000000
+P = ctypes.c_void_p
+OK, INVALID, UNSUPPORTED, ALIGNMENT, CAPACITY, WORKSPACE, CUDA = range(7)
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    from int2_kv_cache_02_gb300 import oscar
+    return oscar.library()
+
+
+def cache(at=0, **kw):
+    from int2_kv_cache_02_gb300.oscar import OscarKV16CacheStruct
+    s = OscarKV16CacheStruct()
+    s.B, s.Hkv, s.max_blocks, s.n_pages, s.T_cap, s.dtype = 2, 2, 8, 16, 256, 0
+    base = FAKE + at
+    s.k, s.v, s.weight = base, base + 0x1000000, base + 0x2000000
+    s.block_table, s.n_tok = base + 0x3000000, base + 0x4000000
+    for name, x in kw.items():
+        setattr(s, name, x)
+    return s
+
+
+BAD_CACHES = [(dict(B=0), INVALID), (dict(Hkv=-1), INVALID), (dict(k=None), INVALID),
+              (dict(v=None), INVALID), (dict(n_tok=None), INVALID), (dict(dtype=2), INVALID),
+              (dict(dtype=-1), INVALID), (dict(max_blocks=0), INVALID), (dict(n_pages=0), INVALID),
+              (dict(block_table=None, T_cap=0), INVALID), (dict(k=FAKE + 8), ALIGNMENT),
+              (dict(v=FAKE + 2), ALIGNMENT), (dict(weight=FAKE + 4), ALIGNMENT),
+              (dict(block_table=FAKE + 2), ALIGNMENT), (dict(n_tok=FAKE + 1), ALIGNMENT),
+              (dict(n_pages=2**26), UNSUPPORTED), (dict(max_blocks=2**30), UNSUPPORTED),
+              (dict(B=2**16, max_blocks=2**15), UNSUPPORTED),
+              (dict(block_table=None, T_cap=2**30), UNSUPPORTED)]
+
+
+@no_gpu_only
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_every_call_checks_its_cache(L, bad, status):
+    c, good = cache(**bad), cache(at=0x100000000)
+    r = ctypes.byref(c)
+    x = P(FAKE)
+    assert L.oscar_kv16_write(r, x, 256, x, 256, x, x, 4, None) == status
+    assert L.oscar_kv16_attention(r, x, 512, x, 4, 4, 1.0, 64, 0, 0, x, None, x, 1 << 30,
+                                  None) == status
+    assert L.oscar_kv16_decode_attention(r, x, 512, 4, 1.0, 64, 0, 0, 0, x, x, 1 << 30,
+                                         None) == status
+    assert L.oscar_kv16_accumulate(r, x, 512, x, x, 4, 4, 1.0, 64, 0, 0, 0, None) == status
+    assert L.oscar_kv16_evict(r, ctypes.byref(good), 64, 1, 1, 1, None, x, 1 << 30,
+                              None) == status
+    assert L.oscar_kv16_evict(ctypes.byref(good), r, 64, 1, 1, 1, None, x, 1 << 30,
+                              None) == status
+    assert L.oscar_kv16_decode_workspace_bytes(r, 4, 64, 0, 0, 0) == 0
+    assert L.oscar_kv16_attention_workspace_bytes(r, 4, 4, 64, 0, 0) == 0
+    assert L.oscar_kv16_evict_workspace_bytes(r, 64, 1, 1, 1) == 0
+
+
+@no_gpu_only
+def test_write_refusals(L):
+    c = cache()
+    r, x = ctypes.byref(c), P(FAKE)
+    f = lambda k=x, ks=256, v=x, vs=256, st=x, pos=x, n=4: L.oscar_kv16_write(r, k, ks, v, vs, st, pos, n, None)
+    assert f(k=None) == f(v=None) == f(st=None) == f(pos=None) == f(n=-1) == INVALID
+    assert f(ks=255) == f(vs=128) == f(ks=260) == f(ks=-256) == f(vs=1 << 41) == INVALID
+    assert f(k=P(FAKE + 8)) == f(v=P(FAKE + 2)) == f(st=P(FAKE + 2)) == f(pos=P(FAKE + 1)) == ALIGNMENT
+    # the lengths are written while the positions and ranges are read
+    assert f(pos=P(c.n_tok)) == f(pos=P(c.n_tok + 4)) == f(pos=P(c.n_tok - 4)) == INVALID
+    assert f(st=P(c.n_tok - 8)) == INVALID
+    assert L.oscar_kv16_write(None, x, 256, x, 256, x, x, 4, None) == INVALID
+
+
+@no_gpu_only
+def test_attention_refusals(L):
+    c = cache()
+    r, x = ctypes.byref(c), P(FAKE)
+
+    def f(q=x, qs=512, st=x, n=4, Hq=4, scale=1.0, most=64, win=0, sink=0, out=x, lse=None, ws=x, wb=1 << 34):
+        return L.oscar_kv16_attention(r, q, qs, st, n, Hq, scale, most, win, sink, out, lse, ws, wb, None)
+
+    assert f(q=None) == f(out=None) == f(st=None) == f(n=-1) == f(qs=511) == f(qs=516) == INVALID
+    assert f(scale=float("nan")) == f(scale=float("inf")) == f(most=-1) == f(win=-1) == f(sink=-1) == INVALID
+    assert f(Hq=0) == f(Hq=3) == f(Hq=34) == f(Hq=-4) == UNSUPPORTED
+    assert f(q=P(FAKE + 8)) == f(out=P(FAKE + 4)) == f(lse=P(FAKE + 2)) == f(st=P(FAKE + 2)) == ALIGNMENT
+    assert f(n=2**30) == UNSUPPORTED
+    assert f(n=0, q=None, out=None) == OK                 # nothing to do
+    need = L.oscar_kv16_attention_workspace_bytes(r, 4, 4, 64, 0, 0)
+    if need:
+        assert f(ws=None) == f(wb=need - 1) == WORKSPACE
+
+
+@no_gpu_only
+def test_decode_refusals(L):
+    c = cache()
+    r, x = ctypes.byref(c), P(FAKE)
+
+    def f(ref=r, q=x, qs=512, Hq=4, scale=1.0, most=64, win=0, sink=0, acc=0, out=x, ws=x, wb=1 << 34):
+        return L.oscar_kv16_decode_attention(ref, q, qs, Hq, scale, most, win, sink, acc, out, ws, wb, None)
+
+    assert f(q=None) == f(out=None) == f(qs=500) == f(acc=2) == INVALID
+    assert f(scale=float("nan")) == f(most=-1) == f(win=-1) == f(sink=-1) == INVALID
+    assert f(ref=ctypes.byref(cache(weight=None)), acc=1) == INVALID
+    assert f(Hq=3) == f(Hq=0) == f(Hq=64) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=8193))) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=8192, Hkv=9)), qs=36 * 128, Hq=36) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=8000, Hkv=8, max_blocks=2**18)), qs=1024, Hq=8, most=2**23) == UNSUPPORTED
+    for acc in (0, 1):
+        need = L.oscar_kv16_decode_workspace_bytes(r, 4, 64, 0, 0, acc)
+        assert need >= 65536 * 4
+        assert f(acc=acc, wb=need - 1) == f(acc=acc, ws=None) == WORKSPACE
+        assert f(acc=acc, ws=P(FAKE + 8), wb=need) == ALIGNMENT
+    assert f(out=P(FAKE + 8)) == f(q=P(FAKE + 2)) == ALIGNMENT
+
+
+@no_gpu_only
+def test_accumulate_refusals(L):
+    c = cache()
+    x = P(FAKE)
+
+    def f(c=c, q=x, qs=512, lse=x, st=x, n=4, Hq=4, scale=1.0, most=64, win=0, sink=0, obs=0):
+        return L.oscar_kv16_accumulate(ctypes.byref(c), q, qs, lse, st, n, Hq, scale, most, win, sink, obs, None)
+
+    assert f(q=None) == f(lse=None) == f(st=None) == f(n=-1) == f(obs=-1) == f(qs=8) == INVALID
+    assert f(c=cache(weight=None)) == f(scale=float("inf")) == f(most=-1) == f(win=-2) == f(sink=-2) == INVALID
+    assert f(Hq=5) == UNSUPPORTED
+    assert f(q=P(FAKE + 8)) == f(lse=P(FAKE + 2)) == f(st=P(FAKE + 3)) == ALIGNMENT
+    assert f(n=0, q=None, lse=None) == f(most=0) == OK
+
+
+@no_gpu_only
+def test_evict_refusals(L):
+    src, dst = cache(), cache(at=0x100000000)
+    x = P(FAKE + 0x200000000)
+
+    def f(src=src, dst=dst, most=64, first=1, recent=2, top=3, kept=None, ws=x, wb=1 << 34):
+        return L.oscar_kv16_evict(ctypes.byref(src), ctypes.byref(dst), most, first, recent, top, kept, ws, wb, None)
+
+    assert f(most=-1) == f(first=-1) == f(recent=-1) == f(top=-1) == INVALID
+    assert f(first=0, recent=0, top=0) == f(first=2**30, recent=2**30, top=2**30) == INVALID
+    assert f(src=cache(weight=None)) == f(dst=cache(at=1 << 32, B=3)) == INVALID
+    assert f(dst=cache(at=1 << 32, Hkv=4)) == f(dst=cache(at=1 << 32, dtype=1)) == INVALID
+    assert f(top=300) == CAPACITY
+    assert f(dst=src) == INVALID
+    for name in ("k", "v", "weight", "n_tok"):            # one shared buffer is enough
+        assert f(dst=cache(at=1 << 32, **{name: getattr(src, name)})) == INVALID
+    assert f(dst=cache(at=1 << 32, v=src.k + 256)) == INVALID
+    assert f(kept=P(FAKE + 2)) == ALIGNMENT
+    need = L.oscar_kv16_evict_workspace_bytes(ctypes.byref(src), 64, 1, 2, 3)
+    assert need > 0 and f(wb=need - 1) == f(ws=None) == WORKSPACE
+    assert f(ws=P(FAKE + 8)) == ALIGNMENT
+
+
+def test_page_allocator_takes_pages_back():
+    """release_blocks frees the pages behind the kept ones, for any sequence."""
+    from int2_kv_cache_02_gb300 import oscar as O
+
+    class Pool(O._PagePool):
+        def __init__(self):
+            self.block_table = torch.full((2, 4), -1, dtype=torch.int32)
+            self._init_pool(2, 4, 6)
+
+    p = Pool()
+    p.map_blocks(0, 4)
+    p.map_blocks(1, 2, order=[5, 4, 3, 2, 1, 0])
+    assert p.block_table.tolist() == [[0, 1, 2, 3], [5, 4, -1, -1]] and p._free == []
+    with pytest.raises(O.OscarError):
+        p.map_blocks(1, 3)
+    p.release_blocks(0, 1)
+    assert p.block_table[0].tolist() == [0, -1, -1, -1] and sorted(p._free) == [1, 2, 3]
+    p.map_blocks(1, 4)
+    assert set(p.block_table[1].tolist()[2:]) <= {1, 2, 3} and p.page_of(0, 1) == -1
+    p.release_blocks(1)
+    assert len(p._free) == 5
+
+
+def test_cache_takes_fitting_tensors_only():
+    from int2_kv_cache_02_gb300 import oscar as O
+    k = torch.zeros((4, 2, 32, 128), dtype=torch.bfloat16)
+    n, t = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32)
+    for bad in (dict(k=k.float(), v=k.float()), dict(v=k[:3]), dict(v=k.half()),
+                dict(k=k[:, :, :16], v=k[:, :, :16]), dict(block_table=t[0]),
+                dict(k=k[..., :64], v=k[..., :64]), dict(weight=torch.zeros(4, 2, 31))):
+        with pytest.raises(ValueError):
+            O.KV16Cache(**{**dict(k=k, v=k, n_tok=n, block_table=t), **bad})
