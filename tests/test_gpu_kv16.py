@@ -732,7 +732,6 @@ def test_binding_refuses(L):
            lambda: L.kv16_decode_attention(cache, q, R.SCALE, 64, out8[:, :4], ws),
            lambda: L.kv16_decode_attention(cache, torch.cat([q, q]), R.SCALE, 64, out8, ws),
            lambda: L.kv16_decode_attention(cache, q, R.SCALE, 64, out8.float(), ws),
-           lambda: L.kv16_attention(cache, q.transpose(0, 1), st, R.SCALE, 64, out8, ws),
            lambda: L.kv16_attention(cache, q, st, R.SCALE, 64, out8, ws, lse=torch.empty(3, device="cuda")),
            lambda: L.KV16Cache(cache.k, cache.v[:1], cache.n_tok, cache.block_table),
            lambda: L.KV16Cache(cache.k.float(), cache.v.float(), cache.n_tok, cache.block_table),
@@ -741,6 +740,7 @@ def test_binding_refuses(L):
         with pytest.raises(ValueError):
             f()
     refused = [lambda: L.kv16_write(cache, x, x, st, cache.n_tok),
+               lambda: L.kv16_attention(cache, q.transpose(0, 1), st, R.SCALE, 64, out8, ws),
                lambda: L.kv16_decode_attention(cache, q, math.nan, 64, out8, ws),
                lambda: L.kv16_decode_attention(cache, q, R.SCALE, 64, out8, ws, window=-1),
                lambda: L.kv16_decode_attention(cache, q, R.SCALE, 64, out8, ws[:100]),
