@@ -543,7 +543,7 @@ size_t oscar_kv16_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, i
  * workspace: a decode workspace (see oscar_decode_attention: its header of
  * OSCAR_DECODE_WS_HEADER_BYTES is zero before the first use and after every
  * call) of oscar_kv16_decode_workspace_bytes bytes.  B*Hkv <= 65536,
- * B <= 8192 and B*Hkv*ceil(max_tok/32) < 2^31 (else OSCAR_ERR_UNSUPPORTED).
+ * B <= 4096 and B*Hkv*ceil(max_tok/32) < 2^31 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                          long long q_stride, int Hq, float softmax_scale,

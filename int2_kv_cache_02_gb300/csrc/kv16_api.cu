@@ -90,7 +90,7 @@ bool overlap(Range a, Range b) {
 bool decode_size_ok(const oscar_kv16_cache* c, int max_tok) {
   const long long blocks = (std::min<long long>(max_tok, capacity(c)) + kPage - 1) / kPage;
   const long long rows = (long long)c->B * c->Hkv;
-  return c->B <= 8192 && rows <= kMaxDecodeRows && rows * blocks <= kMaxTokens;
+  return c->B <= kMaxDecodeBatch && rows <= kMaxDecodeRows && rows * blocks <= kMaxTokens;
 }
 
 // -1 if the three counts are no valid budget.

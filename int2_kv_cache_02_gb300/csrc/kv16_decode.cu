@@ -45,9 +45,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 namespace {
 
-constexpr int NW = 4;                    // warps of a CTA
+constexpr int NW = 10;                   // warps of a CTA, each with a slot of its own
 constexpr int kSlotBytes = 4 * 4096;     // a page: K and V, two halves of 64 channels each
-constexpr int kMinPages = 8;             // pages of a CTA's run, if the batch has as many
+constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many
 constexpr int kORow = 136;               // floats of a head's output row in shared memory
 
 struct DecodeParams {
@@ -58,14 +58,14 @@ struct DecodeParams {
   float* part;          // [grid][2][g][kRecFloats]
   float2* stats;        // [B][Hq] (m, 1 / l), accumulate only
   float* scores;        // [pages][g][32] log2-domain scores, accumulate only
-  int g, slots;
+  int g;
+  bool halves;          // the warps' outputs are joined in two steps
 };
 
-// First entries of each sequence in the line of pages (per KV head), and the
-// lengths: first[b] .. first[B], len[b].  Called by all threads; ends with a
-// barrier.  Returns the pages of one KV head over all sequences.
-__device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* len, int* scan,
-                       int threads, bool report) {
+// First pages of the sequences in the line of pages (of one KV head): first[0]
+// .. first[B].  Called by all threads; ends with a barrier.  Returns first[B].
+__device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* scan, int threads,
+                       bool report) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = threads >> 5;
   int carry = 0;
   for (int b0 = 0; b0 < c.B; b0 += threads) {
@@ -77,7 +77,6 @@ __device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* len, 
         if (report) record_error(c.status, kDevErrBadPaged);
         n = 0;
       }
-      len[b] = n;
     }
     int x = Span(n - 1, n - 1, q.window, q.n_sink).blocks;
     const int mine = x;
@@ -108,8 +107,7 @@ struct Row {
   Span sp;
 };
 
-__device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, const int* first,
-                                         const int* len) {
+__device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, const int* first) {
   const int key = x / p.c.Hkv;     // first[b] <= key < first[b + 1]
   int lo = 0, hi = p.c.B;
   while (hi - lo > 1) {
@@ -121,7 +119,7 @@ __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, c
   r.h = (x - first[lo] * p.c.Hkv) / pages;
   r.r0 = first[lo] * p.c.Hkv + r.h * pages;
   r.r1 = r.r0 + pages;
-  r.at = len[lo] - 1;
+  r.at = __ldg(p.c.n_tok + lo) - 1;
   r.sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
 }
 
@@ -173,25 +171,23 @@ __global__ void __launch_bounds__(NW * 32, 1)
 kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[NW][4];
+  __shared__ __align__(8) uint64_t full[NW];
   __shared__ int scan[NW];
-  __shared__ float sm_m[NW][16], sm_l[NW][16];
+  __shared__ float sm_m[NW][kMaxGroup], sm_l[NW][kMaxGroup];
   __shared__ int s_last, s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = p.slots;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;   // swizzle atoms
-  uint8_t* ring = smem + warp * slots * kSlotBytes;
-  float* obuf = reinterpret_cast<float*>(smem + NW * slots * kSlotBytes);   // [NW][g][kORow]
-  int* first = reinterpret_cast<int*>(obuf + NW * p.g * kORow);
-  int* len = first + p.c.B + 1;
+  uint8_t* slot = smem + warp * kSlotBytes;
+  const int parts = p.halves ? NW / 2 : NW;
+  float* obuf = reinterpret_cast<float*>(smem + NW * kSlotBytes);   // [parts][g][kORow]
+  int* first = reinterpret_cast<int*>(obuf + parts * p.g * kORow);
 
   if (tid == 0) {
-    for (int w = 0; w < NW; ++w)
-      for (int s = 0; s < 4; ++s) mbar_init(&full[w][s], 1);
+    for (int w = 0; w < NW; ++w) mbar_init(&full[w], 1);
     mbar_fence_init();
     s_abort = 0;
   }
-  const int line = line_up(p.c, p.q, first, len, scan, NW * 32, blockIdx.x == 0);
+  const int line = line_up(p.c, p.q, first, scan, NW * 32, blockIdx.x == 0);
   // rows without visible tokens: zeros
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x)
     if (first[b] == first[b + 1]) {
@@ -209,9 +205,9 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   // the warp's next page to fetch, and the row it is in
   Row nr;
   nr.r0 = nr.r1 = 0;
-  auto fetch = [&](int x, int slot) {
+  auto fetch = [&](int x) {
     if (x >= x1) return;
-    if (x < nr.r0 || x >= nr.r1) find_row(nr, x, p, first, len);
+    if (x < nr.r0 || x >= nr.r1) find_row(nr, x, p, first);
     int row = kv16_block_row(p.c, nr.b, nr.h, nr.sp.block(x - nr.r0));
     if (row < 0) {
       // past the end of the pool: the copy reads zeros
@@ -219,24 +215,22 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       if (lane == 0) record_error(p.c.status, kDevErrBadPaged);
     }
     if (lane == 0) {
-      uint8_t* s = ring + slot * kSlotBytes;
-      mbar_arrive_expect_tx(&full[warp][slot], kSlotBytes);
-      tma_box(s, &map_k, 0, row, &full[warp][slot]);
-      tma_box(s + 4096, &map_k, 64, row, &full[warp][slot]);
-      tma_box(s + 8192, &map_v, 0, row, &full[warp][slot]);
-      tma_box(s + 12288, &map_v, 64, row, &full[warp][slot]);
+      mbar_arrive_expect_tx(&full[warp], kSlotBytes);
+      tma_box(slot, &map_k, 0, row, &full[warp]);
+      tma_box(slot + 4096, &map_k, 64, row, &full[warp]);
+      tma_box(slot + 8192, &map_v, 0, row, &full[warp]);
+      tma_box(slot + 12288, &map_v, 64, row, &full[warp]);
     }
   };
   int x = x0 + warp;                // the warp's next page to work on
-  for (int s = 0; s < slots; ++s) fetch(x + s * NW, s);
-  int slot = 0;
+  fetch(x);
   unsigned phase = 0;
 
   const int hr = lane >> 2, hc = 2 * (lane & 3);    // accumulator row, column
   int seg = x0;
   Row r;
   while (seg < x1) {
-    find_row(r, seg, p, first, len);
+    find_row(r, seg, p, first);
     const int seg_end = min(r.r1, x1);
     // the group's queries as A operands: rows are heads, padding rows zero
     uint32_t qa[8][4];
@@ -255,8 +249,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
     for (; x < seg_end; x += NW) {
-      uint8_t* s = ring + slot * kSlotBytes;
-      if (!mbar_wait_bounded(&full[warp][slot], phase, kWaitLimit)) {
+      if (!mbar_wait_bounded(&full[warp], phase, kWaitLimit)) {
         if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
         s_abort = 1;
         break;
@@ -270,7 +263,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         if (!kv16_visible(j, r.at, p.q.window, p.q.n_sink)) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            reinterpret_cast<uint4*>(s + 8192 + (i >> 3) * 4096 + lane * 128)[i & 7] =
+            reinterpret_cast<uint4*>(slot + 8192 + (i >> 3) * 4096 + lane * 128)[i & 7] =
                 make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
@@ -279,7 +272,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       float sc[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
-      const unsigned sa = smem_u32(s);
+      const unsigned sa = smem_u32(slot);
       const int mrow = lane & 7, mid = lane >> 3;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -336,15 +329,19 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         }
       }
       const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-      uint32_t pa[2][4];
+      uint32_t pa[2][4], pb[2][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p0 = fast_exp2(sc[i][0] - ms[0]), p1 = fast_exp2(sc[i][1] - ms[0]);
         const float p2 = fast_exp2(sc[i][2] - ms[1]), p3 = fast_exp2(sc[i][3] - ms[1]);
         l[0] += p0 + p1;
         l[1] += p2 + p3;
-        pa[i >> 1][2 * (i & 1)] = T::pack(p0, p1);
-        pa[i >> 1][2 * (i & 1) + 1] = T::pack(p2, p3);
+        const uint32_t h0 = T::pack(p0, p1), h1 = T::pack(p2, p3);
+        const float2 u0 = T::unpack(h0), u1 = T::unpack(h1);
+        pa[i >> 1][2 * (i & 1)] = h0;
+        pa[i >> 1][2 * (i & 1) + 1] = h1;
+        pb[i >> 1][2 * (i & 1)] = T::pack(p0 - u0.x, p1 - u0.y);
+        pb[i >> 1][2 * (i & 1) + 1] = T::pack(p2 - u1.x, p3 - u1.y);
       }
       // O += P V: 8x8 tiles, transposed on the way: tokens t, t + 8 of channels c, c + 8
 #pragma unroll
@@ -359,34 +356,67 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         mma<T>(o[2 * n + 1], pa[0], b0[2], b0[3]);
         mma<T>(o[2 * n], pa[1], b1[0], b1[1]);
         mma<T>(o[2 * n + 1], pa[1], b1[2], b1[3]);
+        mma<T>(o[2 * n], pb[0], b0[0], b0[1]);
+        mma<T>(o[2 * n + 1], pb[0], b0[2], b0[3]);
+        mma<T>(o[2 * n], pb[1], b1[0], b1[1]);
+        mma<T>(o[2 * n + 1], pb[1], b1[2], b1[3]);
       }
       // refill the slot once every lane has read it; cleared values first
       // become visible to the copy engine
       if (!whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      fetch(x + slots * NW, slot);
-      if (++slot == slots) {
-        slot = 0;
-        phase ^= 1;
-      }
+      fetch(x + NW);
+      phase ^= 1;
     }
 
-    // join the warps
+    // join the warps: in one step, or the upper half's results into the lower
+    // half's first where the buffer holds half of them
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int head = hr + 8 * i;
-      if (head < p.g) {
+    }
+    auto leave = [&](int part) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int head = hr + 8 * i;
+        if (head >= p.g) continue;
         if ((lane & 3) == 0) {
-          sm_m[warp][head] = m[i];
-          sm_l[warp][head] = l[i];
+          sm_m[part][head] = m[i];
+          sm_l[part][head] = l[i];
         }
-        float* d = obuf + (warp * p.g + head) * kORow + hc;
+        float* d = obuf + (part * p.g + head) * kORow + hc;
 #pragma unroll
         for (int n = 0; n < 16; ++n)
           *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
       }
+    };
+    if (p.halves) {
+      if (warp >= NW / 2) leave(warp - NW / 2);
+      __syncthreads();
+      if (warp < NW / 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int head = hr + 8 * i;
+          if (head >= p.g) continue;
+          const float m2 = sm_m[warp][head], M = fmaxf(m[i], m2);
+          const float a = M == -INFINITY ? 1.0f : fast_exp2(m[i] - M);
+          const float a2 = M == -INFINITY ? 1.0f : fast_exp2(m2 - M);
+          const float* d = obuf + (warp * p.g + head) * kORow + hc;
+          m[i] = M;
+          l[i] = a * l[i] + a2 * sm_l[warp][head];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const float2 v = *reinterpret_cast<const float2*>(d + 8 * n);
+            o[n][2 * i] = a * o[n][2 * i] + a2 * v.x;
+            o[n][2 * i + 1] = a * o[n][2 * i + 1] + a2 * v.y;
+          }
+        }
+        __syncwarp();    // a warp's own part: read by all lanes, then written
+        leave(warp);
+      }
+    } else {
+      leave(warp);
     }
     __syncthreads();
     const bool own_row = seg == r.r0 && seg_end == r.r1;
@@ -395,10 +425,9 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int i = tid; i < p.g * 64; i += NW * 32) {
       const int head = i >> 6, pair = i & 63;
       float M = -INFINITY, L = 0.0f, a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w][head]);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
+      for (int w = 0; w < parts; ++w) M = fmaxf(M, sm_m[w][head]);
+#pragma unroll 5
+      for (int w = 0; w < parts; ++w) {
         const float mw = sm_m[w][head];
         const float a = mw == -INFINITY && M == -INFINITY ? 1.0f : fast_exp2(mw - M);
         const float2 v = *reinterpret_cast<const float2*>(obuf + (w * p.g + head) * kORow + 2 * pair);
@@ -452,48 +481,59 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     seg = seg_end;
   }
-  if (s_abort) {
-    // copies still in flight land before the CTA's memory is given back
-    for (int s = 0; s < slots; ++s) {
-      if (x + s * NW < x1 && !mbar_wait_bounded(&full[warp][slot], phase, kDrainLimit) && lane == 0)
-        record_error(p.c.status, kDevErrDrainTimeout);
-      if (++slot == slots) {
-        slot = 0;
-        phase ^= 1;
-      }
-    }
-  }
+  // after a time-out the warp's copy in flight lands before its memory is given back
+  if (s_abort && x < x1 && !mbar_wait_bounded(&full[warp], phase, kDrainLimit) && lane == 0)
+    record_error(p.c.status, kDevErrDrainTimeout);
 }
 
 constexpr int kWThreads = 256;
 
-// weight[j] += sum over the group's heads of 2^(s_j - m) / l, a warp per page.
+
+// weight[j] += sum over the group's heads of 2^(s_j - m) / l: a warp takes four
+// neighbouring pages at a time, eight lanes a page and four tokens a lane.
+// The scores are addressed by the page's place in the line alone, so their
+// loads do not wait for the row's to be found.
 __global__ void __launch_bounds__(kWThreads) kv16_decode_weights_kernel(const DecodeParams p) {
-  extern __shared__ int lines[];
+  extern __shared__ int first[];
   __shared__ int scan[kWThreads / 32];
-  int* first = lines;
-  int* len = lines + p.c.B + 1;
-  const int P = line_up(p.c, p.q, first, len, scan, kWThreads, false) * p.c.Hkv;
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kWThreads / 32);
-  const int per = P > 0 ? (P - 1) / warps + 1 : 0;   // a run of pages, so rows change seldom
-  const long long w = (long long)blockIdx.x * (kWThreads / 32) + (threadIdx.x >> 5);
+  const int P = line_up(p.c, p.q, first, scan, kWThreads, false) * p.c.Hkv;
+  const int lane = threadIdx.x & 31, t0 = 4 * (lane & 7);
+  const long long step = (long long)gridDim.x * (kWThreads / 32) * 4;
+  long long x = ((long long)blockIdx.x * (kWThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
   Row r;
   r.r0 = r.r1 = 0;
-  for (long long x = w * per; x < min((long long)P, (w + 1) * per); ++x) {
-    if (x >= r.r1) find_row(r, (int)x, p, first, len);
-    const int row = kv16_block_row(p.c, r.b, r.h, r.sp.block((int)x - r.r0));
-    const float* s = p.scores + (size_t)x * p.g * kPage + lane;
+  for (; x < P; x += step) {
+    const float* sp = p.scores + (size_t)x * p.g * kPage + t0;
+    float4 s[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h < p.g) s[h] = __ldcs(reinterpret_cast<const float4*>(sp + h * kPage));
+    if (x < r.r0 || x >= r.r1) find_row(r, (int)x, p, first);
+    const int j0 = r.sp.block((int)x - r.r0);
+    const int row = kv16_block_row(p.c, r.b, r.h, j0);
+    if (row < 0) continue;
     const float2* st = p.stats + (long long)r.b * p.q.Hq + r.h * p.g;
-    float sum = 0.0f;
-    bool seen = false;
-    for (int i = 0; i < p.g; ++i) {
-      const float v = __ldcs(s + i * kPage);
-      const float2 ml = st[i];
-      seen |= v != -INFINITY;
-      if (v != -INFINITY) sum += fast_exp2(v - ml.x) * ml.y;
+    float* wp = p.c.weight + (long long)row + t0;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h0 = 0; h0 < p.g; h0 += 8) {
+      if (h0 > 0) {
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (h0 + h < p.g) s[h] = __ldcs(reinterpret_cast<const float4*>(sp + (h0 + h) * kPage));
+      }
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        if (h0 + h < p.g) {
+          const float2 ml = st[h0 + h];
+          const float v[4] = {s[h].x, s[h].y, s[h].z, s[h].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (v[i] != -INFINITY) sum[i] += fast_exp2(v[i] - ml.x) * ml.y;
+        }
     }
-    if (seen && row >= 0) p.c.weight[(long long)row + lane] += sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (kv16_visible(j0 * kPage + t0 + i, r.at, p.q.window, p.q.n_sink)) wp[i] += sum[i];
   }
 }
 
@@ -522,6 +562,11 @@ long long line_pages(const Kv16& c, int max_tok, int window, int n_sink) {
 int decode_grid(long long pages) {
   return (int)std::max<long long>(1, std::min<long long>(sm_count(), (pages + kMinPages - 1) / kMinPages));
 }
+
+// Dynamic shared memory that a CTA may have beside the static.
+constexpr size_t kSmemMost = 227 * 1024 - 2048;
+static_assert(NW * kSlotBytes + NW / 2 * kMaxGroup * kORow * 4 + (kMaxDecodeBatch + 1) * 4 + 1024 <=
+                  kSmemMost, "the widest group of the largest batch");
 
 size_t part_bytes(int grid, int g) { return (size_t)grid * 2 * g * kRecFloats * sizeof(float); }
 size_t stats_bytes(int B, int Hq) { return ((size_t)B * Hq * sizeof(float2) + 15) / 16 * 16; }
@@ -560,12 +605,10 @@ cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulat
   p.part = decode_partials(ws);
   p.stats = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(p.part) + part_bytes(grid, p.g));
   p.scores = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.stats) + stats_bytes(c.B, q.Hq));
-  // three slots per warp where the heads' outputs and the lengths leave room
-  const size_t fixed = (size_t)NW * p.g * kORow * 4 + (size_t)(2 * c.B + 1) * 4 + 1024;
-  constexpr size_t kSmemMost = 227 * 1024 - 2048;
-  p.slots = 3;
-  while (p.slots > 1 && fixed + (size_t)NW * p.slots * kSlotBytes > kSmemMost) --p.slots;
-  const size_t smem = fixed + (size_t)NW * p.slots * kSlotBytes;
+  const size_t lines = (size_t)(c.B + 1) * 4;
+  const size_t heads = (size_t)NW * p.g * kORow * 4;
+  p.halves = NW * kSlotBytes + heads + lines + 1024 > kSmemMost;
+  const size_t smem = NW * kSlotBytes + (p.halves ? heads / 2 : heads) + lines + 1024;
   CUtensorMap mk, mv;
   if (!kv16_row_map(&mk, c, c.k) || !kv16_row_map(&mv, c, c.v)) return cudaErrorNotSupported;
   cudaError_t e =
@@ -575,12 +618,11 @@ cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulat
                            : launch_main<Bf16, false>(mk, mv, p, grid, smem, s));
   *launches = 1;
   if (e != cudaSuccess || !accumulate) return e;
-  const size_t lines = (size_t)(2 * c.B + 1) * 4;
   e = cudaFuncSetAttribute(kv16_decode_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)lines);
   if (e != cudaSuccess) return e;
   const int wgrid = (int)std::max<long long>(
-      1, std::min<long long>((pages + 7) / 8, 4LL * sm_count()));
+      1, std::min<long long>((pages + 31) / 32, 8LL * sm_count()));
   kv16_decode_weights_kernel<<<wgrid, kWThreads, lines, s>>>(p);
   *launches = 2;
   return cudaGetLastError();

@@ -223,6 +223,7 @@ cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* o
                                   void* ws, int* launches, cudaStream_t s);
 size_t kv16_attention_ws_bytes(const Kv16& c, int Hq, int total, int max_tok, int window,
                                int n_sink);
+constexpr int kMaxDecodeBatch = 4096;   // sequences of one call
 cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
                                void* ws, int* launches, cudaStream_t s);
 size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int n_sink,

@@ -112,9 +112,9 @@ def test_decode_refusals(L):
     assert f(scale=float("nan")) == f(most=-1) == f(win=-1) == f(sink=-1) == INVALID
     assert f(ref=ctypes.byref(cache(weight=None)), acc=1) == INVALID
     assert f(Hq=3) == f(Hq=0) == f(Hq=64) == UNSUPPORTED
-    assert f(ref=ctypes.byref(cache(B=8193))) == UNSUPPORTED
-    assert f(ref=ctypes.byref(cache(B=8192, Hkv=9)), qs=36 * 128, Hq=36) == UNSUPPORTED
-    assert f(ref=ctypes.byref(cache(B=8000, Hkv=8, max_blocks=2**18)), qs=1024, Hq=8, most=2**23) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=4097))) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=4096, Hkv=17)), qs=34 * 128, Hq=34) == UNSUPPORTED
+    assert f(ref=ctypes.byref(cache(B=4000, Hkv=16, max_blocks=2**18)), qs=2048, Hq=16, most=2**23) == UNSUPPORTED
     for acc in (0, 1):
         need = L.oscar_kv16_decode_workspace_bytes(r, 4, 64, 0, 0, acc)
         assert need >= 65536 * 4
