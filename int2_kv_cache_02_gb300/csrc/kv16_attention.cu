@@ -1,59 +1,584 @@
-// Attention of a ragged batch of queries over the 16-bit cache.
+// Attention of a ragged batch of queries over the 16-bit cache, on the
+// tcgen05 tensor cores: 4 * 128 flops per visible (query, key) pair and head.
+//
+// Tiles.  A CTA takes up to two tiles of 128 query rows of one (sequence, KV
+// head): a row is a (token, head of the group) pair, token-major, so the whole
+// group reads each key and value once and a tile spans only 128 / g tokens
+// (less masked work on the diagonal and at the edges of a window).  Keys come
+// in tiles of four pages = 128 tokens; the pages that any row of the CTA sees
+// (the sinks', then the window's) are numbered through, so a tile mixes pages
+// from both places and pages outside are never read.
+//
+// Roles (12 warps): a softmax warpgroup per query tile (a thread per row, so
+// maxima and sums need no shuffles), one warp that copies (TMA, five stages of
+// 32 KB that hold key and value tiles in turn), one that issues the MMAs.
+//   S_w = Q_w K^T   128 x 128 x 128, both operands in shared memory
+//   O_w += P_w V    P_w from TMEM, where it takes the place of S_w; V as it
+//                   lies (along N)
+// While one tile's softmax runs, the tensor cores work on the other tile.
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+//
+// Softmax.  One pass, running maximum and sum in fp32, base 2.  O is rescaled
+// only when a row's maximum has grown by more than 2^8 since the last time: the
+// probabilities then stay below 2^8, which both 16-bit types hold, and the
+// final division makes up for it.  Probabilities are rounded to the type of V
+// for the product (half a step relative, as the output itself); the sum is of
+// the unrounded ones.
+//
+// Hidden values.  A hidden token's probability is exactly 0, but 0 * NaN is
+// not: rows past the end of the sequence are cleared in shared memory, and a
+// row whose output is not finite is worked again by a warp that touches only
+// the tokens the row sees (kv16_warp_row).
+//
+// Few tiles over a long cache: the key tiles are split over several CTAs, which
+// leave (m, l, o[128]) records that a second kernel joins.
+#include <algorithm>
+#include <cmath>
+
 #include "kv16.cuh"
+#include "kv16_tma.h"
+#include "tc5.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kStages = 5;
+constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
+constexpr int kHalf = 16384;
+constexpr int kKeyPages = 4;           // pages of a key tile
+constexpr float kGrowth = 8.0f;        // log2 of the growth that O is not rescaled for
+constexpr uint32_t kO = 256;           // TMEM columns: S_w at 128 w, O_w at 256 + 128 w
 
-// A warp per (query, head).
+struct AttnParams {
+  Kv16 c;
+  Kv16Query q;
+  uint16_t* out;
+  float* lse;
+  float* part;          // [total * Hq][splits][kRecFloats] if splits > 1
+  int g, tokens;        // heads of a group, tokens of a query tile
+  int tiles;            // upper bound on CTAs of one KV head
+  int splits;
+  float scale;          // |scale| in the log2 domain
+  bool negate;
+};
+
+// Where a row's result goes and what it may see.
+struct RowPlace {
+  int row, head, at;
+};
+
+struct Smem {
+  uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
 template <class T>
-__global__ void __launch_bounds__(kWarps * 32)
-kv16_rows_kernel(const Kv16 c, const Kv16Query q, uint16_t* __restrict__ out,
-                 float* __restrict__ lse) {
-  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (w >= q.total * q.Hq) return;
-  const int r = w / q.Hq, head = w - r * q.Hq;
-  int b = r, at = 0;
-  if (q.start) {
-    b = ragged_sequence(q.start, c.B, r);
-    if (b < 0) return;
-  }
-  const int n = kv16_length(c, b, q.max_tok);
-  at = q.start ? n - (__ldg(q.start + b + 1) - r) : n - 1;
-  if (n < 0 || (q.start && at < 0)) {
-    if (lane == 0) record_error(c.status, kDevErrBadPaged);
-    at = -1;
-  }
-  const Span sp(at, at, q.window, q.n_sink);
-  float m, l, o[4];
-  kv16_warp_row<T>(c, q.q + r * q.stride + (long long)head * kD, b, head / (q.Hq / c.Hkv), at, sp,
-                   0, sp.blocks, q.window, q.n_sink, q.scale_log2, m, l, o);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const long long row = (long long)r * q.Hq + head;
-  reinterpret_cast<uint2*>(out + row * kD)[lane] =
+__device__ __forceinline__ void store_row4(const AttnParams& p, long long row, int lane,
+                                           const float (&o)[4], float inv) {
+  reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
       make_uint2(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv));
-  if (lse && lane == 0) lse[row] = kv16_lse(m, l);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 1)
+kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) Smem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- the CTA's work: tile t of sequence b, KV head h, split s.  Sequence
+  // b's CTAs start at start[b] / (2 tokens) + b, which leaves room for each.
+  const int two = 2 * p.tokens;
+  const int h = blockIdx.x % p.c.Hkv, t = blockIdx.x / p.c.Hkv, split = blockIdx.y;
+  int lo = 0, hi = p.c.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (min(max(__ldg(p.q.start + mid), 0), p.q.total) / two + mid <= t) lo = mid; else hi = mid;
+  }
+  const int b = lo;
+  const int r0 = __ldg(p.q.start + b), r1 = __ldg(p.q.start + b + 1), nq = r1 - r0;
+  if (r0 < 0 || r1 > p.q.total || nq < 0) {
+    if (tid == 0) record_error(p.c.status, kDevErrBadPaged);
+    return;
+  }
+  const int tile_in_seq = t - (r0 / two + b), seq_tiles = (nq + two - 1) / two;
+  if (tile_in_seq < 0 || tile_in_seq >= seq_tiles) return;
+  int n = kv16_length(p.c, b, p.q.max_tok);
+  if (n < nq) {     // a length out of range, or fewer tokens than queries
+    if (tid == 0) record_error(p.c.status, kDevErrBadPaged);
+    if (n < 0) n = 0;
+  }
+  const int q0 = (seq_tiles - 1 - tile_in_seq) * two;        // the longest rows first
+  const int nrow = min(two, nq - q0);                        // tokens of this CTA
+  const int ntile = nrow > p.tokens ? 2 : 1;
+  const int at0 = n - nq + q0;                               // position of its first token
+  const Span sp(at0, at0 + nrow - 1, p.q.window, p.q.n_sink);
+  const int kt_all = (sp.blocks + kKeyPages - 1) / kKeyPages;
+  const int k0 = (int)((long long)kt_all * split / p.splits);
+  const int k1 = (int)((long long)kt_all * (split + 1) / p.splits);
+  // key tiles of the first query tile: it ends before the second
+  const int blocks0 = Span(at0, at0 + min(nrow, p.tokens) - 1, p.q.window, p.q.n_sink).blocks;
+  const int k1_0 = min(k1, max(k0, (blocks0 + kKeyPages - 1) / kKeyPages));
+  const int cnt[2] = {ntile == 2 ? k1_0 - k0 : k1 - k0, ntile == 2 ? k1 - k0 : 0};
+
+  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t* sq = smem;                            // two query tiles
+  uint8_t* ring = smem + 2 * kTileBytes;
+
+  if (warp == 8) tc5_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    mbar_init(&sm.q_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.o_full[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    mbar_fence_init();
+    sm.abort = 0;
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort = &sm.abort;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
+                                 : p.c.B * p.c.Hkv * p.c.T_cap;      // reads zeros
+      if (lane == 0 && k1 > k0) {
+        const unsigned bytes = 64 * 2 * p.g * p.tokens;
+        mbar_arrive_expect_tx(&sm.q_full, 2 * bytes * ntile);
+        for (int w = 0; w < ntile; ++w)
+          for (int i = 0; i < 2; ++i)
+            tma_box3(sq + w * kTileBytes + i * kHalf, &map_q, 64 * i, h * p.g,
+                     r0 + q0 + w * p.tokens, &sm.q_full);
+      }
+      int used = 0;     // stages filled so far
+      bool ok = true;
+      for (int k = k0; k < k1 && ok; ++k) {
+        int row = none;
+        if (lane < kKeyPages && k * kKeyPages + lane < sp.blocks) {
+          row = kv16_block_row(p.c, b, h, sp.block(k * kKeyPages + lane));
+          if (row < 0) {
+            record_error(p.c.status, kDevErrBadPaged);
+            row = none;
+          }
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = used % kStages;
+          if (used >= kStages && !tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort)) {
+            if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+            ok = false;
+            break;
+          }
+          uint8_t* dst = ring + st * kTileBytes;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+#pragma unroll
+          for (int i = 0; i < kKeyPages; ++i) {
+            const int y = __shfl_sync(0xffffffffu, row, i);
+            if (lane == 0) {
+              tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, &sm.full[st]);
+              tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, &sm.full[st]);
+            }
+          }
+          __syncwarp();
+          ++used;
+        }
+      }
+      // after a time-out: what is in flight lands before the memory is given back
+      if (*abort) {
+        if (k1 > k0) mbar_wait_bounded(&sm.q_full, 0, kDrainLimit);
+        for (int i = max(0, used - kStages); i < used; ++i)
+          if (!mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit) && lane == 0)
+            record_error(p.c.status, kDevErrDrainTimeout);
+      }
+    } else if (warp == 9 && k1 > k0) {
+      // -------------------------------------------------------------- MMAs
+      const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
+      const uint32_t id_o = tc5_idesc(T::kHalf, 128, 128, true, false);
+      const uint64_t along_k = tc5_desc_base(16, 1024);          // Q, K
+      const uint64_t along_n = tc5_desc_base(kHalf, 1024);       // V
+      auto qk = [&](int w, const uint8_t* ktile) {
+        const unsigned qa = smem_u32(sq + w * kTileBytes), ka = smem_u32(ktile);
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const unsigned off = (i >> 2) * kHalf + (i & 3) * 32;
+            tc5_mma_ss(tmem + 128 * w, tc5_desc(along_k, qa + off), tc5_desc(along_k, ka + off),
+                       id_s, i > 0);
+          }
+          tc5_commit(&sm.s_full[w]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](int st) {
+        if (lane == 0) tc5_commit(&sm.empty[st]);
+        __syncwarp();
+      };
+      const int last = ntile - 1, nk = k1 - k0;
+      bool ok = tc5_wait(&sm.q_full, 0, abort) && tc5_wait(&sm.full[0], 0, abort);
+      if (ok) {
+        tc5_fence_after();
+        for (int w = 0; w < ntile; ++w)
+          if (cnt[w] > 0) qk(w, ring);
+        release(0);
+      }
+      for (int j = 0; j < nk && ok; ++j) {
+        // stages: K_j is number 2j, V_j 2j + 1
+        const int vs = (2 * j + 1) % kStages, ks = (2 * j + 2) % kStages;
+        uint8_t* vt = ring + vs * kTileBytes;
+        ok = tc5_wait(&sm.full[vs], ((2 * j + 1) / kStages) & 1, abort);
+        if (!ok) break;
+        // the rows behind the sequence's last token hold anything: clear them
+        const int last_page = sp.blocks - 1 - (k0 + j) * kKeyPages;
+        if (last_page >= 0 && last_page < kKeyPages) {
+          const int blk = sp.block(sp.blocks - 1);
+          const int r = blk * kPage + lane;
+          if (r >= n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              reinterpret_cast<uint4*>(vt + (i >> 3) * kHalf + (last_page * kPage + lane) * 128)[i & 7] =
+                  make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        const bool more = j + 1 < nk;
+        if (more) {
+          ok = tc5_wait(&sm.full[ks], ((2 * j + 2) / kStages) & 1, abort);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j < cnt[w]) {
+            ok = ok && tc5_wait(&sm.p_full[w], j & 1, abort);
+            if (!ok) break;
+            tc5_fence_after();
+            const unsigned va = smem_u32(vt);
+            if (lane == 0) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i,
+                           tc5_desc(along_n, va + i * 2048), id_o, j > 0 || i > 0);
+              if (j + 1 == cnt[w]) tc5_commit(&sm.o_full[w]);
+            }
+            __syncwarp();
+          }
+          if (w == last) release(vs);
+          if (more && j + 1 < cnt[w]) qk(w, ring + ks * kTileBytes);
+          if (more && w == last) release(ks);
+        }
+      }
+      if (!ok && lane == 0) {
+        record_error(p.c.status, kDevErrWaitTimeout);
+        tc5_commit(&sm.drain);
+        mbar_wait_bounded(&sm.drain, 0, kDrainLimit);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    // -------------------------------------------------------------- softmax
+    const int w = warp >> 2, r = tid & 127;
+    if (w < ntile) {
+      const uint32_t lane_addr = tmem + ((uint32_t)(warp & 3) << 21);
+      const uint32_t s_addr = lane_addr + 128 * w, o_addr = lane_addr + kO + 128 * w;
+      // the thread's row; rows past the tile's end work like its last token
+      const int ntok = min(p.tokens, nrow - w * p.tokens);
+      const int tok = r / p.g, head = r - tok * p.g;
+      const bool valid = tok < ntok;
+      const int at = at0 + w * p.tokens + min(tok, ntok - 1);
+      const int at_min = __shfl_sync(0xffffffffu, at, 0), at_max = __shfl_sync(0xffffffffu, at, 31);
+      const int my_n = w ? cnt[1] : cnt[0];
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < my_n; ++j) {
+        if (!tc5_wait(&sm.s_full[w], j & 1, abort)) {
+          if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+          ok = false;
+          break;
+        }
+        tc5_fence_after();
+        uint32_t sr[128];
+        float* s = reinterpret_cast<float*>(sr);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc5_ld32(sr + 32 * i, s_addr + 32 * i);
+        tc5_wait_ld();
+        // mask, page by page
+#pragma unroll
+        for (int i = 0; i < kKeyPages; ++i) {
+          const int v = (k0 + j) * kKeyPages + i;
+          const int base = sp.block(v) * kPage;
+          const bool whole = v < sp.blocks && base + kPage - 1 <= at_min &&
+                             (p.q.window == 0 || base > at_max - p.q.window ||
+                              base + kPage <= p.q.n_sink);
+          if (!whole) {
+            // columns [0, up) at or before the query; of them [from, ..) in the
+            // window and [0, sink) sinks
+            const int up = v >= sp.blocks || at < base ? 0 : min(at - base + 1, 32);
+            const int from = p.q.window == 0 ? 0 : max(at - p.q.window + 1, 0) - base;
+            const int sink = p.q.n_sink <= base ? 0 : min(p.q.n_sink - base, 32);
+            const uint32_t below_up = up >= 32 ? 0xffffffffu : (1u << up) - 1;
+            const uint32_t near = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+            const uint32_t first = sink >= 32 ? 0xffffffffu : (1u << sink) - 1;
+            const uint32_t see = below_up & (near | first);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
+          }
+        }
+        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+        float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
+#pragma unroll
+        for (int e = 8; e < 128; e += 8) {
+          mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
+          mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
+          mx2 = fmaxf(mx2, fmaxf(s[e + 4], s[e + 5]));
+          mx3 = fmaxf(mx3, fmaxf(s[e + 6], s[e + 7]));
+        }
+        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale;
+        if (j == 0) {
+          m = mx;
+        } else {
+          const bool grow = mx > m + kGrowth;      // true where m is -inf and mx is not
+          if (__any_sync(0xffffffffu, grow)) {
+            // S_w of this tile is there, so the products before it are complete
+            const float a = grow ? fast_exp2(m - mx) : 1.0f;
+            if (grow) m = mx;
+            l *= a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[32];
+              tc5_ld32(o, o_addr + 32 * i);
+              tc5_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+              tc5_st32(o_addr + 32 * i, o);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.0f : m;
+        const float2 sc2 = make_float2(p.scale, p.scale), m2 = make_float2(-ms, -ms);
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int e = 0; e < 128; e += 4) {
+          float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
+          float2 y = fma2(make_float2(s[e + 2], s[e + 3]), sc2, m2);
+          x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          sum0 = add2(sum0, x);
+          sum1 = add2(sum1, y);
+          sr[e / 2] = T::pack(x.x, x.y);
+          sr[e / 2 + 1] = T::pack(y.x, y.y);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        tc5_st32(s_addr, sr);
+        tc5_st32(s_addr + 32, sr + 32);
+        tc5_wait_st();
+        tc5_fence_before();
+        mbar_arrive(&sm.p_full[w]);
+      }
+
+      // ------------------------------------------------------------ results
+      if (ok && my_n > 0 && !tc5_wait(&sm.o_full[w], 0, abort)) {
+        if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+        ok = false;
+      }
+      if (ok) {
+        tc5_fence_after();
+        const long long row = (long long)(r0 + q0 + w * p.tokens + tok) * p.q.Hq + h * p.g + head;
+        const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+        float odd = l * 0.0f;            // NaN once anything is not finite
+        // the tile's queries are done with: its shared memory stages the rows
+        uint8_t* stage = sq + w * kTileBytes + (warp & 3) * 8192;
+        float* rec = p.part + (row * p.splits + split) * kRecFloats;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          if (my_n > 0) {
+            tc5_ld32(o, o_addr + 32 * i);
+            tc5_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+          if (p.splits > 1) {
+            if (valid)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
+                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 v;
+              v.x = T::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              v.y = T::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              v.z = T::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+              v.w = T::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+              const int chunk = 4 * i + e / 8;
+              reinterpret_cast<uint4*>(stage + lane * 256)[chunk ^ (lane & 7)] = v;
+            }
+          }
+        }
+        if (valid) {
+          if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+          else if (p.lse) p.lse[row] = kv16_lse(m, l);
+        }
+        __syncwarp();
+        if (p.splits == 1) {
+          // two rows at a time, 16 lanes each: whole rows of 256 B
+#pragma unroll 4
+          for (int i = 0; i < 32; i += 2) {
+            const int src = i + (lane >> 4);
+            const long long dst = __shfl_sync(0xffffffffu, row, src);
+            const bool there = __shfl_sync(0xffffffffu, (int)valid, src);
+            const uint4 v = reinterpret_cast<const uint4*>(stage + src * 256)[(lane & 15) ^ (src & 7)];
+            if (there) reinterpret_cast<uint4*>(p.out + dst * kD)[lane & 15] = v;
+          }
+        }
+        // rows with a result that is not finite, token by token
+        for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
+          const int src = __ffs(bad) - 1;
+          const long long rw = __shfl_sync(0xffffffffu, row, src);
+          const int a = __shfl_sync(0xffffffffu, at, src);
+          const long long token = rw / p.q.Hq;
+          const int hd = (int)(rw - token * p.q.Hq);
+          float mm, ll, oo[4];
+          kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)hd * kD, b, h, a, sp,
+                           k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
+                           p.q.scale_log2, mm, ll, oo);
+          if (p.splits > 1) {
+            float* d = p.part + (rw * p.splits + split) * kRecFloats;
+            if (lane == 0) *reinterpret_cast<float2*>(d) = make_float2(mm, ll);
+            *reinterpret_cast<float4*>(d + 4 + 4 * lane) = make_float4(oo[0], oo[1], oo[2], oo[3]);
+          } else {
+            store_row4<T>(p, rw, lane, oo, ll == 0.0f ? 0.0f : 1.0f / ll);
+            if (p.lse && lane == 0) p.lse[rw] = kv16_lse(mm, ll);
+          }
+        }
+      }
+      tc5_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc5_fence_after();
+    tc5_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits' records of a (query, head), a warp each; queries that
+// belong to no sequence are left alone.
+template <class T>
+__global__ void __launch_bounds__(128) kv16_join_kernel(const AttnParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (long long)p.q.total * p.q.Hq) return;
+  const int b = ragged_sequence(p.q.start, p.c.B, (int)(row / p.q.Hq));
+  if (b < 0 || __ldg(p.q.start + b) < 0 || __ldg(p.q.start + b + 1) > p.q.total) return;
+  const float* rec = p.part + row * p.splits * kRecFloats;
+  float M = -INFINITY, L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < p.splits; ++s) M = fmaxf(M, rec[s * kRecFloats]);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(rec + s * kRecFloats);
+    const float4 v = *reinterpret_cast<const float4*>(rec + s * kRecFloats + 4 + 4 * lane);
+    const float a = M == -INFINITY ? 1.0f : fast_exp2(ml.x - M);
+    L += a * ml.y;
+    o[0] += a * v.x;
+    o[1] += a * v.y;
+    o[2] += a * v.z;
+    o[3] += a * v.w;
+  }
+  store_row4<T>(p, row, lane, o, L == 0.0f ? 0.0f : 1.0f / L);
+  if (p.lse && lane == 0) p.lse[row] = kv16_lse(M, L);
+}
+
+// Upper bound on the CTAs of one KV head: every sequence's last may be partial.
+long long attention_tiles(int B, int g, int total) {
+  const int two = 2 * (128 / g);
+  return (long long)total / two + B;
+}
+
+// Splits of the key tiles: so many that the CTAs fill the SMs about once, each
+// with at least four key tiles.
+int attention_splits(const Kv16& c, int Hq, int total, int max_tok, int window, int n_sink) {
+  const int g = Hq / c.Hkv, two = 2 * (128 / g);
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 152;
+  const long long ctas = ((total + two - 1) / two + std::min(c.B, total) - 1LL) * c.Hkv;
+  long long keys = std::min(max_tok, c.cap);
+  if (window > 0) keys = std::min<long long>(keys, (long long)window + two + n_sink + 3 * kPage);
+  const long long by_keys = keys / (4 * 128);
+  return (int)std::max<long long>(1, std::min<long long>({sms / std::max(1LL, ctas), by_keys, 64}));
+}
+
+template <class T>
+cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  if (!kv16_query_map(&mq, p.q, p.c.half, p.g, p.tokens) || !kv16_row_map(&mk, p.c, p.c.k) ||
+      !kv16_row_map(&mv, p.c, p.c.v))
+    return cudaErrorNotSupported;
+  const auto kernel = kv16_attention_kernel<T>;
+  constexpr int smem = (2 + kStages) * kTileBytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(p.tiles * p.c.Hkv, p.splits), kThreads, smem, s>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  *launches = 1;
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const long long rows = (long long)p.q.total * p.q.Hq;
+  kv16_join_kernel<T><<<(int)((rows + 3) / 4), 128, 0, s>>>(p);
+  *launches = 2;
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv16_rows(const Kv16& c, const Kv16Query& q, uint16_t* out, float* lse,
-                             cudaStream_t s) {
-  const int grid = (q.total * q.Hq + kWarps - 1) / kWarps;
-  if (c.half)
-    kv16_rows_kernel<Fp16><<<grid, kWarps * 32, 0, s>>>(c, q, out, lse);
-  else
-    kv16_rows_kernel<Bf16><<<grid, kWarps * 32, 0, s>>>(c, q, out, lse);
-  return cudaGetLastError();
+size_t kv16_attention_ws_bytes(const Kv16& c, int Hq, int total, int max_tok, int window,
+                               int n_sink) {
+  const int splits = attention_splits(c, Hq, total, max_tok, window, n_sink);
+  return splits > 1 ? (size_t)total * Hq * splits * kRecFloats * sizeof(float) : 0;
 }
 
-size_t kv16_attention_ws_bytes(const Kv16&, int, int, int, int, int) { return 0; }
-
 cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* out, float* lse,
-                                  void*, int* launches, cudaStream_t s) {
-  *launches = 1;
-  return launch_kv16_rows(c, q, out, lse, s);
+                                  void* ws, int* launches, cudaStream_t s) {
+  AttnParams p;
+  p.c = c;
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.part = static_cast<float*>(ws);
+  p.g = q.Hq / c.Hkv;
+  p.tokens = 128 / p.g;
+  const long long tiles = attention_tiles(c.B, p.g, q.total);
+  if (tiles * c.Hkv > 0x7fffffffLL) return cudaErrorInvalidValue;
+  p.tiles = (int)tiles;
+  p.splits = attention_splits(c, q.Hq, q.total, q.max_tok, q.window, q.n_sink);
+  // a negative scale becomes a negated Q in the product, so that the largest
+  // score is always the largest sum; a scale of 0 a scale too small to matter,
+  // so that a masked -inf stays one
+  p.negate = q.scale_log2 < 0.0f;
+  p.scale = std::max(std::fabs(q.scale_log2), 1e-30f);
+  return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);
 }
 
 }  // namespace oscar

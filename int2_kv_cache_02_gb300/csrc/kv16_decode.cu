@@ -27,6 +27,7 @@
 
 #include "kv16.cuh"
 #include "kv16_tma.h"
+#include "tc5.cuh"
 
 namespace oscar {
 
@@ -123,15 +124,6 @@ __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, c
   r.sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
 }
 
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* m, int x, int y,
-                                        uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -216,10 +208,10 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp], kSlotBytes);
-      tma_box(slot, &map_k, 0, row, &full[warp]);
-      tma_box(slot + 4096, &map_k, 64, row, &full[warp]);
-      tma_box(slot + 8192, &map_v, 0, row, &full[warp]);
-      tma_box(slot + 12288, &map_v, 64, row, &full[warp]);
+      tma_box2(slot, &map_k, 0, row, &full[warp]);
+      tma_box2(slot + 4096, &map_k, 64, row, &full[warp]);
+      tma_box2(slot + 8192, &map_v, 0, row, &full[warp]);
+      tma_box2(slot + 12288, &map_v, 64, row, &full[warp]);
     }
   };
   int x = x0 + warp;                // the warp's next page to work on

@@ -30,4 +30,18 @@ inline bool kv16_row_map(CUtensorMap* m, const Kv16& c, const uint16_t* base) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [total][Hq][128], fetched 64 columns x g heads x `tokens` rows
+// at a time with the 128-byte swizzle; rows past the end read 0.
+inline bool kv16_query_map(CUtensorMap* m, const Kv16Query& q, bool half, int g, int tokens) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {OSCAR_HEAD_DIM, (cuuint64_t)q.Hq, (cuuint64_t)q.total};
+  const cuuint64_t strides[2] = {OSCAR_HEAD_DIM * 2, (cuuint64_t)q.stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)tokens}, step[3] = {1, 1, 1};
+  return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<uint16_t*>(q.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace oscar
