@@ -1,65 +1,446 @@
-// Attention weight of stored tokens under a ragged batch of queries.
+// Attention weight of stored tokens under a ragged batch of queries, on the
+// tcgen05 tensor cores: weight[j] += sum over rows i of 2^(scale s_ij - lse_i),
+// a row being a (query, head of the group) pair.  The log of the sum is known,
+// so nothing is kept per row and the value side is not read: 2 * 128 flops and
+// one exponential per visible pair and head.
+//
+// Tiles.  S^T = K Q^T with 128 keys as the rows of a tile: a thread owns a key
+// and adds up its row of S^T, so the column sum of the probabilities needs no
+// exchange between threads and has one order.  A work item is 256 keys (two
+// tiles, a warpgroup each) of one (sequence, KV head): its keys stay in shared
+// memory while the query tiles (128 rows, token-major as in kv16_attention)
+// that see any of them stream by, each used twice, 32 KB per 1024 tensor
+// cycles.  With 128 keys per item the query tiles alone would take all of an
+// SM's 64 B per cycle from L2.
+//
+// Many items: one CTA per SM walks over them, the next item's keys on their way
+// while it works.  Few (few heads or short caches): the query tiles of an item
+// are cut over a cluster's CTAs, which hand their sums to the first through
+// distributed shared memory, added in order of rank.
+//
+// Roles (12 warps): two warpgroups that sum, one warp that copies, one that
+// issues the MMAs, two that lay out the query rows' lse.
+// TMEM: two buffers of S^T for each warpgroup.
 #include <algorithm>
 
 #include "kv16.cuh"
+#include "kv16_tma.h"
+#include "tc5.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kTileBytes = 32768, kHalf = 16384;
+constexpr int kQStages = 3, kKBufs = 2, kLseSlots = 3;
+constexpr int kItemKeys = 256;
 
-// A warp per (token, KV head), over the sequence's queries in order.
+struct AccParams {
+  Kv16 c;
+  Kv16Query q;
+  const float* lse;
+  int n_obs, g, tokens;
+  int items;        // key blocks * B * Hkv
+  int cluster;      // CTAs that share an item
+};
+
+struct Smem {
+  uint64_t k_full[kKBufs], k_empty[kKBufs], q_full[kQStages], q_empty[kQStages];
+  uint64_t s_full[2][2], s_empty[2][2], l_full[kLseSlots], l_empty[kLseSlots], drain;
+  uint32_t tmem;
+  int abort;
+  alignas(16) float lse[kLseSlots][128];   // at the end: the CTA's sums
+};
+static_assert(kLseSlots * 128 >= kItemKeys, "room for the sums");
+
+// A work item as every role sees it; t1 <= t0: nothing to do.
+struct Item {
+  int b, h, key0, n;
+  int r0, at_first;   // first row of the sequence's queries, its position
+  int ia, ib;         // its queries that may see a key of the item
+  int t0, t1;         // this CTA's query tiles of them
+  int halves;         // key tiles that hold tokens
+};
+
+__device__ __forceinline__ Item find_item(const AccParams& p, int x, int rank, bool report) {
+  Item it;
+  const int rows = p.c.B * p.c.Hkv;
+  const int kb = x / rows, row = x - kb * rows;     // the first keys have the most queries
+  it.b = row / p.c.Hkv;
+  it.h = row - it.b * p.c.Hkv;
+  it.key0 = kb * kItemKeys;
+  it.t0 = it.t1 = 0;
+  it.halves = 0;
+  const int n = __ldg(p.c.n_tok + it.b);
+  const int r0 = __ldg(p.q.start + it.b), r1 = __ldg(p.q.start + it.b + 1), nq = r1 - r0;
+  it.n = n;
+  it.r0 = r0;
+  if (n < 0 || n > p.c.cap || n > p.q.max_tok || r0 < 0 || r1 > p.q.total || nq < 0 || nq > n) {
+    if (report && kb == 0) record_error(p.c.status, kDevErrBadPaged);
+    return it;
+  }
+  if (it.key0 >= n) return it;
+  it.at_first = n - nq;
+  it.ia = max(max(0, it.key0 - it.at_first), p.n_obs > 0 ? nq - p.n_obs : 0);
+  it.ib = nq;
+  const int last = min(it.key0 + kItemKeys, n) - 1;
+  if (p.q.window > 0 && it.key0 >= p.q.n_sink)
+    it.ib = (int)min((long long)nq, (long long)last + p.q.window - it.at_first);
+  if (it.ib <= it.ia) return it;
+  const int nt = (it.ib - it.ia + p.tokens - 1) / p.tokens;
+  it.t0 = (int)((long long)nt * rank / p.cluster);
+  it.t1 = (int)((long long)nt * (rank + 1) / p.cluster);
+  it.halves = n - it.key0 > 128 ? 2 : 1;
+  return it;
+}
+
 template <class T>
-__global__ void __launch_bounds__(kWarps * 32)
-kv16_weight_kernel(const Kv16 c, const Kv16Query q, const float* __restrict__ lse, int n_obs) {
-  const int lane = threadIdx.x & 31;
-  const int j = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
-  const int n = kv16_length(c, b, q.max_tok);
-  if (n < 0) {
-    if (lane == 0 && j == 0) record_error(c.status, kDevErrBadPaged);
-    return;
-  }
-  if (j >= n) return;
-  const int r1 = q.start ? min(__ldg(q.start + b + 1), q.total) : b + 1;
-  int r0 = q.start ? max(0, __ldg(q.start + b)) : b;
-  if (r1 - r0 > n) {
-    if (lane == 0) record_error(c.status, kDevErrBadPaged);
-    return;
-  }
-  if (n_obs > 0) r0 = max(r0, r1 - n_obs);
-  const int row = kv16_block_row(c, b, h, j / kPage);
-  if (row < 0) {
-    if (lane == 0) record_error(c.status, kDevErrBadPaged);
-    return;
-  }
-  const uint2 kr = reinterpret_cast<const uint2*>(c.k)[((long long)row + j % kPage) * 32 + lane];
-  const float2 k0 = T::unpack(kr.x), k1 = T::unpack(kr.y);
-  const int g = q.Hq / c.Hkv;
-  float w = 0.0f;
-  for (int r = r0; r < r1; ++r) {
-    if (!kv16_visible(j, n - (r1 - r), q.window, q.n_sink)) continue;
-    for (int i = 0; i < g; ++i) {
-      const uint2 qr = reinterpret_cast<const uint2*>(q.q + r * q.stride + (h * g + i) * kD)[lane];
-      const float2 q0 = T::unpack(qr.x), q1 = T::unpack(qr.y);
-      float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      w += fast_exp2(s * q.scale_log2 - lse[(long long)r * q.Hq + h * g + i] * kLog2e);
+__global__ void __launch_bounds__(kThreads, 1)
+kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k, const AccParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Smem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % p.cluster, first = blockIdx.x / p.cluster;
+  const int step = gridDim.x / p.cluster;
+  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t* kbuf = smem;                                    // [kKBufs][2] key tiles
+  uint8_t* qring = smem + kKBufs * 2 * kTileBytes;         // [kQStages] query tiles
+
+  if (warp == 8) tc5_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < kKBufs; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
     }
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm.s_full[w][i], 1);
+        mbar_init(&sm.s_empty[w][i], 128);
+      }
+    for (int i = 0; i < kLseSlots; ++i) {
+      mbar_init(&sm.l_full[i], 64);
+      mbar_init(&sm.l_empty[i], 256);
+    }
+    mbar_init(&sm.drain, 1);
+    mbar_fence_init();
+    sm.abort = 0;
   }
-  if (lane == 0) c.weight[(long long)row + j % kPage] += w;
+  float sum = 0.0f;      // of the thread's key
+  // query rows that no copy fills (groups that do not divide 128) hold zeros
+  const int pad = 128 - p.g * p.tokens;
+  for (int i = tid; i < kQStages * 2 * pad * 8; i += kThreads) {
+    const int tile = i / (pad * 8), rest = i - tile * pad * 8;
+    reinterpret_cast<uint4*>(qring + tile * kHalf + (p.g * p.tokens) * 128)[rest] =
+        make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort = &sm.abort;
+  bool ok = true;
+
+  if (warp == 8) {
+    // -------------------------------------------------------------- copies
+    const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
+                               : p.c.B * p.c.Hkv * p.c.T_cap;        // reads zeros
+    int uk = 0, uq = 0;
+    for (int x = first; x < p.items && ok; x += step) {
+      const Item it = find_item(p, x, rank, rank == 0 && lane == 0);
+      if (it.t1 <= it.t0) continue;
+      int row = none;
+      if (lane < 8) {
+        const int blk = it.key0 / kPage + lane;
+        if (blk * kPage < it.n) {
+          row = kv16_block_row(p.c, it.b, it.h, blk);
+          if (row < 0) {
+            record_error(p.c.status, kDevErrBadPaged);
+            row = none;
+          }
+        }
+      }
+      const int kb = uk % kKBufs;
+      if (uk >= kKBufs) ok = tc5_wait(&sm.k_empty[kb], (uk / kKBufs - 1) & 1, abort);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[kb], it.halves * kTileBytes);
+      for (int i = 0; i < 4 * it.halves; ++i) {
+        const int y = __shfl_sync(0xffffffffu, row, i);
+        if (lane == 0) {
+          uint8_t* dst = kbuf + (kb * 2 + i / 4) * kTileBytes + (i & 3) * 4096;
+          tma_box2(dst, &map_k, 0, y, &sm.k_full[kb]);
+          tma_box2(dst + kHalf, &map_k, 64, y, &sm.k_full[kb]);
+        }
+      }
+      __syncwarp();
+      ++uk;
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int st = uq % kQStages;
+        if (uq >= kQStages) ok = tc5_wait(&sm.q_empty[st], (uq / kQStages - 1) & 1, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full[st], 2 * 64 * 2 * p.g * p.tokens);
+          uint8_t* dst = qring + st * kTileBytes;
+          tma_box3(dst, &map_q, 0, it.h * p.g, it.r0 + it.ia + t * p.tokens, &sm.q_full[st]);
+          tma_box3(dst + kHalf, &map_q, 64, it.h * p.g, it.r0 + it.ia + t * p.tokens, &sm.q_full[st]);
+        }
+        __syncwarp();
+        ++uq;
+      }
+    }
+    if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    if (*abort) {
+      // what is in flight lands before the memory is given back
+      for (int i = max(0, uk - kKBufs); i < uk; ++i)
+        if (!mbar_wait_bounded(&sm.k_full[i % kKBufs], (i / kKBufs) & 1, kDrainLimit) && lane == 0)
+          record_error(p.c.status, kDevErrDrainTimeout);
+      for (int i = max(0, uq - kQStages); i < uq; ++i)
+        if (!mbar_wait_bounded(&sm.q_full[i % kQStages], (i / kQStages) & 1, kDrainLimit) && lane == 0)
+          record_error(p.c.status, kDevErrDrainTimeout);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMAs
+    const uint32_t idesc = tc5_idesc(T::kHalf, 128, 128, false, false);
+    const uint64_t base = tc5_desc_base(16, 1024);
+    int uk = 0, uq = 0, us[2] = {0, 0};
+    for (int x = first; x < p.items && ok; x += step) {
+      const Item it = find_item(p, x, rank, false);
+      if (it.t1 <= it.t0) continue;
+      const int kb = uk % kKBufs;
+      ok = tc5_wait(&sm.k_full[kb], (uk / kKBufs) & 1, abort);
+      for (int t = it.t0; t < it.t1 && ok; ++t) {
+        const int st = uq % kQStages;
+        ok = tc5_wait(&sm.q_full[st], (uq / kQStages) & 1, abort);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (w >= it.halves || !ok) break;
+          const int buf = us[w] & 1;
+          if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, abort);
+          if (!ok) break;
+          tc5_fence_after();
+          if (lane == 0) {
+            const unsigned ka = smem_u32(kbuf + (kb * 2 + w) * kTileBytes);
+            const unsigned qa = smem_u32(qring + st * kTileBytes);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const unsigned off = (i >> 2) * kHalf + (i & 3) * 32;
+              tc5_mma_ss(tmem + 256 * w + 128 * buf, tc5_desc(base, ka + off),
+                         tc5_desc(base, qa + off), idesc, i > 0);
+            }
+            tc5_commit(&sm.s_full[w][buf]);
+          }
+          __syncwarp();
+          ++us[w];
+        }
+        if (ok && lane == 0) tc5_commit(&sm.q_empty[st]);
+        __syncwarp();
+        ++uq;
+      }
+      if (ok && lane == 0) tc5_commit(&sm.k_empty[kb]);
+      __syncwarp();
+      ++uk;
+    }
+    // the summing warps have seen every product they waited for; the last
+    // commits' arrivals land before the CTA ends
+    if (lane == 0) {
+      if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
+      tc5_commit(&sm.drain);
+      if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit)) record_error(p.c.status, kDevErrDrainTimeout);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ---------------------------------------------- lse of the rows
+    int ul = 0;
+    const int i0 = tid - 320;
+    for (int x = first; x < p.items && ok; x += step) {
+      const Item it = find_item(p, x, rank, false);
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int slot = ul % kLseSlots;
+        float v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = i0 + 64 * k, tok = r / p.g, head = r - tok * p.g;
+          const int q = it.ia + t * p.tokens + tok;
+          const bool there = tok < p.tokens && q < it.ib;
+          v[k] = there ? -kLog2e * __ldg(p.lse + (long long)(it.r0 + q) * p.q.Hq + it.h * p.g + head)
+                       : -INFINITY;
+        }
+        if (ul >= kLseSlots) ok = tc5_wait(&sm.l_empty[slot], (ul / kLseSlots - 1) & 1, abort);
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sm.lse[slot][i0 + 64 * k] = v[k];
+        mbar_arrive(&sm.l_full[slot]);
+        ++ul;
+      }
+    }
+    if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+  } else {
+    // ---------------------------------------------------------------- sums
+    const int w = warp >> 2;
+    const uint32_t s_base = tmem + ((uint32_t)(warp & 3) << 21) + 256 * w;
+    const float2 sc = make_float2(p.q.scale_log2, p.q.scale_log2);
+    int ul = 0, us = 0;
+    for (int x = first; x < p.items && ok; x += step) {
+      const Item it = find_item(p, x, rank, false);
+      if (it.t1 <= it.t0) continue;
+      const int tile0 = it.key0 + 128 * w, j = tile0 + (tid & 127);
+      float2 a0 = make_float2(0.0f, 0.0f), a1 = a0;
+      for (int t = it.t0; t < it.t1; ++t) {
+        const int slot = ul % kLseSlots;
+        ok = tc5_wait(&sm.l_full[slot], (ul / kLseSlots) & 1, abort);
+        if (!ok) break;
+        if (w < it.halves) {
+          const int buf = us & 1;
+          ok = tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, abort);
+          if (!ok) break;
+          tc5_fence_after();
+          // the tokens [lo, hi) of the tile that see the thread's key: rows are
+          // token-major, so they are columns [lo g, hi g)
+          const int q_lo = it.ia + t * p.tokens, ntok = min(p.tokens, it.ib - q_lo);
+          const int at = it.at_first + q_lo;
+          const int lo = max(0, j - at);
+          int hi = ntok;
+          if (p.q.window > 0 && j >= p.q.n_sink)
+            hi = (int)min((long long)hi, max(0LL, (long long)j + p.q.window - at));
+          const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == p.tokens);
+          const int clo = min(lo, 128) * p.g;
+          const unsigned cn = max(hi - lo, 0) * p.g;
+          const float* ls = sm.lse[slot];
+          uint32_t s0[64], s1[64];
+          const uint32_t sa = s_base + 128 * buf;
+          auto add = [&](const uint32_t* s, int c0) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const float4 z = *reinterpret_cast<const float4*>(ls + c0 + e);
+              float2 u = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc,
+                              make_float2(z.x, z.y));
+              float2 v = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sc,
+                              make_float2(z.z, z.w));
+              u = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+              v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+              if (!whole) {
+                const int c = c0 + e - clo;
+                u.x = (unsigned)c < cn ? u.x : 0.0f;
+                u.y = (unsigned)(c + 1) < cn ? u.y : 0.0f;
+                v.x = (unsigned)(c + 2) < cn ? v.x : 0.0f;
+                v.y = (unsigned)(c + 3) < cn ? v.y : 0.0f;
+              }
+              a0 = add2(a0, u);
+              a1 = add2(a1, v);
+            }
+          };
+          tc5_ld32(s0, sa);
+          tc5_ld32(s0 + 32, sa + 32);
+          tc5_wait_ld();
+          tc5_ld32(s1, sa + 64);
+          tc5_ld32(s1 + 32, sa + 96);
+          add(s0, 0);
+          tc5_wait_ld();
+          tc5_fence_before();
+          mbar_arrive(&sm.s_empty[w][buf]);
+          add(s1, 64);
+          ++us;
+        }
+        mbar_arrive(&sm.l_empty[slot]);
+        ++ul;
+      }
+      sum = (a0.x + a0.y) + (a1.x + a1.y);
+      if (p.cluster == 1 && ok && j < it.n) {
+        const int row = kv16_block_row(p.c, it.b, it.h, j / kPage);
+        if (row >= 0) p.c.weight[(long long)row + j % kPage] += sum;
+      }
+    }
+    if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    tc5_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc5_fence_after();
+    tc5_dealloc(tmem, 512);
+  }
+  if (p.cluster > 1) {
+    // one item per cluster: its sums in order of rank
+    float* sums = sm.lse[0];
+    if (tid < kItemKeys) sums[tid] = sum;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0 && tid < kItemKeys && first < p.items) {
+      const Item it = find_item(p, first, 0, false);
+      const int j = it.key0 + tid;
+      if (it.halves > 0 && j < it.n) {
+        float all = 0.0f;
+        for (int r = 0; r < p.cluster; ++r) {
+          unsigned far;
+          float v;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(smem_u32(sums + tid)), "r"(r));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
+          all += v;
+        }
+        const int row = kv16_block_row(p.c, it.b, it.h, j / kPage);
+        if (row >= 0) p.c.weight[(long long)row + j % kPage] += all;
+      }
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+template <class T>
+cudaError_t launch(AccParams p, cudaStream_t s) {
+  CUtensorMap mq, mk;
+  if (!kv16_query_map(&mq, p.q, p.c.half, p.g, p.tokens) || !kv16_row_map(&mk, p.c, p.c.k))
+    return cudaErrorNotSupported;
+  int dev = 0, sms = 152;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // two items for every SM keep the SMs about equally busy; fewer are cut over
+  // clusters until the CTAs are three for every SM, at two query tiles or more each
+  const long long rows = p.n_obs > 0 ? std::min<long long>(p.q.total, (long long)p.n_obs * p.c.B)
+                                     : p.q.total;
+  const long long tiles = std::max(1LL, rows / p.c.B / p.tokens);
+  p.cluster = 1;
+  if (p.items < 2 * sms)
+    while (p.cluster < 8 && (long long)p.items * p.cluster < 3LL * sms && tiles >= 4 * p.cluster)
+      p.cluster *= 2;
+  const auto kernel = kv16_accumulate_kernel<T>;
+  constexpr int smem = (kKBufs * 2 + kQStages) * kTileBytes + 1024;
+  static_assert(smem + (int)sizeof(Smem) <= 227 * 1024, "shared memory of a CTA");
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.cluster > 1 ? p.items * p.cluster : std::min(p.items, sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const float* lse, int n_obs,
                                    cudaStream_t s) {
-  const dim3 grid((std::min(q.max_tok, c.cap) + kWarps - 1) / kWarps, c.Hkv, c.B);
-  if (c.half)
-    kv16_weight_kernel<Fp16><<<grid, kWarps * 32, 0, s>>>(c, q, lse, n_obs);
-  else
-    kv16_weight_kernel<Bf16><<<grid, kWarps * 32, 0, s>>>(c, q, lse, n_obs);
-  return cudaGetLastError();
+  AccParams p;
+  p.c = c;
+  p.q = q;
+  p.lse = lse;
+  p.n_obs = n_obs;
+  p.g = q.Hq / c.Hkv;
+  p.tokens = 128 / p.g;
+  const long long blocks = ((long long)std::min(q.max_tok, c.cap) + kItemKeys - 1) / kItemKeys;
+  const long long items = blocks * c.B * c.Hkv;
+  if (items > 0x3fffffffLL) return cudaErrorInvalidValue;
+  p.items = (int)items;
+  return c.half ? launch<Fp16>(p, s) : launch<Bf16>(p, s);
 }
 
 }  // namespace oscar

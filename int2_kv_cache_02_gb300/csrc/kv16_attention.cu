@@ -282,10 +282,12 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (more && w == last) release(ks);
         }
       }
-      if (!ok && lane == 0) {
-        record_error(p.c.status, kDevErrWaitTimeout);
+      // the last commits' arrivals land before the CTA ends
+      if (lane == 0) {
+        if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
         tc5_commit(&sm.drain);
-        mbar_wait_bounded(&sm.drain, 0, kDrainLimit);
+        if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
+          record_error(p.c.status, kDevErrDrainTimeout);
       }
       __syncwarp();
     }
