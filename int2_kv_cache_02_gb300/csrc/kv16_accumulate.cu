@@ -120,11 +120,11 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     for (int w = 0; w < 2; ++w)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.s_full[w][i], 1);
-        mbar_init(&sm.s_empty[w][i], 128);
+        mbar_init(&sm.s_empty[w][i], 4);
       }
     for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(&sm.l_full[i], 64);
-      mbar_init(&sm.l_empty[i], 256);
+      mbar_init(&sm.l_full[i], 2);
+      mbar_init(&sm.l_empty[i], 8);
     }
     mbar_init(&sm.drain, 1);
     mbar_fence_init();
@@ -205,52 +205,51 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t idesc = tc5_idesc(T::kHalf, 128, 128, false, false);
-    const uint64_t base = tc5_desc_base(16, 1024);
-    int uk = 0, uq = 0, us[2] = {0, 0};
-    for (int x = first; x < p.items && ok; x += step) {
-      const Item it = find_item(p, x, rank, false);
-      if (it.t1 <= it.t0) continue;
-      const int kb = uk % kKBufs;
-      ok = tc5_wait(&sm.k_full[kb], (uk / kKBufs) & 1, abort);
-      for (int t = it.t0; t < it.t1 && ok; ++t) {
-        const int st = uq % kQStages;
-        ok = tc5_wait(&sm.q_full[st], (uq / kQStages) & 1, abort);
+    if (elect_one()) {
+      const uint32_t idesc = tc5_idesc(T::kHalf, 128, 128, false, false);
+      constexpr uint64_t kBase = tc5_desc_base(16, 1024);
+      const uint64_t dk = tc5_desc(kBase, smem_u32(kbuf)), dq = tc5_desc(kBase, smem_u32(qring));
+      unsigned kb = 0, kp = 0, st = 0, sp = 0, us[2] = {0, 0};
+      for (int x = first; x < p.items && ok; x += step) {
+        const Item it = find_item(p, x, rank, false);
+        if (it.t1 <= it.t0) continue;
+        ok = tc5_wait(&sm.k_full[kb], kp, abort);
+        for (int t = it.t0; t < it.t1 && ok; ++t) {
+          ok = tc5_wait(&sm.q_full[st], sp, abort);
+          const uint64_t q = dq + st * (kTileBytes >> 4);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (w >= it.halves || !ok) break;
-          const int buf = us[w] & 1;
-          if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, abort);
-          if (!ok) break;
-          tc5_fence_after();
-          if (lane == 0) {
-            const unsigned ka = smem_u32(kbuf + (kb * 2 + w) * kTileBytes);
-            const unsigned qa = smem_u32(qring + st * kTileBytes);
+          for (int w = 0; w < 2; ++w) {
+            if (w >= it.halves || !ok) break;
+            const unsigned buf = us[w] & 1;
+            if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, abort);
+            if (!ok) break;
+            tc5_fence_after();
+            const uint64_t k = dk + (kb * 2 + w) * (kTileBytes >> 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const unsigned off = (i >> 2) * kHalf + (i & 3) * 32;
-              tc5_mma_ss(tmem + 256 * w + 128 * buf, tc5_desc(base, ka + off),
-                         tc5_desc(base, qa + off), idesc, i > 0);
+              const unsigned off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+              tc5_mma_ss(tmem + 256 * w + 128 * buf, k + off, q + off, idesc, i > 0);
             }
             tc5_commit(&sm.s_full[w][buf]);
+            ++us[w];
           }
-          __syncwarp();
-          ++us[w];
+          if (ok) tc5_commit(&sm.q_empty[st]);
+          if (++st == kQStages) {
+            st = 0;
+            sp ^= 1;
+          }
         }
-        if (ok && lane == 0) tc5_commit(&sm.q_empty[st]);
-        __syncwarp();
-        ++uq;
+        if (ok) tc5_commit(&sm.k_empty[kb]);
+        if (++kb == kKBufs) {
+          kb = 0;
+          kp ^= 1;
+        }
       }
-      if (ok && lane == 0) tc5_commit(&sm.k_empty[kb]);
-      __syncwarp();
-      ++uk;
-    }
-    // the summing warps have seen every product they waited for; the last
-    // commits' arrivals land before the CTA ends
-    if (lane == 0) {
+      // the last commits' arrivals land before the CTA ends
       if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
       tc5_commit(&sm.drain);
-      if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit)) record_error(p.c.status, kDevErrDrainTimeout);
+      if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
+        record_error(p.c.status, kDevErrDrainTimeout);
     }
     __syncwarp();
   } else if (warp >= 10) {
@@ -274,7 +273,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 2; ++k) sm.lse[slot][i0 + 64 * k] = v[k];
-        mbar_arrive(&sm.l_full[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.l_full[slot]);
         ++ul;
       }
     }
@@ -342,11 +342,13 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
           add(s0, 0);
           tc5_wait_ld();
           tc5_fence_before();
-          mbar_arrive(&sm.s_empty[w][buf]);
+          __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
           add(s1, 64);
           ++us;
         }
-        mbar_arrive(&sm.l_empty[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.l_empty[slot]);
         ++ul;
       }
       sum = (a0.x + a0.y) + (a1.x + a1.y);

@@ -69,7 +69,7 @@ struct RowPlace {
 };
 
 struct Smem {
-  uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], clean, drain;
   uint32_t tmem;
   int abort;
 };
@@ -125,6 +125,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   const int k1_0 = min(k1, max(k0, (blocks0 + kKeyPages - 1) / kKeyPages));
   const int cnt[2] = {ntile == 2 ? k1_0 - k0 : k1 - k0, ntile == 2 ? k1 - k0 : 0};
 
+  // the key tile with the last page of the sequence, if tokens are missing from it
+  const int tail = (sp.blocks - 1) / kKeyPages - k0;
+  const int clear_at = k1 > k0 && k1 == kt_all && n % kPage != 0 &&
+                               sp.block(sp.blocks - 1) == (n - 1) / kPage ? tail : -1;
+
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   uint8_t* sq = smem;                            // two query tiles
   uint8_t* ring = smem + 2 * kTileBytes;
@@ -138,9 +143,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
     }
+    mbar_init(&sm.clean, 1);
     mbar_init(&sm.drain, 1);
     mbar_fence_init();
     sm.abort = 0;
@@ -207,89 +213,81 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       }
     } else if (warp == 9 && k1 > k0) {
       // -------------------------------------------------------------- MMAs
-      const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
-      const uint32_t id_o = tc5_idesc(T::kHalf, 128, 128, true, false);
-      const uint64_t along_k = tc5_desc_base(16, 1024);          // Q, K
-      const uint64_t along_n = tc5_desc_base(kHalf, 1024);       // V
-      auto qk = [&](int w, const uint8_t* ktile) {
-        const unsigned qa = smem_u32(sq + w * kTileBytes), ka = smem_u32(ktile);
-        if (lane == 0) {
+      if (elect_one()) {
+        const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
+        const uint32_t id_o = tc5_idesc(T::kHalf, 128, 128, true, false);
+        constexpr uint64_t kAlongK = tc5_desc_base(16, 1024);          // Q, K
+        constexpr uint64_t kAlongN = tc5_desc_base(kHalf, 1024);       // V
+        const uint64_t dq = tc5_desc(kAlongK, smem_u32(sq));
+        const unsigned ring_addr = smem_u32(ring);
+        auto qk = [&](int w, unsigned stage) {
+          const uint64_t a = dq + w * (kTileBytes >> 4);
+          const uint64_t k = tc5_desc(kAlongK, ring_addr + stage * kTileBytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const unsigned off = (i >> 2) * kHalf + (i & 3) * 32;
-            tc5_mma_ss(tmem + 128 * w, tc5_desc(along_k, qa + off), tc5_desc(along_k, ka + off),
-                       id_s, i > 0);
+            const unsigned off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+            tc5_mma_ss(tmem + 128 * w, a + off, k + off, id_s, i > 0);
           }
           tc5_commit(&sm.s_full[w]);
+        };
+        const int last = ntile - 1, nk = k1 - k0;
+        bool ok = tc5_wait(&sm.q_full, 0, abort) && tc5_wait(&sm.full[0], 0, abort);
+        if (ok) {
+          if (cnt[0] > 0) qk(0, 0);
+          if (cnt[1] > 0) qk(1, 0);
+          tc5_commit(&sm.empty[0]);
         }
-        __syncwarp();
-      };
-      auto release = [&](int st) {
-        if (lane == 0) tc5_commit(&sm.empty[st]);
-        __syncwarp();
-      };
-      const int last = ntile - 1, nk = k1 - k0;
-      bool ok = tc5_wait(&sm.q_full, 0, abort) && tc5_wait(&sm.full[0], 0, abort);
-      if (ok) {
-        tc5_fence_after();
-        for (int w = 0; w < ntile; ++w)
-          if (cnt[w] > 0) qk(w, ring);
-        release(0);
-      }
-      for (int j = 0; j < nk && ok; ++j) {
-        // stages: K_j is number 2j, V_j 2j + 1
-        const int vs = (2 * j + 1) % kStages, ks = (2 * j + 2) % kStages;
-        uint8_t* vt = ring + vs * kTileBytes;
-        ok = tc5_wait(&sm.full[vs], ((2 * j + 1) / kStages) & 1, abort);
-        if (!ok) break;
-        // the rows behind the sequence's last token hold anything: clear them
-        const int last_page = sp.blocks - 1 - (k0 + j) * kKeyPages;
-        if (last_page >= 0 && last_page < kKeyPages) {
-          const int blk = sp.block(sp.blocks - 1);
-          const int r = blk * kPage + lane;
-          if (r >= n) {
+        // stages in turn: K_0 V_0 K_1 V_1 ...
+        unsigned vs = 1, vp = 0;
+        for (int j = 0; j < nk && ok; ++j) {
+          const unsigned ks = vs + 1 == kStages ? 0 : vs + 1, kp = vs + 1 == kStages ? vp ^ 1 : vp;
+          const bool more = j + 1 < nk;
+          ok = tc5_wait(&sm.full[vs], vp, abort);
+          // the tile with the sequence's last page: its tail is cleared first
+          if (ok && j == clear_at) ok = tc5_wait(&sm.clean, 0, abort);
+          if (ok && more) ok = tc5_wait(&sm.full[ks], kp, abort);
+          const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              reinterpret_cast<uint4*>(vt + (i >> 3) * kHalf + (last_page * kPage + lane) * 128)[i & 7] =
-                  make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        const bool more = j + 1 < nk;
-        if (more) {
-          ok = tc5_wait(&sm.full[ks], ((2 * j + 2) / kStages) & 1, abort);
-          if (!ok) break;
-        }
+          for (int w = 0; w < 2; ++w) {
+            if (ok && j < cnt[w]) {
+              ok = tc5_wait(&sm.p_full[w], j & 1, abort);
+              if (ok) {
+                tc5_fence_after();
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (j < cnt[w]) {
-            ok = ok && tc5_wait(&sm.p_full[w], j & 1, abort);
-            if (!ok) break;
-            tc5_fence_after();
-            const unsigned va = smem_u32(vt);
-            if (lane == 0) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i,
-                           tc5_desc(along_n, va + i * 2048), id_o, j > 0 || i > 0);
-              if (j + 1 == cnt[w]) tc5_commit(&sm.o_full[w]);
+                for (int i = 0; i < 8; ++i)
+                  tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i, v + i * (2048 >> 4),
+                             id_o, j > 0 || i > 0);
+                if (w == last) tc5_commit(&sm.empty[vs]);
+                if (j + 1 < cnt[w]) qk(w, ks);
+                else tc5_commit(&sm.o_full[w]);
+                if (w == last && more) tc5_commit(&sm.empty[ks]);
+              }
             }
-            __syncwarp();
           }
-          if (w == last) release(vs);
-          if (more && j + 1 < cnt[w]) qk(w, ring + ks * kTileBytes);
-          if (more && w == last) release(ks);
+          vs = ks + 1 == kStages ? 0 : ks + 1;
+          vp = ks + 1 == kStages ? kp ^ 1 : kp;
         }
-      }
-      // the last commits' arrivals land before the CTA ends
-      if (lane == 0) {
+        // the last commits' arrivals land before the CTA ends
         if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
         tc5_commit(&sm.drain);
         if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
           record_error(p.c.status, kDevErrDrainTimeout);
       }
       __syncwarp();
+    } else if (warp == 10 && clear_at >= 0) {
+      // ---- the rows behind the sequence's last token hold anything: clear them
+      const int f = 2 * clear_at + 1, page = sp.blocks - 1 - (k0 + clear_at) * kKeyPages;
+      if (tc5_wait(&sm.full[f % kStages], (f / kStages) & 1, abort)) {
+        if (sp.block(sp.blocks - 1) * kPage + lane >= n) {
+          uint8_t* row = ring + (f % kStages) * kTileBytes + (page * kPage + lane) * 128;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.clean);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -391,7 +389,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         tc5_st32(s_addr + 32, sr + 32);
         tc5_wait_st();
         tc5_fence_before();
-        mbar_arrive(&sm.p_full[w]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[w]);
       }
 
       // ------------------------------------------------------------ results

@@ -11,8 +11,9 @@ namespace oscar {
 __host__ __device__ constexpr uint64_t tc5_desc_base(unsigned lbo, unsigned sbo) {
   return ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
+// The descriptor of an operand at shared-memory address `addr` (below 2^18).
 __device__ __forceinline__ uint64_t tc5_desc(uint64_t base, unsigned addr) {
-  return base | (uint64_t)((addr & 0x3ffffu) >> 4);
+  return ((base >> 32) << 32) | (uint32_t)((uint32_t)base | (addr >> 4));
 }
 // Instruction descriptor of kind::f16 with an fp32 accumulator.
 __host__ __device__ constexpr uint32_t tc5_idesc(bool half, int M, int N, bool b_along_n,
@@ -95,6 +96,15 @@ __device__ __forceinline__ void tc5_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
