@@ -57,22 +57,86 @@ struct AttnParams {
   float* lse;
   float* part;          // [total * Hq][splits][kRecFloats] if splits > 1
   int g, tokens;        // heads of a group, tokens of a query tile
-  int tiles;            // upper bound on CTAs of one KV head
+  int tiles;            // upper bound on work items of one KV head and split
   int splits;
   float scale;          // |scale| in the log2 domain
   bool negate;
+  bool wide;            // out is 32-byte aligned
 };
 
-// Where a row's result goes and what it may see.
-struct RowPlace {
-  int row, head, at;
+constexpr int kItems = 4;              // work items on their way to the other warps
+
+// A work item as the scheduling warp hands it on.
+struct Item {
+  int stop;            // no more items
+  int b, h, split, n;
+  int row0, nrow;      // first row of q, tokens (of one or two tiles)
+  int at0;             // position of the first token
+  Span sp;
+  int k0, k1;          // key tiles
+  int cnt[2];          // of them, for each query tile: k0 .. k0 + cnt - 1
+  int clear_at;        // the one whose last page lacks tokens (counted from k0), or -1
 };
 
 struct Smem {
-  uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], clean, drain;
+  uint64_t q_full[2], q_empty[2], full[kStages], empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], clean, drain;
+  uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int abort;
+  Item item[kItems];
 };
+constexpr int kItemReaders = 11;       // warps that read an item: all but the scheduling one
+
+// Work item x.  One KV head's items are numbered through: sequence b's start
+// at start[b] / (2 tokens) + b, which leaves room for all of them; those left
+// over are empty (false).
+__device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) {
+  const int two = 2 * p.tokens, per_split = p.tiles * p.c.Hkv;
+  it.split = x / per_split;
+  const int y = x - it.split * per_split, t = y / p.c.Hkv;
+  it.h = y - t * p.c.Hkv;
+  int lo = 0, hi = p.c.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (min(max(__ldg(p.q.start + mid), 0), p.q.total) / two + mid <= t) lo = mid; else hi = mid;
+  }
+  it.b = lo;
+  const int r0 = __ldg(p.q.start + lo), r1 = __ldg(p.q.start + lo + 1), nq = r1 - r0;
+  const bool report = (threadIdx.x & 31) == 0;
+  if (r0 < 0 || r1 > p.q.total || nq < 0) {
+    if (report) record_error(p.c.status, kDevErrBadPaged);
+    return false;
+  }
+  const int mine = t - (r0 / two + lo), all = (nq + two - 1) / two;
+  if (mine < 0 || mine >= all) return false;
+  it.n = kv16_length(p.c, lo, p.q.max_tok);
+  if (it.n < nq) {     // a length out of range, or fewer tokens than queries
+    if (report) record_error(p.c.status, kDevErrBadPaged);
+    it.n = max(it.n, 0);
+  }
+  const int q0 = (all - 1 - mine) * two;        // the longest rows first
+  it.row0 = r0 + q0;
+  it.nrow = min(two, nq - q0);
+  it.at0 = it.n - nq + q0;
+  it.sp = Span(it.at0, it.at0 + it.nrow - 1, p.q.window, p.q.n_sink);
+  const int kt = (it.sp.blocks + kKeyPages - 1) / kKeyPages;
+  it.k0 = (int)((long long)kt * it.split / p.splits);
+  it.k1 = (int)((long long)kt * (it.split + 1) / p.splits);
+  it.cnt[0] = it.k1 - it.k0;
+  it.cnt[1] = 0;
+  if (it.nrow > p.tokens) {
+    // the first tile's keys end before the second's
+    it.cnt[1] = it.cnt[0];
+    const int blocks = Span(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink).blocks;
+    it.cnt[0] = min(it.k1, max(it.k0, (blocks + kKeyPages - 1) / kKeyPages)) - it.k0;
+  }
+  it.clear_at = it.k1 > it.k0 && it.k1 == kt && it.n % kPage != 0 &&
+                        it.sp.block(it.sp.blocks - 1) == (it.n - 1) / kPage
+                    ? kt - 1 - it.k0
+                    : -1;
+  return true;
+}
 
 template <class T>
 __device__ __forceinline__ void store_row4(const AttnParams& p, long long row, int lane,
@@ -87,64 +151,28 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) Smem sm;
+  __shared__ __align__(16) Smem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  // ---- the CTA's work: tile t of sequence b, KV head h, split s.  Sequence
-  // b's CTAs start at start[b] / (2 tokens) + b, which leaves room for each.
-  const int two = 2 * p.tokens;
-  const int h = blockIdx.x % p.c.Hkv, t = blockIdx.x / p.c.Hkv, split = blockIdx.y;
-  int lo = 0, hi = p.c.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (min(max(__ldg(p.q.start + mid), 0), p.q.total) / two + mid <= t) lo = mid; else hi = mid;
-  }
-  const int b = lo;
-  const int r0 = __ldg(p.q.start + b), r1 = __ldg(p.q.start + b + 1), nq = r1 - r0;
-  if (r0 < 0 || r1 > p.q.total || nq < 0) {
-    if (tid == 0) record_error(p.c.status, kDevErrBadPaged);
-    return;
-  }
-  const int tile_in_seq = t - (r0 / two + b), seq_tiles = (nq + two - 1) / two;
-  if (tile_in_seq < 0 || tile_in_seq >= seq_tiles) return;
-  int n = kv16_length(p.c, b, p.q.max_tok);
-  if (n < nq) {     // a length out of range, or fewer tokens than queries
-    if (tid == 0) record_error(p.c.status, kDevErrBadPaged);
-    if (n < 0) n = 0;
-  }
-  const int q0 = (seq_tiles - 1 - tile_in_seq) * two;        // the longest rows first
-  const int nrow = min(two, nq - q0);                        // tokens of this CTA
-  const int ntile = nrow > p.tokens ? 2 : 1;
-  const int at0 = n - nq + q0;                               // position of its first token
-  const Span sp(at0, at0 + nrow - 1, p.q.window, p.q.n_sink);
-  const int kt_all = (sp.blocks + kKeyPages - 1) / kKeyPages;
-  const int k0 = (int)((long long)kt_all * split / p.splits);
-  const int k1 = (int)((long long)kt_all * (split + 1) / p.splits);
-  // key tiles of the first query tile: it ends before the second
-  const int blocks0 = Span(at0, at0 + min(nrow, p.tokens) - 1, p.q.window, p.q.n_sink).blocks;
-  const int k1_0 = min(k1, max(k0, (blocks0 + kKeyPages - 1) / kKeyPages));
-  const int cnt[2] = {ntile == 2 ? k1_0 - k0 : k1 - k0, ntile == 2 ? k1 - k0 : 0};
-
-  // the key tile with the last page of the sequence, if tokens are missing from it
-  const int tail = (sp.blocks - 1) / kKeyPages - k0;
-  const int clear_at = k1 > k0 && k1 == kt_all && n % kPage != 0 &&
-                               sp.block(sp.blocks - 1) == (n - 1) / kPage ? tail : -1;
-
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   uint8_t* sq = smem;                            // two query tiles
   uint8_t* ring = smem + 2 * kTileBytes;
 
   if (warp == 8) tc5_alloc(&sm.tmem, 512);
   if (tid == 0) {
-    mbar_init(&sm.q_full, 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sm.i_full[i], 1);
+      mbar_init(&sm.i_empty[i], kItemReaders);
     }
     mbar_init(&sm.clean, 1);
     mbar_init(&sm.drain, 1);
@@ -156,62 +184,104 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   tc5_fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int* abort = &sm.abort;
+  // an item is read by every warp but the scheduling one, and then given back
+  auto take = [&](unsigned n) -> const Item* {
+    return tc5_wait(&sm.i_full[n % kItems], (n / kItems) & 1, abort) ? &sm.item[n % kItems]
+                                                                     : nullptr;
+  };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    bool ok = true;
+    if (warp == 11) {
+      // -------------------------------------------------- scheduling: the items
+      // x, rounds of the grid in turn forwards and backwards, so that a CTA
+      // with the longest of one round gets the shortest of the next
+      unsigned n = 0;
+      const int items = p.tiles * p.c.Hkv * p.splits, grid = gridDim.x;
+      for (int round = 0; ok; ++round) {
+        const long long x = (long long)round * grid +
+                            ((round & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+        const bool stop = (long long)round * grid >= items;
+        Item it;
+        if (!stop && (x >= items || !find_item(p, (int)x, it))) continue;
+        it.stop = stop;
+        if (n >= kItems) ok = tc5_wait(&sm.i_empty[n % kItems], (n / kItems - 1) & 1, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          sm.item[n % kItems] = it;
+          mbar_arrive(&sm.i_full[n % kItems]);
+        }
+        __syncwarp();
+        ++n;
+        if (stop) break;
+      }
+    } else if (warp == 8) {
       // ------------------------------------------------------------ copies
       const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
                                  : p.c.B * p.c.Hkv * p.c.T_cap;      // reads zeros
-      if (lane == 0 && k1 > k0) {
-        const unsigned bytes = 64 * 2 * p.g * p.tokens;
-        mbar_arrive_expect_tx(&sm.q_full, 2 * bytes * ntile);
-        for (int w = 0; w < ntile; ++w)
-          for (int i = 0; i < 2; ++i)
-            tma_box3(sq + w * kTileBytes + i * kHalf, &map_q, 64 * i, h * p.g,
-                     r0 + q0 + w * p.tokens, &sm.q_full);
-      }
-      int used = 0;     // stages filled so far
-      bool ok = true;
-      for (int k = k0; k < k1 && ok; ++k) {
-        int row = none;
-        if (lane < kKeyPages && k * kKeyPages + lane < sp.blocks) {
-          row = kv16_block_row(p.c, b, h, sp.block(k * kKeyPages + lane));
-          if (row < 0) {
-            record_error(p.c.status, kDevErrBadPaged);
-            row = none;
-          }
-        }
+      const unsigned qbytes = 2 * 64 * 2 * p.g * p.tokens;
+      unsigned used = 0, q_used[2] = {0, 0};
+      for (unsigned ni = 0; ok; ++ni) {
+        const Item* ip = take(ni);
+        if (!(ok = ip != nullptr) || ip->stop) break;
+        const Item it = *ip;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int st = used % kStages;
-          if (used >= kStages && !tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort)) {
-            if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-            ok = false;
-            break;
-          }
-          uint8_t* dst = ring + st * kTileBytes;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || it.cnt[w] == 0) continue;
+          if (q_used[w] > 0) ok = tc5_wait(&sm.q_empty[w], (q_used[w] - 1) & 1, abort);
+          if (!ok) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.q_full[w], qbytes);
 #pragma unroll
-          for (int i = 0; i < kKeyPages; ++i) {
-            const int y = __shfl_sync(0xffffffffu, row, i);
-            if (lane == 0) {
-              tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, &sm.full[st]);
-              tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, &sm.full[st]);
-            }
+            for (int i = 0; i < 2; ++i)
+              tma_box3(sq + w * kTileBytes + i * kHalf, &map_q, 64 * i, it.h * p.g,
+                       it.row0 + w * p.tokens, &sm.q_full[w]);
           }
           __syncwarp();
-          ++used;
+          ++q_used[w];
+        }
+        for (int k = it.k0; k < it.k1 && ok; ++k) {
+          int row = none;
+          if (lane < kKeyPages && k * kKeyPages + lane < it.sp.blocks) {
+            row = kv16_block_row(p.c, it.b, it.h, it.sp.block(k * kKeyPages + lane));
+            if (row < 0) {
+              record_error(p.c.status, kDevErrBadPaged);
+              row = none;
+            }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const unsigned st = used % kStages;
+            if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort);
+            if (!ok) break;
+            uint8_t* dst = ring + st * kTileBytes;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+#pragma unroll
+            for (int i = 0; i < kKeyPages; ++i) {
+              const int y = __shfl_sync(0xffffffffu, row, i);
+              if (lane == 0) {
+                tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, &sm.full[st]);
+                tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, &sm.full[st]);
+              }
+            }
+            __syncwarp();
+            ++used;
+          }
         }
       }
       // after a time-out: what is in flight lands before the memory is given back
       if (*abort) {
-        if (k1 > k0) mbar_wait_bounded(&sm.q_full, 0, kDrainLimit);
-        for (int i = max(0, used - kStages); i < used; ++i)
-          if (!mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit) && lane == 0)
-            record_error(p.c.status, kDevErrDrainTimeout);
+        bool landed = true;
+        for (int w = 0; w < 2; ++w)
+          if (q_used[w]) landed &= mbar_wait_bounded(&sm.q_full[w], (q_used[w] - 1) & 1, kDrainLimit);
+        for (unsigned i = used > kStages ? used - kStages : 0; i < used; ++i)
+          landed &= mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit);
+        if (!landed && lane == 0) record_error(p.c.status, kDevErrDrainTimeout);
       }
-    } else if (warp == 9 && k1 > k0) {
+    } else if (warp == 9) {
       // -------------------------------------------------------------- MMAs
       if (elect_one()) {
         const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
@@ -230,102 +300,143 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           }
           tc5_commit(&sm.s_full[w]);
         };
-        const int last = ntile - 1, nk = k1 - k0;
-        bool ok = tc5_wait(&sm.q_full, 0, abort) && tc5_wait(&sm.full[0], 0, abort);
-        if (ok) {
-          if (cnt[0] > 0) qk(0, 0);
-          if (cnt[1] > 0) qk(1, 0);
-          tc5_commit(&sm.empty[0]);
-        }
-        // stages in turn: K_0 V_0 K_1 V_1 ...
-        unsigned vs = 1, vp = 0;
-        for (int j = 0; j < nk && ok; ++j) {
-          const unsigned ks = vs + 1 == kStages ? 0 : vs + 1, kp = vs + 1 == kStages ? vp ^ 1 : vp;
-          const bool more = j + 1 < nk;
-          ok = tc5_wait(&sm.full[vs], vp, abort);
-          // the tile with the sequence's last page: its tail is cleared first
-          if (ok && j == clear_at) ok = tc5_wait(&sm.clean, 0, abort);
-          if (ok && more) ok = tc5_wait(&sm.full[ks], kp, abort);
-          const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
+        unsigned st = 0, ph = 0;         // the next stage: K_0 V_0 K_1 V_1 ...
+        unsigned q_used[2] = {0, 0}, p_used[2] = {0, 0}, cleaned = 0;
+        for (unsigned ni = 0; ok; ++ni) {
+          const Item* ip = take(ni);
+          if (!(ok = ip != nullptr) || ip->stop) break;
+          const int cnt[2] = {ip->cnt[0], ip->cnt[1]}, clear_at = ip->clear_at;
+          mbar_arrive(&sm.i_empty[ni % kItems]);
+          const int nk = max(cnt[0], cnt[1]), last = cnt[1] > 0 ? 1 : 0;
+          if (nk == 0) continue;
+          ok = tc5_wait(&sm.full[st], ph, abort);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (ok && j < cnt[w]) {
-              ok = tc5_wait(&sm.p_full[w], j & 1, abort);
-              if (ok) {
-                tc5_fence_after();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i, v + i * (2048 >> 4),
-                             id_o, j > 0 || i > 0);
-                if (w == last) tc5_commit(&sm.empty[vs]);
-                if (j + 1 < cnt[w]) qk(w, ks);
-                else tc5_commit(&sm.o_full[w]);
-                if (w == last && more) tc5_commit(&sm.empty[ks]);
-              }
-            }
+            if (cnt[w] == 0 || !ok) continue;
+            ok = tc5_wait(&sm.q_full[w], q_used[w]++ & 1, abort);
+            if (!ok) continue;
+            tc5_fence_after();
+            qk(w, st);
+            if (cnt[w] == 1) tc5_commit(&sm.q_empty[w]);
           }
-          vs = ks + 1 == kStages ? 0 : ks + 1;
-          vp = ks + 1 == kStages ? kp ^ 1 : kp;
+          if (ok) tc5_commit(&sm.empty[st]);
+          unsigned vs = st + 1 == kStages ? 0 : st + 1, vp = st + 1 == kStages ? ph ^ 1 : ph;
+          for (int j = 0; j < nk && ok; ++j) {
+            const unsigned ks = vs + 1 == kStages ? 0 : vs + 1, kp = vs + 1 == kStages ? vp ^ 1 : vp;
+            const bool more = j + 1 < nk;
+            ok = tc5_wait(&sm.full[vs], vp, abort);
+            // the tile with the sequence's last page: its tail is cleared first
+            if (ok && j == clear_at) ok = tc5_wait(&sm.clean, cleaned++ & 1, abort);
+            if (ok && more) ok = tc5_wait(&sm.full[ks], kp, abort);
+            const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (!ok || j >= cnt[w]) continue;
+              ok = tc5_wait(&sm.p_full[w], p_used[w]++ & 1, abort);
+              if (!ok) continue;
+              tc5_fence_after();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i, v + i * (2048 >> 4), id_o,
+                           j > 0 || i > 0);
+              if (w == last) tc5_commit(&sm.empty[vs]);
+              if (j + 1 < cnt[w]) {
+                qk(w, ks);
+                if (j + 2 == cnt[w]) tc5_commit(&sm.q_empty[w]);
+              } else {
+                tc5_commit(&sm.o_full[w]);
+              }
+              if (w == last && more) tc5_commit(&sm.empty[ks]);
+            }
+            // the next value tile, or the next item's first key tile
+            st = more ? ks : (vs + 1 == kStages ? 0 : vs + 1);
+            ph = more ? kp : (vs + 1 == kStages ? vp ^ 1 : vp);
+            vs = st + 1 == kStages ? 0 : st + 1;
+            vp = st + 1 == kStages ? ph ^ 1 : ph;
+          }
         }
         // the last commits' arrivals land before the CTA ends
-        if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
         tc5_commit(&sm.drain);
         if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
           record_error(p.c.status, kDevErrDrainTimeout);
       }
       __syncwarp();
-    } else if (warp == 10 && clear_at >= 0) {
-      // ---- the rows behind the sequence's last token hold anything: clear them
-      const int f = 2 * clear_at + 1, page = sp.blocks - 1 - (k0 + clear_at) * kKeyPages;
-      if (tc5_wait(&sm.full[f % kStages], (f / kStages) & 1, abort)) {
-        if (sp.block(sp.blocks - 1) * kPage + lane >= n) {
-          uint8_t* row = ring + (f % kStages) * kTileBytes + (page * kPage + lane) * 128;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    } else {
+      // ---- warp 10: the rows behind a sequence's last token hold anything: clear them
+      unsigned base = 0;      // fills of the ring before the item
+      for (unsigned ni = 0; ok; ++ni) {
+        const Item* ip = take(ni);
+        if (!(ok = ip != nullptr) || ip->stop) break;
+        const Item it = *ip;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.clean);
+        if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
+        if (it.clear_at >= 0) {
+          const unsigned f = base + 2 * it.clear_at + 1;
+          const int page = it.sp.blocks - 1 - (it.k0 + it.clear_at) * kKeyPages;
+          ok = tc5_wait(&sm.full[f % kStages], (f / kStages) & 1, abort);
+          if (!ok) break;
+          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
+            uint8_t* row = ring + (f % kStages) * kTileBytes + (page * kPage + lane) * 128;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.clean);
+        }
+        base += 2 * (it.k1 - it.k0);
       }
     }
+    if (*abort && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // -------------------------------------------------------------- softmax
     const int w = warp >> 2, r = tid & 127;
-    if (w < ntile) {
-      const uint32_t lane_addr = tmem + ((uint32_t)(warp & 3) << 21);
-      const uint32_t s_addr = lane_addr + 128 * w, o_addr = lane_addr + kO + 128 * w;
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t s_addr = lane_addr + 128 * w, o_addr = lane_addr + kO + 128 * w;
+    const int tok = r / p.g, head = r - tok * p.g;
+    const float2 sc2 = make_float2(p.scale, p.scale);
+    unsigned s_used = 0, o_used = 0;
+    bool ok = true;
+    for (unsigned ni = 0; ok; ++ni) {
+      const Item* ip = take(ni);
+      if (!(ok = ip != nullptr) || ip->stop) break;
+      const int ntok = min(p.tokens, ip->nrow - w * p.tokens), my_n = ip->cnt[w];
+      const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
+      const int at_first = ip->at0 + w * p.tokens, row_first = ip->row0 + w * p.tokens;
+      const Span sp = ip->sp;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
+      if (ntok <= 0) continue;
       // the thread's row; rows past the tile's end work like its last token
-      const int ntok = min(p.tokens, nrow - w * p.tokens);
-      const int tok = r / p.g, head = r - tok * p.g;
       const bool valid = tok < ntok;
-      const int at = at0 + w * p.tokens + min(tok, ntok - 1);
+      const int at = at_first + min(tok, ntok - 1);
       const int at_min = __shfl_sync(0xffffffffu, at, 0), at_max = __shfl_sync(0xffffffffu, at, 31);
-      const int my_n = w ? cnt[1] : cnt[0];
+      // key tiles [in0, in1), counted from k0, whose pages the warp's rows all see
+      int in0, in1;
+      {
+        const int first = p.q.window == 0 ? 0 : max(at_max - p.q.window + kPage, 0) / kPage;
+        const int v0 = sp.sink_blocks + max(first - sp.w0, 0);
+        const int v1 = sp.sink_blocks + (at_min + 1) / kPage - sp.w0;      // behind the last
+        in0 = (v0 + kKeyPages - 1) / kKeyPages - k0;
+        in1 = (max(v1, 0)) / kKeyPages - k0;
+      }
       float m = -INFINITY, l = 0.0f;
-      bool ok = true;
       for (int j = 0; j < my_n; ++j) {
-        if (!tc5_wait(&sm.s_full[w], j & 1, abort)) {
-          if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-          ok = false;
-          break;
-        }
+        ok = tc5_wait(&sm.s_full[w], s_used++ & 1, abort);
+        if (!ok) break;
         tc5_fence_after();
         uint32_t sr[128];
         float* s = reinterpret_cast<float*>(sr);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc5_ld32(sr + 32 * i, s_addr + 32 * i);
         tc5_wait_ld();
-        // mask, page by page
+        if (j < in0 || j >= in1) {
+          // mask, page by page
 #pragma unroll
-        for (int i = 0; i < kKeyPages; ++i) {
-          const int v = (k0 + j) * kKeyPages + i;
-          const int base = sp.block(v) * kPage;
-          const bool whole = v < sp.blocks && base + kPage - 1 <= at_min &&
-                             (p.q.window == 0 || base > at_max - p.q.window ||
-                              base + kPage <= p.q.n_sink);
-          if (!whole) {
+          for (int i = 0; i < kKeyPages; ++i) {
+            const int v = (k0 + j) * kKeyPages + i, base = sp.block(v) * kPage;
             // columns [0, up) at or before the query; of them [from, ..) in the
             // window and [0, sink) sinks
             const int up = v >= sp.blocks || at < base ? 0 : min(at - base + 1, 32);
@@ -335,9 +446,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             const uint32_t near = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
             const uint32_t first = sink >= 32 ? 0xffffffffu : (1u << sink) - 1;
             const uint32_t see = below_up & (near | first);
+            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
+            }
           }
         }
         float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
@@ -371,7 +484,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         }
         const float ms = m == -INFINITY ? 0.0f : m;
-        const float2 sc2 = make_float2(p.scale, p.scale), m2 = make_float2(-ms, -ms);
+        const float2 m2 = make_float2(-ms, -ms);
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
         for (int e = 0; e < 128; e += 4) {
@@ -394,88 +507,78 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       }
 
       // ------------------------------------------------------------ results
-      if (ok && my_n > 0 && !tc5_wait(&sm.o_full[w], 0, abort)) {
-        if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-        ok = false;
-      }
-      if (ok) {
-        tc5_fence_after();
-        const long long row = (long long)(r0 + q0 + w * p.tokens + tok) * p.q.Hq + h * p.g + head;
-        const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-        float odd = l * 0.0f;            // NaN once anything is not finite
-        // the tile's queries are done with: its shared memory stages the rows
-        uint8_t* stage = sq + w * kTileBytes + (warp & 3) * 8192;
-        float* rec = p.part + (row * p.splits + split) * kRecFloats;
+      if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, abort);
+      if (!ok) break;
+      tc5_fence_after();
+      const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
+      const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      float odd = l * 0.0f;            // NaN once anything is not finite
+      float* rec = p.part + (row * p.splits + split) * kRecFloats;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          if (my_n > 0) {
-            tc5_ld32(o, o_addr + 32 * i);
-            tc5_wait_ld();
-          } else {
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        if (my_n > 0) {
+          tc5_ld32(o, o_addr + 32 * i);
+          tc5_wait_ld();
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
-          if (p.splits > 1) {
-            if (valid)
+        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+        if (p.splits > 1) {
+          if (valid)
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
-                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else {
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
+          uint32_t v[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v;
-              v.x = T::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              v.y = T::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              v.z = T::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              v.w = T::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-              const int chunk = 4 * i + e / 8;
-              reinterpret_cast<uint4*>(stage + lane * 256)[chunk ^ (lane & 7)] = v;
+          for (int e = 0; e < 16; ++e)
+            v[e] = T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (valid) {
+            uint32_t* d = reinterpret_cast<uint32_t*>(p.out + row * kD) + 16 * i;
+            if (p.wide) {
+              st_global32(d, v);
+              st_global32(d + 8, v + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(d + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
           }
         }
-        if (valid) {
-          if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
-          else if (p.lse) p.lse[row] = kv16_lse(m, l);
-        }
-        __syncwarp();
-        if (p.splits == 1) {
-          // two rows at a time, 16 lanes each: whole rows of 256 B
-#pragma unroll 4
-          for (int i = 0; i < 32; i += 2) {
-            const int src = i + (lane >> 4);
-            const long long dst = __shfl_sync(0xffffffffu, row, src);
-            const bool there = __shfl_sync(0xffffffffu, (int)valid, src);
-            const uint4 v = reinterpret_cast<const uint4*>(stage + src * 256)[(lane & 15) ^ (src & 7)];
-            if (there) reinterpret_cast<uint4*>(p.out + dst * kD)[lane & 15] = v;
-          }
-        }
-        // rows with a result that is not finite, token by token
-        for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
-          const int src = __ffs(bad) - 1;
-          const long long rw = __shfl_sync(0xffffffffu, row, src);
-          const int a = __shfl_sync(0xffffffffu, at, src);
-          const long long token = rw / p.q.Hq;
-          const int hd = (int)(rw - token * p.q.Hq);
-          float mm, ll, oo[4];
-          kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)hd * kD, b, h, a, sp,
-                           k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
-                           p.q.scale_log2, mm, ll, oo);
-          if (p.splits > 1) {
-            float* d = p.part + (rw * p.splits + split) * kRecFloats;
-            if (lane == 0) *reinterpret_cast<float2*>(d) = make_float2(mm, ll);
-            *reinterpret_cast<float4*>(d + 4 + 4 * lane) = make_float4(oo[0], oo[1], oo[2], oo[3]);
-          } else {
-            store_row4<T>(p, rw, lane, oo, ll == 0.0f ? 0.0f : 1.0f / ll);
-            if (p.lse && lane == 0) p.lse[rw] = kv16_lse(mm, ll);
-          }
+      }
+      tc5_fence_before();       // O has been read: the next item's products may follow
+      if (valid) {
+        if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+        else if (p.lse) p.lse[row] = kv16_lse(m, l);
+      }
+      // rows with a result that is not finite, token by token
+      __syncwarp();
+      for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
+        const int src = __ffs(bad) - 1;
+        const long long rw = __shfl_sync(0xffffffffu, row, src);
+        const int a = __shfl_sync(0xffffffffu, at, src);
+        const long long token = rw / p.q.Hq;
+        const int hd = (int)(rw - token * p.q.Hq);
+        float mm, ll, oo[4];
+        kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)hd * kD, b, h, a, sp,
+                         k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
+                         p.q.scale_log2, mm, ll, oo);
+        if (p.splits > 1) {
+          float* d = p.part + (rw * p.splits + split) * kRecFloats;
+          if (lane == 0) *reinterpret_cast<float2*>(d) = make_float2(mm, ll);
+          *reinterpret_cast<float4*>(d + 4 + 4 * lane) = make_float4(oo[0], oo[1], oo[2], oo[3]);
+        } else {
+          store_row4<T>(p, rw, lane, oo, ll == 0.0f ? 0.0f : 1.0f / ll);
+          if (p.lse && lane == 0) p.lse[rw] = kv16_lse(mm, ll);
         }
       }
-      tc5_fence_before();
     }
+    if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    tc5_fence_before();
   }
   __syncthreads();
   if (warp == 8) {
@@ -511,7 +614,15 @@ __global__ void __launch_bounds__(128) kv16_join_kernel(const AttnParams p) {
   if (p.lse && lane == 0) p.lse[row] = kv16_lse(M, L);
 }
 
-// Upper bound on the CTAs of one KV head: every sequence's last may be partial.
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 152;
+  return sms;
+}
+
+// Upper bound on the work items of one KV head: every sequence's last may be partial.
 long long attention_tiles(int B, int g, int total) {
   const int two = 2 * (128 / g);
   return (long long)total / two + B;
@@ -521,10 +632,7 @@ long long attention_tiles(int B, int g, int total) {
 // with at least four key tiles.
 int attention_splits(const Kv16& c, int Hq, int total, int max_tok, int window, int n_sink) {
   const int g = Hq / c.Hkv, two = 2 * (128 / g);
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    sms = 152;
+  const int sms = sm_count();
   const long long ctas = ((total + two - 1) / two + std::min(c.B, total) - 1LL) * c.Hkv;
   long long keys = std::min(max_tok, c.cap);
   if (window > 0) keys = std::min<long long>(keys, (long long)window + two + n_sink + 3 * kPage);
@@ -542,7 +650,8 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   constexpr int smem = (2 + kStages) * kTileBytes + 1024;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(p.tiles * p.c.Hkv, p.splits), kThreads, smem, s>>>(mq, mk, mv, p);
+  const int grid = std::min(p.tiles * p.c.Hkv * p.splits, sm_count());
+  kernel<<<grid, kThreads, smem, s>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   *launches = 1;
   if (e != cudaSuccess || p.splits == 1) return e;
@@ -571,12 +680,13 @@ cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* o
   p.g = q.Hq / c.Hkv;
   p.tokens = 128 / p.g;
   const long long tiles = attention_tiles(c.B, p.g, q.total);
-  if (tiles * c.Hkv > 0x7fffffffLL) return cudaErrorInvalidValue;
-  p.tiles = (int)tiles;
   p.splits = attention_splits(c, q.Hq, q.total, q.max_tok, q.window, q.n_sink);
+  if (tiles * c.Hkv * p.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
+  p.tiles = (int)tiles;
   // a negative scale becomes a negated Q in the product, so that the largest
   // score is always the largest sum; a scale of 0 a scale too small to matter,
   // so that a masked -inf stays one
+  p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
   p.negate = q.scale_log2 < 0.0f;
   p.scale = std::max(std::fabs(q.scale_log2), 1e-30f);
   return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);

@@ -122,6 +122,13 @@ __device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatil
   return false;
 }
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tma_box2(void* dst, const void* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
