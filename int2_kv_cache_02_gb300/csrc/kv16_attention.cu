@@ -18,10 +18,13 @@
 // While one tile's softmax runs, the tensor cores work on the other tile.
 // TMEM: S_0, S_1, O_0, O_1, 128 columns each.
 //
-// Softmax.  One pass, running maximum and sum in fp32, base 2.  O is rescaled
-// only when a row's maximum has grown by more than 2^8 since the last time: the
-// probabilities then stay below 2^8, which both 16-bit types hold, and the
-// final division makes up for it.  Probabilities are rounded to the type of V
+// Softmax.  One pass, running maximum and sum in fp32, base 2.  The maximum in
+// use is replaced only when a row has grown by more than 2^8 over it: the
+// probabilities stay below 2^8, which both 16-bit types hold, and the final
+// division makes up for it.  So a tile's probabilities are taken on the maximum
+// so far while its own is found on the way (no pass over the scores before the
+// exponentials); where it turns out too large, O is rescaled and the tile done
+// once more.  Probabilities are rounded to the type of V
 // for the product (half a step relative, as the output itself); the sum is of
 // the unrounded ones.
 //
@@ -422,57 +425,84 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         in0 = (v0 + kKeyPages - 1) / kKeyPages - k0;
         in1 = (max(v1, 0)) / kKeyPages - k0;
       }
+      // page v of the span: scores of the tokens that the row does not see to -inf.
+      // It sees the columns [0, up); of them [from, ..) in the window, [0, sink) sinks.
+      auto hide = [&](float* s, int v) {
+        const int base = sp.block(v) * kPage;
+        const int up = v >= sp.blocks || at < base ? 0 : min(at - base + 1, 32);
+        const int from = p.q.window == 0 ? 0 : max(at - p.q.window + 1, 0) - base;
+        const int sink = p.q.n_sink <= base ? 0 : min(p.q.n_sink - base, 32);
+        const uint32_t below_up = up >= 32 ? 0xffffffffu : (1u << up) - 1;
+        const uint32_t near = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+        const uint32_t first = sink >= 32 ? 0xffffffffu : (1u << sink) - 1;
+        const uint32_t see = below_up & (near | first);
+        if (__all_sync(0xffffffffu, see == 0xffffffffu)) return;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!((see >> e) & 1u)) s[e] = -INFINITY;
+      };
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
         ok = tc5_wait(&sm.s_full[w], s_used++ & 1, abort);
         if (!ok) break;
         tc5_fence_after();
-        uint32_t sr[128];
-        float* s = reinterpret_cast<float*>(sr);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tc5_ld32(sr + 32 * i, s_addr + 32 * i);
-        tc5_wait_ld();
-        if (j < in0 || j >= in1) {
-          // mask, page by page
+        const bool inside = j >= in0 && j < in1;
+        if (j == 0) {
+          // the first maximum; later tiles start from what there is
+          float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < kKeyPages; ++i) {
-            const int v = (k0 + j) * kKeyPages + i, base = sp.block(v) * kPage;
-            // columns [0, up) at or before the query; of them [from, ..) in the
-            // window and [0, sink) sinks
-            const int up = v >= sp.blocks || at < base ? 0 : min(at - base + 1, 32);
-            const int from = p.q.window == 0 ? 0 : max(at - p.q.window + 1, 0) - base;
-            const int sink = p.q.n_sink <= base ? 0 : min(p.q.n_sink - base, 32);
-            const uint32_t below_up = up >= 32 ? 0xffffffffu : (1u << up) - 1;
-            const uint32_t near = from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
-            const uint32_t first = sink >= 32 ? 0xffffffffu : (1u << sink) - 1;
-            const uint32_t see = below_up & (near | first);
-            if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+            uint32_t sr[32];
+            float* s = reinterpret_cast<float*>(sr);
+            tc5_ld32(sr, s_addr + 32 * i);
+            tc5_wait_ld();
+            if (!inside) hide(s, (k0 + j) * kKeyPages + i);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1u)) s[32 * i + e] = -INFINITY;
+            for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(s[e], s[e + 1]));
+          }
+          m = mx * p.scale;
+        }
+        uint32_t pr[64];
+        float sum;
+        for (;;) {
+          // probabilities on the maximum so far, and this tile's maximum on the way
+          const float ms = m == -INFINITY ? 0.0f : m;
+          const float2 m2 = make_float2(-ms, -ms);
+          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          uint32_t sr[2][32];
+          tc5_ld32(sr[0], s_addr);
+#pragma unroll
+          for (int i = 0; i < kKeyPages; ++i) {
+            float* s = reinterpret_cast<float*>(sr[i & 1]);
+            tc5_wait_ld();
+            if (i + 1 < kKeyPages) tc5_ld32(sr[(i + 1) & 1], s_addr + 32 * (i + 1));
+            if (!inside) hide(s, (k0 + j) * kKeyPages + i);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
+              mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
+              float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
+              float2 y = fma2(make_float2(s[e + 2], s[e + 3]), sc2, m2);
+              x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              sum0 = add2(sum0, x);
+              sum1 = add2(sum1, y);
+              pr[16 * i + e / 2] = T::pack(x.x, x.y);
+              pr[16 * i + e / 2 + 1] = T::pack(y.x, y.y);
             }
           }
-        }
-        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
-        float mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
-#pragma unroll
-        for (int e = 8; e < 128; e += 8) {
-          mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
-          mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
-          mx2 = fmaxf(mx2, fmaxf(s[e + 4], s[e + 5]));
-          mx3 = fmaxf(mx3, fmaxf(s[e + 6], s[e + 7]));
-        }
-        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * p.scale;
-        if (j == 0) {
-          m = mx;
-        } else {
+          sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          const float mx = fmaxf(mx0, mx1) * p.scale;
           const bool grow = mx > m + kGrowth;      // true where m is -inf and mx is not
-          if (__any_sync(0xffffffffu, grow)) {
+          if (!__any_sync(0xffffffffu, grow)) break;
+          // rare: a new maximum, O and l on it, and the tile once more
+          const float a = grow ? fast_exp2(m - mx) : 1.0f;
+          if (grow) m = mx;
+          l *= a;
+          if (j > 0) {
             // S_w of this tile is there, so the products before it are complete
-            const float a = grow ? fast_exp2(m - mx) : 1.0f;
-            if (grow) m = mx;
-            l *= a;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               uint32_t o[32];
               tc5_ld32(o, o_addr + 32 * i);
@@ -483,23 +513,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             }
           }
         }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        const float2 m2 = make_float2(-ms, -ms);
-        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
-        for (int e = 0; e < 128; e += 4) {
-          float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
-          float2 y = fma2(make_float2(s[e + 2], s[e + 3]), sc2, m2);
-          x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          sum0 = add2(sum0, x);
-          sum1 = add2(sum1, y);
-          sr[e / 2] = T::pack(x.x, x.y);
-          sr[e / 2 + 1] = T::pack(y.x, y.y);
-        }
-        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        tc5_st32(s_addr, sr);
-        tc5_st32(s_addr + 32, sr + 32);
+        l += sum;
+        tc5_st32(s_addr, pr);
+        tc5_st32(s_addr + 32, pr + 32);
         tc5_wait_st();
         tc5_fence_before();
         __syncwarp();
