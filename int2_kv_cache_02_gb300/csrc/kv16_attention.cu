@@ -45,7 +45,8 @@
 namespace oscar {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 16;      // per query tile 2 x 4, each half of the columns
+constexpr int kThreads = kSoftmaxWarps * 32 + 128;
 constexpr int kStages = 5;
 constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
 constexpr int kHalf = 16384;
@@ -83,13 +84,15 @@ struct Item {
 
 struct Smem {
   uint64_t q_full[2], q_empty[2], full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], clean, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], clean, drain[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int abort;
   Item item[kItems];
+  int quit[8];           // per pair of warps: the step at which one of them gave up
+  float ex[2][2][128];   // what the halves of a row tell each other
 };
-constexpr int kItemReaders = 11;       // warps that read an item: all but the scheduling one
+constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: all but one
 
 // Work item x.  One KV head's items are numbered through: sequence b's start
 // at start[b] / (2 tokens) + b, which leaves room for all of them; those left
@@ -153,34 +156,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) Smem sm;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   uint8_t* sq = smem;                            // two query tiles
   uint8_t* ring = smem + 2 * kTileBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(smem + (2 + kStages) * kTileBytes);
+  if (smem_u32(smem) & 1023) {                   // the swizzle counts on it
+    if (tid == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    return;
+  }
 
-  if (warp == 8) tc5_alloc(&sm.tmem, 512);
+  if (warp == kSoftmaxWarps) tc5_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_full[i], 8);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.drain[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sm.i_full[i], 1);
       mbar_init(&sm.i_empty[i], kItemReaders);
     }
     mbar_init(&sm.clean, 1);
-    mbar_init(&sm.drain, 1);
     mbar_fence_init();
     sm.abort = 0;
+    for (int i = 0; i < 8; ++i) sm.quit[i] = 0x7fffffff;
   }
   tc5_fence_before();
   __syncthreads();
@@ -193,10 +200,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                                                                      : nullptr;
   };
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     bool ok = true;
-    if (warp == 11) {
+    if (warp == kSoftmaxWarps + 3) {
       // -------------------------------------------------- scheduling: the items
       // x, rounds of the grid in turn forwards and backwards, so that a CTA
       // with the longest of one round gets the shortest of the next
@@ -219,7 +226,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         ++n;
         if (stop) break;
       }
-    } else if (warp == 8) {
+    } else if (warp == kSoftmaxWarps) {
       // ------------------------------------------------------------ copies
       const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
                                  : p.c.B * p.c.Hkv * p.c.T_cap;      // reads zeros
@@ -274,6 +281,23 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ++used;
           }
         }
+        if (ok && it.clear_at >= 0) {
+          // the rows behind the sequence's last token hold anything: clear them
+          // in its last value tile, the one just asked for
+          const unsigned st = (used - 1) % kStages;
+          const int page = it.sp.blocks - 1 - (it.k0 + it.clear_at) * kKeyPages;
+          ok = tc5_wait(&sm.full[st], ((used - 1) / kStages) & 1, abort);
+          if (!ok) break;
+          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
+            uint8_t* row = ring + st * kTileBytes + (page * kPage + lane) * 128;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.clean);
+        }
       }
       // after a time-out: what is in flight lands before the memory is given back
       if (*abort) {
@@ -284,127 +308,139 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           landed &= mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit);
         if (!landed && lane == 0) record_error(p.c.status, kDevErrDrainTimeout);
       }
-    } else if (warp == 9) {
+    } else {
       // -------------------------------------------------------------- MMAs
+      // A warp per query tile: what one waits for passes under what the other
+      // has issued (the tensor cores' queue is too short to cover a wait).
+      const int w = warp - kSoftmaxWarps - 1;
       if (elect_one()) {
         const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
         const uint32_t id_o = tc5_idesc(T::kHalf, 128, 128, true, false);
         constexpr uint64_t kAlongK = tc5_desc_base(16, 1024);          // Q, K
         constexpr uint64_t kAlongN = tc5_desc_base(kHalf, 1024);       // V
-        const uint64_t dq = tc5_desc(kAlongK, smem_u32(sq));
+        const uint64_t dq = tc5_desc(kAlongK, smem_u32(sq + w * kTileBytes));
+        const uint32_t ts = tmem + 128 * w, to = tmem + kO + 128 * w;
         const unsigned ring_addr = smem_u32(ring);
-        auto qk = [&](int w, unsigned stage) {
-          const uint64_t a = dq + w * (kTileBytes >> 4);
+        auto qk = [&](unsigned stage) {
           const uint64_t k = tc5_desc(kAlongK, ring_addr + stage * kTileBytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const unsigned off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-            tc5_mma_ss(tmem + 128 * w, a + off, k + off, id_s, i > 0);
+            tc5_mma_ss(ts, dq + off, k + off, id_s, i > 0);
           }
           tc5_commit(&sm.s_full[w]);
         };
         unsigned st = 0, ph = 0;         // the next stage: K_0 V_0 K_1 V_1 ...
-        unsigned q_used[2] = {0, 0}, p_used[2] = {0, 0}, cleaned = 0;
+        auto next = [&] {
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
+        };
+        unsigned q_used = 0, p_used = 0, cleaned = 0;
         for (unsigned ni = 0; ok; ++ni) {
           const Item* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
-          const int cnt[2] = {ip->cnt[0], ip->cnt[1]}, clear_at = ip->clear_at;
+          const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0, clear_at = ip->clear_at;
           mbar_arrive(&sm.i_empty[ni % kItems]);
-          const int nk = max(cnt[0], cnt[1]), last = cnt[1] > 0 ? 1 : 0;
           if (nk == 0) continue;
+          // a stage that this tile has no use for is given back as it comes
           ok = tc5_wait(&sm.full[st], ph, abort);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (cnt[w] == 0 || !ok) continue;
-            ok = tc5_wait(&sm.q_full[w], q_used[w]++ & 1, abort);
-            if (!ok) continue;
+          if (ok && cnt > 0) {
+            ok = tc5_wait(&sm.q_full[w], q_used++ & 1, abort);
+            if (!ok) break;
             tc5_fence_after();
-            qk(w, st);
-            if (cnt[w] == 1) tc5_commit(&sm.q_empty[w]);
+            qk(st);
+            if (cnt == 1) tc5_commit(&sm.q_empty[w]);
+            tc5_commit(&sm.empty[st]);
+          } else if (ok) {
+            mbar_arrive(&sm.empty[st]);
           }
-          if (ok) tc5_commit(&sm.empty[st]);
-          unsigned vs = st + 1 == kStages ? 0 : st + 1, vp = st + 1 == kStages ? ph ^ 1 : ph;
+          next();
           for (int j = 0; j < nk && ok; ++j) {
-            const unsigned ks = vs + 1 == kStages ? 0 : vs + 1, kp = vs + 1 == kStages ? vp ^ 1 : vp;
+            const unsigned vs = st, vp = ph;
+            next();
             const bool more = j + 1 < nk;
             ok = tc5_wait(&sm.full[vs], vp, abort);
             // the tile with the sequence's last page: its tail is cleared first
             if (ok && j == clear_at) ok = tc5_wait(&sm.clean, cleaned++ & 1, abort);
-            if (ok && more) ok = tc5_wait(&sm.full[ks], kp, abort);
-            const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (!ok || j >= cnt[w]) continue;
-              ok = tc5_wait(&sm.p_full[w], p_used[w]++ & 1, abort);
-              if (!ok) continue;
+            if (ok && more) ok = tc5_wait(&sm.full[st], ph, abort);
+            if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w], p_used++ & 1, abort);
+            if (!ok) break;
+            if (j < cnt) {
               tc5_fence_after();
+              const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                tc5_mma_ts(tmem + kO + 128 * w, tmem + 128 * w + 8 * i, v + i * (2048 >> 4), id_o,
+                tc5_mma_ts(to, ts + (i >> 2) * 64 + (i & 3) * 8, v + i * (2048 >> 4), id_o,
                            j > 0 || i > 0);
-              if (w == last) tc5_commit(&sm.empty[vs]);
-              if (j + 1 < cnt[w]) {
-                qk(w, ks);
-                if (j + 2 == cnt[w]) tc5_commit(&sm.q_empty[w]);
-              } else {
-                tc5_commit(&sm.o_full[w]);
-              }
-              if (w == last && more) tc5_commit(&sm.empty[ks]);
+              if (j + 1 < cnt) qk(st);
+              else tc5_commit(&sm.o_full[w]);
+              tc5_commit(&sm.empty[vs]);
+              if (j + 2 == cnt) tc5_commit(&sm.q_empty[w]);
+            } else {
+              mbar_arrive(&sm.empty[vs]);
             }
-            // the next value tile, or the next item's first key tile
-            st = more ? ks : (vs + 1 == kStages ? 0 : vs + 1);
-            ph = more ? kp : (vs + 1 == kStages ? vp ^ 1 : vp);
-            vs = st + 1 == kStages ? 0 : st + 1;
-            vp = st + 1 == kStages ? ph ^ 1 : ph;
+            if (more) {
+              if (j + 1 < cnt) tc5_commit(&sm.empty[st]);
+              else mbar_arrive(&sm.empty[st]);
+              next();
+            }
           }
         }
         // the last commits' arrivals land before the CTA ends
-        tc5_commit(&sm.drain);
-        if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
+        tc5_commit(&sm.drain[w]);
+        if (!mbar_wait_bounded(&sm.drain[w], 0, kWaitLimit))
           record_error(p.c.status, kDevErrDrainTimeout);
       }
       __syncwarp();
-    } else {
-      // ---- warp 10: the rows behind a sequence's last token hold anything: clear them
-      unsigned base = 0;      // fills of the ring before the item
-      for (unsigned ni = 0; ok; ++ni) {
-        const Item* ip = take(ni);
-        if (!(ok = ip != nullptr) || ip->stop) break;
-        const Item it = *ip;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
-        if (it.clear_at >= 0) {
-          const unsigned f = base + 2 * it.clear_at + 1;
-          const int page = it.sp.blocks - 1 - (it.k0 + it.clear_at) * kKeyPages;
-          ok = tc5_wait(&sm.full[f % kStages], (f / kStages) & 1, abort);
-          if (!ok) break;
-          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
-            uint8_t* row = ring + (f % kStages) * kTileBytes + (page * kPage + lane) * 128;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.clean);
-        }
-        base += 2 * (it.k1 - it.k0);
-      }
     }
     if (*abort && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // -------------------------------------------------------------- softmax
-    const int w = warp >> 2, r = tid & 127;
+    // Tile w; a row has two threads, each with half of the columns of S, and
+    // of O when O is touched.  Their warps meet at a barrier of their own.
+    const int w = warp >> 3, half = (warp >> 2) & 1, r = tid & 127, pair = 4 * w + (warp & 3);
     const uint32_t lane_addr = tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t s_addr = lane_addr + 128 * w, o_addr = lane_addr + kO + 128 * w;
+    const uint32_t s_addr = lane_addr + 128 * w + 64 * half;
+    const uint32_t o_addr = lane_addr + kO + 128 * w + 64 * half;
     const int tok = r / p.g, head = r - tok * p.g;
     const float2 sc2 = make_float2(p.scale, p.scale);
+    volatile int* quit = &sm.quit[pair];
+    float* ex_mine = &sm.ex[w][half][r];
+    const float* ex_other = &sm.ex[w][half ^ 1][r];
     unsigned s_used = 0, o_used = 0;
+    // A warp that gives up at a wait says so, meets its partner once more and
+    // leaves; the partner, at its next meeting, sees a step that is not ahead
+    // of its own and leaves too: neither is left alone at the barrier.
+    int step = 0;
     bool ok = true;
+    auto meet = [&](bool x) -> bool {
+      uint32_t any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"((uint32_t)x), "r"(1 + pair)
+          : "memory");
+      if (*quit <= step) ok = false;
+      return any != 0;
+    };
+    auto give_up = [&] {
+      *quit = step;
+      __syncwarp();
+      meet(true);
+      ok = false;
+    };
     for (unsigned ni = 0; ok; ++ni) {
       const Item* ip = take(ni);
-      if (!(ok = ip != nullptr) || ip->stop) break;
+      ++step;
+      if (__any_sync(0xffffffffu, ip == nullptr)) {
+        give_up();
+        break;
+      }
+      if (ip->stop) break;
       const int ntok = min(p.tokens, ip->nrow - w * p.tokens), my_n = ip->cnt[w];
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
       const int at_first = ip->at0 + w * p.tokens, row_first = ip->row0 + w * p.tokens;
@@ -415,15 +451,16 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       // the thread's row; rows past the tile's end work like its last token
       const bool valid = tok < ntok;
       const int at = at_first + min(tok, ntok - 1);
-      const int at_min = __shfl_sync(0xffffffffu, at, 0), at_max = __shfl_sync(0xffffffffu, at, 31);
       // key tiles [in0, in1), counted from k0, whose pages the warp's rows all see
       int in0, in1;
       {
+        const int at_min = __shfl_sync(0xffffffffu, at, 0);
+        const int at_max = __shfl_sync(0xffffffffu, at, 31);
         const int first = p.q.window == 0 ? 0 : max(at_max - p.q.window + kPage, 0) / kPage;
         const int v0 = sp.sink_blocks + max(first - sp.w0, 0);
         const int v1 = sp.sink_blocks + (at_min + 1) / kPage - sp.w0;      // behind the last
         in0 = (v0 + kKeyPages - 1) / kKeyPages - k0;
-        in1 = (max(v1, 0)) / kKeyPages - k0;
+        in1 = max(v1, 0) / kKeyPages - k0;
       }
       // page v of the span: scores of the tokens that the row does not see to -inf.
       // It sees the columns [0, up); of them [from, ..) in the window, [0, sink) sinks.
@@ -443,137 +480,138 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       };
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < my_n; ++j) {
-        ok = tc5_wait(&sm.s_full[w], s_used++ & 1, abort);
-        if (!ok) break;
+        ++step;
+        if (!__all_sync(0xffffffffu, tc5_wait(&sm.s_full[w], s_used & 1, abort))) {
+          give_up();
+          break;
+        }
+        ++s_used;
         tc5_fence_after();
         const bool inside = j >= in0 && j < in1;
-        if (j == 0) {
-          // the first maximum; later tiles start from what there is
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < kKeyPages; ++i) {
-            uint32_t sr[32];
-            float* s = reinterpret_cast<float*>(sr);
-            tc5_ld32(sr, s_addr + 32 * i);
-            tc5_wait_ld();
-            if (!inside) hide(s, (k0 + j) * kKeyPages + i);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(s[e], s[e + 1]));
+        uint32_t sr[64];
+        float* s = reinterpret_cast<float*>(sr);
+        const bool first = j == 0;
+        {
+          tc5_ld32(sr, s_addr);
+          tc5_ld32(sr + 32, s_addr + 32);
+          tc5_wait_ld();
+          if (!inside) {
+            hide(s, (k0 + j) * kKeyPages + 2 * half);
+            hide(s + 32, (k0 + j) * kKeyPages + 2 * half + 1);
           }
-          m = mx * p.scale;
-        }
-        uint32_t pr[64];
-        float sum;
-        for (;;) {
-          // probabilities on the maximum so far, and this tile's maximum on the way
-          const float ms = m == -INFINITY ? 0.0f : m;
-          const float2 m2 = make_float2(-ms, -ms);
-          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          uint32_t sr[2][32];
-          tc5_ld32(sr[0], s_addr);
+          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
 #pragma unroll
-          for (int i = 0; i < kKeyPages; ++i) {
-            float* s = reinterpret_cast<float*>(sr[i & 1]);
-            tc5_wait_ld();
-            if (i + 1 < kKeyPages) tc5_ld32(sr[(i + 1) & 1], s_addr + 32 * (i + 1));
-            if (!inside) hide(s, (k0 + j) * kKeyPages + i);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
-              mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
-              float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
-              float2 y = fma2(make_float2(s[e + 2], s[e + 3]), sc2, m2);
-              x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-              sum0 = add2(sum0, x);
-              sum1 = add2(sum1, y);
-              pr[16 * i + e / 2] = T::pack(x.x, x.y);
-              pr[16 * i + e / 2 + 1] = T::pack(y.x, y.y);
-            }
+          for (int e = 4; e < 64; e += 4) {
+            mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
+            mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
           }
-          sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
-          const float mx = fmaxf(mx0, mx1) * p.scale;
-          const bool grow = mx > m + kGrowth;      // true where m is -inf and mx is not
-          if (!__any_sync(0xffffffffu, grow)) break;
-          // rare: a new maximum, O and l on it, and the tile once more
-          const float a = grow ? fast_exp2(m - mx) : 1.0f;
-          if (grow) m = mx;
-          l *= a;
-          if (j > 0) {
-            // S_w of this tile is there, so the products before it are complete
+          float mx = fmaxf(mx0, mx1) * p.scale;
+          // Is the maximum in use too small for a row?  Both halves agree.
+          if (meet(first || mx > m + kGrowth)) {
+            if (ok) *ex_mine = mx;
+            if (ok) meet(false);
+            if (!ok) break;
+            mx = fmaxf(mx, *ex_other);
+            const bool grow = first || mx > m + kGrowth;   // true where m is -inf and mx is not
+            const float a = grow && !first ? fast_exp2(m - mx) : 1.0f;
+            if (grow) m = mx;
+            if (!first) {
+              l *= a;
+              // S_w of this tile is there, so the products before it are complete
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[32];
-              tc5_ld32(o, o_addr + 32 * i);
-              tc5_wait_ld();
+              for (int i = 0; i < 2; ++i) {
+                uint32_t o[32];
+                tc5_ld32(o, o_addr + 32 * i);
+                tc5_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tc5_st32(o_addr + 32 * i, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                tc5_st32(o_addr + 32 * i, o);
+              }
             }
           }
         }
-        l += sum;
-        tc5_st32(s_addr, pr);
-        tc5_st32(s_addr + 32, pr + 32);
+        if (!ok) break;
+        const float ms = m == -INFINITY ? 0.0f : m;
+        const float2 m2 = make_float2(-ms, -ms);
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, m2);
+          float2 y = fma2(make_float2(s[e + 2], s[e + 3]), sc2, m2);
+          x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          sum0 = add2(sum0, x);
+          sum1 = add2(sum1, y);
+          sr[e / 2] = T::pack(x.x, x.y);
+          sr[e / 2 + 1] = T::pack(y.x, y.y);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        tc5_st32(s_addr, sr);
         tc5_wait_st();
         tc5_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[w]);
       }
+      if (!ok) break;
 
       // ------------------------------------------------------------ results
-      if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, abort);
-      if (!ok) break;
-      tc5_fence_after();
-      const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
-      const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-      float odd = l * 0.0f;            // NaN once anything is not finite
-      float* rec = p.part + (row * p.splits + split) * kRecFloats;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        if (my_n > 0) {
-          tc5_ld32(o, o_addr + 32 * i);
-          tc5_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+      uint32_t o[64];
+      float odd = 0.0f;                // NaN once anything is not finite
+      ++step;
+      if (my_n > 0) {
+        if (!__all_sync(0xffffffffu, tc5_wait(&sm.o_full[w], o_used & 1, abort))) {
+          give_up();
+          break;
         }
+        ++o_used;
+        tc5_fence_after();
+        tc5_ld32(o, o_addr);
+        tc5_ld32(o + 32, o_addr + 32);
+        tc5_wait_ld();
+        tc5_fence_before();            // the next item's products may overwrite O
 #pragma unroll
-        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+        for (int e = 0; e < 64; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+        // the row's sum, and whether either half has anything that is not finite
+        *ex_mine = odd != 0.0f ? NAN : l;
+        meet(false);
+        if (!ok) break;
+        odd = 0.0f * (*ex_other + l + odd);
+        l += *ex_other;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) o[e] = 0u;
+      }
+      const bool bad_row = odd != 0.0f;
+      const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
+      if (valid && !bad_row) {
         if (p.splits > 1) {
-          if (valid)
+          float* rec = p.part + (row * p.splits + split) * kRecFloats;
+          if (half == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+#pragma unroll
+          for (int e = 0; e < 64; e += 4)
+            *reinterpret_cast<uint4*>(rec + 4 + 64 * half + e) =
+                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          uint32_t* d = reinterpret_cast<uint32_t*>(p.out + row * kD) + 32 * half;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (p.wide) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global32(d + e, o + e);
+          } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
-                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        } else {
-          uint32_t v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (valid) {
-            uint32_t* d = reinterpret_cast<uint32_t*>(p.out + row * kD) + 16 * i;
-            if (p.wide) {
-              st_global32(d, v);
-              st_global32(d + 8, v + 8);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(d + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            }
+              *reinterpret_cast<uint4*>(d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
+          if (p.lse && half == 0) p.lse[row] = kv16_lse(m, l);
         }
       }
-      tc5_fence_before();       // O has been read: the next item's products may follow
-      if (valid) {
-        if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
-        else if (p.lse) p.lse[row] = kv16_lse(m, l);
-      }
-      // rows with a result that is not finite, token by token
+      // rows with a result that is not finite, token by token, by the first half's warp
       __syncwarp();
-      for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
+      for (unsigned bad = __ballot_sync(0xffffffffu, valid && bad_row && half == 0); bad;
+           bad &= bad - 1) {
         const int src = __ffs(bad) - 1;
         const long long rw = __shfl_sync(0xffffffffu, row, src);
         const int a = __shfl_sync(0xffffffffu, at, src);
@@ -597,7 +635,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     tc5_fence_before();
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSoftmaxWarps) {
     tc5_fence_after();
     tc5_dealloc(tmem, 512);
   }
@@ -663,7 +701,8 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
       !kv16_row_map(&mv, p.c, p.c.v))
     return cudaErrorNotSupported;
   const auto kernel = kv16_attention_kernel<T>;
-  constexpr int smem = (2 + kStages) * kTileBytes + 1024;
+  constexpr int smem = (2 + kStages) * kTileBytes + (int)sizeof(Smem);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(p.tiles * p.c.Hkv * p.splits, sm_count());
