@@ -45,13 +45,13 @@
 namespace oscar {
 namespace {
 
-constexpr int kSoftmaxWarps = 16;      // per query tile 2 x 4, each half of the columns
+constexpr int kSoftmaxWarps = 8;       // a warpgroup per query tile, a thread per row
 constexpr int kThreads = kSoftmaxWarps * 32 + 128;
 constexpr int kStages = 5;
 constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
 constexpr int kHalf = 16384;
 constexpr int kKeyPages = 4;           // pages of a key tile
-constexpr float kGrowth = 8.0f;        // log2 of the growth that O is not rescaled for
+constexpr float kMost = 4096.0f;       // sum of 64 probabilities that asks for a new maximum
 constexpr uint32_t kO = 256;           // TMEM columns: S_w at 128 w, O_w at 256 + 128 w
 
 struct AttnParams {
@@ -84,13 +84,11 @@ struct Item {
 
 struct Smem {
   uint64_t q_full[2], q_empty[2], full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], clean, drain[2];
+  uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], clean, drain[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int abort;
   Item item[kItems];
-  int quit[8];           // per pair of warps: the step at which one of them gave up
-  float ex[2][2][128];   // what the halves of a row tell each other
 };
 constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: all but one
 
@@ -176,7 +174,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 8);
+      mbar_init(&sm.p_full[i][0], 4);
+      mbar_init(&sm.p_full[i][1], 4);
+      mbar_init(&sm.h_full[i], 1);
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.drain[i], 1);
     }
@@ -187,7 +187,6 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_init(&sm.clean, 1);
     mbar_fence_init();
     sm.abort = 0;
-    for (int i = 0; i < 8; ++i) sm.quit[i] = 0x7fffffff;
   }
   tc5_fence_before();
   __syncthreads();
@@ -201,7 +200,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   };
 
   if (warp >= kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     bool ok = true;
     if (warp == kSoftmaxWarps + 3) {
       // -------------------------------------------------- scheduling: the items
@@ -365,15 +364,22 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             // the tile with the sequence's last page: its tail is cleared first
             if (ok && j == clear_at) ok = tc5_wait(&sm.clean, cleaned++ & 1, abort);
             if (ok && more) ok = tc5_wait(&sm.full[st], ph, abort);
-            if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w], p_used++ & 1, abort);
+            if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, abort);
             if (!ok) break;
             if (j < cnt) {
-              tc5_fence_after();
+              // P comes in halves of 64 keys
               const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
+              tc5_fence_after();
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                tc5_mma_ts(to, ts + (i >> 2) * 64 + (i & 3) * 8, v + i * (2048 >> 4), id_o,
-                           j > 0 || i > 0);
+              for (int i = 0; i < 4; ++i)
+                tc5_mma_ts(to, ts + 8 * i, v + i * (2048 >> 4), id_o, j > 0 || i > 0);
+              tc5_commit(&sm.h_full[w]);
+              ok = tc5_wait(&sm.p_full[w][1], p_used++ & 1, abort);
+              if (!ok) break;
+              tc5_fence_after();
+#pragma unroll
+              for (int i = 4; i < 8; ++i)
+                tc5_mma_ts(to, ts + 32 + 8 * i, v + i * (2048 >> 4), id_o, true);
               if (j + 1 < cnt) qk(st);
               else tc5_commit(&sm.o_full[w]);
               tc5_commit(&sm.empty[vs]);
@@ -397,50 +403,18 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     if (*abort && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // -------------------------------------------------------------- softmax
-    // Tile w; a row has two threads, each with half of the columns of S, and
-    // of O when O is touched.  Their warps meet at a barrier of their own.
-    const int w = warp >> 3, half = (warp >> 2) & 1, r = tid & 127, pair = 4 * w + (warp & 3);
+    const int w = warp >> 2, r = tid & 127;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t s_addr = lane_addr + 128 * w + 64 * half;
-    const uint32_t o_addr = lane_addr + kO + 128 * w + 64 * half;
+    const uint32_t s_addr = lane_addr + 128 * w, o_addr = lane_addr + kO + 128 * w;
     const int tok = r / p.g, head = r - tok * p.g;
     const float2 sc2 = make_float2(p.scale, p.scale);
-    volatile int* quit = &sm.quit[pair];
-    float* ex_mine = &sm.ex[w][half][r];
-    const float* ex_other = &sm.ex[w][half ^ 1][r];
     unsigned s_used = 0, o_used = 0;
-    // A warp that gives up at a wait says so, meets its partner once more and
-    // leaves; the partner, at its next meeting, sees a step that is not ahead
-    // of its own and leaves too: neither is left alone at the barrier.
-    int step = 0;
     bool ok = true;
-    auto meet = [&](bool x) -> bool {
-      uint32_t any;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-          "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(any)
-          : "r"((uint32_t)x), "r"(1 + pair)
-          : "memory");
-      if (*quit <= step) ok = false;
-      return any != 0;
-    };
-    auto give_up = [&] {
-      *quit = step;
-      __syncwarp();
-      meet(true);
-      ok = false;
-    };
     for (unsigned ni = 0; ok; ++ni) {
       const Item* ip = take(ni);
-      ++step;
-      if (__any_sync(0xffffffffu, ip == nullptr)) {
-        give_up();
-        break;
-      }
-      if (ip->stop) break;
+      if (!(ok = ip != nullptr) || ip->stop) break;
       const int ntok = min(p.tokens, ip->nrow - w * p.tokens), my_n = ip->cnt[w];
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
       const int at_first = ip->at0 + w * p.tokens, row_first = ip->row0 + w * p.tokens;
@@ -478,59 +452,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         for (int e = 0; e < 32; ++e)
           if (!((see >> e) & 1u)) s[e] = -INFINITY;
       };
+      // 64 scores to probabilities on the maximum in use, packed in place; their sum
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < my_n; ++j) {
-        ++step;
-        if (!__all_sync(0xffffffffu, tc5_wait(&sm.s_full[w], s_used & 1, abort))) {
-          give_up();
-          break;
-        }
-        ++s_used;
-        tc5_fence_after();
-        const bool inside = j >= in0 && j < in1;
-        uint32_t sr[64];
+      auto weigh = [&](uint32_t* sr) -> float {
         float* s = reinterpret_cast<float*>(sr);
-        const bool first = j == 0;
-        {
-          tc5_ld32(sr, s_addr);
-          tc5_ld32(sr + 32, s_addr + 32);
-          tc5_wait_ld();
-          if (!inside) {
-            hide(s, (k0 + j) * kKeyPages + 2 * half);
-            hide(s + 32, (k0 + j) * kKeyPages + 2 * half + 1);
-          }
-          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
-#pragma unroll
-          for (int e = 4; e < 64; e += 4) {
-            mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
-            mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
-          }
-          float mx = fmaxf(mx0, mx1) * p.scale;
-          // Is the maximum in use too small for a row?  Both halves agree.
-          if (meet(first || mx > m + kGrowth)) {
-            if (ok) *ex_mine = mx;
-            if (ok) meet(false);
-            if (!ok) break;
-            mx = fmaxf(mx, *ex_other);
-            const bool grow = first || mx > m + kGrowth;   // true where m is -inf and mx is not
-            const float a = grow && !first ? fast_exp2(m - mx) : 1.0f;
-            if (grow) m = mx;
-            if (!first) {
-              l *= a;
-              // S_w of this tile is there, so the products before it are complete
-#pragma unroll 1
-              for (int i = 0; i < 2; ++i) {
-                uint32_t o[32];
-                tc5_ld32(o, o_addr + 32 * i);
-                tc5_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                tc5_st32(o_addr + 32 * i, o);
-              }
-            }
-          }
-        }
-        if (!ok) break;
         const float ms = m == -INFINITY ? 0.0f : m;
         const float2 m2 = make_float2(-ms, -ms);
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
@@ -545,73 +470,133 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           sr[e / 2] = T::pack(x.x, x.y);
           sr[e / 2 + 1] = T::pack(y.x, y.y);
         }
-        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        tc5_st32(s_addr, sr);
-        tc5_wait_st();
-        tc5_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[w]);
+        return (sum0.x + sum0.y) + (sum1.x + sum1.y);
+      };
+      for (int j = 0; j < my_n; ++j) {
+        ok = tc5_wait(&sm.s_full[w], s_used & 1, abort);
+        if (!ok) break;
+        tc5_fence_after();
+        const bool inside = j >= in0 && j < in1;
+        uint32_t sr[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc5_ld32(sr + 32 * i, s_addr + 32 * i);
+        tc5_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t* x = sr + 64 * i;
+          const int v = (k0 + j) * kKeyPages + 2 * i;
+          if (!inside) {
+            hide(reinterpret_cast<float*>(x), v);
+            hide(reinterpret_cast<float*>(x) + 32, v + 1);
+          }
+          bool again = __any_sync(0xffffffffu, m == -INFINITY);
+          float sum = 0.0f;
+          if (!again) {
+            sum = weigh(x);
+            again = __any_sync(0xffffffffu, sum > kMost);
+          }
+          if (again) {
+            // a row without a maximum, or one that has outgrown it: the maximum
+            // of these 64 scores, O and l on the new one, and once more
+            tc5_ld32(x, s_addr + 64 * i);
+            tc5_ld32(x + 32, s_addr + 64 * i + 32);
+            tc5_wait_ld();
+            float* s = reinterpret_cast<float*>(x);
+            if (!inside) {
+              hide(s, v);
+              hide(s + 32, v + 1);
+            }
+            float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+            for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(s[e], s[e + 1]));
+            mx *= p.scale;
+            const bool grow = mx > m;       // true where m is -inf and mx is not
+            const float a = grow ? fast_exp2(m - mx) : 1.0f;
+            if (grow) m = mx;
+            l *= a;
+            if (i == 1) {
+              // the first half's product is under way
+              ok = tc5_wait(&sm.h_full[w], s_used & 1, abort);
+              if (!ok) break;
+              tc5_fence_after();
+            }
+            if (j > 0 || i == 1) {
+              // S of this tile is there, so the products of the tiles before are complete
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                uint32_t o[32];
+                tc5_ld32(o, o_addr + 32 * k);
+                tc5_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                tc5_st32(o_addr + 32 * k, o);
+              }
+            }
+            sum = weigh(x);
+          }
+          l += sum;
+          tc5_st32(s_addr + 64 * i, x);
+          tc5_wait_st();
+          tc5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[w][i]);
+        }
+        if (!ok) break;
+        ++s_used;
       }
-      if (!ok) break;
 
       // ------------------------------------------------------------ results
-      uint32_t o[64];
-      float odd = 0.0f;                // NaN once anything is not finite
-      ++step;
-      if (my_n > 0) {
-        if (!__all_sync(0xffffffffu, tc5_wait(&sm.o_full[w], o_used & 1, abort))) {
-          give_up();
-          break;
-        }
-        ++o_used;
-        tc5_fence_after();
-        tc5_ld32(o, o_addr);
-        tc5_ld32(o + 32, o_addr + 32);
-        tc5_wait_ld();
-        tc5_fence_before();            // the next item's products may overwrite O
-#pragma unroll
-        for (int e = 0; e < 64; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
-        // the row's sum, and whether either half has anything that is not finite
-        *ex_mine = odd != 0.0f ? NAN : l;
-        meet(false);
-        if (!ok) break;
-        odd = 0.0f * (*ex_other + l + odd);
-        l += *ex_other;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 64; ++e) o[e] = 0u;
-      }
-      const bool bad_row = odd != 0.0f;
+      if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, abort);
+      if (!ok) break;
+      tc5_fence_after();
       const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
-      if (valid && !bad_row) {
-        if (p.splits > 1) {
-          float* rec = p.part + (row * p.splits + split) * kRecFloats;
-          if (half == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+      const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      float odd = l * 0.0f;            // NaN once anything is not finite
+      float* rec = p.part + (row * p.splits + split) * kRecFloats;
 #pragma unroll
-          for (int e = 0; e < 64; e += 4)
-            *reinterpret_cast<uint4*>(rec + 4 + 64 * half + e) =
-                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        if (my_n > 0) {
+          tc5_ld32(o, o_addr + 32 * i);
+          tc5_wait_ld();
         } else {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          uint32_t* d = reinterpret_cast<uint32_t*>(p.out + row * kD) + 32 * half;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          if (p.wide) {
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) st_global32(d + e, o + e);
-          } else {
+        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+        if (p.splits > 1) {
+          if (valid)
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
+          uint32_t v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          if (valid) {
+            uint32_t* d = reinterpret_cast<uint32_t*>(p.out + row * kD) + 16 * i;
+            if (p.wide) {
+              st_global32(d, v);
+              st_global32(d + 8, v + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(d + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
           }
-          if (p.lse && half == 0) p.lse[row] = kv16_lse(m, l);
         }
       }
-      // rows with a result that is not finite, token by token, by the first half's warp
+      tc5_fence_before();       // O has been read: the next item's products may follow
+      if (valid) {
+        if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
+        else if (p.lse) p.lse[row] = kv16_lse(m, l);
+      }
+      // rows with a result that is not finite, token by token
       __syncwarp();
-      for (unsigned bad = __ballot_sync(0xffffffffu, valid && bad_row && half == 0); bad;
-           bad &= bad - 1) {
+      for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
         const int src = __ffs(bad) - 1;
         const long long rw = __shfl_sync(0xffffffffu, row, src);
         const int a = __shfl_sync(0xffffffffu, at, src);
