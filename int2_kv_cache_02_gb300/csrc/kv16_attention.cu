@@ -84,7 +84,7 @@ struct Item {
 
 struct Smem {
   uint64_t q_full[2], q_empty[2], full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], clean, drain[2];
+  uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], clean, drain[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int abort;
@@ -178,6 +178,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.h_full[i], 1);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.turn[i], 1);
       mbar_init(&sm.drain[i], 1);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -310,7 +311,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     } else {
       // -------------------------------------------------------------- MMAs
       // A warp per query tile: what one waits for passes under what the other
-      // has issued (the tensor cores' queue is too short to cover a wait).
+      // has issued (the tensor cores' queue is too short to cover a wait).  They
+      // take turns, a key tile's products at a time: so one tile's scores come
+      // while the other's softmax runs, and not both at once.
       const int w = warp - kSoftmaxWarps - 1;
       if (elect_one()) {
         const uint32_t id_s = tc5_idesc(T::kHalf, 128, 128, false, p.negate);
@@ -336,7 +339,12 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ph ^= 1;
           }
         };
-        unsigned q_used = 0, p_used = 0, cleaned = 0;
+        unsigned q_used = 0, p_used = 0, cleaned = 0, turns = 0;
+        auto my_turn = [&]() -> bool {
+          const unsigned n = turns++;
+          if (w == 1) return tc5_wait(&sm.turn[1], n & 1, abort);
+          return n == 0 || tc5_wait(&sm.turn[0], (n - 1) & 1, abort);
+        };
         for (unsigned ni = 0; ok; ++ni) {
           const Item* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
@@ -345,16 +353,18 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (nk == 0) continue;
           // a stage that this tile has no use for is given back as it comes
           ok = tc5_wait(&sm.full[st], ph, abort);
-          if (ok && cnt > 0) {
-            ok = tc5_wait(&sm.q_full[w], q_used++ & 1, abort);
-            if (!ok) break;
+          if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, abort);
+          if (ok) ok = my_turn();
+          if (!ok) break;
+          if (cnt > 0) {
             tc5_fence_after();
             qk(st);
             if (cnt == 1) tc5_commit(&sm.q_empty[w]);
             tc5_commit(&sm.empty[st]);
-          } else if (ok) {
+          } else {
             mbar_arrive(&sm.empty[st]);
           }
+          mbar_arrive(&sm.turn[w ^ 1]);
           next();
           for (int j = 0; j < nk && ok; ++j) {
             const unsigned vs = st, vp = ph;
@@ -365,6 +375,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             if (ok && j == clear_at) ok = tc5_wait(&sm.clean, cleaned++ & 1, abort);
             if (ok && more) ok = tc5_wait(&sm.full[st], ph, abort);
             if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, abort);
+            if (ok) ok = my_turn();
             if (!ok) break;
             if (j < cnt) {
               // P comes in halves of 64 keys
@@ -382,9 +393,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                 tc5_mma_ts(to, ts + 32 + 8 * i, v + i * (2048 >> 4), id_o, true);
               if (j + 1 < cnt) qk(st);
               else tc5_commit(&sm.o_full[w]);
+              mbar_arrive(&sm.turn[w ^ 1]);
               tc5_commit(&sm.empty[vs]);
               if (j + 2 == cnt) tc5_commit(&sm.q_empty[w]);
             } else {
+              mbar_arrive(&sm.turn[w ^ 1]);
               mbar_arrive(&sm.empty[vs]);
             }
             if (more) {
