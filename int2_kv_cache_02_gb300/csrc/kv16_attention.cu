@@ -498,43 +498,36 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         for (int i = 0; i < 2; ++i) {
           uint32_t* x = sr + 64 * i;
           const int v = (k0 + j) * kKeyPages + 2 * i;
-          if (!inside) {
+          auto mask = [&] {
+            if (inside) return;
             hide(reinterpret_cast<float*>(x), v);
             hide(reinterpret_cast<float*>(x) + 32, v + 1);
-          }
-          bool again = __any_sync(0xffffffffu, m == -INFINITY);
-          float sum = 0.0f;
-          if (!again) {
-            sum = weigh(x);
-            again = __any_sync(0xffffffffu, sum > kMost);
-          }
-          if (again) {
-            // a row without a maximum, or one that has outgrown it: the maximum
-            // of these 64 scores, O and l on the new one, and once more
-            tc5_ld32(x, s_addr + 64 * i);
-            tc5_ld32(x + 32, s_addr + 64 * i + 32);
-            tc5_wait_ld();
-            float* s = reinterpret_cast<float*>(x);
-            if (!inside) {
-              hide(s, v);
-              hide(s + 32, v + 1);
-            }
-            float mx = fmaxf(s[0], s[1]);
+          };
+          // the maximum of these scores where a row has none or outgrew it, and
+          // l and O on it
+          auto raise = [&] {
+            const float* s = reinterpret_cast<const float*>(x);
+            float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
 #pragma unroll
-            for (int e = 2; e < 64; e += 2) mx = fmaxf(mx, fmaxf(s[e], s[e + 1]));
-            mx *= p.scale;
-            const bool grow = mx > m;       // true where m is -inf and mx is not
-            const float a = grow ? fast_exp2(m - mx) : 1.0f;
+            for (int e = 4; e < 64; e += 4) {
+              mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
+              mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
+            }
+            const float mx = fmaxf(mx0, mx1) * p.scale;
+            const bool grow = mx > m;         // true where m is -inf and mx is not
+            const bool worked = grow && m != -INFINITY;    // (else l and O are 0)
+            const float a = worked ? fast_exp2(m - mx) : 1.0f;
             if (grow) m = mx;
+            if (!__any_sync(0xffffffffu, worked)) return;
             l *= a;
+            // S of this tile is there, so the products of the tiles before it are
+            // complete; that of the first half may be under way
             if (i == 1) {
-              // the first half's product is under way
               ok = tc5_wait(&sm.h_full[w], s_used & 1, abort);
-              if (!ok) break;
+              if (!ok) return;
               tc5_fence_after();
             }
             if (j > 0 || i == 1) {
-              // S of this tile is there, so the products of the tiles before are complete
 #pragma unroll 1
               for (int k = 0; k < 4; ++k) {
                 uint32_t o[32];
@@ -545,8 +538,19 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                 tc5_st32(o_addr + 32 * k, o);
               }
             }
+          };
+          mask();
+          if (__any_sync(0xffffffffu, m == -INFINITY)) raise();
+          float sum = weigh(x);
+          if (__any_sync(0xffffffffu, sum > kMost)) {
+            tc5_ld32(x, s_addr + 64 * i);
+            tc5_ld32(x + 32, s_addr + 64 * i + 32);
+            tc5_wait_ld();
+            mask();
+            raise();
             sum = weigh(x);
           }
+          if (!ok) break;
           l += sum;
           tc5_st32(s_addr + 64 * i, x);
           tc5_wait_st();
@@ -564,7 +568,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       tc5_fence_after();
       const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
       const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-      float odd = l * 0.0f;            // NaN once anything is not finite
+      float odd = l * 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: not finite
       float* rec = p.part + (row * p.splits + split) * kRecFloats;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -577,7 +581,12 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+        for (int e = 0; e < 32; e += 4) {
+          odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+          odd1 = fmaf(__uint_as_float(o[e + 1]), 0.0f, odd1);
+          odd2 = fmaf(__uint_as_float(o[e + 2]), 0.0f, odd2);
+          odd3 = fmaf(__uint_as_float(o[e + 3]), 0.0f, odd3);
+        }
         if (p.splits > 1) {
           if (valid)
 #pragma unroll
@@ -603,6 +612,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
       }
       tc5_fence_before();       // O has been read: the next item's products may follow
+      odd += odd1 + odd2 + odd3;
       if (valid) {
         if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
         else if (p.lse) p.lse[row] = kv16_lse(m, l);
