@@ -132,7 +132,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // log(sum exp) from a maximum in the log2 domain and a sum relative to it.
 __device__ __forceinline__ float kv16_lse(float m, float l) {
-  return l > 0.0f ? (m + log2f(l)) * kLn2 : (l == 0.0f ? -INFINITY : l);
+  return l > 0.0f ? (m + __log2f(l)) * kLn2 : (l == 0.0f ? -INFINITY : l);
 }
 
 }  // namespace oscar

@@ -22,6 +22,7 @@
 // issues the MMAs, two that lay out the query rows' lse.
 // TMEM: two buffers of S^T for each warpgroup.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv16.cuh"
 #include "kv16_tma.h"
@@ -311,9 +312,9 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
           const int clo = min(lo, 128) * p.g;
           const unsigned cn = max(hi - lo, 0) * p.g;
           const float* ls = sm.lse[slot];
-          uint32_t s0[64], s1[64];
           const uint32_t sa = s_base + 128 * buf;
-          auto add = [&](const uint32_t* s, int c0) {
+          // 64 columns; tiles that every row of sees every key take the short way
+          auto add = [&](auto all, const uint32_t* s, int c0) {
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
               const float4 z = *reinterpret_cast<const float4*>(ls + c0 + e);
@@ -323,7 +324,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
                               make_float2(z.z, z.w));
               u = make_float2(fast_exp2(u.x), fast_exp2(u.y));
               v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
-              if (!whole) {
+              if constexpr (!decltype(all)::value) {
                 const int c = c0 + e - clo;
                 u.x = (unsigned)c < cn ? u.x : 0.0f;
                 u.y = (unsigned)(c + 1) < cn ? u.y : 0.0f;
@@ -334,17 +335,22 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
               a1 = add2(a1, v);
             }
           };
-          tc5_ld32(s0, sa);
-          tc5_ld32(s0 + 32, sa + 32);
-          tc5_wait_ld();
-          tc5_ld32(s1, sa + 64);
-          tc5_ld32(s1 + 32, sa + 96);
-          add(s0, 0);
-          tc5_wait_ld();
-          tc5_fence_before();
-          __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
-          add(s1, 64);
+          auto tile = [&](auto all) {
+            uint32_t s0[64], s1[64];
+            tc5_ld32(s0, sa);
+            tc5_ld32(s0 + 32, sa + 32);
+            tc5_wait_ld();
+            tc5_ld32(s1, sa + 64);
+            tc5_ld32(s1 + 32, sa + 96);
+            add(all, s0, 0);
+            tc5_wait_ld();
+            tc5_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
+            add(all, s1, 64);
+          };
+          if (whole) tile(std::true_type());
+          else tile(std::false_type());
           ++us;
         }
         __syncwarp();
