@@ -13,10 +13,11 @@
 // cycles.  With 128 keys per item the query tiles alone would take all of an
 // SM's 64 B per cycle from L2.
 //
-// Many items: one CTA per SM walks over them, the next item's keys on their way
-// while it works.  Few (few heads or short caches): the query tiles of an item
-// are cut over a cluster's CTAs, which hand their sums to the first through
-// distributed shared memory, added in order of rank.
+// Fewer work items than two for every SM: 128 keys each, whose query tiles the
+// two warpgroups take by turns.  One CTA per SM walks over the items, the
+// next one's keys on their way while it works.  Fewer items than SMs: their
+// query tiles are cut over a cluster's CTAs, which hand their sums to the first
+// through distributed shared memory, added in order of rank.
 //
 // Roles (12 warps): two warpgroups that sum, one warp that copies, one that
 // issues the MMAs, two that lay out the query rows' lse.
@@ -34,23 +35,25 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTileBytes = 32768, kHalf = 16384;
 constexpr int kQStages = 3, kKBufs = 2, kLseSlots = 3;
-constexpr int kItemKeys = 256;
+constexpr int kItemKeys = 256;     // or 128
 
 struct AccParams {
   Kv16 c;
   Kv16Query q;
   const float* lse;
   int n_obs, g, tokens;
+  int keys;         // keys of a work item: 256 or 128
   int items;        // key blocks * B * Hkv
   int cluster;      // CTAs that share an item
 };
 
 struct Smem {
   uint64_t k_full[kKBufs], k_empty[kKBufs], q_full[kQStages], q_empty[kQStages];
-  uint64_t s_full[2][2], s_empty[2][2], l_full[kLseSlots], l_empty[kLseSlots], drain;
+  uint64_t s_full[2][2], s_empty[2][2], l_full[kLseSlots], l_empty[kLseSlots], c_full, c_empty, drain;
   uint32_t tmem;
   int abort;
   alignas(16) float lse[kLseSlots][128];   // at the end: the CTA's sums
+  float part[128];                         // one warpgroup's sums of a lone key tile
 };
 static_assert(kLseSlots * 128 >= kItemKeys, "room for the sums");
 
@@ -60,18 +63,20 @@ struct Item {
   int r0, at_first;   // first row of the sequence's queries, its position
   int ia, ib;         // its queries that may see a key of the item
   int t0, t1;         // this CTA's query tiles of them
-  int halves;         // key tiles that hold tokens
+  int halves;         // key tiles that hold tokens: a warpgroup each, or one for both,
+                      // which take its query tiles by turns
 };
 
 __device__ __forceinline__ Item find_item(const AccParams& p, int x, int rank, bool report) {
   Item it;
+  it.t0 = it.t1 = 0;
+  it.halves = 0;
+  if (x >= p.items) return it;
   const int rows = p.c.B * p.c.Hkv;
   const int kb = x / rows, row = x - kb * rows;     // the first keys have the most queries
   it.b = row / p.c.Hkv;
   it.h = row - it.b * p.c.Hkv;
-  it.key0 = kb * kItemKeys;
-  it.t0 = it.t1 = 0;
-  it.halves = 0;
+  it.key0 = kb * p.keys;
   const int n = __ldg(p.c.n_tok + it.b);
   const int r0 = __ldg(p.q.start + it.b), r1 = __ldg(p.q.start + it.b + 1), nq = r1 - r0;
   it.n = n;
@@ -84,14 +89,14 @@ __device__ __forceinline__ Item find_item(const AccParams& p, int x, int rank, b
   it.at_first = n - nq;
   it.ia = max(max(0, it.key0 - it.at_first), p.n_obs > 0 ? nq - p.n_obs : 0);
   it.ib = nq;
-  const int last = min(it.key0 + kItemKeys, n) - 1;
+  const int last = min(it.key0 + p.keys, n) - 1;
   if (p.q.window > 0 && it.key0 >= p.q.n_sink)
     it.ib = (int)min((long long)nq, (long long)last + p.q.window - it.at_first);
   if (it.ib <= it.ia) return it;
   const int nt = (it.ib - it.ia + p.tokens - 1) / p.tokens;
   it.t0 = (int)((long long)nt * rank / p.cluster);
   it.t1 = (int)((long long)nt * (rank + 1) / p.cluster);
-  it.halves = n - it.key0 > 128 ? 2 : 1;
+  it.halves = p.keys == 256 && n - it.key0 > 128 ? 2 : 1;
   return it;
 }
 
@@ -99,14 +104,25 @@ template <class T>
 __global__ void __launch_bounds__(kThreads, 1)
 kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_k, const AccParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Smem sm;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % p.cluster, first = blockIdx.x / p.cluster;
+  // item of a round, or -1: rounds in turn forwards and backwards, so that a CTA
+  // with the longest of one round gets the shortest of the next
   const int step = gridDim.x / p.cluster;
-  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  auto item_of = [&](int round) -> int {
+    if ((long long)round * step >= p.items) return -1;
+    const long long x = (long long)round * step + ((round & 1) ? step - 1 - first : first);
+    return x < p.items ? (int)x : p.items;
+  };
+  Smem& sm = *reinterpret_cast<Smem*>(smem + (kKBufs * 2 + kQStages) * kTileBytes);
   uint8_t* kbuf = smem;                                    // [kKBufs][2] key tiles
   uint8_t* qring = smem + kKBufs * 2 * kTileBytes;         // [kQStages] query tiles
+
+  if (smem_u32(smem) & 1023) {                             // the swizzle counts on it
+    if (tid == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    return;
+  }
 
   if (warp == 8) tc5_alloc(&sm.tmem, 512);
   if (tid == 0) {
@@ -127,6 +143,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&sm.l_full[i], 2);
       mbar_init(&sm.l_empty[i], 8);
     }
+    mbar_init(&sm.c_full, 4);
+    mbar_init(&sm.c_empty, 4);
     mbar_init(&sm.drain, 1);
     mbar_fence_init();
     sm.abort = 0;
@@ -152,8 +170,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
                                : p.c.B * p.c.Hkv * p.c.T_cap;        // reads zeros
     int uk = 0, uq = 0;
-    for (int x = first; x < p.items && ok; x += step) {
-      const Item it = find_item(p, x, rank, rank == 0 && lane == 0);
+    for (int round = 0; ok && item_of(round) >= 0; ++round) {
+      const Item it = find_item(p, item_of(round), rank, rank == 0 && lane == 0);
       if (it.t1 <= it.t0) continue;
       int row = none;
       if (lane < 8) {
@@ -211,8 +229,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       constexpr uint64_t kBase = tc5_desc_base(16, 1024);
       const uint64_t dk = tc5_desc(kBase, smem_u32(kbuf)), dq = tc5_desc(kBase, smem_u32(qring));
       unsigned kb = 0, kp = 0, st = 0, sp = 0, us[2] = {0, 0};
-      for (int x = first; x < p.items && ok; x += step) {
-        const Item it = find_item(p, x, rank, false);
+      for (int round = 0; ok && item_of(round) >= 0; ++round) {
+        const Item it = find_item(p, item_of(round), rank, false);
         if (it.t1 <= it.t0) continue;
         ok = tc5_wait(&sm.k_full[kb], kp, abort);
         for (int t = it.t0; t < it.t1 && ok; ++t) {
@@ -220,12 +238,12 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
           const uint64_t q = dq + st * (kTileBytes >> 4);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (w >= it.halves || !ok) break;
+            if (!ok || (it.halves == 1 && ((t - it.t0) & 1) != w)) continue;
             const unsigned buf = us[w] & 1;
             if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, abort);
-            if (!ok) break;
+            if (!ok) continue;
             tc5_fence_after();
-            const uint64_t k = dk + (kb * 2 + w) * (kTileBytes >> 4);
+            const uint64_t k = dk + (kb * 2 + (it.halves == 2 ? w : 0)) * (kTileBytes >> 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const unsigned off = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
@@ -257,8 +275,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     // ---------------------------------------------- lse of the rows
     int ul = 0;
     const int i0 = tid - 320;
-    for (int x = first; x < p.items && ok; x += step) {
-      const Item it = find_item(p, x, rank, false);
+    for (int round = 0; ok && item_of(round) >= 0; ++round) {
+      const Item it = find_item(p, item_of(round), rank, false);
       for (int t = it.t0; t < it.t1; ++t) {
         const int slot = ul % kLseSlots;
         float v[2];
@@ -285,17 +303,17 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     const int w = warp >> 2;
     const uint32_t s_base = tmem + ((uint32_t)(warp & 3) << 21) + 256 * w;
     const float2 sc = make_float2(p.q.scale_log2, p.q.scale_log2);
-    int ul = 0, us = 0;
-    for (int x = first; x < p.items && ok; x += step) {
-      const Item it = find_item(p, x, rank, false);
+    int ul = 0, us = 0, lone = 0;
+    for (int round = 0; ok && item_of(round) >= 0; ++round) {
+      const Item it = find_item(p, item_of(round), rank, false);
       if (it.t1 <= it.t0) continue;
-      const int tile0 = it.key0 + 128 * w, j = tile0 + (tid & 127);
+      const int tile0 = it.key0 + (it.halves == 2 ? 128 * w : 0), j = tile0 + (tid & 127);
       float2 a0 = make_float2(0.0f, 0.0f), a1 = a0;
       for (int t = it.t0; t < it.t1; ++t) {
         const int slot = ul % kLseSlots;
         ok = tc5_wait(&sm.l_full[slot], (ul / kLseSlots) & 1, abort);
         if (!ok) break;
-        if (w < it.halves) {
+        if (it.halves == 2 || ((t - it.t0) & 1) == w) {
           const int buf = us & 1;
           ok = tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, abort);
           if (!ok) break;
@@ -358,7 +376,26 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
         ++ul;
       }
       sum = (a0.x + a0.y) + (a1.x + a1.y);
-      if (p.cluster == 1 && ok && j < it.n) {
+      if (p.cluster > 1 || !ok) continue;
+      if (it.halves == 1) {
+        // both warpgroups have a part: the second hands its over
+        if (w == 1) {
+          if (lone > 0) ok = tc5_wait(&sm.c_empty, (lone - 1) & 1, abort);
+          if (!ok) break;
+          sm.part[tid & 127] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.c_full);
+        } else {
+          ok = tc5_wait(&sm.c_full, lone & 1, abort);
+          if (!ok) break;
+          sum += sm.part[tid];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.c_empty);
+        }
+        ++lone;
+        if (w == 1) continue;
+      }
+      if (j < it.n) {
         const int row = kv16_block_row(p.c, it.b, it.h, j / kPage);
         if (row >= 0) p.c.weight[(long long)row + j % kPage] += sum;
       }
@@ -379,15 +416,17 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     if (rank == 0 && tid < kItemKeys && first < p.items) {
       const Item it = find_item(p, first, 0, false);
       const int j = it.key0 + tid;
-      if (it.halves > 0 && j < it.n) {
+      if (it.halves > 0 && j < it.n && tid < p.keys) {
         float all = 0.0f;
-        for (int r = 0; r < p.cluster; ++r) {
-          unsigned far;
-          float v;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(smem_u32(sums + tid)), "r"(r));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
-          all += v;
-        }
+        for (int r = 0; r < p.cluster; ++r)
+          for (int i = tid; i < kItemKeys; i += it.halves == 2 ? kItemKeys : 128) {
+            unsigned far;
+            float v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(far) : "r"(smem_u32(sums + i)), "r"(r));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
+            all += v;
+          }
         const int row = kv16_block_row(p.c, it.b, it.h, j / kPage);
         if (row >= 0) p.c.weight[(long long)row + j % kPage] += all;
       }
@@ -405,18 +444,23 @@ cudaError_t launch(AccParams p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // two items for every SM keep the SMs about equally busy; fewer are cut over
-  // clusters until the CTAs are three for every SM, at two query tiles or more each
+  // items of 256 keys where there are two for every SM, else of 128; where even
+  // those are fewer than the SMs, clusters share them, at four query tiles or
+  // more for every CTA
   const long long rows = p.n_obs > 0 ? std::min<long long>(p.q.total, (long long)p.n_obs * p.c.B)
                                      : p.q.total;
   const long long tiles = std::max(1LL, rows / p.c.B / p.tokens);
+  const int most = std::min(p.q.max_tok, p.c.cap);
+  auto items = [&](int keys) { return ((long long)most + keys - 1) / keys * p.c.B * p.c.Hkv; };
+  p.keys = items(256) >= 2 * sms ? 256 : 128;
+  if (items(p.keys) > 0x3fffffffLL) return cudaErrorInvalidValue;
+  p.items = (int)items(p.keys);
   p.cluster = 1;
-  if (p.items < 2 * sms)
-    while (p.cluster < 8 && (long long)p.items * p.cluster < 3LL * sms && tiles >= 4 * p.cluster)
-      p.cluster *= 2;
+  while (p.cluster < 8 && (long long)p.items * p.cluster < sms && tiles >= 8 * p.cluster)
+    p.cluster *= 2;
   const auto kernel = kv16_accumulate_kernel<T>;
-  constexpr int smem = (kKBufs * 2 + kQStages) * kTileBytes + 1024;
-  static_assert(smem + (int)sizeof(Smem) <= 227 * 1024, "shared memory of a CTA");
+  constexpr int smem = (kKBufs * 2 + kQStages) * kTileBytes + (int)sizeof(Smem);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -444,10 +488,6 @@ cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const floa
   p.n_obs = n_obs;
   p.g = q.Hq / c.Hkv;
   p.tokens = 128 / p.g;
-  const long long blocks = ((long long)std::min(q.max_tok, c.cap) + kItemKeys - 1) / kItemKeys;
-  const long long items = blocks * c.B * c.Hkv;
-  if (items > 0x3fffffffLL) return cudaErrorInvalidValue;
-  p.items = (int)items;
   return c.half ? launch<Fp16>(p, s) : launch<Bf16>(p, s);
 }
 
