@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTileBytes = 32768, kHalf = 16384;
-constexpr int kQStages = 3, kKBufs = 2, kLseSlots = 3;
+constexpr int kQStages = 3, kKBufs = 2, kLseSlots = 2;
 constexpr int kItemKeys = 256;     // or 128
 
 struct AccParams {
@@ -49,13 +49,13 @@ struct AccParams {
 
 struct Smem {
   uint64_t k_full[kKBufs], k_empty[kKBufs], q_full[kQStages], q_empty[kQStages];
-  uint64_t s_full[2][2], s_empty[2][2], l_full[kLseSlots], l_empty[kLseSlots], c_full, c_empty, drain;
+  uint64_t s_full[2][2], s_empty[2][2], l_full[2][kLseSlots], l_empty[2][kLseSlots], c_full, c_empty, drain;
   uint32_t tmem;
   int abort;
-  alignas(16) float lse[kLseSlots][128];   // at the end: the CTA's sums
+  alignas(16) float lse[2][kLseSlots][128];   // per warpgroup; at the end: the CTA's sums
   float part[128];                         // one warpgroup's sums of a lone key tile
 };
-static_assert(kLseSlots * 128 >= kItemKeys, "room for the sums");
+static_assert(2 * kLseSlots * 128 >= kItemKeys, "room for the sums");
 
 // A work item as every role sees it; t1 <= t0: nothing to do.
 struct Item {
@@ -139,10 +139,11 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
         mbar_init(&sm.s_full[w][i], 1);
         mbar_init(&sm.s_empty[w][i], 4);
       }
-    for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(&sm.l_full[i], 2);
-      mbar_init(&sm.l_empty[i], 8);
-    }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < kLseSlots; ++i) {
+        mbar_init(&sm.l_full[w][i], 1);
+        mbar_init(&sm.l_empty[w][i], 4);
+      }
     mbar_init(&sm.c_full, 4);
     mbar_init(&sm.c_empty, 4);
     mbar_init(&sm.drain, 1);
@@ -272,28 +273,43 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     __syncwarp();
   } else if (warp >= 10) {
-    // ---------------------------------------------- lse of the rows
-    int ul = 0;
-    const int i0 = tid - 320;
+    // ------------------------------ lse of the rows, a warp for each warpgroup
+    const int w = warp - 10;
+    int tok[4], col[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = lane + 32 * k;
+      tok[k] = r / p.g;
+      col[k] = r - tok[k] * p.g;
+    }
+    unsigned ul = 0;
     for (int round = 0; ok && item_of(round) >= 0; ++round) {
       const Item it = find_item(p, item_of(round), rank, false);
-      for (int t = it.t0; t < it.t1; ++t) {
-        const int slot = ul % kLseSlots;
-        float v[2];
+      const int by = it.halves == 1 ? 2 : 1;
+      float v[4], next[4];
+      auto load = [&](int t, float (&x)[4]) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = i0 + 64 * k, tok = r / p.g, head = r - tok * p.g;
-          const int q = it.ia + t * p.tokens + tok;
-          const bool there = tok < p.tokens && q < it.ib;
-          v[k] = there ? -kLog2e * __ldg(p.lse + (long long)(it.r0 + q) * p.q.Hq + it.h * p.g + head)
-                       : -INFINITY;
+        for (int k = 0; k < 4; ++k) {
+          const int q = it.ia + t * p.tokens + tok[k];
+          x[k] = tok[k] < p.tokens && q < it.ib
+                     ? -kLog2e * __ldg(p.lse + (long long)(it.r0 + q) * p.q.Hq + it.h * p.g + col[k])
+                     : -INFINITY;
         }
-        if (ul >= kLseSlots) ok = tc5_wait(&sm.l_empty[slot], (ul / kLseSlots - 1) & 1, abort);
+      };
+      int t = it.t0 + (by == 2 ? w : 0);
+      if (t < it.t1) load(t, v);
+      for (; t < it.t1; t += by) {
+        if (t + by < it.t1) load(t + by, next);      // on its way while this one waits
+        const unsigned slot = ul % kLseSlots;
+        if (ul >= kLseSlots) ok = tc5_wait(&sm.l_empty[w][slot], (ul / kLseSlots - 1) & 1, abort);
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) sm.lse[slot][i0 + 64 * k] = v[k];
+        for (int k = 0; k < 4; ++k) {
+          sm.lse[w][slot][lane + 32 * k] = v[k];
+          v[k] = next[k];
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.l_full[slot]);
+        if (lane == 0) mbar_arrive(&sm.l_full[w][slot]);
         ++ul;
       }
     }
@@ -303,76 +319,73 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     const int w = warp >> 2;
     const uint32_t s_base = tmem + ((uint32_t)(warp & 3) << 21) + 256 * w;
     const float2 sc = make_float2(p.q.scale_log2, p.q.scale_log2);
-    int ul = 0, us = 0, lone = 0;
+    unsigned ul = 0, us = 0, lone = 0;
     for (int round = 0; ok && item_of(round) >= 0; ++round) {
       const Item it = find_item(p, item_of(round), rank, false);
       if (it.t1 <= it.t0) continue;
       const int tile0 = it.key0 + (it.halves == 2 ? 128 * w : 0), j = tile0 + (tid & 127);
       float2 a0 = make_float2(0.0f, 0.0f), a1 = a0;
-      for (int t = it.t0; t < it.t1; ++t) {
-        const int slot = ul % kLseSlots;
-        ok = tc5_wait(&sm.l_full[slot], (ul / kLseSlots) & 1, abort);
+      const int by = it.halves == 1 ? 2 : 1;
+      for (int t = it.t0 + (by == 2 ? w : 0); t < it.t1; t += by) {
+        const unsigned slot = ul % kLseSlots, buf = us & 1;
+        ok = tc5_wait(&sm.l_full[w][slot], (ul / kLseSlots) & 1, abort) &&
+             tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, abort);
         if (!ok) break;
-        if (it.halves == 2 || ((t - it.t0) & 1) == w) {
-          const int buf = us & 1;
-          ok = tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, abort);
-          if (!ok) break;
-          tc5_fence_after();
-          // the tokens [lo, hi) of the tile that see the thread's key: rows are
-          // token-major, so they are columns [lo g, hi g)
-          const int q_lo = it.ia + t * p.tokens, ntok = min(p.tokens, it.ib - q_lo);
-          const int at = it.at_first + q_lo;
-          const int lo = max(0, j - at);
-          int hi = ntok;
-          if (p.q.window > 0 && j >= p.q.n_sink)
-            hi = (int)min((long long)hi, max(0LL, (long long)j + p.q.window - at));
-          const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == p.tokens);
-          const int clo = min(lo, 128) * p.g;
-          const unsigned cn = max(hi - lo, 0) * p.g;
-          const float* ls = sm.lse[slot];
-          const uint32_t sa = s_base + 128 * buf;
-          // 64 columns; tiles that every row of sees every key take the short way
-          auto add = [&](auto all, const uint32_t* s, int c0) {
+        tc5_fence_after();
+        // the tokens [lo, hi) of the tile that see the thread's key: rows are
+        // token-major, so they are columns [lo g, hi g)
+        const int q_lo = it.ia + t * p.tokens, ntok = min(p.tokens, it.ib - q_lo);
+        const int at = it.at_first + q_lo;
+        const int lo = max(0, j - at);
+        int hi = ntok;
+        if (p.q.window > 0 && j >= p.q.n_sink)
+          hi = (int)min((long long)hi, max(0LL, (long long)j + p.q.window - at));
+        const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == p.tokens);
+        const int clo = min(lo, 128) * p.g;
+        const unsigned cn = max(hi - lo, 0) * p.g;
+        const float* ls = sm.lse[w][slot];
+        const uint32_t sa = s_base + 128 * buf;
+        // 64 columns; tiles that every row of sees every key take the short way
+        auto add = [&](auto all, const uint32_t* s, int c0) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              const float4 z = *reinterpret_cast<const float4*>(ls + c0 + e);
-              float2 u = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc,
-                              make_float2(z.x, z.y));
-              float2 v = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sc,
-                              make_float2(z.z, z.w));
-              u = make_float2(fast_exp2(u.x), fast_exp2(u.y));
-              v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
-              if constexpr (!decltype(all)::value) {
-                const int c = c0 + e - clo;
-                u.x = (unsigned)c < cn ? u.x : 0.0f;
-                u.y = (unsigned)(c + 1) < cn ? u.y : 0.0f;
-                v.x = (unsigned)(c + 2) < cn ? v.x : 0.0f;
-                v.y = (unsigned)(c + 3) < cn ? v.y : 0.0f;
-              }
-              a0 = add2(a0, u);
-              a1 = add2(a1, v);
+          for (int e = 0; e < 64; e += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(ls + c0 + e);
+            float2 u = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc,
+                            make_float2(z.x, z.y));
+            float2 v = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sc,
+                            make_float2(z.z, z.w));
+            u = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+            v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+            if constexpr (!decltype(all)::value) {
+              const int c = c0 + e - clo;
+              u.x = (unsigned)c < cn ? u.x : 0.0f;
+              u.y = (unsigned)(c + 1) < cn ? u.y : 0.0f;
+              v.x = (unsigned)(c + 2) < cn ? v.x : 0.0f;
+              v.y = (unsigned)(c + 3) < cn ? v.y : 0.0f;
             }
-          };
-          auto tile = [&](auto all) {
-            uint32_t s0[64], s1[64];
-            tc5_ld32(s0, sa);
-            tc5_ld32(s0 + 32, sa + 32);
-            tc5_wait_ld();
-            tc5_ld32(s1, sa + 64);
-            tc5_ld32(s1 + 32, sa + 96);
-            add(all, s0, 0);
-            tc5_wait_ld();
-            tc5_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
-            add(all, s1, 64);
-          };
-          if (whole) tile(std::true_type());
-          else tile(std::false_type());
-          ++us;
-        }
+            a0 = add2(a0, u);
+            a1 = add2(a1, v);
+          }
+        };
+        auto tile = [&](auto all) {
+          uint32_t s0[64], s1[64];
+          tc5_ld32(s0, sa);
+          tc5_ld32(s0 + 32, sa + 32);
+          tc5_wait_ld();
+          tc5_ld32(s1, sa + 64);
+          tc5_ld32(s1 + 32, sa + 96);
+          add(all, s0, 0);
+          tc5_wait_ld();
+          tc5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
+          add(all, s1, 64);
+        };
+        if (whole) tile(std::true_type());
+        else tile(std::false_type());
+        ++us;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.l_empty[slot]);
+        if (lane == 0) mbar_arrive(&sm.l_empty[w][slot]);
         ++ul;
       }
       sum = (a0.x + a0.y) + (a1.x + a1.y);
@@ -410,7 +423,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   if (p.cluster > 1) {
     // one item per cluster: its sums in order of rank
-    float* sums = sm.lse[0];
+    float* sums = sm.lse[0][0];
     if (tid < kItemKeys) sums[tid] = sum;
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && tid < kItemKeys && first < p.items) {
