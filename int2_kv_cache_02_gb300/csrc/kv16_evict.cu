@@ -6,6 +6,16 @@
 // of the same order; three rounds of counting (11, 11 and 10 bits) find the
 // key of the last one kept and how many of its equals are kept.  One more pass
 // numbers the kept tokens in order of position.
+//
+// A row is worked by a cluster of 1 to 8 CTAs, each with a run of the row's
+// tokens, whose keys it reads once and holds in shared memory (rows too long
+// for that are read again in each pass).  The CTAs add up one another's counts
+// through distributed shared memory and come to the same key; integer counts,
+// so the choice does not depend on any order.
+//
+// The copy is bound by its bytes, 1 KB per kept token read and written.
+#include <algorithm>
+
 #include "kv16.cuh"
 
 namespace oscar {
@@ -21,117 +31,186 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int kKeysMost = 48 * 1024;     // keys that a CTA holds
+constexpr int kLoads = 16;               // weights that a thread has in flight
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// The int at the same place in the shared memory of another CTA of the cluster.
+__device__ __forceinline__ int peer_int(const int* p, int rank) {
+  unsigned far;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(far) : "memory");
+  return v;
+}
+
+// *p += v in shared memory.  With v not known to be 1 the compiler leaves the
+// adding to the memory; of a constant 1 it makes a loop over the warp's distinct
+// addresses, which for keys this spread took most of the kernel's time.
+__device__ __forceinline__ void count_up(int* p, int v) {
+  asm volatile("red.relaxed.cta.shared::cta.add.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v)
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kSelThreads)
-kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, int32_t* counts,
-                   int32_t* kept) {
+kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, int cluster,
+                   int held, int32_t* counts, int32_t* kept) {
+  extern __shared__ uint32_t keys[];     // [held]
   __shared__ int hist[kBins];
   __shared__ int s_scan[2][kSelWarps];
+  __shared__ int s_total[2];
   __shared__ int s_bin, s_need;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x, b = row / c.Hkv, h = row - b * c.Hkv;
+  const int rank = blockIdx.x % cluster, row = blockIdx.x / cluster;
+  const int b = row / c.Hkv, h = row - b * c.Hkv;
   const int keep = first + recent + top;
   int32_t* out = kept + (long long)row * keep;
   const int n = kv16_length(c, b, max_tok);
   if (n < 0 && tid == 0) record_error(c.status, kDevErrBadPaged);
-  if (n <= keep) {
-    for (int i = tid; i < keep; i += kSelThreads) out[i] = i < n ? i : -1;
-    if (tid == 0) counts[row] = n;
+  if (rank == 0 && tid == 0) counts[row] = min(n, keep);
+  if (n <= keep) {     // the whole cluster leaves
+    for (int i = rank * kSelThreads + tid; i < keep; i += cluster * kSelThreads)
+      out[i] = i < n ? i : -1;
     return;
   }
-  auto key_at = [&](int j) -> uint32_t {
-    const int r = kv16_block_row(c, b, h, j / kPage);
+  for (int i = rank * kSelThreads + tid; i < first; i += cluster * kSelThreads) out[i] = i;
+  for (int i = rank * kSelThreads + tid; i < recent; i += cluster * kSelThreads)
+    out[first + top + i] = n - recent + i;
+  if (top == 0) return;
+
+  // this CTA's tokens [lo, lo + len) of those to choose from
+  const int mid = n - recent - first;
+  const int lo = first + (int)((long long)mid * rank / cluster);
+  const int len = first + (int)((long long)mid * (rank + 1) / cluster) - lo;
+  auto read_key = [&](int i) -> uint32_t {
+    const int j = lo + i, r = kv16_block_row(c, b, h, j / kPage);
     if (r < 0) {
       record_error(c.status, kDevErrBadPaged);
       return 0u;
     }
-    return order_key(c.weight[(long long)r + j % kPage]);
+    return order_key(__ldg(c.weight + (long long)r + j % kPage));
   };
-  const int lo = first, hi = n - recent;    // the tokens to choose from
+  const bool in_smem = len <= held;
+  if (in_smem)
+    for (int i0 = tid; i0 < len; i0 += kLoads * kSelThreads) {
+      uint32_t k[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (i0 + u * kSelThreads < len) k[u] = read_key(i0 + u * kSelThreads);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (i0 + u * kSelThreads < len) keys[i0 + u * kSelThreads] = k[u];
+    }
+  auto key_at = [&](int i) { return in_smem ? keys[i] : read_key(i); };
+
   // the key of the last kept token, found from its top bits down
   uint32_t prefix = 0, mask = 0;
-  int need = top;
-  if (top > 0) {
-    for (int round = 0; round < 3; ++round) {
-      const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
-      const int bins = round == 2 ? 1024 : 2048;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
-        const uint32_t k = key_at(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
-      }
-      __syncthreads();
-      // the bin in which the count from above reaches `need`: a thread takes
-      // two bins, highest first
-      const int b0 = kBins - 1 - 2 * tid;
-      const int c0 = hist[b0], c1 = hist[b0 - 1];
-      int x = c0 + c1;
+  int need = top, one;
+  asm volatile("mov.u32 %0, 1;" : "=r"(one));
+  for (int round = 0; round < 3; ++round) {
+    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+    const int bins = round == 2 ? 1024 : 2048;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < len; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      if ((k & mask) == prefix) count_up(&hist[(k >> shift) & (bins - 1)], one);
+    }
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+    // the bin in which the count from above reaches `need`: a thread takes
+    // two bins, highest first
+    const int b0 = kBins - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    for (int r = 0; r < cluster; ++r) {
+      c0 += cluster > 1 ? peer_int(hist + b0, r) : hist[b0];
+      c1 += cluster > 1 ? peer_int(hist + b0 - 1, r) : hist[b0 - 1];
+    }
+    int x = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) s_scan[0][warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int y = s_scan[0][lane];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        const int z = __shfl_up_sync(0xffffffffu, y, d);
+        if (lane >= d) y += z;
       }
-      if (lane == 31) s_scan[0][warp] = x;
-      __syncthreads();
-      if (warp == 0) {
-        int y = s_scan[0][lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int z = __shfl_up_sync(0xffffffffu, y, d);
-          if (lane >= d) y += z;
-        }
-        s_scan[0][lane] = y;
-      }
-      __syncthreads();
-      const int above = x - c0 - c1 + (warp ? s_scan[0][warp - 1] : 0);
-      if (above < need && above + c0 + c1 >= need) {
-        const bool second = above + c0 < need;
-        s_bin = second ? b0 - 1 : b0;
-        s_need = need - above - (second ? c0 : 0);
-      }
-      __syncthreads();
-      prefix |= (uint32_t)s_bin << shift;
-      mask |= (uint32_t)(bins - 1) << shift;
-      need = s_need;
-      __syncthreads();
+      s_scan[0][lane] = y;
     }
+    __syncthreads();
+    const int above = x - c0 - c1 + (warp ? s_scan[0][warp - 1] : 0);
+    if (above < need && above + c0 + c1 >= need) {
+      const bool second = above + c0 < need;
+      s_bin = second ? b0 - 1 : b0;
+      s_need = need - above - (second ? c0 : 0);
+    }
+    __syncthreads();
+    prefix |= (uint32_t)s_bin << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    need = s_need;
+    // the others have read this CTA's counts
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
   }
   // number the kept tokens: each warp a run of 32-token pieces
-  const int pieces = top > 0 ? (hi - lo + 31) / 32 : 0;
+  const int pieces = (len + 31) / 32;
   const int per = (pieces + kSelWarps - 1) / kSelWarps;
   const int p0 = min(pieces, warp * per), p1 = min(pieces, p0 + per);
   int gt = 0, eq = 0;
+#pragma unroll 4
   for (int p = p0; p < p1; ++p) {
-    const int j = lo + p * 32 + lane;
-    const uint32_t k = j < hi ? key_at(j) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, j < hi && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, j < hi && k == prefix));
+    const int i = p * 32 + lane;
+    const uint32_t k = i < len ? key_at(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < len && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i < len && k == prefix));
   }
   if (lane == 0) {
     s_scan[0][warp] = gt;
     s_scan[1][warp] = eq;
   }
   __syncthreads();
+  if (tid < 2) {
+    int t = 0;
+    for (int w = 0; w < kSelWarps; ++w) t += s_scan[tid][w];
+    s_total[tid] = t;
+  }
   gt = eq = 0;
   for (int w = 0; w < warp; ++w) {
     gt += s_scan[0][w];
     eq += s_scan[1][w];
   }
+  if (cluster > 1) {
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      gt += peer_int(&s_total[0], r);
+      eq += peer_int(&s_total[1], r);
+    }
+  }
   const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
   for (int p = p0; p < p1; ++p) {
-    const int j = lo + p * 32 + lane;
-    const uint32_t k = j < hi ? key_at(j) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, j < hi && k > prefix);
-    const uint32_t me = __ballot_sync(0xffffffffu, j < hi && k == prefix);
+    const int i = p * 32 + lane;
+    const uint32_t k = i < len ? key_at(i) : 0u;
+    const uint32_t mg = __ballot_sync(0xffffffffu, i < len && k > prefix);
+    const uint32_t me = __ballot_sync(0xffffffffu, i < len && k == prefix);
     const int g_here = gt + __popc(mg & below), e_here = eq + __popc(me & below);
     if (((mg >> lane) & 1) || (((me >> lane) & 1) && e_here < need))
-      out[first + g_here + min(e_here, need)] = j;
+      out[first + g_here + min(e_here, need)] = lo + i;
     gt += __popc(mg);
     eq += __popc(me);
   }
-  for (int i = tid; i < first; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < recent; i += kSelThreads) out[first + top + i] = n - recent + i;
-  if (tid == 0) counts[row] = keep;
+  if (cluster > 1) cluster_sync();     // the others have read this CTA's totals
 }
 
 constexpr int kCopyThreads = 128;
@@ -188,9 +267,31 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   const int rows = src.B * src.Hkv, keep = keep_first + keep_recent + keep_top;
   int32_t* counts = static_cast<int32_t*>(ws);
   if (!kept) kept = counts + (((size_t)rows + 3) / 4) * 4;
-  kv16_select_kernel<<<rows, kSelThreads, 0, s>>>(src, max_tok, keep_first, keep_recent, keep_top,
-                                                  counts, kept);
-  cudaError_t e = cudaGetLastError();
+  // CTAs per row: as many as it takes to hold the row's keys.  More of them for
+  // fewer keys each is slower: the rounds' cluster barriers and remote reads
+  // cost more than the counting that they save.
+  const int most = std::min(max_tok, src.cap);
+  int cluster = 1;
+  while (cluster < 8 && most / cluster >= kKeysMost) cluster *= 2;
+  const int held = std::min(kKeysMost, most / cluster + 1);
+  const size_t smem = (size_t)held * sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(kv16_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem);
+  if (e != cudaSuccess) return e;
+  if ((long long)rows * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(rows * cluster);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv16_select_kernel, src, max_tok, keep_first, keep_recent,
+                         keep_top, cluster, held, counts, kept);
   if (e != cudaSuccess) return e;
   const long long warps = (long long)rows * ((keep + kCopyTokens - 1) / kCopyTokens);
   const int grid = (int)((warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32));
