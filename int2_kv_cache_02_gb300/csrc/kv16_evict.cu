@@ -56,10 +56,12 @@ __device__ __forceinline__ void count_up(int* p, int v) {
                : "memory");
 }
 
+// HELD: a CTA's keys fit in its dynamic shared memory.
+template <bool HELD>
 __global__ void __launch_bounds__(kSelThreads)
 kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, int cluster,
-                   int held, int32_t* counts, int32_t* kept) {
-  extern __shared__ uint32_t keys[];     // [held]
+                   int32_t* counts, int32_t* kept) {
+  extern __shared__ uint32_t keys[];
   __shared__ int hist[kBins];
   __shared__ int s_scan[2][kSelWarps];
   __shared__ int s_total[2];
@@ -86,26 +88,24 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
   const int mid = n - recent - first;
   const int lo = first + (int)((long long)mid * rank / cluster);
   const int len = first + (int)((long long)mid * (rank + 1) / cluster) - lo;
+  // no branch around the loads, so that a thread's are in flight together
+  bool bad = false;
   auto read_key = [&](int i) -> uint32_t {
     const int j = lo + i, r = kv16_block_row(c, b, h, j / kPage);
-    if (r < 0) {
-      record_error(c.status, kDevErrBadPaged);
-      return 0u;
-    }
-    return order_key(__ldg(c.weight + (long long)r + j % kPage));
+    bad |= r < 0;
+    const float w = __ldg(c.weight + (long long)max(r, 0) + j % kPage);
+    return r < 0 ? 0u : order_key(w);
   };
-  const bool in_smem = len <= held;
-  if (in_smem)
+  if (HELD)
     for (int i0 = tid; i0 < len; i0 += kLoads * kSelThreads) {
       uint32_t k[kLoads];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (i0 + u * kSelThreads < len) k[u] = read_key(i0 + u * kSelThreads);
+      for (int u = 0; u < kLoads; ++u) k[u] = read_key(min(i0 + u * kSelThreads, len - 1));
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
         if (i0 + u * kSelThreads < len) keys[i0 + u * kSelThreads] = k[u];
     }
-  auto key_at = [&](int i) { return in_smem ? keys[i] : read_key(i); };
+  auto key_at = [&](int i) { return HELD ? keys[i] : read_key(i); };
 
   // the key of the last kept token, found from its top bits down
   uint32_t prefix = 0, mask = 0;
@@ -116,10 +116,14 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     const int bins = round == 2 ? 1024 : 2048;
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < len; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if ((k & mask) == prefix) count_up(&hist[(k >> shift) & (bins - 1)], one);
+    for (int i0 = tid; i0 < len; i0 += 8 * kSelThreads) {
+      uint32_t k[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k[u] = key_at(min(i0 + u * kSelThreads, len - 1));
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kSelThreads < len && (k[u] & mask) == prefix)
+          count_up(&hist[(k[u] >> shift) & (bins - 1)], one);
     }
     if (cluster > 1) cluster_sync();
     else __syncthreads();
@@ -168,13 +172,19 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
   const int per = (pieces + kSelWarps - 1) / kSelWarps;
   const int p0 = min(pieces, warp * per), p1 = min(pieces, p0 + per);
   int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int p = p0; p < p1; ++p) {
-    const int i = p * 32 + lane;
-    const uint32_t k = i < len ? key_at(i) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < len && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < len && k == prefix));
+  for (int q = p0; q < p1; q += 8) {
+    uint32_t k[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) k[u] = key_at(min((q + u) * 32 + lane, len - 1));
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool mine = q + u < p1 && (q + u) * 32 + lane < len;
+      gt += mine && k[u] > prefix;
+      eq += mine && k[u] == prefix;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     s_scan[0][warp] = gt;
     s_scan[1][warp] = eq;
@@ -198,18 +208,24 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     }
   }
   const uint32_t below = (1u << lane) - 1;
-#pragma unroll 4
-  for (int p = p0; p < p1; ++p) {
-    const int i = p * 32 + lane;
-    const uint32_t k = i < len ? key_at(i) : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, i < len && k > prefix);
-    const uint32_t me = __ballot_sync(0xffffffffu, i < len && k == prefix);
-    const int g_here = gt + __popc(mg & below), e_here = eq + __popc(me & below);
-    if (((mg >> lane) & 1) || (((me >> lane) & 1) && e_here < need))
-      out[first + g_here + min(e_here, need)] = lo + i;
-    gt += __popc(mg);
-    eq += __popc(me);
+  for (int q = p0; q < p1; q += 8) {
+    uint32_t k[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) k[u] = key_at(min((q + u) * 32 + lane, len - 1));
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = (q + u) * 32 + lane;
+      const bool mine = q + u < p1 && i < len;
+      const uint32_t mg = __ballot_sync(0xffffffffu, mine && k[u] > prefix);
+      const uint32_t me = __ballot_sync(0xffffffffu, mine && k[u] == prefix);
+      const int g_here = gt + __popc(mg & below), e_here = eq + __popc(me & below);
+      if (((mg >> lane) & 1) || (((me >> lane) & 1) && e_here < need))
+        out[first + g_here + min(e_here, need)] = lo + i;
+      gt += __popc(mg);
+      eq += __popc(me);
+    }
   }
+  if (bad) record_error(c.status, kDevErrBadPaged);
   if (cluster > 1) cluster_sync();     // the others have read this CTA's totals
 }
 
@@ -273,10 +289,11 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   const int most = std::min(max_tok, src.cap);
   int cluster = 1;
   while (cluster < 8 && most / cluster >= kKeysMost) cluster *= 2;
-  const int held = std::min(kKeysMost, most / cluster + 1);
-  const size_t smem = (size_t)held * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(kv16_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
+  const int held = most / cluster + 1;
+  const auto select = held <= kKeysMost ? kv16_select_kernel<true> : kv16_select_kernel<false>;
+  const size_t smem = held <= kKeysMost ? (size_t)held * sizeof(uint32_t) : 0;
+  cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
   if (e != cudaSuccess) return e;
   if ((long long)rows * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -290,8 +307,8 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv16_select_kernel, src, max_tok, keep_first, keep_recent,
-                         keep_top, cluster, held, counts, kept);
+  e = cudaLaunchKernelEx(&cfg, select, src, max_tok, keep_first, keep_recent, keep_top, cluster,
+                         counts, kept);
   if (e != cudaSuccess) return e;
   const long long warps = (long long)rows * ((keep + kCopyTokens - 1) / kCopyTokens);
   const int grid = (int)((warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32));
