@@ -32,7 +32,7 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 constexpr int kKeysMost = 48 * 1024;     // keys that a CTA holds
-constexpr int kLoads = 16;               // weights that a thread has in flight
+constexpr int kLoads = 8;                // pages that a warp has in flight
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile(
@@ -84,28 +84,52 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     out[first + top + i] = n - recent + i;
   if (top == 0) return;
 
-  // this CTA's tokens [lo, lo + len) of those to choose from
-  const int mid = n - recent - first;
-  const int lo = first + (int)((long long)mid * rank / cluster);
-  const int len = first + (int)((long long)mid * (rank + 1) / cluster) - lo;
-  // no branch around the loads, so that a thread's are in flight together
+  // of the tokens to choose from, [first, n - recent), this CTA's are those of
+  // the pages [page0, page0 + pages): place i is token 32 page0 + i, and the
+  // places [from, from + len) count
+  const int end = n - recent, all0 = first / kPage, all = (end + kPage - 1) / kPage - all0;
+  const int page0 = all0 + (int)((long long)all * rank / cluster);
+  const int pages = all0 + (int)((long long)all * (rank + 1) / cluster) - page0;
+  const int from = max(first - page0 * kPage, 0);
+  const int len = max(min(end - page0 * kPage, pages * kPage) - from, 0);
   bool bad = false;
-  auto read_key = [&](int i) -> uint32_t {
-    const int j = lo + i, r = kv16_block_row(c, b, h, j / kPage);
-    bad |= r < 0;
-    const float w = __ldg(c.weight + (long long)max(r, 0) + j % kPage);
-    return r < 0 ? 0u : order_key(w);
-  };
-  if (HELD)
-    for (int i0 = tid; i0 < len; i0 += kLoads * kSelThreads) {
-      uint32_t k[kLoads];
+  // kLoads pages of a warp at once: a lane each finds its page, then all lanes
+  // read every page's 32 weights
+  auto read_pages = [&](int q, uint32_t (&k)[kLoads]) {
+    int row = 0;
+    if (lane < kLoads && q + lane < pages) {
+      row = kv16_block_row(c, b, h, page0 + q + lane);
+      bad |= row < 0;
+    }
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) k[u] = read_key(min(i0 + u * kSelThreads, len - 1));
+    for (int u = 0; u < kLoads; ++u) {
+      const int r = __shfl_sync(0xffffffffu, row, u);
+      // (a contiguous row may end inside its last page)
+      const bool counts = (unsigned)((q + u) * kPage + lane - from) < (unsigned)len;
+      const float w = __ldg(c.weight + (counts ? (long long)max(r, 0) + lane : 0));
+      k[u] = r < 0 ? 0u : order_key(w);
+    }
+  };
+  auto pages_at = [&](int q, uint32_t (&k)[kLoads]) {
+    if (HELD) {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) k[u] = keys[min(q + u, pages - 1) * kPage + lane];
+    } else {
+      read_pages(q, k);
+    }
+  };
+  // each warp a run of the pages
+  const int per = (pages + kSelWarps - 1) / kSelWarps;
+  const int p0 = min(pages, warp * per), p1 = min(pages, p0 + per);
+  auto mine = [&](int q) { return q < p1 && (unsigned)(q * kPage + lane - from) < (unsigned)len; };
+  if (HELD)
+    for (int q = p0; q < p1; q += kLoads) {
+      uint32_t k[kLoads];
+      read_pages(q, k);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        if (i0 + u * kSelThreads < len) keys[i0 + u * kSelThreads] = k[u];
+        if (q + u < p1) keys[(q + u) * kPage + lane] = k[u];
     }
-  auto key_at = [&](int i) { return HELD ? keys[i] : read_key(i); };
 
   // the key of the last kept token, found from its top bits down
   uint32_t prefix = 0, mask = 0;
@@ -116,13 +140,12 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     const int bins = round == 2 ? 1024 : 2048;
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int i0 = tid; i0 < len; i0 += 8 * kSelThreads) {
-      uint32_t k[8];
+    for (int q = p0; q < p1; q += kLoads) {
+      uint32_t k[kLoads];
+      pages_at(q, k);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) k[u] = key_at(min(i0 + u * kSelThreads, len - 1));
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (i0 + u * kSelThreads < len && (k[u] & mask) == prefix)
+      for (int u = 0; u < kLoads; ++u)
+        if (mine(q + u) && (k[u] & mask) == prefix)
           count_up(&hist[(k[u] >> shift) & (bins - 1)], one);
     }
     if (cluster > 1) cluster_sync();
@@ -167,20 +190,15 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     if (cluster > 1) cluster_sync();
     else __syncthreads();
   }
-  // number the kept tokens: each warp a run of 32-token pieces
-  const int pieces = (len + 31) / 32;
-  const int per = (pieces + kSelWarps - 1) / kSelWarps;
-  const int p0 = min(pieces, warp * per), p1 = min(pieces, p0 + per);
+  // number the kept tokens
   int gt = 0, eq = 0;
-  for (int q = p0; q < p1; q += 8) {
-    uint32_t k[8];
+  for (int q = p0; q < p1; q += kLoads) {
+    uint32_t k[kLoads];
+    pages_at(q, k);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) k[u] = key_at(min((q + u) * 32 + lane, len - 1));
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const bool mine = q + u < p1 && (q + u) * 32 + lane < len;
-      gt += mine && k[u] > prefix;
-      eq += mine && k[u] == prefix;
+    for (int u = 0; u < kLoads; ++u) {
+      gt += mine(q + u) && k[u] > prefix;
+      eq += mine(q + u) && k[u] == prefix;
     }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
@@ -208,19 +226,16 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
     }
   }
   const uint32_t below = (1u << lane) - 1;
-  for (int q = p0; q < p1; q += 8) {
-    uint32_t k[8];
+  for (int q = p0; q < p1; q += kLoads) {
+    uint32_t k[kLoads];
+    pages_at(q, k);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) k[u] = key_at(min((q + u) * 32 + lane, len - 1));
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = (q + u) * 32 + lane;
-      const bool mine = q + u < p1 && i < len;
-      const uint32_t mg = __ballot_sync(0xffffffffu, mine && k[u] > prefix);
-      const uint32_t me = __ballot_sync(0xffffffffu, mine && k[u] == prefix);
+    for (int u = 0; u < kLoads; ++u) {
+      const uint32_t mg = __ballot_sync(0xffffffffu, mine(q + u) && k[u] > prefix);
+      const uint32_t me = __ballot_sync(0xffffffffu, mine(q + u) && k[u] == prefix);
       const int g_here = gt + __popc(mg & below), e_here = eq + __popc(me & below);
       if (((mg >> lane) & 1) || (((me >> lane) & 1) && e_here < need))
-        out[first + g_here + min(e_here, need)] = lo + i;
+        out[first + g_here + min(e_here, need)] = (page0 + q + u) * kPage + lane;
       gt += __popc(mg);
       eq += __popc(me);
     }
@@ -288,8 +303,8 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   // cost more than the counting that they save.
   const int most = std::min(max_tok, src.cap);
   int cluster = 1;
-  while (cluster < 8 && most / cluster >= kKeysMost) cluster *= 2;
-  const int held = most / cluster + 1;
+  while (cluster < 8 && most / cluster > kKeysMost - 2 * kPage) cluster *= 2;
+  const int held = (most / kPage / cluster + 2) * kPage;
   const auto select = held <= kKeysMost ? kv16_select_kernel<true> : kv16_select_kernel<false>;
   const size_t smem = held <= kKeysMost ? (size_t)held * sizeof(uint32_t) : 0;
   cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
