@@ -101,14 +101,22 @@ kv16_select_kernel(const Kv16 c, int max_tok, int first, int recent, int top, in
       row = kv16_block_row(c, b, h, page0 + q + lane);
       bad |= row < 0;
     }
+    const float* at[kLoads];
+    float w[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int r = __shfl_sync(0xffffffffu, row, u);
       // (a contiguous row may end inside its last page)
+      const int r = max(__shfl_sync(0xffffffffu, row, u), 0);
       const bool counts = (unsigned)((q + u) * kPage + lane - from) < (unsigned)len;
-      const float w = __ldg(c.weight + (counts ? (long long)max(r, 0) + lane : 0));
-      k[u] = r < 0 ? 0u : order_key(w);
+      at[u] = c.weight + (counts ? (long long)r + lane : 0);
     }
+    // in this order: left to itself the compiler waits for each before the next
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(w[u]) : "l"(at[u]));
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      k[u] = __shfl_sync(0xffffffffu, row, u) < 0 ? 0u : order_key(w[u]);
   };
   auto pages_at = [&](int q, uint32_t (&k)[kLoads]) {
     if (HELD) {
