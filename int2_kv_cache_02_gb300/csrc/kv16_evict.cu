@@ -306,16 +306,24 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   const int rows = src.B * src.Hkv, keep = keep_first + keep_recent + keep_top;
   int32_t* counts = static_cast<int32_t*>(ws);
   if (!kept) kept = counts + (((size_t)rows + 3) / 4) * 4;
-  // CTAs per row: as many as it takes to hold the row's keys.  More of them for
-  // fewer keys each is slower: the rounds' cluster barriers and remote reads
-  // cost more than the counting that they save.
+  // CTAs per row: as many as it takes to hold the row's keys, and more while
+  // that leaves no SM with two and each 8192 tokens (64 rows of 32K tokens: 27.8
+  // us with one CTA a row, 21.6 with two).  Smaller shares are slower: a cluster's
+  // barriers and remote reads then cost more than the counting that they save
+  // (eight CTAs a row, on top of one another: 146 us).
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   const int most = std::min(max_tok, src.cap);
   int cluster = 1;
-  while (cluster < 8 && most / cluster > kKeysMost - 2 * kPage) cluster *= 2;
+  while (cluster < 8 && (most / cluster > kKeysMost - 2 * kPage ||
+                         (2LL * rows * cluster <= sms && most / cluster >= 8192)))
+    cluster *= 2;
   const int held = (most / kPage / cluster + 2) * kPage;
   const auto select = held <= kKeysMost ? kv16_select_kernel<true> : kv16_select_kernel<false>;
   const size_t smem = held <= kKeysMost ? (size_t)held * sizeof(uint32_t) : 0;
-  cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   if ((long long)rows * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
