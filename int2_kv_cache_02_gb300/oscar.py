@@ -346,6 +346,7 @@ class KV16Cache:
             raise ValueError("weight: the shape of k without its last dimension")
         self.B = int(k.shape[0] if block_table is None else block_table.shape[0])
         self.Hkv, self.dtype, self.device = int(k.shape[1]), k.dtype, k.device
+        self._index = k.get_device()
         s = OscarKV16CacheStruct()
         s.B, s.Hkv, s.dtype = self.B, self.Hkv, _KV16_DTYPES[k.dtype]
         if block_table is None:
@@ -359,32 +360,37 @@ class KV16Cache:
         self.struct = s
         self._ref = ctypes.byref(s)
 
+    # A decode step is a handful of microseconds on the GPU, so the checks below
+    # use the cheapest accessors (an int device index, identity of dtypes).
+
     def _mine(self, t: torch.Tensor | None, dtype: torch.dtype, n: int | None):
         """Pointer of a dense tensor that goes with the cache."""
         if t is None:
             return None
-        if t.dtype != dtype or (n is not None and t.numel() != n):
+        if t.dtype is not dtype or (n is not None and t.numel() != n):
             raise ValueError(f"expected {n if n is not None else ''} {dtype} elements, "
                              f"got {tuple(t.shape)} {t.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"tensor on {t.device}, cache on {self.device}")
-        return _ptr(t)
+        if t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"expected a dense tensor on {self.device}, got one on {t.device}")
+        return t.data_ptr()
 
-    def _rows(self, t: torch.Tensor, heads: int, total: int | None = None):
-        """(pointer, row stride, rows) of a [rows][heads][128] tensor of the cache's
-        type, dense within a row."""
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != self.dtype:
-            raise ValueError(f"expected [rows][{heads}][{D}] of {self.dtype}, "
-                             f"got {tuple(t.shape)} {t.dtype}")
-        rows = t.shape[0]
-        if total is not None and rows != total:
-            raise ValueError(f"expected {total} rows, got {rows}")
-        if not t.is_cuda or t.device != self.device:
+    def _rows(self, t: torch.Tensor, heads: int | None, total: int | None = None):
+        """(pointer, row stride, rows, heads) of a [rows][heads][128] tensor of the
+        cache's type, dense within a row."""
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != D or t.dtype is not self.dtype or \
+                (heads is not None and shape[1] != heads) or \
+                (total is not None and shape[0] != total):
+            raise ValueError(f"expected [{total if total is not None else 'rows'}]"
+                             f"[{heads if heads is not None else 'heads'}][{D}] of {self.dtype}, "
+                             f"got {tuple(shape)} {t.dtype}")
+        if t.get_device() != self._index:
             raise ValueError(f"tensor on {t.device}, cache on {self.device}")
-        stride = t.stride()
-        if stride[2] != 1 or (heads > 1 and stride[1] != D):
+        rows, heads, _ = shape
+        row, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != D):
             raise ValueError("a row's heads have to lie densely one behind another")
-        return t.data_ptr(), (stride[0] if rows > 1 else heads * D), rows
+        return t.data_ptr(), (row if rows > 1 else heads * D), rows, heads
 
     def ref(self):
         return self._ref
@@ -547,19 +553,23 @@ def bf16_decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, B: 
 def _kv16_call(cache: KV16Cache, where: str, fn, args, stream):
     """Calls the library with the cache's device current, on `stream` or that
     device's current stream."""
-    if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
-        with torch.cuda.device(cache.device):
-            st = fn(*args, _stream(stream))
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(cache._index)
     else:
-        st = fn(*args, _stream(stream))
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == cache._index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(cache.device):
+            st = fn(*args, raw)
     if st != 0:
         raise OscarError(st, where)
 
 
 def _bytes(workspace: torch.Tensor, cache: KV16Cache):
-    if workspace.device != cache.device:
-        raise ValueError(f"workspace on {workspace.device}, cache on {cache.device}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != cache._index or not workspace.is_contiguous():
+        raise ValueError(f"expected a dense workspace on {cache.device}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def kv16_write(cache: KV16Cache, k_new: torch.Tensor, v_new: torch.Tensor, start: torch.Tensor,
@@ -567,8 +577,8 @@ def kv16_write(cache: KV16Cache, k_new: torch.Tensor, v_new: torch.Tensor, start
     """New tokens into the cache: rows start[b] .. start[b+1] of k_new, v_new
     [total][Hkv][128] (a row may be a slice of a wider one) go to sequence b's
     positions pos0[b] .., and n_tok[b] = pos0[b] + their number."""
-    k, ks, total = cache._rows(k_new, cache.Hkv)
-    v, vs, _ = cache._rows(v_new, cache.Hkv, total)
+    k, ks, total, _ = cache._rows(k_new, cache.Hkv)
+    v, vs, _, _ = cache._rows(v_new, cache.Hkv, total)
     _kv16_call(cache, "oscar_kv16_write", _lib.oscar_kv16_write,
                (cache._ref, k, ks, v, vs, cache._mine(start, torch.int32, cache.B + 1),
                 cache._mine(pos0, torch.int32, cache.B), total), stream)
@@ -589,8 +599,7 @@ def kv16_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor, softm
     sees the last `window` tokens up to its own and the first n_sink.  out
     [total][Hq][128]; lse float32 [total][Hq]: the logarithm of the sum of the
     exponentials.  max_tok bounds the n_tok[b]."""
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    qp, qs, total = cache._rows(q, Hq)
+    qp, qs, total, Hq = cache._rows(q, None)
     w, wb = _bytes(workspace, cache)
     _kv16_call(cache, "oscar_kv16_attention", _lib.oscar_kv16_attention,
                (cache._ref, qp, qs, cache._mine(start, torch.int32, cache.B + 1), total, Hq,
@@ -611,8 +620,7 @@ def kv16_decode_attention(cache: KV16Cache, q: torch.Tensor, softmax_scale: floa
     """Attention of each sequence's newest token, q and out [B][Hq][128];
     accumulate adds its probabilities to the weights of the tokens it sees.
     The workspace comes zeroed from alloc_workspace."""
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    qp, qs, _ = cache._rows(q, Hq, cache.B)
+    qp, qs, _, Hq = cache._rows(q, None, cache.B)
     w, wb = _bytes(workspace, cache)
     _kv16_call(cache, "oscar_kv16_decode_attention", _lib.oscar_kv16_decode_attention,
                (cache._ref, qp, qs, Hq, softmax_scale, max_tok, window, n_sink, int(accumulate),
@@ -625,8 +633,7 @@ def kv16_accumulate(cache: KV16Cache, q: torch.Tensor, lse: torch.Tensor, start:
     """Adds to each cached token's weight the probabilities it got from the
     last n_obs queries (0: all) of its sequence; q, start and the window as for
     kv16_attention, lse as it wrote it."""
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    qp, qs, total = cache._rows(q, Hq)
+    qp, qs, total, Hq = cache._rows(q, None)
     _kv16_call(cache, "oscar_kv16_accumulate", _lib.oscar_kv16_accumulate,
                (cache._ref, qp, qs, cache._mine(lse, torch.float32, total * Hq),
                 cache._mine(start, torch.int32, cache.B + 1), total, Hq, softmax_scale, max_tok,
