@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTileBytes = 32768, kHalf = 16384;
 constexpr int kQStages = 3, kKBufs = 2, kLseSlots = 2;
-constexpr int kItemKeys = 256;     // or 128
+constexpr int kItemKeys = 256;     // at most
 
 struct AccParams {
   Kv16 c;
@@ -368,18 +368,16 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
           }
         };
         auto tile = [&](auto all) {
-          uint32_t s0[64], s1[64];
-          tc5_ld32(s0, sa);
-          tc5_ld32(s0 + 32, sa + 32);
-          tc5_wait_ld();
-          tc5_ld32(s1, sa + 64);
-          tc5_ld32(s1 + 32, sa + 96);
-          add(all, s0, 0);
+          // all columns at once: loads left in flight under the sums slow them down
+          uint32_t x[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc5_ld32(x + 32 * i, sa + 32 * i);
           tc5_wait_ld();
           tc5_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.s_empty[w][buf]);
-          add(all, s1, 64);
+          add(all, x, 0);
+          add(all, x + 64, 64);
         };
         if (whole) tile(std::true_type());
         else tile(std::false_type());
