@@ -268,7 +268,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       // the last commits' arrivals land before the CTA ends
       if (!ok) record_error(p.c.status, kDevErrWaitTimeout);
       tc5_commit(&sm.drain);
-      if (!mbar_wait_bounded(&sm.drain, 0, kWaitLimit))
+      if (!mbar_wait_bounded(&sm.drain, 0, kTcWaitLimit))
         record_error(p.c.status, kDevErrDrainTimeout);
     }
     __syncwarp();

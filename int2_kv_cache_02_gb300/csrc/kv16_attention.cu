@@ -409,7 +409,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         // the last commits' arrivals land before the CTA ends
         tc5_commit(&sm.drain[w]);
-        if (!mbar_wait_bounded(&sm.drain[w], 0, kWaitLimit))
+        if (!mbar_wait_bounded(&sm.drain[w], 0, kTcWaitLimit))
           record_error(p.c.status, kDevErrDrainTimeout);
       }
       __syncwarp();

@@ -123,25 +123,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-constexpr unsigned long long kGiveUpNs = 2000000000ull;
+// Polls of a wait before it gives up: an unsuccessful try_wait takes about a
+// microsecond, so two to three seconds.  (No clock is read: the waits are
+// inlined many times over, and the kernels' time goes by their code's size.)
+constexpr unsigned kTcWaitLimit = 1u << 21;
 
-// Waits for phase `parity` of `bar`, two seconds at most.  Gives up soon after
-// another warp has (*abort set), and sets *abort itself.
+// Waits for phase `parity` of `bar`.  Gives up after the limit, or soon after
+// another warp has (*abort set), and then sets *abort itself.
 __device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
   if (mbar_test_wait(bar, parity)) return true;
-  unsigned long long since = 0;
-  for (unsigned i = 0; i < kWaitLimit; ++i) {
+  for (unsigned i = 0; i < kTcWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 63u) {
-      const unsigned long long t = now_ns();
-      if (since == 0) since = t;
-      if (*abort || t - since > kGiveUpNs) break;
-    }
+    if ((i & 255u) == 255u && *abort) return false;
   }
   *abort = 1;
   return false;
