@@ -79,12 +79,12 @@ struct Item {
   Span sp;
   int k0, k1;          // key tiles
   int cnt[2];          // of them, for each query tile: k0 .. k0 + cnt - 1
-  int clear_at;        // the one whose last page lacks tokens (counted from k0), or -1
+  bool clear;          // the last one's last page is the sequence's and lacks tokens
 };
 
 struct Smem {
   uint64_t q_full[2], q_empty[2], full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], clean, drain[2];
+  uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], tail, drain[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int abort;
@@ -135,10 +135,8 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
     const int blocks = Span(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink).blocks;
     it.cnt[0] = min(it.k1, max(it.k0, (blocks + kKeyPages - 1) / kKeyPages)) - it.k0;
   }
-  it.clear_at = it.k1 > it.k0 && it.k1 == kt && it.n % kPage != 0 &&
-                        it.sp.block(it.sp.blocks - 1) == (it.n - 1) / kPage
-                    ? kt - 1 - it.k0
-                    : -1;
+  it.clear = it.k1 > it.k0 && it.k1 == kt && it.n % kPage != 0 &&
+             it.sp.block(it.sp.blocks - 1) == (it.n - 1) / kPage;
   return true;
 }
 
@@ -185,7 +183,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&sm.i_full[i], 1);
       mbar_init(&sm.i_empty[i], kItemReaders);
     }
-    mbar_init(&sm.clean, 1);
+    mbar_init(&sm.tail, 1);
     mbar_fence_init();
     sm.abort = 0;
   }
@@ -231,7 +229,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const int none = p.c.table ? p.c.n_pages * p.c.Hkv * kPage
                                  : p.c.B * p.c.Hkv * p.c.T_cap;      // reads zeros
       const unsigned qbytes = 2 * 64 * 2 * p.g * p.tokens;
-      unsigned used = 0, q_used[2] = {0, 0};
+      unsigned used = 0, q_used[2] = {0, 0}, tails = 0;
       for (unsigned ni = 0; ok; ++ni) {
         const Item* ip = take(ni);
         if (!(ok = ip != nullptr) || ip->stop) break;
@@ -268,35 +266,38 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort);
             if (!ok) break;
             uint8_t* dst = ring + st * kTileBytes;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+            // The rows behind the sequence's last token hold anything.  The value
+            // tile that has them lands on a barrier of this warp's, which clears
+            // them and only then passes the tile on.
+            const bool clear = kv == 1 && it.clear && k + 1 == it.k1;
+            uint64_t* bar = clear ? &sm.tail : &sm.full[st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
 #pragma unroll
             for (int i = 0; i < kKeyPages; ++i) {
               const int y = __shfl_sync(0xffffffffu, row, i);
               if (lane == 0) {
-                tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, &sm.full[st]);
-                tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, &sm.full[st]);
+                tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, bar);
+                tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, bar);
               }
             }
             __syncwarp();
             ++used;
-          }
-        }
-        if (ok && it.clear_at >= 0) {
-          // the rows behind the sequence's last token hold anything: clear them
-          // in its last value tile, the one just asked for
-          const unsigned st = (used - 1) % kStages;
-          const int page = it.sp.blocks - 1 - (it.k0 + it.clear_at) * kKeyPages;
-          ok = tc5_wait(&sm.full[st], ((used - 1) / kStages) & 1, abort);
-          if (!ok) break;
-          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
-            uint8_t* row = ring + st * kTileBytes + (page * kPage + lane) * 128;
+            if (clear) {
+              ok = tc5_wait(&sm.tail, tails & 1, abort);
+              ++tails;
+              if (!ok) break;
+              const int page = it.sp.blocks - 1 - k * kKeyPages;
+              if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
+                uint8_t* r = dst + (page * kPage + lane) * 128;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              reinterpret_cast<uint4*>(row + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 16; ++i)
+                  reinterpret_cast<uint4*>(r + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.full[st]);
+            }
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.clean);
         }
       }
       // after a time-out: what is in flight lands before the memory is given back
@@ -304,6 +305,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         bool landed = true;
         for (int w = 0; w < 2; ++w)
           if (q_used[w]) landed &= mbar_wait_bounded(&sm.q_full[w], (q_used[w] - 1) & 1, kDrainLimit);
+        if (tails) landed &= mbar_wait_bounded(&sm.tail, (tails - 1) & 1, kDrainLimit);
         for (unsigned i = used > kStages ? used - kStages : 0; i < used; ++i)
           landed &= mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit);
         if (!landed && lane == 0) record_error(p.c.status, kDevErrDrainTimeout);
@@ -339,7 +341,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ph ^= 1;
           }
         };
-        unsigned q_used = 0, p_used = 0, cleaned = 0, turns = 0;
+        unsigned q_used = 0, p_used = 0, turns = 0;
         auto my_turn = [&]() -> bool {
           const unsigned n = turns++;
           if (w == 1) return tc5_wait(&sm.turn[1], n & 1, abort);
@@ -348,7 +350,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         for (unsigned ni = 0; ok; ++ni) {
           const Item* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
-          const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0, clear_at = ip->clear_at;
+          const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0;
           mbar_arrive(&sm.i_empty[ni % kItems]);
           if (nk == 0) continue;
           // a stage that this tile has no use for is given back as it comes
@@ -371,8 +373,6 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             next();
             const bool more = j + 1 < nk;
             ok = tc5_wait(&sm.full[vs], vp, abort);
-            // the tile with the sequence's last page: its tail is cleared first
-            if (ok && j == clear_at) ok = tc5_wait(&sm.clean, cleaned++ & 1, abort);
             if (ok && more) ok = tc5_wait(&sm.full[st], ph, abort);
             if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, abort);
             if (ok) ok = my_turn();

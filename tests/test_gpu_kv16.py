@@ -749,3 +749,99 @@ def test_binding_refuses(L):
         with pytest.raises(L.OscarError):
             f()
     assert L.kernel_launches() == n0
+
+
+# ------------------------------------------------- many items, odd placements
+
+def test_attention_many_sequences(L):
+    """Far more work than one round of the grid, of very unequal sizes."""
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(1, 220, (300,), generator=g).tolist()
+    news = [max(1, int(n * f)) for n, f in zip(lens, torch.rand(300, generator=g).tolist())]
+    for Hq, Hkv, window, sink in ((8, 2, 0, 0), (5, 1, 40, 3)):
+        case = R.Case(lens, Hkv, BF, seed=Hq)
+        run_attention(L, case, case.cache(L), news, Hq, window, sink, extra=1)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (1, 1)])
+def test_smallest_cache(L, Hq, Hkv):
+    """One sequence of one token in a cache with room for one, and its step."""
+    case = R.Case([1], Hkv, FP, paged=False, slack=0, weights=True)
+    cache = case.cache(L)
+    assert cache.capacity == 1
+    run_attention(L, case, cache, [1], Hq)
+    run_decode(L, case, cache, Hq, accumulate=True)
+
+
+def test_outputs_at_16_byte_addresses(L):
+    """Outputs need 16-byte alignment, no more."""
+    case = R.Case([150, 40], 2, BF, seed=12)
+    cache = case.cache(L)
+    q = case.normal(190, 8)
+    flat = torch.zeros(190 * 8 * 128 + 8, dtype=BF, device="cuda")
+    out = flat[8:].view(190, 8, 128)
+    assert out.data_ptr() % 32 == 16
+    ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, 8, 190, 256))
+    L.kv16_attention(cache, q.cuda(), i32([0, 150, 190]), R.SCALE, 256, out, ws)
+    for b, rows in enumerate((slice(0, 150), slice(150, 190))):
+        o, _, _, tol, _, _ = R.attend(case, b, q[rows])
+        R.assert_within(out[rows], o, tol, str(b))
+    one = flat[8:8 + 2 * 8 * 128].view(2, 8, 128)
+    last = q[[149, 189]]
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, 8, 256))
+    L.kv16_decode_attention(cache, last.cuda(), R.SCALE, 256, one, ws)
+    for b in range(2):
+        o, _, _, tol, _, _ = R.attend(case, b, last[b:b + 1])
+        R.assert_within(one[b:b + 1], o, tol, str(b))
+    assert L.device_status() == 0
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,n_obs,window,sink", [
+    ([2500], 16, 1, 0, 0, 0),            # few items: clusters of eight share them
+    ([900, 700], 6, 2, 0, 0, 0),         # clusters, groups that do not divide a tile
+    (None, 16, 8, 20, 0, 0),             # many items of 256 keys, whole and partial
+    (None, 24, 8, 0, 100, 3)])
+def test_accumulate_item_sizes(L, lens, Hq, Hkv, n_obs, window, sink):
+    if lens is None:
+        g = torch.Generator().manual_seed(Hq)
+        lens = torch.randint(1, 420, (40,), generator=g).tolist()
+    news = [max(1, n - n // 3) for n in lens]
+    case = R.Case(lens, Hkv, BF, seed=Hq, weights=True)
+    cache, start = case.cache(L), R.start_of(news)
+    q = case.normal(start[-1], Hq)
+    out, lse = torch.empty((start[-1], Hq, 128), dtype=BF, device="cuda"), torch.empty((start[-1], Hq), device="cuda")
+    ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, Hq, start[-1], cache.capacity, window, sink))
+    L.kv16_attention(cache, q.cuda(), i32(start), R.SCALE, cache.capacity, out, ws, window, sink, lse)
+    L.kv16_accumulate(cache, q.cuda(), lse, i32(start), R.SCALE, cache.capacity, window, sink, n_obs)
+    assert L.device_status() == 0
+    for b, n in enumerate(lens):
+        o, z, p, tol, ztol, dmax = R.attend(case, b, q[start[b]:start[b + 1]], window, sink)
+        R.assert_within(out[start[b]:start[b + 1]], o, tol, f"out {b}")
+        skip = max(0, news[b] - n_obs) if n_obs else 0
+        w, t = R.weight_of(p[skip:], dmax[skip:], Hq // Hkv)
+        R.assert_within(R.tokens(cache, b, n, "weight"), w + case.w[b].double(),
+                        t + 4 * float(ztol.max()) * w, f"weight {b}")
+
+
+def test_calls_on_two_streams_at_once(L):
+    """The same caches read by attention and decode on two streams, each with a
+    workspace of its own."""
+    case = R.Case([700, 300], 2, BF, seed=21)
+    cache = case.cache(L)
+    q, q1 = case.normal(400, 8), case.normal(2, 8)
+    qd, q1d, st = q.cuda(), q1.cuda(), i32([0, 300, 400])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out, one = torch.empty_like(qd), torch.empty_like(q1d)
+    wa = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, 8, 400, 800))
+    wd = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, 8, 800))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        L.kv16_attention(cache, qd, st, R.SCALE, 800, out, wa, stream=streams[0])
+        L.kv16_decode_attention(cache, q1d, R.SCALE, 800, one, wd, stream=streams[1])
+    torch.cuda.synchronize()
+    assert L.device_status() == 0
+    for b, rows in enumerate((slice(0, 300), slice(300, 400))):
+        o, _, _, tol, _, _ = R.attend(case, b, q[rows])
+        R.assert_within(out[rows], o, tol, str(b))
+        o, _, _, tol, _, _ = R.attend(case, b, q1[b:b + 1])
+        R.assert_within(one[b:b + 1], o, tol, str(b))
