@@ -189,13 +189,11 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       if (uk >= kKBufs) ok = tc5_wait(&sm.k_empty[kb], (uk / kKBufs - 1) & 1, abort);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[kb], it.halves * kTileBytes);
-      for (int i = 0; i < 4 * it.halves; ++i) {
-        const int y = __shfl_sync(0xffffffffu, row, i);
-        if (lane == 0) {
-          uint8_t* dst = kbuf + (kb * 2 + i / 4) * kTileBytes + (i & 3) * 4096;
-          tma_box2(dst, &map_k, 0, y, &sm.k_full[kb]);
-          tma_box2(dst + kHalf, &map_k, 64, y, &sm.k_full[kb]);
-        }
+      __syncwarp();
+      if (lane < 4 * it.halves) {          // a lane per page
+        uint8_t* dst = kbuf + (kb * 2 + lane / 4) * kTileBytes + (lane & 3) * 4096;
+        tma_box2(dst, &map_k, 0, row, &sm.k_full[kb]);
+        tma_box2(dst + kHalf, &map_k, 64, row, &sm.k_full[kb]);
       }
       __syncwarp();
       ++uk;

@@ -251,8 +251,19 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           __syncwarp();
           ++q_used[w];
         }
+        int row = none;
+        auto ask = [&](int kv, unsigned st, uint64_t* bar) {
+          uint8_t* dst = ring + st * kTileBytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
+          __syncwarp();
+          if (lane < kKeyPages) {          // a lane per page
+            tma_box2(dst + lane * 4096, kv ? &map_v : &map_k, 0, row, bar);
+            tma_box2(dst + kHalf + lane * 4096, kv ? &map_v : &map_k, 64, row, bar);
+          }
+          __syncwarp();
+        };
         for (int k = it.k0; k < it.k1 && ok; ++k) {
-          int row = none;
+          row = none;
           if (lane < kKeyPages && k * kKeyPages + lane < it.sp.blocks) {
             row = kv16_block_row(p.c, it.b, it.h, it.sp.block(k * kKeyPages + lane));
             if (row < 0) {
@@ -264,40 +275,30 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           for (int kv = 0; kv < 2; ++kv) {
             const unsigned st = used % kStages;
             if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort);
-            if (!ok) break;
-            uint8_t* dst = ring + st * kTileBytes;
-            // The rows behind the sequence's last token hold anything.  The value
-            // tile that has them lands on a barrier of this warp's, which clears
-            // them and only then passes the tile on.
-            const bool clear = kv == 1 && it.clear && k + 1 == it.k1;
-            uint64_t* bar = clear ? &sm.tail : &sm.full[st];
-            if (lane == 0) mbar_arrive_expect_tx(bar, kTileBytes);
-#pragma unroll
-            for (int i = 0; i < kKeyPages; ++i) {
-              const int y = __shfl_sync(0xffffffffu, row, i);
-              if (lane == 0) {
-                tma_box2(dst + i * 4096, kv ? &map_v : &map_k, 0, y, bar);
-                tma_box2(dst + kHalf + i * 4096, kv ? &map_v : &map_k, 64, y, bar);
-              }
-            }
-            __syncwarp();
+            if (!ok || (kv == 1 && it.clear && k + 1 == it.k1)) break;
+            ask(kv, st, &sm.full[st]);
             ++used;
-            if (clear) {
-              ok = tc5_wait(&sm.tail, tails & 1, abort);
-              ++tails;
-              if (!ok) break;
-              const int page = it.sp.blocks - 1 - k * kKeyPages;
-              if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
-                uint8_t* r = dst + (page * kPage + lane) * 128;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  reinterpret_cast<uint4*>(r + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
-              }
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.full[st]);
-            }
           }
+        }
+        if (ok && it.clear) {
+          // The rows behind the sequence's last token hold anything.  The value
+          // tile that has them, the last one, lands on a barrier of this warp's,
+          // which clears them and only then passes the tile on.
+          const unsigned st = used % kStages;
+          ask(1, st, &sm.tail);
+          ++used;
+          ok = tc5_wait(&sm.tail, tails++ & 1, abort);
+          if (!ok) break;
+          const int page = it.sp.blocks - 1 - (it.k1 - 1) * kKeyPages;
+          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
+            uint8_t* r = ring + st * kTileBytes + (page * kPage + lane) * 128;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              reinterpret_cast<uint4*>(r + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[st]);
         }
       }
       // after a time-out: what is in flight lands before the memory is given back
