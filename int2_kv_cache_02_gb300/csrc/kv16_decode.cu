@@ -10,19 +10,35 @@
 // written at once.  A CTA has at most two partial rows: the one it enters in
 // the middle (slot 0) and the one it leaves in the middle (slot 1).
 //
-// Inside a CTA each of 4 warps takes every fourth page of the run through its
-// own ring of shared-memory slots: 4 tensor copies (TMA, 128-byte swizzle) per
+// Inside a CTA each of 10 warps takes every tenth page of the run, through a
+// shared-memory slot of its own: 4 tensor copies (TMA, 128-byte swizzle) per
 // page, keys and values in halves of 64 channels, completing on the slot's
-// barrier.  With 3 slots of 16 KB per warp an SM keeps 192 KB in flight.
+// barrier.  While one warp computes, the other nine's pages are on their way
+// (160 KB per SM), so a deeper ring per warp gains nothing and more warps do:
+// with 4 warps of three slots each a page's chain of mma and softmax (about a
+// microsecond) bounded the stream (batch 16 x 64K, 8 heads a group: 349 us; 8
+// warps 320, 10 warps 314).  One page (32 tokens) per step is also what the
+// block table gives.
 //
 // Mathematics.  S = Q K^T by mma.sync m16n8k16 with the group's query heads as
 // the 16 rows (up to 16 heads in one pass over the keys, the rest padding):
-// the tensor work of a page, 64 instructions, is a fifth of the time that its
-// 16 KB take to arrive, so padding rows cost nothing.  The accumulator layout
-// of S is the operand layout of P in O += P V, so probabilities stay in
-// registers.  One pass with the running maximum and sum in fp32 (log2 domain);
-// a probability is rounded to the cache's type for the product with V (half a
-// step, as the output itself), the sum l is of the unrounded ones.
+// the tensor work of a page, 96 instructions, is under the time that its 16 KB
+// take to arrive, so padding rows cost nothing.  The accumulator layout of S is
+// the operand layout of P in O += P V, so probabilities stay in registers.  One
+// pass with the running maximum and sum in fp32 (log2 domain); probabilities
+// enter the product with V as the sum of two numbers of the cache's type (hi +
+// lo, 16 bits of mantissa and more), so the output is rounded once, at the end.
+//
+// The accumulated weights need the joined maximum and sum.  So the scores go to
+// the workspace (4 bytes per token and query head beside 512 per token and KV
+// head) and a second launch turns them into probabilities.
+//
+// Measured (GB300, copies run at 6.71 TB/s): batch 16 x 64K, 32/4 heads, even
+// lengths 314 us, 6.84 TB/s; lengths of 13K to 64K 197 us (floor 193), with
+// weights 218 + 21 us; batch 48 x 16K with a window of 4096, 32/8 heads, 129 us
+// (floor 119: 129 pages a row leave three rows and their joins to a CTA); one
+// head and 1024 tokens 8.4 us, a chain of dependent loads: length, table, page,
+// records.
 #include <algorithm>
 
 #include "kv16.cuh"
@@ -48,7 +64,7 @@ namespace {
 
 constexpr int NW = 10;                   // warps of a CTA, each with a slot of its own
 constexpr int kSlotBytes = 4 * 4096;     // a page: K and V, two halves of 64 channels each
-constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many
+constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many: one a warp
 constexpr int kORow = 136;               // floats of a head's output row in shared memory
 
 struct DecodeParams {

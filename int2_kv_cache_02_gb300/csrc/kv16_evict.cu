@@ -14,6 +14,9 @@
 // so the choice does not depend on any order.
 //
 // The copy is bound by its bytes, 1 KB per kept token read and written.
+//
+// Measured (GB300): 64 rows of 10K to 32K tokens cut to 2048: choice 21.6 us,
+// copy 23.2 (floor of both 21); 16 rows of 2176: 8.2 + 5.3 us, latency.
 #include <algorithm>
 
 #include "kv16.cuh"
