@@ -36,11 +36,11 @@
 // rounded to the type of V for the product (half a step relative, as the output
 // itself); the sum is of the unrounded ones.
 //
-// Measured (GB300): 8K-token causal prompt, 32/8 heads, bf16: 335 us, 1.64
-// PFLOP/s, 0.84 of the measured bf16 burst rate; in a loop of seconds the power
-// limit is reached and it takes 370 us (0.84 of the sustained rate).  Four
-// sequences of 2K to 4K new tokens, window 1000 and 4 sinks, 32/4 heads, fp16:
-// 209 us against 119; each 32-token item spends 9 key tiles on 7.9 tiles' worth
+// Measured (GB300): 8K-token causal prompt, 32/8 heads, bf16: 330 us, 1.67
+// PFLOP/s, 0.86 of the measured bf16 burst rate; in a loop of seconds the power
+// limit is reached and it takes 362 us (0.89 of the sustained rate).  Four
+// sequences of 3K to 4K new tokens, window 1000 and 4 sinks, 32/4 heads, fp16:
+// 207 us against 119; each 32-token item spends 9 key tiles on 7.9 tiles' worth
 // of visible keys, and its first tile, masks and results (about 7 of 30
 // thousand cycles) leave the tensor cores idle.
 //

@@ -123,10 +123,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
-// Polls of a wait before it gives up: an unsuccessful try_wait takes about a
-// microsecond, so two to three seconds.  (No clock is read: the waits are
+// Polls of a wait before it gives up: an unsuccessful try_wait takes about four
+// microseconds, so about two seconds.  (No clock is read: the waits are
 // inlined many times over, and the kernels' time goes by their code's size.)
-constexpr unsigned kTcWaitLimit = 1u << 21;
+constexpr unsigned kTcWaitLimit = 1u << 19;
 
 // Waits for phase `parity` of `bar`.  Gives up after the limit, or soon after
 // another warp has (*abort set), and then sets *abort itself.
