@@ -520,6 +520,7 @@ oscar_status oscar_kv16_write(const oscar_kv16_cache* c, const uint16_t* k_new,
  *       (a query that sees nothing: out 0, lse -inf)
  *  max_tok  host bound on the n_tok[b]; plans the split of long caches over
  *       several blocks when there are few queries
+ * out and lse share no memory with q (rows and the gaps between them).
  * window >= 0, n_sink >= 0.  workspace: oscar_kv16_attention_workspace_bytes
  * of device memory (no initialisation; NULL if that is 0).  Calls that use
  * one workspace must not overlap on the GPU.
@@ -537,7 +538,7 @@ size_t oscar_kv16_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, i
  * n_tok[b] - 1), with the work split evenly over the tokens of the whole
  * batch and joined: one launch (accumulate: two).
  *  q    [B][Hq][128], rows q_stride elements apart;  out [B][Hq][128], dense
- *       (a sequence without tokens gives zeros)
+ *       and apart from q's memory (a sequence without tokens gives zeros)
  *  accumulate  1 adds to weight[j] of every visible token j of KV head h the
  *       softmax probabilities it got from h's query heads (c->weight set)
  * workspace: a decode workspace (see oscar_decode_attention: its header of

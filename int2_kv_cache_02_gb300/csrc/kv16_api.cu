@@ -86,6 +86,14 @@ bool overlap(Range a, Range b) {
   return a.p && b.p && a.n && b.n && a.p < b.p + b.n && b.p < a.p + a.n;
 }
 
+// Does [n bytes at p] share memory with the queries?  (Rows whose result is not
+// finite read their query again after results are written.)
+bool in_queries(const void* p, size_t n, const uint16_t* q, long long stride, int rows, int Hq) {
+  return overlap({static_cast<const char*>(p), n},
+                 {reinterpret_cast<const char*>(q),
+                  ((size_t)(rows - 1) * (size_t)stride + (size_t)Hq * kD) * sizeof(uint16_t)});
+}
+
 // The decode's pages are numbered in 32 bits over all rows.
 bool decode_size_ok(const oscar_kv16_cache* c, int max_tok) {
   const long long blocks = (std::min<long long>(max_tok, capacity(c)) + kPage - 1) / kPage;
@@ -161,6 +169,10 @@ oscar_status oscar_kv16_attention(const oscar_kv16_cache* c, const uint16_t* q,
   const size_t need = kv16_attention_ws_bytes(v, Hq, total, max_tok, window, n_sink);
   if (need && (!workspace || ws_bytes < need)) return OSCAR_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
+  const size_t heads = (size_t)total * Hq;
+  if (in_queries(out, heads * kD * sizeof(uint16_t), q, q_stride, total, Hq) ||
+      in_queries(lse, heads * sizeof(float), q, q_stride, total, Hq))
+    return OSCAR_ERR_INVALID_ARG;
   v.status = device_status_word();
   if (!v.status) return OSCAR_ERR_CUDA;
   int launches = 0;
@@ -198,6 +210,8 @@ oscar_status oscar_kv16_decode_attention(const oscar_kv16_cache* c, const uint16
       ws_bytes < kv16_decode_ws_bytes(v, Hq, max_tok, window, n_sink, accumulate != 0))
     return OSCAR_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
+  if (in_queries(out, (size_t)c->B * Hq * kD * sizeof(uint16_t), q, q_stride, c->B, Hq))
+    return OSCAR_ERR_INVALID_ARG;
   v.status = device_status_word();
   if (!v.status) return OSCAR_ERR_CUDA;
   int launches = 0;

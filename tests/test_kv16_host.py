@@ -193,3 +193,22 @@ def test_cache_takes_fitting_tensors_only():
                 dict(k=k[..., :64], v=k[..., :64]), dict(weight=torch.zeros(4, 2, 31))):
         with pytest.raises(ValueError):
             O.KV16Cache(**{**dict(k=k, v=k, n_tok=n, block_table=t), **bad})
+
+
+@no_gpu_only
+def test_output_apart_from_the_queries(L):
+    """A row whose result is not finite reads its query again after results
+    are written, so an output in the queries' memory is refused."""
+    r, x, ws = ctypes.byref(cache()), P(FAKE), P(FAKE + 0x8000000)
+    n = 4 * 4 * 128 * 2
+    far = P(FAKE + 0x6000000)
+    prompt = lambda out, lse=None: L.oscar_kv16_attention(
+        r, x, 512, x, 4, 4, 1.0, 64, 0, 0, out, lse, ws, 1 << 30, None)
+    assert prompt(x) == prompt(P(FAKE + n - 16)) == prompt(P(FAKE - n + 16)) == INVALID
+    assert prompt(far, x) == prompt(far, P(FAKE + n - 4)) == INVALID
+    assert prompt(P(FAKE + n)) == prompt(P(FAKE - n)) == prompt(far, P(FAKE + n)) == CUDA
+    n = 2 * 4 * 128 * 2
+    step = lambda out: L.oscar_kv16_decode_attention(
+        r, x, 512, 4, 1.0, 64, 0, 0, 0, out, ws, 1 << 30, None)
+    assert step(x) == step(P(FAKE + n - 16)) == step(P(FAKE - n + 16)) == INVALID
+    assert step(P(FAKE + n)) == step(P(FAKE - n)) == CUDA
