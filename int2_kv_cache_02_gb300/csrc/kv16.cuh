@@ -3,11 +3,10 @@
 #pragma once
 
 #include "common.cuh"
+#include "kv16_span.h"
 #include "launch.h"
 
 namespace oscar {
-
-constexpr int kPage = OSCAR_GROUP;   // tokens of one page
 
 // bf16 and fp16 as the element type of keys, values, queries and outputs.
 struct Bf16 {
@@ -51,32 +50,6 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* start, int B, int 
     if (__ldg(start + mid) <= r) lo = mid; else hi = mid;
   }
   return __ldg(start + lo) <= r && r < __ldg(start + lo + 1) ? lo : -1;
-}
-
-// The tokens that queries at positions [first, last] of one sequence can see:
-// whole blocks, the sinks' (sink_blocks of them from block 0) and then the
-// window's (from block w0), numbered 0 .. blocks - 1.
-struct Span {
-  int sink_blocks, w0, blocks;
-  __device__ __forceinline__ Span() {}
-  __device__ __forceinline__ Span(int first, int last, int window, int n_sink) {
-    if (last < 0) {
-      sink_blocks = w0 = blocks = 0;
-      return;
-    }
-    const int lo = window > 0 ? max(0, first - window + 1) : 0;
-    const int end = (last + kPage) / kPage;    // blocks up to the last position
-    w0 = lo / kPage;
-    sink_blocks = min((int)(((long long)min(n_sink, last + 1) + kPage - 1) / kPage), w0);
-    blocks = sink_blocks + end - w0;
-  }
-  __device__ __forceinline__ int block(int i) const {
-    return i < sink_blocks ? i : w0 + i - sink_blocks;
-  }
-};
-
-__device__ __forceinline__ bool kv16_visible(int j, int at, int window, int n_sink) {
-  return j <= at && (window == 0 || j > at - window || j < n_sink);
 }
 
 // One query against the blocks [i0, i1) of a span, worked by a warp: the

@@ -369,7 +369,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!(ok = ip != nullptr) || ip->stop) break;
           const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0;
           mbar_arrive(&sm.i_empty[ni % kItems]);
-          if (nk == 0) continue;
+          if (nk <= 0) continue;
           // a stage that this tile has no use for is given back as it comes
           ok = tc5_wait(&sm.full[st], ph, abort);
           if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, abort);
@@ -454,7 +454,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       if (ntok <= 0) continue;
       // the thread's row; rows past the tile's end work like its last token
       const bool valid = tok < ntok;
-      const int at = at_first + min(tok, ntok - 1);
+      const int at = max(at_first + min(tok, ntok - 1), -1);   // (-1: before the first token)
       // key tiles [in0, in1), counted from k0, whose pages the warp's rows all see
       int in0, in1;
       {
