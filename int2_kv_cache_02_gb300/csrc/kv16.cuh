@@ -55,12 +55,15 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* start, int B, int 
 // One query against the blocks [i0, i1) of a span, worked by a warp: the
 // running maximum m (log2 domain) and sum l, and the unnormalised output of
 // channels 4 lane .. 4 lane + 3.  fp32 throughout; a token that the query
-// does not see is not touched, whatever its key and value hold.
+// does not see is not touched, whatever its key and value hold.  Ends early,
+// with m and l not complete, once every channel that `open` (a bit for each of
+// the lane's four) asks for is NaN: nothing changes it any more.
+constexpr int kRowTokens = 8;    // tokens whose loads are in flight together
 template <class T>
 __device__ __forceinline__ void kv16_warp_row(const Kv16& c, const uint16_t* q, int b, int h,
                                               int at, const Span& sp, int i0, int i1, int window,
-                                              int n_sink, float scale_log2, float& m, float& l,
-                                              float (&o)[4]) {
+                                              int n_sink, float scale_log2, unsigned open,
+                                              float& m, float& l, float (&o)[4]) {
   const int lane = threadIdx.x & 31;
   const uint2 qr = reinterpret_cast<const uint2*>(q)[lane];
   const float2 q0 = T::unpack(qr.x), q1 = T::unpack(qr.y);
@@ -74,29 +77,58 @@ __device__ __forceinline__ void kv16_warp_row(const Kv16& c, const uint16_t* q, 
       if (lane == 0) record_error(c.status, kDevErrBadPaged);
       continue;
     }
+    const unsigned see =
+        __ballot_sync(0xffffffffu, kv16_visible(blk * kPage + lane, at, window, n_sink));
 #pragma unroll 1
-    for (int t = 0; t < kPage; ++t) {
-      if (!kv16_visible(blk * kPage + t, at, window, n_sink)) continue;
-      const long long e = ((long long)row + t) * 32 + lane;
-      const uint2 kr = reinterpret_cast<const uint2*>(c.k)[e];
-      const uint2 vr = reinterpret_cast<const uint2*>(c.v)[e];
-      const float2 k0 = T::unpack(kr.x), k1 = T::unpack(kr.y);
-      float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+    for (int t0 = 0; t0 < kPage; t0 += kRowTokens) {
+      const unsigned here = see >> t0;
+      if ((here & ((1u << kRowTokens) - 1)) == 0) continue;
+      uint2 kr[kRowTokens], vr[kRowTokens];
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= scale_log2;
-      const float mn = fmaxf(m, s);
+      for (int u = 0; u < kRowTokens; ++u) {
+        const long long e = ((long long)row + t0 + u) * 32 + lane;
+        kr[u] = vr[u] = make_uint2(0u, 0u);
+        if ((here >> u) & 1u) {
+          kr[u] = reinterpret_cast<const uint2*>(c.k)[e];
+          vr[u] = reinterpret_cast<const uint2*>(c.v)[e];
+        }
+      }
+      float s[kRowTokens], mn = m;
+#pragma unroll
+      for (int u = 0; u < kRowTokens; ++u) {
+        const float2 k0 = T::unpack(kr[u].x), k1 = T::unpack(kr[u].y);
+        s[u] = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+        for (int u = 0; u < kRowTokens; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+#pragma unroll
+      for (int u = 0; u < kRowTokens; ++u) {
+        s[u] = (here >> u) & 1u ? s[u] * scale_log2 : -INFINITY;
+        mn = fmaxf(mn, s[u]);
+      }
       // a maximum of -inf has met only scores of -inf: they weigh nothing
       const float a = mn == -INFINITY ? 1.0f : fast_exp2(m - mn);
-      const float p = s == -INFINITY ? 0.0f : fast_exp2(s - mn);
       m = mn;
-      l = l * a + p;
-      const float2 v0 = T::unpack(vr.x), v1 = T::unpack(vr.y);
-      o[0] = o[0] * a + p * v0.x;
-      o[1] = o[1] * a + p * v0.y;
-      o[2] = o[2] * a + p * v1.x;
-      o[3] = o[3] * a + p * v1.y;
+      l *= a;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] *= a;
+#pragma unroll
+      for (int u = 0; u < kRowTokens; ++u) {
+        const float p = s[u] == -INFINITY ? 0.0f : fast_exp2(s[u] - mn);
+        const float2 v0 = T::unpack(vr[u].x), v1 = T::unpack(vr[u].y);
+        l += p;
+        o[0] += p * v0.x;
+        o[1] += p * v0.y;
+        o[2] += p * v1.x;
+        o[3] += p * v1.y;
+      }
     }
+    bool settled = true;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) settled &= !((open >> x) & 1u) || o[x] != o[x];
+    if (__all_sync(0xffffffffu, settled)) return;
   }
 }
 

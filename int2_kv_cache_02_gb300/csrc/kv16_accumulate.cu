@@ -59,7 +59,7 @@ struct Smem {
   uint64_t k_full[kKBufs], k_empty[kKBufs], q_full[kQStages], q_empty[kQStages];
   uint64_t s_full[2][2], s_empty[2][2], l_full[2][kLseSlots], l_empty[2][kLseSlots], c_full, c_empty, drain;
   uint32_t tmem;
-  int abort;
+  int state;           // of the waits
   alignas(16) float lse[2][kLseSlots][128];   // per warpgroup; at the end: the CTA's sums
   float part[128];                         // one warpgroup's sums of a lone key tile
 };
@@ -156,7 +156,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_init(&sm.c_empty, 4);
     mbar_init(&sm.drain, 1);
     mbar_fence_init();
-    sm.abort = 0;
+    sm.state = 0;
   }
   float sum = 0.0f;      // of the thread's key
   // query rows that no copy fills (groups that do not divide 128) hold zeros
@@ -171,7 +171,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   tc5_fence_after();
   const uint32_t tmem = sm.tmem;
-  volatile int* abort = &sm.abort;
+  volatile int* state = &sm.state;
   bool ok = true;
 
   if (warp == 8) {
@@ -194,7 +194,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
         }
       }
       const int kb = uk % kKBufs;
-      if (uk >= kKBufs) ok = tc5_wait(&sm.k_empty[kb], (uk / kKBufs - 1) & 1, abort);
+      if (uk >= kKBufs) ok = tc5_wait(&sm.k_empty[kb], (uk / kKBufs - 1) & 1, state);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[kb], it.halves * kTileBytes);
       __syncwarp();
@@ -207,7 +207,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       ++uk;
       for (int t = it.t0; t < it.t1; ++t) {
         const int st = uq % kQStages;
-        if (uq >= kQStages) ok = tc5_wait(&sm.q_empty[st], (uq / kQStages - 1) & 1, abort);
+        if (uq >= kQStages) ok = tc5_wait(&sm.q_empty[st], (uq / kQStages - 1) & 1, state);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.q_full[st], 2 * 64 * 2 * p.g * p.tokens);
@@ -220,7 +220,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       }
     }
     if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-    if (*abort) {
+    if (*state & 1) {
       // what is in flight lands before the memory is given back
       for (int i = max(0, uk - kKBufs); i < uk; ++i)
         if (!mbar_wait_bounded(&sm.k_full[i % kKBufs], (i / kKBufs) & 1, kDrainLimit) && lane == 0)
@@ -239,15 +239,15 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       for (int round = 0; ok && item_of(round) >= 0; ++round) {
         const Item it = find_item(p, item_of(round), rank, false);
         if (it.t1 <= it.t0) continue;
-        ok = tc5_wait(&sm.k_full[kb], kp, abort);
+        ok = tc5_wait(&sm.k_full[kb], kp, state);
         for (int t = it.t0; t < it.t1 && ok; ++t) {
-          ok = tc5_wait(&sm.q_full[st], sp, abort);
+          ok = tc5_wait(&sm.q_full[st], sp, state);
           const uint64_t q = dq + st * (kTileBytes >> 4);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || (it.halves == 1 && ((t - it.t0) & 1) != w)) continue;
             const unsigned buf = us[w] & 1;
-            if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, abort);
+            if (us[w] >= 2) ok = tc5_wait(&sm.s_empty[w][buf], (us[w] / 2 - 1) & 1, state);
             if (!ok) continue;
             tc5_fence_after();
             const uint64_t k = dk + (kb * 2 + (it.halves == 2 ? w : 0)) * (kTileBytes >> 4);
@@ -307,7 +307,7 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       for (; t < it.t1; t += by) {
         if (t + by < it.t1) load(t + by, next);      // on its way while this one waits
         const unsigned slot = ul % kLseSlots;
-        if (ul >= kLseSlots) ok = tc5_wait(&sm.l_empty[w][slot], (ul / kLseSlots - 1) & 1, abort);
+        if (ul >= kLseSlots) ok = tc5_wait(&sm.l_empty[w][slot], (ul / kLseSlots - 1) & 1, state);
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -334,8 +334,8 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       const int by = it.halves == 1 ? 2 : 1;
       for (int t = it.t0 + (by == 2 ? w : 0); t < it.t1; t += by) {
         const unsigned slot = ul % kLseSlots, buf = us & 1;
-        ok = tc5_wait(&sm.l_full[w][slot], (ul / kLseSlots) & 1, abort) &&
-             tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, abort);
+        ok = tc5_wait(&sm.l_full[w][slot], (ul / kLseSlots) & 1, state) &&
+             tc5_wait(&sm.s_full[w][buf], (us / 2) & 1, state);
         if (!ok) break;
         tc5_fence_after();
         // the tokens [lo, hi) of the tile that see the thread's key: rows are
@@ -397,13 +397,13 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       if (it.halves == 1) {
         // both warpgroups have a part: the second hands its over
         if (w == 1) {
-          if (lone > 0) ok = tc5_wait(&sm.c_empty, (lone - 1) & 1, abort);
+          if (lone > 0) ok = tc5_wait(&sm.c_empty, (lone - 1) & 1, state);
           if (!ok) break;
           sm.part[tid & 127] = sum;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.c_full);
         } else {
-          ok = tc5_wait(&sm.c_full, lone & 1, abort);
+          ok = tc5_wait(&sm.c_full, lone & 1, state);
           if (!ok) break;
           sum += sm.part[tid];
           __syncwarp();

@@ -45,9 +45,15 @@
 // thousand cycles) leave the tensor cores idle.
 //
 // Hidden values.  A hidden token's probability is exactly 0, but 0 * NaN is
-// not: rows past the end of the sequence are cleared in shared memory, and a
-// row whose output is not finite is worked again by a warp that touches only
-// the tokens the row sees (kv16_warp_row).
+// not: rows past the end of the sequence are cleared in shared memory, and the
+// channels of a row that are NaN although its sum is a number are worked again
+// by a warp that touches only the tokens the row sees (redo_row).  That may take
+// longer than the bounded waits allow, so they do not run out while a warp says
+// that it is at it.  A sum that is NaN has met a visible score that is NaN or
+// +inf: the whole row is NaN and stays so.  (An 8K prompt, 32/8 heads, 0.36 ms:
+// with a NaN in a key the same, in its first value 1.1 ms, in its middle one 41;
+// bf16 with an infinity in the first value 70.  Done after the last item instead,
+// in line or out of line, it cost every prompt 2 to 5 %: the loop's registers.)
 //
 // Few tiles over a long cache: the key tiles are split over several CTAs, which
 // leave (m, l, o[128]) records that a second kernel joins.
@@ -103,7 +109,7 @@ struct Smem {
   uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], tail, drain[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
-  int abort;
+  int state;           // of the waits
   Item item[kItems];
 };
 constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: all but one
@@ -163,6 +169,68 @@ __device__ __forceinline__ void store_row4(const AttnParams& p, long long row, i
       make_uint2(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv));
 }
 
+// Is a channel of O (or of the result) one to be worked again?  NaN is, and in
+// bf16 an infinity too: sums of probabilities up to kMost times the largest
+// values can overflow.  In fp16 they cannot: an infinity there is a visible one.
+template <class T>
+__device__ __forceinline__ bool is_open(float x) {
+  return T::kHalf ? x != x : !(fabsf(x) < INFINITY);
+}
+// NaN once x was such a channel.
+template <class T>
+__device__ __forceinline__ float gather_open(float x, float so_far) {
+  if constexpr (T::kHalf) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(so_far));
+    return y;
+  } else {
+    return fmaf(x, 0.0f, so_far);
+  }
+}
+
+// Row `row` of a work item, position `at`, whose results this warp has just
+// written: its open channels again, from the tokens alone that it sees.
+template <class T>
+__device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int split, int k0,
+                                         int k1, const Span& sp, long long row, int at) {
+  const int lane = threadIdx.x & 31;
+  float* rec = p.part + (row * p.splits + split) * kRecFloats;
+  uint2* out = reinterpret_cast<uint2*>(p.out + row * kD) + lane;
+  float x[4];
+  if (p.splits > 1) {
+    if (rec[1] != rec[1]) return;            // the sum
+    const float4 v = *reinterpret_cast<const float4*>(rec + 4 + 4 * lane);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *out;
+    const float2 a = T::unpack(v.x), b = T::unpack(v.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+  }
+  unsigned open = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) open |= is_open<T>(x[i]) ? 1u << i : 0u;
+  if (!__any_sync(0xffffffffu, open != 0)) return;
+  const long long token = row / p.q.Hq;
+  const int head = (int)(row - token * p.q.Hq);
+  float m, l, o[4];
+  kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)head * kD, b, h, at, sp,
+                   k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
+                   p.q.scale_log2, open, m, l, o);
+  // a record's channels stand on the record's maximum
+  float f = l == 0.0f ? 0.0f : 1.0f / l;
+  if (p.splits > 1) {
+    const float m0 = rec[0];
+    f = m == -INFINITY || m0 == -INFINITY ? 1.0f : fast_exp2(m - m0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if ((open >> i) & 1u) x[i] = o[i] * f;
+  if (p.splits > 1)
+    *reinterpret_cast<float4*>(rec + 4 + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *out = make_uint2(T::pack(x[0], x[1]), T::pack(x[2], x[3]));
+}
+
 template <class T>
 __global__ void __launch_bounds__(kThreads, 1)
 kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -201,16 +269,16 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     mbar_init(&sm.tail, 1);
     mbar_fence_init();
-    sm.abort = 0;
+    sm.state = 0;
   }
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
   const uint32_t tmem = sm.tmem;
-  volatile int* abort = &sm.abort;
+  volatile int* state = &sm.state;
   // an item is read by every warp but the scheduling one, and then given back
   auto take = [&](unsigned n) -> const Item* {
-    return tc5_wait(&sm.i_full[n % kItems], (n / kItems) & 1, abort) ? &sm.item[n % kItems]
+    return tc5_wait(&sm.i_full[n % kItems], (n / kItems) & 1, state) ? &sm.item[n % kItems]
                                                                      : nullptr;
   };
 
@@ -230,7 +298,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         Item it;
         if (!stop && (x >= items || !find_item(p, (int)x, it))) continue;
         it.stop = stop;
-        if (n >= kItems) ok = tc5_wait(&sm.i_empty[n % kItems], (n / kItems - 1) & 1, abort);
+        if (n >= kItems) ok = tc5_wait(&sm.i_empty[n % kItems], (n / kItems - 1) & 1, state);
         if (!ok) break;
         if (lane == 0) {
           sm.item[n % kItems] = it;
@@ -255,7 +323,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || it.cnt[w] == 0) continue;
-          if (q_used[w] > 0) ok = tc5_wait(&sm.q_empty[w], (q_used[w] - 1) & 1, abort);
+          if (q_used[w] > 0) ok = tc5_wait(&sm.q_empty[w], (q_used[w] - 1) & 1, state);
           if (!ok) continue;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sm.q_full[w], qbytes);
@@ -290,7 +358,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const unsigned st = used % kStages;
-            if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, abort);
+            if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, state);
             if (!ok || (kv == 1 && it.clear && k + 1 == it.k1)) break;
             ask(kv, st, &sm.full[st]);
             ++used;
@@ -303,7 +371,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           const unsigned st = used % kStages;
           ask(1, st, &sm.tail);
           ++used;
-          ok = tc5_wait(&sm.tail, tails++ & 1, abort);
+          ok = tc5_wait(&sm.tail, tails++ & 1, state);
           if (!ok) break;
           const int page = it.sp.blocks - 1 - (it.k1 - 1) * kKeyPages;
           if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
@@ -318,7 +386,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
       }
       // after a time-out: what is in flight lands before the memory is given back
-      if (*abort) {
+      if (*state & 1) {
         bool landed = true;
         for (int w = 0; w < 2; ++w)
           if (q_used[w]) landed &= mbar_wait_bounded(&sm.q_full[w], (q_used[w] - 1) & 1, kDrainLimit);
@@ -361,8 +429,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         unsigned q_used = 0, p_used = 0, turns = 0;
         auto my_turn = [&]() -> bool {
           const unsigned n = turns++;
-          if (w == 1) return tc5_wait(&sm.turn[1], n & 1, abort);
-          return n == 0 || tc5_wait(&sm.turn[0], (n - 1) & 1, abort);
+          if (w == 1) return tc5_wait(&sm.turn[1], n & 1, state);
+          return n == 0 || tc5_wait(&sm.turn[0], (n - 1) & 1, state);
         };
         for (unsigned ni = 0; ok; ++ni) {
           const Item* ip = take(ni);
@@ -371,8 +439,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           mbar_arrive(&sm.i_empty[ni % kItems]);
           if (nk <= 0) continue;
           // a stage that this tile has no use for is given back as it comes
-          ok = tc5_wait(&sm.full[st], ph, abort);
-          if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, abort);
+          ok = tc5_wait(&sm.full[st], ph, state);
+          if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, state);
           if (ok) ok = my_turn();
           if (!ok) break;
           if (cnt > 0) {
@@ -389,9 +457,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             const unsigned vs = st, vp = ph;
             next();
             const bool more = j + 1 < nk;
-            ok = tc5_wait(&sm.full[vs], vp, abort);
-            if (ok && more) ok = tc5_wait(&sm.full[st], ph, abort);
-            if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, abort);
+            ok = tc5_wait(&sm.full[vs], vp, state);
+            if (ok && more) ok = tc5_wait(&sm.full[st], ph, state);
+            if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, state);
             if (ok) ok = my_turn();
             if (!ok) break;
             if (j < cnt) {
@@ -402,7 +470,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
               for (int i = 0; i < 4; ++i)
                 tc5_mma_ts(to, ts + 8 * i, v + i * (2048 >> 4), id_o, j > 0 || i > 0);
               tc5_commit(&sm.h_full[w]);
-              ok = tc5_wait(&sm.p_full[w][1], p_used++ & 1, abort);
+              ok = tc5_wait(&sm.p_full[w][1], p_used++ & 1, state);
               if (!ok) break;
               tc5_fence_after();
 #pragma unroll
@@ -431,7 +499,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       __syncwarp();
     }
-    if (*abort && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
+    if ((*state & 1) && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // -------------------------------------------------------------- softmax
@@ -503,7 +571,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         return (sum0.x + sum0.y) + (sum1.x + sum1.y);
       };
       for (int j = 0; j < my_n; ++j) {
-        ok = tc5_wait(&sm.s_full[w], s_used & 1, abort);
+        ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
         if (!ok) break;
         tc5_fence_after();
         const bool inside = j >= in0 && j < in1;
@@ -540,7 +608,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             // S of this tile is there, so the products of the tiles before it are
             // complete; that of the first half may be under way
             if (i == 1) {
-              ok = tc5_wait(&sm.h_full[w], s_used & 1, abort);
+              ok = tc5_wait(&sm.h_full[w], s_used & 1, state);
               if (!ok) return;
               tc5_fence_after();
             }
@@ -580,12 +648,12 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       }
 
       // ------------------------------------------------------------ results
-      if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, abort);
+      if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, state);
       if (!ok) break;
       tc5_fence_after();
       const long long row = (long long)(row_first + tok) * p.q.Hq + h * p.g + head;
       const float inv = p.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-      float odd = l * 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: not finite
+      float odd = 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: a channel is open
       float* rec = p.part + (row * p.splits + split) * kRecFloats;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -599,10 +667,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
-          odd1 = fmaf(__uint_as_float(o[e + 1]), 0.0f, odd1);
-          odd2 = fmaf(__uint_as_float(o[e + 2]), 0.0f, odd2);
-          odd3 = fmaf(__uint_as_float(o[e + 3]), 0.0f, odd3);
+          odd = gather_open<T>(__uint_as_float(o[e]), odd);
+          odd1 = gather_open<T>(__uint_as_float(o[e + 1]), odd1);
+          odd2 = gather_open<T>(__uint_as_float(o[e + 2]), odd2);
+          odd3 = gather_open<T>(__uint_as_float(o[e + 3]), odd3);
         }
         if (p.splits > 1) {
           if (valid)
@@ -634,26 +702,18 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
         else if (p.lse) p.lse[row] = kv16_lse(m, l);
       }
-      // rows with a result that is not finite, token by token
+      // rows with open channels, by the whole warp; the other warps' waits do not
+      // run out meanwhile
       __syncwarp();
-      for (unsigned bad = __ballot_sync(0xffffffffu, valid && odd != 0.0f); bad; bad &= bad - 1) {
-        const int src = __ffs(bad) - 1;
-        const long long rw = __shfl_sync(0xffffffffu, row, src);
-        const int a = __shfl_sync(0xffffffffu, at, src);
-        const long long token = rw / p.q.Hq;
-        const int hd = (int)(rw - token * p.q.Hq);
-        float mm, ll, oo[4];
-        kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)hd * kD, b, h, a, sp,
-                         k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
-                         p.q.scale_log2, mm, ll, oo);
-        if (p.splits > 1) {
-          float* d = p.part + (rw * p.splits + split) * kRecFloats;
-          if (lane == 0) *reinterpret_cast<float2*>(d) = make_float2(mm, ll);
-          *reinterpret_cast<float4*>(d + 4 + 4 * lane) = make_float4(oo[0], oo[1], oo[2], oo[3]);
-        } else {
-          store_row4<T>(p, rw, lane, oo, ll == 0.0f ? 0.0f : 1.0f / ll);
-          if (p.lse && lane == 0) p.lse[rw] = kv16_lse(mm, ll);
+      unsigned bad = __ballot_sync(0xffffffffu, valid && odd != odd && l == l);
+      if (bad) {
+        if (lane == 0) atomicAdd(&sm.state, kTcBusy);
+        for (; bad; bad &= bad - 1) {
+          const int src = __ffs(bad) - 1;
+          redo_row<T>(p, b, h, split, k0, k1, sp, __shfl_sync(0xffffffffu, row, src),
+                      __shfl_sync(0xffffffffu, at, src));
         }
+        if (lane == 0) atomicAdd(&sm.state, -kTcBusy);
       }
     }
     if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);

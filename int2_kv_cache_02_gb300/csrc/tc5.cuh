@@ -123,23 +123,30 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
-// Polls of a wait before it gives up: an unsuccessful try_wait takes about four
-// microseconds, so about two seconds.  (No clock is read: the waits are
+// Polls of a wait before it gives up: an unsuccessful try_wait takes 3.8
+// microseconds (measured), so two seconds.  (No clock is read: the waits are
 // inlined many times over, and the kernels' time goes by their code's size.)
 constexpr unsigned kTcWaitLimit = 1u << 19;
 
-// Waits for phase `parity` of `bar`.  Gives up after the limit, or soon after
-// another warp has (*abort set), and then sets *abort itself.
-__device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
+// A CTA's state of the waits: bit 0 once a wait has given up, and kTcBusy for
+// every warp that is at work of its own of unknown length.
+constexpr int kTcBusy = 2;
+
+// Waits for phase `parity` of `bar`.  Gives up after the limit, or as soon as
+// another warp has, and then says so in *state (the count of busy warps may be
+// lost then; bit 0 stays).  The limit counts from when no warp is busy.
+__device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* state) {
   if (mbar_test_wait(bar, parity)) return true;
-  for (unsigned i = 0; i < kTcWaitLimit; ++i) {
+  unsigned i = 0;
+  do {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && *abort) return false;
-  }
-  *abort = 1;
+    const int x = *state;
+    if (x & 1) return false;
+    i = x ? 0 : i + 1;
+  } while (i < kTcWaitLimit);
+  *state = 1;
   return false;
 }
-
 // 32 bytes to a 32-byte aligned address.
 __device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),

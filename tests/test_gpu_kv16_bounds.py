@@ -71,3 +71,109 @@ def test_decode_bad_lengths_under_a_window(L, window, sink):
             w, t = R.weight_of(p, dmax, 4)
             R.assert_within(R.tokens(cache, b, case.lens[b], "weight"), w + case.w[b].double(),
                             t + 2 * R.U32, str(b))
+
+
+# --------------------------------------------------- values that are not finite
+
+def poke(case, cache, b, t, k=None, v=None, channel=None, head=0):
+    """Puts numbers that are not finite into a token of the device's cache (the
+    host's keep what they are)."""
+    at = (b, head, t) if cache.block_table is None else (int(cache.block_table[b, t // 32]), head, t % 32)
+    if k is not None:
+        cache.k[at] = k
+    if v is not None:
+        cache.v[at if channel is None else at + (channel,)] = v
+
+
+def attention_of(L, case, cache, news, Hq, window=0, sink=0):
+    start = R.start_of(news)
+    q = case.normal(start[-1], Hq)
+    out = torch.full((start[-1], Hq, 128), 7.0, dtype=case.dtype, device="cuda")
+    lse = torch.full((start[-1], Hq), 7.0, device="cuda")
+    ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, Hq, start[-1], cache.capacity, window, sink))
+    L.kv16_attention(cache, q.cuda(), i32(start), R.SCALE, cache.capacity, out, ws, window, sink, lse)
+    assert L.device_status() == 0
+    return start, q, out.cpu(), lse.cpu()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lens,news", [([700, 6000, 300], [700, 6000, 300]), ([9000, 4000], [5, 3])])
+def test_nan_key_makes_its_own_rows_nan(L, dtype, lens, news):
+    """A NaN in the first key of a sequence: all of that KV head's rows are NaN,
+    output and lse, whole prompts and split caches alike; nothing else changes."""
+    case = R.Case(lens, 2, dtype, seed=1)
+    cache = case.cache(L)
+    poke(case, cache, 1, 0, k=math.nan)
+    start, q, out, lse = attention_of(L, case, cache, news, 8)
+    mine = slice(start[1], start[2])
+    assert torch.isnan(out[mine, :4]).all() and torch.isnan(lse[mine, :4]).all()
+    for b in range(len(lens)):
+        rows = slice(max(start[b], start[b + 1] - 40), start[b + 1])
+        o, z, _, tol, ztol, _ = R.attend(case, b, q[rows])
+        h = slice(4, 8) if b == 1 else slice(0, 8)
+        R.assert_within(out[rows, h], o[:, h], tol[:, h], f"out {b}")
+        R.assert_within(lse[rows, h], z[:, h], ztol[:, h], f"lse {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("lens,news,window,sink", [
+    ([700, 900], [700, 900], 0, 0), ([900, 9000], [3, 5], 0, 0), ([300, 900], [300, 900], 70, 4)])
+def test_a_value_reaches_its_channel_where_it_is_seen(L, dtype, what, lens, news, window, sink):
+    """One channel of one value is NaN or infinite: the rows that see the token
+    have that in this channel, and what they have without it in all others; rows
+    that do not see it are as without it."""
+    case = R.Case(lens, 2, dtype, seed=2)
+    cache = case.cache(L)
+    token, ch = {0: 2, 70: 500}[window], 37
+    poke(case, cache, 1, token, v=what, channel=ch, head=1)
+    start, q, out, lse = attention_of(L, case, cache, news, 6, window, sink)
+    for b in range(2):
+        rows = slice(start[b], start[b + 1])
+        o, z, _, tol, ztol, _ = R.attend(case, b, q[rows], window, sink)
+        if b == 1:
+            at = torch.arange(lens[1] - news[1], lens[1])
+            see = R.visible(at, lens[1], window, sink)[:, token]
+            got = out[rows, 3:, ch][see]
+            assert torch.isnan(got).all() if math.isnan(what) else (got == what).all()
+            assert see.any()
+            # that channel has been judged: the rest against the host's values
+            out[rows, 3:, ch] = torch.where(see[:, None], o[:, 3:, ch].to(dtype), out[rows, 3:, ch])
+        R.assert_within(out[rows], o, tol, f"out {b}")
+        R.assert_within(lse[rows], z, ztol, f"lse {b}")
+
+
+@pytest.mark.parametrize("n,dtype,what", [
+    (100000, BF, math.nan), (100000, FP, math.inf), (1000000, BF, math.inf)])
+def test_hidden_value_of_a_long_sequence(L, n, dtype, what):
+    """The last value of a long sequence is not finite: the queries before it in its
+    tile are as without it, however long their rows take (a million tokens: longer
+    than the waits allow otherwise), and so are the short sequences whose work comes
+    after them on the same multiprocessors."""
+    new, short = 20000, 400
+    case = R.Case([n] + [40] * short, 1, dtype, paged=False, slack=0, seed=3)
+    blocks = n // 32
+    table = torch.full((1 + short, blocks), -1, dtype=torch.int32)
+    table[0] = torch.arange(blocks)
+    table[1:, :2] = blocks + torch.arange(2 * short, dtype=torch.int32).view(short, 2)
+    k = torch.zeros((blocks + 2 * short, 1, 32, 128), dtype=dtype, device="cuda")
+    v = torch.zeros_like(k)
+    for x, y in ((k, case.k), (v, case.v)):
+        x[:blocks] = y[0].view(blocks, 1, 32, 128).cuda()
+        tail = torch.zeros((short, 64, 128), dtype=dtype)
+        tail[:, :40] = torch.cat(y[1:])
+        x[blocks:] = tail.view(2 * short, 1, 32, 128).cuda()
+    cache = L.KV16Cache(k, v, i32(case.lens), block_table=table.cuda())
+    poke(case, cache, 0, n - 1, v=what)
+    start, q, out, lse = attention_of(L, case, cache, [new] + [40] * short, 1)
+    seen = out[new - 1].float()
+    assert torch.isnan(seen).all() if math.isnan(what) else (seen == math.inf).all()
+    for i in (new - 2, new - 100, new - 129, 0):
+        o, z, _, tol, ztol, _ = R.attend(case, 0, q[i:i + 1], lens=[n - new + i + 1])
+        R.assert_within(out[i:i + 1], o, tol, str(i))
+        R.assert_within(lse[i:i + 1], z, ztol, str(i))
+    assert torch.isfinite(out[:new - 1].float()).all() and torch.isfinite(lse).all()
+    for b in range(1, 1 + short, 23):
+        rows = slice(start[b], start[b + 1])
+        o, z, _, tol, ztol, _ = R.attend(case, b, q[rows])
+        R.assert_within(out[rows], o, tol, str(b))
