@@ -598,6 +598,14 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * iterations: 1 .. 1<<20, else OSCAR_ERR_INVALID_ARG (nothing launched). */
 oscar_status oscar_selftest_wait_timeout(unsigned iterations, void* stream);
 
+/* Self-test of the 16-bit decode's waits: oscar_kv16_decode_attention (dense q,
+ * no window) in which every wait for a copy gives up at once.  out is
+ * unspecified, the status word reports the time-out, and the workspace's header
+ * is zero afterwards as after every call. */
+oscar_status oscar_selftest_kv16_decode_timeout(const oscar_kv16_cache* c, const uint16_t* q,
+                                                int Hq, int max_tok, uint16_t* out,
+                                                void* workspace, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* oscar_status_string(oscar_status s);
 

@@ -49,10 +49,12 @@ enum : unsigned {
   kDevErrArrival = 8u,       // a decode row's arrival counter was not zero at the start
 };
 
-// Iteration limits of the bounded spin-waits.  One try_wait may itself
-// suspend for a while, so these bound the wait at a few seconds.
+// Iteration limits of the bounded spin-waits.  A try_wait suspends for 3.8
+// microseconds before it fails (measured), so these are a minute, four seconds
+// and, for the kernels of the 16-bit cache, two.
 constexpr unsigned kWaitLimit = 1u << 24;
 constexpr unsigned kDrainLimit = 1u << 20;
+constexpr unsigned kTcWaitLimit = 1u << 19;
 
 __device__ __forceinline__ unsigned smem_u32(const void* p) {
   return static_cast<unsigned>(__cvta_generic_to_shared(p));

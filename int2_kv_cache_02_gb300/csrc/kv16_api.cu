@@ -113,6 +113,36 @@ size_t evict_ws_bytes(const oscar_kv16_cache* src, long long keep) {
   return (size_t)((long long)src->B * src->Hkv) * (size_t)(keep + 4) * sizeof(int32_t);
 }
 
+oscar_status decode(const oscar_kv16_cache* c, const uint16_t* q, long long q_stride, int Hq,
+                    float softmax_scale, int max_tok, int window, int n_sink, int accumulate,
+                    uint16_t* out, void* workspace, size_t ws_bytes, unsigned wait_limit,
+                    void* stream) {
+  oscar_status st = check(c);
+  if (st != OSCAR_OK) return st;
+  if (!q || !out || !window_ok(softmax_scale, max_tok, window, n_sink) ||
+      (accumulate != 0 && accumulate != 1) || (accumulate && !c->weight))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!heads_ok(Hq, c->Hkv)) return OSCAR_ERR_UNSUPPORTED;
+  if (!stride_ok(q_stride, Hq)) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16)) return OSCAR_ERR_ALIGNMENT;
+  if (!decode_size_ok(c, max_tok)) return OSCAR_ERR_UNSUPPORTED;
+  Kv16 v = view(c);
+  if (!workspace ||
+      ws_bytes < kv16_decode_ws_bytes(v, Hq, max_tok, window, n_sink, accumulate != 0))
+    return OSCAR_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
+  if (in_queries(out, (size_t)c->B * Hq * kD * sizeof(uint16_t), q, q_stride, c->B, Hq))
+    return OSCAR_ERR_INVALID_ARG;
+  v.status = device_status_word();
+  if (!v.status) return OSCAR_ERR_CUDA;
+  int launches = 0;
+  const cudaError_t e = launch_kv16_decode(
+      v, query(q, q_stride, nullptr, c->B, Hq, softmax_scale, max_tok, window, n_sink),
+      accumulate != 0, out, workspace, wait_limit, &launches, as_stream(stream));
+  count_launches(launches);
+  return from_cuda(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -196,30 +226,15 @@ oscar_status oscar_kv16_decode_attention(const oscar_kv16_cache* c, const uint16
                                          int max_tok, int window, int n_sink, int accumulate,
                                          uint16_t* out, void* workspace, size_t ws_bytes,
                                          void* stream) {
-  oscar_status st = check(c);
-  if (st != OSCAR_OK) return st;
-  if (!q || !out || !window_ok(softmax_scale, max_tok, window, n_sink) ||
-      (accumulate != 0 && accumulate != 1) || (accumulate && !c->weight))
-    return OSCAR_ERR_INVALID_ARG;
-  if (!heads_ok(Hq, c->Hkv)) return OSCAR_ERR_UNSUPPORTED;
-  if (!stride_ok(q_stride, Hq)) return OSCAR_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16)) return OSCAR_ERR_ALIGNMENT;
-  if (!decode_size_ok(c, max_tok)) return OSCAR_ERR_UNSUPPORTED;
-  Kv16 v = view(c);
-  if (!workspace ||
-      ws_bytes < kv16_decode_ws_bytes(v, Hq, max_tok, window, n_sink, accumulate != 0))
-    return OSCAR_ERR_WORKSPACE;
-  if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
-  if (in_queries(out, (size_t)c->B * Hq * kD * sizeof(uint16_t), q, q_stride, c->B, Hq))
-    return OSCAR_ERR_INVALID_ARG;
-  v.status = device_status_word();
-  if (!v.status) return OSCAR_ERR_CUDA;
-  int launches = 0;
-  const cudaError_t e = launch_kv16_decode(
-      v, query(q, q_stride, nullptr, c->B, Hq, softmax_scale, max_tok, window, n_sink),
-      accumulate != 0, out, workspace, &launches, as_stream(stream));
-  count_launches(launches);
-  return from_cuda(e);
+  return decode(c, q, q_stride, Hq, softmax_scale, max_tok, window, n_sink, accumulate, out,
+                workspace, ws_bytes, kTcWaitLimit, stream);
+}
+
+oscar_status oscar_selftest_kv16_decode_timeout(const oscar_kv16_cache* c, const uint16_t* q,
+                                                int Hq, int max_tok, uint16_t* out,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+  return decode(c, q, (long long)Hq * kD, Hq, 1.0f, max_tok, 0, 0, 0, out, workspace, ws_bytes, 0,
+                stream);
 }
 
 oscar_status oscar_kv16_accumulate(const oscar_kv16_cache* c, const uint16_t* q,

@@ -76,6 +76,7 @@ struct DecodeParams {
   float2* stats;        // [B][Hq] (m, 1 / l), accumulate only
   float* scores;        // [pages][g][32] log2-domain scores, accumulate only
   int g;
+  unsigned wait_limit;  // polls of a wait for a copy
   bool halves;          // the warps' outputs are joined in two steps
 };
 
@@ -182,7 +183,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   __shared__ __align__(8) uint64_t full[NW];
   __shared__ int scan[NW];
   __shared__ float sm_m[NW][kMaxGroup], sm_l[NW][kMaxGroup];
-  __shared__ int s_last, s_abort;
+  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;   // swizzle atoms
   uint8_t* slot = smem + warp * kSlotBytes;
@@ -193,7 +194,6 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   if (tid == 0) {
     for (int w = 0; w < NW; ++w) mbar_init(&full[w], 1);
     mbar_fence_init();
-    s_abort = 0;
   }
   const int line = line_up(p.c, p.q, first, scan, NW * 32, blockIdx.x == 0);
   // rows without visible tokens: zeros
@@ -233,6 +233,9 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   int x = x0 + warp;                // the warp's next page to work on
   fetch(x);
   unsigned phase = 0;
+  // A warp whose copies do not land in time works no further pages, but joins in
+  // all that follows: the rows' counters have to come back to zero.
+  bool gave_up = false;
 
   const int hr = lane >> 2, hc = 2 * (lane & 3);    // accumulator row, column
   int seg = x0;
@@ -256,10 +259,11 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-    for (; x < seg_end; x += NW) {
-      if (!mbar_wait_bounded(&full[warp], phase, kWaitLimit)) {
+    for (; x < seg_end && !gave_up; x += NW) {
+      // (one answer for the warp: its lanes may see the barrier differently)
+      gave_up = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp], phase, p.wait_limit));
+      if (gave_up) {
         if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-        s_abort = 1;
         break;
       }
       const int j0 = r.sp.block(x - r.r0) * kPage;
@@ -452,7 +456,6 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       }
     }
     __syncthreads();
-    if (s_abort) break;      // uniform: written before the barriers above
     if (!own_row) {
       // the row's CTAs are c0 .. c1; the last to arrive joins their records
       if (tid == 0) {
@@ -489,8 +492,8 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     seg = seg_end;
   }
-  // after a time-out the warp's copy in flight lands before its memory is given back
-  if (s_abort && x < x1 && !mbar_wait_bounded(&full[warp], phase, kDrainLimit) && lane == 0)
+  // the copy in flight lands before its memory is given back
+  if (gave_up && !mbar_wait_bounded(&full[warp], phase, kDrainLimit) && lane == 0)
     record_error(p.c.status, kDevErrDrainTimeout);
 }
 
@@ -601,12 +604,13 @@ size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int 
 }
 
 cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
-                               void* ws, int* launches, cudaStream_t s) {
+                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s) {
   DecodeParams p;
   p.c = c;
   p.q = q;
   p.out = out;
   p.g = q.Hq / c.Hkv;
+  p.wait_limit = wait_limit;
   const long long pages = line_pages(c, q.max_tok, q.window, q.n_sink);
   const int grid = decode_grid(pages);
   p.counters = decode_row_counters(ws);

@@ -224,8 +224,9 @@ cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* o
 size_t kv16_attention_ws_bytes(const Kv16& c, int Hq, int total, int max_tok, int window,
                                int n_sink);
 constexpr int kMaxDecodeBatch = 4096;   // sequences of one call
+// wait_limit: polls of a wait for a copy before it gives up.
 cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
-                               void* ws, int* launches, cudaStream_t s);
+                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s);
 size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int n_sink,
                             bool accumulate);
 cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const float* lse, int n_obs,

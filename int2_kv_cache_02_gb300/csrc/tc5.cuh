@@ -123,18 +123,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, unsigned parity) {
   return ok != 0;
 }
 
-// Polls of a wait before it gives up: an unsuccessful try_wait takes 3.8
-// microseconds (measured), so two seconds.  (No clock is read: the waits are
-// inlined many times over, and the kernels' time goes by their code's size.)
-constexpr unsigned kTcWaitLimit = 1u << 19;
-
 // A CTA's state of the waits: bit 0 once a wait has given up, and kTcBusy for
 // every warp that is at work of its own of unknown length.
 constexpr int kTcBusy = 2;
 
 // Waits for phase `parity` of `bar`.  Gives up after the limit, or as soon as
 // another warp has, and then says so in *state (the count of busy warps may be
-// lost then; bit 0 stays).  The limit counts from when no warp is busy.
+// lost then; bit 0 stays).  The limit counts from when no warp is busy.  (Polls
+// are counted and no clock is read: the waits are inlined many times over, and
+// the kernels' time goes by their code's size.)
 __device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* state) {
   if (mbar_test_wait(bar, parity)) return true;
   unsigned i = 0;

@@ -124,6 +124,8 @@ def _load() -> ctypes.CDLL:
         "oscar_kv16_evict_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int]),
         "oscar_device_status": (c_int, [c_void_p]),
         "oscar_selftest_wait_timeout": (c_int, [c_uint, c_void_p]),
+        "oscar_selftest_kv16_decode_timeout": (c_int, [P16, c_void_p, c_int, c_int, c_void_p,
+                                                       c_void_p, c_size_t, c_void_p]),
         "oscar_status_string": (ctypes.c_char_p, [c_int]),
         "oscar_kernel_launches": (c_ulonglong, []),
     }
@@ -667,6 +669,19 @@ def selftest_wait_timeout(iterations: int = 256, stream=None):
     gives up after `iterations` polls and sets the device status word."""
     _check(_lib.oscar_selftest_wait_timeout(iterations, _stream(stream)),
            "oscar_selftest_wait_timeout")
+
+
+def selftest_kv16_decode_timeout(cache: KV16Cache, q: torch.Tensor, max_tok: int,
+                                 out: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """kv16_decode_attention (dense q, no window) in which every wait for a copy
+    gives up at once: the status word reports it, the workspace stays usable."""
+    qp, _, _, Hq = cache._rows(q, None, cache.B)
+    if not q.is_contiguous():
+        raise ValueError("expected dense queries")
+    w, wb = _bytes(workspace, cache)
+    _kv16_call(cache, "oscar_selftest_kv16_decode_timeout", _lib.oscar_selftest_kv16_decode_timeout,
+               (cache._ref, qp, Hq, max_tok, cache._mine(out, cache.dtype, cache.B * Hq * D), w, wb),
+               stream)
 
 
 def device_status(stream=None) -> int:

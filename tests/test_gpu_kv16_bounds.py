@@ -177,3 +177,21 @@ def test_hidden_value_of_a_long_sequence(L, n, dtype, what):
         rows = slice(start[b], start[b + 1])
         o, z, _, tol, ztol, _ = R.attend(case, b, q[rows])
         R.assert_within(out[rows], o, tol, str(b))
+
+
+# ------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("lens,Hq,Hkv", [([20000], 4, 1), ([5000, 1, 9000, 64, 0, 3000], 16, 2), ([50] * 300, 8, 4)])
+def test_decode_workspace_after_waits_run_out(L, lens, Hq, Hkv):
+    """When no copy lands in time the status word says so, the rows' counters come
+    back to zero, and the next call on the workspace is right."""
+    case = R.Case(lens, Hkv, BF, seed=9)
+    cache = case.cache(L)
+    q = case.normal(case.B, Hq).cuda()
+    out = torch.empty_like(q)
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, Hq, cache.capacity))
+    for _ in range(2):
+        L.selftest_kv16_decode_timeout(cache, q, cache.capacity, out, ws)
+        assert L.device_status() == 7 and L.device_status() == 0
+        assert (ws[:65536].view(torch.int32) == 0).all()
+    run_decode(L, case, cache, Hq, ws=ws)

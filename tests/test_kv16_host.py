@@ -212,3 +212,15 @@ def test_output_apart_from_the_queries(L):
         r, x, 512, 4, 1.0, 64, 0, 0, 0, out, ws, 1 << 30, None)
     assert step(x) == step(P(FAKE + n - 16)) == step(P(FAKE - n + 16)) == INVALID
     assert step(P(FAKE + n)) == step(P(FAKE - n)) == CUDA
+
+
+@no_gpu_only
+def test_decode_timeout_selftest_refusals(L):
+    """The self-test of the decode's waits takes what the decode takes."""
+    r, x, out, ws = ctypes.byref(cache()), P(FAKE), P(FAKE + 0x6000000), P(FAKE + 0x8000000)
+    f = lambda q=x, Hq=4, most=64, o=out, w=ws, n=1 << 30: L.oscar_selftest_kv16_decode_timeout(
+        r, q, Hq, most, o, w, n, None)
+    assert f(q=None) == f(o=None) == f(most=-1) == f(o=x) == INVALID
+    assert f(Hq=3) == UNSUPPORTED and f(o=P(FAKE + 0x6000008)) == ALIGNMENT
+    assert f(w=None) == f(n=100) == WORKSPACE
+    assert L.oscar_selftest_kv16_decode_timeout(None, x, 4, 64, out, ws, 1 << 30, None) == INVALID
