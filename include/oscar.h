@@ -598,6 +598,16 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * iterations: 1 .. 1<<20, else OSCAR_ERR_INVALID_ARG (nothing launched). */
 oscar_status oscar_selftest_wait_timeout(unsigned iterations, void* stream);
 
+/* Self-test of the waits of the tensor-core kernels (prompt attention and
+ * accumulated weight).  One CTA holds tensor memory; a warp of it waits for
+ * something that never comes, with a limit of `iterations` polls, another with
+ * the usual limit, a third is busy for four times `iterations` polls, while
+ * which no limit counts.  report (device int32 [3]): 1 if the first gave up, 1
+ * if the second followed, 1 if one of them did while the third was busy (so
+ * 1, 1, 0).  The status word reports the time-out.
+ * iterations: 1 .. 1<<16, else OSCAR_ERR_INVALID_ARG (nothing launched). */
+oscar_status oscar_selftest_tc_wait_timeout(unsigned iterations, int32_t* report, void* stream);
+
 /* Self-test of the 16-bit decode's waits: oscar_kv16_decode_attention (dense q,
  * no window) in which every wait for a copy gives up at once.  out is
  * unspecified, the status word reports the time-out, and the workspace's header

@@ -620,6 +620,16 @@ oscar_status oscar_selftest_wait_timeout(unsigned iterations, void* stream) {
   return from_cuda(e);
 }
 
+oscar_status oscar_selftest_tc_wait_timeout(unsigned iterations, int32_t* report, void* stream) {
+  if (iterations == 0 || iterations > (1u << 16) || !report) return OSCAR_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(report) & 3) return OSCAR_ERR_ALIGNMENT;
+  unsigned* p = status_ptr();
+  if (!p) return OSCAR_ERR_CUDA;
+  cudaError_t e = launch_tc_wait_timeout_selftest(p, iterations, report, as_stream(stream));
+  g_launches++;
+  return from_cuda(e);
+}
+
 oscar_status oscar_device_status(void* stream) {
   unsigned* p = status_ptr();
   if (!p) return OSCAR_ERR_CUDA;

@@ -9,6 +9,7 @@
 // the loads of successive partials do not wait on one another.  Lane l holds
 // channels 4 l .. 4 l + 3; shared memory adds the warps' results.
 #include "common.cuh"
+#include "tc5.cuh"
 #include "launch.h"
 
 namespace oscar {
@@ -90,6 +91,49 @@ __global__ void wait_timeout_selftest_kernel(unsigned* status, unsigned iteratio
 
 cudaError_t launch_wait_timeout_selftest(unsigned* status, unsigned iterations, cudaStream_t s) {
   wait_timeout_selftest_kernel<<<1, 32, 0, s>>>(status, iterations);
+  return cudaGetLastError();
+}
+
+// Self-test of the tensor-core kernels' waits, on barriers that nothing arrives
+// at.  Warp 2 is busy for four times the limit, then no longer; warp 0 gives up
+// after the limit; warp 1, whose own limit is far off, leaves because of it.
+__global__ void tc_wait_timeout_selftest_kernel(unsigned* status, unsigned iterations,
+                                                int* report) {
+  __shared__ __align__(8) uint64_t bar[3];
+  __shared__ uint32_t tmem;
+  __shared__ int state;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) tc5_alloc(&tmem, 32);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+    mbar_fence_init();
+    state = kTcBusy;
+  }
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  bool gave_up;
+  if (warp == 2) {
+    mbar_wait_bounded(&bar[2], 0u, 4 * iterations);
+    gave_up = *static_cast<volatile int*>(&state) & 1;     // while this warp was busy
+    __syncwarp();
+    if (lane == 0) atomicAdd(&state, -kTcBusy);
+  } else {
+    gave_up = !tc5_wait(&bar[warp], 0u, &state, warp == 0 ? iterations : kTcWaitLimit);
+    if (gave_up && lane == 0) record_error(status, kDevErrWaitTimeout);
+  }
+  if (lane == 0) report[warp] = gave_up;
+  tc5_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc5_fence_after();
+    tc5_dealloc(tmem, 32);
+  }
+}
+
+cudaError_t launch_tc_wait_timeout_selftest(unsigned* status, unsigned iterations, int* report,
+                                            cudaStream_t s) {
+  tc_wait_timeout_selftest_kernel<<<1, 96, 0, s>>>(status, iterations, report);
   return cudaGetLastError();
 }
 

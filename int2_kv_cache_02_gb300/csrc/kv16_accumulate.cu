@@ -220,15 +220,13 @@ kv16_accumulate_kernel(const __grid_constant__ CUtensorMap map_q,
       }
     }
     if (!ok && lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
-    if (*state & 1) {
-      // what is in flight lands before the memory is given back
-      for (int i = max(0, uk - kKBufs); i < uk; ++i)
-        if (!mbar_wait_bounded(&sm.k_full[i % kKBufs], (i / kKBufs) & 1, kDrainLimit) && lane == 0)
-          record_error(p.c.status, kDevErrDrainTimeout);
-      for (int i = max(0, uq - kQStages); i < uq; ++i)
-        if (!mbar_wait_bounded(&sm.q_full[i % kQStages], (i / kQStages) & 1, kDrainLimit) && lane == 0)
-          record_error(p.c.status, kDevErrDrainTimeout);
-    }
+    // what is in flight lands before the memory is given back, whoever gives up
+    for (int i = max(0, uk - kKBufs); i < uk; ++i)
+      if (!mbar_wait_bounded(&sm.k_full[i % kKBufs], (i / kKBufs) & 1, kDrainLimit) && lane == 0)
+        record_error(p.c.status, kDevErrDrainTimeout);
+    for (int i = max(0, uq - kQStages); i < uq; ++i)
+      if (!mbar_wait_bounded(&sm.q_full[i % kQStages], (i / kQStages) & 1, kDrainLimit) && lane == 0)
+        record_error(p.c.status, kDevErrDrainTimeout);
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
     if (elect_one()) {

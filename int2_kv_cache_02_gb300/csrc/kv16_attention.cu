@@ -314,6 +314,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                                  : p.c.B * p.c.Hkv * p.c.T_cap;      // reads zeros
       const unsigned qbytes = 2 * 64 * 2 * p.g * p.tokens;
       unsigned used = 0, q_used[2] = {0, 0}, tails = 0;
+      unsigned kept = ~0u;     // the tile that has come and is not passed on yet
       for (unsigned ni = 0; ok; ++ni) {
         const Item* ip = take(ni);
         if (!(ok = ip != nullptr) || ip->stop) break;
@@ -370,7 +371,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           // which clears them and only then passes the tile on.
           const unsigned st = used % kStages;
           ask(1, st, &sm.tail);
-          ++used;
+          kept = used++;
           ok = tc5_wait(&sm.tail, tails++ & 1, state);
           if (!ok) break;
           const int page = it.sp.blocks - 1 - (it.k1 - 1) * kKeyPages;
@@ -383,18 +384,18 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.full[st]);
+          kept = ~0u;
         }
       }
-      // after a time-out: what is in flight lands before the memory is given back
-      if (*state & 1) {
-        bool landed = true;
-        for (int w = 0; w < 2; ++w)
-          if (q_used[w]) landed &= mbar_wait_bounded(&sm.q_full[w], (q_used[w] - 1) & 1, kDrainLimit);
-        if (tails) landed &= mbar_wait_bounded(&sm.tail, (tails - 1) & 1, kDrainLimit);
-        for (unsigned i = used > kStages ? used - kStages : 0; i < used; ++i)
+      // what is in flight lands before the memory is given back, whoever gives up
+      bool landed = true;
+      for (int w = 0; w < 2; ++w)
+        if (q_used[w]) landed &= mbar_wait_bounded(&sm.q_full[w], (q_used[w] - 1) & 1, kDrainLimit);
+      if (tails) landed &= mbar_wait_bounded(&sm.tail, (tails - 1) & 1, kDrainLimit);
+      for (unsigned i = used > kStages ? used - kStages : 0; i < used; ++i)
+        if (i != kept)
           landed &= mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, kDrainLimit);
-        if (!landed && lane == 0) record_error(p.c.status, kDevErrDrainTimeout);
-      }
+      if (!landed && lane == 0) record_error(p.c.status, kDevErrDrainTimeout);
     } else {
       // -------------------------------------------------------------- MMAs
       // A warp per query tile: what one waits for passes under what the other

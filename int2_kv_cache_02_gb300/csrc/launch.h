@@ -239,6 +239,11 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
 // records kDevErrWaitTimeout in *status (self-test of the bounded waits).
 cudaError_t launch_wait_timeout_selftest(unsigned* status, unsigned iterations, cudaStream_t s);
 
+// The same of the tensor-core kernels' waits: report[0]: a wait gave up,
+// report[1]: another warp's followed, report[2]: one did while a warp was busy.
+cudaError_t launch_tc_wait_timeout_selftest(unsigned* status, unsigned iterations, int* report,
+                                            cudaStream_t s);
+
 // Log-sum-exp combine of n_parts partial records per (b, q-head).
 cudaError_t launch_combine(const float* ws, float* out, int n_rows, int n_parts, cudaStream_t s);
 

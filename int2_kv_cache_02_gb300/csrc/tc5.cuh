@@ -131,19 +131,23 @@ constexpr int kTcBusy = 2;
 // another warp has, and then says so in *state (the count of busy warps may be
 // lost then; bit 0 stays).  The limit counts from when no warp is busy.  (Polls
 // are counted and no clock is read: the waits are inlined many times over, and
-// the kernels' time goes by their code's size.)
-__device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* state) {
+// the kernels' time goes by their code's size.)  One thread or a whole warp; a
+// warp's lanes get one answer, which what follows relies on: the last look is
+// theirs together, and sees what any of them has seen before.  (A vote on the
+// way that does not give up costs the 8K prompt 2 %, accumulated weight 3 %.)
+__device__ __forceinline__ bool tc5_wait(uint64_t* bar, unsigned parity, volatile int* state,
+                                         unsigned limit = kTcWaitLimit) {
   if (mbar_test_wait(bar, parity)) return true;
   unsigned i = 0;
   do {
     if (mbar_try_wait(bar, parity)) return true;
     const int x = *state;
-    if (x & 1) return false;
-    i = x ? 0 : i + 1;
-  } while (i < kTcWaitLimit);
+    i = x & 1 ? limit : x ? 0 : i + 1;
+  } while (i < limit);
   *state = 1;
-  return false;
+  return __any_sync(__activemask(), mbar_test_wait(bar, parity));
 }
+
 // 32 bytes to a 32-byte aligned address.
 __device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),

@@ -124,6 +124,7 @@ def _load() -> ctypes.CDLL:
         "oscar_kv16_evict_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int]),
         "oscar_device_status": (c_int, [c_void_p]),
         "oscar_selftest_wait_timeout": (c_int, [c_uint, c_void_p]),
+        "oscar_selftest_tc_wait_timeout": (c_int, [c_uint, c_void_p, c_void_p]),
         "oscar_selftest_kv16_decode_timeout": (c_int, [P16, c_void_p, c_int, c_int, c_void_p,
                                                        c_void_p, c_size_t, c_void_p]),
         "oscar_status_string": (ctypes.c_char_p, [c_int]),
@@ -669,6 +670,15 @@ def selftest_wait_timeout(iterations: int = 256, stream=None):
     gives up after `iterations` polls and sets the device status word."""
     _check(_lib.oscar_selftest_wait_timeout(iterations, _stream(stream)),
            "oscar_selftest_wait_timeout")
+
+
+def selftest_tc_wait_timeout(report: torch.Tensor, iterations: int = 256, stream=None):
+    """The same of the tensor-core kernels' waits; report (int32 [3]): a wait gave
+    up, another warp's followed it, one did while a warp was busy (1, 1, 0)."""
+    if report.dtype is not torch.int32 or report.numel() != 3:
+        raise ValueError("report: int32 [3]")
+    _check(_lib.oscar_selftest_tc_wait_timeout(iterations, _ptr(report), _stream(stream)),
+           "oscar_selftest_tc_wait_timeout")
 
 
 def selftest_kv16_decode_timeout(cache: KV16Cache, q: torch.Tensor, max_tok: int,

@@ -195,3 +195,15 @@ def test_decode_workspace_after_waits_run_out(L, lens, Hq, Hkv):
         assert L.device_status() == 7 and L.device_status() == 0
         assert (ws[:65536].view(torch.int32) == 0).all()
     run_decode(L, case, cache, Hq, ws=ws)
+
+
+def test_tensor_core_waits_run_out_together(L):
+    """A wait that gives up takes the other warps of its block with it, none does
+    while a warp is busy, and calls that use the same tensor memory are right after."""
+    for iterations in (1, 64, 1000):
+        report = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+        L.selftest_tc_wait_timeout(report, iterations)
+        assert L.device_status() == 7 and L.device_status() == 0
+        assert report.tolist() == [1, 1, 0]
+    case = R.Case([300, 200], 2, BF, seed=10, weights=True)
+    run_attention(L, case, case.cache(L), [300, 100], 8)

@@ -224,3 +224,10 @@ def test_decode_timeout_selftest_refusals(L):
     assert f(Hq=3) == UNSUPPORTED and f(o=P(FAKE + 0x6000008)) == ALIGNMENT
     assert f(w=None) == f(n=100) == WORKSPACE
     assert L.oscar_selftest_kv16_decode_timeout(None, x, 4, 64, out, ws, 1 << 30, None) == INVALID
+
+
+def test_tc_wait_selftest_refusals(L):
+    # rejected on the host before any device call: safe with or without a GPU
+    f = L.oscar_selftest_tc_wait_timeout
+    assert f(0, P(FAKE), None) == f((1 << 16) + 1, P(FAKE), None) == f(16, None, None) == INVALID
+    assert f(16, P(FAKE + 2), None) == ALIGNMENT
