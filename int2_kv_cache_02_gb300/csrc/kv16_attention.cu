@@ -31,10 +31,15 @@
 //
 // Softmax.  One pass, fp32, base 2.  A row's maximum is looked for only where it
 // has none yet, and where the probabilities of 64 keys on the old one sum to
-// more than 2^12: so the loop over scores takes no maximum at all, P stays in
-// the range of both 16-bit types, and O is seldom rescaled.  Probabilities are
-// rounded to the type of V for the product (half a step relative, as the output
-// itself); the sum is of the unrounded ones.
+// more than kMost: so the loop over scores takes no maximum at all, P stays in
+// the range of the type, and O is seldom rescaled.  Probabilities are rounded to
+// the type of V for the product (half a step relative, as the output itself);
+// the sum is of the unrounded ones.  fp16 has little range below 1 (2^-14 for
+// whole steps, 2^-24 in all) and a token may outweigh the others by more, so
+// there the largest score gives 2^7: whole steps down to 2^-21 of the largest
+// and something down to 2^-32.  What is left below the largest number, 65504, is
+// room to grow before O is rescaled: with 2^9 the window case below took 234 us,
+// with 2^8 228, with 2^7 or 2^6 215.
 //
 // Measured (GB300): 8K-token causal prompt, 32/8 heads, bf16: 330 us, 1.67
 // PFLOP/s, 0.86 of the measured bf16 burst rate; in a loop of seconds the power
@@ -73,7 +78,13 @@ constexpr int kStages = 5;
 constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
 constexpr int kHalf = 16384;
 constexpr int kKeyPages = 4;           // pages of a key tile
-constexpr float kMost = 4096.0f;       // sum of 64 probabilities that asks for a new maximum
+// The maximum in use lies kBelow (log2) under the largest score that it was taken
+// from, and a sum of 64 probabilities above kMost asks for a new one.
+template <class T>
+struct Range {
+  static constexpr float kBelow = T::kHalf ? 7.0f : 0.0f;
+  static constexpr float kMost = T::kHalf ? 65000.0f : 4096.0f;
+};
 constexpr uint32_t kO = 256;           // TMEM columns: S_w at 128 w, O_w at 256 + 128 w
 
 struct AttnParams {
@@ -167,6 +178,13 @@ __device__ __forceinline__ void store_row4(const AttnParams& p, long long row, i
                                            const float (&o)[4], float inv) {
   reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
       make_uint2(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv));
+}
+
+// log(sum exp) of a row: the sum as it is on the largest score, whose logarithm
+// is the small one.
+template <class T>
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return kv16_lse(m + Range<T>::kBelow, l * (T::kHalf ? 1.0f / 128.0f : 1.0f));
 }
 
 // Is a channel of O (or of the result) one to be worked again?  NaN is, and in
@@ -599,7 +617,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
               mx0 = fmaxf(mx0, fmaxf(s[e], s[e + 1]));
               mx1 = fmaxf(mx1, fmaxf(s[e + 2], s[e + 3]));
             }
-            const float mx = fmaxf(mx0, mx1) * p.scale;
+            const float mx = fmaxf(mx0, mx1) * p.scale - Range<T>::kBelow;
             const bool grow = mx > m;         // true where m is -inf and mx is not
             const bool worked = grow && m != -INFINITY;    // (else l and O are 0)
             const float a = worked ? fast_exp2(m - mx) : 1.0f;
@@ -628,7 +646,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           mask();
           if (__any_sync(0xffffffffu, m == -INFINITY)) raise();
           float sum = weigh(x);
-          if (__any_sync(0xffffffffu, sum > kMost)) {
+          if (__any_sync(0xffffffffu, sum > Range<T>::kMost)) {
             tc5_ld32(x, s_addr + 64 * i);
             tc5_ld32(x + 32, s_addr + 64 * i + 32);
             tc5_wait_ld();
@@ -701,7 +719,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       odd += odd1 + odd2 + odd3;
       if (valid) {
         if (p.splits > 1) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
-        else if (p.lse) p.lse[row] = kv16_lse(m, l);
+        else if (p.lse) p.lse[row] = row_lse<T>(m, l);
       }
       // rows with open channels, by the whole warp; the other warps' waits do not
       // run out meanwhile
@@ -751,7 +769,7 @@ __global__ void __launch_bounds__(128) kv16_join_kernel(const AttnParams p) {
     o[3] += a * v.w;
   }
   store_row4<T>(p, row, lane, o, L == 0.0f ? 0.0f : 1.0f / L);
-  if (p.lse && lane == 0) p.lse[row] = kv16_lse(M, L);
+  if (p.lse && lane == 0) p.lse[row] = row_lse<T>(M, L);
 }
 
 int sm_count() {

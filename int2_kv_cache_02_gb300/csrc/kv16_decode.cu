@@ -28,6 +28,10 @@
 // pass with the running maximum and sum in fp32 (log2 domain); probabilities
 // enter the product with V as the sum of two numbers of the cache's type (hi +
 // lo, 16 bits of mantissa and more), so the output is rounded once, at the end.
+// fp16's smallest number is 2^-24, so there the largest probability stands at
+// 2^14, not at 1: the two parts keep 16 bits down to 2^-30 of the largest and
+// something of a probability down to 2^-39 (a sink may outweigh every other
+// token by more than 2^24, and with a value near 0 leave them the output).
 //
 // The accumulated weights need the joined maximum and sum.  So the scores go to
 // the workspace (4 bytes per token and query head beside 512 per token and KV
@@ -65,6 +69,7 @@ namespace {
 constexpr int NW = 10;                   // warps of a CTA, each with a slot of its own
 constexpr int kSlotBytes = 4 * 4096;     // a page: K and V, two halves of 64 channels each
 constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many: one a warp
+constexpr float kBelow = 14.0f;          // fp16: the maximum in use is 2^14 below the largest
 constexpr int kORow = 136;               // floats of a head's output row in shared memory
 
 struct DecodeParams {
@@ -324,6 +329,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       for (int i = 0; i < 2; ++i) {
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        if (T::kHalf) mx[i] -= kBelow;
         grew |= mx[i] > m[i];
       }
       if (__any_sync(0xffffffffu, grew)) {

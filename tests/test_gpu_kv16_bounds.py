@@ -207,3 +207,54 @@ def test_tensor_core_waits_run_out_together(L):
         assert report.tolist() == [1, 1, 0]
     case = R.Case([300, 200], 2, BF, seed=10, weights=True)
     run_attention(L, case, case.cache(L), [300, 100], 8)
+
+
+# ------------------------------------------------ weights of very unequal size
+
+def far_bound(case, b, q, rel, flush, **kw):
+    """As R.attend, with the probabilities' rounding taken token by token: off by
+    `rel` of itself, or by `flush` of the row's largest where that is more."""
+    o, z, p, _, ztol, dmax = R.attend(case, b, q, **kw)
+    n, g = p.shape[2], q.shape[1] // case.Hkv
+    v = case.v[b].double().repeat_interleave(g, 0)[:, :n].abs()
+    each = torch.maximum(rel * p, flush * p.amax(-1, keepdim=True)) + (4 * dmax[..., None] + 2 * n * R.U32) * p
+    tol = R.U[case.dtype] * o.abs() + torch.einsum("qhn,hnd->qhd", each, v) + 2.0 ** -25
+    return o, z, tol, ztol
+
+
+# fp16: the prompt's probabilities stand at 2^7 (or more) where the largest is 1,
+# the decode's up to 2^14 and in two parts; half the smallest number is 2^-25
+FAR = {BF: (2.0 ** -8, 0.0, 2.0 ** -15, 0.0), FP: (2.0 ** -11, 2.0 ** -32, 2.0 ** -21, 2.0 ** -39)}
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("heavy", [0, 1500])
+@pytest.mark.parametrize("octaves", [20.0, 23.4, 24.4, 26.0])
+def test_one_token_far_heavier_than_the_rest(L, dtype, heavy, octaves):
+    """One token, with a value of zero as a sink has it, weighs 2^20 to 2^26 times
+    what any other does: the others still make the output."""
+    lens, news = [8192, 3001], [5, 1400]
+    case = R.Case(lens, 1, dtype, seed=4, factor=0.05)
+    e = torch.where(torch.rand(128, generator=case.gen) < 0.5, -1.0, 1.0)
+    size = (octaves * math.log(2) / (128 * R.SCALE)) ** 0.5
+    for b in range(2):
+        case.k[b][0, heavy] = (size * e).to(dtype)
+        case.v[b] = (case.v[b].float() * 0.25 + 1.0).to(dtype)
+        case.v[b][0, heavy] = 0.0
+    cache = case.cache(L)
+    case.normal = lambda n, h: (size * e).to(dtype).expand(n, h, 128).contiguous()
+    start, q, out, lse = attention_of(L, case, cache, news, 4)
+    rel, flush, rel2, flush2 = FAR[dtype]
+    for b in range(2):
+        rows = slice(start[b], start[b + 1])
+        o, z, tol, ztol = far_bound(case, b, q[rows], rel, flush)
+        R.assert_within(out[rows], o, tol, f"prompt {b}")
+        R.assert_within(lse[rows], z, ztol, f"lse {b}")
+    q1 = q[[start[1] - 1, start[2] - 1]]
+    one = torch.empty((2, 4, 128), dtype=dtype, device="cuda")
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, 4, cache.capacity))
+    L.kv16_decode_attention(cache, q1.cuda(), R.SCALE, cache.capacity, one, ws)
+    assert L.device_status() == 0
+    for b in range(2):
+        o, _, tol, _ = far_bound(case, b, q1[b:b + 1], rel2, flush2)
+        R.assert_within(one[b:b + 1], o, tol, f"decode {b}")
