@@ -619,7 +619,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             }
             const float mx = fmaxf(mx0, mx1) * p.scale - Range<T>::kBelow;
             const bool grow = mx > m;         // true where m is -inf and mx is not
-            const bool worked = grow && m != -INFINITY;    // (else l and O are 0)
+            const bool worked = valid && grow && m != -INFINITY;    // (else l and O are 0)
             const float a = worked ? fast_exp2(m - mx) : 1.0f;
             if (grow) m = mx;
             if (!__any_sync(0xffffffffu, worked)) return;
@@ -644,9 +644,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             }
           };
           mask();
-          if (__any_sync(0xffffffffu, m == -INFINITY)) raise();
+          // (rows past the tile's end have no say: they hold the next sequence's
+          // queries, or what was in shared memory)
+          if (__any_sync(0xffffffffu, valid && m == -INFINITY)) raise();
           float sum = weigh(x);
-          if (__any_sync(0xffffffffu, sum > Range<T>::kMost)) {
+          if (__any_sync(0xffffffffu, valid && sum > Range<T>::kMost)) {
             tc5_ld32(x, s_addr + 64 * i);
             tc5_ld32(x + 32, s_addr + 64 * i + 32);
             tc5_wait_ld();

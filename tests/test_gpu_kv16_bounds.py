@@ -258,3 +258,48 @@ def test_one_token_far_heavier_than_the_rest(L, dtype, heavy, octaves):
     for b in range(2):
         o, _, tol, _ = far_bound(case, b, q1[b:b + 1], rel2, flush2)
         R.assert_within(one[b:b + 1], o, tol, f"decode {b}")
+
+
+# ------------------------------------------------------------- the same bits
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("Hq", [3, 5, 6, 7, 12, 15])
+def test_prompt_bits_do_not_depend_on_what_memory_held(L, dtype, Hq):
+    """Groups that do not fill a tile's rows: the same call gives the same bits after
+    calls that leave NaN or large numbers in shared memory."""
+    case = R.Case([300, 90, 41], 1, dtype, seed=Hq)
+    cache, q = case.cache(L), case.normal(431, Hq).cuda()
+    fill = R.Case([64] * 320, 1, dtype, paged=False, slack=0, seed=1)
+    full, qf = fill.cache(L), fill.normal(320 * 64, 8).cuda()
+    got = []
+    for x in (0.0, math.nan, 300.0, math.inf):
+        other = torch.empty_like(qf)
+        ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(full, 8, qf.shape[0], 64))
+        L.kv16_attention(full, qf * x, i32(R.start_of([64] * 320)), R.SCALE, 64, other, ws)
+        out, lse = torch.empty_like(q), torch.empty((431, Hq), device="cuda")
+        ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, Hq, 431, 320))
+        L.kv16_attention(cache, q, i32([0, 300, 390, 431]), 3 * R.SCALE, 320, out, ws, lse=lse)
+        got.append((out, lse))
+    assert L.device_status() == 0
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("Hq", [1, 4, 7])
+def test_prompt_bits_do_not_depend_on_the_neighbours(L, dtype, Hq):
+    """A sequence's results are the same bits whatever the queries of the others."""
+    case = R.Case([300, 90, 41], 1, dtype, seed=Hq)
+    cache, q = case.cache(L), case.normal(431, Hq)
+    got = []
+    for x in (1.0, 100.0, math.nan):
+        mixed = q.clone()
+        mixed[:300] *= x
+        mixed[390:] *= x
+        out, lse = torch.empty((431, Hq, 128), dtype=dtype, device="cuda"), torch.empty((431, Hq), device="cuda")
+        ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, Hq, 431, 320))
+        L.kv16_attention(cache, mixed.cuda(), i32([0, 300, 390, 431]), 3 * R.SCALE, 320, out, ws, lse=lse)
+        got.append((out[300:390], lse[300:390]))
+    assert L.device_status() == 0
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
