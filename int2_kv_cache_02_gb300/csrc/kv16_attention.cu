@@ -64,6 +64,7 @@
 // leave (m, l, o[128]) records that a second kernel joins.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "kv16.cuh"
 #include "kv16_tma.h"
@@ -844,12 +845,12 @@ cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* o
   p.splits = attention_splits(c, q.Hq, q.total, q.max_tok, q.window, q.n_sink);
   if (tiles * c.Hkv * p.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
   p.tiles = (int)tiles;
-  // a negative scale becomes a negated Q in the product, so that the largest
-  // score is always the largest sum; a scale of 0 a scale too small to matter,
-  // so that a masked -inf stays one
   p.wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+  // a negative scale becomes a negated Q in the product, so that the largest
+  // score is always the largest sum; a scale of 0 the smallest number there is,
+  // so that a masked -inf stays one (times the largest score it is 5e-7)
   p.negate = q.scale_log2 < 0.0f;
-  p.scale = std::max(std::fabs(q.scale_log2), 1e-30f);
+  p.scale = std::max(std::fabs(q.scale_log2), std::numeric_limits<float>::denorm_min());
   return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);
 }
 

@@ -303,3 +303,33 @@ def test_prompt_bits_do_not_depend_on_the_neighbours(L, dtype, Hq):
     assert L.device_status() == 0
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("scale,size", [(0.0, 1e17), (1e-33, 1e16), (-3e-34, 1e16), (1e-38, 1e18), (1e-41, 1e18)])
+def test_scales_next_to_zero(L, scale, size):
+    """Scales down to the smallest numbers and to zero, with keys and queries so large
+    that they count (or, at zero, do not)."""
+    case = R.Case([200, 700], 1, BF, seed=7, factor=size, weights=True)
+    cache, start = case.cache(L), [0, 200, 400]
+    q = (case.normal(400, 4).float() * size).to(BF)
+    out, lse = torch.empty((400, 4, 128), dtype=BF, device="cuda"), torch.empty((400, 4), device="cuda")
+    ws = L.alloc_workspace(L.kv16_attention_workspace_bytes(cache, 4, 400, 704))
+    L.kv16_attention(cache, q.cuda(), i32(start), scale, 704, out, ws, lse=lse)
+    one = torch.empty((2, 4, 128), dtype=BF, device="cuda")
+    q1 = q[[199, 399]]
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, 4, 704))
+    L.kv16_decode_attention(cache, q1.cuda(), scale, 704, one, ws)
+    L.kv16_accumulate(cache, q.cuda(), lse, i32(start), scale, 704)
+    assert L.device_status() == 0
+    # the scale as the calls take it: a float, times log2(e) to a float
+    s32 = torch.tensor(scale, dtype=torch.float32)
+    s64 = float((s32 * torch.tensor(1.4426950408889634)).double()) / 1.4426950408889634
+    for b in range(2):
+        rows = slice(start[b], start[b + 1])
+        o, z, p, tol, ztol, dmax = R.attend(case, b, q[rows], scale=s64)
+        R.assert_within(out[rows], o, tol, f"out {b}")
+        R.assert_within(lse[rows], z, ztol, f"lse {b}")
+        R.assert_within(one[b:b + 1], o[-1:], tol[-1:], f"decode {b}")
+        w, t = R.weight_of(p, dmax, 4)
+        R.assert_within(R.tokens(cache, b, case.lens[b], "weight"), w + case.w[b].double(),
+                        t + 4 * float(ztol.max()) * w + 2 * R.U32, f"weight {b}")
