@@ -33,6 +33,11 @@
 // something of a probability down to 2^-39 (a sink may outweigh every other
 // token by more than 2^24, and with a value near 0 leave them the output).
 //
+// A probability whose second part is 0 or negative turns a visible infinity in V
+// into NaN.  A row with a channel that is NaN although its sum is a number is
+// therefore looked at again once it is joined: what its visible values hold in
+// that channel decides (settle_row).
+//
 // The accumulated weights need the joined maximum and sum.  So the scores go to
 // the workspace (4 bytes per token and query head beside 512 per token and KV
 // head) and a second launch turns them into probabilities.
@@ -180,15 +185,90 @@ __device__ __forceinline__ void write_out(const DecodeParams& p, const Row& r, i
   if (stats && pair == 0) p.stats[row] = make_float2(M, inv);
 }
 
+// What the values that a row sees hold in a channel.
+constexpr unsigned kSeenNan = 1, kSeenPlus = 2, kSeenMinus = 4, kOpen = 8;
+__device__ __forceinline__ unsigned seen_in(float x) {
+  return x != x ? kSeenNan : x == INFINITY ? kSeenPlus : x == -INFINITY ? kSeenMinus : 0u;
+}
+
+// The open channels (ch[c] & kOpen) of row r's written result, NaN so far, for
+// the heads whose sum is a number: infinite where the visible values hold
+// infinities of one sign and no NaN.  All threads; leaves ch at zero.  A CTA reads
+// the values alone, 16 tokens of every warp in flight, and stops early once every
+// open channel has met a NaN or both infinities.
+template <class T>
+__device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* ch,
+                                        const uint8_t* sum_nan) {
+  constexpr int kTokens = 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile unsigned* mine = ch + 4 * lane;
+  for (int x = r.r0 + warp; x < r.r1; x += NW) {
+    bool undecided = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned c = mine[i];
+      undecided |= (c & kOpen) && !(c & kSeenNan) && (c & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
+    }
+    if (!__any_sync(0xffffffffu, undecided)) break;
+    const int blk = r.sp.block(x - r.r0), row = kv16_block_row(p.c, r.b, r.h, blk);
+    if (row < 0) continue;
+    const unsigned see = __ballot_sync(
+        0xffffffffu, kv16_visible(blk * kPage + lane, r.at, p.q.window, p.q.n_sink));
+    unsigned f[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int t0 = 0; t0 < kPage; t0 += kTokens) {
+      uint2 v[kTokens];
+#pragma unroll
+      for (int u = 0; u < kTokens; ++u) {
+        v[u] = make_uint2(0u, 0u);
+        if ((see >> (t0 + u)) & 1u)
+          v[u] = reinterpret_cast<const uint2*>(p.c.v)[((long long)row + t0 + u) * 32 + lane];
+      }
+#pragma unroll
+      for (int u = 0; u < kTokens; ++u) {
+        const float2 a = T::unpack(v[u].x), b = T::unpack(v[u].y);
+        f[0] |= seen_in(a.x);
+        f[1] |= seen_in(a.y);
+        f[2] |= seen_in(b.x);
+        f[3] |= seen_in(b.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (f[i]) atomicOr(ch + 4 * lane + i, f[i]);
+  }
+  __syncthreads();
+  for (int i = tid; i < p.g * 64; i += NW * 32) {
+    const int head = i >> 6, pair = i & 63;
+    if (sum_nan[head]) continue;
+    uint32_t* o = reinterpret_cast<uint32_t*>(
+                      p.out + ((long long)r.b * p.q.Hq + r.h * p.g + head) * kD) + pair;
+    float2 v = T::unpack(*o);
+    auto settled = [&](float y, unsigned c) {
+      c &= kOpen | kSeenNan | kSeenPlus | kSeenMinus;
+      return y == y ? y : c == (kOpen | kSeenPlus) ? INFINITY : c == (kOpen | kSeenMinus) ? -INFINITY : y;
+    };
+    v.x = settled(v.x, ch[2 * pair]);
+    v.y = settled(v.y, ch[2 * pair + 1]);
+    *o = T::pack(v.x, v.y);
+  }
+  __syncthreads();
+  for (int i = tid; i < kD; i += NW * 32) ch[i] = 0u;
+  __syncthreads();
+}
+
 template <class T, bool ACC>
 __global__ void __launch_bounds__(NW * 32, 1)
 kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, const DecodeParams p) {
+                   const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[NW];
   __shared__ int scan[NW];
   __shared__ float sm_m[NW][kMaxGroup], sm_l[NW][kMaxGroup];
-  __shared__ int s_last;
+  __shared__ int s_last, s_open;
+  __shared__ unsigned s_ch[kD];            // of settle_row
+  __shared__ uint8_t s_nan[kMaxGroup];     // heads whose sum is NaN
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;   // swizzle atoms
   uint8_t* slot = smem + warp * kSlotBytes;
@@ -199,7 +279,9 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   if (tid == 0) {
     for (int w = 0; w < NW; ++w) mbar_init(&full[w], 1);
     mbar_fence_init();
+    s_open = 0;
   }
+  for (int i = tid; i < kD; i += NW * 32) s_ch[i] = 0u;
   const int line = line_up(p.c, p.q, first, scan, NW * 32, blockIdx.x == 0);
   // rows without visible tokens: zeros
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x)
@@ -439,6 +521,16 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     __syncthreads();
     const bool own_row = seg == r.r0 && seg_end == r.r1;
     const int c0 = r.r0 / per, c1 = (r.r1 - 1) / per;
+    // the row's result, and which of its channels are open
+    auto result = [&](int head, int pair, float M, float L, float a0, float a1) {
+      write_out<T>(p, r, head, pair, M, L, a0, a1, ACC);
+      if (pair == 0) s_nan[head] = L != L;
+      if (L == L && (a0 != a0 || a1 != a1)) {
+        if (a0 != a0) s_ch[2 * pair] = kOpen;
+        if (a1 != a1) s_ch[2 * pair + 1] = kOpen;
+        s_open = 1;
+      }
+    };
     float* rec0 = p.part + ((long long)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * p.g * kRecFloats;
     for (int i = tid; i < p.g * 64; i += NW * 32) {
       const int head = i >> 6, pair = i & 63;
@@ -454,7 +546,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         a1 += a * v.y;
       }
       if (own_row) {
-        write_out<T>(p, r, head, pair, M, L, a0, a1, ACC);
+        result(head, pair, M, L, a0, a1);
       } else {
         float* rec = rec0 + head * kRecFloats;
         if (pair == 0) *reinterpret_cast<float2*>(rec) = make_float2(M, L);
@@ -492,9 +584,15 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
             a0 += a * v.x;
             a1 += a * v.y;
           }
-          write_out<T>(p, r, head, pair, M, L, a0, a1, ACC);
+          result(head, pair, M, L, a0, a1);
         }
+        __syncthreads();
       }
+    }
+    if (s_open) {
+      settle_row<T>(p, r, s_ch, s_nan);
+      if (tid == 0) s_open = 0;
+      __syncthreads();
     }
     seg = seg_end;
   }

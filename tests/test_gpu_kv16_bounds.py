@@ -333,3 +333,56 @@ def test_scales_next_to_zero(L, scale, size):
         w, t = R.weight_of(p, dmax, 4)
         R.assert_within(R.tokens(cache, b, case.lens[b], "weight"), w + case.w[b].double(),
                         t + 4 * float(ztol.max()) * w + 2 * R.U32, f"weight {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([700, 900, 40], 6, 2), ([9000, 20000, 1], 8, 2), ([700, 900, 40], 16, 1)])
+def test_decode_of_values_that_are_not_finite(L, dtype, accumulate, lens, Hq, Hkv):
+    """Infinite and NaN values that a query sees reach its output as they are: the
+    infinity, NaN for a NaN or infinities of both signs; every other channel, row
+    and weight as without them."""
+    case = R.Case(lens, Hkv, dtype, seed=5, weights=True)
+    cache, h = case.cache(L), Hkv - 1
+    want = {3: math.inf, 4: -math.inf, 70: math.nan, 71: math.nan, 127: math.inf, 0: -math.inf}
+    n = lens[1]
+    for t, ch, x in ((2, 3, math.inf), (n - 1, 4, -math.inf), (n // 2, 70, math.nan), (40, 71, math.inf),
+                     (n - 40, 71, -math.inf), (50, 127, math.inf), (n - 2, 127, math.inf), (n // 3, 0, -math.inf)):
+        poke(case, cache, 1, t, v=x, channel=ch, head=h)
+    # (each channel's token also as the one whose probability is the largest)
+    q = case.normal(3, Hq)
+    g = Hq // Hkv
+    for i, t in enumerate((2, n - 1, n // 2, 40, 50, n // 3)[:g]):
+        q[1, h * g + i] = (3 * case.k[1][h, t].float()).to(dtype)
+    out = torch.empty((3, Hq, 128), dtype=dtype, device="cuda")
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, Hq, cache.capacity, 0, 0, accumulate))
+    L.kv16_decode_attention(cache, q.cuda(), R.SCALE, cache.capacity, out, ws, accumulate=accumulate)
+    assert L.device_status() == 0 and (ws[:65536].view(torch.int32) == 0).all()
+    out = out.cpu()
+    for b in range(3):
+        o, _, p, tol, _, dmax = R.attend(case, b, q[b:b + 1])
+        if b == 1:
+            for ch, x in want.items():
+                got = out[1, h * g:, ch].float()
+                assert torch.isnan(got).all() if math.isnan(x) else (got == x).all(), ch
+                out[1, h * g:, ch] = o[0, h * g:, ch].to(dtype)
+        R.assert_within(out[b:b + 1], o, tol, f"out {b}")
+        if accumulate:
+            w, t = R.weight_of(p, dmax, g)
+            R.assert_within(R.tokens(cache, b, lens[b], "weight"), w + case.w[b].double(),
+                            t + 2 * R.U32 * case.w[b].double(), f"weight {b}")
+
+
+def test_decode_nan_score_beside_infinite_values(L):
+    """A row whose scores hold a NaN is NaN in every channel, infinite values or not."""
+    case = R.Case([500, 300], 1, BF, seed=6)
+    cache = case.cache(L)
+    poke(case, cache, 0, 9, k=math.nan)
+    poke(case, cache, 0, 70, v=math.inf, channel=5)
+    out = torch.empty((2, 4, 128), dtype=BF, device="cuda")
+    q = case.normal(2, 4)
+    ws = L.alloc_workspace(L.kv16_decode_workspace_bytes(cache, 4, cache.capacity))
+    L.kv16_decode_attention(cache, q.cuda(), R.SCALE, cache.capacity, out, ws)
+    assert torch.isnan(out[0]).all() and L.device_status() == 0
+    o, _, _, tol, _, _ = R.attend(case, 1, q[1:])
+    R.assert_within(out[1:], o, tol, "the other row")
