@@ -255,7 +255,7 @@ class _PagePool:
         for j in range(n_blocks):
             if row[j] < 0:
                 if not self._free:
-                    raise OscarError(4, "PagedKVCache.map_blocks: page pool exhausted")
+                    raise OscarError(4, f"{type(self).__name__}.map_blocks: page pool exhausted")
                 row[j] = self._free.pop(0)
         self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
 

@@ -231,3 +231,19 @@ def test_tc_wait_selftest_refusals(L):
     f = L.oscar_selftest_tc_wait_timeout
     assert f(0, P(FAKE), None) == f((1 << 16) + 1, P(FAKE), None) == f(16, None, None) == INVALID
     assert f(16, P(FAKE + 2), None) == ALIGNMENT
+
+
+def pool_of(kind, B=2, blocks=4, pages=6):
+    from int2_kv_cache_02_gb300 import oscar as O
+    p = object.__new__(getattr(O, kind))
+    p.block_table = torch.full((B, blocks), -1, dtype=torch.int32)
+    p._init_pool(B, blocks, pages)
+    return p
+
+
+@pytest.mark.parametrize("kind", ["PagedKVCache", "PagedKV16Cache"])
+def test_an_empty_pool_names_its_cache(kind):
+    from int2_kv_cache_02_gb300 import oscar as O
+    p = pool_of(kind, pages=1)
+    with pytest.raises(O.OscarError, match=f"^{kind}.map_blocks: page pool exhausted"):
+        p.map_blocks(0, 2)
