@@ -247,16 +247,17 @@ class _PagePool:
     def map_blocks(self, b: int, n_blocks: int, order=None):
         """Gives sequence b pages for its logical blocks 0..n_blocks-1 (those
         not mapped yet), taking free pages in `order` (a permutation of page
-        ids, for tests) or in pool order."""
+        ids, for tests) or in pool order.  A pool with too few of them gives
+        none."""
+        row = self._table_host[b]
+        missing = [j for j in range(n_blocks) if row[j] < 0]
+        if len(missing) > len(self._free):
+            raise OscarError(4, f"{type(self).__name__}.map_blocks: page pool exhausted")
         if order is not None:
             free = set(self._free)
             self._free = [p for p in order if p in free]
-        row = self._table_host[b]
-        for j in range(n_blocks):
-            if row[j] < 0:
-                if not self._free:
-                    raise OscarError(4, f"{type(self).__name__}.map_blocks: page pool exhausted")
-                row[j] = self._free.pop(0)
+        for j in missing:
+            row[j] = self._free.pop(0)
         self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
 
     def page_of(self, b: int, block: int) -> int:

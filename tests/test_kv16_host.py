@@ -247,3 +247,18 @@ def test_an_empty_pool_names_its_cache(kind):
     p = pool_of(kind, pages=1)
     with pytest.raises(O.OscarError, match=f"^{kind}.map_blocks: page pool exhausted"):
         p.map_blocks(0, 2)
+
+
+@pytest.mark.parametrize("kind", ["PagedKVCache", "PagedKV16Cache"])
+def test_a_pool_with_too_few_pages_gives_none(kind):
+    """The pages stay free and the host's table stays the device's."""
+    from int2_kv_cache_02_gb300 import oscar as O
+    p = pool_of(kind)
+    p.map_blocks(0, 3)
+    for n in (4, 5):                            # more than are free, more than a row has
+        with pytest.raises((O.OscarError, IndexError)):
+            p.map_blocks(1, n)
+        assert p._free == [3, 4, 5] and p.block_table[1].tolist() == [-1] * 4
+        assert [p.page_of(1, j) for j in range(4)] == [-1] * 4
+    p.map_blocks(1, 3)
+    assert p.block_table.tolist() == [[0, 1, 2, -1], [3, 4, 5, -1]]
