@@ -476,6 +476,9 @@ oscar_status oscar_paged_decode_attention(const oscar_paged_cache* c, const floa
  * access and is recorded in the status word (oscar_device_status); what the
  * call writes for that sequence is then unspecified, but stays within the
  * sequence's own rows.
+ *
+ * The device that is current is the one that a call runs on and that a
+ * workspace's size is planned for: that of the cache's memory.
  * ----------------------------------------------------------------------
  */
 #define OSCAR_KV16_BF16 0

@@ -554,6 +554,14 @@ def bf16_decode_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, B: 
 
 # ---- the 16-bit cache ------------------------------------------------------
 
+def _on_device(cache: KV16Cache, fn, args):
+    """Calls the library with the cache's device current."""
+    if torch._C._cuda_getDevice() == cache._index:
+        return fn(*args)
+    with torch.cuda.device(cache.device):
+        return fn(*args)
+
+
 def _kv16_call(cache: KV16Cache, where: str, fn, args, stream):
     """Calls the library with the cache's device current, on `stream` or that
     device's current stream."""
@@ -561,11 +569,7 @@ def _kv16_call(cache: KV16Cache, where: str, fn, args, stream):
         raw = torch._C._cuda_getCurrentRawStream(cache._index)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == cache._index:
-        st = fn(*args, raw)
-    else:
-        with torch.cuda.device(cache.device):
-            st = fn(*args, raw)
+    st = _on_device(cache, fn, (*args, raw))
     if st != 0:
         raise OscarError(st, where)
 
@@ -590,8 +594,8 @@ def kv16_write(cache: KV16Cache, k_new: torch.Tensor, v_new: torch.Tensor, start
 
 def kv16_attention_workspace_bytes(cache: KV16Cache, Hq: int, total: int, max_tok: int,
                                    window: int = 0, n_sink: int = 0) -> int:
-    return int(_lib.oscar_kv16_attention_workspace_bytes(cache._ref, Hq, total, max_tok, window,
-                                                         n_sink))
+    return int(_on_device(cache, _lib.oscar_kv16_attention_workspace_bytes,
+                          (cache._ref, Hq, total, max_tok, window, n_sink)))
 
 
 def kv16_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor, softmax_scale: float,
@@ -614,8 +618,8 @@ def kv16_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor, softm
 
 def kv16_decode_workspace_bytes(cache: KV16Cache, Hq: int, max_tok: int, window: int = 0,
                                 n_sink: int = 0, accumulate: bool = False) -> int:
-    return int(_lib.oscar_kv16_decode_workspace_bytes(cache._ref, Hq, max_tok, window, n_sink,
-                                                      int(accumulate)))
+    return int(_on_device(cache, _lib.oscar_kv16_decode_workspace_bytes,
+                          (cache._ref, Hq, max_tok, window, n_sink, int(accumulate))))
 
 
 def kv16_decode_attention(cache: KV16Cache, q: torch.Tensor, softmax_scale: float, max_tok: int,
@@ -646,8 +650,8 @@ def kv16_accumulate(cache: KV16Cache, q: torch.Tensor, lse: torch.Tensor, start:
 
 def kv16_evict_workspace_bytes(src: KV16Cache, max_tok: int, keep_first: int, keep_recent: int,
                                keep_top: int) -> int:
-    return int(_lib.oscar_kv16_evict_workspace_bytes(src._ref, max_tok, keep_first, keep_recent,
-                                                     keep_top))
+    return int(_on_device(src, _lib.oscar_kv16_evict_workspace_bytes,
+                          (src._ref, max_tok, keep_first, keep_recent, keep_top)))
 
 
 def kv16_evict(src: KV16Cache, dst: KV16Cache, max_tok: int, keep_first: int, keep_recent: int,

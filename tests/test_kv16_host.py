@@ -262,3 +262,38 @@ def test_a_pool_with_too_few_pages_gives_none(kind):
         assert [p.page_of(1, j) for j in range(4)] == [-1] * 4
     p.map_blocks(1, 3)
     assert p.block_table.tolist() == [[0, 1, 2, -1], [3, 4, 5, -1]]
+
+
+def test_calls_and_sizes_use_the_cache_device(monkeypatch):
+    """Every call, those that plan a workspace too, runs with the cache's device
+    current and leaves the caller's as it was."""
+    import types
+    from int2_kv_cache_02_gb300 import oscar as O
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.to = torch.device(d).index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.to
+
+        def __exit__(self, *_):
+            now[0] = self.was
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, now[0])) or 0
+
+    monkeypatch.setattr(O, "_lib", Lib())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for index in (0, 1):
+        cache = types.SimpleNamespace(_ref=None, _index=index, device=torch.device("cuda", index))
+        O.kv16_attention_workspace_bytes(cache, 4, 4, 64)
+        O.kv16_decode_workspace_bytes(cache, 4, 64)
+        O.kv16_evict_workspace_bytes(cache, 64, 1, 1, 1)
+        O._kv16_call(cache, "call", O._lib.call, (), None)
+        assert len(seen) == 4 and all(d == index for _, d in seen) and now == [0]
+        seen.clear()
