@@ -386,3 +386,54 @@ def test_decode_nan_score_beside_infinite_values(L):
     assert torch.isnan(out[0]).all() and L.device_status() == 0
     o, _, _, tol, _, _ = R.attend(case, 1, q[1:])
     R.assert_within(out[1:], o, tol, "the other row")
+
+
+# ----------------------------------------------------- rows too long to hold
+
+def test_evict_rows_too_long_to_hold(L):
+    """A capacity beyond what a cluster's shared memory holds (8 times 48K tokens):
+    the weights are read again in every pass.  Rows of a few thousand tokens, one
+    over many pages of the table, with NaN, infinite and equal weights."""
+    blocks = 13000
+    lens = [5000, 4000, 300, 0, 20000]
+    case = R.Case(lens, 2, BF, seed=11, weights=True)
+    for b in (0, 1, 4):
+        w = torch.round(case.w[b] * 4) / 4
+        w[0, 700:720] = math.nan
+        w[1, 30], w[1, 31] = math.inf, -math.inf
+        case.w[b] = w
+    case.w[1][:] = 0.25
+    small = case.cache(L)
+    table = torch.full((5, blocks), -1, dtype=torch.int32, device="cuda")
+    table[:, :small.block_table.shape[1]] = small.block_table
+    src = L.KV16Cache(small.k, small.v, small.n_tok, block_table=table, weight=small.weight)
+    assert src.capacity > 8 * 48 * 1024
+    for first, recent, top in ((4, 100, 400), (0, 0, 1), (40, 60, 3000)):
+        keep = first + recent + top
+        dst = R.Case([keep] * 5, 2, BF, seed=1, weights=True).cache(L, [0] * 5)
+        ws = L.alloc_workspace(L.kv16_evict_workspace_bytes(src, src.capacity, first, recent, top))
+        kept = torch.full((5, 2, keep), 9, dtype=torch.int32, device="cuda")
+        L.kv16_evict(src, dst, src.capacity, first, recent, top, ws, kept=kept)
+        assert L.device_status() == 0
+        assert dst.n_tok.tolist() == [min(n, keep) for n in lens]
+        for b, n in enumerate(lens):
+            m = min(n, keep)
+            for h in range(2):
+                want = R.evicted(case.w[b][h].numpy(), n, first, recent, top)
+                assert kept[b, h].tolist() == want + [-1] * (keep - m)
+                assert torch.equal(R.tokens(dst, b, m, "k")[h], case.k[b][h][want])
+                assert torch.equal(R.tokens(dst, b, m, "v")[h], case.v[b][h][want])
+
+
+def test_evict_rows_over_a_cluster_keep_the_status_clean(L):
+    """Rows of 70000 tokens, held by a cluster: the right tokens and no error."""
+    n = 70000
+    case = R.Case([n, n - 31], 1, BF, seed=2, weights=True)
+    src = case.cache(L)
+    dst = R.Case([2000, 2000], 1, BF, seed=1, weights=False).cache(L)
+    ws = L.alloc_workspace(L.kv16_evict_workspace_bytes(src, n, 4, 100, 1896))
+    kept = torch.empty((2, 1, 2000), dtype=torch.int32, device="cuda")
+    L.kv16_evict(src, dst, n, 4, 100, 1896, ws, kept=kept)
+    assert L.device_status() == 0
+    for b in range(2):
+        assert kept[b, 0].tolist() == R.evicted(case.w[b][0].numpy(), case.lens[b], 4, 100, 1896)
