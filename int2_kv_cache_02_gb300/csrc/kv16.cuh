@@ -57,13 +57,14 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* start, int B, int 
 // channels 4 lane .. 4 lane + 3.  fp32 throughout; a token that the query
 // does not see is not touched, whatever its key and value hold.  Ends early,
 // with m and l not complete, once every channel that `open` (a bit for each of
-// the lane's four) asks for is NaN: nothing changes it any more.
+// the lane's four) asks for is NaN: nothing changes it any more.  The block that
+// it ended with, or -1.
 constexpr int kRowTokens = 8;    // tokens whose loads are in flight together
 template <class T>
-__device__ __forceinline__ void kv16_warp_row(const Kv16& c, const uint16_t* q, int b, int h,
-                                              int at, const Span& sp, int i0, int i1, int window,
-                                              int n_sink, float scale_log2, unsigned open,
-                                              float& m, float& l, float (&o)[4]) {
+__device__ __forceinline__ int kv16_warp_row(const Kv16& c, const uint16_t* q, int b, int h,
+                                             int at, const Span& sp, int i0, int i1, int window,
+                                             int n_sink, float scale_log2, unsigned open,
+                                             float& m, float& l, float (&o)[4]) {
   const int lane = threadIdx.x & 31;
   const uint2 qr = reinterpret_cast<const uint2*>(q)[lane];
   const float2 q0 = T::unpack(qr.x), q1 = T::unpack(qr.y);
@@ -128,8 +129,9 @@ __device__ __forceinline__ void kv16_warp_row(const Kv16& c, const uint16_t* q, 
     bool settled = true;
 #pragma unroll
     for (int x = 0; x < 4; ++x) settled &= !((open >> x) & 1u) || o[x] != o[x];
-    if (__all_sync(0xffffffffu, settled)) return;
+    if (__all_sync(0xffffffffu, settled)) return i;
   }
+  return -1;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -56,8 +56,9 @@
 // longer than the bounded waits allow, so they do not run out while a warp says
 // that it is at it.  A sum that is NaN has met a visible score that is NaN or
 // +inf: the whole row is NaN and stays so.  (An 8K prompt, 32/8 heads, 0.36 ms:
-// with a NaN in a key the same, in its first value 1.1 ms, in its middle one 41;
-// bf16 with an infinity in the first value 70.  Done after the last item instead,
+// with a NaN in a key the same, in its first value 1.1 ms, in its middle one 10,
+// in its last, hidden from the rest of its tile, 21; bf16 with an infinity in the
+// first value 71.  Done after the last item instead,
 // in line or out of line, it cost every prompt 2 to 5 %: the loop's registers.)
 //
 // Few tiles over a long cache: the key tiles are split over several CTAs, which
@@ -122,6 +123,7 @@ struct Smem {
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int state;           // of the waits
+  int met[kSoftmaxWarps];
   Item item[kItems];
 };
 constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: all but one
@@ -208,10 +210,12 @@ __device__ __forceinline__ float gather_open(float x, float so_far) {
 }
 
 // Row `row` of a work item, position `at`, whose results this warp has just
-// written: its open channels again, from the tokens alone that it sees.
+// written: its open channels again, from the tokens alone that it sees.  *met is
+// the block in which such a row of this warp has last met its NaN: the others
+// most likely meet it there too, so they look there first.
 template <class T>
 __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int split, int k0,
-                                         int k1, const Span& sp, long long row, int at) {
+                                         int k1, const Span& sp, long long row, int at, int* met) {
   const int lane = threadIdx.x & 31;
   float* rec = p.part + (row * p.splits + split) * kRecFloats;
   uint2* out = reinterpret_cast<uint2*>(p.out + row * kD) + lane;
@@ -232,9 +236,18 @@ __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int 
   const long long token = row / p.q.Hq;
   const int head = (int)(row - token * p.q.Hq);
   float m, l, o[4];
-  kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)head * kD, b, h, at, sp,
-                   k0 * kKeyPages, min(k1 * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
-                   p.q.scale_log2, open, m, l, o);
+  const int i0 = k0 * kKeyPages, i1 = min(k1 * kKeyPages, sp.blocks), there = *met;
+#pragma unroll 1
+  for (int look = there >= i0 && there < i1 ? 0 : 1; look < 2; ++look) {
+    const int i = kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)head * kD, b, h,
+                                   at, sp, look ? i0 : there, look ? i1 : there + 1, p.q.window,
+                                   p.q.n_sink, p.q.scale_log2, open, m, l, o);
+    if (i < 0) continue;
+    __syncwarp();
+    if (lane == 0) *met = i;
+    __syncwarp();
+    break;
+  }
   // a record's channels stand on the record's maximum
   float f = l == 0.0f ? 0.0f : 1.0f / l;
   if (p.splits > 1) {
@@ -289,6 +302,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     mbar_init(&sm.tail, 1);
     mbar_fence_init();
     sm.state = 0;
+    for (int i = 0; i < kSoftmaxWarps; ++i) sm.met[i] = -1;
   }
   tc5_fence_before();
   __syncthreads();
@@ -733,7 +747,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         for (; bad; bad &= bad - 1) {
           const int src = __ffs(bad) - 1;
           redo_row<T>(p, b, h, split, k0, k1, sp, __shfl_sync(0xffffffffu, row, src),
-                      __shfl_sync(0xffffffffu, at, src));
+                      __shfl_sync(0xffffffffu, at, src), &sm.met[warp]);
         }
         if (lane == 0) atomicAdd(&sm.state, -kTcBusy);
       }
