@@ -470,6 +470,9 @@ oscar_status oscar_paged_decode_attention(const oscar_paged_cache* c, const floa
  * Visibility.  A query at position p sees the tokens j <= p with
  * window == 0, or j > p - window, or j < n_sink.  Tokens that a query does
  * not see do not reach its output, whatever they hold (NaN, infinity).
+ * What it sees does: a score that is NaN or +infinity makes the whole row NaN,
+ * a value its own channel alone (NaN as NaN; infinities of one sign as that
+ * infinity, of both as NaN).
  *
  * The device checks lengths (n_tok[b] in [0, capacity], and <= the host's
  * max_tok where a call takes it), start and page ids: a bad one skips the
@@ -525,8 +528,9 @@ oscar_status oscar_kv16_write(const oscar_kv16_cache* c, const uint16_t* k_new,
  *       several blocks when there are few queries
  * out and lse share no memory with q (rows and the gaps between them).
  * window >= 0, n_sink >= 0.  workspace: oscar_kv16_attention_workspace_bytes
- * of device memory (no initialisation; NULL if that is 0).  Calls that use
- * one workspace must not overlap on the GPU.
+ * of device memory (no initialisation; NULL if that is 0), asked for with this
+ * call's numbers: fewer queries may need more, since their caches are split.
+ * Calls that use one workspace must not overlap on the GPU.
  */
 oscar_status oscar_kv16_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                   long long q_stride, const int32_t* start, int total, int Hq,

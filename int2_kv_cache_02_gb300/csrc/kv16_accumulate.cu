@@ -24,8 +24,8 @@
 // S^T for each warpgroup.
 //
 // Measured (GB300): the last 128 queries of four 7K to 16K-token sequences, 32/8
-// heads, 66 us (floor 27); all queries of two prompts of 4K tokens, 32/4
-// heads, 128 us (floor 68).  Bound by the summing warps: 525 cycles of
+// heads, 65 us (floor 27); all queries of two prompts of 4K tokens, 32/4
+// heads, 129 us (floor 68).  Bound by the summing warps: 525 cycles of
 // exponentials per tile of S^T on each quarter of an SM, 950 with the waits, the
 // loads from TMEM and those of lse, against 512 of the tensor cores.  Four
 // warpgroups with a buffer each were slower (148 us), as was fetching the next

@@ -41,11 +41,11 @@
 // room to grow before O is rescaled: with 2^9 the window case below took 234 us,
 // with 2^8 228, with 2^7 or 2^6 215.
 //
-// Measured (GB300): 8K-token causal prompt, 32/8 heads, bf16: 330 us, 1.67
-// PFLOP/s, 0.86 of the measured bf16 burst rate; in a loop of seconds the power
-// limit is reached and it takes 362 us (0.89 of the sustained rate).  Four
+// Measured (GB300): 8K-token causal prompt, 32/8 heads, bf16: 333 us, 1.65
+// PFLOP/s, 0.85 of the measured bf16 burst rate; in a loop of seconds the power
+// limit is reached and it takes 363 us (0.89 of the sustained rate).  Four
 // sequences of 3K to 4K new tokens, window 1000 and 4 sinks, 32/4 heads, fp16:
-// 207 us against 119; each 32-token item spends 9 key tiles on 7.9 tiles' worth
+// 204 us against 119; each 32-token item spends 9 key tiles on 7.9 tiles' worth
 // of visible keys, and its first tile, masks and results (about 7 of 30
 // thousand cycles) leave the tensor cores idle.
 //
@@ -58,8 +58,8 @@
 // +inf: the whole row is NaN and stays so.  (An 8K prompt, 32/8 heads, 0.36 ms:
 // with a NaN in a key the same, in its first value 1.1 ms, in its middle one 10,
 // in its last, hidden from the rest of its tile, 21; bf16 with an infinity in the
-// first value 71.  Done after the last item instead,
-// in line or out of line, it cost every prompt 2 to 5 %: the loop's registers.)
+// first value 71.  Done after the last item instead, in line or out of line, it
+// cost every prompt 2 to 5 %: the loop's registers.)
 //
 // Few tiles over a long cache: the key tiles are split over several CTAs, which
 // leave (m, l, o[128]) records that a second kernel joins.

@@ -44,7 +44,7 @@
 //
 // Measured (GB300, copies run at 6.79 TB/s): batch 16 x 64K, 32/4 heads, even
 // lengths 314 us, 6.84 TB/s; lengths of 14K to 64K 198 us (floor 191), with
-// weights 218 + 21 us; batch 48 x 16K with a window of 4096, 32/8 heads, 129 us
+// weights 217 + 21 us; batch 48 x 16K with a window of 4096, 32/8 heads, 130 us
 // (floor 118: 129 pages a row leave three rows and their joins to a CTA); one
 // head and 1024 tokens 8.4 us, a chain of dependent loads: length, table, page,
 // records.
