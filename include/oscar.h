@@ -596,6 +596,116 @@ oscar_status oscar_kv16_evict(const oscar_kv16_cache* src, const oscar_kv16_cach
 size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok, int keep_first,
                                         int keep_recent, int keep_top);
 
+/*
+ * ----------------------------------------------------------------------
+ * Sequences with tokens in common.  oscar_kv16_fork makes them, the two
+ * attention calls read what they share once, oscar_page_compact and
+ * oscar_kv16_copy_pages tidy a pool.
+ * ----------------------------------------------------------------------
+ */
+
+/*
+ * oscar_kv16_decode_attention of sequences that share prefixes: the sequences
+ * group[i] .. group[i+1] - 1 are group i, whose first prefix[i] tokens are the
+ * same ones.  The prefix's whole pages (tokens below 32 * (prefix[i] / 32)) are
+ * read once for the group, from its first sequence's place in the cache: the
+ * others' table entries (contiguous: rows) for them are not used.  The rest of
+ * the prefix stands in every sequence's own pages, as oscar_kv16_fork leaves
+ * it.  A sequence in no group shares nothing, and one with fewer tokens than
+ * the prefix sees those that it has.
+ *  group   device int32 [n_groups + 1], not decreasing, within [0, B]
+ *  prefix  device int32 [n_groups], within [0, max_tok] and the capacity
+ *  q, out, positions and visibility are those of oscar_kv16_decode_attention
+ * A group out of range is recorded in the status word and shares nothing.
+ * workspace: a decode workspace (its header of OSCAR_DECODE_WS_HEADER_BYTES is
+ * zero before the first use and after every call) of
+ * oscar_kv16_shared_decode_workspace_bytes.  The limits of the decode call hold,
+ * and n_groups <= 4096 (else OSCAR_ERR_UNSUPPORTED).
+ */
+oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                                long long q_stride, int Hq, const int32_t* group,
+                                                const int32_t* prefix, int n_groups,
+                                                float softmax_scale, int max_tok, int window,
+                                                int n_sink, uint16_t* out, void* workspace,
+                                                size_t ws_bytes, void* stream);
+size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int Hq, int n_groups,
+                                                int max_tok, int window, int n_sink);
+
+/*
+ * oscar_kv16_attention of sequences that share prefixes, for the newest tokens
+ * of each: q, start, out, lse, positions and visibility as there, groups as
+ * above (a prefix may reach into the new tokens).  workspace: a decode
+ * workspace of oscar_kv16_shared_attention_workspace_bytes, asked for with this
+ * call's numbers.  B <= 4096 and n_groups <= 4096 (else OSCAR_ERR_UNSUPPORTED).
+ */
+oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                         long long q_stride, const int32_t* start, int total,
+                                         int Hq, const int32_t* group, const int32_t* prefix,
+                                         int n_groups, float softmax_scale, int max_tok,
+                                         int window, int n_sink, uint16_t* out, float* lse,
+                                         void* workspace, size_t ws_bytes, void* stream);
+size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, int n_groups,
+                                                   int total, int max_tok, int window, int n_sink);
+
+/*
+ * Makes sequence b of dst a continuation of sequence parent[b] of src: its
+ * tokens become the parent's, dst->n_tok[b] the parent's length n.
+ *  parent  device int32 [dst->B]; negative: sequence b of dst stays as it is
+ *  share 1 the whole pages are taken over by reference (dst's table entries
+ *          below n / 32 become the parent's: the call writes dst's
+ *          block_table) and the tokens behind them are copied; src and dst are
+ *          then paged and of one pool (the same k, v and n_pages)
+ *  share 0 every token is copied
+ *  max_tok host bound on the parents' lengths
+ * Tokens are copied to the pages (contiguous: rows) that dst's block table
+ * names, with their weights if dst has any (src then has them too).  No page
+ * that the call writes may be one that it reads, except that a block whose page
+ * is the parent's own is left as it is.  Shared pages share their weights.
+ * src and dst may be one cache: then a sequence that is forked from is not
+ * forked to by the same call, unless from itself, which changes nothing.
+ * Otherwise their lengths and tables lie apart, and their keys, values and
+ * weights too unless they are one pool's.  A parent, a length or a page out of
+ * range is recorded in the status word; what cannot be copied stays as it was.
+ */
+oscar_status oscar_kv16_fork(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
+                             const int32_t* parent, int share, int max_tok, void* stream);
+
+/*
+ * Plans the compaction of a page pool.  The L pages that the table names
+ * (negative entries name none) are to have the ids 0 .. L - 1: those that have
+ * such an id keep it, and the i-th lowest of the others moves to the i-th
+ * lowest id below L that no entry names.  Pages that several sequences share
+ * move once.  No page is copied here: oscar_kv16_copy_pages does that for every
+ * cache (every layer) that goes by this table.  For the pages of either cache.
+ *  new_table  [B][max_blocks], block_table with the new ids; may be block_table
+ *             itself, else apart from it
+ *  moves      device int32 [n_pages / 2][2], 8-byte aligned: (old, new) ids,
+ *             rising; (-1, -1) behind the last.  Old ids are >= L and new ones
+ *             < L, so the moves can be made in any order.
+ *  counts     device int32 [2]: the number of moves, L
+ * An entry of n_pages or more is recorded in the status word and stays as it is.
+ * workspace: oscar_page_compact_workspace_bytes (no initialisation).
+ * B * max_blocks < 2^31 - 128 (else OSCAR_ERR_UNSUPPORTED).
+ */
+oscar_status oscar_page_compact(const int32_t* block_table, int32_t* new_table, int B,
+                                int max_blocks, int n_pages, int32_t* moves, int32_t* counts,
+                                void* workspace, size_t ws_bytes, void* stream);
+size_t oscar_page_compact_workspace_bytes(int B, int max_blocks, int n_pages);
+
+/*
+ * Copies pages: keys, values and (if dst->weight is set) weights of src's page
+ * pairs[i][0] to dst's page pairs[i][1], for i below *n_pairs.
+ *  pairs    device int32 [max_pairs][2], 8-byte aligned
+ *  n_pairs  device int32, within [0, max_pairs] (else recorded in the status
+ *           word and nothing is copied)
+ * src and dst are paged, of one type and number of heads; they are one pool, in
+ * which no page is written twice or both written and read, or lie apart.  Pairs
+ * with a page out of range are skipped and recorded.
+ */
+oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
+                                   const int32_t* pairs, const int32_t* n_pairs, int max_pairs,
+                                   void* stream);
+
 /* Self-test of the bounded waits (failure detection; the pages have no
  * counterpart).  One CTA waits on an mbarrier that nothing arrives at,
  * gives up after `iterations` polls, records the wait-timeout bit in the

@@ -101,6 +101,15 @@ bool decode_size_ok(const oscar_kv16_cache* c, int max_tok) {
   return c->B <= kMaxDecodeBatch && rows <= kMaxDecodeRows && rows * blocks <= kMaxTokens;
 }
 
+// The key tiles of 128 tokens of all (query tile, KV head) rows are numbered in 32 bits.
+bool shared_size_ok(const oscar_kv16_cache* c, int Hq, int n_groups, int total, int max_tok) {
+  const long long two = 2 * (128 / (Hq / c->Hkv));
+  const long long rows = (total / two + n_groups) * c->Hkv;
+  const long long tiles = (std::min<long long>(max_tok, capacity(c)) + 127) / 128;
+  return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxTokens &&
+         rows <= kMaxTokens && rows * tiles <= kMaxTokens;
+}
+
 // -1 if the three counts are no valid budget.
 long long keep_of(int keep_first, int keep_recent, int keep_top) {
   if (keep_first < 0 || keep_recent < 0 || keep_top < 0) return -1;
@@ -111,6 +120,76 @@ long long keep_of(int keep_first, int keep_recent, int keep_top) {
 // The rows' counts, then the kept positions (where the caller takes none).
 size_t evict_ws_bytes(const oscar_kv16_cache* src, long long keep) {
   return (size_t)((long long)src->B * src->Hkv) * (size_t)(keep + 4) * sizeof(int32_t);
+}
+
+size_t table_bytes(long long B, long long max_blocks) { return (size_t)(B * max_blocks) * sizeof(int32_t); }
+
+// The memory of a cache: keys, values, weights, lengths, table.
+struct Extent {
+  Range r[5];
+};
+Extent extent(const oscar_kv16_cache* c) {
+  const size_t rows = cache_rows(c);
+  auto at = [](const void* p, size_t n) { return Range{static_cast<const char*>(p), n}; };
+  return Extent{{at(c->k, rows * kD * 2), at(c->v, rows * kD * 2), at(c->weight, rows * 4),
+                 at(c->n_tok, (size_t)c->B * 4),
+                 at(c->block_table, c->block_table ? table_bytes(c->B, c->max_blocks) : 0)}};
+}
+
+// Are the pages of a and b the same memory, page for page?
+bool same_pool(const oscar_kv16_cache* a, const oscar_kv16_cache* b) {
+  return a->block_table && b->block_table && a->k == b->k && a->v == b->v &&
+         a->n_pages == b->n_pages && (a->weight == b->weight || !b->weight);
+}
+
+// May a call copy tokens from src to dst?  They are of one kind, and their
+// keys, values and weights lie apart or are one pool's.
+oscar_status copy_ok(const oscar_kv16_cache* src, const oscar_kv16_cache* dst) {
+  if (src->Hkv != dst->Hkv || src->dtype != dst->dtype || (dst->weight && !src->weight))
+    return OSCAR_ERR_INVALID_ARG;
+  if (same_pool(src, dst)) return OSCAR_OK;
+  const Extent a = extent(src), b = extent(dst);
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlap(a.r[i], b.r[j])) return OSCAR_ERR_INVALID_ARG;
+  return OSCAR_OK;
+}
+
+bool groups_ok(const int32_t* group, const int32_t* prefix, int n) {
+  return n >= 1 && group && prefix;
+}
+
+oscar_status shared(const oscar_kv16_cache* c, const uint16_t* q, long long q_stride,
+                    const int32_t* start, int total, int Hq, const int32_t* group,
+                    const int32_t* prefix, int n_groups, float softmax_scale, int max_tok,
+                    int window, int n_sink, uint16_t* out, float* lse, void* workspace,
+                    size_t ws_bytes, void* stream) {
+  if (total < 0 || !groups_ok(group, prefix, n_groups) ||
+      !window_ok(softmax_scale, max_tok, window, n_sink))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!heads_ok(Hq, c->Hkv)) return OSCAR_ERR_UNSUPPORTED;
+  if ((total > 0 && (!q || !out)) || !stride_ok(q_stride, Hq)) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(start, 4) ||
+      !aligned(group, 4) || !aligned(prefix, 4))
+    return OSCAR_ERR_ALIGNMENT;
+  if (!shared_size_ok(c, Hq, n_groups, total, max_tok)) return OSCAR_ERR_UNSUPPORTED;
+  if (total == 0) return OSCAR_OK;
+  Kv16 v = view(c);
+  if (!workspace || ws_bytes < kv16_shared_ws_bytes(v, Hq, n_groups, total, max_tok, window, n_sink))
+    return OSCAR_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
+  const size_t heads = (size_t)total * Hq;
+  if (in_queries(out, heads * kD * sizeof(uint16_t), q, q_stride, total, Hq) ||
+      in_queries(lse, heads * sizeof(float), q, q_stride, total, Hq))
+    return OSCAR_ERR_INVALID_ARG;
+  v.status = device_status_word();
+  if (!v.status) return OSCAR_ERR_CUDA;
+  int launches = 0;
+  const cudaError_t e = launch_kv16_shared(
+      v, query(q, q_stride, start, total, Hq, softmax_scale, max_tok, window, n_sink),
+      Kv16Groups{group, prefix, n_groups}, out, lse, workspace, &launches, as_stream(stream));
+  count_launches(launches);
+  return from_cuda(e);
 }
 
 oscar_status decode(const oscar_kv16_cache* c, const uint16_t* q, long long q_stride, int Hq,
@@ -303,6 +382,136 @@ oscar_status oscar_kv16_evict(const oscar_kv16_cache* src, const oscar_kv16_cach
   const cudaError_t e = launch_kv16_evict(s, d, max_tok, keep_first, keep_recent, keep_top, kept,
                                           workspace, as_stream(stream));
   count_launches(2);
+  return from_cuda(e);
+}
+
+size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int Hq, int n_groups,
+                                                int max_tok, int window, int n_sink) {
+  if (check(c) != OSCAR_OK || !heads_ok(Hq, c->Hkv) || n_groups < 1 ||
+      !window_ok(0.0f, max_tok, window, n_sink) ||
+      !shared_size_ok(c, Hq, n_groups, c->B, max_tok) || !decode_size_ok(c, max_tok))
+    return 0;
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, 0, max_tok, window, n_sink);
+}
+
+oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                                long long q_stride, int Hq, const int32_t* group,
+                                                const int32_t* prefix, int n_groups,
+                                                float softmax_scale, int max_tok, int window,
+                                                int n_sink, uint16_t* out, void* workspace,
+                                                size_t ws_bytes, void* stream) {
+  const oscar_status st = check(c);
+  if (st != OSCAR_OK) return st;
+  if (max_tok >= 0 && !decode_size_ok(c, max_tok)) return OSCAR_ERR_UNSUPPORTED;
+  return shared(c, q, q_stride, nullptr, c->B, Hq, group, prefix, n_groups, softmax_scale, max_tok,
+                window, n_sink, out, nullptr, workspace, ws_bytes, stream);
+}
+
+size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, int n_groups,
+                                                   int total, int max_tok, int window, int n_sink) {
+  if (check(c) != OSCAR_OK || !heads_ok(Hq, c->Hkv) || n_groups < 1 || total <= 0 ||
+      !window_ok(0.0f, max_tok, window, n_sink) || !shared_size_ok(c, Hq, n_groups, total, max_tok))
+    return 0;
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, total, max_tok, window, n_sink);
+}
+
+oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,
+                                         long long q_stride, const int32_t* start, int total,
+                                         int Hq, const int32_t* group, const int32_t* prefix,
+                                         int n_groups, float softmax_scale, int max_tok,
+                                         int window, int n_sink, uint16_t* out, float* lse,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  const oscar_status st = check(c);
+  if (st != OSCAR_OK) return st;
+  if (!start) return OSCAR_ERR_INVALID_ARG;
+  return shared(c, q, q_stride, start, total, Hq, group, prefix, n_groups, softmax_scale, max_tok,
+                window, n_sink, out, lse, workspace, ws_bytes, stream);
+}
+
+oscar_status oscar_kv16_fork(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
+                             const int32_t* parent, int share, int max_tok, void* stream) {
+  oscar_status st = check(src);
+  if (st == OSCAR_OK) st = check(dst);
+  if (st != OSCAR_OK) return st;
+  if (!parent || (share != 0 && share != 1) || max_tok < 0) return OSCAR_ERR_INVALID_ARG;
+  if (!aligned(parent, 4)) return OSCAR_ERR_ALIGNMENT;
+  st = copy_ok(src, dst);
+  if (st != OSCAR_OK) return st;
+  if (share && !same_pool(src, dst)) return OSCAR_ERR_INVALID_ARG;
+  // one cache, or lengths and tables apart from each other's and from all that is read
+  const bool same = same_pool(src, dst) && src->n_tok == dst->n_tok &&
+                    src->block_table == dst->block_table && src->B == dst->B &&
+                    src->max_blocks == dst->max_blocks;
+  const Extent a = extent(src), b = extent(dst);
+  const Range par{reinterpret_cast<const char*>(parent), (size_t)dst->B * sizeof(int32_t)};
+  if (!same)
+    for (int i = 3; i < 5; ++i)
+      for (int j = 3; j < 5; ++j)
+        if (overlap(a.r[i], b.r[j])) return OSCAR_ERR_INVALID_ARG;
+  for (int j = 0; j < 5; ++j)
+    if (overlap(par, b.r[j])) return OSCAR_ERR_INVALID_ARG;
+  Kv16 s = view(src), d = view(dst);
+  s.status = d.status = device_status_word();
+  if (!s.status) return OSCAR_ERR_CUDA;
+  const cudaError_t e = launch_kv16_fork(s, d, parent, share != 0, same, max_tok, as_stream(stream));
+  count_launches(1);
+  return from_cuda(e);
+}
+
+oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
+                                   const int32_t* pairs, const int32_t* n_pairs, int max_pairs,
+                                   void* stream) {
+  oscar_status st = check(src);
+  if (st == OSCAR_OK) st = check(dst);
+  if (st != OSCAR_OK) return st;
+  if (!src->block_table || !dst->block_table || max_pairs < 0 || !n_pairs ||
+      (max_pairs > 0 && !pairs))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!aligned(pairs, 8) || !aligned(n_pairs, 4)) return OSCAR_ERR_ALIGNMENT;
+  st = copy_ok(src, dst);
+  if (st != OSCAR_OK || max_pairs == 0) return st;
+  Kv16 s = view(src), d = view(dst);
+  s.status = d.status = device_status_word();
+  if (!s.status) return OSCAR_ERR_CUDA;
+  const cudaError_t e = launch_kv16_copy_pages(s, d, pairs, n_pairs, max_pairs, as_stream(stream));
+  count_launches(1);
+  return from_cuda(e);
+}
+
+size_t oscar_page_compact_workspace_bytes(int B, int max_blocks, int n_pages) {
+  if (B <= 0 || max_blocks <= 0 || n_pages <= 0) return 0;
+  return page_compact_ws_bytes(n_pages);
+}
+
+oscar_status oscar_page_compact(const int32_t* block_table, int32_t* new_table, int B,
+                                int max_blocks, int n_pages, int32_t* moves, int32_t* counts,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  if (!block_table || !new_table || B <= 0 || max_blocks <= 0 || n_pages <= 0 || !counts ||
+      (n_pages > 1 && !moves))
+    return OSCAR_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(new_table, 4) || !aligned(moves, 8) ||
+      !aligned(counts, 4))
+    return OSCAR_ERR_ALIGNMENT;
+  const long long entries = (long long)B * max_blocks;
+  if (entries > kMaxTokens) return OSCAR_ERR_UNSUPPORTED;
+  const size_t tb = table_bytes(B, max_blocks);
+  const Range out[] = {{reinterpret_cast<const char*>(new_table), tb},
+                       {reinterpret_cast<const char*>(moves), (size_t)(n_pages / 2) * 8},
+                       {reinterpret_cast<const char*>(counts), 8}};
+  const Range in{reinterpret_cast<const char*>(block_table), tb};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(in, out[i]) && !(i == 0 && block_table == new_table)) return OSCAR_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return OSCAR_ERR_INVALID_ARG;
+  }
+  if (!workspace || ws_bytes < page_compact_ws_bytes(n_pages)) return OSCAR_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
+  unsigned* status = device_status_word();
+  if (!status) return OSCAR_ERR_CUDA;
+  int launches = 0;
+  const cudaError_t e = launch_page_compact(block_table, new_table, entries, n_pages, moves, counts,
+                                            workspace, status, &launches, as_stream(stream));
+  count_launches(launches);
   return from_cuda(e);
 }
 

@@ -36,6 +36,25 @@ struct Span {
     blocks = sink_blocks + end - w0;
   }
   KV16_BOTH int block(int i) const { return i < sink_blocks ? i : w0 + i - sink_blocks; }
+
+  // Of these blocks, those below n.
+  KV16_BOTH Span below(int n) const {
+    Span s;
+    s.sink_blocks = std::min(sink_blocks, n);
+    s.w0 = w0;
+    s.blocks = s.sink_blocks + std::max(0, std::min(w0 + blocks - sink_blocks, n) - w0);
+    return s;
+  }
+  // Those from n on; where n lies among the sinks', the blocks between them and
+  // the window's too (hidden ones: a span has one gap, behind block 0).
+  KV16_BOTH Span from(int n) const {
+    Span s;
+    const int end = w0 + blocks - sink_blocks;
+    s.sink_blocks = n > 0 ? 0 : sink_blocks;
+    s.w0 = n >= sink_blocks ? std::max(w0, n) : n > 0 ? n : w0;
+    s.blocks = s.sink_blocks + std::max(0, end - s.w0);
+    return s;
+  }
 };
 
 KV16_BOTH bool kv16_visible(int j, int at, int window, int n_sink) {

@@ -234,6 +234,27 @@ cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const floa
 cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int keep_first,
                               int keep_recent, int keep_top, int32_t* kept, void* ws,
                               cudaStream_t s);
+// Groups of sequences with a common prefix: group i is the sequences
+// [group[i], group[i+1]), whose first prefix[i] tokens are the same.
+struct Kv16Groups {
+  const int32_t* group;
+  const int32_t* prefix;
+  int n;
+};
+constexpr int kMaxGroups = 4096;        // groups of one call
+// q.start nullptr: the decode (lse nullptr).
+cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
+                               uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s);
+size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok, int window,
+                            int n_sink);
+cudaError_t launch_kv16_fork(const Kv16& src, const Kv16& dst, const int32_t* parent, bool share,
+                             bool same, int max_tok, cudaStream_t s);
+cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long long entries,
+                                int n_pages, int32_t* moves, int32_t* counts, void* ws,
+                                unsigned* status, int* launches, cudaStream_t s);
+size_t page_compact_ws_bytes(int n_pages);
+cudaError_t launch_kv16_copy_pages(const Kv16& src, const Kv16& dst, const int32_t* pairs,
+                                   const int32_t* n_pairs, int max_pairs, cudaStream_t s);
 
 // One CTA polls an mbarrier nothing arrives at, `iterations` times, then
 // records kDevErrWaitTimeout in *status (self-test of the bounded waits).

@@ -122,6 +122,23 @@ def _load() -> ctypes.CDLL:
         "oscar_kv16_evict": (c_int, [P16, P16, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
                                      c_size_t, c_void_p]),
         "oscar_kv16_evict_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int]),
+        "oscar_kv16_shared_decode_attention": (c_int, [P16, c_void_p, c_longlong, c_int, c_void_p,
+                                                       c_void_p, c_int, c_float, c_int, c_int,
+                                                       c_int, c_void_p, c_void_p, c_size_t,
+                                                       c_void_p]),
+        "oscar_kv16_shared_decode_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int,
+                                                                c_int]),
+        "oscar_kv16_shared_attention": (c_int, [P16, c_void_p, c_longlong, c_void_p, c_int, c_int,
+                                                c_void_p, c_void_p, c_int, c_float, c_int, c_int,
+                                                c_int, c_void_p, c_void_p, c_void_p, c_size_t,
+                                                c_void_p]),
+        "oscar_kv16_shared_attention_workspace_bytes": (c_size_t, [P16, c_int, c_int, c_int, c_int,
+                                                                   c_int, c_int]),
+        "oscar_kv16_fork": (c_int, [P16, P16, c_void_p, c_int, c_int, c_void_p]),
+        "oscar_page_compact": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
+                                       c_void_p, c_size_t, c_void_p]),
+        "oscar_page_compact_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+        "oscar_kv16_copy_pages": (c_int, [P16, P16, c_void_p, c_void_p, c_int, c_void_p]),
         "oscar_device_status": (c_int, [c_void_p]),
         "oscar_selftest_wait_timeout": (c_int, [c_uint, c_void_p]),
         "oscar_selftest_tc_wait_timeout": (c_int, [c_uint, c_void_p, c_void_p]),
@@ -237,11 +254,13 @@ class KVCache:
 
 
 class _PagePool:
-    """Host-side page allocator of the paged caches: which pages are free, and
-    the block table's host copy beside the device's (self.block_table)."""
+    """Host-side page allocator of the paged caches: which pages are free, how
+    many table entries name each of the others, and the block table's host copy
+    beside the device's (self.block_table)."""
 
     def _init_pool(self, B: int, max_blocks: int, n_pages: int):
         self._free = list(range(n_pages))
+        self._named = [0] * n_pages
         self._table_host = [[-1] * max_blocks for _ in range(B)]
 
     def map_blocks(self, b: int, n_blocks: int, order=None):
@@ -258,20 +277,62 @@ class _PagePool:
             self._free = [p for p in order if p in free]
         for j in missing:
             row[j] = self._free.pop(0)
+            self._named[row[j]] = 1
         self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
+
+    def share_blocks(self, b: int, parent: int, n_blocks: int):
+        """Lets sequence b's logical blocks 0..n_blocks-1 be the pages of sequence
+        parent's; those that b had there are given back.  Whole pages only: what
+        is written to a shared page reaches every sequence that has it."""
+        row, theirs = self._table_host[b], self._table_host[parent]
+        if not 0 <= n_blocks <= len(row) or any(p < 0 for p in theirs[:n_blocks]):
+            raise OscarError(1, f"{type(self).__name__}.share_blocks: sequence {parent} has no "
+                                f"{n_blocks} blocks")
+        for j in range(n_blocks):
+            if row[j] == theirs[j]:
+                continue
+            self._named[theirs[j]] += 1
+            self._give_back(row, j)
+            row[j] = theirs[j]
+        self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
+
+    def _give_back(self, row: list, j: int):
+        page, row[j] = row[j], -1
+        if page >= 0:
+            self._named[page] -= 1
+            if self._named[page] == 0:
+                self._free.append(page)
+
+    def compact(self):
+        """Gives the pages in use the lowest ids (page_compact): the table and the
+        allocator go by the new ids from here on.  Returns (moves, counts) for
+        the copies (kv16_copy_pages), which come next on the current stream."""
+        table, n_pages = self.block_table, len(self._named)
+        moves = torch.empty((n_pages // 2, 2), dtype=torch.int32, device=table.device)
+        counts = torch.empty(2, dtype=torch.int32, device=table.device)
+        workspace = alloc_workspace(page_compact_workspace_bytes(table, n_pages), table.device)
+        page_compact(table, table, n_pages, moves, counts, workspace)
+        # the same rule on the host's copy
+        live = sum(n > 0 for n in self._named)
+        old = [p for p in range(live, n_pages) if self._named[p]]
+        to = dict(zip(old, [p for p in range(live) if not self._named[p]]))
+        self._table_host = [[to.get(p, p) for p in row] for row in self._table_host]
+        for p, q in to.items():
+            self._named[q], self._named[p] = self._named[p], 0
+        self._free = list(range(live, n_pages))
+        return moves, counts
 
     def page_of(self, b: int, block: int) -> int:
         return self._table_host[b][block]
 
     def release_blocks(self, b: int, n_blocks: int = 0):
         """Takes back sequence b's pages behind its first n_blocks logical
-        blocks; they are free for any sequence from then on, so work that
-        reads them has to be queued before what writes them."""
+        blocks; those that no other sequence shares are free for any sequence
+        from then on, so work that reads them has to be queued before what
+        writes them."""
         row = self._table_host[b]
         for j in range(n_blocks, len(row)):
-            if row[j] >= 0:
-                self._free.append(row[j])
-                row[j] = -1
+            self._give_back(row, j)
         self.block_table[b].copy_(torch.tensor(row, dtype=torch.int32))
 
 
@@ -668,6 +729,111 @@ def kv16_evict(src: KV16Cache, dst: KV16Cache, max_tok: int, keep_first: int, ke
     _kv16_call(src, "oscar_kv16_evict", _lib.oscar_kv16_evict,
                (src._ref, dst._ref, max_tok, keep_first, keep_recent, keep_top,
                 src._mine(kept, torch.int32, src.B * src.Hkv * keep), w, wb), stream)
+
+
+# ---- sequences with tokens in common ---------------------------------------
+
+def kv16_shared_decode_workspace_bytes(cache: KV16Cache, Hq: int, n_groups: int, max_tok: int,
+                                       window: int = 0, n_sink: int = 0) -> int:
+    return int(_on_device(cache, _lib.oscar_kv16_shared_decode_workspace_bytes,
+                          (cache._ref, Hq, n_groups, max_tok, window, n_sink)))
+
+
+def kv16_shared_decode_attention(cache: KV16Cache, q: torch.Tensor, group: torch.Tensor,
+                                 prefix: torch.Tensor, softmax_scale: float, max_tok: int,
+                                 out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+                                 n_sink: int = 0, stream=None):
+    """kv16_decode_attention of sequences that share prefixes: sequences group[i]
+    .. group[i+1] - 1 have their first prefix[i] tokens in common, whose whole
+    pages are read once for all of them, from the first one's place in the cache.
+    group int32 [n + 1], prefix int32 [n].  The workspace comes zeroed from
+    alloc_workspace."""
+    qp, qs, _, Hq = cache._rows(q, None, cache.B)
+    w, wb = _bytes(workspace, cache)
+    n = prefix.numel()
+    _kv16_call(cache, "oscar_kv16_shared_decode_attention", _lib.oscar_kv16_shared_decode_attention,
+               (cache._ref, qp, qs, Hq, cache._mine(group, torch.int32, n + 1),
+                cache._mine(prefix, torch.int32, n), n, softmax_scale, max_tok, window, n_sink,
+                cache._mine(out, cache.dtype, cache.B * Hq * D), w, wb), stream)
+
+
+def kv16_shared_attention_workspace_bytes(cache: KV16Cache, Hq: int, n_groups: int, total: int,
+                                          max_tok: int, window: int = 0, n_sink: int = 0) -> int:
+    return int(_on_device(cache, _lib.oscar_kv16_shared_attention_workspace_bytes,
+                          (cache._ref, Hq, n_groups, total, max_tok, window, n_sink)))
+
+
+def kv16_shared_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor,
+                          group: torch.Tensor, prefix: torch.Tensor, softmax_scale: float,
+                          max_tok: int, out: torch.Tensor, workspace: torch.Tensor,
+                          window: int = 0, n_sink: int = 0, lse: torch.Tensor | None = None,
+                          stream=None):
+    """kv16_attention of sequences that share prefixes (groups as for
+    kv16_shared_decode_attention).  The workspace comes zeroed from
+    alloc_workspace."""
+    qp, qs, total, Hq = cache._rows(q, None)
+    w, wb = _bytes(workspace, cache)
+    n = prefix.numel()
+    _kv16_call(cache, "oscar_kv16_shared_attention", _lib.oscar_kv16_shared_attention,
+               (cache._ref, qp, qs, cache._mine(start, torch.int32, cache.B + 1), total, Hq,
+                cache._mine(group, torch.int32, n + 1), cache._mine(prefix, torch.int32, n), n,
+                softmax_scale, max_tok, window, n_sink,
+                cache._mine(out, cache.dtype, total * Hq * D),
+                cache._mine(lse, torch.float32, total * Hq), w, wb), stream)
+
+
+def kv16_fork(src: KV16Cache, dst: KV16Cache, parent: torch.Tensor, max_tok: int,
+              share: bool = True, stream=None):
+    """Sequence b of dst becomes a copy of sequence parent[b] of src (int32
+    [dst.B]; negative: stays as it is).  share: its whole pages are the parent's
+    own (dst's table is written), the tokens behind them are copied; else every
+    token is copied, to the places that dst's table names.  max_tok bounds the
+    parents' lengths."""
+    if dst.device != src.device:
+        raise ValueError(f"source on {src.device}, destination on {dst.device}")
+    _kv16_call(src, "oscar_kv16_fork", _lib.oscar_kv16_fork,
+               (src._ref, dst._ref, dst._mine(parent, torch.int32, dst.B), int(share), max_tok),
+               stream)
+
+
+def page_compact_workspace_bytes(block_table: torch.Tensor, n_pages: int) -> int:
+    B, max_blocks = block_table.shape
+    return int(_lib.oscar_page_compact_workspace_bytes(B, max_blocks, n_pages))
+
+
+def page_compact(block_table: torch.Tensor, new_table: torch.Tensor, n_pages: int,
+                 moves: torch.Tensor, counts: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """Plans the compaction of a pool of n_pages pages: the pages that
+    block_table [B][max_blocks] names get the ids 0 .. L - 1.  new_table: the
+    table with the new ids (may be block_table itself); moves int32
+    [n_pages // 2][2]: the pages to copy, old and new id, for kv16_copy_pages;
+    counts int32 [2]: the number of moves, L."""
+    tensors = (block_table, new_table, moves, counts)
+    if any(t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or
+           t.device != block_table.device for t in tensors) or \
+            block_table.dim() != 2 or new_table.shape != block_table.shape or \
+            moves.numel() != n_pages // 2 * 2 or counts.numel() != 2:
+        raise ValueError("expected dense int32 tensors on one device: tables [B][max_blocks], "
+                         "moves [n_pages // 2][2], counts [2]")
+    if workspace.device != block_table.device or not workspace.is_contiguous():
+        raise ValueError(f"expected a dense workspace on {block_table.device}")
+    with torch.cuda.device(block_table.device):
+        _check(_lib.oscar_page_compact(_ptr(block_table), _ptr(new_table), *block_table.shape,
+                                       n_pages, _ptr(moves), _ptr(counts), _ptr(workspace),
+                                       workspace.nbytes, _stream(stream)), "oscar_page_compact")
+
+
+def kv16_copy_pages(src: KV16Cache, dst: KV16Cache, pairs: torch.Tensor, n_pairs: torch.Tensor,
+                    stream=None):
+    """Pages pairs[i][0] of src to pages pairs[i][1] of dst (which may be one
+    pool), int32 [..][2], for i below the first element of n_pairs (int32)."""
+    if dst.device != src.device:
+        raise ValueError(f"source on {src.device}, destination on {dst.device}")
+    if n_pairs.numel() < 1 or pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("expected pairs [..][2] and their number")
+    _kv16_call(src, "oscar_kv16_copy_pages", _lib.oscar_kv16_copy_pages,
+               (src._ref, dst._ref, src._mine(pairs, torch.int32, None),
+                src._mine(n_pairs, torch.int32, None), pairs.shape[0]), stream)
 
 
 def selftest_wait_timeout(iterations: int = 256, stream=None):
