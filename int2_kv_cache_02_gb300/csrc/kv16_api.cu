@@ -175,7 +175,8 @@ oscar_status shared(const oscar_kv16_cache* c, const uint16_t* q, long long q_st
   if (!shared_size_ok(c, Hq, n_groups, total, max_tok)) return OSCAR_ERR_UNSUPPORTED;
   if (total == 0) return OSCAR_OK;
   Kv16 v = view(c);
-  if (!workspace || ws_bytes < kv16_shared_ws_bytes(v, Hq, n_groups, total, max_tok, window, n_sink))
+  if (!workspace ||
+      ws_bytes < kv16_shared_ws_bytes(v, Hq, n_groups, total, !start, max_tok, window, n_sink))
     return OSCAR_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
   const size_t heads = (size_t)total * Hq;
@@ -391,7 +392,7 @@ size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int H
       !window_ok(0.0f, max_tok, window, n_sink) ||
       !shared_size_ok(c, Hq, n_groups, c->B, max_tok) || !decode_size_ok(c, max_tok))
     return 0;
-  return kv16_shared_ws_bytes(view(c), Hq, n_groups, 0, max_tok, window, n_sink);
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, c->B, true, max_tok, window, n_sink);
 }
 
 oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
@@ -412,7 +413,7 @@ size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, in
   if (check(c) != OSCAR_OK || !heads_ok(Hq, c->Hkv) || n_groups < 1 || total <= 0 ||
       !window_ok(0.0f, max_tok, window, n_sink) || !shared_size_ok(c, Hq, n_groups, total, max_tok))
     return 0;
-  return kv16_shared_ws_bytes(view(c), Hq, n_groups, total, max_tok, window, n_sink);
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, total, false, max_tok, window, n_sink);
 }
 
 oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,

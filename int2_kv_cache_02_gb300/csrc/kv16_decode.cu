@@ -50,7 +50,7 @@
 // records.
 #include <algorithm>
 
-#include "kv16.cuh"
+#include "kv16_groups.cuh"
 #include "kv16_tma.h"
 #include "tc5.cuh"
 
@@ -88,12 +88,16 @@ struct DecodeParams {
   int g;
   unsigned wait_limit;  // polls of a wait for a copy
   bool halves;          // the warps' outputs are joined in two steps
+  SharedParts shared;   // SHARED only
 };
 
 // First pages of the sequences in the line of pages (of one KV head): first[0]
 // .. first[B].  Called by all threads; ends with a barrier.  Returns first[B].
-__device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* scan, int threads,
-                       bool report) {
+// SHARED: the pages behind the shared blocks, one at least (of hidden tokens
+// where there is none), so that every sequence has its rows.
+template <bool SHARED>
+__device__ int line_up(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups, int* first,
+                       int* scan, int threads, bool report) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = threads >> 5;
   int carry = 0;
   for (int b0 = 0; b0 < c.B; b0 += threads) {
@@ -106,7 +110,13 @@ __device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* scan,
         n = 0;
       }
     }
-    int x = Span(n - 1, n - 1, q.window, q.n_sink).blocks;
+    Span sp(n - 1, n - 1, q.window, q.n_sink);
+    if constexpr (SHARED) {
+      const int i = b < c.B ? group_of(groups, b) : -1;
+      if (i >= 0) sp = sp.from(shared_of(c, groups, i, q.max_tok, false).blocks);
+      sp.blocks = b < c.B ? max(sp.blocks, 1) : 0;
+    }
+    int x = sp.blocks;
     const int mine = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -133,8 +143,10 @@ __device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* scan,
 struct Row {
   int b, h, r0, r1, at;
   Span sp;
+  int group, lead, shared;     // SHARED: blocks below `shared` stand with sequence `lead`
 };
 
+template <bool SHARED>
 __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, const int* first) {
   const int key = x / p.c.Hkv;     // first[b] <= key < first[b + 1]
   int lo = 0, hi = p.c.B;
@@ -148,7 +160,19 @@ __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, c
   r.r0 = first[lo] * p.c.Hkv + r.h * pages;
   r.r1 = r.r0 + pages;
   r.at = __ldg(p.c.n_tok + lo) - 1;
+  if constexpr (SHARED) r.at = max(kv16_length(p.c, lo, p.q.max_tok), 0) - 1;
   r.sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
+  if constexpr (SHARED) {
+    r.group = group_of(p.shared.groups, lo);
+    r.lead = lo;
+    r.shared = 0;
+    if (r.group >= 0) {
+      const Shared s = shared_of(p.c, p.shared.groups, r.group, p.q.max_tok, false);
+      r.lead = s.lead;
+      r.shared = s.blocks;
+    }
+    r.sp = r.sp.from(r.shared);
+  }
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
@@ -196,13 +220,19 @@ __device__ __forceinline__ unsigned seen_in(float x) {
 // infinities of one sign and no NaN.  All threads; leaves ch at zero.  A CTA reads
 // the values alone, 16 tokens of every warp in flight, and stops early once every
 // open channel has met a NaN or both infinities.
-template <class T>
+template <class T, bool SHARED>
 __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* ch,
                                         const uint8_t* sum_nan) {
   constexpr int kTokens = 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile unsigned* mine = ch + 4 * lane;
-  for (int x = r.r0 + warp; x < r.r1; x += NW) {
+  Span sp = r.sp;
+  int pages = r.r1 - r.r0;
+  if constexpr (SHARED) {
+    sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
+    pages = sp.blocks;
+  }
+  for (int x = warp; x < pages; x += NW) {
     bool undecided = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -210,7 +240,8 @@ __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* 
       undecided |= (c & kOpen) && !(c & kSeenNan) && (c & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
     }
     if (!__any_sync(0xffffffffu, undecided)) break;
-    const int blk = r.sp.block(x - r.r0), row = kv16_block_row(p.c, r.b, r.h, blk);
+    const int blk = sp.block(x);
+    const int row = kv16_block_row(p.c, SHARED && blk < r.shared ? r.lead : r.b, r.h, blk);
     if (row < 0) continue;
     const unsigned see = __ballot_sync(
         0xffffffffu, kv16_visible(blk * kPage + lane, r.at, p.q.window, p.q.n_sink));
@@ -257,7 +288,7 @@ __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* 
   __syncthreads();
 }
 
-template <class T, bool ACC>
+template <class T, bool ACC, bool SHARED>
 __global__ void __launch_bounds__(NW * 32, 1)
 kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
@@ -282,8 +313,9 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     s_open = 0;
   }
   for (int i = tid; i < kD; i += NW * 32) s_ch[i] = 0u;
-  const int line = line_up(p.c, p.q, first, scan, NW * 32, blockIdx.x == 0);
+  const int line = line_up<SHARED>(p.c, p.q, p.shared.groups, first, scan, NW * 32, blockIdx.x == 0);
   // rows without visible tokens: zeros
+  if constexpr (!SHARED)
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x)
     if (first[b] == first[b + 1]) {
       uint4* o = reinterpret_cast<uint4*>(p.out + (long long)b * p.q.Hq * kD);
@@ -291,10 +323,12 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
 
   const int P = line * p.c.Hkv;                     // pages in the line
-  if (P == 0) return;
   const int per = max(kMinPages, (P - 1) / (int)gridDim.x + 1);
   const long long x0l = (long long)blockIdx.x * per;
-  if (x0l >= P) return;
+  if (P == 0 || x0l >= P) {
+    if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int x0 = (int)x0l, x1 = (int)min((long long)P, x0l + per);
 
   // the warp's next page to fetch, and the row it is in
@@ -302,12 +336,13 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   nr.r0 = nr.r1 = 0;
   auto fetch = [&](int x) {
     if (x >= x1) return;
-    if (x < nr.r0 || x >= nr.r1) find_row(nr, x, p, first);
-    int row = kv16_block_row(p.c, nr.b, nr.h, nr.sp.block(x - nr.r0));
+    if (x < nr.r0 || x >= nr.r1) find_row<SHARED>(nr, x, p, first);
+    const bool none = SHARED && x - nr.r0 >= nr.sp.blocks;     // a row without pages of its own
+    int row = none ? -1 : kv16_block_row(p.c, nr.b, nr.h, nr.sp.block(x - nr.r0));
     if (row < 0) {
       // past the end of the pool: the copy reads zeros
-      row = p.c.n_pages * p.c.Hkv * kPage;
-      if (lane == 0) record_error(p.c.status, kDevErrBadPaged);
+      row = SHARED && !p.c.table ? p.c.B * p.c.Hkv * p.c.T_cap : p.c.n_pages * p.c.Hkv * kPage;
+      if (!none && lane == 0) record_error(p.c.status, kDevErrBadPaged);
     }
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp], kSlotBytes);
@@ -328,7 +363,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   int seg = x0;
   Row r;
   while (seg < x1) {
-    find_row(r, seg, p, first);
+    find_row<SHARED>(r, seg, p, first);
     const int seg_end = min(r.r1, x1);
     // the group's queries as A operands: rows are heads, padding rows zero
     uint32_t qa[8][4];
@@ -469,6 +504,37 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       phase ^= 1;
     }
 
+    if constexpr (SHARED) {
+      // the prefix's records, a warp every tenth, by the CTA that has the row's first page
+      if (seg == r.r0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const Joint rec = joint_of(p.shared, p.c, p.q, r.b, r.h, r.group);
+        for (int j = warp; j < rec.n; j += NW) {
+          const float* d = rec.record(j);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int head = hr + 8 * i;
+            if (head >= p.g) continue;
+            const float* e = d + head * kRecFloats;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(e));
+            float2 v[16];
+#pragma unroll
+            for (int n = 0; n < 16; ++n) v[n] = __ldcg(reinterpret_cast<const float2*>(e + 4 + hc + 8 * n));
+            const float M = fmaxf(m[i], ml.x);
+            const float a = M == -INFINITY ? 1.0f : fast_exp2(m[i] - M);
+            const float a2 = M == -INFINITY ? 1.0f : fast_exp2(ml.x - M);
+            m[i] = M;
+            l[i] = a * l[i] + ((lane & 3) == 0 ? a2 * ml.y : 0.0f);     // (summed over four lanes below)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              o[n][2 * i] = a * o[n][2 * i] + a2 * v[n].x;
+              o[n][2 * i + 1] = a * o[n][2 * i + 1] + a2 * v[n].y;
+            }
+          }
+        }
+      }
+    }
+
     // join the warps: in one step, or the upper half's results into the lower
     // half's first where the buffer holds half of them
 #pragma unroll
@@ -590,7 +656,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       }
     }
     if (s_open) {
-      settle_row<T>(p, r, s_ch, s_nan);
+      settle_row<T, SHARED>(p, r, s_ch, s_nan);
       if (tid == 0) s_open = 0;
       __syncthreads();
     }
@@ -599,6 +665,8 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   // the copy in flight lands before its memory is given back
   if (gave_up && !mbar_wait_bounded(&full[warp], phase, kDrainLimit) && lane == 0)
     record_error(p.c.status, kDevErrDrainTimeout);
+  // (complete only once the prefixes' kernel is, so that who follows has both)
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 constexpr int kWThreads = 256;
@@ -611,7 +679,7 @@ constexpr int kWThreads = 256;
 __global__ void __launch_bounds__(kWThreads) kv16_decode_weights_kernel(const DecodeParams p) {
   extern __shared__ int first[];
   __shared__ int scan[kWThreads / 32];
-  const int P = line_up(p.c, p.q, first, scan, kWThreads, false) * p.c.Hkv;
+  const int P = line_up<false>(p.c, p.q, Kv16Groups{}, first, scan, kWThreads, false) * p.c.Hkv;
   const int lane = threadIdx.x & 31, t0 = 4 * (lane & 7);
   const long long step = (long long)gridDim.x * (kWThreads / 32) * 4;
   long long x = ((long long)blockIdx.x * (kWThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
@@ -623,7 +691,7 @@ __global__ void __launch_bounds__(kWThreads) kv16_decode_weights_kernel(const De
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < p.g) s[h] = __ldcs(reinterpret_cast<const float4*>(sp + h * kPage));
-    if (x < r.r0 || x >= r.r1) find_row(r, (int)x, p, first);
+    if (x < r.r0 || x >= r.r1) find_row<false>(r, (int)x, p, first);
     const int j0 = r.sp.block((int)x - r.r0);
     const int row = kv16_block_row(p.c, r.b, r.h, j0);
     if (row < 0) continue;
@@ -686,14 +754,23 @@ static_assert(NW * kSlotBytes + NW / 2 * kMaxGroup * kORow * 4 + (kMaxDecodeBatc
 size_t part_bytes(int grid, int g) { return (size_t)grid * 2 * g * kRecFloats * sizeof(float); }
 size_t stats_bytes(int B, int Hq) { return ((size_t)B * Hq * sizeof(float2) + 15) / 16 * 16; }
 
-template <class T, bool ACC>
+template <class T, bool ACC, bool SHARED>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                         int grid, size_t smem, cudaStream_t s) {
-  const auto kernel = kv16_decode_kernel<T, ACC>;
+  const auto kernel = kv16_decode_kernel<T, ACC, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, NW * 32, smem, s>>>(mk, mv, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = NW * 32;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = SHARED ? 1 : 0;      // starts as the prefixes' kernel ends
+  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
 }
 
 }  // namespace
@@ -707,11 +784,15 @@ size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int 
   return n;
 }
 
-cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
-                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s) {
+namespace {
+
+cudaError_t start_decode(const Kv16& c, const Kv16Query& q, bool accumulate,
+                         const SharedParts* shared, uint16_t* out, void* ws, unsigned wait_limit,
+                         int* launches, cudaStream_t s) {
   DecodeParams p;
   p.c = c;
   p.q = q;
+  p.shared = shared ? *shared : SharedParts{};
   p.out = out;
   p.g = q.Hq / c.Hkv;
   p.wait_limit = wait_limit;
@@ -727,11 +808,16 @@ cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulat
   const size_t smem = NW * kSlotBytes + (p.halves ? heads / 2 : heads) + lines + 1024;
   CUtensorMap mk, mv;
   if (!kv16_row_map(&mk, c, c.k) || !kv16_row_map(&mv, c, c.v)) return cudaErrorNotSupported;
-  cudaError_t e =
-      c.half ? (accumulate ? launch_main<Fp16, true>(mk, mv, p, grid, smem, s)
-                           : launch_main<Fp16, false>(mk, mv, p, grid, smem, s))
-             : (accumulate ? launch_main<Bf16, true>(mk, mv, p, grid, smem, s)
-                           : launch_main<Bf16, false>(mk, mv, p, grid, smem, s));
+  cudaError_t e;
+  if (shared)
+    e = c.half ? launch_main<Fp16, false, true>(mk, mv, p, grid, smem, s)
+               : launch_main<Bf16, false, true>(mk, mv, p, grid, smem, s);
+  else if (accumulate)
+    e = c.half ? launch_main<Fp16, true, false>(mk, mv, p, grid, smem, s)
+               : launch_main<Bf16, true, false>(mk, mv, p, grid, smem, s);
+  else
+    e = c.half ? launch_main<Fp16, false, false>(mk, mv, p, grid, smem, s)
+               : launch_main<Bf16, false, false>(mk, mv, p, grid, smem, s);
   *launches = 1;
   if (e != cudaSuccess || !accumulate) return e;
   e = cudaFuncSetAttribute(kv16_decode_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -742,6 +828,18 @@ cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulat
   kv16_decode_weights_kernel<<<wgrid, kWThreads, lines, s>>>(p);
   *launches = 2;
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
+                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s) {
+  return start_decode(c, q, accumulate, nullptr, out, ws, wait_limit, launches, s);
+}
+
+cudaError_t launch_kv16_decode_own(const Kv16& c, const Kv16Query& q, const SharedParts& shared,
+                                   uint16_t* out, void* ws, int* launches, cudaStream_t s) {
+  return start_decode(c, q, false, &shared, out, ws, kTcWaitLimit, launches, s);
 }
 
 }  // namespace oscar
