@@ -617,10 +617,10 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  *  prefix  device int32 [n_groups], within [0, max_tok] and the capacity
  *  q, out, positions and visibility are those of oscar_kv16_decode_attention
  * A group out of range is recorded in the status word and shares nothing.
- * workspace: a decode workspace (its header of OSCAR_DECODE_WS_HEADER_BYTES is
- * zero before the first use and after every call) of
- * oscar_kv16_shared_decode_workspace_bytes.  The limits of the decode call hold,
- * and n_groups <= 4096 (else OSCAR_ERR_UNSUPPORTED).
+ * workspace: oscar_kv16_shared_decode_workspace_bytes of device memory (no
+ * initialisation).  Calls that use one workspace must not overlap on the GPU.
+ * The limits of the decode call hold, and n_groups <= 4096 (else
+ * OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                                 long long q_stride, int Hq, const int32_t* group,
@@ -634,9 +634,9 @@ size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int H
 /*
  * oscar_kv16_attention of sequences that share prefixes, for the newest tokens
  * of each: q, start, out, lse, positions and visibility as there, groups as
- * above (a prefix may reach into the new tokens).  workspace: a decode
- * workspace of oscar_kv16_shared_attention_workspace_bytes, asked for with this
- * call's numbers.  B <= 4096 and n_groups <= 4096 (else OSCAR_ERR_UNSUPPORTED).
+ * above (a prefix may reach into the new tokens).  workspace:
+ * oscar_kv16_shared_attention_workspace_bytes of device memory (no
+ * initialisation), asked for with this call's numbers.  B <= 4096 and n_groups <= 4096 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                          long long q_stride, const int32_t* start, int total,

@@ -67,10 +67,9 @@
 // Parts.  Sequences that share a prefix have their attention worked in two parts,
 // by the same kernel: kPrefix the shared blocks, for all sequences of a group at
 // once, kOwn the blocks behind them, a sequence at a time.  Both leave records.
-// In kPrefix the key tiles of all (group, KV head, query tile) rows stand in one
-// line, row after row, and every CTA takes an equal run of it (its items): groups
-// of unequal length leave no CTA idle.  A row's first run writes its records at
-// the rows' own places, a run that begins inside a row at the CTA's.
+// In kPrefix the key tiles of all groups stand in one line (SharedLine), and every
+// CTA takes an equal run of it (its items): groups of unequal length leave no CTA
+// idle.
 #pragma once
 
 #include <algorithm>
@@ -107,8 +106,8 @@ struct AttnParams {
   uint16_t* out;
   float* lse;
   float* part;          // [total * Hq][splits][kRecFloats] if splits > 1 or a part
-  float* cut;           // kPrefix: [CTAs][2 * 128][kRecFloats], runs that begin inside a row
-  SharedLine* line;     // kPrefix: [groups + 1], for who joins the records
+  float* cut;           // kPrefix: see SharedParts
+  SharedLine* line;     // kPrefix
   Kv16Groups groups;    // kPrefix, kOwn
   int g, tokens;        // heads of a group, tokens of a query tile
   int tiles;            // upper bound on work items of one KV head and split
@@ -255,11 +254,11 @@ __device__ __forceinline__ void line_of_tiles(const AttnParams& p, int* first, i
   for (int i0 = 0; i0 < p.groups.n; i0 += kThreads) {
     const int i = i0 + tid;
     unsigned x = 0;
+    Piece g;
     if (i < p.groups.n) {
-      const Piece g = group_piece(p, i, 0, 1, blockIdx.x == 0);
+      g = group_piece(p, i, 0, 1, blockIdx.x == 0);
       const long long n = (long long)((g.r1 - g.r0 + two - 1) / two) * p.c.Hkv * g.tiles();
       x = (unsigned)min(n, 0x7fffffffLL);
-      if (blockIdx.x == 0) p.line[i].tiles = g.tiles();
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -275,13 +274,18 @@ __device__ __forceinline__ void line_of_tiles(const AttnParams& p, int* first, i
       if (w < warp) base = plus(base, (unsigned)scan[w]);
       carry = plus(carry, (unsigned)scan[w]);
     }
-    if (i < p.groups.n) first[i] = (int)plus(base, before);
+    if (i < p.groups.n) {
+      first[i] = (int)plus(base, before);
+      if (blockIdx.x == 0)
+        p.line[i] = SharedLine{first[i], g.tiles(), (g.r1 - g.r0 + two - 1) / two, g.r0};
+    }
     __syncthreads();
   }
-  if (tid == 0) first[p.groups.n] = (int)carry;
+  if (tid == 0) {
+    first[p.groups.n] = (int)carry;
+    if (blockIdx.x == 0) p.line[p.groups.n] = SharedLine{(int)carry, 0, 0, 0};
+  }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.groups.n; i += kThreads) p.line[i].first = first[i];
 }
 
 // The item at place x of the line, as far as x1.
@@ -296,21 +300,34 @@ __device__ __forceinline__ void find_piece(const AttnParams& p, const int* first
   // (the maxima: whatever the groups hold by now, what follows stays in bounds)
   const int two = 2 * p.tokens, chunks = max((g.r1 - g.r0 + two - 1) / two, 1);
   const int tiles = max(g.tiles(), 1), at = x - first[lo];
-  const int row = at / tiles, chunk = row % chunks;
-  it.h = min(row / chunks, p.c.Hkv - 1);
+  const int per_head = chunks * tiles;          // (no more than the line has: it fits)
+  it.h = min(at / per_head, p.c.Hkv - 1);
+  const int y = at - it.h * per_head, z = min(y / chunks, tiles - 1);
+  const int blocks = line_blocks(tiles, chunks, line_share(first[p.groups.n], gridDim.x));
+  int i = (int)((long long)z * blocks / tiles);
+  if (block_tile(tiles, blocks, i + 1) <= z) ++i;
+  const int t0 = block_tile(tiles, blocks, i), t1 = block_tile(tiles, blocks, i + 1);
+  const int in = y - chunks * t0, chunk = min(in / (t1 - t0), chunks - 1);
   it.b = g.s.lead;
   it.n = g.s.end;
   it.row0 = g.r0 + chunk * two;
   it.nrow = min(two, g.r1 - it.row0);
   it.sp = g.sp;
-  it.k0 = at - row * tiles;
-  it.k1 = min(min((long long)it.k0 + (x1 - x), (long long)tiles),
+  it.k0 = t0 + in - chunk * (t1 - t0);
+  it.k1 = min(min((long long)it.k0 + (x1 - x), (long long)t1),
               (long long)it.k0 + (first[lo + 1] - x));
-  it.split = it.k0 > 0;            // begins inside the row
-  it.cnt[0] = it.nrow > 0 ? it.k1 - it.k0 : 0;
+  it.split = it.k0 == 0 ? 0 : it.k0 > t0 ? 1 : 2;       // where the records go
+  it.cnt[0] = it.nrow > 0 ? max(it.k1 - it.k0, 0) : 0;
   it.cnt[1] = it.nrow > p.tokens ? it.cnt[0] : 0;
   it.clear = false;
   it.at0 = 0;
+}
+
+// The record of a row: at the row's place, or (split 1, 2) the CTA's.
+__device__ __forceinline__ float* prefix_record(const AttnParams& p, int split, long long row,
+                                                int cut_row) {
+  return split == 0 ? p.part + row * kRecFloats
+                    : p.cut + (((long long)blockIdx.x * 2 + split - 1) * 256 + cut_row) * kRecFloats;
 }
 
 // The position of query row r of a group's sequences [b0, b1).
@@ -369,10 +386,10 @@ __device__ __forceinline__ float gather_open(float x, float so_far) {
 template <class T, int PART>
 __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int split, int k0,
                                          int k1, const Span& sp, long long row, int at, int* met,
-                                         long long cut_row) {
+                                         int cut_row) {
   const int lane = threadIdx.x & 31;
   const bool record = PART != kWhole || p.splits > 1;
-  float* rec = PART == kPrefix ? (split ? p.cut + cut_row * kRecFloats : p.part + row * kRecFloats)
+  float* rec = PART == kPrefix ? prefix_record(p, split, row, cut_row)
                                : p.part + (row * p.splits + split) * kRecFloats;
   uint2* out = reinterpret_cast<uint2*>(p.out + row * kD) + lane;
   float x[4];
@@ -873,9 +890,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const bool record = PART != kWhole || p.splits > 1;
       const float inv = record ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       float odd = 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: a channel is open
-      const long long cut_row = (long long)blockIdx.x * 256 + w * 128;
-      float* rec = PART == kPrefix ? (split ? p.cut + (cut_row + r) * kRecFloats
-                                            : p.part + row * kRecFloats)
+      const int cut_row = w * 128;
+      float* rec = PART == kPrefix ? prefix_record(p, split, row, cut_row + r)
                                    : p.part + (row * p.splits + split) * kRecFloats;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

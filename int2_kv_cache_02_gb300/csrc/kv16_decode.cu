@@ -50,7 +50,7 @@
 // records.
 #include <algorithm>
 
-#include "kv16_groups.cuh"
+#include "kv16_page.cuh"
 #include "kv16_tma.h"
 #include "tc5.cuh"
 
@@ -72,9 +72,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 namespace {
 
 constexpr int NW = 10;                   // warps of a CTA, each with a slot of its own
-constexpr int kSlotBytes = 4 * 4096;     // a page: K and V, two halves of 64 channels each
 constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many: one a warp
-constexpr float kBelow = 14.0f;          // fp16: the maximum in use is 2^14 below the largest
 constexpr int kORow = 136;               // floats of a head's output row in shared memory
 
 struct DecodeParams {
@@ -88,16 +86,12 @@ struct DecodeParams {
   int g;
   unsigned wait_limit;  // polls of a wait for a copy
   bool halves;          // the warps' outputs are joined in two steps
-  SharedParts shared;   // SHARED only
 };
 
 // First pages of the sequences in the line of pages (of one KV head): first[0]
 // .. first[B].  Called by all threads; ends with a barrier.  Returns first[B].
-// SHARED: the pages behind the shared blocks, one at least (of hidden tokens
-// where there is none), so that every sequence has its rows.
-template <bool SHARED>
-__device__ int line_up(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups, int* first,
-                       int* scan, int threads, bool report) {
+__device__ int line_up(const Kv16& c, const Kv16Query& q, int* first, int* scan, int threads,
+                       bool report) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = threads >> 5;
   int carry = 0;
   for (int b0 = 0; b0 < c.B; b0 += threads) {
@@ -110,13 +104,7 @@ __device__ int line_up(const Kv16& c, const Kv16Query& q, const Kv16Groups& grou
         n = 0;
       }
     }
-    Span sp(n - 1, n - 1, q.window, q.n_sink);
-    if constexpr (SHARED) {
-      const int i = b < c.B ? group_of(groups, b) : -1;
-      if (i >= 0) sp = sp.from(shared_of(c, groups, i, q.max_tok, false).blocks);
-      sp.blocks = b < c.B ? max(sp.blocks, 1) : 0;
-    }
-    int x = sp.blocks;
+    int x = Span(n - 1, n - 1, q.window, q.n_sink).blocks;
     const int mine = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -143,10 +131,8 @@ __device__ int line_up(const Kv16& c, const Kv16Query& q, const Kv16Groups& grou
 struct Row {
   int b, h, r0, r1, at;
   Span sp;
-  int group, lead, shared;     // SHARED: blocks below `shared` stand with sequence `lead`
 };
 
-template <bool SHARED>
 __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, const int* first) {
   const int key = x / p.c.Hkv;     // first[b] <= key < first[b + 1]
   int lo = 0, hi = p.c.B;
@@ -160,43 +146,7 @@ __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, c
   r.r0 = first[lo] * p.c.Hkv + r.h * pages;
   r.r1 = r.r0 + pages;
   r.at = __ldg(p.c.n_tok + lo) - 1;
-  if constexpr (SHARED) r.at = max(kv16_length(p.c, lo, p.q.max_tok), 0) - 1;
   r.sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
-  if constexpr (SHARED) {
-    r.group = group_of(p.shared.groups, lo);
-    r.lead = lo;
-    r.shared = 0;
-    if (r.group >= 0) {
-      const Shared s = shared_of(p.c, p.shared.groups, r.group, p.q.max_tok, false);
-      r.lead = s.lead;
-      r.shared = s.blocks;
-    }
-    r.sp = r.sp.from(r.shared);
-  }
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-template <class T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-  if constexpr (T::kHalf)
-    mma_16816_acc(d, a, b0, b1);
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The row's joined result (M, L, o of channel pair `pair`) to the output.
@@ -220,19 +170,13 @@ __device__ __forceinline__ unsigned seen_in(float x) {
 // infinities of one sign and no NaN.  All threads; leaves ch at zero.  A CTA reads
 // the values alone, 16 tokens of every warp in flight, and stops early once every
 // open channel has met a NaN or both infinities.
-template <class T, bool SHARED>
+template <class T>
 __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* ch,
                                         const uint8_t* sum_nan) {
   constexpr int kTokens = 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile unsigned* mine = ch + 4 * lane;
-  Span sp = r.sp;
-  int pages = r.r1 - r.r0;
-  if constexpr (SHARED) {
-    sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
-    pages = sp.blocks;
-  }
-  for (int x = warp; x < pages; x += NW) {
+  for (int x = r.r0 + warp; x < r.r1; x += NW) {
     bool undecided = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -240,8 +184,7 @@ __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* 
       undecided |= (c & kOpen) && !(c & kSeenNan) && (c & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
     }
     if (!__any_sync(0xffffffffu, undecided)) break;
-    const int blk = sp.block(x);
-    const int row = kv16_block_row(p.c, SHARED && blk < r.shared ? r.lead : r.b, r.h, blk);
+    const int blk = r.sp.block(x - r.r0), row = kv16_block_row(p.c, r.b, r.h, blk);
     if (row < 0) continue;
     const unsigned see = __ballot_sync(
         0xffffffffu, kv16_visible(blk * kPage + lane, r.at, p.q.window, p.q.n_sink));
@@ -288,7 +231,7 @@ __device__ __noinline__ void settle_row(const DecodeParams& p, Row r, unsigned* 
   __syncthreads();
 }
 
-template <class T, bool ACC, bool SHARED>
+template <class T, bool ACC>
 __global__ void __launch_bounds__(NW * 32, 1)
 kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
@@ -313,9 +256,8 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     s_open = 0;
   }
   for (int i = tid; i < kD; i += NW * 32) s_ch[i] = 0u;
-  const int line = line_up<SHARED>(p.c, p.q, p.shared.groups, first, scan, NW * 32, blockIdx.x == 0);
+  const int line = line_up(p.c, p.q, first, scan, NW * 32, blockIdx.x == 0);
   // rows without visible tokens: zeros
-  if constexpr (!SHARED)
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x)
     if (first[b] == first[b + 1]) {
       uint4* o = reinterpret_cast<uint4*>(p.out + (long long)b * p.q.Hq * kD);
@@ -323,12 +265,10 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
     }
 
   const int P = line * p.c.Hkv;                     // pages in the line
+  if (P == 0) return;
   const int per = max(kMinPages, (P - 1) / (int)gridDim.x + 1);
   const long long x0l = (long long)blockIdx.x * per;
-  if (P == 0 || x0l >= P) {
-    if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  if (x0l >= P) return;
   const int x0 = (int)x0l, x1 = (int)min((long long)P, x0l + per);
 
   // the warp's next page to fetch, and the row it is in
@@ -336,13 +276,12 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   nr.r0 = nr.r1 = 0;
   auto fetch = [&](int x) {
     if (x >= x1) return;
-    if (x < nr.r0 || x >= nr.r1) find_row<SHARED>(nr, x, p, first);
-    const bool none = SHARED && x - nr.r0 >= nr.sp.blocks;     // a row without pages of its own
-    int row = none ? -1 : kv16_block_row(p.c, nr.b, nr.h, nr.sp.block(x - nr.r0));
+    if (x < nr.r0 || x >= nr.r1) find_row(nr, x, p, first);
+    int row = kv16_block_row(p.c, nr.b, nr.h, nr.sp.block(x - nr.r0));
     if (row < 0) {
       // past the end of the pool: the copy reads zeros
-      row = SHARED && !p.c.table ? p.c.B * p.c.Hkv * p.c.T_cap : p.c.n_pages * p.c.Hkv * kPage;
-      if (!none && lane == 0) record_error(p.c.status, kDevErrBadPaged);
+      row = p.c.n_pages * p.c.Hkv * kPage;
+      if (lane == 0) record_error(p.c.status, kDevErrBadPaged);
     }
     if (lane == 0) {
       mbar_arrive_expect_tx(&full[warp], kSlotBytes);
@@ -363,20 +302,10 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   int seg = x0;
   Row r;
   while (seg < x1) {
-    find_row<SHARED>(r, seg, p, first);
+    find_row(r, seg, p, first);
     const int seg_end = min(r.r1, x1);
-    // the group's queries as A operands: rows are heads, padding rows zero
     uint32_t qa[8][4];
-    {
-      const uint16_t* q0 = p.q.q + r.b * p.q.stride + (long long)r.h * p.g * kD;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int head = hr + 8 * (i & 1), ch = 16 * k + hc + 8 * (i >> 1);
-          qa[k][i] = head < p.g ? __ldg(reinterpret_cast<const uint32_t*>(q0 + head * kD + ch)) : 0u;
-        }
-    }
+    page_queries(qa, p.q.q + r.b * p.q.stride + (long long)r.h * p.g * kD, p.g);
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -389,150 +318,25 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         break;
       }
       const int j0 = r.sp.block(x - r.r0) * kPage;
-      const bool whole = j0 + kPage - 1 <= r.at &&
-                         (p.q.window == 0 || j0 > r.at - p.q.window || j0 + kPage <= p.q.n_sink);
-      if (!whole) {
-        // a hidden token's value must not meet its zero probability: clear it
-        const int j = j0 + lane;
-        if (!kv16_visible(j, r.at, p.q.window, p.q.n_sink)) {
+      const bool whole = page_step<T>(
+          slot, j0, r.at, p.q.window, p.q.n_sink, p.q.scale_log2, qa, o, m, l,
+          [&](const float (&sc)[4][4]) {
+            if constexpr (ACC) {
+              float* d = p.scores + ((size_t)x * p.g + hr) * kPage + hc;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            reinterpret_cast<uint4*>(slot + 8192 + (i >> 3) * 4096 + lane * 128)[i & 7] =
-                make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
-      // S: 16 heads x 32 tokens
-      float sc[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
-      const unsigned sa = smem_u32(slot);
-      const int mrow = lane & 7, mid = lane >> 3;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // 8x8 tiles: channels 16k, 16k + 8 of tokens t, t + 8
-        const int chunk = 2 * (k & 3) + (mid & 1);
-        const unsigned a = sa + (k >> 2) * 4096 + ((mid >> 1) * 8 + mrow) * 128 + ((chunk ^ mrow) << 4);
-        uint32_t b0[4], b1[4];
-        ldsm4(b0, a);
-        ldsm4(b1, a + 16 * 128);
-        mma<T>(sc[0], qa[k], b0[0], b0[1]);
-        mma<T>(sc[1], qa[k], b0[2], b0[3]);
-        mma<T>(sc[2], qa[k], b1[0], b1[1]);
-        mma<T>(sc[3], qa[k], b1[2], b1[3]);
-      }
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = sc[i][e] * p.q.scale_log2;
-          if (!whole && !kv16_visible(j0 + 8 * i + hc + (e & 1), r.at, p.q.window, p.q.n_sink))
-            v = -INFINITY;
-          sc[i][e] = v;
-          mx[e >> 1] = fmaxf(mx[e >> 1], v);
-        }
-      if constexpr (ACC) {
-        float* d = p.scores + ((size_t)x * p.g + hr) * kPage + hc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (hr < p.g) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(sc[i][0], sc[i][1]);
-          if (hr + 8 < p.g)
-            *reinterpret_cast<float2*>(d + 8 * kPage + 8 * i) = make_float2(sc[i][2], sc[i][3]);
-        }
-      }
-      bool grew = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        if (T::kHalf) mx[i] -= kBelow;
-        grew |= mx[i] > m[i];
-      }
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mn = fmaxf(m[i], mx[i]);
-          const float a = mn == -INFINITY ? 1.0f : fast_exp2(m[i] - mn);
-          m[i] = mn;
-          l[i] *= a;
-#pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            o[n][2 * i] *= a;
-            o[n][2 * i + 1] *= a;
-          }
-        }
-      }
-      const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-      uint32_t pa[2][4], pb[2][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p0 = fast_exp2(sc[i][0] - ms[0]), p1 = fast_exp2(sc[i][1] - ms[0]);
-        const float p2 = fast_exp2(sc[i][2] - ms[1]), p3 = fast_exp2(sc[i][3] - ms[1]);
-        l[0] += p0 + p1;
-        l[1] += p2 + p3;
-        const uint32_t h0 = T::pack(p0, p1), h1 = T::pack(p2, p3);
-        const float2 u0 = T::unpack(h0), u1 = T::unpack(h1);
-        pa[i >> 1][2 * (i & 1)] = h0;
-        pa[i >> 1][2 * (i & 1) + 1] = h1;
-        pb[i >> 1][2 * (i & 1)] = T::pack(p0 - u0.x, p1 - u0.y);
-        pb[i >> 1][2 * (i & 1) + 1] = T::pack(p2 - u1.x, p3 - u1.y);
-      }
-      // O += P V: 8x8 tiles, transposed on the way: tokens t, t + 8 of channels c, c + 8
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int chunk = 2 * (n & 3) + (mid >> 1);
-        const unsigned a = sa + 8192 + (n >> 2) * 4096 + ((mid & 1) * 8 + mrow) * 128 +
-                           ((chunk ^ mrow) << 4);
-        uint32_t b0[4], b1[4];
-        ldsm4t(b0, a);
-        ldsm4t(b1, a + 16 * 128);
-        mma<T>(o[2 * n], pa[0], b0[0], b0[1]);
-        mma<T>(o[2 * n + 1], pa[0], b0[2], b0[3]);
-        mma<T>(o[2 * n], pa[1], b1[0], b1[1]);
-        mma<T>(o[2 * n + 1], pa[1], b1[2], b1[3]);
-        mma<T>(o[2 * n], pb[0], b0[0], b0[1]);
-        mma<T>(o[2 * n + 1], pb[0], b0[2], b0[3]);
-        mma<T>(o[2 * n], pb[1], b1[0], b1[1]);
-        mma<T>(o[2 * n + 1], pb[1], b1[2], b1[3]);
-      }
+              for (int i = 0; i < 4; ++i) {
+                if (hr < p.g) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(sc[i][0], sc[i][1]);
+                if (hr + 8 < p.g)
+                  *reinterpret_cast<float2*>(d + 8 * kPage + 8 * i) = make_float2(sc[i][2], sc[i][3]);
+              }
+            }
+          });
       // refill the slot once every lane has read it; cleared values first
       // become visible to the copy engine
       if (!whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       fetch(x + NW);
       phase ^= 1;
-    }
-
-    if constexpr (SHARED) {
-      // the prefix's records, a warp every tenth, by the CTA that has the row's first page
-      if (seg == r.r0) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        const Joint rec = joint_of(p.shared, p.c, p.q, r.b, r.h, r.group);
-        for (int j = warp; j < rec.n; j += NW) {
-          const float* d = rec.record(j);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int head = hr + 8 * i;
-            if (head >= p.g) continue;
-            const float* e = d + head * kRecFloats;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(e));
-            float2 v[16];
-#pragma unroll
-            for (int n = 0; n < 16; ++n) v[n] = __ldcg(reinterpret_cast<const float2*>(e + 4 + hc + 8 * n));
-            const float M = fmaxf(m[i], ml.x);
-            const float a = M == -INFINITY ? 1.0f : fast_exp2(m[i] - M);
-            const float a2 = M == -INFINITY ? 1.0f : fast_exp2(ml.x - M);
-            m[i] = M;
-            l[i] = a * l[i] + ((lane & 3) == 0 ? a2 * ml.y : 0.0f);     // (summed over four lanes below)
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              o[n][2 * i] = a * o[n][2 * i] + a2 * v[n].x;
-              o[n][2 * i + 1] = a * o[n][2 * i + 1] + a2 * v[n].y;
-            }
-          }
-        }
-      }
     }
 
     // join the warps: in one step, or the upper half's results into the lower
@@ -656,7 +460,7 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
       }
     }
     if (s_open) {
-      settle_row<T, SHARED>(p, r, s_ch, s_nan);
+      settle_row<T>(p, r, s_ch, s_nan);
       if (tid == 0) s_open = 0;
       __syncthreads();
     }
@@ -665,8 +469,6 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   // the copy in flight lands before its memory is given back
   if (gave_up && !mbar_wait_bounded(&full[warp], phase, kDrainLimit) && lane == 0)
     record_error(p.c.status, kDevErrDrainTimeout);
-  // (complete only once the prefixes' kernel is, so that who follows has both)
-  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 constexpr int kWThreads = 256;
@@ -679,7 +481,7 @@ constexpr int kWThreads = 256;
 __global__ void __launch_bounds__(kWThreads) kv16_decode_weights_kernel(const DecodeParams p) {
   extern __shared__ int first[];
   __shared__ int scan[kWThreads / 32];
-  const int P = line_up<false>(p.c, p.q, Kv16Groups{}, first, scan, kWThreads, false) * p.c.Hkv;
+  const int P = line_up(p.c, p.q, first, scan, kWThreads, false) * p.c.Hkv;
   const int lane = threadIdx.x & 31, t0 = 4 * (lane & 7);
   const long long step = (long long)gridDim.x * (kWThreads / 32) * 4;
   long long x = ((long long)blockIdx.x * (kWThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
@@ -691,7 +493,7 @@ __global__ void __launch_bounds__(kWThreads) kv16_decode_weights_kernel(const De
 #pragma unroll
     for (int h = 0; h < 8; ++h)
       if (h < p.g) s[h] = __ldcs(reinterpret_cast<const float4*>(sp + h * kPage));
-    if (x < r.r0 || x >= r.r1) find_row<false>(r, (int)x, p, first);
+    if (x < r.r0 || x >= r.r1) find_row(r, (int)x, p, first);
     const int j0 = r.sp.block((int)x - r.r0);
     const int row = kv16_block_row(p.c, r.b, r.h, j0);
     if (row < 0) continue;
@@ -754,23 +556,14 @@ static_assert(NW * kSlotBytes + NW / 2 * kMaxGroup * kORow * 4 + (kMaxDecodeBatc
 size_t part_bytes(int grid, int g) { return (size_t)grid * 2 * g * kRecFloats * sizeof(float); }
 size_t stats_bytes(int B, int Hq) { return ((size_t)B * Hq * sizeof(float2) + 15) / 16 * 16; }
 
-template <class T, bool ACC, bool SHARED>
+template <class T, bool ACC>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                         int grid, size_t smem, cudaStream_t s) {
-  const auto kernel = kv16_decode_kernel<T, ACC, SHARED>;
+  const auto kernel = kv16_decode_kernel<T, ACC>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = NW * 32;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = SHARED ? 1 : 0;      // starts as the prefixes' kernel ends
-  return cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
+  kernel<<<grid, NW * 32, smem, s>>>(mk, mv, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -784,15 +577,11 @@ size_t kv16_decode_ws_bytes(const Kv16& c, int Hq, int max_tok, int window, int 
   return n;
 }
 
-namespace {
-
-cudaError_t start_decode(const Kv16& c, const Kv16Query& q, bool accumulate,
-                         const SharedParts* shared, uint16_t* out, void* ws, unsigned wait_limit,
-                         int* launches, cudaStream_t s) {
+cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
+                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s) {
   DecodeParams p;
   p.c = c;
   p.q = q;
-  p.shared = shared ? *shared : SharedParts{};
   p.out = out;
   p.g = q.Hq / c.Hkv;
   p.wait_limit = wait_limit;
@@ -808,16 +597,11 @@ cudaError_t start_decode(const Kv16& c, const Kv16Query& q, bool accumulate,
   const size_t smem = NW * kSlotBytes + (p.halves ? heads / 2 : heads) + lines + 1024;
   CUtensorMap mk, mv;
   if (!kv16_row_map(&mk, c, c.k) || !kv16_row_map(&mv, c, c.v)) return cudaErrorNotSupported;
-  cudaError_t e;
-  if (shared)
-    e = c.half ? launch_main<Fp16, false, true>(mk, mv, p, grid, smem, s)
-               : launch_main<Bf16, false, true>(mk, mv, p, grid, smem, s);
-  else if (accumulate)
-    e = c.half ? launch_main<Fp16, true, false>(mk, mv, p, grid, smem, s)
-               : launch_main<Bf16, true, false>(mk, mv, p, grid, smem, s);
-  else
-    e = c.half ? launch_main<Fp16, false, false>(mk, mv, p, grid, smem, s)
-               : launch_main<Bf16, false, false>(mk, mv, p, grid, smem, s);
+  cudaError_t e =
+      c.half ? (accumulate ? launch_main<Fp16, true>(mk, mv, p, grid, smem, s)
+                           : launch_main<Fp16, false>(mk, mv, p, grid, smem, s))
+             : (accumulate ? launch_main<Bf16, true>(mk, mv, p, grid, smem, s)
+                           : launch_main<Bf16, false>(mk, mv, p, grid, smem, s));
   *launches = 1;
   if (e != cudaSuccess || !accumulate) return e;
   e = cudaFuncSetAttribute(kv16_decode_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -828,18 +612,6 @@ cudaError_t start_decode(const Kv16& c, const Kv16Query& q, bool accumulate,
   kv16_decode_weights_kernel<<<wgrid, kWThreads, lines, s>>>(p);
   *launches = 2;
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulate, uint16_t* out,
-                               void* ws, unsigned wait_limit, int* launches, cudaStream_t s) {
-  return start_decode(c, q, accumulate, nullptr, out, ws, wait_limit, launches, s);
-}
-
-cudaError_t launch_kv16_decode_own(const Kv16& c, const Kv16Query& q, const SharedParts& shared,
-                                   uint16_t* out, void* ws, int* launches, cudaStream_t s) {
-  return start_decode(c, q, false, &shared, out, ws, kTcWaitLimit, launches, s);
 }
 
 }  // namespace oscar

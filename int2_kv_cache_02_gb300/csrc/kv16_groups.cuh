@@ -27,55 +27,67 @@ __device__ __forceinline__ int group_of(const Kv16Groups& g, int b) {
   return ragged_sequence(g.group, g.n, b);
 }
 
-// The line of key tiles that the prefixes' kernel has cut: group i's tiles stand
-// from first on, `tiles` of them for each (KV head, 256 query rows).  Left in the
-// workspace for who joins the records; the last entry's first is the line's end.
+// What the prefixes' kernel leaves in the workspace for who joins the records.
+// All key tiles of 128 tokens stand in one line, and each of `ctas` CTAs takes an
+// equal run of it.  Group by group and, in a group, KV head by KV head, a line
+// has the tiles of `chunks` query tiles (256 rows each): block after block of
+// them, and within a block chunk after chunk.  A single chunk has one block, all
+// its tiles; several have blocks of a run's length or a little more, so that the
+// CTAs that work the same keys for different chunks do so at the same time, and
+// the keys come from HBM once.
 struct SharedLine {
-  int first, tiles;
+  int first;          // place of the group's first tile (the last entry: the line's end)
+  int tiles, chunks;  // tiles of a chunk (0: nothing shared), chunks of a head
+  int r0;             // the group's first query row
 };
 constexpr int kMinTiles = 1;    // key tiles of a CTA's run, if the line has as many
 __host__ __device__ __forceinline__ int line_share(int tiles, int ctas) {
   const int per = tiles / ctas + (tiles % ctas != 0);
   return per > kMinTiles ? per : kMinTiles;
 }
+__host__ __device__ __forceinline__ int line_blocks(int tiles, int chunks, int per) {
+  return chunks > 1 && tiles >= 2 * per ? tiles / per : 1;
+}
+// First tile of block i of n.
+__host__ __device__ __forceinline__ int block_tile(int tiles, int n, int i) {
+  return (int)((long long)tiles * i / n);
+}
 
-
-// The records (m, l, o[128], as the decode's) of the prefixes' kernel.
+// Where the records (m, l, o[128], as the decode's) of both parts lie.
 struct SharedParts {
   Kv16Groups groups;
-  const float* part;        // [total][Hq]: of a row's first run of tiles
-  const float* cut;         // [ctas][256]: of a run that begins inside a row
-  const SharedLine* line;
-  int ctas, tokens, g;      // tokens of a query tile, heads of a group
+  // the prefixes': a chunk's records stand at its rows' own places for the run
+  // that has the chunk's first tile, else with the CTA: [2][256], 0 for a run that
+  // begins inside a block, 1 for one that begins a block
+  float* part;              // [total][Hq]
+  float* cut;               // [ctas][2][256]
+  SharedLine* line;         // [groups + 1]
+  int ctas;
+  // the sequences' own: several queries each: [total][Hq][splits]; one query: as
+  // above, the first run of pages at the row's place, else with the warp
+  float* own;
+  float* own_cut;           // [workers][g]
+  int* own_line;            // [B + 1]: pages of one KV head before sequence b
+  int splits, workers;
+  int tokens, g;            // tokens of a query tile, heads of a group
 };
-// Those of query row r and KV head h, head 0 of its group (head i: i records on).
-struct Joint {
-  int n;
-  const float* first;
-  const float* cut;
-  __device__ __forceinline__ const float* record(int j) const {
-    return j == 0 ? first : cut + (long long)j * 256 * kRecFloats;
+constexpr int kMinRun = 2;      // pages of a warp's run, if the line has as many
+__host__ __device__ __forceinline__ int run_share(int pages, int workers) {
+  const int per = pages / workers + (pages % workers != 0);
+  return per > kMinRun ? per : kMinRun;
+}
+
+// The last i in [0, n) with a[i] <= x (0 if there is none), by a warp.
+__device__ __forceinline__ int warp_search(const int32_t* a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, at = lo + (lane + 1) * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && __ldg(a + min(at, n - 1)) <= x);
+    lo += __popc(le) * step;
+    hi = min(hi, lo + step);
   }
-};
-__device__ __forceinline__ Joint joint_of(const SharedParts& s, const Kv16& c, const Kv16Query& q,
-                                          int r, int h, int i) {
-  Joint x{0, nullptr, nullptr};
-  if (i < 0) return x;
-  const int tiles = __ldcg(&s.line[i].tiles);
-  if (tiles <= 0) return x;
-  int r0 = __ldg(s.groups.group + i), r1 = __ldg(s.groups.group + i + 1);
-  if (q.start) r0 = __ldg(q.start + r0), r1 = __ldg(q.start + r1);
-  if (r < r0 || r >= r1) return x;
-  const int two = 2 * s.tokens, chunks = (r1 - r0 + two - 1) / two;
-  const int chunk = (r - r0) / two, in = (r - r0) % two, w = in >= s.tokens ? 1 : 0;
-  const long long at = __ldcg(&s.line[i].first) + ((long long)h * chunks + chunk) * tiles;
-  const int per = line_share(__ldcg(&s.line[s.groups.n].first), s.ctas);
-  const int c0 = (int)(at / per);
-  if (c0 >= s.ctas) return x;
-  x.n = (int)min((at + tiles - 1) / per, (long long)s.ctas - 1) - c0 + 1;
-  x.first = s.part + ((long long)r * q.Hq + h * s.g) * kRecFloats;
-  x.cut = s.cut + ((long long)c0 * 256 + w * 128 + (in - w * s.tokens) * s.g) * kRecFloats;
-  return x;
+  return lo;
 }
 
 }  // namespace oscar

