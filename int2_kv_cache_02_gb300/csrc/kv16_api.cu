@@ -101,11 +101,12 @@ bool decode_size_ok(const oscar_kv16_cache* c, int max_tok) {
   return c->B <= kMaxDecodeBatch && rows <= kMaxDecodeRows && rows * blocks <= kMaxTokens;
 }
 
-// The key tiles of 128 tokens of all (query tile, KV head) rows are numbered in 32 bits.
+// The key tiles of 128 tokens of all rows of the line (the groups' and the
+// sequences' 256-row chunks), and a few places a row, are numbered in 32 bits.
 bool shared_size_ok(const oscar_kv16_cache* c, int Hq, int n_groups, int total, int max_tok) {
   const long long two = 2 * (128 / (Hq / c->Hkv));
-  const long long rows = (total / two + n_groups) * c->Hkv;
-  const long long tiles = (std::min<long long>(max_tok, capacity(c)) + 127) / 128;
+  const long long rows = (2 * (total / two) + n_groups + c->B) * c->Hkv;
+  const long long tiles = (std::min<long long>(max_tok, capacity(c)) + 127) / 128 + 8;
   return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxTokens &&
          rows <= kMaxTokens && rows * tiles <= kMaxTokens;
 }
@@ -175,8 +176,7 @@ oscar_status shared(const oscar_kv16_cache* c, const uint16_t* q, long long q_st
   if (!shared_size_ok(c, Hq, n_groups, total, max_tok)) return OSCAR_ERR_UNSUPPORTED;
   if (total == 0) return OSCAR_OK;
   Kv16 v = view(c);
-  if (!workspace ||
-      ws_bytes < kv16_shared_ws_bytes(v, Hq, n_groups, total, !start, max_tok, window, n_sink))
+  if (!workspace || ws_bytes < kv16_shared_ws_bytes(v, Hq, n_groups, total, max_tok))
     return OSCAR_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
   const size_t heads = (size_t)total * Hq;
@@ -392,7 +392,7 @@ size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int H
       !window_ok(0.0f, max_tok, window, n_sink) ||
       !shared_size_ok(c, Hq, n_groups, c->B, max_tok) || !decode_size_ok(c, max_tok))
     return 0;
-  return kv16_shared_ws_bytes(view(c), Hq, n_groups, c->B, true, max_tok, window, n_sink);
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, c->B, max_tok);
 }
 
 oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
@@ -413,7 +413,7 @@ size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, in
   if (check(c) != OSCAR_OK || !heads_ok(Hq, c->Hkv) || n_groups < 1 || total <= 0 ||
       !window_ok(0.0f, max_tok, window, n_sink) || !shared_size_ok(c, Hq, n_groups, total, max_tok))
     return 0;
-  return kv16_shared_ws_bytes(view(c), Hq, n_groups, total, false, max_tok, window, n_sink);
+  return kv16_shared_ws_bytes(view(c), Hq, n_groups, total, max_tok);
 }
 
 oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,

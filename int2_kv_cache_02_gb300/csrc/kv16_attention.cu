@@ -71,9 +71,7 @@ cudaError_t launch_kv16_attention(const Kv16& c, const Kv16Query& q, uint16_t* o
   p.out = out;
   p.lse = lse;
   p.part = static_cast<float*>(ws);
-  p.cut = nullptr;
-  p.line = nullptr;
-  p.groups = Kv16Groups{};
+  p.line = SharedParts{};
   p.g = q.Hq / c.Hkv;
   p.tokens = 128 / p.g;
   const long long tiles = attention_tiles(c.B, p.g, q.total);

@@ -64,12 +64,10 @@
 // Few tiles over a long cache: the key tiles are split over several CTAs, which
 // leave (m, l, o[128]) records that a second kernel joins.
 //
-// Parts.  Sequences that share a prefix have their attention worked in two parts,
-// by the same kernel: kPrefix the shared blocks, for all sequences of a group at
-// once, kOwn the blocks behind them, a sequence at a time.  Both leave records.
-// In kPrefix the key tiles of all groups stand in one line (SharedLine), and every
-// CTA takes an equal run of it (its items): groups of unequal length leave no CTA
-// idle.
+// kLine: sequences that share prefixes.  The same kernel over a line of work (see
+// kv16_groups.cuh) in which a group's queries meet its shared blocks together and
+// each sequence's queries the blocks behind; an item is the piece of a CTA's run
+// that lies in one row of the line.  All items leave records.
 #pragma once
 
 #include <algorithm>
@@ -85,9 +83,12 @@ namespace {
 
 constexpr int kSoftmaxWarps = 8;       // a warpgroup per query tile, a thread per row
 constexpr int kThreads = kSoftmaxWarps * 32 + 128;
-enum Part { kWhole, kPrefix, kOwn };
-// (The prefix's line of tiles takes a stage's room, and four keep up with HBM.)
-constexpr int stages_of(int part) { return part == kPrefix ? 4 : 5; }
+enum Part { kWhole, kLine };
+// Floats of a record and before its o.
+constexpr int rec_floats(int part) { return part == kWhole ? kRecFloats : kPartFloats; }
+constexpr int rec_head(int part) { return part == kWhole ? 4 : kPartHead; }
+// (The line's entries take a stage's room, and four keep up with HBM.)
+constexpr int stages_of(int part) { return part == kLine ? 4 : 5; }
 constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
 constexpr int kHalf = 16384;
 constexpr int kKeyPages = 4;           // pages of a key tile
@@ -105,10 +106,8 @@ struct AttnParams {
   Kv16Query q;
   uint16_t* out;
   float* lse;
-  float* part;          // [total * Hq][splits][kRecFloats] if splits > 1 or a part
-  float* cut;           // kPrefix: see SharedParts
-  SharedLine* line;     // kPrefix
-  Kv16Groups groups;    // kPrefix, kOwn
+  float* part;          // [total * Hq][splits][kRecFloats] if splits > 1
+  SharedParts line;     // kLine
   int g, tokens;        // heads of a group, tokens of a query tile
   int tiles;            // upper bound on work items of one KV head and split
   int splits;
@@ -122,7 +121,9 @@ constexpr int kItems = 4;              // work items on their way to the other w
 // A work item as the scheduling warp hands it on.
 struct Item {
   int stop;            // no more items
-  int b, h, split, n;  // (kPrefix: b is the group's first sequence, n the one behind its last)
+  int b, h, split, n;
+  int end;             // kLine: the sequence behind a group's last (b is its first), -1: b's own
+  int only;            // kLine: the query tile that works it alone, or -1
   int row0, nrow;      // first row of q, tokens (of one or two tiles)
   int at0;             // position of the first token
   Span sp;
@@ -146,7 +147,6 @@ constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: al
 // Work item x.  One KV head's items are numbered through: sequence b's start
 // at start[b] / (2 tokens) + b, which leaves room for all of them; those left
 // over are empty (false).
-template <int PART>
 __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) {
   const int two = 2 * p.tokens, per_split = p.tiles * p.c.Hkv;
   it.split = x / per_split;
@@ -176,12 +176,6 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
   it.nrow = min(two, nq - q0);
   it.at0 = it.n - nq + q0;
   it.sp = Span(it.at0, it.at0 + it.nrow - 1, p.q.window, p.q.n_sink);
-  int shared = 0;
-  if constexpr (PART == kOwn) {
-    const int i = group_of(p.groups, it.b);
-    if (i >= 0) shared = shared_of(p.c, p.groups, i, p.q.max_tok, false).blocks;
-    it.sp = it.sp.from(shared);
-  }
   const int kt = (it.sp.blocks + kKeyPages - 1) / kKeyPages;
   it.k0 = (int)((long long)kt * it.split / p.splits);
   it.k1 = (int)((long long)kt * (it.split + 1) / p.splits);
@@ -190,9 +184,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
   if (it.nrow > p.tokens) {
     // the first tile's keys end before the second's
     it.cnt[1] = it.cnt[0];
-    Span sp(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink);
-    if constexpr (PART == kOwn) sp = sp.from(shared);
-    const int blocks = sp.blocks;
+    const int blocks = Span(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink).blocks;
     it.cnt[0] = min(it.k1, max(it.k0, (blocks + kKeyPages - 1) / kKeyPages)) - it.k0;
   }
   it.clear = it.k1 > it.k0 && it.k1 == kt && it.n % kPage != 0 &&
@@ -200,18 +192,21 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
   return true;
 }
 
-// What kPrefix works for a group: its sequences' queries [r0, r1) against the
-// blocks of `sp`.  One thread looks, or a warp (step 32, one answer).
-struct Piece {
+__device__ __forceinline__ int key_tiles(int blocks) { return (blocks + kKeyPages - 1) / kKeyPages; }
+// Places of a row of the line.
+__device__ __forceinline__ int row_places(int tiles) { return tiles > 0 ? tiles + kRowCost : 0; }
+
+// A group's entry of the line: its sequences' queries [r0, r1) against the blocks
+// of `sp`.  One thread looks, or a warp (step 32, one answer).
+struct GroupEntry {
   Shared s;
   int r0, r1;
   Span sp;
-  __device__ __forceinline__ int tiles() const { return (sp.blocks + kKeyPages - 1) / kKeyPages; }
 };
-__device__ __forceinline__ Piece group_piece(const AttnParams& p, int i, int first, int step,
-                                             bool report) {
-  Piece x;
-  x.s = shared_of(p.c, p.groups, i, p.q.max_tok, report);
+__device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, int first, int step,
+                                                  bool report) {
+  GroupEntry x;
+  x.s = shared_of(p.c, p.line.groups, i, p.q.max_tok, report);
   x.r0 = x.s.lead;
   x.r1 = x.s.end;
   if (p.q.start && x.r1 > x.r0) {
@@ -243,22 +238,64 @@ __device__ __forceinline__ Piece group_piece(const AttnParams& p, int i, int fir
   return x;
 }
 
-// The line of key tiles: group i's begin at first[i] (no more than the largest
-// int in all, so that groups that overlap do not wrap around).  All threads of
-// the CTA; ends with a barrier.
-__device__ __forceinline__ void line_of_tiles(const AttnParams& p, int* first, int* scan) {
+// A sequence's own entry: nq queries from row r0 on, the first at position at0,
+// against its blocks from `shared` on.
+struct OwnEntry {
+  int r0, nq, n, at0, shared;
+  __device__ __forceinline__ Span span(const AttnParams& p, int tok, int count) const {
+    return Span(at0 + tok, at0 + tok + count - 1, p.q.window, p.q.n_sink).from(shared);
+  }
+  // key tiles of chunk i
+  __device__ __forceinline__ int tiles(const AttnParams& p, int i) const {
+    const int two = 2 * p.tokens;
+    return key_tiles(span(p, i * two, min(two, nq - i * two)).blocks);
+  }
+};
+__device__ __forceinline__ OwnEntry own_entry(const AttnParams& p, int b, bool report) {
+  OwnEntry x;
+  x.r0 = b;
+  x.nq = 1;
+  x.n = kv16_length(p.c, b, p.q.max_tok);
+  bool ok = x.n >= 0;
+  if (p.q.start) {
+    const int r0 = __ldg(p.q.start + b), r1 = __ldg(p.q.start + b + 1);
+    x.r0 = r0;
+    x.nq = r1 - r0;
+    if (r0 < 0 || r1 > p.q.total || r1 < r0) x.nq = 0, ok = false;
+    ok = ok && x.n >= x.nq;            // (fewer tokens than queries)
+  }
+  if (!ok && report) record_error(p.c.status, kDevErrBadPaged);
+  x.n = max(x.n, 0);
+  x.at0 = x.n - x.nq;
+  const int i = group_of(p.line.groups, b);
+  x.shared = i < 0 ? 0 : shared_of(p.c, p.line.groups, i, p.q.max_tok, false).blocks;
+  return x;
+}
+
+__device__ __forceinline__ int saturate(long long x) { return (int)min(x, 0x7fffffffLL); }
+
+// The entries' first places, first[0 .. groups + B] (no more than the largest int,
+// so that groups that overlap do not wrap around).  All threads of the CTA; ends
+// with a barrier.
+__device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* scan) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int two = 2 * p.tokens;
+  const int two = 2 * p.tokens, G = p.line.groups.n, entries = G + p.c.B;
+  const bool report = blockIdx.x == 0;
   unsigned carry = 0;      // sums of two numbers below 2^31
   auto plus = [](unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); };
-  for (int i0 = 0; i0 < p.groups.n; i0 += kThreads) {
-    const int i = i0 + tid;
+  for (int e0 = 0; e0 < entries; e0 += kThreads) {
+    const int e = e0 + tid;
     unsigned x = 0;
-    Piece g;
-    if (i < p.groups.n) {
-      g = group_piece(p, i, 0, 1, blockIdx.x == 0);
-      const long long n = (long long)((g.r1 - g.r0 + two - 1) / two) * p.c.Hkv * g.tiles();
-      x = (unsigned)min(n, 0x7fffffffLL);
+    if (e < G) {
+      const GroupEntry y = group_entry(p, e, 0, 1, report);
+      const int places = row_places(key_tiles(y.sp.blocks));
+      x = (unsigned)saturate((long long)((y.r1 - y.r0 + two - 1) / two) * p.c.Hkv * places);
+      if (report) p.line.group[e] = make_int2(places, y.r0);
+    } else if (e < entries) {
+      const OwnEntry y = own_entry(p, e - G, report);
+      long long n = 0;
+      for (int i = 0; i * two < y.nq; ++i) n += row_places(y.tiles(p, i));
+      x = (unsigned)saturate(n * p.c.Hkv);
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -274,60 +311,112 @@ __device__ __forceinline__ void line_of_tiles(const AttnParams& p, int* first, i
       if (w < warp) base = plus(base, (unsigned)scan[w]);
       carry = plus(carry, (unsigned)scan[w]);
     }
-    if (i < p.groups.n) {
-      first[i] = (int)plus(base, before);
-      if (blockIdx.x == 0)
-        p.line[i] = SharedLine{first[i], g.tiles(), (g.r1 - g.r0 + two - 1) / two, g.r0};
+    if (e < entries) {
+      first[e] = (int)plus(base, before);
+      if (report) p.line.first[e] = first[e];
     }
     __syncthreads();
   }
   if (tid == 0) {
-    first[p.groups.n] = (int)carry;
-    if (blockIdx.x == 0) p.line[p.groups.n] = SharedLine{(int)carry, 0, 0, 0};
+    first[entries] = (int)carry;
+    if (report) p.line.first[entries] = (int)carry;
   }
   __syncthreads();
 }
 
-// The item at place x of the line, as far as x1.
-__device__ __forceinline__ void find_piece(const AttnParams& p, const int* first, int x, int x1,
+// The item at place x of the line, as far as x1; its number of places.  A warp.
+// (Maxima and minima: whatever the groups and lengths hold by now, what follows
+// stays in bounds.)
+__device__ __forceinline__ int find_piece(const AttnParams& p, const int* first, int x, int x1,
                                            Item& it) {
-  int lo = 0, hi = p.groups.n;     // first[i] <= x < first[i + 1]
+  const int G = p.line.groups.n, two = 2 * p.tokens, lane = threadIdx.x & 31;
+  int lo = 0, hi = G + p.c.B;     // first[i] <= x < first[i + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= x) lo = mid; else hi = mid;
   }
-  const Piece g = group_piece(p, lo, threadIdx.x & 31, 32, false);
-  // (the maxima: whatever the groups hold by now, what follows stays in bounds)
-  const int two = 2 * p.tokens, chunks = max((g.r1 - g.r0 + two - 1) / two, 1);
-  const int tiles = max(g.tiles(), 1), at = x - first[lo];
-  const int per_head = chunks * tiles;          // (no more than the line has: it fits)
-  it.h = min(at / per_head, p.c.Hkv - 1);
-  const int y = at - it.h * per_head, z = min(y / chunks, tiles - 1);
-  const int blocks = line_blocks(tiles, chunks, line_share(first[p.groups.n], gridDim.x));
-  int i = (int)((long long)z * blocks / tiles);
-  if (block_tile(tiles, blocks, i + 1) <= z) ++i;
-  const int t0 = block_tile(tiles, blocks, i), t1 = block_tile(tiles, blocks, i + 1);
-  const int in = y - chunks * t0, chunk = min(in / (t1 - t0), chunks - 1);
-  it.b = g.s.lead;
-  it.n = g.s.end;
-  it.row0 = g.r0 + chunk * two;
-  it.nrow = min(two, g.r1 - it.row0);
-  it.sp = g.sp;
-  it.k0 = t0 + in - chunk * (t1 - t0);
-  it.k1 = min(min((long long)it.k0 + (x1 - x), (long long)t1),
-              (long long)it.k0 + (first[lo + 1] - x));
-  it.split = it.k0 == 0 ? 0 : it.k0 > t0 ? 1 : 2;       // where the records go
+  const int at = x - first[lo];
+  int from, to, tiles0 = 0;       // places of the row; tiles0: of a sequence's first query tile, whose keys end first
+  it.clear = false;
+  if (lo < G) {
+    const GroupEntry y = group_entry(p, lo, lane, 32, false);
+    const int chunks = max((y.r1 - y.r0 + two - 1) / two, 1);
+    const int places = max(row_places(key_tiles(y.sp.blocks)), 1);
+    const int per_head = chunks * places;         // (no more than the line has: it fits)
+    it.h = min(at / per_head, p.c.Hkv - 1);
+    const int in_head = at - it.h * per_head, z = min(in_head / chunks, places - 1);
+    const int blocks = line_blocks(places, chunks, line_share(first[G + p.c.B], gridDim.x));
+    int i = (int)((long long)z * blocks / places);
+    if (block_place(places, blocks, i + 1) <= z) ++i;
+    const int t0 = block_place(places, blocks, i), t1 = block_place(places, blocks, i + 1);
+    const int in = in_head - chunks * t0, chunk = min(in / (t1 - t0), chunks - 1);
+    it.b = y.s.lead;
+    it.end = y.s.end;
+    it.n = it.at0 = 0;
+    it.row0 = y.r0 + chunk * two;
+    it.nrow = min(two, y.r1 - it.row0);
+    it.sp = y.sp;
+    from = t0 + in - chunk * (t1 - t0);
+    to = t1;
+    it.split = from <= kRowCost ? 0 : from > t0 ? 1 : 2;  // where the records go
+  } else {
+    const OwnEntry y = own_entry(p, lo - G, false);
+    const int chunks = max((y.nq + two - 1) / two, 1);
+    const int per_head = max((first[lo + 1] - first[lo]) / p.c.Hkv, 1);
+    it.h = min(at / per_head, p.c.Hkv - 1);
+    int in = at - it.h * per_head, chunk = 0;
+    if (chunks > 1) {
+      // the chunk that has tile `in` of the head's
+      for (int c0 = 0;; c0 += 32) {
+        const int mine = c0 + lane < chunks ? row_places(y.tiles(p, c0 + lane)) : 0;
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int z = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += z;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, sum > in);
+        if (past == 0 && c0 + 32 < chunks) {
+          in -= __shfl_sync(0xffffffffu, sum, 31);
+          continue;
+        }
+        const int l = past ? __ffs(past) - 1 : 31;
+        chunk = min(c0 + l, chunks - 1);
+        in -= __shfl_sync(0xffffffffu, sum - mine, l);
+        break;
+      }
+    }
+    it.b = lo - G;
+    it.end = -1;
+    it.n = y.n;
+    it.row0 = y.r0 + chunk * two;
+    it.nrow = min(two, y.nq - chunk * two);
+    it.at0 = y.at0 + chunk * two;
+    it.sp = y.span(p, chunk * two, it.nrow);
+    from = max(in, 0);
+    to = row_places(key_tiles(it.sp.blocks));
+    tiles0 = key_tiles(y.span(p, chunk * two, min(it.nrow, p.tokens)).blocks);
+    it.split = from <= kRowCost ? -1 : 1;
+  }
+  const int end = (int)min(min((long long)from + (x1 - x), (long long)to),
+                           (long long)from + (first[lo + 1] - x));
+  it.k0 = max(from - kRowCost, 0);
+  it.k1 = max(end - kRowCost, 0);
   it.cnt[0] = it.nrow > 0 ? max(it.k1 - it.k0, 0) : 0;
   it.cnt[1] = it.nrow > p.tokens ? it.cnt[0] : 0;
-  it.clear = false;
-  it.at0 = 0;
+  if (lo >= G && it.cnt[0] > 0) {
+    if (it.cnt[1] > 0) it.cnt[0] = min(it.k1, max(it.k0, tiles0)) - it.k0;
+    it.clear = end == to && it.n % kPage != 0 &&
+               it.sp.block(it.sp.blocks - 1) == (it.n - 1) / kPage;
+  }
+  return max(end - from, 1);
 }
 
-// The record of a row: at the row's place, or (split 1, 2) the CTA's.
-__device__ __forceinline__ float* prefix_record(const AttnParams& p, int split, long long row,
-                                                int cut_row) {
-  return split == 0 ? p.part + row * kRecFloats
-                    : p.cut + (((long long)blockIdx.x * 2 + split - 1) * 256 + cut_row) * kRecFloats;
+// The record of a row of an item: at the row's place, or the CTA's.
+__device__ __forceinline__ float* line_record(const AttnParams& p, int split, long long row,
+                                              int cut_row) {
+  return split <= 0 ? (split == 0 ? p.line.prefix : p.line.own) + row * kPartFloats
+                    : p.line.cut + (((long long)blockIdx.x * 2 + split - 1) * 256 + cut_row) * kPartFloats;
 }
 
 // The position of query row r of a group's sequences [b0, b1).
@@ -389,13 +478,13 @@ __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int 
                                          int cut_row) {
   const int lane = threadIdx.x & 31;
   const bool record = PART != kWhole || p.splits > 1;
-  float* rec = PART == kPrefix ? prefix_record(p, split, row, cut_row)
-                               : p.part + (row * p.splits + split) * kRecFloats;
+  float* rec = PART == kLine ? line_record(p, split, row, cut_row)
+                               : p.part + (row * p.splits + split) * rec_floats(PART);
   uint2* out = reinterpret_cast<uint2*>(p.out + row * kD) + lane;
   float x[4];
   if (record) {
     if (rec[1] != rec[1]) return;            // the sum
-    const float4 v = *reinterpret_cast<const float4*>(rec + 4 + 4 * lane);
+    const float4 v = *reinterpret_cast<const float4*>(rec + rec_head(PART) + 4 * lane);
     x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
   } else {
     const uint2 v = *out;
@@ -431,7 +520,7 @@ __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int 
   for (int i = 0; i < 4; ++i)
     if ((open >> i) & 1u) x[i] = o[i] * f;
   if (record)
-    *reinterpret_cast<float4*>(rec + 4 + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(rec + rec_head(PART) + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
   else
     *out = make_uint2(T::pack(x[0], x[1]), T::pack(x[2], x[3]));
 }
@@ -447,17 +536,22 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   uint8_t* sq = smem;                            // two query tiles
   uint8_t* ring = smem + 2 * kTileBytes;
   auto& sm = *reinterpret_cast<Smem<kStages>*>(smem + (2 + kStages) * kTileBytes);
-  int* first = reinterpret_cast<int*>(&sm + 1);  // kPrefix: [groups + 1], then a number a warp
+  int* first = reinterpret_cast<int*>(&sm + 1);  // kLine: [groups + B + 1], then a number a warp
   if (smem_u32(smem) & 1023) {                   // the swizzle counts on it
     if (tid == 0) record_error(p.c.status, kDevErrWaitTimeout);
     return;
   }
 
-  int x0 = 0, x1 = 0;                            // kPrefix: the CTA's run of the line
-  if constexpr (PART != kWhole) asm volatile("griddepcontrol.launch_dependents;");
-  if constexpr (PART == kPrefix) {
-    line_of_tiles(p, first, first + p.groups.n + 1);
-    const int total = first[p.groups.n], per = line_share(total, gridDim.x);
+  int x0 = 0, x1 = 0;                            // kLine: the CTA's run of the line
+  if constexpr (PART != kWhole) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (tid < 3)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(tid == 0 ? &map_q : tid == 1 ? &map_k : &map_v));
+  }
+  if constexpr (PART == kLine) {
+    const int entries = p.line.groups.n + p.c.B;
+    line_up(p, first, first + entries + 1);
+    const int total = first[entries], per = line_share(total, gridDim.x);
     x0 = (int)min((long long)blockIdx.x * per, (long long)total);
     x1 = (int)min((long long)x0 + per, (long long)total);
     if (x0 == x1) return;
@@ -511,17 +605,27 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       for (int round = 0; ok; ++round) {
         bool stop;
         Item it;
-        if constexpr (PART == kPrefix) {
+        if constexpr (PART == kLine) {
           stop = x0 >= x1;
           if (!stop) {
-            find_piece(p, first, x0, x1, it);
-            x0 += max(it.k1 - it.k0, 1);
+            x0 += find_piece(p, first, x0, x1, it);
+            if (it.cnt[0] <= 0 && it.cnt[1] <= 0) continue;      // (places without tiles)
+            // rows for one query tile: the two take such items in turn, each at its
+            // own pace
+            it.only = it.nrow > p.tokens ? -1 : (int)(n & 1);
+            if (it.only == 1) {
+              it.row0 -= p.tokens;
+              it.at0 -= p.tokens;
+              it.nrow += p.tokens;
+              it.cnt[1] = it.cnt[0];
+              it.cnt[0] = 0;
+            }
           }
         } else {
           const long long x = (long long)round * grid +
                               ((round & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
           stop = (long long)round * grid >= items;
-          if (!stop && (x >= items || !find_item<PART>(p, (int)x, it))) continue;
+          if (!stop && (x >= items || !find_item(p, (int)x, it))) continue;
         }
         it.stop = stop;
         if (n >= kItems) ok = tc5_wait(&sm.i_empty[n % kItems], (n / kItems - 1) & 1, state);
@@ -541,16 +645,45 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const unsigned qbytes = 2 * 64 * 2 * p.g * p.tokens;
       unsigned used = 0, q_used[2] = {0, 0}, tails = 0;
       unsigned kept = ~0u;     // the tile that has come and is not passed on yet
+      int kept_page = 0, kept_at = 0;          // kLine: its last page, and the tokens there
+      // Clears the rows behind the sequence's last token in the kept tile and passes
+      // it on.
+      auto pass_on = [&](int page, int tokens) {
+        const unsigned st = kept % kStages;
+        ok = ok && tc5_wait(&sm.tail, (tails - 1) & 1, state);
+        if (!ok) return;
+        if (lane >= tokens) {
+          uint8_t* r = ring + st * kTileBytes + (page * kPage + lane) * 128;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            reinterpret_cast<uint4*>(r + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[st]);
+        kept = ~0u;
+      };
+      // kLine: what may take long is waited for only once the kept tile is passed on,
+      // but what is ready is begun before (the kept tile's way here and the next
+      // item's first copies overlap)
+      auto settled_wait = [&](uint64_t* bar, unsigned parity) -> bool {
+        if (PART == kLine && kept != ~0u) {
+          if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+          pass_on(kept_page, kept_at);
+        }
+        return ok && tc5_wait(bar, parity, state);
+      };
       for (unsigned ni = 0; ok; ++ni) {
-        const Item* ip = take(ni);
-        if (!(ok = ip != nullptr) || ip->stop) break;
+        if (!(ok = settled_wait(&sm.i_full[ni % kItems], (ni / kItems) & 1))) break;
+        const Item* ip = &sm.item[ni % kItems];
+        if (ip->stop) break;
         const Item it = *ip;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || it.cnt[w] == 0) continue;
-          if (q_used[w] > 0) ok = tc5_wait(&sm.q_empty[w], (q_used[w] - 1) & 1, state);
+          if (q_used[w] > 0) ok = settled_wait(&sm.q_empty[w], (q_used[w] - 1) & 1);
           if (!ok) continue;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sm.q_full[w], qbytes);
@@ -585,7 +718,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const unsigned st = used % kStages;
-            if (used >= kStages) ok = ok && tc5_wait(&sm.empty[st], (used / kStages - 1) & 1, state);
+            if (used >= kStages) ok = ok && settled_wait(&sm.empty[st], (used / kStages - 1) & 1);
             if (!ok || (kv == 1 && it.clear && k + 1 == it.k1)) break;
             ask(kv, st, &sm.full[st]);
             ++used;
@@ -596,23 +729,18 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           // tile that has them, the last one, lands on a barrier of this warp's,
           // which clears them and only then passes the tile on.
           const unsigned st = used % kStages;
-          ask(1, st, &sm.tail);
-          kept = used++;
-          ok = tc5_wait(&sm.tail, tails++ & 1, state);
+          if (PART == kLine && kept != ~0u) pass_on(kept_page, kept_at);
           if (!ok) break;
-          const int page = it.sp.blocks - 1 - (it.k1 - 1) * kKeyPages;
-          if (it.sp.block(it.sp.blocks - 1) * kPage + lane >= it.n) {
-            uint8_t* r = ring + st * kTileBytes + (page * kPage + lane) * 128;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              reinterpret_cast<uint4*>(r + (i >> 3) * kHalf)[i & 7] = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.full[st]);
-          kept = ~0u;
+          ask(1, st, &sm.tail);
+          ++tails;
+          kept = used++;
+          const int last = it.sp.blocks - 1;
+          kept_page = last - (it.k1 - 1) * kKeyPages;
+          kept_at = it.n - it.sp.block(last) * kPage;
+          if (PART == kWhole) pass_on(kept_page, kept_at);
         }
       }
+      if (PART == kLine && ok && kept != ~0u) pass_on(kept_page, kept_at);
       // what is in flight lands before the memory is given back, whoever gives up
       bool landed = true;
       for (int w = 0; w < 2; ++w)
@@ -663,12 +791,13 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           const Item* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
           const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0;
+          const bool pair = PART == kWhole || ip->only < 0;      // the tiles take turns
           mbar_arrive(&sm.i_empty[ni % kItems]);
           if (nk <= 0) continue;
           // a stage that this tile has no use for is given back as it comes
           ok = tc5_wait(&sm.full[st], ph, state);
           if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, state);
-          if (ok) ok = my_turn();
+          if (ok && pair) ok = my_turn();
           if (!ok) break;
           if (cnt > 0) {
             tc5_fence_after();
@@ -678,7 +807,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           } else {
             mbar_arrive(&sm.empty[st]);
           }
-          mbar_arrive(&sm.turn[w ^ 1]);
+          if (pair) mbar_arrive(&sm.turn[w ^ 1]);
           next();
           for (int j = 0; j < nk && ok; ++j) {
             const unsigned vs = st, vp = ph;
@@ -687,7 +816,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ok = tc5_wait(&sm.full[vs], vp, state);
             if (ok && more) ok = tc5_wait(&sm.full[st], ph, state);
             if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, state);
-            if (ok) ok = my_turn();
+            if (ok && pair) ok = my_turn();
             if (!ok) break;
             if (j < cnt) {
               // P comes in halves of 64 keys
@@ -705,11 +834,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                 tc5_mma_ts(to, ts + 32 + 8 * i, v + i * (2048 >> 4), id_o, true);
               if (j + 1 < cnt) qk(st);
               else tc5_commit(&sm.o_full[w]);
-              mbar_arrive(&sm.turn[w ^ 1]);
+              if (pair) mbar_arrive(&sm.turn[w ^ 1]);
               tc5_commit(&sm.empty[vs]);
               if (j + 2 == cnt) tc5_commit(&sm.q_empty[w]);
             } else {
-              mbar_arrive(&sm.turn[w ^ 1]);
+              if (pair) mbar_arrive(&sm.turn[w ^ 1]);
               mbar_arrive(&sm.empty[vs]);
             }
             if (more) {
@@ -742,28 +871,29 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       if (!(ok = ip != nullptr) || ip->stop) break;
       const int ntok = min(p.tokens, ip->nrow - w * p.tokens), my_n = ip->cnt[w];
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
-      const int seq_end = ip->n;
+      const int seq_end = PART == kLine ? ip->end : 0, only = PART == kLine ? ip->only : -1;
       const int at_first = ip->at0 + w * p.tokens, row_first = ip->row0 + w * p.tokens;
       const Span sp = ip->sp;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
-      if (ntok <= 0) continue;
+      if (ntok <= 0 || (only >= 0 && w != only)) continue;
       // the thread's row; rows past the tile's end work like its last token
       const bool valid = tok < ntok;
       const int at =                                          // (-1: before the first token)
-          PART == kPrefix ? position_of(p, b, seq_end, row_first + min(tok, ntok - 1))
-                          : max(at_first + min(tok, ntok - 1), -1);
+          PART == kLine && seq_end >= 0
+              ? position_of(p, b, seq_end, row_first + min(tok, ntok - 1))
+              : max(at_first + min(tok, ntok - 1), -1);
       // key tiles [in0, in1), counted from k0, whose pages the warp's rows all see
       int in0, in1;
       {
-        const int at_min = PART == kPrefix ? __reduce_min_sync(0xffffffffu, at)
-                                           : __shfl_sync(0xffffffffu, at, 0);
-        const int at_max = PART == kPrefix ? __reduce_max_sync(0xffffffffu, at)
-                                           : __shfl_sync(0xffffffffu, at, 31);
+        const int at_min = PART == kLine ? __reduce_min_sync(0xffffffffu, at)
+                                         : __shfl_sync(0xffffffffu, at, 0);
+        const int at_max = PART == kLine ? __reduce_max_sync(0xffffffffu, at)
+                                         : __shfl_sync(0xffffffffu, at, 31);
         const int first = p.q.window == 0 ? 0 : max(at_max - p.q.window + kPage, 0) / kPage;
         const int v0 = sp.sink_blocks + max(first - sp.w0, 0);
         int v1 = sp.sink_blocks + (at_min + 1) / kPage - sp.w0;            // behind the last
-        if (PART == kPrefix) v1 = min(v1, sp.blocks);
+        if (PART == kLine) v1 = min(v1, sp.blocks);
         in0 = (v0 + kKeyPages - 1) / kKeyPages - k0;
         in1 = max(v1, 0) / kKeyPages - k0;
       }
@@ -890,9 +1020,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const bool record = PART != kWhole || p.splits > 1;
       const float inv = record ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       float odd = 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: a channel is open
-      const int cut_row = w * 128;
-      float* rec = PART == kPrefix ? prefix_record(p, split, row, cut_row + r)
-                                   : p.part + (row * p.splits + split) * kRecFloats;
+      const int cut_row = only >= 0 ? 0 : w * 128;
+      float* rec = PART == kLine ? line_record(p, split, row, cut_row + r)
+                                   : p.part + (row * p.splits + split) * rec_floats(PART);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t o[32];
@@ -911,11 +1041,17 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           odd3 = gather_open<T>(__uint_as_float(o[e + 3]), odd3);
         }
         if (record) {
-          if (valid)
+          if constexpr (PART == kWhole) {
+            if (valid)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
-                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(rec + 4 + 32 * i + e) =
+                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+            if (valid)
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) st_global32(rec + kPartHead + 32 * i + e, o + e);
+          }
         } else {
           uint32_t v[16];
 #pragma unroll
@@ -963,8 +1099,6 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     tc5_fence_after();
     tc5_dealloc(tmem, 512);
   }
-  // (complete only once the prefixes' kernel is, so that who follows has both)
-  if constexpr (PART == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 int sm_count() {

@@ -27,67 +27,52 @@ __device__ __forceinline__ int group_of(const Kv16Groups& g, int b) {
   return ragged_sequence(g.group, g.n, b);
 }
 
-// What the prefixes' kernel leaves in the workspace for who joins the records.
-// All key tiles of 128 tokens stand in one line, and each of `ctas` CTAs takes an
-// equal run of it.  Group by group and, in a group, KV head by KV head, a line
-// has the tiles of `chunks` query tiles (256 rows each): block after block of
-// them, and within a block chunk after chunk.  A single chunk has one block, all
-// its tiles; several have blocks of a run's length or a little more, so that the
-// CTAs that work the same keys for different chunks do so at the same time, and
-// the keys come from HBM once.
-struct SharedLine {
-  int first;          // place of the group's first tile (the last entry: the line's end)
-  int tiles, chunks;  // tiles of a chunk (0: nothing shared), chunks of a head
-  int r0;             // the group's first query row
-};
-constexpr int kMinTiles = 1;    // key tiles of a CTA's run, if the line has as many
-__host__ __device__ __forceinline__ int line_share(int tiles, int ctas) {
-  const int per = tiles / ctas + (tiles % ctas != 0);
-  return per > kMinTiles ? per : kMinTiles;
+// The work of a call stands in one line of key tiles (128 tokens against up to 256
+// query rows), and each of `ctas` CTAs takes an equal run of it.  A row of the line
+// (the tiles of one chunk of query rows and KV head) begins with kRowCost places
+// without a tile, for what it costs to begin and end an item.  Entry i below
+// the number of groups is group i's prefix, the others are the sequences' own
+// blocks behind it.  An entry has its tiles KV head by KV head:
+//  a sequence  chunk of query rows after chunk, each its own tiles (causal: a
+//              later chunk has more)
+//  a group     block after block of places, and within a block chunk after chunk.
+//              A single chunk has one block, the whole row; several have blocks of
+//              a run's length or a little more, so that the CTAs that work the
+//              same keys for different chunks do so at the same time, and the keys
+//              come from HBM once.
+constexpr int kRowCost = 3;
+constexpr int kMinPlaces = 2;   // of a CTA's run, if the line has as many
+__host__ __device__ __forceinline__ int line_share(int places, int ctas) {
+  const int per = places / ctas + (places % ctas != 0);
+  return per > kMinPlaces ? per : kMinPlaces;
 }
-__host__ __device__ __forceinline__ int line_blocks(int tiles, int chunks, int per) {
-  return chunks > 1 && tiles >= 2 * per ? tiles / per : 1;
+// Blocks of a group's row of so many places.
+__host__ __device__ __forceinline__ int line_blocks(int places, int chunks, int per) {
+  return chunks > 1 && places >= 2 * per ? places / per : 1;
 }
-// First tile of block i of n.
-__host__ __device__ __forceinline__ int block_tile(int tiles, int n, int i) {
-  return (int)((long long)tiles * i / n);
+// First place of block i of n.
+__host__ __device__ __forceinline__ int block_place(int places, int n, int i) {
+  return (int)((long long)places * i / n);
 }
 
-// Where the records (m, l, o[128], as the decode's) of both parts lie.
+// A record of a run: m, l, 6 floats' room, o[128]; every piece that a thread
+// writes is a whole 32-byte sector (with 16-byte pieces, of the split records'
+// layout, an item of 256 rows took 8 us to write instead of 1).
+constexpr int kPartHead = 8, kPartFloats = kPartHead + 128;
+
+// The line and its records in the workspace (32-byte aligned).  A run that has a
+// row's first tile leaves its records at the query rows' places, else with the
+// CTA: [2][256], 0 for a run that begins inside a block, 1 for one that begins a
+// block.
 struct SharedParts {
   Kv16Groups groups;
-  // the prefixes': a chunk's records stand at its rows' own places for the run
-  // that has the chunk's first tile, else with the CTA: [2][256], 0 for a run that
-  // begins inside a block, 1 for one that begins a block
-  float* part;              // [total][Hq]
+  float* prefix;            // [total][Hq]
+  float* own;               // [total][Hq]
   float* cut;               // [ctas][2][256]
-  SharedLine* line;         // [groups + 1]
+  int* first;               // [groups + B + 1]: the entries' first places, the line's end
+  int2* group;              // [groups]: places of a row, the first query row
   int ctas;
-  // the sequences' own: several queries each: [total][Hq][splits]; one query: as
-  // above, the first run of pages at the row's place, else with the warp
-  float* own;
-  float* own_cut;           // [workers][g]
-  int* own_line;            // [B + 1]: pages of one KV head before sequence b
-  int splits, workers;
   int tokens, g;            // tokens of a query tile, heads of a group
 };
-constexpr int kMinRun = 2;      // pages of a warp's run, if the line has as many
-__host__ __device__ __forceinline__ int run_share(int pages, int workers) {
-  const int per = pages / workers + (pages % workers != 0);
-  return per > kMinRun ? per : kMinRun;
-}
-
-// The last i in [0, n) with a[i] <= x (0 if there is none), by a warp.
-__device__ __forceinline__ int warp_search(const int32_t* a, int n, int x) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5, at = lo + (lane + 1) * step;
-    const unsigned le = __ballot_sync(0xffffffffu, at < hi && __ldg(a + min(at, n - 1)) <= x);
-    lo += __popc(le) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
 
 }  // namespace oscar

@@ -1,384 +1,376 @@
 // Attention of sequences that share a prefix.  A group's whole pages below the
-// prefix's end are worked once for all its sequences, by the tensor-core kernel
-// of the prompt attention (kPrefix: rows are the group's queries, so up to 256
-// (query, head) rows meet each key and value that is read); what stands behind
-// them a sequence at a time, by a kernel of the decode's kind for one query each
-// (kv16_shared_decode.cu), else by the prompt attention's (kOwn).  Both leave
-// records, which a third kernel joins by their maxima and sums.
+// prefix's end are worked once for all its queries, so that up to 256 (query,
+// head) rows meet each key and value that is read; what stands behind them a
+// sequence at a time.  Both by the tensor-core kernel of the prompt attention, over
+// one line of key tiles that its CTAs share evenly (kLine, kv16_groups.cuh); the
+// records that it leaves are joined by their maxima and sums in a second launch.
 #include "kv16_attention.cuh"
 
 namespace oscar {
 namespace {
 
 // What the values that a row sees hold in a channel.
-constexpr unsigned kSeenNan = 1, kSeenPlus = 2, kSeenMinus = 4, kOpen = 8;
+constexpr unsigned kSeenNan = 1, kSeenPlus = 2, kSeenMinus = 4;
 __device__ __forceinline__ unsigned seen_in(float x) {
   return x != x ? kSeenNan : x == INFINITY ? kSeenPlus : x == -INFINITY ? kSeenMinus : 0u;
 }
 
 // Blocks of a chunk are at least a run's length and below two: three runs at most.
 constexpr int kBlockRuns = 3;
-// A line has less than half as many blocks as CTAs where it has chunks.
-constexpr int kMaxCtas = 160;
-constexpr int kList = kBlockRuns * (kMaxCtas / 2 + 1);
+constexpr int kMaxCtas = 160;      // of the prefixes' kernel
 
-// The records of both parts of a (query, KV head) joined, by W warps: as many
-// warps for a head as there are (up to W heads at a time), each every so-many-th
-// record.  Queries that belong to no sequence are left alone.
-//
-// A record may hold an infinity (a visible one) that its factor of 0 turns into
-// NaN.  Where a channel is NaN although the row's sum is a number, what the
-// visible values hold there decides, as in the decode.
-template <class T, int W>
-__global__ void __launch_bounds__(W * 32) kv16_shared_join_kernel(
-    const Kv16 c, const Kv16Query q, const SharedParts s, uint16_t* out, float* lse) {
-  __shared__ float4 s_o[W][32];
-  __shared__ float2 s_ml[W];
-  __shared__ int list[kList];
-  __shared__ unsigned s_ch[kD];
-  __shared__ uint8_t s_nan[kMaxGroup];
-  __shared__ int s_open;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = s.g;
-  const int r = blockIdx.x / c.Hkv, h = blockIdx.x - r * c.Hkv;
-  int b = r, back = 1;
-  if (q.start) {
-    b = warp_search(q.start, c.B, r);
-    const int s0 = __ldg(q.start + b), s1 = __ldg(q.start + b + 1);
-    if (s0 < 0 || s0 > r || r >= s1 || s1 > q.total) return;
-    back = s1 - r;
-  }
-  // the sequence's own records
-  const long long row = (long long)r * q.Hq + h * g;
-  int own = s.splits, w0 = 0;
-  if (!q.start) {
-    const int f0 = __ldcg(s.own_line + b), f1 = __ldcg(s.own_line + b + 1);
-    const int per = run_share(__ldcg(s.own_line + c.B) * c.Hkv, s.workers);
-    const int at = f0 * c.Hkv + h * (f1 - f0);
-    w0 = at / per;
-    own = f1 > f0 ? (at + f1 - f0 - 1) / per - w0 + 1 : 0;
-  }
-  // the prefix's
-  const int i = warp_search(s.groups.group, s.groups.n, b);
-  SharedLine line{0, 0, 0, 0};
-  if (__ldg(s.groups.group + i) <= b && b < __ldg(s.groups.group + i + 1)) {
-    const int4 x = __ldcg(reinterpret_cast<const int4*>(s.line) + i);
-    line = SharedLine{x.x, x.y, x.z, x.w};
-  }
-  int n = own, c0 = 0, blocks = 1, in_chunk = 0;
-  const int two = 2 * s.tokens, chunk = r >= line.r0 ? (r - line.r0) / two : line.chunks;
-  if (line.tiles > 0 && chunk < line.chunks) {
-    const int in = (r - line.r0) % two, w = in >= s.tokens ? 1 : 0;
-    in_chunk = w * 128 + (in - w * s.tokens) * g;
-    const int per = line_share(__ldcg(&s.line[s.groups.n].first), s.ctas);
-    blocks = line_blocks(line.tiles, line.chunks, per);
-    const long long base = line.first + (long long)h * line.chunks * line.tiles;
-    auto ctas_of = [&](int k, int& from) {
-      const int t0 = block_tile(line.tiles, blocks, k), t1 = block_tile(line.tiles, blocks, k + 1);
-      const long long at = base + (long long)line.chunks * t0 + (long long)chunk * (t1 - t0);
-      from = (int)min(at / per, s.ctas - 1LL);
-      return (int)min((at + t1 - t0 - 1) / per, s.ctas - 1LL) - from + 1;
-    };
-    if (blocks == 1) {
-      n += ctas_of(0, c0);
-    } else {
-      for (int k = tid; k < blocks; k += W * 32) {
-        int from;
-        const int m = ctas_of(k, from);
-        for (int x = 0; x < kBlockRuns; ++x)
-          list[k * kBlockRuns + x] = x >= m ? -1 : x > 0 || k > 0 ? (from + x) * 2 + (x == 0) : -2;
-      }
-      n += blocks * kBlockRuns;
-    }
-  }
-  for (int x = tid; x < kD; x += W * 32) s_ch[x] = 0u;
-  if (tid == 0) s_open = 0;
-  __syncthreads();
-  // record j for head 0 of the group, or nullptr
-  auto record = [&](int j) -> const float* {
-    if (j < own)
-      return (q.start ? s.own + (row * own + j) * kRecFloats
-              : j == 0 ? s.own + row * kRecFloats
-                       : s.own_cut + (long long)(w0 + j) * g * kRecFloats);
-    j -= own;
-    const int at = blocks > 1 ? list[j] : j == 0 ? -2 : (c0 + j) * 2;
-    return at == -1 ? nullptr
-           : at < 0 ? s.part + row * kRecFloats
-                    : s.cut + ((long long)at * 256 + in_chunk) * kRecFloats;
-  };
-  int subs = W;      // warps of a head
-  while (subs > 1 && W / subs < g) subs >>= 1;
-  const int sub = warp % subs;
-  for (int h0 = 0; h0 < g; h0 += W / subs) {
-    const int head = h0 + warp / subs;
-    float M = -INFINITY, L = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (head < g) {
-      constexpr int U = 4;       // records in flight
-      for (int j0 = sub; j0 < n; j0 += U * subs) {
-        float2 ml[U];
-        float4 v[U];
-        float mx = M;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + u * subs;
-          const float* e = j < n ? record(j) : nullptr;
-          ml[u] = make_float2(-INFINITY, 0.0f);
-          v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (e) {
-            // (own records of several queries: a head's lie behind one another)
-            e += (j < own && q.start ? head * own : head) * kRecFloats;
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(e));
-            v[u] = __ldcg(reinterpret_cast<const float4*>(e + 4) + lane);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
-        const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
-        M = mx;
-        L *= f;
-        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml[u].x - mx);
-          L += a * ml[u].y;
-          o.x += a * v[u].x;
-          o.y += a * v[u].y;
-          o.z += a * v[u].z;
-          o.w += a * v[u].w;
-        }
-      }
-    }
-    if (subs > 1) {
-      s_o[warp][lane] = o;
-      if (lane == 0) s_ml[warp] = make_float2(M, L);
-      __syncthreads();
-      if (sub == 0 && head < g) {
-        float mx = M;
-        for (int u = 1; u < subs; ++u) mx = fmaxf(mx, s_ml[warp + u].x);
-        const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
-        M = mx;
-        L *= f;
-        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-        for (int u = 1; u < subs; ++u) {
-          const float2 ml = s_ml[warp + u];
-          const float4 v = s_o[warp + u][lane];
-          const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml.x - mx);
-          L += a * ml.y;
-          o.x += a * v.x;
-          o.y += a * v.y;
-          o.z += a * v.z;
-          o.w += a * v.w;
-        }
-      }
-      __syncthreads();
-    }
-    if (sub == 0 && head < g) {
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-      reinterpret_cast<uint2*>(out + (row + head) * kD)[lane] =
-          make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
-      if (lse && lane == 0) lse[row + head] = row_lse<T>(M, L);
-      if (lane == 0) s_nan[head] = L != L;
-      if (L == L) {
-        const float x[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (x[k] != x[k]) {
-            s_ch[4 * lane + k] = kOpen;
-            s_open = 1;
-          }
-      }
-    }
-  }
-  __syncthreads();
-  if (!s_open) return;
-
-  // open channels: what the visible values hold in them
-  const int len = kv16_length(c, b, q.max_tok), at = len < 0 ? -1 : max(len - back, -1);
-  const int gi = group_of(s.groups, b);
+// The channels of a row (4 lane .. 4 lane + 3, relative to its sum) that are NaN
+// although the sum is a number: infinite where the visible values hold infinities
+// of one sign and no NaN.  A record may hold an infinity that its factor of 0 has
+// turned into NaN.  A warp; rare, and as slow as one warp's pass over the values.
+template <class T>
+__device__ __noinline__ float4 settle(const AttnParams& p, int b, int h, int back, float4 x) {
+  const int lane = threadIdx.x & 31;
+  const int len = kv16_length(p.c, b, p.q.max_tok), at = len < 0 ? -1 : max(len - back, -1);
+  const int i = group_of(p.line.groups, b);
   Shared sh{b, b, 0};
-  if (gi >= 0) sh = shared_of(c, s.groups, gi, q.max_tok, false);
-  const Span sp(at, at, q.window, q.n_sink);
-  for (int x = warp; x < sp.blocks; x += W) {
-    const int blk = sp.block(x);
-    const int kr = kv16_block_row(c, blk < sh.blocks ? sh.lead : b, h, blk);
-    if (kr < 0) continue;
+  if (i >= 0) sh = shared_of(p.c, p.line.groups, i, p.q.max_tok, false);
+  const Span sp(at, at, p.q.window, p.q.n_sink);
+  float o[4] = {x.x, x.y, x.z, x.w};
+  unsigned f[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int k = 0; k < sp.blocks; ++k) {
+    bool undecided = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      undecided |= o[u] != o[u] && !(f[u] & kSeenNan) &&
+                   (f[u] & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
+    if (!__any_sync(0xffffffffu, undecided)) break;
+    const int blk = sp.block(k);
+    const int row = kv16_block_row(p.c, blk < sh.blocks ? sh.lead : b, h, blk);
+    if (row < 0) continue;
     const unsigned see =
-        __ballot_sync(0xffffffffu, kv16_visible(blk * kPage + lane, at, q.window, q.n_sink));
-    unsigned f[4] = {0u, 0u, 0u, 0u};
+        __ballot_sync(0xffffffffu, kv16_visible(blk * kPage + lane, at, p.q.window, p.q.n_sink));
 #pragma unroll 8
     for (int t = 0; t < kPage; ++t) {
       uint2 v = make_uint2(0u, 0u);
-      if ((see >> t) & 1u) v = reinterpret_cast<const uint2*>(c.v)[((long long)kr + t) * 32 + lane];
+      if ((see >> t) & 1u)
+        v = reinterpret_cast<const uint2*>(p.c.v)[((long long)row + t) * 32 + lane];
       const float2 a = T::unpack(v.x), z = T::unpack(v.y);
       f[0] |= seen_in(a.x);
       f[1] |= seen_in(a.y);
       f[2] |= seen_in(z.x);
       f[3] |= seen_in(z.y);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (f[k]) atomicOr(&s_ch[4 * lane + k], f[k]);
   }
-  __syncthreads();
-  for (int x = tid; x < g * 64; x += W * 32) {
-    const int head = x >> 6, pair = x & 63;
-    if (s_nan[head]) continue;
-    uint32_t* d = reinterpret_cast<uint32_t*>(out + (row + head) * kD) + pair;
-    float2 v = T::unpack(*d);
-    auto settled = [&](float y, unsigned k) {
-      return y == y ? y : k == (kOpen | kSeenPlus) ? INFINITY : k == (kOpen | kSeenMinus) ? -INFINITY : y;
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (o[u] != o[u] && (f[u] == kSeenPlus || f[u] == kSeenMinus))
+      o[u] = f[u] == kSeenPlus ? INFINITY : -INFINITY;
+  return make_float4(o[0], o[1], o[2], o[3]);
+}
+
+// The CTAs [c0, c0 + n) that have tiles [at, at + tiles) of the line.
+struct Runs {
+  int c0, n;
+};
+__device__ __forceinline__ Runs runs_of(unsigned at, unsigned tiles, unsigned per, int ctas) {
+  const int c0 = min((int)(at / per), ctas - 1);
+  return Runs{c0, min((int)((at + tiles - 1) / per), ctas - 1) - c0 + 1};
+}
+
+// The records of both parts of a row (query, head) joined by a warp, or by `subs`
+// of the CTA's four, each every so-many-th record.  A CTA has rows of one KV head,
+// of `batch` queries one after another.  Queries that belong to no sequence are
+// left alone.
+//
+// Bound by latency where rows are few: groups and the line are a chain of loads,
+// then a record's place takes a few divisions.  So a warp's lanes find 32 records at
+// a time, a lane each, with their maxima and sums, and the outputs follow four at a
+// time.  Bound by instructions where rows are many: so places are found once for
+// the queries of a batch that lie in the same rows of the line.
+constexpr int kJoinWarps = 4;
+template <class T>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batch) {
+  __shared__ float4 s_o[kJoinWarps][32];
+  __shared__ float2 s_ml[kJoinWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SharedParts& s = p.line;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = p.g, two = 2 * p.tokens;
+  const int rows = kJoinWarps / subs, slices = (g + rows - 1) / rows, rh = blockIdx.x / slices;
+  const int first_r = rh / p.c.Hkv * batch, h = rh % p.c.Hkv;
+  const int head = (blockIdx.x - rh * slices) * rows + warp / subs, sub = warp % subs;
+  const int G = s.groups.n, end_r = min(first_r + batch, p.q.total);
+  const unsigned per = line_share(__ldcg(s.first + G + p.c.B), s.ctas), hkv = p.c.Hkv;
+
+  // of the queries [.., same): their sequence, and their rows of the line
+  int same = first_r, b = -1, seq0 = 0, seq1 = 0, group0 = 0, n = 0;
+  // the lane's record: 0 none, 1 and 2 at the row's place, 3 and 4 with a CTA (the
+  // sequence's own, the prefix's)
+  int kind = 0;
+  const float* base = nullptr;
+  Runs own{0, 0}, prefix{0, 0};
+  int blocks = 1, places = 0, chunks = 1, chunk = 0;
+  unsigned at = 0;
+  auto locate = [&](int j) {
+    kind = 0;
+    if (j < own.n) {
+      kind = j == 0 ? 1 : 3;
+      base = j == 0 ? s.own : s.cut + (long long)(own.c0 + j) * 512 * kPartFloats;
+    } else if (j < n) {
+      j -= own.n;
+      int t0 = 0;
+      Runs x = prefix;
+      if (blocks > 1) {
+        const int k = j / kBlockRuns;
+        j -= k * kBlockRuns;
+        t0 = block_place(places, blocks, k);
+        const int t1 = block_place(places, blocks, k + 1), skip = max(kRowCost - t0, 0);
+        x.n = 0;
+        if (t0 + skip < t1)
+          x = runs_of(at + (unsigned)chunks * t0 + (unsigned)chunk * (t1 - t0) + skip,
+                      t1 - t0 - skip, per, s.ctas);
+      }
+      if (j >= x.n) return;
+      const bool first = j == 0 && t0 <= kRowCost;
+      kind = first ? 2 : 4;
+      base = first ? s.prefix
+                   : s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0)) * kPartFloats;
+    }
+  };
+  for (int r = first_r; r < end_r; ++r) {
+    if (r >= same) {
+      same = r + 1;
+      b = r;
+      seq0 = r;
+      seq1 = r + 1;
+      if (p.q.start) {
+        b = ragged_sequence(p.q.start, p.c.B, r);
+        if (b < 0) continue;
+        seq0 = __ldg(p.q.start + b);
+        seq1 = __ldg(p.q.start + b + 1);
+        if (seq0 < 0 || seq1 > p.q.total) {
+          b = -1;
+          continue;
+        }
+      }
+      const int f0 = __ldcg(s.first + G + b), f1 = __ldcg(s.first + G + b + 1);
+      const int i = group_of(s.groups, b), own_chunk = (r - seq0) / two;
+      int to = min(seq1, seq0 + (own_chunk + 1) * two);
+      const int per_head = (int)((unsigned)(f1 - f0) / hkv);
+      int at_own = f0 + per_head * h, tiles = per_head - kRowCost;
+      if (seq1 - seq0 > two) {        // several chunks
+        const OwnEntry y = own_entry(p, b, false);
+        int before = 0;
+        for (int k = lane; k < own_chunk; k += 32) before += row_places(y.tiles(p, k));
+        at_own += (int)__reduce_add_sync(0xffffffffu, before);
+        tiles = y.tiles(p, own_chunk);
+      }
+      own = f1 > f0 && tiles > 0 ? runs_of(at_own + kRowCost, tiles, per, s.ctas) : Runs{0, 0};
+      prefix = Runs{0, 0};
+      blocks = 1;
+      if (i >= 0) {
+        const int2 gr = __ldcg(s.group + i);
+        const int g0 = __ldcg(s.first + i), all = (int)((unsigned)(__ldcg(s.first + i + 1) - g0) / hkv);
+        places = gr.x;
+        group0 = gr.y;
+        chunk = (r - group0) / two;
+        if (places > 0 && r >= group0 && chunk < (chunks = all / places)) {
+          at = g0 + (unsigned)all * h;
+          blocks = line_blocks(places, chunks, per);
+          prefix = blocks > 1 ? Runs{0, blocks * kBlockRuns}
+                              : runs_of(at + (unsigned)(chunk * places) + kRowCost, places - kRowCost,
+                                        per, s.ctas);
+          to = min(to, group0 + (chunk + 1) * two);
+        }
+      }
+      same = to;
+      n = head < g ? own.n + prefix.n : 0;
+      locate(sub + lane * subs);
+    }
+    if (b < 0) continue;
+    const long long row = (long long)r * p.q.Hq + h * g + head;
+    auto cut_row = [&](int in) {
+      in %= two;
+      const int w = in >= p.tokens ? 1 : 0;
+      return w * 128 + (in - w * p.tokens) * g + head;
     };
-    v.x = settled(v.x, s_ch[2 * pair]);
-    v.y = settled(v.y, s_ch[2 * pair + 1]);
-    *d = T::pack(v.x, v.y);
+    float M = -INFINITY, L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int j0 = sub; j0 < n; j0 += 32 * subs) {
+      if (n > 32 * subs) locate(j0 + lane * subs);
+      const float* e = base + (kind <= 2 ? row : cut_row(kind == 3 ? r - seq0 : r - group0)) * kPartFloats;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (kind) ml = __ldcg(reinterpret_cast<const float2*>(e));
+      // (lanes behind the records have none)
+      const int width = n - j0 <= 4 * subs ? 4 : 32;
+      float mx = ml.x;
+      for (int x = width >> 1; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      mx = fmaxf(__shfl_sync(0xffffffffu, mx, 0), M);
+      const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
+      const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml.x - mx);
+      M = mx;
+      float add = a * ml.y;
+      for (int x = width >> 1; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+      L = f * L + __shfl_sync(0xffffffffu, add, 0);
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+      unsigned have = __ballot_sync(0xffffffffu, kind != 0);
+#pragma unroll 1
+      while (have) {
+        constexpr int U = 4;
+        float4 v[U];
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int from = have ? __ffs(have) - 1 : 0;
+          const float* d = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(e), from));
+          w[u] = __shfl_sync(0xffffffffu, a, from);
+          v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (have) v[u] = __ldcg(reinterpret_cast<const float4*>(d + kPartHead) + lane);
+          else w[u] = 0.0f;
+          have &= have - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          o.x += w[u] * v[u].x;
+          o.y += w[u] * v[u].y;
+          o.z += w[u] * v[u].z;
+          o.w += w[u] * v[u].w;
+        }
+      }
+    }
+    if (subs > 1) {
+      __syncthreads();
+      s_o[warp][lane] = o;
+      if (lane == 0) s_ml[warp] = make_float2(M, L);
+      __syncthreads();
+      if (sub > 0) continue;
+      float mx = M;
+      for (int u = 1; u < subs; ++u) mx = fmaxf(mx, s_ml[warp + u].x);
+      const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
+      M = mx;
+      L *= f;
+      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+      for (int u = 1; u < subs; ++u) {
+        const float2 ml = s_ml[warp + u];
+        const float4 v = s_o[warp + u][lane];
+        const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml.x - mx);
+        L += a * ml.y;
+        o.x += a * v.x;
+        o.y += a * v.y;
+        o.z += a * v.z;
+        o.w += a * v.w;
+      }
+    }
+    if (head >= g) continue;
+    const bool open = o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w;
+    if (L == L && __any_sync(0xffffffffu, open)) o = settle<T>(p, b, h, seq1 - r, o);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
+        make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
+    if (p.lse && lane == 0) p.lse[row] = row_lse<T>(M, L);
   }
 }
 
-template <class T, int PART>
-cudaError_t launch_part(const AttnParams& p, int grid, size_t more, bool early, cudaStream_t s) {
+size_t up32(size_t n) { return (n + 31) / 32 * 32; }
+
+// The line's CTAs: one per SM, or as many as there can be runs.
+int line_ctas(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
+  const int two = 2 * (128 / (Hq / c.Hkv));
+  const long long rows = (2LL * (total / two) + n_groups + std::min(c.B, total)) * c.Hkv;
+  const long long places = rows * ((std::min(max_tok, c.cap) + 127) / 128 + kRowCost);
+  return (int)std::max<long long>(
+      1, std::min<long long>(places / kMinPlaces, std::min(sm_count(), kMaxCtas)));
+}
+
+// Where the line and its records lie in the workspace, and how much that takes.
+SharedParts layout(const Kv16& c, int Hq, const Kv16Groups& groups, int total, int max_tok,
+                   uint8_t* ws, size_t* bytes) {
+  SharedParts s;
+  s.groups = groups;
+  s.g = Hq / c.Hkv;
+  s.tokens = 128 / s.g;
+  s.ctas = line_ctas(c, Hq, groups.n, total, max_tok);
+  // (the caller's workspace is 16-byte aligned)
+  uintptr_t at = up32(reinterpret_cast<uintptr_t>(ws));
+  auto take = [&](size_t n) {
+    void* p = reinterpret_cast<void*>(at);
+    at += up32(n);
+    return p;
+  };
+  const size_t rec = kPartFloats * sizeof(float), rows = (size_t)total * Hq;
+  s.prefix = static_cast<float*>(take(rows * rec));
+  s.own = static_cast<float*>(take(rows * rec));
+  s.cut = static_cast<float*>(take((size_t)s.ctas * 512 * rec));
+  s.first = static_cast<int*>(take((size_t)(groups.n + c.B + 1) * sizeof(int)));
+  s.group = static_cast<int2*>(take((size_t)groups.n * sizeof(int2)));
+  *bytes = at - reinterpret_cast<uintptr_t>(ws) + 16;
+  return s;
+}
+
+template <class T>
+cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   CUtensorMap mq, mk, mv;
   if (!kv16_query_map(&mq, p.q, p.c.half, p.g, p.tokens) || !kv16_row_map(&mk, p.c, p.c.k) ||
       !kv16_row_map(&mv, p.c, p.c.v))
     return cudaErrorNotSupported;
-  const auto kernel = kv16_attention_kernel<T, PART>;
-  constexpr int kStages = stages_of(PART);
+  const auto kernel = kv16_attention_kernel<T, kLine>;
+  constexpr int kStages = stages_of(kLine);
   constexpr int fixed = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kStages>);
-  static_assert(fixed + (PART == kPrefix ? (kMaxGroups + 1 + kThreads / 32) * 4 : 0) <= 227 * 1024,
+  static_assert(fixed + (kMaxGroups + kMaxDecodeBatch + 1 + kThreads / 32) * 4 <= 227 * 1024,
                 "shared memory of a CTA");
-  const int smem = fixed + (int)more;
+  const int smem = fixed + (p.line.groups.n + p.c.B + 1 + kThreads / 32) * (int)sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  kernel<<<p.line.ctas, kThreads, smem, s>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // warps of a row, where all rows fit the GPU at once (48 warps an SM); else queries
+  // of a CTA, one after another
+  const long long rows = (long long)p.q.total * p.q.Hq, most = 48LL * sm_count();
+  int subs = 1;
+  while (subs < kJoinWarps && rows * subs * 2 <= most) subs *= 2;
+  const int at_once = kJoinWarps / subs;
+  const int batch = (int)std::min<long long>((rows + most - 1) / most, 32);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = kThreads;
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = (unsigned)((long long)((p.q.total + batch - 1) / batch) * p.c.Hkv *
+                          ((p.g + at_once - 1) / at_once));
+  cfg.blockDim = kJoinWarps * 32;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p);
-}
-
-size_t up16(size_t n) { return (n + 15) / 16 * 16; }
-
-// CTAs of the prefixes' kernel: one per SM, or as many as there can be tiles.
-int prefix_grid(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
-  const int two = 2 * (128 / (Hq / c.Hkv));
-  const long long rows = (total / two + std::min(n_groups, total)) * (long long)c.Hkv;
-  const long long tiles = rows * ((std::min(max_tok, c.cap) + 127) / 128);
-  return (int)std::max<long long>(
-      1, std::min<long long>(tiles / kMinTiles + 1, std::min(sm_count(), kMaxCtas)));
-}
-
-// The call's plan: grids, splits, and where the records lie in the workspace.
-struct Plan {
-  SharedParts s;
-  size_t bytes;
-};
-Plan plan(const Kv16& c, int Hq, const Kv16Groups& groups, int total, bool decode, int max_tok,
-          int window, int n_sink, uint8_t* ws) {
-  Plan x{};
-  SharedParts& s = x.s;
-  s.groups = groups;
-  s.g = Hq / c.Hkv;
-  s.tokens = 128 / s.g;
-  s.ctas = prefix_grid(c, Hq, groups.n, total, max_tok);
-  auto take = [&](size_t n) {
-    uint8_t* p = ws + x.bytes;
-    x.bytes += up16(n);
-    return p;
-  };
-  const size_t rec = kRecFloats * sizeof(float), rows = (size_t)total * Hq;
-  s.part = reinterpret_cast<float*>(take(rows * rec));
-  s.cut = reinterpret_cast<float*>(take((size_t)s.ctas * 2 * 256 * rec));
-  s.line = reinterpret_cast<SharedLine*>(take((size_t)(groups.n + 1) * sizeof(SharedLine)));
-  if (decode) {
-    const long long pages = (long long)c.B * c.Hkv * ((std::min(max_tok, c.cap) + kPage - 1) / kPage);
-    s.workers = kv16_own_workers(pages, sm_count());
-    s.own = reinterpret_cast<float*>(take(rows * rec));
-    s.own_cut = reinterpret_cast<float*>(take((size_t)s.workers * s.g * rec));
-    s.own_line = reinterpret_cast<int*>(take((size_t)(c.B + 1) * sizeof(int)));
-  } else {
-    s.splits = attention_splits(c, Hq, total, max_tok, window, n_sink);
-    s.own = reinterpret_cast<float*>(take(rows * s.splits * rec));
-  }
-  return x;
-}
-
-template <class T, int W>
-cudaError_t launch_join(const Kv16& c, const Kv16Query& q, const SharedParts& s, uint16_t* out,
-                        float* lse, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = (unsigned)((long long)q.total * c.Hkv);
-  cfg.blockDim = W * 32;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, W>, c, q, s, out, lse);
-}
-
-template <class T>
-cudaError_t launch(AttnParams p, const SharedParts& s, uint16_t* out, float* lse, int* launches,
-                   cudaStream_t stream) {
-  p.part = s.part;
-  p.splits = 1;
-  cudaError_t e = launch_part<T, kPrefix>(
-      p, s.ctas, (size_t)(p.groups.n + 1 + kThreads / 32) * sizeof(int), false, stream);
-  if (e != cudaSuccess) return e;
-  *launches = 1;
-  if (!p.q.start) {
-    e = launch_kv16_own(p.c, p.q, s, stream);
-  } else {
-    p.part = s.own;
-    p.splits = s.splits;
-    e = launch_part<T, kOwn>(p, std::min(p.tiles * p.c.Hkv * p.splits, sm_count()), 0, true, stream);
-  }
-  if (e != cudaSuccess) return e;
-  *launches = 3;
-  return p.q.start ? launch_join<T, 4>(p.c, p.q, s, out, lse, stream)
-                   : launch_join<T, 8>(p.c, p.q, s, out, lse, stream);
+  *launches = 2;
+  return cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T>, p, subs, batch);
 }
 
 }  // namespace
 
-size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, bool decode,
-                            int max_tok, int window, int n_sink) {
-  return plan(c, Hq, Kv16Groups{nullptr, nullptr, n_groups}, total, decode, max_tok, window, n_sink,
-              nullptr).bytes;
+size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
+  size_t n;
+  layout(c, Hq, Kv16Groups{nullptr, nullptr, n_groups}, total, max_tok, nullptr, &n);
+  return n;
 }
 
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
                                uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s) {
-  const Plan x = plan(c, q.Hq, g, q.total, !q.start, q.max_tok, q.window, q.n_sink,
-                      static_cast<uint8_t*>(ws));
+  size_t n;
   AttnParams p;
   p.c = c;
   p.q = q;
-  p.out = nullptr;
-  p.lse = nullptr;
-  p.cut = x.s.cut;
-  p.line = x.s.line;
-  p.groups = g;
-  p.g = x.s.g;
-  p.tokens = x.s.tokens;
+  p.out = out;
+  p.lse = lse;
+  p.part = nullptr;
+  p.line = layout(c, q.Hq, g, q.total, q.max_tok, static_cast<uint8_t*>(ws), &n);
+  p.g = p.line.g;
+  p.tokens = p.line.tokens;
   p.tiles = 0;
-  if (q.start) {
-    const long long tiles = attention_tiles(c.B, p.g, q.total);
-    if (tiles * c.Hkv * x.s.splits > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.tiles = (int)tiles;
-  }
+  p.splits = 1;
   p.negate = q.scale_log2 < 0.0f;
   p.scale = std::max(std::fabs(q.scale_log2), std::numeric_limits<float>::denorm_min());
   p.wide = false;
   *launches = 0;
-  return c.half ? launch<Fp16>(p, x.s, out, lse, launches, s)
-                : launch<Bf16>(p, x.s, out, lse, launches, s);
+  return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);
 }
 
 }  // namespace oscar

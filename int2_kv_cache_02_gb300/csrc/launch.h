@@ -245,14 +245,7 @@ constexpr int kMaxGroups = 4096;        // groups of one call
 // q.start nullptr: the decode (lse nullptr).
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
                                uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s);
-size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, bool decode,
-                            int max_tok, int window, int n_sink);
-// The decode's own part: the sequences' pages behind the shared ones, by
-// `workers` warps.
-struct SharedParts;
-cudaError_t launch_kv16_own(const Kv16& c, const Kv16Query& q, const SharedParts& parts,
-                            cudaStream_t s);
-int kv16_own_workers(long long pages, int sms);
+size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok);
 cudaError_t launch_kv16_fork(const Kv16& src, const Kv16& dst, const int32_t* parent, bool share,
                              bool same, int max_tok, cudaStream_t s);
 cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long long entries,
