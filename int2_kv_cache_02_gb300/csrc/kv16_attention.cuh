@@ -116,6 +116,10 @@ struct AttnParams {
   bool wide;            // out is 32-byte aligned
 };
 
+// Query rows for two tiles; or for one, worked by both, each with these queries and
+// its own tiles of keys: those in stages 0 and 1 are query tile 0's, those in 2 and
+// 3 tile 1's (first: the one that has the item's first).
+constexpr int kPair = -1;
 constexpr int kItems = 4;              // work items on their way to the other warps
 
 // A work item as the scheduling warp hands it on.
@@ -123,7 +127,7 @@ struct Item {
   int stop;            // no more items
   int b, h, split, n;
   int end;             // kLine: the sequence behind a group's last (b is its first), -1: b's own
-  int only;            // kLine: the query tile that works it alone, or -1
+  int first;           // kLine: kPair, or the query tile that has the first tile of keys
   int row0, nrow;      // first row of q, tokens (of one or two tiles)
   int at0;             // position of the first token
   Span sp;
@@ -136,6 +140,7 @@ template <int STAGES>
 struct Smem {
   uint64_t q_full[2], q_empty[2], full[STAGES], empty[STAGES];
   uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], tail, drain[2];
+  uint64_t together;                     // kLine: both query tiles' MMA warps are at an item
   uint64_t i_full[kItems], i_empty[kItems];
   uint32_t tmem;
   int state;           // of the waits
@@ -290,7 +295,7 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
       const GroupEntry y = group_entry(p, e, 0, 1, report);
       const int places = row_places(key_tiles(y.sp.blocks));
       x = (unsigned)saturate((long long)((y.r1 - y.r0 + two - 1) / two) * p.c.Hkv * places);
-      if (report) p.line.group[e] = make_int2(places, y.r0);
+      if (report) p.line.group[e] = make_int4(places, y.r0, y.r1, 0);
     } else if (e < entries) {
       const OwnEntry y = own_entry(p, e - G, report);
       long long n = 0;
@@ -412,11 +417,14 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
   return max(end - from, 1);
 }
 
-// The record of a row of an item: at the row's place, or the CTA's.
-__device__ __forceinline__ float* line_record(const AttnParams& p, int split, long long row,
-                                              int cut_row) {
-  return split <= 0 ? (split == 0 ? p.line.prefix : p.line.own) + row * kPartFloats
-                    : p.line.cut + (((long long)blockIdx.x * 2 + split - 1) * 256 + cut_row) * kPartFloats;
+// The record of a row of an item: at the row's place (`second`: of query tile 1,
+// where both tiles have these queries), or the CTA's.
+__device__ __forceinline__ float* line_record(const AttnParams& p, int split, bool second,
+                                              long long row, int cut_row) {
+  if (split > 0)
+    return p.line.cut + (((long long)blockIdx.x * 2 + split - 1) * 256 + cut_row) * kPartFloats;
+  if (second) row += (long long)p.q.total * p.q.Hq;
+  return (split == 0 ? p.line.prefix : p.line.own) + row * kPartFloats;
 }
 
 // The position of query row r of a group's sequences [b0, b1).
@@ -475,10 +483,10 @@ __device__ __forceinline__ float gather_open(float x, float so_far) {
 template <class T, int PART>
 __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int split, int k0,
                                          int k1, const Span& sp, long long row, int at, int* met,
-                                         int cut_row) {
+                                         int cut_row, int first_tile, int w) {
   const int lane = threadIdx.x & 31;
   const bool record = PART != kWhole || p.splits > 1;
-  float* rec = PART == kLine ? line_record(p, split, row, cut_row)
+  float* rec = PART == kLine ? line_record(p, split, first_tile != kPair && w == 1, row, cut_row)
                                : p.part + (row * p.splits + split) * rec_floats(PART);
   uint2* out = reinterpret_cast<uint2*>(p.out + row * kD) + lane;
   float x[4];
@@ -498,10 +506,30 @@ __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int 
   const long long token = row / p.q.Hq;
   const int head = (int)(row - token * p.q.Hq);
   float m, l, o[4];
+  const uint16_t* q = p.q.q + token * p.q.stride + (long long)head * kD;
+  if (PART == kLine && first_tile != kPair) {
+    // every other tile of keys is this query tile's
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int k = k0 + ((first_tile ^ w) & 1); k < k1; k += 2) {
+      const int i = kv16_warp_row<T>(p.c, q, b, h, at, sp, k * kKeyPages,
+                                     min((k + 1) * kKeyPages, sp.blocks), p.q.window, p.q.n_sink,
+                                     p.q.scale_log2, open, m, l, o);
+      const float f = m == -INFINITY || rec[0] == -INFINITY ? 1.0f : fast_exp2(m - rec[0]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += o[e] * f;
+      if (i >= 0) break;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((open >> e) & 1u) rec[rec_head(PART) + 4 * lane + e] = sum[e];
+    return;
+  }
   const int i0 = k0 * kKeyPages, i1 = min(k1 * kKeyPages, sp.blocks), there = *met;
 #pragma unroll 1
   for (int look = there >= i0 && there < i1 ? 0 : 1; look < 2; ++look) {
-    const int i = kv16_warp_row<T>(p.c, p.q.q + token * p.q.stride + (long long)head * kD, b, h,
+    const int i = kv16_warp_row<T>(p.c, q, b, h,
                                    at, sp, look ? i0 : there, look ? i1 : there + 1, p.q.window,
                                    p.q.n_sink, p.q.scale_log2, open, m, l, o);
     if (i < 0) continue;
@@ -578,6 +606,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       mbar_init(&sm.i_empty[i], kItemReaders);
     }
     mbar_init(&sm.tail, 1);
+    mbar_init(&sm.together, 2);
     mbar_fence_init();
     sm.state = 0;
     for (int i = 0; i < kSoftmaxWarps; ++i) sm.met[i] = -1;
@@ -600,7 +629,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       // -------------------------------------------------- scheduling: the items
       // x, rounds of the grid in turn forwards and backwards, so that a CTA
       // with the longest of one round gets the shortest of the next
-      unsigned n = 0;
+      unsigned n = 0, passed = 0;      // items, tiles of keys
       const int items = p.tiles * p.c.Hkv * p.splits, grid = gridDim.x;
       for (int round = 0; ok; ++round) {
         bool stop;
@@ -610,16 +639,13 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!stop) {
             x0 += find_piece(p, first, x0, x1, it);
             if (it.cnt[0] <= 0 && it.cnt[1] <= 0) continue;      // (places without tiles)
-            // rows for one query tile: the two take such items in turn, each at its
-            // own pace
-            it.only = it.nrow > p.tokens ? -1 : (int)(n & 1);
-            if (it.only == 1) {
-              it.row0 -= p.tokens;
-              it.at0 -= p.tokens;
-              it.nrow += p.tokens;
-              it.cnt[1] = it.cnt[0];
-              it.cnt[0] = 0;
+            const int nk = it.k1 - it.k0;
+            it.first = it.nrow > p.tokens ? kPair : (int)(passed & 1);
+            if (it.first != kPair) {
+              it.cnt[0] = it.first == 0 ? nk - nk / 2 : nk / 2;
+              it.cnt[1] = nk - it.cnt[0];
             }
+            passed += nk;
           }
         } else {
           const long long x = (long long)round * grid +
@@ -690,7 +716,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               tma_box3(sq + w * kTileBytes + i * kHalf, &map_q, 64 * i, it.h * p.g,
-                       it.row0 + w * p.tokens, &sm.q_full[w]);
+                       it.row0 + (PART == kWhole || it.first == kPair ? w * p.tokens : 0),
+                       &sm.q_full[w]);
           }
           __syncwarp();
           ++q_used[w];
@@ -781,7 +808,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ph ^= 1;
           }
         };
-        unsigned q_used = 0, p_used = 0, turns = 0;
+        unsigned q_used = 0, p_used = 0, turns = 0, meets = 0;
+        bool apart = false;
         auto my_turn = [&]() -> bool {
           const unsigned n = turns++;
           if (w == 1) return tc5_wait(&sm.turn[1], n & 1, state);
@@ -791,13 +819,61 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           const Item* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
           const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0;
-          const bool pair = PART == kWhole || ip->only < 0;      // the tiles take turns
+          const int first_tile = PART == kLine ? ip->first : kPair;
           mbar_arrive(&sm.i_empty[ni % kItems]);
           if (nk <= 0) continue;
+          if (PART == kLine && first_tile != kPair) {
+            // A stage is one query tile's: the other passes over it, and they take no
+            // turns.  (A warp sees every use of its stages, so a phase is the one that it
+            // waits for.)
+            apart = true;
+            int done = 0;
+            for (int j = 0; j < nk && ok; ++j) {
+              const unsigned ks = st, kp = ph;
+              next();
+              const unsigned vs = st, vp = ph;
+              next();
+              if (((first_tile + j) & 1) != w) continue;
+              ok = tc5_wait(&sm.full[ks], kp, state);
+              if (ok && done == 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, state);
+              if (!ok) break;
+              tc5_fence_after();
+              qk(ks);
+              if (done + 1 == cnt) tc5_commit(&sm.q_empty[w]);
+              tc5_commit(&sm.empty[ks]);
+              tc5_commit(&sm.empty[ks]);
+              ok = tc5_wait(&sm.full[vs], vp, state);
+              if (ok) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, state);
+              if (!ok) break;
+              const uint64_t v = tc5_desc(kAlongN, ring_addr + vs * kTileBytes);
+              tc5_fence_after();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                tc5_mma_ts(to, ts + 8 * i, v + i * (2048 >> 4), id_o, done > 0 || i > 0);
+              tc5_commit(&sm.h_full[w]);
+              ok = tc5_wait(&sm.p_full[w][1], p_used++ & 1, state);
+              if (!ok) break;
+              tc5_fence_after();
+#pragma unroll
+              for (int i = 4; i < 8; ++i)
+                tc5_mma_ts(to, ts + 32 + 8 * i, v + i * (2048 >> 4), id_o, true);
+              if (++done == cnt) tc5_commit(&sm.o_full[w]);
+              tc5_commit(&sm.empty[vs]);
+              tc5_commit(&sm.empty[vs]);
+            }
+            continue;
+          }
+          if (PART == kLine && apart) {
+            // from here on both use all stages: neither may be a use ahead of the other
+            mbar_arrive(&sm.together);
+            ok = tc5_wait(&sm.together, meets++ & 1, state);
+            if (!ok) break;
+            apart = false;
+          }
           // a stage that this tile has no use for is given back as it comes
           ok = tc5_wait(&sm.full[st], ph, state);
           if (ok && cnt > 0) ok = tc5_wait(&sm.q_full[w], q_used++ & 1, state);
-          if (ok && pair) ok = my_turn();
+          if (ok) ok = my_turn();
           if (!ok) break;
           if (cnt > 0) {
             tc5_fence_after();
@@ -807,7 +883,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           } else {
             mbar_arrive(&sm.empty[st]);
           }
-          if (pair) mbar_arrive(&sm.turn[w ^ 1]);
+          mbar_arrive(&sm.turn[w ^ 1]);
           next();
           for (int j = 0; j < nk && ok; ++j) {
             const unsigned vs = st, vp = ph;
@@ -816,7 +892,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
             ok = tc5_wait(&sm.full[vs], vp, state);
             if (ok && more) ok = tc5_wait(&sm.full[st], ph, state);
             if (ok && j < cnt) ok = tc5_wait(&sm.p_full[w][0], p_used & 1, state);
-            if (ok && pair) ok = my_turn();
+            if (ok) ok = my_turn();
             if (!ok) break;
             if (j < cnt) {
               // P comes in halves of 64 keys
@@ -834,11 +910,11 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
                 tc5_mma_ts(to, ts + 32 + 8 * i, v + i * (2048 >> 4), id_o, true);
               if (j + 1 < cnt) qk(st);
               else tc5_commit(&sm.o_full[w]);
-              if (pair) mbar_arrive(&sm.turn[w ^ 1]);
+              mbar_arrive(&sm.turn[w ^ 1]);
               tc5_commit(&sm.empty[vs]);
               if (j + 2 == cnt) tc5_commit(&sm.q_empty[w]);
             } else {
-              if (pair) mbar_arrive(&sm.turn[w ^ 1]);
+              mbar_arrive(&sm.turn[w ^ 1]);
               mbar_arrive(&sm.empty[vs]);
             }
             if (more) {
@@ -869,14 +945,17 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     for (unsigned ni = 0; ok; ++ni) {
       const Item* ip = take(ni);
       if (!(ok = ip != nullptr) || ip->stop) break;
-      const int ntok = min(p.tokens, ip->nrow - w * p.tokens), my_n = ip->cnt[w];
+      const int first_tile = PART == kLine ? ip->first : kPair;
+      const bool pair = first_tile == kPair;
+      const int shift = pair ? w * p.tokens : 0;
+      const int ntok = min(p.tokens, ip->nrow - shift), my_n = ip->cnt[w];
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
-      const int seq_end = PART == kLine ? ip->end : 0, only = PART == kLine ? ip->only : -1;
-      const int at_first = ip->at0 + w * p.tokens, row_first = ip->row0 + w * p.tokens;
+      const int seq_end = PART == kLine ? ip->end : 0;
+      const int at_first = ip->at0 + shift, row_first = ip->row0 + shift;
       const Span sp = ip->sp;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
-      if (ntok <= 0 || (only >= 0 && w != only)) continue;
+      if (ntok <= 0) continue;
       // the thread's row; rows past the tile's end work like its last token
       const bool valid = tok < ntok;
       const int at =                                          // (-1: before the first token)
@@ -937,7 +1016,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
         if (!ok) break;
         tc5_fence_after();
-        const bool inside = j >= in0 && j < in1;
+        const int t = pair ? j : ((first_tile ^ w) & 1) + 2 * j;      // key tile of the item
+        const bool inside = t >= in0 && t < in1;
         uint32_t sr[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc5_ld32(sr + 32 * i, s_addr + 32 * i);
@@ -945,7 +1025,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t* x = sr + 64 * i;
-          const int v = (k0 + j) * kKeyPages + 2 * i;
+          const int v = (k0 + t) * kKeyPages + 2 * i;
           auto mask = [&] {
             if (inside) return;
             hide(reinterpret_cast<float*>(x), v);
@@ -1013,6 +1093,14 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       }
 
       // ------------------------------------------------------------ results
+      if (PART == kLine && !pair && my_n == 0) {
+        // the other query tile had the only tile of keys
+        if (valid)
+          *reinterpret_cast<float2*>(line_record(
+              p, split, w == 1, (long long)(row_first + tok) * p.q.Hq + h * p.g + head,
+              w * 128 + r)) = make_float2(-INFINITY, 0.0f);
+        continue;
+      }
       if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, state);
       if (!ok) break;
       tc5_fence_after();
@@ -1020,8 +1108,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const bool record = PART != kWhole || p.splits > 1;
       const float inv = record ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       float odd = 0.0f, odd1 = 0.0f, odd2 = 0.0f, odd3 = 0.0f;   // NaN: a channel is open
-      const int cut_row = only >= 0 ? 0 : w * 128;
-      float* rec = PART == kLine ? line_record(p, split, row, cut_row + r)
+      const int cut_row = w * 128;
+      float* rec = PART == kLine ? line_record(p, split, !pair && w == 1, row, cut_row + r)
                                    : p.part + (row * p.splits + split) * rec_floats(PART);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -1086,7 +1174,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           const int src = __ffs(bad) - 1;
           redo_row<T, PART>(p, b, h, split, k0, k1, sp, __shfl_sync(0xffffffffu, row, src),
                             __shfl_sync(0xffffffffu, at, src), &sm.met[warp],
-                            cut_row + (warp & 3) * 32 + src);
+                            cut_row + (warp & 3) * 32 + src, first_tile, w);
         }
         if (lane == 0) atomicAdd(&sm.state, -kTcBusy);
       }

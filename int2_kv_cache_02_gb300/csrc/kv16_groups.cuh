@@ -63,14 +63,16 @@ constexpr int kPartHead = 8, kPartFloats = kPartHead + 128;
 // The line and its records in the workspace (32-byte aligned).  A run that has a
 // row's first tile leaves its records at the query rows' places, else with the
 // CTA: [2][256], 0 for a run that begins inside a block, 1 for one that begins a
-// block.
+// block.  A chunk that fills one query tile only (rows <= 128 / g * g) is worked by
+// both, with every other tile of keys each: two records a run, the second in the
+// second half.
 struct SharedParts {
   Kv16Groups groups;
-  float* prefix;            // [total][Hq]
-  float* own;               // [total][Hq]
+  float* prefix;            // [2][total][Hq]
+  float* own;               // [2][total][Hq]
   float* cut;               // [ctas][2][256]
   int* first;               // [groups + B + 1]: the entries' first places, the line's end
-  int2* group;              // [groups]: places of a row, the first query row
+  int4* group;              // [groups]: places of a row, first query row, the row behind the last
   int ctas;
   int tokens, g;            // tokens of a query tile, heads of a group
 };

@@ -106,15 +106,22 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
   int kind = 0;
   const float* base = nullptr;
   Runs own{0, 0}, prefix{0, 0};
+  int twice_own = 0, twice = 0;     // two records a run
   int blocks = 1, places = 0, chunks = 1, chunk = 0;
   unsigned at = 0;
   auto locate = [&](int j) {
     kind = 0;
-    if (j < own.n) {
+    const int n_own = own.n << twice_own;
+    if (j < n_own) {
+      const int second = twice_own ? j & 1 : 0;
+      j >>= twice_own;
       kind = j == 0 ? 1 : 3;
-      base = j == 0 ? s.own : s.cut + (long long)(own.c0 + j) * 512 * kPartFloats;
+      base = (j == 0 ? s.own + (long long)second * p.q.total * p.q.Hq * kPartFloats
+                     : s.cut + ((long long)(own.c0 + j) * 512 + second * 128) * kPartFloats);
     } else if (j < n) {
-      j -= own.n;
+      j -= n_own;
+      const int second = twice ? j & 1 : 0;
+      j >>= twice;
       int t0 = 0;
       Runs x = prefix;
       if (blocks > 1) {
@@ -130,8 +137,9 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       if (j >= x.n) return;
       const bool first = j == 0 && t0 <= kRowCost;
       kind = first ? 2 : 4;
-      base = first ? s.prefix
-                   : s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0)) * kPartFloats;
+      base = first ? s.prefix + (long long)second * p.q.total * p.q.Hq * kPartFloats
+                   : s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0) + second * 128) *
+                                 kPartFloats;
     }
   };
   for (int r = first_r; r < end_r; ++r) {
@@ -163,16 +171,18 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
         tiles = y.tiles(p, own_chunk);
       }
       own = f1 > f0 && tiles > 0 ? runs_of(at_own + kRowCost, tiles, per, s.ctas) : Runs{0, 0};
+      twice_own = seq1 - seq0 - own_chunk * two <= p.tokens;
       prefix = Runs{0, 0};
       blocks = 1;
       if (i >= 0) {
-        const int2 gr = __ldcg(s.group + i);
+        const int4 gr = __ldcg(s.group + i);
         const int g0 = __ldcg(s.first + i), all = (int)((unsigned)(__ldcg(s.first + i + 1) - g0) / hkv);
         places = gr.x;
         group0 = gr.y;
         chunk = (r - group0) / two;
         if (places > 0 && r >= group0 && chunk < (chunks = all / places)) {
           at = g0 + (unsigned)all * h;
+          twice = gr.z - group0 - chunk * two <= p.tokens;
           blocks = line_blocks(places, chunks, per);
           prefix = blocks > 1 ? Runs{0, blocks * kBlockRuns}
                               : runs_of(at + (unsigned)(chunk * places) + kRowCost, places - kRowCost,
@@ -181,7 +191,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
         }
       }
       same = to;
-      n = head < g ? own.n + prefix.n : 0;
+      n = head < g ? (own.n << twice_own) + (prefix.n << twice) : 0;
       locate(sub + lane * subs);
     }
     if (b < 0) continue;
@@ -211,7 +221,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       for (int x = width >> 1; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
       L = f * L + __shfl_sync(0xffffffffu, add, 0);
       o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-      unsigned have = __ballot_sync(0xffffffffu, kind != 0);
+      unsigned have = __ballot_sync(0xffffffffu, ml.x != -INFINITY);     // (-inf: nothing seen)
 #pragma unroll 1
       while (have) {
         constexpr int U = 4;
@@ -297,11 +307,11 @@ SharedParts layout(const Kv16& c, int Hq, const Kv16Groups& groups, int total, i
     return p;
   };
   const size_t rec = kPartFloats * sizeof(float), rows = (size_t)total * Hq;
-  s.prefix = static_cast<float*>(take(rows * rec));
-  s.own = static_cast<float*>(take(rows * rec));
+  s.prefix = static_cast<float*>(take(2 * rows * rec));
+  s.own = static_cast<float*>(take(2 * rows * rec));
   s.cut = static_cast<float*>(take((size_t)s.ctas * 512 * rec));
   s.first = static_cast<int*>(take((size_t)(groups.n + c.B + 1) * sizeof(int)));
-  s.group = static_cast<int2*>(take((size_t)groups.n * sizeof(int2)));
+  s.group = static_cast<int4*>(take((size_t)groups.n * sizeof(int4)));
   *bytes = at - reinterpret_cast<uintptr_t>(ws) + 16;
   return s;
 }
