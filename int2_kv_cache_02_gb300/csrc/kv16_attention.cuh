@@ -198,8 +198,6 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
 }
 
 __device__ __forceinline__ int key_tiles(int blocks) { return (blocks + kKeyPages - 1) / kKeyPages; }
-// Places of a row of the line.
-__device__ __forceinline__ int row_places(int tiles) { return tiles > 0 ? tiles + kRowCost : 0; }
 
 // A group's entry of the line: its sequences' queries [r0, r1) against the blocks
 // of `sp`.  One thread looks, or a warp (step 32, one answer).
@@ -250,10 +248,16 @@ struct OwnEntry {
   __device__ __forceinline__ Span span(const AttnParams& p, int tok, int count) const {
     return Span(at0 + tok, at0 + tok + count - 1, p.q.window, p.q.n_sink).from(shared);
   }
-  // key tiles of chunk i
+  // key tiles of chunk i, and the places of its row
   __device__ __forceinline__ int tiles(const AttnParams& p, int i) const {
     const int two = 2 * p.tokens;
     return key_tiles(span(p, i * two, min(two, nq - i * two)).blocks);
+  }
+  __device__ __forceinline__ bool pair(const AttnParams& p, int i) const {
+    return nq - i * 2 * p.tokens > p.tokens;
+  }
+  __device__ __forceinline__ int places(const AttnParams& p, int i) const {
+    return row_places(tiles(p, i), pair(p, i));
   }
 };
 __device__ __forceinline__ OwnEntry own_entry(const AttnParams& p, int b, bool report) {
@@ -293,13 +297,14 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
     unsigned x = 0;
     if (e < G) {
       const GroupEntry y = group_entry(p, e, 0, 1, report);
-      const int places = row_places(key_tiles(y.sp.blocks));
-      x = (unsigned)saturate((long long)((y.r1 - y.r0 + two - 1) / two) * p.c.Hkv * places);
-      if (report) p.line.group[e] = make_int4(places, y.r0, y.r1, 0);
+      const int tiles = key_tiles(y.sp.blocks), rows = y.r1 - y.r0;
+      x = (unsigned)saturate((long long)((rows + two - 1) / two) * p.c.Hkv *
+                             row_places(tiles, rows > p.tokens));
+      if (report) p.line.group[e] = make_int4(tiles, y.r0, y.r1, 0);
     } else if (e < entries) {
       const OwnEntry y = own_entry(p, e - G, report);
       long long n = 0;
-      for (int i = 0; i * two < y.nq; ++i) n += row_places(y.tiles(p, i));
+      for (int i = 0; i * two < y.nq; ++i) n += y.places(p, i);
       x = (unsigned)saturate(n * p.c.Hkv);
     }
 #pragma unroll
@@ -329,11 +334,12 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
   __syncthreads();
 }
 
-// The item at place x of the line, as far as x1; its number of places.  A warp.
+// The item at place x of the line, as far as x1; its number of places.  share: the
+// places of a CTA's run.  A warp.
 // (Maxima and minima: whatever the groups and lengths hold by now, what follows
 // stays in bounds.)
-__device__ __forceinline__ int find_piece(const AttnParams& p, const int* first, int x, int x1,
-                                           Item& it) {
+__device__ __forceinline__ int find_piece(const AttnParams& p, const int* first, int share, int x,
+                                          int x1, Item& it) {
   const int G = p.line.groups.n, two = 2 * p.tokens, lane = threadIdx.x & 31;
   int lo = 0, hi = G + p.c.B;     // first[i] <= x < first[i + 1]
   while (hi - lo > 1) {
@@ -341,39 +347,55 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     if (first[mid] <= x) lo = mid; else hi = mid;
   }
   const int at = x - first[lo];
-  int from, to, tiles0 = 0;       // places of the row; tiles0: of a sequence's first query tile, whose keys end first
+  int from, to;                   // places of the row
+  bool pair;
+  int tiles0 = 0;                 // of a sequence's first query tile, whose keys end first
   it.clear = false;
   if (lo < G) {
     const GroupEntry y = group_entry(p, lo, lane, 32, false);
-    const int chunks = max((y.r1 - y.r0 + two - 1) / two, 1);
-    const int places = max(row_places(key_tiles(y.sp.blocks)), 1);
-    const int per_head = chunks * places;         // (no more than the line has: it fits)
-    it.h = min(at / per_head, p.c.Hkv - 1);
-    const int in_head = at - it.h * per_head, z = min(in_head / chunks, places - 1);
-    const int blocks = line_blocks(places, chunks, line_share(first[G + p.c.B], gridDim.x));
-    int i = (int)((long long)z * blocks / places);
-    if (block_place(places, blocks, i + 1) <= z) ++i;
-    const int t0 = block_place(places, blocks, i), t1 = block_place(places, blocks, i + 1);
-    const int in = in_head - chunks * t0, chunk = min(in / (t1 - t0), chunks - 1);
+    const int rows = y.r1 - y.r0, tiles = max(key_tiles(y.sp.blocks), 1);
+    pair = rows > p.tokens;
+    to = row_places(tiles, pair);
+    int p0 = 0, chunk = 0;
+    if (rows <= two) {
+      it.h = min(at / to, p.c.Hkv - 1);
+      from = at - it.h * to;
+    } else {
+      const int chunks = (rows + two - 1) / two, places = to;
+      const int per_head = chunks * places;       // (no more than the line has: it fits)
+      it.h = min(at / per_head, p.c.Hkv - 1);
+      const int in_head = at - it.h * per_head, z = min(in_head / chunks, places - 1);
+      const Blocks blocks(tiles, chunks, pair, share);
+      const int t = max(z - row_cost(pair), 0) / tile_cost(pair);
+      const int i = min(t / blocks.least, blocks.count - 1);
+      p0 = tile_place(blocks.first(i), pair);
+      if (i + 1 < blocks.count) to = tile_place(blocks.first(i + 1), pair);
+      const int in = in_head - chunks * p0;
+      chunk = min(in / (to - p0), chunks - 1);
+      from = p0 + in - chunk * (to - p0);
+    }
     it.b = y.s.lead;
     it.end = y.s.end;
     it.n = it.at0 = 0;
     it.row0 = y.r0 + chunk * two;
     it.nrow = min(two, y.r1 - it.row0);
     it.sp = y.sp;
-    from = t0 + in - chunk * (t1 - t0);
-    to = t1;
-    it.split = from <= kRowCost ? 0 : from > t0 ? 1 : 2;  // where the records go
+    it.split = from <= row_cost(pair) ? 0 : from > p0 ? 1 : 2;  // where the records go
   } else {
     const OwnEntry y = own_entry(p, lo - G, false);
-    const int chunks = max((y.nq + two - 1) / two, 1);
-    const int per_head = max((first[lo + 1] - first[lo]) / p.c.Hkv, 1);
-    it.h = min(at / per_head, p.c.Hkv - 1);
-    int in = at - it.h * per_head, chunk = 0;
-    if (chunks > 1) {
-      // the chunk that has tile `in` of the head's
+    int in, chunk = 0;
+    if (y.nq <= two) {
+      const int places = max(y.places(p, 0), 1);
+      it.h = min(at / places, p.c.Hkv - 1);
+      in = at - it.h * places;
+    } else {
+      // the chunk that has place `in` of the head's
+      const int chunks = (y.nq + two - 1) / two;
+      const int per_head = max((first[lo + 1] - first[lo]) / p.c.Hkv, 1);
+      it.h = min(at / per_head, p.c.Hkv - 1);
+      in = at - it.h * per_head;
       for (int c0 = 0;; c0 += 32) {
-        const int mine = c0 + lane < chunks ? row_places(y.tiles(p, c0 + lane)) : 0;
+        const int mine = c0 + lane < chunks ? y.places(p, c0 + lane) : 0;
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -399,14 +421,15 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.at0 = y.at0 + chunk * two;
     it.sp = y.span(p, chunk * two, it.nrow);
     from = max(in, 0);
-    to = row_places(key_tiles(it.sp.blocks));
+    pair = y.pair(p, chunk);
+    to = row_places(key_tiles(it.sp.blocks), pair);
     tiles0 = key_tiles(y.span(p, chunk * two, min(it.nrow, p.tokens)).blocks);
-    it.split = from <= kRowCost ? -1 : 1;
+    it.split = from <= row_cost(pair) ? -1 : 1;
   }
   const int end = (int)min(min((long long)from + (x1 - x), (long long)to),
                            (long long)from + (first[lo + 1] - x));
-  it.k0 = max(from - kRowCost, 0);
-  it.k1 = max(end - kRowCost, 0);
+  it.k0 = tiles_before(from, pair);
+  it.k1 = tiles_before(end, pair);
   it.cnt[0] = it.nrow > 0 ? max(it.k1 - it.k0, 0) : 0;
   it.cnt[1] = it.nrow > p.tokens ? it.cnt[0] : 0;
   if (lo >= G && it.cnt[0] > 0) {
@@ -570,7 +593,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     return;
   }
 
-  int x0 = 0, x1 = 0;                            // kLine: the CTA's run of the line
+  int x0 = 0, x1 = 0, share = 0;                 // kLine: the CTA's run of the line
   if constexpr (PART != kWhole) {
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid < 3)
@@ -579,9 +602,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   if constexpr (PART == kLine) {
     const int entries = p.line.groups.n + p.c.B;
     line_up(p, first, first + entries + 1);
-    const int total = first[entries], per = line_share(total, gridDim.x);
-    x0 = (int)min((long long)blockIdx.x * per, (long long)total);
-    x1 = (int)min((long long)x0 + per, (long long)total);
+    const int total = first[entries];
+    share = line_share(total, gridDim.x);
+    x0 = (int)min((long long)blockIdx.x * share, (long long)total);
+    x1 = (int)min((long long)x0 + share, (long long)total);
     if (x0 == x1) return;
   }
   if (warp == kSoftmaxWarps) tc5_alloc(&sm.tmem, 512);
@@ -637,7 +661,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         if constexpr (PART == kLine) {
           stop = x0 >= x1;
           if (!stop) {
-            x0 += find_piece(p, first, x0, x1, it);
+            x0 += find_piece(p, first, share, x0, x1, it);
             if (it.cnt[0] <= 0 && it.cnt[1] <= 0) continue;      // (places without tiles)
             const int nk = it.k1 - it.k0;
             it.first = it.nrow > p.tokens ? kPair : (int)(passed & 1);
@@ -1012,10 +1036,15 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         return (sum0.x + sum0.y) + (sum1.x + sum1.y);
       };
-      for (int j = 0; j < my_n; ++j) {
-        ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
-        if (!ok) break;
-        tc5_fence_after();
+      // kLine: a round before the first, on whatever there is and without effect, while
+      // the first keys are on their way: it fetches the round's instructions
+      for (int j = PART == kLine && ni == 0 ? -1 : 0; j < my_n; ++j) {
+        const bool warm = PART == kLine && j < 0;
+        if (!warm) {
+          ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
+          if (!ok) break;
+          tc5_fence_after();
+        }
         const int t = pair ? j : ((first_tile ^ w) & 1) + 2 * j;      // key tile of the item
         const bool inside = t >= in0 && t < in1;
         uint32_t sr[128];
@@ -1072,6 +1101,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           // queries, or what was in shared memory)
           if (__any_sync(0xffffffffu, valid && m == -INFINITY)) raise();
           float sum = weigh(x);
+          if (warm) {
+            m = -INFINITY;
+            continue;
+          }
           if (__any_sync(0xffffffffu, valid && sum > Range<T>::kMost)) {
             tc5_ld32(x, s_addr + 64 * i);
             tc5_ld32(x + 32, s_addr + 64 * i + 32);
@@ -1089,7 +1122,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (lane == 0) mbar_arrive(&sm.p_full[w][i]);
         }
         if (!ok) break;
-        ++s_used;
+        if (!warm) ++s_used;
       }
 
       // ------------------------------------------------------------ results

@@ -65,13 +65,14 @@ __device__ __noinline__ float4 settle(const AttnParams& p, int b, int h, int bac
   return make_float4(o[0], o[1], o[2], o[3]);
 }
 
-// The CTAs [c0, c0 + n) that have tiles [at, at + tiles) of the line.
+// The CTAs [c0, c0 + n) that have tiles of a block whose first tile is at place `at`
+// of the line and whose last is `more` places on.
 struct Runs {
   int c0, n;
 };
-__device__ __forceinline__ Runs runs_of(unsigned at, unsigned tiles, unsigned per, int ctas) {
+__device__ __forceinline__ Runs runs_of(unsigned at, unsigned more, unsigned per, int ctas) {
   const int c0 = min((int)(at / per), ctas - 1);
-  return Runs{c0, min((int)((at + tiles - 1) / per), ctas - 1) - c0 + 1};
+  return Runs{c0, min((int)((at + more) / per), ctas - 1) - c0 + 1};
 }
 
 // The records of both parts of a row (query, head) joined by a warp, or by `subs`
@@ -79,14 +80,13 @@ __device__ __forceinline__ Runs runs_of(unsigned at, unsigned tiles, unsigned pe
 // of `batch` queries one after another.  Queries that belong to no sequence are
 // left alone.
 //
-// Bound by latency where rows are few: groups and the line are a chain of loads,
-// then a record's place takes a few divisions.  So a warp's lanes find 32 records at
-// a time, a lane each, with their maxima and sums, and the outputs follow four at a
-// time.  Bound by instructions where rows are many: so places are found once for
-// the queries of a batch that lie in the same rows of the line.
+// Bound by latency: groups and the line are a chain of loads, then a record's place
+// takes a few divisions.  So a warp's lanes find 32 records at a time, a lane each,
+// once for the queries of a batch that lie in the same rows of the line, and U
+// records are in flight.
 constexpr int kJoinWarps = 4;
-template <class T>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+template <class T, int U>
+__global__ void __launch_bounds__(kJoinWarps * 32, U == 4 ? 8 : 5)
 kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batch) {
   __shared__ float4 s_o[kJoinWarps][32];
   __shared__ float2 s_ml[kJoinWarps];
@@ -100,56 +100,69 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
   const unsigned per = line_share(__ldcg(s.first + G + p.c.B), s.ctas), hkv = p.c.Hkv;
 
   // of the queries [.., same): their sequence, and their rows of the line
-  int same = first_r, b = -1, seq0 = 0, seq1 = 0, group0 = 0, n = 0;
-  // the lane's record: 0 none, 1 and 2 at the row's place, 3 and 4 with a CTA (the
-  // sequence's own, the prefix's)
-  int kind = 0;
-  const float* base = nullptr;
+  int same = first_r, b = -1, seq1 = 0, n = 0;
   Runs own{0, 0}, prefix{0, 0};
   int twice_own = 0, twice = 0;     // two records a run
-  int blocks = 1, places = 0, chunks = 1, chunk = 0;
+  int in_own = 0, in_prefix = 0;    // the query's place in its chunks
+  bool pair = false;
+  int tiles = 0, chunks = 1, chunk = 0;
   unsigned at = 0;
-  auto locate = [&](int j) {
-    kind = 0;
+  Blocks blocks(0, 1, false, 1);
+  // the lane's record in 32-byte steps from the first of all, or none; from a query to
+  // the next it moves by `step`, and by `fix` more into a chunk's second tile
+  constexpr unsigned kNone = ~0u, kSteps = kPartFloats / 8;
+  const unsigned fix = (128 - p.tokens * g) * kSteps;
+  unsigned off = kNone, step = 0;
+  int in = -1;                      // 0 own, 1 prefix: which chunk the record's place goes by
+  auto locate = [&](int j, long long row) {
+    off = kNone;
+    step = 0;
+    in = -1;
     const int n_own = own.n << twice_own;
-    if (j < n_own) {
-      const int second = twice_own ? j & 1 : 0;
-      j >>= twice_own;
-      kind = j == 0 ? 1 : 3;
-      base = (j == 0 ? s.own + (long long)second * p.q.total * p.q.Hq * kPartFloats
-                     : s.cut + ((long long)(own.c0 + j) * 512 + second * 128) * kPartFloats);
-    } else if (j < n) {
-      j -= n_own;
-      const int second = twice ? j & 1 : 0;
-      j >>= twice;
-      int t0 = 0;
-      Runs x = prefix;
-      if (blocks > 1) {
-        const int k = j / kBlockRuns;
-        j -= k * kBlockRuns;
-        t0 = block_place(places, blocks, k);
-        const int t1 = block_place(places, blocks, k + 1), skip = max(kRowCost - t0, 0);
-        x.n = 0;
-        if (t0 + skip < t1)
-          x = runs_of(at + (unsigned)chunks * t0 + (unsigned)chunk * (t1 - t0) + skip,
-                      t1 - t0 - skip, per, s.ctas);
-      }
-      if (j >= x.n) return;
-      const bool first = j == 0 && t0 <= kRowCost;
-      kind = first ? 2 : 4;
-      base = first ? s.prefix + (long long)second * p.q.total * p.q.Hq * kPartFloats
-                   : s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0) + second * 128) *
-                                 kPartFloats;
+    const bool mine = j < n_own;
+    if (j >= n) return;
+    if (!mine) j -= n_own;
+    const int second = (mine ? twice_own : twice) ? j & 1 : 0;
+    j >>= mine ? twice_own : twice;
+    Runs x = mine ? own : prefix;
+    int k = 0;
+    if (!mine && blocks.count > 1) {
+      k = j / kBlockRuns;
+      j -= k * kBlockRuns;
+      const int t0 = blocks.first(k), t1 = blocks.first(k + 1);
+      const int p0 = tile_place(t0, pair), len = row_places(t1, pair) - p0;
+      x = runs_of(at + (unsigned)chunks * p0 + (unsigned)chunk * len + (k == 0 ? row_cost(pair) : 0),
+                  (t1 - t0 - 1) * tile_cost(pair), per, s.ctas);
     }
+    if (j >= x.n) return;
+    const float* e;
+    if (j == 0 && k == 0) {
+      e = (mine ? s.own : s.prefix) + ((long long)second * p.q.total * p.q.Hq + row) * kPartFloats;
+      step = p.q.Hq * kSteps;
+    } else {
+      in = mine ? 0 : 1;
+      const int i = mine ? in_own : in_prefix, w = i >= p.tokens ? 1 : 0;
+      e = s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0) + (second + w) * 128 +
+                   (i - w * p.tokens) * g + head) * kPartFloats;
+      step = g * kSteps;
+    }
+    off = (unsigned)((e - s.prefix) / 8);
   };
   for (int r = first_r; r < end_r; ++r) {
-    if (r >= same) {
+    const long long row = (long long)r * p.q.Hq + h * g + head;
+    if (r < same) {
+      // the same rows of the line, the next query
+      ++in_own;
+      ++in_prefix;
+      off += step;
+      if ((in == 0 && in_own == p.tokens) || (in == 1 && in_prefix == p.tokens)) off += fix;
+    } else {
       same = r + 1;
       b = r;
-      seq0 = r;
+      int seq0 = r;
       seq1 = r + 1;
       if (p.q.start) {
-        b = ragged_sequence(p.q.start, p.c.B, r);
+        b = warp_sequence(p.q.start, p.c.B, r);
         if (b < 0) continue;
         seq0 = __ldg(p.q.start + b);
         seq1 = __ldg(p.q.start + b + 1);
@@ -159,91 +172,87 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
         }
       }
       const int f0 = __ldcg(s.first + G + b), f1 = __ldcg(s.first + G + b + 1);
-      const int i = group_of(s.groups, b), own_chunk = (r - seq0) / two;
+      const int i = warp_sequence(s.groups.group, G, b), own_chunk = (r - seq0) / two;
       int to = min(seq1, seq0 + (own_chunk + 1) * two);
+      in_own = r - seq0 - own_chunk * two;
       const int per_head = (int)((unsigned)(f1 - f0) / hkv);
-      int at_own = f0 + per_head * h, tiles = per_head - kRowCost;
+      const bool single = seq1 - seq0 - own_chunk * two <= p.tokens;
+      int at_own = f0 + per_head * h;
+      int more = per_head - row_cost(!single) - tile_cost(!single);
       if (seq1 - seq0 > two) {        // several chunks
         const OwnEntry y = own_entry(p, b, false);
         int before = 0;
-        for (int k = lane; k < own_chunk; k += 32) before += row_places(y.tiles(p, k));
+        for (int k = lane; k < own_chunk; k += 32) before += y.places(p, k);
         at_own += (int)__reduce_add_sync(0xffffffffu, before);
-        tiles = y.tiles(p, own_chunk);
+        more = (y.tiles(p, own_chunk) - 1) * tile_cost(!single);
       }
-      own = f1 > f0 && tiles > 0 ? runs_of(at_own + kRowCost, tiles, per, s.ctas) : Runs{0, 0};
-      twice_own = seq1 - seq0 - own_chunk * two <= p.tokens;
+      own = f1 > f0 && more >= 0 ? runs_of(at_own + row_cost(!single), more, per, s.ctas) : Runs{0, 0};
+      twice_own = single;
       prefix = Runs{0, 0};
-      blocks = 1;
+      blocks = Blocks(0, 1, false, 1);
       if (i >= 0) {
         const int4 gr = __ldcg(s.group + i);
         const int g0 = __ldcg(s.first + i), all = (int)((unsigned)(__ldcg(s.first + i + 1) - g0) / hkv);
-        places = gr.x;
-        group0 = gr.y;
-        chunk = (r - group0) / two;
-        if (places > 0 && r >= group0 && chunk < (chunks = all / places)) {
+        tiles = gr.x;
+        const int rows = gr.z - gr.y;
+        pair = rows > p.tokens;
+        chunks = (rows + two - 1) / two;
+        chunk = (r - gr.y) / two;
+        if (tiles > 0 && r >= gr.y && chunk < chunks && all > 0) {
+          in_prefix = r - gr.y - chunk * two;
           at = g0 + (unsigned)all * h;
-          twice = gr.z - group0 - chunk * two <= p.tokens;
-          blocks = line_blocks(places, chunks, per);
-          prefix = blocks > 1 ? Runs{0, blocks * kBlockRuns}
-                              : runs_of(at + (unsigned)(chunk * places) + kRowCost, places - kRowCost,
-                                        per, s.ctas);
-          to = min(to, group0 + (chunk + 1) * two);
+          twice = rows - chunk * two <= p.tokens;
+          blocks = Blocks(tiles, chunks, pair, per);
+          prefix = blocks.count > 1
+                       ? Runs{0, blocks.count * kBlockRuns}
+                       : runs_of(at + (unsigned)chunk * row_places(tiles, pair) + row_cost(pair),
+                                 (tiles - 1) * tile_cost(pair), per, s.ctas);
+          to = min(to, gr.y + (chunk + 1) * two);
         }
       }
       same = to;
       n = head < g ? (own.n << twice_own) + (prefix.n << twice) : 0;
-      locate(sub + lane * subs);
+      locate(sub + lane * subs, row);
     }
     if (b < 0) continue;
-    const long long row = (long long)r * p.q.Hq + h * g + head;
-    auto cut_row = [&](int in) {
-      in %= two;
-      const int w = in >= p.tokens ? 1 : 0;
-      return w * 128 + (in - w * p.tokens) * g + head;
-    };
     float M = -INFINITY, L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
     for (int j0 = sub; j0 < n; j0 += 32 * subs) {
-      if (n > 32 * subs) locate(j0 + lane * subs);
-      const float* e = base + (kind <= 2 ? row : cut_row(kind == 3 ? r - seq0 : r - group0)) * kPartFloats;
-      float2 ml = make_float2(-INFINITY, 0.0f);
-      if (kind) ml = __ldcg(reinterpret_cast<const float2*>(e));
-      // (lanes behind the records have none)
-      const int width = n - j0 <= 4 * subs ? 4 : 32;
-      float mx = ml.x;
-      for (int x = width >> 1; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      mx = fmaxf(__shfl_sync(0xffffffffu, mx, 0), M);
-      const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
-      const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml.x - mx);
-      M = mx;
-      float add = a * ml.y;
-      for (int x = width >> 1; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
-      L = f * L + __shfl_sync(0xffffffffu, add, 0);
-      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-      unsigned have = __ballot_sync(0xffffffffu, ml.x != -INFINITY);     // (-inf: nothing seen)
+      if (n > 32 * subs) locate(j0 + lane * subs, row);
+      const int count = min((n - j0 + subs - 1) / subs, 32);
 #pragma unroll 1
-      while (have) {
-        constexpr int U = 4;
+      for (int u0 = 0; u0 < count; u0 += U) {
+        float2 ml[U];
         float4 v[U];
-        float w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int from = have ? __ffs(have) - 1 : 0;
-          const float* d = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(e), from));
-          w[u] = __shfl_sync(0xffffffffu, a, from);
+          const unsigned from = __shfl_sync(0xffffffffu, off, (u0 + u) & 31);
+          ml[u] = make_float2(-INFINITY, 0.0f);
           v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (have) v[u] = __ldcg(reinterpret_cast<const float4*>(d + kPartHead) + lane);
-          else w[u] = 0.0f;
-          have &= have - 1;
+          if (u0 + u < count && from != kNone) {
+            const float* e = s.prefix + (size_t)from * 8;
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(e));
+            v[u] = __ldcg(reinterpret_cast<const float4*>(e + kPartHead) + lane);
+          }
         }
+        float mx = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+        const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
+        M = mx;
+        L *= f;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          o.x += w[u] * v[u].x;
-          o.y += w[u] * v[u].y;
-          o.z += w[u] * v[u].z;
-          o.w += w[u] * v[u].w;
+          // (a record that has seen nothing has no outputs; its sum may be NaN)
+          const bool seen = ml[u].x != -INFINITY;
+          const float a = seen ? fast_exp2(ml[u].x - mx) : 0.0f;
+          L += seen ? a * ml[u].y : ml[u].y;
+          o.x += a * (seen ? v[u].x : 0.0f);
+          o.y += a * (seen ? v[u].y : 0.0f);
+          o.z += a * (seen ? v[u].z : 0.0f);
+          o.w += a * (seen ? v[u].w : 0.0f);
         }
       }
     }
@@ -286,7 +295,7 @@ size_t up32(size_t n) { return (n + 31) / 32 * 32; }
 int line_ctas(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
   const int two = 2 * (128 / (Hq / c.Hkv));
   const long long rows = (2LL * (total / two) + n_groups + std::min(c.B, total)) * c.Hkv;
-  const long long places = rows * ((std::min(max_tok, c.cap) + 127) / 128 + kRowCost);
+  const long long places = rows * (row_cost(true) + (std::min(max_tok, c.cap) + 127LL) / 128 * tile_cost(true));
   return (int)std::max<long long>(
       1, std::min<long long>(places / kMinPlaces, std::min(sm_count(), kMaxCtas)));
 }
@@ -333,11 +342,12 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   kernel<<<p.line.ctas, kThreads, smem, s>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // warps of a row, where all rows fit the GPU at once (48 warps an SM); else queries
-  // of a CTA, one after another
-  const long long rows = (long long)p.q.total * p.q.Hq, most = 48LL * sm_count();
+  // warps of a row, where all rows fit the GPU at once (20 warps an SM with eight
+  // records in flight); else queries of a CTA one after another, so that the CTAs do
+  // (32 warps an SM with four)
+  const long long rows = (long long)p.q.total * p.q.Hq, most = 32LL * sm_count();
   int subs = 1;
-  while (subs < kJoinWarps && rows * subs * 2 <= most) subs *= 2;
+  while (subs < kJoinWarps && rows * subs * 2 <= 20LL * sm_count()) subs *= 2;
   const int at_once = kJoinWarps / subs;
   const int batch = (int)std::min<long long>((rows + most - 1) / most, 32);
   cudaLaunchConfig_t cfg = {};
@@ -351,7 +361,8 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   *launches = 2;
-  return cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T>, p, subs, batch);
+  return batch > 1 ? cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, 4>, p, subs, batch)
+                   : cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, 8>, p, subs, batch);
 }
 
 }  // namespace
