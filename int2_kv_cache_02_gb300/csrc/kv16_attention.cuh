@@ -244,7 +244,7 @@ __device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, in
 // A sequence's own entry: nq queries from row r0 on, the first at position at0,
 // against its blocks from `shared` on.
 struct OwnEntry {
-  int r0, nq, n, at0, shared;
+  int r0, nq, n, at0, group, shared;
   __device__ __forceinline__ Span span(const AttnParams& p, int tok, int count) const {
     return Span(at0 + tok, at0 + tok + count - 1, p.q.window, p.q.n_sink).from(shared);
   }
@@ -276,8 +276,8 @@ __device__ __forceinline__ OwnEntry own_entry(const AttnParams& p, int b, bool r
   if (!ok && report) record_error(p.c.status, kDevErrBadPaged);
   x.n = max(x.n, 0);
   x.at0 = x.n - x.nq;
-  const int i = group_of(p.line.groups, b);
-  x.shared = i < 0 ? 0 : shared_of(p.c, p.line.groups, i, p.q.max_tok, false).blocks;
+  x.group = group_of(p.line.groups, b);
+  x.shared = x.group < 0 ? 0 : shared_of(p.c, p.line.groups, x.group, p.q.max_tok, false).blocks;
   return x;
 }
 
@@ -306,6 +306,7 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
       long long n = 0;
       for (int i = 0; i * two < y.nq; ++i) n += y.places(p, i);
       x = (unsigned)saturate(n * p.c.Hkv);
+      if (report) p.line.seq[e - G] = make_int2(y.group, y.shared);
     }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -349,7 +350,8 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
   const int at = x - first[lo];
   int from, to;                   // places of the row
   bool pair;
-  int tiles0 = 0;                 // of a sequence's first query tile, whose keys end first
+  int all, tiles0 = 0;            // tiles of the row, of a sequence's first query tile (whose keys end first)
+  int* runs;
   it.clear = false;
   if (lo < G) {
     const GroupEntry y = group_entry(p, lo, lane, 32, false);
@@ -357,6 +359,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     pair = rows > p.tokens;
     to = row_places(tiles, pair);
     int p0 = 0, chunk = 0;
+    all = tiles;
     if (rows <= two) {
       it.h = min(at / to, p.c.Hkv - 1);
       from = at - it.h * to;
@@ -369,6 +372,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
       const int t = max(z - row_cost(pair), 0) / tile_cost(pair);
       const int i = min(t / blocks.least, blocks.count - 1);
       p0 = tile_place(blocks.first(i), pair);
+      if (blocks.count > 1) all = 0;
       if (i + 1 < blocks.count) to = tile_place(blocks.first(i + 1), pair);
       const int in = in_head - chunks * p0;
       chunk = min(in / (to - p0), chunks - 1);
@@ -381,6 +385,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.nrow = min(two, y.r1 - it.row0);
     it.sp = y.sp;
     it.split = from <= row_cost(pair) ? 0 : from > p0 ? 1 : 2;  // where the records go
+    runs = p.line.prefix_runs;
   } else {
     const OwnEntry y = own_entry(p, lo - G, false);
     int in, chunk = 0;
@@ -422,7 +427,9 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.sp = y.span(p, chunk * two, it.nrow);
     from = max(in, 0);
     pair = y.pair(p, chunk);
-    to = row_places(key_tiles(it.sp.blocks), pair);
+    all = key_tiles(it.sp.blocks);
+    to = row_places(all, pair);
+    runs = p.line.own_runs;
     tiles0 = key_tiles(y.span(p, chunk * two, min(it.nrow, p.tokens)).blocks);
     it.split = from <= row_cost(pair) ? -1 : 1;
   }
@@ -432,6 +439,11 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
   it.k1 = tiles_before(end, pair);
   it.cnt[0] = it.nrow > 0 ? max(it.k1 - it.k0, 0) : 0;
   it.cnt[1] = it.nrow > p.tokens ? it.cnt[0] : 0;
+  if (lane == 0 && it.split <= 0 && all > 0 && it.cnt[0] > 0) {
+    const int last = x - from + row_cost(pair) + (all - 1) * tile_cost(pair);
+    const int n = min(last / share, (int)gridDim.x - 1) - (int)blockIdx.x + 1;
+    runs[(long long)it.row0 * p.c.Hkv + it.h] = blockIdx.x | n << 16;
+  }
   if (lo >= G && it.cnt[0] > 0) {
     if (it.cnt[1] > 0) it.cnt[0] = min(it.k1, max(it.k0, tiles0)) - it.k0;
     it.clear = end == to && it.n % kPage != 0 &&
@@ -1127,11 +1139,15 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 
       // ------------------------------------------------------------ results
       if (PART == kLine && !pair && my_n == 0) {
-        // the other query tile had the only tile of keys
-        if (valid)
-          *reinterpret_cast<float2*>(line_record(
-              p, split, w == 1, (long long)(row_first + tok) * p.q.Hq + h * p.g + head,
-              w * 128 + r)) = make_float2(-INFINITY, 0.0f);
+        // the other query tile had the only tile of keys: nothing seen, outputs 0
+        if (valid) {
+          float* none = line_record(p, split, w == 1,
+                                    (long long)(row_first + tok) * p.q.Hq + h * p.g + head, w * 128 + r);
+          const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          *reinterpret_cast<float2*>(none) = make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+          for (int e = 0; e < kD; e += 8) st_global32(none + kPartHead + e, zero);
+        }
         continue;
       }
       if (ok && my_n > 0) ok = tc5_wait(&sm.o_full[w], o_used++ & 1, state);

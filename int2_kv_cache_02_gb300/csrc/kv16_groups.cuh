@@ -93,6 +93,11 @@ struct SharedParts {
   float* cut;               // [ctas][2][256]
   int* first;               // [groups + B + 1]: the entries' first places, the line's end
   int4* group;              // [groups]: tiles of a row, first query row, the row behind the last
+  int2* seq;                // [B]: a sequence's group or -1, the blocks that are its group's
+  // by a chunk's first query row and the KV head: the CTAs that have its tiles (of
+  // rows that have any and, prefixes, one block): first | count << 16
+  int* prefix_runs;         // [total][Hkv]
+  int* own_runs;
   int ctas;
   int tokens, g;            // tokens of a query tile, heads of a group
 };

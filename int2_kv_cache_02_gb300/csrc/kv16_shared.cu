@@ -74,30 +74,47 @@ __device__ __forceinline__ Runs runs_of(unsigned at, unsigned more, unsigned per
   const int c0 = min((int)(at / per), ctas - 1);
   return Runs{c0, min((int)((at + more) / per), ctas - 1) - c0 + 1};
 }
+// (bounded: what is not written for a row out of range may hold anything)
+__device__ __forceinline__ Runs runs_from(int x, int ctas) {
+  const int c0 = min(x & 0xffff, ctas - 1);
+  return Runs{c0, min(x >> 16, ctas - c0)};
+}
 
-// The records of both parts of a row (query, head) joined by a warp, or by `subs`
-// of the CTA's four, each every so-many-th record.  A CTA has rows of one KV head,
-// of `batch` queries one after another.  Queries that belong to no sequence are
-// left alone.
+// The records of both parts of a row (query, head) joined by a warp, and queries that
+// belong to no sequence left alone.  Few rows (BATCH false): a CTA has rows of one
+// query and KV head, a warp each or `subs` of its four warps, each every so-many-th
+// record.  Many: a warp has the group's rows of `batch` queries, one after another.
 //
-// Bound by latency: groups and the line are a chain of loads, then a record's place
-// takes a few divisions.  So a warp's lanes find 32 records at a time, a lane each,
-// once for the queries of a batch that lie in the same rows of the line, and U
-// records are in flight.
-constexpr int kJoinWarps = 4;
-template <class T, int U>
-__global__ void __launch_bounds__(kJoinWarps * 32, U == 4 ? 8 : 5)
+// Bound by latency: the sequence, its group and its runs are a chain of loads, then
+// a record's place is found.  So a warp's lanes find 32 records at a time, a lane
+// each, once for the rows that lie in the same rows of the line, and U records are
+// in flight.
+constexpr int kJoinWarps = 4, kJoinCtas = 6, kBatchCtas = 5;     // warps of a CTA, CTAs of an SM
+template <class T, bool BATCH>
+__global__ void __launch_bounds__(kJoinWarps * 32, BATCH ? kBatchCtas : kJoinCtas)
 kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batch) {
-  __shared__ float4 s_o[kJoinWarps][32];
-  __shared__ float2 s_ml[kJoinWarps];
+  __shared__ float4 s_o[BATCH ? 1 : kJoinWarps][32];
+  __shared__ float2 s_ml[BATCH ? 1 : kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SharedParts& s = p.line;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = p.g, two = 2 * p.tokens;
-  const int rows = kJoinWarps / subs, slices = (g + rows - 1) / rows, rh = blockIdx.x / slices;
-  const int first_r = rh / p.c.Hkv * batch, h = rh % p.c.Hkv;
-  const int head = (blockIdx.x - rh * slices) * rows + warp / subs, sub = warp % subs;
-  const int G = s.groups.n, end_r = min(first_r + batch, p.q.total);
-  const unsigned per = line_share(__ldcg(s.first + G + p.c.B), s.ctas), hkv = p.c.Hkv;
+  int first_r, end_r, h, head0 = 0, sub = 0;
+  if constexpr (BATCH) {
+    const int x = blockIdx.x / p.c.Hkv;
+    h = blockIdx.x - x * p.c.Hkv;
+    first_r = (x * kJoinWarps + warp) * batch;
+    end_r = min(first_r + batch, p.q.total);
+    subs = 1;
+  } else {
+    const int rows = kJoinWarps / subs, slices = (g + rows - 1) / rows, x = blockIdx.x / slices;
+    first_r = x / p.c.Hkv;
+    end_r = first_r + 1;
+    h = x - first_r * p.c.Hkv;
+    head0 = (blockIdx.x - x * slices) * rows + warp / subs;
+    sub = warp % subs;
+  }
+  const int G = s.groups.n;
+  const unsigned per = line_share(__ldcg(s.first + G + p.c.B), s.ctas);
 
   // of the queries [.., same): their sequence, and their rows of the line
   int same = first_r, b = -1, seq1 = 0, n = 0;
@@ -105,16 +122,16 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
   int twice_own = 0, twice = 0;     // two records a run
   int in_own = 0, in_prefix = 0;    // the query's place in its chunks
   bool pair = false;
-  int tiles = 0, chunks = 1, chunk = 0;
+  int chunks = 1, chunk = 0;
   unsigned at = 0;
   Blocks blocks(0, 1, false, 1);
-  // the lane's record in 32-byte steps from the first of all, or none; from a query to
-  // the next it moves by `step`, and by `fix` more into a chunk's second tile
+  // the lane's record of head 0 in 32-byte steps from the first of all, or none; from a
+  // query to the next it moves by `step`, and by `fix` more into a chunk's second tile
   constexpr unsigned kNone = ~0u, kSteps = kPartFloats / 8;
   const unsigned fix = (128 - p.tokens * g) * kSteps;
   unsigned off = kNone, step = 0;
   int in = -1;                      // 0 own, 1 prefix: which chunk the record's place goes by
-  auto locate = [&](int j, long long row) {
+  auto locate = [&](int j, int r) {
     off = kNone;
     step = 0;
     in = -1;
@@ -137,19 +154,20 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
     if (j >= x.n) return;
     const float* e;
     if (j == 0 && k == 0) {
-      e = (mine ? s.own : s.prefix) + ((long long)second * p.q.total * p.q.Hq + row) * kPartFloats;
+      e = (mine ? s.own : s.prefix) +
+          (((long long)second * p.q.total + r) * p.q.Hq + h * g) * kPartFloats;
       step = p.q.Hq * kSteps;
     } else {
       in = mine ? 0 : 1;
       const int i = mine ? in_own : in_prefix, w = i >= p.tokens ? 1 : 0;
       e = s.cut + ((long long)(x.c0 + j) * 512 + (j == 0 ? 256 : 0) + (second + w) * 128 +
-                   (i - w * p.tokens) * g + head) * kPartFloats;
+                   (i - w * p.tokens) * g) * kPartFloats;
       step = g * kSteps;
     }
     off = (unsigned)((e - s.prefix) / 8);
   };
+#pragma unroll 1
   for (int r = first_r; r < end_r; ++r) {
-    const long long row = (long long)r * p.q.Hq + h * g + head;
     if (r < same) {
       // the same rows of the line, the next query
       ++in_own;
@@ -171,121 +189,196 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
           continue;
         }
       }
-      const int f0 = __ldcg(s.first + G + b), f1 = __ldcg(s.first + G + b + 1);
-      const int i = warp_sequence(s.groups.group, G, b), own_chunk = (r - seq0) / two;
-      int to = min(seq1, seq0 + (own_chunk + 1) * two);
-      in_own = r - seq0 - own_chunk * two;
-      const int per_head = (int)((unsigned)(f1 - f0) / hkv);
-      const bool single = seq1 - seq0 - own_chunk * two <= p.tokens;
-      int at_own = f0 + per_head * h;
-      int more = per_head - row_cost(!single) - tile_cost(!single);
-      if (seq1 - seq0 > two) {        // several chunks
-        const OwnEntry y = own_entry(p, b, false);
-        int before = 0;
-        for (int k = lane; k < own_chunk; k += 32) before += y.places(p, k);
-        at_own += (int)__reduce_add_sync(0xffffffffu, before);
-        more = (y.tiles(p, own_chunk) - 1) * tile_cost(!single);
-      }
-      own = f1 > f0 && more >= 0 ? runs_of(at_own + row_cost(!single), more, per, s.ctas) : Runs{0, 0};
-      twice_own = single;
-      prefix = Runs{0, 0};
+      const int2 sq = __ldcg(s.seq + b);
+      const int len = kv16_length(p.c, b, p.q.max_tok), own_chunk = (r - seq0) / two;
+      const int row0 = seq0 + own_chunk * two;
+      int to = min(seq1, row0 + two);
+      in_own = r - row0;
+      twice_own = seq1 - row0 <= p.tokens;
+      own = prefix = Runs{0, 0};
+      // does the chunk's last query stand in or behind the first block of its own?
+      if (len - (seq1 - to) - 1 >= sq.y * kPage && len > 0)
+        own = runs_from(__ldcg(s.own_runs + (long long)row0 * p.c.Hkv + h), s.ctas);
       blocks = Blocks(0, 1, false, 1);
-      if (i >= 0) {
-        const int4 gr = __ldcg(s.group + i);
-        const int g0 = __ldcg(s.first + i), all = (int)((unsigned)(__ldcg(s.first + i + 1) - g0) / hkv);
-        tiles = gr.x;
-        const int rows = gr.z - gr.y;
-        pair = rows > p.tokens;
-        chunks = (rows + two - 1) / two;
+      if (sq.x >= 0) {
+        const int4 gr = __ldcg(s.group + sq.x);
+        const int tiles = gr.x, rows = gr.z - gr.y;
         chunk = (r - gr.y) / two;
-        if (tiles > 0 && r >= gr.y && chunk < chunks && all > 0) {
-          in_prefix = r - gr.y - chunk * two;
-          at = g0 + (unsigned)all * h;
-          twice = rows - chunk * two <= p.tokens;
+        chunks = (rows + two - 1) / two;
+        if (tiles > 0 && r >= gr.y && chunk < chunks) {
+          const int p_row0 = gr.y + chunk * two;
+          pair = rows > p.tokens;
+          in_prefix = r - p_row0;
+          twice = gr.z - p_row0 <= p.tokens;
+          to = min(to, p_row0 + two);
           blocks = Blocks(tiles, chunks, pair, per);
-          prefix = blocks.count > 1
-                       ? Runs{0, blocks.count * kBlockRuns}
-                       : runs_of(at + (unsigned)chunk * row_places(tiles, pair) + row_cost(pair),
-                                 (tiles - 1) * tile_cost(pair), per, s.ctas);
-          to = min(to, gr.y + (chunk + 1) * two);
+          if (blocks.count > 1) {
+            at = __ldcg(s.first + sq.x) + (unsigned)chunks * (unsigned)row_places(tiles, pair) * h;
+            prefix = Runs{0, blocks.count * kBlockRuns};
+          } else {
+            prefix = runs_from(__ldcg(s.prefix_runs + (long long)p_row0 * p.c.Hkv + h), s.ctas);
+          }
         }
       }
       same = to;
-      n = head < g ? (own.n << twice_own) + (prefix.n << twice) : 0;
-      locate(sub + lane * subs, row);
+      n = (own.n << twice_own) + (prefix.n << twice);
+      locate(sub + lane * subs, r);
     }
     if (b < 0) continue;
-    float M = -INFINITY, L = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (BATCH) {
+      const int half = lane >> 4, ch = lane & 15;      // 8 channels a lane
 #pragma unroll 1
-    for (int j0 = sub; j0 < n; j0 += 32 * subs) {
-      if (n > 32 * subs) locate(j0 + lane * subs, row);
-      const int count = min((n - j0 + subs - 1) / subs, 32);
+      for (int pair0 = 0; pair0 < g; pair0 += 2) {
+        const int head = min(pair0 + half, g - 1);     // (an odd group's last row twice)
+        float M = -INFINITY, L = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-      for (int u0 = 0; u0 < count; u0 += U) {
-        float2 ml[U];
-        float4 v[U];
+        for (int j0 = 0; j0 < n; j0 += 32) {
+          if (n > 32) locate(j0 + lane, r);
+          unsigned have = __ballot_sync(0xffffffffu, off != kNone);
+#pragma unroll 1
+          while (have) {
+            constexpr int U = 5;
+            float2 ml[U];
+            float4 v[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const unsigned from = __shfl_sync(0xffffffffu, off, (u0 + u) & 31);
-          ml[u] = make_float2(-INFINITY, 0.0f);
-          v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (u0 + u < count && from != kNone) {
-            const float* e = s.prefix + (size_t)from * 8;
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(e));
-            v[u] = __ldcg(reinterpret_cast<const float4*>(e + kPartHead) + lane);
+            for (int u = 0; u < U; ++u) {
+              const unsigned from = __shfl_sync(0xffffffffu, off, __ffs(have) - 1);
+              ml[u] = make_float2(-INFINITY, 0.0f);
+              v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (have) {
+                const float* e = s.prefix + (size_t)(from + head * kSteps) * 8;
+                ml[u] = __ldcg(reinterpret_cast<const float2*>(e));
+                v[u][0] = __ldcg(reinterpret_cast<const float4*>(e + kPartHead) + 2 * ch);
+                v[u][1] = __ldcg(reinterpret_cast<const float4*>(e + kPartHead) + 2 * ch + 1);
+              }
+              have &= have - 1;
+            }
+            float mx = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+            // (a maximum of -inf has met only sums of 0, or NaN, and outputs of 0)
+            const float ms = mx == -INFINITY ? 0.0f : mx, f = fast_exp2(M - ms);
+            M = mx;
+            L *= f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] *= f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const float a = fast_exp2(ml[u].x - ms);
+              L += a * ml[u].y;
+              o[0] += a * v[u][0].x;
+              o[1] += a * v[u][0].y;
+              o[2] += a * v[u][0].z;
+              o[3] += a * v[u][0].w;
+              o[4] += a * v[u][1].x;
+              o[5] += a * v[u][1].y;
+              o[6] += a * v[u][1].z;
+              o[7] += a * v[u][1].w;
+            }
           }
         }
-        float mx = M;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const long long row = (long long)r * p.q.Hq + h * g + head;
+        reinterpret_cast<uint4*>(p.out + row * kD)[ch] =
+            make_uint4(T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv),
+                       T::pack(o[4] * inv, o[5] * inv), T::pack(o[6] * inv, o[7] * inv));
+        if (p.lse && ch == 0) p.lse[row] = row_lse<T>(M, L);
+        bool open = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
-        const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
+        for (int k = 0; k < 8; ++k) open |= o[k] != o[k];
+        const unsigned bad = __ballot_sync(0xffffffffu, open && L == L);
+        if (bad == 0) continue;
+        // rows with a channel that is NaN though the sum is not, by the whole warp
+        for (int z = 0; z < 2 && pair0 + z < g; ++z) {
+          if (!(bad & (z ? 0xffff0000u : 0xffffu))) continue;
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float lo = __shfl_sync(0xffffffffu, o[k], z * 16 + (lane >> 1));
+            const float hi = __shfl_sync(0xffffffffu, o[k + 4], z * 16 + (lane >> 1));
+            x[k] = lane & 1 ? hi : lo;
+          }
+          const float i = __shfl_sync(0xffffffffu, inv, z * 16);
+          const float4 y = settle<T>(p, b, h, seq1 - r, make_float4(x[0], x[1], x[2], x[3]));
+          __syncwarp();
+          reinterpret_cast<uint2*>(p.out + ((long long)r * p.q.Hq + h * g + pair0 + z) * kD)[lane] =
+              make_uint2(T::pack(y.x * i, y.y * i), T::pack(y.z * i, y.w * i));
+        }
+      }
+    } else {
+      if (head0 >= g) n = 0;
+      float M = -INFINITY, L = 0.0f;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+      for (int j0 = sub; j0 < n; j0 += 32 * subs) {
+        if (n > 32 * subs) locate(j0 + lane * subs, r);
+        unsigned have = __ballot_sync(0xffffffffu, off != kNone);
+#pragma unroll 1
+        while (have) {
+          constexpr int U = 8;
+          float2 ml[U];
+          float4 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const unsigned from = __shfl_sync(0xffffffffu, off, __ffs(have) - 1);
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (have) {
+              const float* e = s.prefix + (size_t)(from + head0 * kSteps) * 8;
+              ml[u] = __ldcg(reinterpret_cast<const float2*>(e));
+              v[u] = __ldcg(reinterpret_cast<const float4*>(e + kPartHead) + lane);
+            }
+            have &= have - 1;
+          }
+          float mx = M;
+#pragma unroll
+          for (int u = 0; u < U; ++u) mx = fmaxf(mx, ml[u].x);
+          const float ms = mx == -INFINITY ? 0.0f : mx, f = fast_exp2(M - ms);
+          M = mx;
+          L *= f;
+          o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float a = fast_exp2(ml[u].x - ms);
+            L += a * ml[u].y;
+            o.x += a * v[u].x;
+            o.y += a * v[u].y;
+            o.z += a * v[u].z;
+            o.w += a * v[u].w;
+          }
+        }
+      }
+      if (subs > 1) {
+        s_o[warp][lane] = o;
+        if (lane == 0) s_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (sub > 0) return;
+        float mx = M;
+        for (int u = 1; u < subs; ++u) mx = fmaxf(mx, s_ml[warp + u].x);
+        const float ms = mx == -INFINITY ? 0.0f : mx, f = fast_exp2(M - ms);
         M = mx;
         L *= f;
         o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          // (a record that has seen nothing has no outputs; its sum may be NaN)
-          const bool seen = ml[u].x != -INFINITY;
-          const float a = seen ? fast_exp2(ml[u].x - mx) : 0.0f;
-          L += seen ? a * ml[u].y : ml[u].y;
-          o.x += a * (seen ? v[u].x : 0.0f);
-          o.y += a * (seen ? v[u].y : 0.0f);
-          o.z += a * (seen ? v[u].z : 0.0f);
-          o.w += a * (seen ? v[u].w : 0.0f);
+        for (int u = 1; u < subs; ++u) {
+          const float2 ml = s_ml[warp + u];
+          const float4 v = s_o[warp + u][lane];
+          const float a = fast_exp2(ml.x - ms);
+          L += a * ml.y;
+          o.x += a * v.x;
+          o.y += a * v.y;
+          o.z += a * v.z;
+          o.w += a * v.w;
         }
       }
+      if (head0 >= g) return;
+      const bool open = o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w;
+      if (L == L && __any_sync(0xffffffffu, open)) o = settle<T>(p, b, h, seq1 - r, o);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const long long row = (long long)r * p.q.Hq + h * g + head0;
+      reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
+          make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
+      if (p.lse && lane == 0) p.lse[row] = row_lse<T>(M, L);
     }
-    if (subs > 1) {
-      __syncthreads();
-      s_o[warp][lane] = o;
-      if (lane == 0) s_ml[warp] = make_float2(M, L);
-      __syncthreads();
-      if (sub > 0) continue;
-      float mx = M;
-      for (int u = 1; u < subs; ++u) mx = fmaxf(mx, s_ml[warp + u].x);
-      const float f = mx == -INFINITY ? 1.0f : fast_exp2(M - mx);
-      M = mx;
-      L *= f;
-      o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-      for (int u = 1; u < subs; ++u) {
-        const float2 ml = s_ml[warp + u];
-        const float4 v = s_o[warp + u][lane];
-        const float a = mx == -INFINITY ? 1.0f : fast_exp2(ml.x - mx);
-        L += a * ml.y;
-        o.x += a * v.x;
-        o.y += a * v.y;
-        o.z += a * v.z;
-        o.w += a * v.w;
-      }
-    }
-    if (head >= g) continue;
-    const bool open = o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w;
-    if (L == L && __any_sync(0xffffffffu, open)) o = settle<T>(p, b, h, seq1 - r, o);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
-        make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
-    if (p.lse && lane == 0) p.lse[row] = row_lse<T>(M, L);
   }
 }
 
@@ -320,6 +413,9 @@ SharedParts layout(const Kv16& c, int Hq, const Kv16Groups& groups, int total, i
   s.own = static_cast<float*>(take(2 * rows * rec));
   s.cut = static_cast<float*>(take((size_t)s.ctas * 512 * rec));
   s.first = static_cast<int*>(take((size_t)(groups.n + c.B + 1) * sizeof(int)));
+  s.seq = static_cast<int2*>(take((size_t)c.B * sizeof(int2)));
+  s.prefix_runs = static_cast<int*>(take((size_t)total * c.Hkv * sizeof(int)));
+  s.own_runs = static_cast<int*>(take((size_t)total * c.Hkv * sizeof(int)));
   s.group = static_cast<int4*>(take((size_t)groups.n * sizeof(int4)));
   *bytes = at - reinterpret_cast<uintptr_t>(ws) + 16;
   return s;
@@ -342,17 +438,18 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   kernel<<<p.line.ctas, kThreads, smem, s>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // warps of a row, where all rows fit the GPU at once (20 warps an SM with eight
-  // records in flight); else queries of a CTA one after another, so that the CTAs do
-  // (32 warps an SM with four)
-  const long long rows = (long long)p.q.total * p.q.Hq, most = 32LL * sm_count();
+  // a warp or more for a row; where that is far more than a wave and the rows have few
+  // records (several queries a sequence), queries of a warp
+  const long long rows = (long long)p.q.total * p.q.Hq, sms = sm_count();
+  const long long wave = kJoinWarps * kJoinCtas * sms, warps = kJoinWarps * kBatchCtas * sms;
+  const bool many = p.q.start && rows > 2 * wave;
+  const int batch = many ? (int)std::min<long long>((rows + warps * p.g - 1) / (warps * p.g), 32) : 1;
   int subs = 1;
-  while (subs < kJoinWarps && rows * subs * 2 <= 20LL * sm_count()) subs *= 2;
-  const int at_once = kJoinWarps / subs;
-  const int batch = (int)std::min<long long>((rows + most - 1) / most, 32);
+  while (subs < kJoinWarps && rows * subs * 2 <= wave) subs *= 2;
+  const int at_once = kJoinWarps / subs, queries = batch * kJoinWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = (unsigned)((long long)((p.q.total + batch - 1) / batch) * p.c.Hkv *
-                          ((p.g + at_once - 1) / at_once));
+  cfg.gridDim = (unsigned)(many ? (long long)((p.q.total + queries - 1) / queries) * p.c.Hkv
+                                : (long long)p.q.total * p.c.Hkv * ((p.g + at_once - 1) / at_once));
   cfg.blockDim = kJoinWarps * 32;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -361,8 +458,8 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   *launches = 2;
-  return batch > 1 ? cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, 4>, p, subs, batch)
-                   : cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, 8>, p, subs, batch);
+  return many ? cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, true>, p, 1, batch)
+              : cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, false>, p, subs, 1);
 }
 
 }  // namespace
