@@ -1048,15 +1048,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         return (sum0.x + sum0.y) + (sum1.x + sum1.y);
       };
-      // kLine: a round before the first, on whatever there is and without effect, while
-      // the first keys are on their way: it fetches the round's instructions
-      for (int j = PART == kLine && ni == 0 ? -1 : 0; j < my_n; ++j) {
-        const bool warm = PART == kLine && j < 0;
-        if (!warm) {
-          ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
-          if (!ok) break;
-          tc5_fence_after();
-        }
+      for (int j = 0; j < my_n; ++j) {
+        ok = tc5_wait(&sm.s_full[w], s_used & 1, state);
+        if (!ok) break;
+        tc5_fence_after();
         const int t = pair ? j : ((first_tile ^ w) & 1) + 2 * j;      // key tile of the item
         const bool inside = t >= in0 && t < in1;
         uint32_t sr[128];
@@ -1113,10 +1108,6 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           // queries, or what was in shared memory)
           if (__any_sync(0xffffffffu, valid && m == -INFINITY)) raise();
           float sum = weigh(x);
-          if (warm) {
-            m = -INFINITY;
-            continue;
-          }
           if (__any_sync(0xffffffffu, valid && sum > Range<T>::kMost)) {
             tc5_ld32(x, s_addr + 64 * i);
             tc5_ld32(x + 32, s_addr + 64 * i + 32);
@@ -1134,7 +1125,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           if (lane == 0) mbar_arrive(&sm.p_full[w][i]);
         }
         if (!ok) break;
-        if (!warm) ++s_used;
+        ++s_used;
       }
 
       // ------------------------------------------------------------ results
