@@ -685,7 +685,7 @@ oscar_status oscar_kv16_fork(const oscar_kv16_cache* src, const oscar_kv16_cache
  *  counts     device int32 [2]: the number of moves, L
  * An entry of n_pages or more is recorded in the status word and stays as it is.
  * workspace: oscar_page_compact_workspace_bytes (no initialisation).
- * B * max_blocks < 2^31 - 128 (else OSCAR_ERR_UNSUPPORTED).
+ * B * max_blocks < 2^31 - 128, n_pages <= 12582912 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_page_compact(const int32_t* block_table, int32_t* new_table, int B,
                                 int max_blocks, int n_pages, int32_t* moves, int32_t* counts,
@@ -701,6 +701,7 @@ size_t oscar_page_compact_workspace_bytes(int B, int max_blocks, int n_pages);
  * src and dst are paged, of one type and number of heads; they are one pool, in
  * which no page is written twice or both written and read, or lie apart.  Pairs
  * with a page out of range are skipped and recorded.
+ * max_pairs * Hkv < 2^31 - 128 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
                                    const int32_t* pairs, const int32_t* n_pairs, int max_pairs,

@@ -471,6 +471,7 @@ oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16
   if (!aligned(pairs, 8) || !aligned(n_pairs, 4)) return OSCAR_ERR_ALIGNMENT;
   st = copy_ok(src, dst);
   if (st != OSCAR_OK || max_pairs == 0) return st;
+  if (max_pairs > kMaxTokens / src->Hkv) return OSCAR_ERR_UNSUPPORTED;
   Kv16 s = view(src), d = view(dst);
   s.status = d.status = device_status_word();
   if (!s.status) return OSCAR_ERR_CUDA;
@@ -480,7 +481,7 @@ oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16
 }
 
 size_t oscar_page_compact_workspace_bytes(int B, int max_blocks, int n_pages) {
-  if (B <= 0 || max_blocks <= 0 || n_pages <= 0) return 0;
+  if (B <= 0 || max_blocks <= 0 || n_pages <= 0 || n_pages > kMaxPages) return 0;
   return page_compact_ws_bytes(n_pages);
 }
 
@@ -494,7 +495,7 @@ oscar_status oscar_page_compact(const int32_t* block_table, int32_t* new_table, 
       !aligned(counts, 4))
     return OSCAR_ERR_ALIGNMENT;
   const long long entries = (long long)B * max_blocks;
-  if (entries > kMaxTokens) return OSCAR_ERR_UNSUPPORTED;
+  if (entries > kMaxTokens || n_pages > kMaxPages) return OSCAR_ERR_UNSUPPORTED;
   const size_t tb = table_bytes(B, max_blocks);
   const Range out[] = {{reinterpret_cast<const char*>(new_table), tb},
                        {reinterpret_cast<const char*>(moves), (size_t)(n_pages / 2) * 8},
@@ -509,10 +510,9 @@ oscar_status oscar_page_compact(const int32_t* block_table, int32_t* new_table, 
   if (!aligned(workspace, 16)) return OSCAR_ERR_ALIGNMENT;
   unsigned* status = device_status_word();
   if (!status) return OSCAR_ERR_CUDA;
-  int launches = 0;
   const cudaError_t e = launch_page_compact(block_table, new_table, entries, n_pages, moves, counts,
-                                            workspace, status, &launches, as_stream(stream));
-  count_launches(launches);
+                                            workspace, status, as_stream(stream));
+  count_launches(1);
   return from_cuda(e);
 }
 

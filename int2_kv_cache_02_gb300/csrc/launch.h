@@ -250,7 +250,8 @@ cudaError_t launch_kv16_fork(const Kv16& src, const Kv16& dst, const int32_t* pa
                              bool same, int max_tok, cudaStream_t s);
 cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long long entries,
                                 int n_pages, int32_t* moves, int32_t* counts, void* ws,
-                                unsigned* status, int* launches, cudaStream_t s);
+                                unsigned* status, cudaStream_t s);
+constexpr int kMaxPages = 12582912;     // of a pool that is compacted
 size_t page_compact_ws_bytes(int n_pages);
 cudaError_t launch_kv16_copy_pages(const Kv16& src, const Kv16& dst, const int32_t* pairs,
                                    const int32_t* n_pairs, int max_pairs, cudaStream_t s);

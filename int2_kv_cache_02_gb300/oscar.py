@@ -806,19 +806,23 @@ def page_compact(block_table: torch.Tensor, new_table: torch.Tensor, n_pages: in
     table with the new ids (may be block_table itself); moves int32
     [n_pages // 2][2]: the pages to copy, old and new id, for kv16_copy_pages;
     counts int32 [2]: the number of moves, L."""
-    tensors = (block_table, new_table, moves, counts)
-    if any(t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or
-           t.device != block_table.device for t in tensors) or \
-            block_table.dim() != 2 or new_table.shape != block_table.shape or \
+    index, i32 = block_table.get_device(), torch.int32
+    for t in (block_table, new_table, moves, counts, workspace):
+        if t.get_device() != index or index < 0 or not t.is_contiguous() or \
+                (t.dtype is not i32 and t is not workspace):
+            raise ValueError("expected dense int32 tensors on one GPU, and a workspace there")
+    if block_table.dim() != 2 or new_table.shape != block_table.shape or \
             moves.numel() != n_pages // 2 * 2 or counts.numel() != 2:
-        raise ValueError("expected dense int32 tensors on one device: tables [B][max_blocks], "
-                         "moves [n_pages // 2][2], counts [2]")
-    if workspace.device != block_table.device or not workspace.is_contiguous():
-        raise ValueError(f"expected a dense workspace on {block_table.device}")
-    with torch.cuda.device(block_table.device):
-        _check(_lib.oscar_page_compact(_ptr(block_table), _ptr(new_table), *block_table.shape,
-                                       n_pages, _ptr(moves), _ptr(counts), _ptr(workspace),
-                                       workspace.nbytes, _stream(stream)), "oscar_page_compact")
+        raise ValueError("expected tables [B][max_blocks], moves [n_pages // 2][2], counts [2]")
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    B, max_blocks = block_table.shape
+    args = (block_table.data_ptr(), new_table.data_ptr(), B, max_blocks, n_pages, moves.data_ptr(),
+            counts.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
+    if torch._C._cuda_getDevice() == index:
+        _check(_lib.oscar_page_compact(*args), "oscar_page_compact")
+    else:
+        with torch.cuda.device(index):
+            _check(_lib.oscar_page_compact(*args), "oscar_page_compact")
 
 
 def kv16_copy_pages(src: KV16Cache, dst: KV16Cache, pairs: torch.Tensor, n_pairs: torch.Tensor,
