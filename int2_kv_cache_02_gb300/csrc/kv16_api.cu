@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "kv16.cuh"
+#include "kv16_line.h"
 #include "launch.h"
 
 namespace {
@@ -101,12 +102,13 @@ bool decode_size_ok(const oscar_kv16_cache* c, int max_tok) {
   return c->B <= kMaxDecodeBatch && rows <= kMaxDecodeRows && rows * blocks <= kMaxTokens;
 }
 
-// The places of the line (kv16_groups.cuh: six a tile of 128 keys, 20 more a row
-// of a group's or a sequence's 256-row chunk) are numbered in 32 bits.
+// The places of the line (kv16_line.h: rows are the groups' and the sequences'
+// chunks of 256 query rows) are numbered in 32 bits.
 bool shared_size_ok(const oscar_kv16_cache* c, int Hq, int n_groups, int total, int max_tok) {
   const long long two = 2 * (128 / (Hq / c->Hkv));
   const long long rows = (2 * (total / two) + n_groups + c->B) * c->Hkv;
-  const long long places = 6 * ((std::min<long long>(max_tok, capacity(c)) + 127) / 128) + 20;
+  const long long places =
+      tile_cost(true) * ((std::min<long long>(max_tok, capacity(c)) + 127) / 128) + row_cost(true);
   return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxTokens &&
          rows <= kMaxTokens && rows * places <= kMaxTokens;
 }

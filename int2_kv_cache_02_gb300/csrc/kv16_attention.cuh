@@ -65,7 +65,7 @@
 // leave (m, l, o[128]) records that a second kernel joins.
 //
 // kLine: sequences that share prefixes.  The same kernel over a line of work (see
-// kv16_groups.cuh) in which a group's queries meet its shared blocks together and
+// kv16_line.h) in which a group's queries meet its shared blocks together and
 // each sequence's queries the blocks behind; an item is the piece of a CTA's run
 // that lies in one row of the line.  All items leave records.
 #pragma once

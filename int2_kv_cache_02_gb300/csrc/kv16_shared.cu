@@ -2,7 +2,7 @@
 // prefix's end are worked once for all its queries, so that up to 256 (query,
 // head) rows meet each key and value that is read; what stands behind them a
 // sequence at a time.  Both by the tensor-core kernel of the prompt attention, over
-// one line of key tiles that its CTAs share evenly (kLine, kv16_groups.cuh); the
+// one line of key tiles that its CTAs share evenly (kLine, kv16_line.h); the
 // records that it leaves are joined by their maxima and sums in a second launch.
 #include "kv16_attention.cuh"
 
@@ -15,8 +15,6 @@ __device__ __forceinline__ unsigned seen_in(float x) {
   return x != x ? kSeenNan : x == INFINITY ? kSeenPlus : x == -INFINITY ? kSeenMinus : 0u;
 }
 
-// Blocks of a chunk are at least a run's length and below two: three runs at most.
-constexpr int kBlockRuns = 3;
 constexpr int kMaxCtas = 160;      // of the prefixes' kernel
 
 // The channels of a row (4 lane .. 4 lane + 3, relative to its sum) that are NaN
@@ -65,15 +63,6 @@ __device__ __noinline__ float4 settle(const AttnParams& p, int b, int h, int bac
   return make_float4(o[0], o[1], o[2], o[3]);
 }
 
-// The CTAs [c0, c0 + n) that have tiles of a block whose first tile is at place `at`
-// of the line and whose last is `more` places on.
-struct Runs {
-  int c0, n;
-};
-__device__ __forceinline__ Runs runs_of(unsigned at, unsigned more, unsigned per, int ctas) {
-  const int c0 = min((int)(at / per), ctas - 1);
-  return Runs{c0, min((int)((at + more) / per), ctas - 1) - c0 + 1};
-}
 // (bounded: what is not written for a row out of range may hold anything)
 __device__ __forceinline__ Runs runs_from(int x, int ctas) {
   const int c0 = min(x & 0xffff, ctas - 1);

@@ -148,6 +148,15 @@ def test_decode_long_prefix(L):
     decode(L, case, case.cache(L), 16)
 
 
+@pytest.mark.parametrize("members,prefix,Hq,Hkv,dtype", [
+    (130, 5000, 4, 1, BF), (200, 2100, 8, 2, FP), (37, 3333, 16, 1, BF), (90, 7000, 5, 1, FP)])
+def test_decode_blocks(L, members, prefix, Hq, Hkv, dtype):
+    """More queries than two tiles hold, over a prefix that is worked in blocks."""
+    lens = [prefix + 1 + (11 * b) % 70 for b in range(members)]
+    case = SharedCase([members, 3], [prefix, 600], lens + [640, 601, 700], Hkv, dtype=dtype, seed=members)
+    decode(L, case, case.cache(L), Hq)
+
+
 def test_decode_many_sequences_and_groups(L):
     """The most sequences, each a group of its own, and all in pairs."""
     lens = [33 + b % 40 for b in range(4096)]
@@ -228,6 +237,54 @@ def test_what_a_query_sees_reaches_it(L, where, dtype):
     assert decode(L, case, cache, 4, q=q, check=False).isnan().all()
     assert attend(L, case, cache, [1, 1], 4, q=q, extra=0, check=False)[0].isnan().all()
     assert L.device_status() == 0
+
+
+@pytest.mark.parametrize("members,new,prefix", [(40, 1, 600), (3, 40, 600), (3, 9, 130), (9, 230, 4000)])
+def test_infinities_in_every_kind_of_row(L, members, new, prefix):
+    """The same for rows that fill both query tiles, for several queries, for many
+    rows: an infinity and a NaN in the prefix's values, others in one sequence's own."""
+    lens = [prefix + new + 3 * b for b in range(members)]
+    case = SharedCase([members], [prefix], lens, 1, seed=members)
+    for b in range(members):
+        case.v[b][:, 77, 3] = math.inf
+        case.v[b][:, 78, 40] = math.nan
+    case.v[1][:, prefix, 9] = -math.inf          # every new query of the sequence sees it
+    cache = case.cache(L)
+    start = R.start_of([new] * members)
+    q = case.normal(start[-1], 4)
+    outs = [attend(L, case, cache, [new] * members, 4, q=q, extra=0, check=False)[0]]
+    if new == 1:
+        outs.append(decode(L, case, cache, 4, q=q, check=False))
+    assert L.device_status() == 0
+    for out in outs:
+        assert (out[:, :, 3] == math.inf).all() and out[:, :, 40].isnan().all()
+        rows = slice(start[1], start[2])
+        assert (out[rows, :, 9] == -math.inf).all()
+        keep = [c for c in range(128) if c not in (3, 9, 40)]
+        assert out[:, :, keep].isfinite().all()
+    for b in (0, 1, members - 1):
+        for c in (3, 9, 40):
+            case.v[b][:, :, c] = 0.0
+        rows = slice(start[b], start[b + 1])
+        o, _, _, tol, _, _ = R.attend(case, b, q[rows])
+        for out in outs:
+            R.assert_within(out[rows][:, :, keep], o[:, :, keep], tol[:, :, keep], f"sequence {b}")
+
+
+def test_workspace_at_any_16_bytes(L):
+    """A workspace that begins 16 bytes behind an allocation's start: the same bits."""
+    case = SharedCase([5], [300], [330, 310, 420, 301, 390], 2)
+    cache = case.cache(L)
+    q = case.normal(5, 8).cuda()
+    group, prefix = case.groups()
+    n = L.kv16_shared_decode_workspace_bytes(cache, 8, 1, cache.capacity)
+    big = torch.full((n + 32,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    for at, out in zip((0, 16), outs):
+        L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, cache.capacity, out, big[at:at + n])
+    assert L.device_status() == 0
+    assert torch.equal(bits(outs[0]), bits(outs[1]))
+    assert (big[n + 16:] == 255).all()
 
 
 def test_far_apart_scores(L):
