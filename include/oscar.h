@@ -608,8 +608,9 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * oscar_kv16_decode_attention of sequences that share prefixes: the sequences
  * group[i] .. group[i+1] - 1 are group i, whose first prefix[i] tokens are the
  * same ones.  The prefix's whole pages (tokens below 32 * (prefix[i] / 32)) are
- * read once for the group, from its first sequence's place in the cache: the
- * others' table entries (contiguous: rows) for them are not used.  The rest of
+ * read once for the group, from its first sequence's place in the cache, which
+ * holds them whatever that sequence's length; the others' table entries
+ * (contiguous: rows) for them are not used.  The rest of
  * the prefix stands in every sequence's own pages, as oscar_kv16_fork leaves
  * it.  A sequence in no group shares nothing, and one with fewer tokens than
  * the prefix sees those that it has.
@@ -706,6 +707,12 @@ size_t oscar_page_compact_workspace_bytes(int B, int max_blocks, int n_pages);
 oscar_status oscar_kv16_copy_pages(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,
                                    const int32_t* pairs, const int32_t* n_pairs, int max_pairs,
                                    void* stream);
+
+/* The same within the pool of a packed cache: the records of page pairs[i][0] to
+ * page pairs[i][1].  (A packed page is never written again, so sequences may share
+ * it; what a sequence has beside its pages, the residual window, is its own.) */
+oscar_status oscar_paged_copy_pages(const oscar_paged_cache* c, const int32_t* pairs,
+                                    const int32_t* n_pairs, int max_pairs, void* stream);
 
 /* Self-test of the bounded waits (failure detection; the pages have no
  * counterpart).  One CTA waits on an mbarrier that nothing arrives at,

@@ -573,6 +573,26 @@ oscar_status oscar_paged_decode_attention(const oscar_paged_cache* c, const floa
   return from_cuda(e);
 }
 
+oscar_status oscar_paged_copy_pages(const oscar_paged_cache* c, const int32_t* pairs,
+                                    const int32_t* n_pairs, int max_pairs, void* stream) {
+  oscar_status st = check_paged(c);
+  if (st != OSCAR_OK) return st;
+  if (max_pairs < 0 || !n_pairs || (max_pairs > 0 && !pairs)) return OSCAR_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(pairs) & 7u) || !al4(n_pairs)) return OSCAR_ERR_ALIGNMENT;
+  const long long page_bytes = (long long)c->Hkv * rec_bytes(code_bits(c->bits));
+  // a warp's number, 4 KB of a pair each, fits in 31 bits
+  if (page_bytes > 0x7fffffffLL || max_pairs > 0x7fffffffLL / (page_bytes / 4096 + 1))
+    return OSCAR_ERR_UNSUPPORTED;
+  if (max_pairs == 0) return OSCAR_OK;
+  unsigned* status = status_ptr();
+  if (!status) return OSCAR_ERR_CUDA;
+  const cudaError_t e =
+      launch_paged_copy_pages(c->pages, c->n_pages, (int)page_bytes, pairs, n_pairs, max_pairs,
+                              status, as_stream(stream));
+  g_launches += 1;
+  return from_cuda(e);
+}
+
 oscar_status oscar_bf16_decode_attention(const oscar_bf16* q, const oscar_bf16* K,
                                          const oscar_bf16* V, int B, int Hq, int Hkv, int T,
                                          int T_stride, float softmax_scale, float* out,

@@ -87,7 +87,9 @@ enum Part { kWhole, kLine };
 // Floats of a record and before its o.
 constexpr int rec_floats(int part) { return part == kWhole ? kRecFloats : kPartFloats; }
 constexpr int rec_head(int part) { return part == kWhole ? 4 : kPartHead; }
-// (The line's entries take a stage's room, and four keep up with HBM.)
+// (The line's entries take a stage's room.  A ring of five for chunks that fill both
+// query tiles and of three a query tile for the others, the table elsewhere, was
+// slower, 5 to 15 %: more to count between two products.)
 constexpr int stages_of(int part) { return part == kLine ? 4 : 5; }
 constexpr int kTileBytes = 32768;      // 128 rows of 128 elements, two halves of 64 columns
 constexpr int kHalf = 16384;
@@ -674,7 +676,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           stop = x0 >= x1;
           if (!stop) {
             x0 += find_piece(p, first, share, x0, x1, it);
-            if (it.cnt[0] <= 0 && it.cnt[1] <= 0) continue;      // (places without tiles)
+            if (it.cnt[0] <= 0 && it.cnt[1] <= 0) {              // (places without tiles)
+              ok = !(*state & 1);
+              continue;
+            }
             const int nk = it.k1 - it.k0;
             it.first = it.nrow > p.tokens ? kPair : (int)(passed & 1);
             if (it.first != kPair) {

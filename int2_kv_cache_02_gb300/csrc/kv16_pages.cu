@@ -170,6 +170,37 @@ kv16_copy_pages_kernel(const Kv16 src, const Kv16 dst, const int2* __restrict__ 
   if (dst.weight) dst.weight[d0 + lane] = src.weight[s0 + lane];
 }
 
+// Packed pages, as 16-byte pieces: a warp takes 256 of a pair's.
+constexpr int kPieces = 256;
+__global__ void __launch_bounds__(kCopyThreads)
+paged_copy_pages_kernel(uint4* pages, int n_pages, int pieces, const int2* __restrict__ pairs,
+                        const int32_t* __restrict__ n_pairs, int max_pairs, unsigned* status) {
+  const int n = __ldg(n_pairs), lane = threadIdx.x & 31;
+  const long long gid = (long long)blockIdx.x * kCopyThreads + threadIdx.x;
+  if (n < 0 || n > max_pairs) {
+    if (gid == 0) record_error(status, kDevErrBadPaged);
+    return;
+  }
+  const int parts = (pieces + kPieces - 1) / kPieces;
+  const long long u = gid >> 5;
+  if (u >= (long long)n * parts) return;
+  const int2 pair = __ldg(pairs + u / parts);
+  if ((unsigned)pair.x >= (unsigned)n_pages || (unsigned)pair.y >= (unsigned)n_pages) {
+    if (lane == 0) record_error(status, kDevErrBadPaged);
+    return;
+  }
+  const int i0 = (int)(u % parts) * kPieces + lane;
+  const uint4* s = pages + (long long)pair.x * pieces;
+  uint4* d = pages + (long long)pair.y * pieces;
+  uint4 x[kPieces / 32];
+#pragma unroll
+  for (int i = 0; i < kPieces / 32; ++i)
+    if (i0 + 32 * i < pieces) x[i] = __ldcs(s + i0 + 32 * i);
+#pragma unroll
+  for (int i = 0; i < kPieces / 32; ++i)
+    if (i0 + 32 * i < pieces) d[i0 + 32 * i] = x[i];
+}
+
 // Words of the bits of one CTA.
 int compact_words(int n_pages) { return (n_pages + 32 * kCluster - 1) / (32 * kCluster); }
 
@@ -197,6 +228,17 @@ cudaError_t launch_kv16_copy_pages(const Kv16& src, const Kv16& dst, const int32
   const long long ctas = ((long long)max_pairs * src.Hkv * 32 + kCopyThreads - 1) / kCopyThreads;
   kv16_copy_pages_kernel<<<(int)ctas, kCopyThreads, 0, s>>>(
       src, dst, reinterpret_cast<const int2*>(pairs), n_pairs, max_pairs);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_copy_pages(uint8_t* pages, int n_pages, int page_bytes,
+                                    const int32_t* pairs, const int32_t* n_pairs, int max_pairs,
+                                    unsigned* status, cudaStream_t s) {
+  const int pieces = page_bytes / 16, parts = (pieces + kPieces - 1) / kPieces;
+  const long long ctas = ((long long)max_pairs * parts * 32 + kCopyThreads - 1) / kCopyThreads;
+  paged_copy_pages_kernel<<<(int)ctas, kCopyThreads, 0, s>>>(
+      reinterpret_cast<uint4*>(pages), n_pages, pieces, reinterpret_cast<const int2*>(pairs),
+      n_pairs, max_pairs, status);
   return cudaGetLastError();
 }
 

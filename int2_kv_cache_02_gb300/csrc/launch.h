@@ -255,6 +255,9 @@ constexpr int kMaxPages = 12582912;     // of a pool that is compacted
 size_t page_compact_ws_bytes(int n_pages);
 cudaError_t launch_kv16_copy_pages(const Kv16& src, const Kv16& dst, const int32_t* pairs,
                                    const int32_t* n_pairs, int max_pairs, cudaStream_t s);
+cudaError_t launch_paged_copy_pages(uint8_t* pages, int n_pages, int page_bytes,
+                                    const int32_t* pairs, const int32_t* n_pairs, int max_pairs,
+                                    unsigned* status, cudaStream_t s);
 
 // One CTA polls an mbarrier nothing arrives at, `iterations` times, then
 // records kDevErrWaitTimeout in *status (self-test of the bounded waits).

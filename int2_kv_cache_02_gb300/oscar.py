@@ -139,6 +139,7 @@ def _load() -> ctypes.CDLL:
                                        c_void_p, c_size_t, c_void_p]),
         "oscar_page_compact_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
         "oscar_kv16_copy_pages": (c_int, [P16, P16, c_void_p, c_void_p, c_int, c_void_p]),
+        "oscar_paged_copy_pages": (c_int, [PP, c_void_p, c_void_p, c_int, c_void_p]),
         "oscar_device_status": (c_int, [c_void_p]),
         "oscar_selftest_wait_timeout": (c_int, [c_uint, c_void_p]),
         "oscar_selftest_tc_wait_timeout": (c_int, [c_uint, c_void_p, c_void_p]),
@@ -306,7 +307,8 @@ class _PagePool:
     def compact(self):
         """Gives the pages in use the lowest ids (page_compact): the table and the
         allocator go by the new ids from here on.  Returns (moves, counts) for
-        the copies (kv16_copy_pages), which come next on the current stream."""
+        the copies (kv16_copy_pages, paged_copy_pages), which come next on the
+        current stream."""
         table, n_pages = self.block_table, len(self._named)
         moves = torch.empty((n_pages // 2, 2), dtype=torch.int32, device=table.device)
         counts = torch.empty(2, dtype=torch.int32, device=table.device)
@@ -823,6 +825,17 @@ def page_compact(block_table: torch.Tensor, new_table: torch.Tensor, n_pages: in
     else:
         with torch.cuda.device(index):
             _check(_lib.oscar_page_compact(*args), "oscar_page_compact")
+
+
+def paged_copy_pages(cache: PagedKVCache, pairs: torch.Tensor, n_pairs: torch.Tensor, stream=None):
+    """Pages pairs[i][0] of a packed cache's pool to pages pairs[i][1], int32
+    [..][2], for i below the first element of n_pairs (int32)."""
+    if pairs.dim() != 2 or pairs.shape[1] != 2 or n_pairs.numel() < 1 or \
+            any(t.dtype is not torch.int32 or t.device != cache.pages.device for t in (pairs, n_pairs)):
+        raise ValueError(f"expected int32 pairs [..][2] and their number on {cache.pages.device}")
+    with torch.cuda.device(cache.pages.device):
+        _check(_lib.oscar_paged_copy_pages(cache.ref(), _ptr(pairs), _ptr(n_pairs), pairs.shape[0],
+                                           _stream(stream)), "oscar_paged_copy_pages")
 
 
 def kv16_copy_pages(src: KV16Cache, dst: KV16Cache, pairs: torch.Tensor, n_pairs: torch.Tensor,

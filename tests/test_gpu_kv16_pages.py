@@ -151,6 +151,20 @@ def test_fork_bad_parents_lengths_and_pages(L):
                 assert torch.equal(bits(R.tokens(dst, b, 40)), bits(case.k[parent[b]]))
 
 
+def test_fork_does_not_take_over_unmapped_pages(L):
+    """A whole page that the parent's table does not name is recorded, and the entry stays."""
+    case = R.Case([70, 40], 2)
+    cache = case.cache(L)
+    cache.block_table[0, 1] = -1
+    before = cache.block_table.clone()
+    dst = L.KV16Cache(cache.k, cache.v, i32([0, 0]), block_table=before.flip(0).contiguous())
+    other = dst.block_table.clone()
+    L.kv16_fork(cache, dst, i32([0, -1]), 128)
+    assert L.device_status() != 0 and L.device_status() == 0
+    other[0, 0] = before[0, 0]
+    assert torch.equal(dst.block_table, other) and dst.n_tok.tolist() == [70, 0]
+
+
 # -------------------------------------------------------------- compaction
 
 def random_table(rng, B, blocks, n_pages, mapped, shared=0.2):
@@ -167,7 +181,7 @@ def random_table(rng, B, blocks, n_pages, mapped, shared=0.2):
 
 
 def run_compact(L, table, n_pages, in_place=False):
-    t = i32(table)
+    t = table.cuda() if torch.is_tensor(table) else i32(table)
     new = t if in_place else torch.full_like(t, 7)
     moves = torch.full((n_pages // 2, 2), 7, dtype=torch.int32, device="cuda")
     counts = i32([7, 7])
@@ -197,13 +211,12 @@ def test_compact(L, B, blocks, n_pages, mapped, in_place):
 
 def test_compact_large_pool(L):
     """More pages than one block of threads holds at a time, sparse and dense."""
-    n_pages = 3_000_001
     gen = torch.Generator().manual_seed(5)
-    for live in (1000, 2_500_000):
+    for n_pages, live in ((3_000_001, 1000), (3_000_001, 2_500_000), (12_582_912, 70_000)):
         ids = torch.randperm(n_pages, generator=gen)[:live].int()
         table = torch.full((2, (live + 1) // 2 + 3), -1, dtype=torch.int32)
         table.view(-1)[:live] = ids
-        old, new, moves, counts = run_compact(L, table.tolist(), n_pages)
+        old, new, moves, counts = run_compact(L, table, n_pages)
         assert L.device_status() == 0
         n = int(counts[0])
         named = torch.zeros(n_pages, dtype=torch.bool)
@@ -252,6 +265,37 @@ def test_copy_pages(L, Hkv, dtype, weights):
         L.kv16_copy_pages(a, a, i32(pairs), i32([n]))
         assert L.device_status() != 0
         assert torch.equal(bits(a.k), bits(want))
+
+
+@pytest.mark.parametrize("bits_", [2, 4])
+@pytest.mark.parametrize("Hkv", [1, 3, 8])
+def test_packed_pages_are_compacted(L, Hkv, bits_):
+    """A packed cache's pool after a sequence has ended: the others' records are where
+    the table says, bit for bit, and nothing else has moved."""
+    cache = L.PagedKVCache(4, Hkv, 6, 40, bits=bits_)
+    cache.pages.copy_(torch.randint(0, 256, cache.pages.shape, dtype=torch.uint8))
+    for b, n in enumerate((5, 2, 6, 3)):
+        cache.map_blocks(b, n, order=random.Random(b).sample(range(40), 40))
+    cache.share_blocks(3, 0, 2)
+    cache.release_blocks(1)
+    cache.release_blocks(2, 4)
+    blocks = {0: 5, 2: 4, 3: 3}
+    want = {(b, j): cache.pages[cache.page_of(b, j)].clone() for b, n in blocks.items() for j in range(n)}
+    before = cache.pages.clone()
+    moves, counts = cache.compact()
+    L.paged_copy_pages(cache, moves, counts)
+    assert L.device_status() == 0
+    live = len({x for row in cache._table_host for x in row if x >= 0})
+    assert counts[1] == live and cache.block_table.tolist() == cache._table_host
+    for (b, j), page in want.items():
+        assert cache.page_of(b, j) < live
+        assert torch.equal(cache.pages[cache.page_of(b, j)], page)
+    assert torch.equal(cache.pages[live:], before[live:])
+    L.paged_copy_pages(cache, i32([[1, 100], [2, 39]]), i32([2]))
+    assert L.device_status() != 0 and L.device_status() == 0
+    assert torch.equal(cache.pages[39], cache.pages[2])
+    with pytest.raises(ValueError):
+        L.paged_copy_pages(cache, moves.long(), counts)
 
 
 # ------------------------------------------------- all calls, as a server's

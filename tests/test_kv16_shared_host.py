@@ -113,7 +113,30 @@ def test_copy_refusals(L):
     assert copy(L, a, cache(at=far, block_table=None)) == copy(L, cache(block_table=None), b) == INVALID
     assert copy(L, a, cache(at=far, Hkv=1)) == copy(L, a, cache(at=far, dtype=1)) == INVALID
     assert copy(L, cache(weight=None), b) == copy(L, a, cache(at=far, k=FAKE)) == INVALID
+    assert copy(L, a, b, most=2**31 - 1) == UNSUPPORTED
     assert copy(L, a, b, most=0, pairs=None) == OK
+
+
+def packed(**kw):
+    from int2_kv_cache_02_gb300.oscar import OscarPagedCacheStruct
+    s = OscarPagedCacheStruct()
+    s.B, s.Hkv, s.max_blocks, s.n_pages = 2, 2, 8, 16
+    for i, name in enumerate(("pages", "block_table", "n_packed", "n_res", "k_res", "v_res", "k_res_norm")):
+        setattr(s, name, FAKE + i * 0x1000000)
+    for name, x in kw.items():
+        setattr(s, name, x)
+    return s
+
+
+@no_gpu_only
+def test_packed_copy_refusals(L):
+    f = lambda c=packed(), pairs=P(FAKE), n=P(FAKE), most=4: L.oscar_paged_copy_pages(
+        ctypes.byref(c) if c is not None else None, pairs, n, most, None)
+    assert f(c=None) == f(pairs=None) == f(n=None) == f(most=-1) == f(c=packed(pages=None)) == INVALID
+    assert f(c=packed(Hkv=0)) == f(c=packed(n_pages=0)) == f(c=packed(bits=3)) == INVALID
+    assert f(pairs=P(FAKE + 4)) == f(n=P(FAKE + 2)) == f(c=packed(pages=FAKE + 8)) == ALIGNMENT
+    assert f(c=packed(Hkv=1 << 20)) == f(c=packed(Hkv=1 << 12), most=2**20) == UNSUPPORTED
+    assert f(most=0, pairs=None) == OK
 
 
 @no_gpu_only
@@ -122,7 +145,8 @@ def test_compact_refusals(L):
     assert compact(L, B=0) == compact(L, blocks=0) == compact(L, pages=0) == INVALID
     assert compact(L, table=P(FAKE + 2)) == compact(L, new=P(FAKE + 1)) == compact(L, moves=P(FAKE + 4)) == \
         compact(L, counts=P(FAKE + 2)) == compact(L, ws=P(FAKE + 8)) == ALIGNMENT
-    assert compact(L, B=2**16, blocks=2**15) == UNSUPPORTED
+    assert compact(L, B=2**16, blocks=2**15) == compact(L, pages=12582913) == UNSUPPORTED
+    assert L.oscar_page_compact_workspace_bytes(2, 8, 12582913) == 0
     # outputs in the table or in one another (but for the table in place)
     assert compact(L, new=P(FAKE + 4)) == compact(L, moves=P(FAKE + 8)) == compact(L, counts=P(FAKE + 60)) == INVALID
     assert compact(L, moves=P(FAKE + 0x1008)) == compact(L, counts=P(FAKE + 0x1000)) == compact(L, counts=P(FAKE + 0x2008)) == INVALID
