@@ -22,7 +22,8 @@ LIBS = {
     "liboscar.so": ["rotate.cu", "quantize.cu", "decode_int2.cu", "decode_int2_pad.cu", "decode_bf16.cu",
                     "combine.cu", "api.cu", "decode_static.cu", "kv16_api.cu", "kv16_write.cu",
                     "kv16_attention.cu", "kv16_decode.cu", "kv16_accumulate.cu", "kv16_evict.cu",
-                    "kv16_shared.cu", "kv16_fork.cu", "kv16_pages.cu"],
+                    "kv16_shared.cu", "kv16_shared_short.cu",
+                    "kv16_fork.cu", "kv16_pages.cu"],
     "liboscar_synth.so": ["synth.cu"],
 }
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -50,7 +50,7 @@
 // records.
 #include <algorithm>
 
-#include "kv16.cuh"
+#include "kv16_page.cuh"
 #include "kv16_tma.h"
 #include "tc5.cuh"
 
@@ -72,9 +72,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 namespace {
 
 constexpr int NW = 10;                   // warps of a CTA, each with a slot of its own
-constexpr int kSlotBytes = 4 * 4096;     // a page: K and V, two halves of 64 channels each
 constexpr int kMinPages = NW;            // pages of a CTA's run, if the batch has as many: one a warp
-constexpr float kBelow = 14.0f;          // fp16: the maximum in use is 2^14 below the largest
 constexpr int kORow = 136;               // floats of a head's output row in shared memory
 
 struct DecodeParams {
@@ -149,30 +147,6 @@ __device__ __forceinline__ void find_row(Row& r, int x, const DecodeParams& p, c
   r.r1 = r.r0 + pages;
   r.at = __ldg(p.c.n_tok + lo) - 1;
   r.sp = Span(r.at, r.at, p.q.window, p.q.n_sink);
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-template <class T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-  if constexpr (T::kHalf)
-    mma_16816_acc(d, a, b0, b1);
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The row's joined result (M, L, o of channel pair `pair`) to the output.
@@ -330,18 +304,8 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
   while (seg < x1) {
     find_row(r, seg, p, first);
     const int seg_end = min(r.r1, x1);
-    // the group's queries as A operands: rows are heads, padding rows zero
     uint32_t qa[8][4];
-    {
-      const uint16_t* q0 = p.q.q + r.b * p.q.stride + (long long)r.h * p.g * kD;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int head = hr + 8 * (i & 1), ch = 16 * k + hc + 8 * (i >> 1);
-          qa[k][i] = head < p.g ? __ldg(reinterpret_cast<const uint32_t*>(q0 + head * kD + ch)) : 0u;
-        }
-    }
+    page_queries(qa, p.q.q + r.b * p.q.stride + (long long)r.h * p.g * kD, p.g);
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -354,113 +318,19 @@ kv16_decode_kernel(const __grid_constant__ CUtensorMap map_k,
         break;
       }
       const int j0 = r.sp.block(x - r.r0) * kPage;
-      const bool whole = j0 + kPage - 1 <= r.at &&
-                         (p.q.window == 0 || j0 > r.at - p.q.window || j0 + kPage <= p.q.n_sink);
-      if (!whole) {
-        // a hidden token's value must not meet its zero probability: clear it
-        const int j = j0 + lane;
-        if (!kv16_visible(j, r.at, p.q.window, p.q.n_sink)) {
+      const bool whole = page_step<T>(
+          slot, j0, r.at, p.q.window, p.q.n_sink, p.q.scale_log2, qa, o, m, l,
+          [&](const float (&sc)[4][4]) {
+            if constexpr (ACC) {
+              float* d = p.scores + ((size_t)x * p.g + hr) * kPage + hc;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            reinterpret_cast<uint4*>(slot + 8192 + (i >> 3) * 4096 + lane * 128)[i & 7] =
-                make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
-      // S: 16 heads x 32 tokens
-      float sc[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
-      const unsigned sa = smem_u32(slot);
-      const int mrow = lane & 7, mid = lane >> 3;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // 8x8 tiles: channels 16k, 16k + 8 of tokens t, t + 8
-        const int chunk = 2 * (k & 3) + (mid & 1);
-        const unsigned a = sa + (k >> 2) * 4096 + ((mid >> 1) * 8 + mrow) * 128 + ((chunk ^ mrow) << 4);
-        uint32_t b0[4], b1[4];
-        ldsm4(b0, a);
-        ldsm4(b1, a + 16 * 128);
-        mma<T>(sc[0], qa[k], b0[0], b0[1]);
-        mma<T>(sc[1], qa[k], b0[2], b0[3]);
-        mma<T>(sc[2], qa[k], b1[0], b1[1]);
-        mma<T>(sc[3], qa[k], b1[2], b1[3]);
-      }
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = sc[i][e] * p.q.scale_log2;
-          if (!whole && !kv16_visible(j0 + 8 * i + hc + (e & 1), r.at, p.q.window, p.q.n_sink))
-            v = -INFINITY;
-          sc[i][e] = v;
-          mx[e >> 1] = fmaxf(mx[e >> 1], v);
-        }
-      if constexpr (ACC) {
-        float* d = p.scores + ((size_t)x * p.g + hr) * kPage + hc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (hr < p.g) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(sc[i][0], sc[i][1]);
-          if (hr + 8 < p.g)
-            *reinterpret_cast<float2*>(d + 8 * kPage + 8 * i) = make_float2(sc[i][2], sc[i][3]);
-        }
-      }
-      bool grew = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        if (T::kHalf) mx[i] -= kBelow;
-        grew |= mx[i] > m[i];
-      }
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mn = fmaxf(m[i], mx[i]);
-          const float a = mn == -INFINITY ? 1.0f : fast_exp2(m[i] - mn);
-          m[i] = mn;
-          l[i] *= a;
-#pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            o[n][2 * i] *= a;
-            o[n][2 * i + 1] *= a;
-          }
-        }
-      }
-      const float ms[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-      uint32_t pa[2][4], pb[2][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p0 = fast_exp2(sc[i][0] - ms[0]), p1 = fast_exp2(sc[i][1] - ms[0]);
-        const float p2 = fast_exp2(sc[i][2] - ms[1]), p3 = fast_exp2(sc[i][3] - ms[1]);
-        l[0] += p0 + p1;
-        l[1] += p2 + p3;
-        const uint32_t h0 = T::pack(p0, p1), h1 = T::pack(p2, p3);
-        const float2 u0 = T::unpack(h0), u1 = T::unpack(h1);
-        pa[i >> 1][2 * (i & 1)] = h0;
-        pa[i >> 1][2 * (i & 1) + 1] = h1;
-        pb[i >> 1][2 * (i & 1)] = T::pack(p0 - u0.x, p1 - u0.y);
-        pb[i >> 1][2 * (i & 1) + 1] = T::pack(p2 - u1.x, p3 - u1.y);
-      }
-      // O += P V: 8x8 tiles, transposed on the way: tokens t, t + 8 of channels c, c + 8
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int chunk = 2 * (n & 3) + (mid >> 1);
-        const unsigned a = sa + 8192 + (n >> 2) * 4096 + ((mid & 1) * 8 + mrow) * 128 +
-                           ((chunk ^ mrow) << 4);
-        uint32_t b0[4], b1[4];
-        ldsm4t(b0, a);
-        ldsm4t(b1, a + 16 * 128);
-        mma<T>(o[2 * n], pa[0], b0[0], b0[1]);
-        mma<T>(o[2 * n + 1], pa[0], b0[2], b0[3]);
-        mma<T>(o[2 * n], pa[1], b1[0], b1[1]);
-        mma<T>(o[2 * n + 1], pa[1], b1[2], b1[3]);
-        mma<T>(o[2 * n], pb[0], b0[0], b0[1]);
-        mma<T>(o[2 * n + 1], pb[0], b0[2], b0[3]);
-        mma<T>(o[2 * n], pb[1], b1[0], b1[1]);
-        mma<T>(o[2 * n + 1], pb[1], b1[2], b1[3]);
-      }
+              for (int i = 0; i < 4; ++i) {
+                if (hr < p.g) *reinterpret_cast<float2*>(d + 8 * i) = make_float2(sc[i][0], sc[i][1]);
+                if (hr + 8 < p.g)
+                  *reinterpret_cast<float2*>(d + 8 * kPage + 8 * i) = make_float2(sc[i][2], sc[i][3]);
+              }
+            }
+          });
       // refill the slot once every lane has read it; cleared values first
       // become visible to the copy engine
       if (!whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -68,4 +68,57 @@ __device__ __forceinline__ int warp_sequence(const int32_t* start, int B, int r)
   return __ldg(start + lo) <= r && r < __ldg(start + lo + 1) ? lo : -1;
 }
 
+// What the values that a row sees hold in a channel.
+constexpr unsigned kSeenNan = 1, kSeenPlus = 2, kSeenMinus = 4;
+__device__ __forceinline__ unsigned seen_in(float x) {
+  return x != x ? kSeenNan : x == INFINITY ? kSeenPlus : x == -INFINITY ? kSeenMinus : 0u;
+}
+
+// The channels of a row (4 lane .. 4 lane + 3, relative to its sum) that are NaN
+// although the sum is a number: infinite where the visible values hold infinities
+// of one sign and no NaN.  A record may hold an infinity that its factor of 0 has
+// turned into NaN.  A warp; rare, and as slow as one warp's pass over the values.
+template <class T>
+__device__ __noinline__ float4 settle(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups,
+                                      int b, int h, int back, float4 x) {
+  const int lane = threadIdx.x & 31;
+  const int len = kv16_length(c, b, q.max_tok), at = len < 0 ? -1 : max(len - back, -1);
+  const int i = group_of(groups, b);
+  Shared sh{b, b, 0};
+  if (i >= 0) sh = shared_of(c, groups, i, q.max_tok, false);
+  const Span sp(at, at, q.window, q.n_sink);
+  float o[4] = {x.x, x.y, x.z, x.w};
+  unsigned f[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int k = 0; k < sp.blocks; ++k) {
+    bool undecided = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      undecided |= o[u] != o[u] && !(f[u] & kSeenNan) &&
+                   (f[u] & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
+    if (!__any_sync(0xffffffffu, undecided)) break;
+    const int blk = sp.block(k);
+    const int row = kv16_block_row(c, blk < sh.blocks ? sh.lead : b, h, blk);
+    if (row < 0) continue;
+    const unsigned see =
+        __ballot_sync(0xffffffffu, kv16_visible(blk * kPage + lane, at, q.window, q.n_sink));
+#pragma unroll 8
+    for (int t = 0; t < kPage; ++t) {
+      uint2 v = make_uint2(0u, 0u);
+      if ((see >> t) & 1u)
+        v = reinterpret_cast<const uint2*>(c.v)[((long long)row + t) * 32 + lane];
+      const float2 a = T::unpack(v.x), z = T::unpack(v.y);
+      f[0] |= seen_in(a.x);
+      f[1] |= seen_in(a.y);
+      f[2] |= seen_in(z.x);
+      f[3] |= seen_in(z.y);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (o[u] != o[u] && (f[u] == kSeenPlus || f[u] == kSeenMinus))
+      o[u] = f[u] == kSeenPlus ? INFINITY : -INFINITY;
+  return make_float4(o[0], o[1], o[2], o[3]);
+}
+
 }  // namespace oscar

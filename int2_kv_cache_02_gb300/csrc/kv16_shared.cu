@@ -9,59 +9,7 @@
 namespace oscar {
 namespace {
 
-// What the values that a row sees hold in a channel.
-constexpr unsigned kSeenNan = 1, kSeenPlus = 2, kSeenMinus = 4;
-__device__ __forceinline__ unsigned seen_in(float x) {
-  return x != x ? kSeenNan : x == INFINITY ? kSeenPlus : x == -INFINITY ? kSeenMinus : 0u;
-}
-
 constexpr int kMaxCtas = 160;      // of the prefixes' kernel
-
-// The channels of a row (4 lane .. 4 lane + 3, relative to its sum) that are NaN
-// although the sum is a number: infinite where the visible values hold infinities
-// of one sign and no NaN.  A record may hold an infinity that its factor of 0 has
-// turned into NaN.  A warp; rare, and as slow as one warp's pass over the values.
-template <class T>
-__device__ __noinline__ float4 settle(const AttnParams& p, int b, int h, int back, float4 x) {
-  const int lane = threadIdx.x & 31;
-  const int len = kv16_length(p.c, b, p.q.max_tok), at = len < 0 ? -1 : max(len - back, -1);
-  const int i = group_of(p.line.groups, b);
-  Shared sh{b, b, 0};
-  if (i >= 0) sh = shared_of(p.c, p.line.groups, i, p.q.max_tok, false);
-  const Span sp(at, at, p.q.window, p.q.n_sink);
-  float o[4] = {x.x, x.y, x.z, x.w};
-  unsigned f[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-  for (int k = 0; k < sp.blocks; ++k) {
-    bool undecided = false;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      undecided |= o[u] != o[u] && !(f[u] & kSeenNan) &&
-                   (f[u] & (kSeenPlus | kSeenMinus)) != (kSeenPlus | kSeenMinus);
-    if (!__any_sync(0xffffffffu, undecided)) break;
-    const int blk = sp.block(k);
-    const int row = kv16_block_row(p.c, blk < sh.blocks ? sh.lead : b, h, blk);
-    if (row < 0) continue;
-    const unsigned see =
-        __ballot_sync(0xffffffffu, kv16_visible(blk * kPage + lane, at, p.q.window, p.q.n_sink));
-#pragma unroll 8
-    for (int t = 0; t < kPage; ++t) {
-      uint2 v = make_uint2(0u, 0u);
-      if ((see >> t) & 1u)
-        v = reinterpret_cast<const uint2*>(p.c.v)[((long long)row + t) * 32 + lane];
-      const float2 a = T::unpack(v.x), z = T::unpack(v.y);
-      f[0] |= seen_in(a.x);
-      f[1] |= seen_in(a.y);
-      f[2] |= seen_in(z.x);
-      f[3] |= seen_in(z.y);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (o[u] != o[u] && (f[u] == kSeenPlus || f[u] == kSeenMinus))
-      o[u] = f[u] == kSeenPlus ? INFINITY : -INFINITY;
-  return make_float4(o[0], o[1], o[2], o[3]);
-}
 
 // (bounded: what is not written for a row out of range may hold anything)
 __device__ __forceinline__ Runs runs_from(int x, int ctas) {
@@ -288,7 +236,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
             x[k] = lane & 1 ? hi : lo;
           }
           const float i = __shfl_sync(0xffffffffu, inv, z * 16);
-          const float4 y = settle<T>(p, b, h, seq1 - r, make_float4(x[0], x[1], x[2], x[3]));
+          const float4 y = settle<T>(p.c, p.q, s.groups, b, h, seq1 - r, make_float4(x[0], x[1], x[2], x[3]));
           __syncwarp();
           reinterpret_cast<uint2*>(p.out + ((long long)r * p.q.Hq + h * g + pair0 + z) * kD)[lane] =
               make_uint2(T::pack(y.x * i, y.y * i), T::pack(y.z * i, y.w * i));
@@ -361,7 +309,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       }
       if (head0 >= g) return;
       const bool open = o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w;
-      if (L == L && __any_sync(0xffffffffu, open)) o = settle<T>(p, b, h, seq1 - r, o);
+      if (L == L && __any_sync(0xffffffffu, open)) o = settle<T>(p.c, p.q, s.groups, b, h, seq1 - r, o);
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       const long long row = (long long)r * p.q.Hq + h * g + head0;
       reinterpret_cast<uint2*>(p.out + row * kD)[lane] =
@@ -451,6 +399,16 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
               : cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, false>, p, subs, 1);
 }
 
+// Is a CTA for each (sequence, KV head) the quicker way?  A wave of them takes 3.6 us
+// and 7.7 for each 1000 tokens of the longest, the line about 15 and 2 for each 100
+// rows.  Measured, that way and by the line (rows, tokens; us): 16 of 533 8.7 and
+// 15.8, 128 of 1021 11.8 and 18.5, 128 of 2001 19.1 and 19.2, 256 of 301 11.6 and
+// 21.4, 512 of 511 24.9 and 25.7, 1024 of 131 27 and 37, 1024 of 511 43 and 42.
+bool short_rows(const Kv16& c, const Kv16Query& q) {
+  const long long rows = (long long)c.B * c.Hkv, sms = sm_count();
+  return !q.start && (rows + sms - 1) / sms * (q.max_tok + 470LL) * 10 <= 19500 + 26 * rows;
+}
+
 }  // namespace
 
 size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
@@ -477,6 +435,10 @@ cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Grou
   p.scale = std::max(std::fabs(q.scale_log2), std::numeric_limits<float>::denorm_min());
   p.wide = false;
   *launches = 0;
+  if (short_rows(c, q)) {
+    *launches = 1;
+    return launch_kv16_shared_short(c, q, g, out, s);
+  }
   return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);
 }
 

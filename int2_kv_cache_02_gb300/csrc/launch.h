@@ -246,6 +246,9 @@ constexpr int kMaxGroups = 4096;        // groups of one call
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
                                uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s);
 size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok);
+// A CTA for each (sequence, KV head): q.start is nullptr.
+cudaError_t launch_kv16_shared_short(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups,
+                                     uint16_t* out, cudaStream_t s);
 cudaError_t launch_kv16_fork(const Kv16& src, const Kv16& dst, const int32_t* parent, bool share,
                              bool same, int max_tok, cudaStream_t s);
 cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long long entries,

@@ -32,26 +32,29 @@ def strided(q):
     return wide[:, 1:1 + q.shape[1]]
 
 
-def decode(L, case, cache, Hq, window=0, sink=0, scale=R.SCALE, q=None, check=True, max_tok=None):
+def decode(L, case, cache, Hq, window=0, sink=0, scale=R.SCALE, q=None, check=True):
+    """By both ways, which the bound on the lengths chooses between."""
     q = case.normal(case.B, Hq) if q is None else q
     group, prefix = case.groups()
-    out = torch.full((case.B, Hq, 128), 7.0, dtype=case.dtype, device="cuda")
-    max_tok = cache.capacity if max_tok is None else max_tok
-    n = L.kv16_shared_decode_workspace_bytes(cache, Hq, len(case.prefix), max_tok, window, sink)
-    ws = L.alloc_workspace(n)
-    ws.fill_(math.nan)
-    L.kv16_shared_decode_attention(cache, strided(q), group, prefix, scale, max_tok, out, ws,
-                                   window=window, n_sink=sink)
-    if not check:
-        return out
-    assert L.device_status() == 0
-    for b in range(case.B):
-        if case.lens[b] == 0:
-            assert (out[b] == 0).all()
+    want = [R.attend(case, b, q[b:b + 1], window, sink, scale) if check and case.lens[b] else None for b in range(case.B)]
+    for max_tok in (cache.capacity, 1 << 20):
+        out = torch.full((case.B, Hq, 128), 7.0, dtype=case.dtype, device="cuda")
+        n = L.kv16_shared_decode_workspace_bytes(cache, Hq, len(case.prefix), max_tok, window, sink)
+        ws = L.alloc_workspace(n)
+        ws.fill_(math.nan)
+        L.kv16_shared_decode_attention(cache, strided(q), group, prefix, scale, max_tok, out, ws,
+                                       window=window, n_sink=sink)
+        if not check:
+            if max_tok == cache.capacity:
+                first = out
             continue
-        o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1], window, sink, scale)
-        R.assert_within(out[b:b + 1], o, tol, f"out of sequence {b}")
-    return out
+        assert L.device_status() == 0
+        for b in range(case.B):
+            if case.lens[b] == 0:
+                assert (out[b] == 0).all()
+                continue
+            R.assert_within(out[b:b + 1], want[b][0], want[b][3], f"out of sequence {b}, bound {max_tok}")
+    return out if check else (first, out)
 
 
 def attend(L, case, cache, news, Hq, window=0, sink=0, scale=R.SCALE, extra=2, check=True, lse=True, q=None):
@@ -163,7 +166,7 @@ def test_decode_many_sequences_and_groups(L):
     case = SharedCase([1] * 4096, [32] * 4096, lens, 1)
     cache = case.cache(L)
     q = case.normal(4096, 1)
-    out = decode(L, case, cache, 1, q=q, check=False)
+    out = decode(L, case, cache, 1, q=q, check=False)[1]
     assert L.device_status() == 0
     for b in range(0, 4096, 97):
         o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1])
@@ -196,18 +199,18 @@ def test_hidden_values_do_not_leak(L):
             x[2][:, 100:180] = math.nan
         cache = case.cache(L)
         q = case.normal(3, 4)
-        out = decode(L, case, cache, 4, window=90, sink=7, q=q, check=False)
+        outs = decode(L, case, cache, 4, window=90, sink=7, q=q, check=False)
         assert L.device_status() == 0
-        for b in range(3):
-            o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1], 90, 7)
-            if b != 0 and b != 2:
-                R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
+        o, _, _, tol, _, _ = R.attend(case, 1, q[1:2], 90, 7)
+        for out in outs:
+            R.assert_within(out[1:2], o, tol, "sequence 1")
         # the 90 tokens before position 299 and 279 start behind 180
         clean = SharedCase([3], [256], [300, 100, 280], 1, dtype=dtype)
         for b in (0, 2):
             clean.k[b], clean.v[b] = case.k[b].nan_to_num(0.0), case.v[b].nan_to_num(0.0)
             o, _, _, tol, _, _ = R.attend(clean, b, q[b:b + 1], 90, 7)
-            R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
+            for out in outs:
+                R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -224,7 +227,7 @@ def test_what_a_query_sees_reaches_it(L, where, dtype):
         case.v[b][:, 11, 77] = -math.inf
     cache = case.cache(L)
     q = case.normal(2, 4)
-    for out in (decode(L, case, cache, 4, q=q, check=False),
+    for out in (*decode(L, case, cache, 4, q=q, check=False),
                 attend(L, case, cache, [1, 1], 4, q=q, extra=0, check=False)[0]):
         assert L.device_status() == 0
         assert (out[:, :, 3] == math.inf).all() and (out[:, :, 9] == -math.inf).all()
@@ -234,7 +237,7 @@ def test_what_a_query_sees_reaches_it(L, where, dtype):
     for b in range(2):
         case.k[b][:, where] = math.nan
     cache = case.cache(L)
-    assert decode(L, case, cache, 4, q=q, check=False).isnan().all()
+    assert all(out.isnan().all() for out in decode(L, case, cache, 4, q=q, check=False))
     assert attend(L, case, cache, [1, 1], 4, q=q, extra=0, check=False)[0].isnan().all()
     assert L.device_status() == 0
 
@@ -254,7 +257,7 @@ def test_infinities_in_every_kind_of_row(L, members, new, prefix):
     q = case.normal(start[-1], 4)
     outs = [attend(L, case, cache, [new] * members, 4, q=q, extra=0, check=False)[0]]
     if new == 1:
-        outs.append(decode(L, case, cache, 4, q=q, check=False))
+        outs += decode(L, case, cache, 4, q=q, check=False)
     assert L.device_status() == 0
     for out in outs:
         assert (out[:, :, 3] == math.inf).all() and out[:, :, 40].isnan().all()
@@ -277,11 +280,11 @@ def test_workspace_at_any_16_bytes(L):
     cache = case.cache(L)
     q = case.normal(5, 8).cuda()
     group, prefix = case.groups()
-    n = L.kv16_shared_decode_workspace_bytes(cache, 8, 1, cache.capacity)
+    n = L.kv16_shared_decode_workspace_bytes(cache, 8, 1, 1 << 20)
     big = torch.full((n + 32,), 255, dtype=torch.uint8, device="cuda")
     outs = [torch.empty_like(q) for _ in range(2)]
     for at, out in zip((0, 16), outs):
-        L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, cache.capacity, out, big[at:at + n])
+        L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, 1 << 20, out, big[at:at + n])
     assert L.device_status() == 0
     assert torch.equal(bits(outs[0]), bits(outs[1]))
     assert (big[n + 16:] == 255).all()
@@ -306,26 +309,29 @@ def test_bad_groups_and_pages_are_recorded(L):
     cache = case.cache(L)
     whole = R.Case.cache(case, L)
     for group, prefix in (([0, 2, 5], [64, 64]), ([0, 2, 4], [64, -1]), ([0, 2, 4], [64, 100000])):
-        out = torch.empty((4, 2, 128), dtype=BF, device="cuda")
-        ws = L.alloc_workspace(L.kv16_shared_decode_workspace_bytes(whole, 2, 2, 96))
-        L.kv16_shared_decode_attention(whole, q.cuda(), i32(group), i32(prefix), R.SCALE, 96, out, ws)
-        assert L.device_status() != 0 and L.device_status() == 0
-        for b in range(4):
-            o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1])
-            R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
+        for most in (96, 1 << 20):
+            out = torch.empty((4, 2, 128), dtype=BF, device="cuda")
+            ws = L.alloc_workspace(L.kv16_shared_decode_workspace_bytes(whole, 2, 2, most))
+            L.kv16_shared_decode_attention(whole, q.cuda(), i32(group), i32(prefix), R.SCALE, most, out, ws)
+            assert L.device_status() != 0 and L.device_status() == 0
+            for b in range(4):
+                o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1])
+                R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
     cache.block_table[0, 0] = 1 << 20
-    out = decode(L, case, cache, 2, q=q, check=False)
+    outs = decode(L, case, cache, 2, q=q, check=False)
     assert L.device_status() != 0 and L.device_status() == 0
     for b in (2, 3):
         o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1])
-        R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
+        for out in outs:
+            R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
     cache = case.cache(L)
     cache.n_tok[1] = 100000
-    out = decode(L, case, cache, 2, q=q, check=False)
+    outs = decode(L, case, cache, 2, q=q, check=False)
     assert L.device_status() != 0 and L.device_status() == 0
     for b in (0, 2, 3):
         o, _, _, tol, _, _ = R.attend(case, b, q[b:b + 1])
-        R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
+        for out in outs:
+            R.assert_within(out[b:b + 1], o, tol, f"sequence {b}")
 
 
 # ------------------------------------------------------ several new tokens
@@ -372,17 +378,18 @@ def test_attention_many_rows(L):
 # ------------------------------------------- graphs, streams, workspaces
 
 def test_graphs_share_a_workspace(L):
-    """Two captured calls on one workspace, replayed in turn, with lengths, prefixes
+    """Three captured calls on one workspace, replayed in turn, with lengths, prefixes
     and groups that change between replays: the same bits as the calls themselves."""
     case = SharedCase([3, 3], [400, 320], [430, 420, 410, 330, 350, 390], 2)
     cache = case.cache(L)
     group, prefix = case.groups()
     q = case.normal(6, 8).cuda()
     start = i32([0, 1, 2, 3, 4, 5, 6])
-    outs = [torch.empty_like(q) for _ in range(2)]
-    ws = L.alloc_workspace(max(L.kv16_shared_decode_workspace_bytes(cache, 8, 2, cache.capacity),
+    outs = [torch.empty_like(q) for _ in range(3)]
+    ws = L.alloc_workspace(max(L.kv16_shared_decode_workspace_bytes(cache, 8, 2, 1 << 20),
                                L.kv16_shared_attention_workspace_bytes(cache, 8, 2, 6, cache.capacity)))
-    calls = [lambda: L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, cache.capacity, outs[0], ws),
+    calls = [lambda: L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, 1 << 20, outs[0], ws),
+             lambda: L.kv16_shared_decode_attention(cache, q, group, prefix, R.SCALE, cache.capacity, outs[2], ws),
              lambda: L.kv16_shared_attention(cache, q, start, group, prefix, R.SCALE, cache.capacity, outs[1], ws)]
     graphs = []
     for call in calls:
@@ -400,7 +407,7 @@ def test_graphs_share_a_workspace(L):
         prefix.copy_(i32(p))
         cache.n_tok.copy_(i32(n))
         got = []
-        for call, out, g in zip(calls, outs, graphs):
+        for call, out in zip(calls, (outs[0], outs[2], outs[1])):
             out.fill_(7)
             call()
             torch.cuda.synchronize()
@@ -410,7 +417,7 @@ def test_graphs_share_a_workspace(L):
             for g in graphs:
                 g.replay()
         torch.cuda.synchronize()
-        for out, want in zip(outs, got):
+        for out, want in zip((outs[0], outs[2], outs[1]), got):
             assert torch.equal(bits(out), bits(want))
     L.device_status()
 
