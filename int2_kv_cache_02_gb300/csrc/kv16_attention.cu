@@ -40,7 +40,7 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
     return cudaErrorNotSupported;
   const auto kernel = kv16_attention_kernel<T, kWhole>;
   constexpr int kStages = stages_of(kWhole);
-  constexpr int smem = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kStages>);
+  constexpr int smem = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kWhole>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

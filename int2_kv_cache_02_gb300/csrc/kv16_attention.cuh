@@ -67,7 +67,11 @@
 // kLine: sequences that share prefixes.  The same kernel over a line of work (see
 // kv16_line.h) in which a group's queries meet its shared blocks together and
 // each sequence's queries the blocks behind; an item is the piece of a CTA's run
-// that lies in one row of the line.  All items leave records.
+// that lies in one row of the line.  All items leave records.  Rows for one query
+// tile only (a decode step's, mostly) are worked by both, every other tile of keys
+// each and at their own pace: a tile's chain of product, softmax and product takes
+// 2.6 us with its loads, and two chains keep up with HBM (one: 165 us against 151 for
+// 128 requests under four prompts).  A wider Item in kWhole's way cost it 0.8 %.
 #pragma once
 
 #include <algorithm>
@@ -128,8 +132,6 @@ constexpr int kItems = 4;              // work items on their way to the other w
 struct Item {
   int stop;            // no more items
   int b, h, split, n;
-  int end;             // kLine: the sequence behind a group's last (b is its first), -1: b's own
-  int first;           // kLine: kPair, or the query tile that has the first tile of keys
   int row0, nrow;      // first row of q, tokens (of one or two tiles)
   int at0;             // position of the first token
   Span sp;
@@ -138,8 +140,26 @@ struct Item {
   bool clear;          // the last one's last page is the sequence's and lacks tokens
 };
 
-template <int STAGES>
+struct LineItem : Item {
+  int end;             // the sequence behind a group's last (b is its first), -1: b's own
+  int first;           // kPair, or the query tile that has the first tile of keys
+};
+template <int PART>
+struct ItemOf {
+  using type = Item;
+  static __device__ __forceinline__ int end(const Item*) { return -1; }
+  static __device__ __forceinline__ int first(const Item*) { return kPair; }
+};
+template <>
+struct ItemOf<kLine> {
+  using type = LineItem;
+  static __device__ __forceinline__ int end(const LineItem* it) { return it->end; }
+  static __device__ __forceinline__ int first(const LineItem* it) { return it->first; }
+};
+
+template <int PART>
 struct Smem {
+  static constexpr int STAGES = stages_of(PART);
   uint64_t q_full[2], q_empty[2], full[STAGES], empty[STAGES];
   uint64_t s_full[2], p_full[2][2], h_full[2], o_full[2], turn[2], tail, drain[2];
   uint64_t together;                     // kLine: both query tiles' MMA warps are at an item
@@ -147,7 +167,7 @@ struct Smem {
   uint32_t tmem;
   int state;           // of the waits
   int met[kSoftmaxWarps];
-  Item item[kItems];
+  typename ItemOf<PART>::type item[kItems];
 };
 constexpr int kItemReaders = kSoftmaxWarps + 3;   // warps that read an item: all but one
 
@@ -342,7 +362,7 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
 // (Maxima and minima: whatever the groups and lengths hold by now, what follows
 // stays in bounds.)
 __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first, int share, int x,
-                                          int x1, Item& it) {
+                                          int x1, LineItem& it) {
   const int G = p.line.groups.n, two = 2 * p.tokens, lane = threadIdx.x & 31;
   int lo = 0, hi = G + p.c.B;     // first[i] <= x < first[i + 1]
   while (hi - lo > 1) {
@@ -600,7 +620,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* sq = smem;                            // two query tiles
   uint8_t* ring = smem + 2 * kTileBytes;
-  auto& sm = *reinterpret_cast<Smem<kStages>*>(smem + (2 + kStages) * kTileBytes);
+  using It = typename ItemOf<PART>::type;
+  auto& sm = *reinterpret_cast<Smem<PART>*>(smem + (2 + kStages) * kTileBytes);
   int* first = reinterpret_cast<int*>(&sm + 1);  // kLine: [groups + B + 1], then a number a warp
   if (smem_u32(smem) & 1023) {                   // the swizzle counts on it
     if (tid == 0) record_error(p.c.status, kDevErrWaitTimeout);
@@ -655,7 +676,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   const uint32_t tmem = sm.tmem;
   volatile int* state = &sm.state;
   // an item is read by every warp but the scheduling one, and then given back
-  auto take = [&](unsigned n) -> const Item* {
+  auto take = [&](unsigned n) -> const It* {
     return tc5_wait(&sm.i_full[n % kItems], (n / kItems) & 1, state) ? &sm.item[n % kItems]
                                                                      : nullptr;
   };
@@ -671,7 +692,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const int items = p.tiles * p.c.Hkv * p.splits, grid = gridDim.x;
       for (int round = 0; ok; ++round) {
         bool stop;
-        Item it;
+        It it;
         if constexpr (PART == kLine) {
           stop = x0 >= x1;
           if (!stop) {
@@ -742,9 +763,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       };
       for (unsigned ni = 0; ok; ++ni) {
         if (!(ok = settled_wait(&sm.i_full[ni % kItems], (ni / kItems) & 1))) break;
-        const Item* ip = &sm.item[ni % kItems];
+        const It* ip = &sm.item[ni % kItems];
         if (ip->stop) break;
-        const Item it = *ip;
+        const It it = *ip;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
 #pragma unroll
@@ -757,7 +778,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               tma_box3(sq + w * kTileBytes + i * kHalf, &map_q, 64 * i, it.h * p.g,
-                       it.row0 + (PART == kWhole || it.first == kPair ? w * p.tokens : 0),
+                       it.row0 + (ItemOf<PART>::first(&it) == kPair ? w * p.tokens : 0),
                        &sm.q_full[w]);
           }
           __syncwarp();
@@ -857,10 +878,10 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           return n == 0 || tc5_wait(&sm.turn[0], (n - 1) & 1, state);
         };
         for (unsigned ni = 0; ok; ++ni) {
-          const Item* ip = take(ni);
+          const It* ip = take(ni);
           if (!(ok = ip != nullptr) || ip->stop) break;
           const int cnt = ip->cnt[w], nk = ip->k1 - ip->k0;
-          const int first_tile = PART == kLine ? ip->first : kPair;
+          const int first_tile = ItemOf<PART>::first(ip);
           mbar_arrive(&sm.i_empty[ni % kItems]);
           if (nk <= 0) continue;
           if (PART == kLine && first_tile != kPair) {
@@ -984,14 +1005,14 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
     unsigned s_used = 0, o_used = 0;
     bool ok = true;
     for (unsigned ni = 0; ok; ++ni) {
-      const Item* ip = take(ni);
+      const It* ip = take(ni);
       if (!(ok = ip != nullptr) || ip->stop) break;
-      const int first_tile = PART == kLine ? ip->first : kPair;
+      const int first_tile = ItemOf<PART>::first(ip);
       const bool pair = first_tile == kPair;
       const int shift = pair ? w * p.tokens : 0;
       const int ntok = min(p.tokens, ip->nrow - shift), my_n = ip->cnt[w];
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
-      const int seq_end = PART == kLine ? ip->end : 0;
+      const int seq_end = ItemOf<PART>::end(ip);
       const int at_first = ip->at0 + shift, row_first = ip->row0 + shift;
       const Span sp = ip->sp;
       __syncwarp();

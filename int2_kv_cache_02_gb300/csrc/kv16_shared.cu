@@ -3,13 +3,42 @@
 // head) rows meet each key and value that is read; what stands behind them a
 // sequence at a time.  Both by the tensor-core kernel of the prompt attention, over
 // one line of key tiles that its CTAs share evenly (kLine, kv16_line.h); the
-// records that it leaves are joined by their maxima and sums in a second launch.
+// records that it leaves are joined by their maxima and sums in a second launch,
+// which is placed while the first ends.
+//
+// Probabilities are rounded to the type of V for the product, as in the prompt's
+// attention (the decode's own kernel keeps the remainder too: it has tensor time to
+// spare where 256 rows a key have not): half a step relative, as the output itself.
+//
+// What bounds it.  256 rows need 256 flops for each byte of keys and values; the GPU
+// has 287 for each byte that HBM delivers (both measured).  A group of fewer rows is
+// bound by HBM, of more by the tensor cores; what the sequences have of their own is
+// bound by HBM, at g rows for each key.
+//
+// Measured (GB300, in a graph; in brackets the same by the calls that do not know of
+// groups).  Sixteen samples of an 8K prompt, 32/8 heads, 200 to 512 tokens each of
+// their own: 25 us [62] (floor 8.3; of the rest about 9 pass before the first product
+// and 6 after the last).  128 requests under four prompts of 8K to 16K, 0.2K to 2K
+// tokens each of their own: 157 us [780], 827 MB from HBM (floor 120).  128 requests
+// about two documents of 33K and 65K, 32/4 heads, fp16: 156 us [1590] (floor 65; the
+// prefixes' 7.5K tiles take 1.48 us each, 0.89 of the measured bf16 rate, on two
+// thirds of the SMs, while the others read what the requests have of their own).
+// 951 tokens of 16 questions behind two instructions of 4K to 8K: 127 us [181] (floor
+// 64, 20 of it the join of 30K rows).  112 drafted tokens of 32 samples of 32K: 91 us
+// [685] (floor 31).
+//
+// Tried, slower: the prefixes in a launch of their own with the decode's kernel for
+// the rest, whose CTAs joined a row at a time (236 us for the four prompts), or with
+// warps on their own for the rest (157, three launches, and 151 for the documents);
+// the two query tiles' results merged in the CTA (3 us an item); tiles called into L2
+// four ahead of their copies (185); a round of the softmax before the first scores to
+// fetch its instructions (0.5 to 1 us).
 #include "kv16_attention.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kMaxCtas = 160;      // of the prefixes' kernel
+constexpr int kMaxCtas = 160;      // of the line's kernel
 
 // (bounded: what is not written for a row out of range may hold anything)
 __device__ __forceinline__ Runs runs_from(int x, int ctas) {
@@ -366,7 +395,7 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
     return cudaErrorNotSupported;
   const auto kernel = kv16_attention_kernel<T, kLine>;
   constexpr int kStages = stages_of(kLine);
-  constexpr int fixed = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kStages>);
+  constexpr int fixed = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kLine>);
   static_assert(fixed + (kMaxGroups + kMaxDecodeBatch + 1 + kThreads / 32) * 4 <= 227 * 1024,
                 "shared memory of a CTA");
   const int smem = fixed + (p.line.groups.n + p.c.B + 1 + kThreads / 32) * (int)sizeof(int);
