@@ -108,7 +108,7 @@ bool shared_size_ok(const oscar_kv16_cache* c, int Hq, int n_groups, int total, 
   const long long two = 2 * (128 / (Hq / c->Hkv));
   const long long rows = (2 * (total / two) + n_groups + c->B) * c->Hkv;
   const long long places =
-      tile_cost(true) * ((std::min<long long>(max_tok, capacity(c)) + 127) / 128) + row_cost(true);
+      kMostTileCost * ((std::min<long long>(max_tok, capacity(c)) + 127) / 128) + row_cost(3);
   return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxTokens &&
          rows <= kMaxTokens && rows * places <= kMaxTokens;
 }

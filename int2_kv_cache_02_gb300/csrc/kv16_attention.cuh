@@ -263,6 +263,11 @@ __device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, in
   return x;
 }
 
+// Kind of a group's rows (kv16_line.h).
+__device__ __forceinline__ int group_kind(const AttnParams& p, int rows) {
+  return (rows > p.tokens ? 1 : 0) | (p.q.window > 0 ? 2 : 0);
+}
+
 // A sequence's own entry: nq queries from row r0 on, the first at position at0,
 // against its blocks from `shared` on.
 struct OwnEntry {
@@ -275,11 +280,11 @@ struct OwnEntry {
     const int two = 2 * p.tokens;
     return key_tiles(span(p, i * two, min(two, nq - i * two)).blocks);
   }
-  __device__ __forceinline__ bool pair(const AttnParams& p, int i) const {
+  __device__ __forceinline__ int kind(const AttnParams& p, int i) const {
     return nq - i * 2 * p.tokens > p.tokens;
   }
   __device__ __forceinline__ int places(const AttnParams& p, int i) const {
-    return row_places(tiles(p, i), pair(p, i));
+    return row_places(tiles(p, i), kind(p, i));
   }
 };
 __device__ __forceinline__ OwnEntry own_entry(const AttnParams& p, int b, bool report) {
@@ -321,7 +326,7 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
       const GroupEntry y = group_entry(p, e, 0, 1, report);
       const int tiles = key_tiles(y.sp.blocks), rows = y.r1 - y.r0;
       x = (unsigned)saturate((long long)((rows + two - 1) / two) * p.c.Hkv *
-                             row_places(tiles, rows > p.tokens));
+                             row_places(tiles, group_kind(p, rows)));
       if (report) p.line.group[e] = make_int4(tiles, y.r0, y.r1, 0);
     } else if (e < entries) {
       const OwnEntry y = own_entry(p, e - G, report);
@@ -371,15 +376,15 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
   }
   const int at = x - first[lo];
   int from, to;                   // places of the row
-  bool pair;
+  int kind;
   int all, tiles0 = 0;            // tiles of the row, of a sequence's first query tile (whose keys end first)
   int* runs;
   it.clear = false;
   if (lo < G) {
     const GroupEntry y = group_entry(p, lo, lane, 32, false);
     const int rows = y.r1 - y.r0, tiles = max(key_tiles(y.sp.blocks), 1);
-    pair = rows > p.tokens;
-    to = row_places(tiles, pair);
+    kind = group_kind(p, rows);
+    to = row_places(tiles, kind);
     int p0 = 0, chunk = 0;
     all = tiles;
     if (rows <= two) {
@@ -390,12 +395,12 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
       const int per_head = chunks * places;       // (no more than the line has: it fits)
       it.h = min(at / per_head, p.c.Hkv - 1);
       const int in_head = at - it.h * per_head, z = min(in_head / chunks, places - 1);
-      const Blocks blocks(tiles, chunks, pair, share);
-      const int t = max(z - row_cost(pair), 0) / tile_cost(pair);
+      const Blocks blocks(tiles, chunks, kind, share);
+      const int t = whole_tiles(max(z - row_cost(kind), 0), kind);
       const int i = min(t / blocks.least, blocks.count - 1);
-      p0 = tile_place(blocks.first(i), pair);
+      p0 = tile_place(blocks.first(i), kind);
       if (blocks.count > 1) all = 0;
-      if (i + 1 < blocks.count) to = tile_place(blocks.first(i + 1), pair);
+      if (i + 1 < blocks.count) to = tile_place(blocks.first(i + 1), kind);
       const int in = in_head - chunks * p0;
       chunk = min(in / (to - p0), chunks - 1);
       from = p0 + in - chunk * (to - p0);
@@ -406,7 +411,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.row0 = y.r0 + chunk * two;
     it.nrow = min(two, y.r1 - it.row0);
     it.sp = y.sp;
-    it.split = from <= row_cost(pair) ? 0 : from > p0 ? 1 : 2;  // where the records go
+    it.split = from <= row_cost(kind) ? 0 : from > p0 ? 1 : 2;  // where the records go
     runs = p.line.prefix_runs;
   } else {
     const OwnEntry y = own_entry(p, lo - G, false);
@@ -448,21 +453,21 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.at0 = y.at0 + chunk * two;
     it.sp = y.span(p, chunk * two, it.nrow);
     from = max(in, 0);
-    pair = y.pair(p, chunk);
+    kind = y.kind(p, chunk);
     all = key_tiles(it.sp.blocks);
-    to = row_places(all, pair);
+    to = row_places(all, kind);
     runs = p.line.own_runs;
     tiles0 = key_tiles(y.span(p, chunk * two, min(it.nrow, p.tokens)).blocks);
-    it.split = from <= row_cost(pair) ? -1 : 1;
+    it.split = from <= row_cost(kind) ? -1 : 1;
   }
   const int end = (int)min(min((long long)from + (x1 - x), (long long)to),
                            (long long)from + (first[lo + 1] - x));
-  it.k0 = tiles_before(from, pair);
-  it.k1 = tiles_before(end, pair);
+  it.k0 = tiles_before(from, kind);
+  it.k1 = tiles_before(end, kind);
   it.cnt[0] = it.nrow > 0 ? max(it.k1 - it.k0, 0) : 0;
   it.cnt[1] = it.nrow > p.tokens ? it.cnt[0] : 0;
   if (lane == 0 && it.split <= 0 && all > 0 && it.cnt[0] > 0) {
-    const int last = x - from + row_cost(pair) + (all - 1) * tile_cost(pair);
+    const int last = x - from + row_cost(kind) + (all - 1) * tile_cost(kind);
     const int n = min(last / share, (int)gridDim.x - 1) - (int)blockIdx.x + 1;
     runs[(long long)it.row0 * p.c.Hkv + it.h] = blockIdx.x | n << 16;
   }

@@ -15,10 +15,9 @@ namespace oscar {
 // The work of a call stands in one line, and each of `ctas` CTAs takes an equal run
 // of it.  A row of the line is one chunk of up to 256 query rows and one KV head
 // against its tiles of 128 keys: some places for what it costs to begin and end an
-// item, then some a tile, by what they took on the GPU (in 0.14 us; `pair`: a chunk
-// that fills both query tiles).  Entry i below the number of groups is group i's
-// prefix, the others are the sequences' own blocks behind it.  An entry has its
-// rows KV head by KV head:
+// item, then some a tile, by what they took on the GPU (in 0.14 us).  Entry i below
+// the number of groups is group i's prefix, the others are the sequences' own blocks
+// behind it.  An entry has its rows KV head by KV head:
 //  a sequence  chunk after chunk, each its own tiles (causal: a later chunk has
 //              more)
 //  a group     block after block of tiles, and within a block chunk after chunk.
@@ -27,9 +26,22 @@ namespace oscar {
 //              different chunks do so at the same time, and the keys come from HBM
 //              once.
 // A tile is the run's that has its first place.
-KV16_CONST int row_cost(bool pair) { return pair ? 56 : 20; }
-KV16_CONST int tile_cost(bool pair) { return pair ? 11 : 8; }
-constexpr int kMinPlaces = 12;   // of a CTA's run: any within a row has a tile
+// The kind of a row has bit 0 if its chunk fills both query tiles, and bit 1 if it is a
+// group's under a window: its sequences' windows begin at different tokens, so its
+// tiles are masked row by row, which takes twice as long (4 groups of 12 sequences, 6 K
+// tokens in common, a window of 4 K: 33.1 us, 38.2 with both weighed alike, 35.9 with
+// three times; the sequences' own tiles weighed twice too: 37.2).
+KV16_CONST int row_cost(int kind) { return kind & 1 ? 56 : 20; }
+KV16_CONST int tile_cost(int kind) {
+  return (kind & 1 ? 11 : 8) << (kind >> 1);
+}
+// Whole tiles in so many places (the divisors are constants: quick).
+KV16_CONST int whole_tiles(int places, int kind) {
+  const int x = places >> (kind >> 1);
+  return kind & 1 ? x / 11 : x / 8;
+}
+constexpr int kMostTileCost = tile_cost(3);
+constexpr int kMinPlaces = kMostTileCost;   // of a CTA's run: any within a row has a tile
 KV16_BOTH int line_share(int places, int ctas) {
   const int per = places / ctas + (places % ctas != 0);
   return per > kMinPlaces ? per : kMinPlaces;
@@ -38,26 +50,25 @@ KV16_BOTH int line_share(int places, int ctas) {
 // long as a run or a little longer; the last has what is left too.
 struct Blocks {
   int count, least, tiles;
-  KV16_BOTH Blocks(int tiles, int chunks, bool pair, int per)
+  KV16_BOTH Blocks(int tiles, int chunks, int kind, int per)
       : count(1), least(tiles), tiles(tiles) {
-    const int run = (per + tile_cost(pair) - 1) / tile_cost(pair);
+    const int run = whole_tiles(per + tile_cost(kind) - 1, kind);
     if (chunks > 1 && tiles >= 2 * run) count = tiles / run, least = run;
   }
   KV16_BOTH int first(int i) const { return i < count ? i * least : tiles; }
 };
 // Place in its row where tile t begins (those of tile 0 with the row's own).
-KV16_BOTH int tile_place(int t, bool pair) {
-  return t == 0 ? 0 : row_cost(pair) + t * tile_cost(pair);
+KV16_BOTH int tile_place(int t, int kind) {
+  return t == 0 ? 0 : row_cost(kind) + t * tile_cost(kind);
 }
 // Tiles that begin before place x of a row.
-KV16_BOTH int tiles_before(int x, bool pair) {
-  x -= row_cost(pair);
-  return x <= 0 ? 0 : pair ? (x + tile_cost(true) - 1) / tile_cost(true)
-                           : (x + tile_cost(false) - 1) / tile_cost(false);
+KV16_BOTH int tiles_before(int x, int kind) {
+  x -= row_cost(kind);
+  return x <= 0 ? 0 : whole_tiles(x + tile_cost(kind) - 1, kind);
 }
 // Places of a row of so many tiles.
-KV16_BOTH int row_places(int tiles, bool pair) {
-  return tiles > 0 ? row_cost(pair) + tiles * tile_cost(pair) : 0;
+KV16_BOTH int row_places(int tiles, int kind) {
+  return tiles > 0 ? row_cost(kind) + tiles * tile_cost(kind) : 0;
 }
 
 // The CTAs [c0, c0 + n) that have tiles of a block whose first tile is at place `at`

@@ -23,6 +23,8 @@
 // about two documents of 33K and 65K, 32/4 heads, fp16: 156 us [1590] (floor 65; the
 // prefixes' 7.5K tiles take 1.48 us each, 0.89 of the measured bf16 rate, on two
 // thirds of the SMs, while the others read what the requests have of their own).
+// 48 sequences under four instructions of 6K, a window of 4K and 4 sinks, 24/2 heads,
+// fp16: 33 us [40] (floor 13; masked tiles of two query tiles take 3 us each).
 // 951 tokens of 16 questions behind two instructions of 4K to 8K: 127 us [181] (floor
 // 64, 20 of it the join of 30K rows).  112 drafted tokens of 32 samples of 32K: 91 us
 // [685] (floor 31).
@@ -49,12 +51,14 @@ __device__ __forceinline__ Runs runs_from(int x, int ctas) {
 // The records of both parts of a row (query, head) joined by a warp, and queries that
 // belong to no sequence left alone.  Few rows (BATCH false): a CTA has rows of one
 // query and KV head, a warp each or `subs` of its four warps, each every so-many-th
-// record.  Many: a warp has the group's rows of `batch` queries, one after another.
+// record.  Many: a warp has the group's rows of `batch` queries one after another,
+// two rows at a time, half its lanes each.
 //
-// Bound by latency: the sequence, its group and its runs are a chain of loads, then
-// a record's place is found.  So a warp's lanes find 32 records at a time, a lane
-// each, once for the rows that lie in the same rows of the line, and U records are
-// in flight.
+// Bound by latency where rows are few: the sequence, its group and its runs are a
+// chain of loads, then a record's place is found.  So a warp's lanes find 32 records
+// at a time, a lane each, once for the queries that lie in the same rows of the line,
+// and eight records are in flight.  Bound by instructions where rows are many (30K
+// rows: 28 us by a warp a row, 20 by halves).
 constexpr int kJoinWarps = 4, kJoinCtas = 6, kBatchCtas = 5;     // warps of a CTA, CTAs of an SM
 template <class T, bool BATCH>
 __global__ void __launch_bounds__(kJoinWarps * 32, BATCH ? kBatchCtas : kJoinCtas)
@@ -87,10 +91,10 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
   Runs own{0, 0}, prefix{0, 0};
   int twice_own = 0, twice = 0;     // two records a run
   int in_own = 0, in_prefix = 0;    // the query's place in its chunks
-  bool pair = false;
+  int kind = 0;
   int chunks = 1, chunk = 0;
   unsigned at = 0;
-  Blocks blocks(0, 1, false, 1);
+  Blocks blocks(0, 1, 0, 1);
   // the lane's record of head 0 in 32-byte steps from the first of all, or none; from a
   // query to the next it moves by `step`, and by `fix` more into a chunk's second tile
   constexpr unsigned kNone = ~0u, kSteps = kPartFloats / 8;
@@ -113,9 +117,9 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       k = j / kBlockRuns;
       j -= k * kBlockRuns;
       const int t0 = blocks.first(k), t1 = blocks.first(k + 1);
-      const int p0 = tile_place(t0, pair), len = row_places(t1, pair) - p0;
-      x = runs_of(at + (unsigned)chunks * p0 + (unsigned)chunk * len + (k == 0 ? row_cost(pair) : 0),
-                  (t1 - t0 - 1) * tile_cost(pair), per, s.ctas);
+      const int p0 = tile_place(t0, kind), len = row_places(t1, kind) - p0;
+      x = runs_of(at + (unsigned)chunks * p0 + (unsigned)chunk * len + (k == 0 ? row_cost(kind) : 0),
+                  (t1 - t0 - 1) * tile_cost(kind), per, s.ctas);
     }
     if (j >= x.n) return;
     const float* e;
@@ -165,7 +169,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       // does the chunk's last query stand in or behind the first block of its own?
       if (len - (seq1 - to) - 1 >= sq.y * kPage && len > 0)
         own = runs_from(__ldcg(s.own_runs + (long long)row0 * p.c.Hkv + h), s.ctas);
-      blocks = Blocks(0, 1, false, 1);
+      blocks = Blocks(0, 1, 0, 1);
       if (sq.x >= 0) {
         const int4 gr = __ldcg(s.group + sq.x);
         const int tiles = gr.x, rows = gr.z - gr.y;
@@ -173,13 +177,13 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
         chunks = (rows + two - 1) / two;
         if (tiles > 0 && r >= gr.y && chunk < chunks) {
           const int p_row0 = gr.y + chunk * two;
-          pair = rows > p.tokens;
+          kind = group_kind(p, rows);
           in_prefix = r - p_row0;
           twice = gr.z - p_row0 <= p.tokens;
           to = min(to, p_row0 + two);
-          blocks = Blocks(tiles, chunks, pair, per);
+          blocks = Blocks(tiles, chunks, kind, per);
           if (blocks.count > 1) {
-            at = __ldcg(s.first + sq.x) + (unsigned)chunks * (unsigned)row_places(tiles, pair) * h;
+            at = __ldcg(s.first + sq.x) + (unsigned)chunks * (unsigned)row_places(tiles, kind) * h;
             prefix = Runs{0, blocks.count * kBlockRuns};
           } else {
             prefix = runs_from(__ldcg(s.prefix_runs + (long long)p_row0 * p.c.Hkv + h), s.ctas);
@@ -354,7 +358,7 @@ size_t up32(size_t n) { return (n + 31) / 32 * 32; }
 int line_ctas(const Kv16& c, int Hq, int n_groups, int total, int max_tok) {
   const int two = 2 * (128 / (Hq / c.Hkv));
   const long long rows = (2LL * (total / two) + n_groups + std::min(c.B, total)) * c.Hkv;
-  const long long places = rows * (row_cost(true) + (std::min(max_tok, c.cap) + 127LL) / 128 * tile_cost(true));
+  const long long places = rows * (row_cost(3) + (std::min(max_tok, c.cap) + 127LL) / 128 * kMostTileCost);
   return (int)std::max<long long>(
       1, std::min<long long>(places / kMinPlaces, std::min(sm_count(), kMaxCtas)));
 }

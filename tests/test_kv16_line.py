@@ -14,14 +14,14 @@ HARNESS = r"""
 #include "kv16_line.h"
 using namespace oscar;
 extern "C" {
-int row_cost_(int pair) { return row_cost(pair); }
-int tile_cost_(int pair) { return tile_cost(pair); }
+int row_cost_(int kind) { return row_cost(kind); }
+int tile_cost_(int kind) { return tile_cost(kind); }
 int share(int places, int ctas) { return line_share(places, ctas); }
-int count(int tiles, int chunks, int pair, int per) { return Blocks(tiles, chunks, pair, per).count; }
-int first(int tiles, int chunks, int pair, int per, int i) { return Blocks(tiles, chunks, pair, per).first(i); }
-int place(int t, int pair) { return tile_place(t, pair); }
-int before(int x, int pair) { return tiles_before(x, pair); }
-int places(int tiles, int pair) { return row_places(tiles, pair); }
+int count(int tiles, int chunks, int kind, int per) { return Blocks(tiles, chunks, kind, per).count; }
+int first(int tiles, int chunks, int kind, int per, int i) { return Blocks(tiles, chunks, kind, per).first(i); }
+int place(int t, int kind) { return tile_place(t, kind); }
+int before(int x, int kind) { return tiles_before(x, kind); }
+int places(int tiles, int kind) { return row_places(tiles, kind); }
 int runs(unsigned at, unsigned more, unsigned per, int ctas) {
   const Runs r = runs_of(at, more, per, ctas);
   return r.c0 | r.n << 16;
@@ -42,11 +42,12 @@ def lib(tmp_path_factory):
 
 
 def draw_entries(rng):
-    """Groups (chunks, tiles, pair) and sequences [(tiles, pair) of each chunk]."""
+    """Groups (chunks, tiles, kind) and sequences [(tiles, kind) of each chunk]."""
     groups, seqs = [], []
     for _ in range(rng.randint(1, 4)):
         chunks = rng.choice([1, 1, 2, 3, 7])
-        groups.append((chunks, rng.choice([0, 1, 2, 5, 17, 60, 200, 2000]), chunks > 1 or rng.random() < 0.5))
+        groups.append((chunks, rng.choice([0, 1, 2, 5, 17, 60, 200, 2000]),
+                       (chunks > 1 or rng.random() < 0.5) + 2 * (rng.random() < 0.3)))
     for _ in range(rng.randint(1, 9)):
         n = rng.choice([1, 1, 2, 3])
         rows = [(rng.randint(0, 6) + 3 * i, True) for i in range(n)]
@@ -59,8 +60,8 @@ def draw_entries(rng):
 def pieces(lib, groups, seqs, heads, ctas):
     """What the kernel's CTAs work: (entry, head, chunk) -> {tile: (CTA, record place)}."""
     first = [0]
-    for chunks, tiles, pair in groups:
-        first.append(first[-1] + heads * chunks * lib.places(tiles, pair))
+    for chunks, tiles, kind in groups:
+        first.append(first[-1] + heads * chunks * lib.places(tiles, kind))
     for rows in seqs:
         first.append(first[-1] + heads * sum(lib.places(t, p) for t, p in rows))
     total = first[-1]
@@ -72,23 +73,23 @@ def pieces(lib, groups, seqs, heads, ctas):
             e = next(i for i in range(len(first) - 1) if first[i] <= x < first[i + 1])
             at = x - first[e]
             if e < len(groups):
-                chunks, tiles, pair = groups[e]
-                to, p0, chunk = lib.places(tiles, pair), 0, 0
+                chunks, tiles, kind = groups[e]
+                to, p0, chunk = lib.places(tiles, kind), 0, 0
                 if chunks == 1:
                     head, start = divmod(at, to)
                 else:
                     head, y = divmod(at, chunks * to)
-                    t = max(y // chunks - lib.row_cost_(pair), 0) // lib.tile_cost_(pair)
-                    n = lib.count(tiles, chunks, pair, per)
-                    least = lib.first(tiles, chunks, pair, per, 1)
+                    t = max(y // chunks - lib.row_cost_(kind), 0) // lib.tile_cost_(kind)
+                    n = lib.count(tiles, chunks, kind, per)
+                    least = lib.first(tiles, chunks, kind, per, 1)
                     i = min(t // least, n - 1)
-                    p0 = lib.place(lib.first(tiles, chunks, pair, per, i), pair)
+                    p0 = lib.place(lib.first(tiles, chunks, kind, per, i), kind)
                     if i + 1 < n:
-                        to = lib.place(lib.first(tiles, chunks, pair, per, i + 1), pair)
+                        to = lib.place(lib.first(tiles, chunks, kind, per, i + 1), kind)
                     y -= chunks * p0
                     chunk = min(y // (to - p0), chunks - 1)
                     start = p0 + y - chunk * (to - p0)
-                where = "row" if start <= lib.row_cost_(pair) else 1 if start > p0 else 2
+                where = "row" if start <= lib.row_cost_(kind) else 1 if start > p0 else 2
             else:
                 rows = seqs[e - len(groups)]
                 head, start = divmod(at, (first[e + 1] - first[e]) // heads)
@@ -96,11 +97,11 @@ def pieces(lib, groups, seqs, heads, ctas):
                 while start >= lib.places(*rows[chunk]):
                     start -= lib.places(*rows[chunk])
                     chunk += 1
-                tiles, pair = rows[chunk]
-                to = lib.places(tiles, pair)
-                where = "row" if start <= lib.row_cost_(pair) else 1
+                tiles, kind = rows[chunk]
+                to = lib.places(tiles, kind)
+                where = "row" if start <= lib.row_cost_(kind) else 1
             end = min(start + x1 - x, to, start + first[e + 1] - x)
-            k0, k1 = lib.before(start, pair), lib.before(end, pair)
+            k0, k1 = lib.before(start, kind), lib.before(end, kind)
             row = (e, head, chunk)
             if k1 > k0:
                 place = ("row", row) if where == "row" else (cta, where)
@@ -124,7 +125,7 @@ def test_every_tile_is_worked_and_joined_once(lib, heads, ctas):
         for e in range(len(groups) + len(seqs)):
             rows = [groups[e][1:]] * groups[e][0] if e < len(groups) else seqs[e - len(groups)]
             for head in range(heads):
-                for chunk, (tiles, pair) in enumerate(rows):
+                for chunk, (tiles, kind) in enumerate(rows):
                     if tiles == 0:
                         continue
                     n += tiles
@@ -140,18 +141,18 @@ def test_every_tile_is_worked_and_joined_once(lib, heads, ctas):
                             found.add(((r & 0xffff) + j, 1) if j else begins(r & 0xffff))
                         return r >> 16
 
-                    blocks = lib.count(tiles, len(rows), pair, per) if e < len(groups) else 1
+                    blocks = lib.count(tiles, len(rows), kind, per) if e < len(groups) else 1
                     if blocks == 1:
                         at += sum(lib.places(t, p) for t, p in rows[:chunk])
-                        add(at + lib.row_cost_(pair), (tiles - 1) * lib.tile_cost_(pair), lambda c: "row")
+                        add(at + lib.row_cost_(kind), (tiles - 1) * lib.tile_cost_(kind), lambda c: "row")
                     else:
                         assert 2 * blocks <= ctas + 1
                         for i in range(blocks):
-                            t0, t1 = (lib.first(tiles, len(rows), pair, per, i + z) for z in (0, 1))
-                            p0 = lib.place(t0, pair)
-                            span = lib.places(t1, pair) - p0
-                            runs = add(at + len(rows) * p0 + chunk * span + (0 if i else lib.row_cost_(pair)),
-                                       (t1 - t0 - 1) * lib.tile_cost_(pair), lambda c: (c, 2) if i else "row")
+                            t0, t1 = (lib.first(tiles, len(rows), kind, per, i + z) for z in (0, 1))
+                            p0 = lib.place(t0, kind)
+                            span = lib.places(t1, kind) - p0
+                            runs = add(at + len(rows) * p0 + chunk * span + (0 if i else lib.row_cost_(kind)),
+                                       (t1 - t0 - 1) * lib.tile_cost_(kind), lambda c: (c, 2) if i else "row")
                             assert runs <= lib.block_runs()
                     assert found == wrote
         assert n == len(done)
