@@ -624,7 +624,7 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * whole batch's lengths: the same call gives the same bits, another batch may round
  * differently.
  * B <= 4096, n_groups <= 4096 and, with c = 2 * (128 / (Hq / Hkv)) query tokens in a
- * chunk, (2 * (B / c) + n_groups + B) * Hkv * (22 * ceil(max_tok / 128) + 56) < 2^31 -
+ * chunk, (2 * (B / c) + n_groups + B) * Hkv * (22 * ceil(max_tok / 128) + 48) < 2^31 -
  * 128 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,

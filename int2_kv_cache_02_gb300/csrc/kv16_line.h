@@ -28,17 +28,21 @@ namespace oscar {
 // A tile is the run's that has its first place.
 // The kind of a row has bit 0 if its chunk fills both query tiles, and bit 1 if it is a
 // group's under a window: its sequences' windows begin at different tokens, so its
-// tiles are masked row by row, which takes twice as long (4 groups of 12 sequences, 6 K
-// tokens in common, a window of 4 K: 33.1 us, 38.2 with both weighed alike, 35.9 with
-// three times; the sequences' own tiles weighed twice too: 37.2).
-KV16_CONST int row_cost(int kind) { return kind & 1 ? 56 : 20; }
+// tiles are masked row by row, which takes longer.  The costs are by the CTAs' ends in
+// seven calls of 26 to 160 us (with 20 and 56 for the rows, 8 and 11 for the tiles, 16
+// and 22 masked, CTAs ended up to 30 us apart: 128 requests about two documents 155 us
+// instead of 148, drafts of 32 samples 90 instead of 84; 36 other calls of 26 to 1180
+// us took 1.2 % longer on average).
+constexpr int kRow = 28, kPairRow = 48;
+constexpr int kTile = 10, kPairTile = 13, kMaskedTile = 16, kMaskedPairTile = 22;
+KV16_CONST int row_cost(int kind) { return kind & 1 ? kPairRow : kRow; }
 KV16_CONST int tile_cost(int kind) {
-  return (kind & 1 ? 11 : 8) << (kind >> 1);
+  return kind & 2 ? (kind & 1 ? kMaskedPairTile : kMaskedTile) : kind & 1 ? kPairTile : kTile;
 }
 // Whole tiles in so many places (the divisors are constants: quick).
-KV16_CONST int whole_tiles(int places, int kind) {
-  const int x = places >> (kind >> 1);
-  return kind & 1 ? x / 11 : x / 8;
+KV16_CONST int whole_tiles(int x, int kind) {
+  return kind & 2 ? (kind & 1 ? x / kMaskedPairTile : x / kMaskedTile)
+                  : (kind & 1 ? x / kPairTile : x / kTile);
 }
 constexpr int kMostTileCost = tile_cost(3);
 constexpr int kMinPlaces = kMostTileCost;   // of a CTA's run: any within a row has a tile

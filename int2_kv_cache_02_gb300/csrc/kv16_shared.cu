@@ -17,24 +17,28 @@
 //
 // Measured (GB300, in a graph; in brackets the same by the calls that do not know of
 // groups).  Sixteen samples of an 8K prompt, 32/8 heads, 200 to 512 tokens each of
-// their own: 25 us [62] (floor 8.3; of the rest about 9 pass before the first product
-// and 6 after the last).  128 requests under four prompts of 8K to 16K, 0.2K to 2K
-// tokens each of their own: 157 us [780], 827 MB from HBM (floor 120).  128 requests
-// about two documents of 33K and 65K, 32/4 heads, fp16: 156 us [1590] (floor 65; the
-// prefixes' 7.5K tiles take 1.48 us each, 0.89 of the measured bf16 rate, on two
-// thirds of the SMs, while the others read what the requests have of their own).
+// their own: 25 us [62] (floor 8.3; of the rest 6 pass before the first product, as
+// many after the last).  128 requests under four prompts of 8K to 16K, 0.2K to 2K
+// tokens each of their own: 159 us [780], 827 MB from HBM (floor 120).  128 requests
+// about two documents of 33K and 65K, 32/4 heads, fp16: 148 us [1590] (floor 65; the
+// prefixes' 7.5K tiles of two query tiles take 1.65 us each, 0.79 of the measured bf16
+// rate, on 108 of the SMs, while the others read what the requests have of their own).
 // 48 sequences under four instructions of 6K, a window of 4K and 4 sinks, 24/2 heads,
 // fp16: 33 us [40] (floor 13; masked tiles of two query tiles take 3 us each).
-// 951 tokens of 16 questions behind two instructions of 4K to 8K: 127 us [181] (floor
-// 64, 20 of it the join of 30K rows).  112 drafted tokens of 32 samples of 32K: 91 us
+// 951 tokens of 16 questions behind two instructions of 4K to 8K: 126 us [181] (floor
+// 64, 20 of it the join of 30K rows).  112 drafted tokens of 32 samples of 32K: 84 us
 // [685] (floor 31).
 //
 // Tried, slower: the prefixes in a launch of their own with the decode's kernel for
 // the rest, whose CTAs joined a row at a time (236 us for the four prompts), or with
 // warps on their own for the rest (157, three launches, and 151 for the documents);
 // the two query tiles' results merged in the CTA (3 us an item); tiles called into L2
-// four ahead of their copies (185); a round of the softmax before the first scores to
-// fetch its instructions (0.5 to 1 us).
+// four ahead of their copies (185); pages looked up eight tiles ahead (1 to 4 %); a
+// round of the softmax before the first scores to fetch its instructions (0.5 to 1 us).
+// The two SMs of a pair slow each other down where one has long rows of two query tiles
+// and the other many of a single tile of keys (a CTA of the questions 132 us instead of
+// 100); the sequences' rows begun with an even CTA, so that no pair has both, cost
+// other calls more (1 % on average).
 #include "kv16_attention.cuh"
 
 namespace oscar {
