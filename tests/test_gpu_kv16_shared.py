@@ -160,6 +160,17 @@ def test_decode_blocks(L, members, prefix, Hq, Hkv, dtype):
     decode(L, case, case.cache(L), Hq)
 
 
+@pytest.mark.parametrize("window,sink", [(2600, 4), (700, 130), (4999, 0), (40, 1)])
+@pytest.mark.parametrize("members,Hq,Hkv,dtype", [(130, 4, 1, BF), (20, 4, 2, FP), (90, 12, 2, FP)])
+def test_decode_windows_in_blocks(L, members, Hq, Hkv, dtype, window, sink):
+    """A prefix in blocks (or one row) under windows that begin in it, at unequal
+    places, and behind it."""
+    prefix = 5000
+    lens = [prefix + 1 + (613 * b) % 3000 for b in range(members)]
+    case = SharedCase([members, 3], [prefix, 600], lens + [640, 601, 2900], Hkv, dtype=dtype, seed=members + sink)
+    decode(L, case, case.cache(L), Hq, window, sink)
+
+
 def test_decode_many_sequences_and_groups(L):
     """The most sequences, each a group of its own, and all in pairs."""
     lens = [33 + b % 40 for b in range(4096)]
@@ -373,6 +384,12 @@ def test_attention_many_rows(L):
     attend(L, case, case.cache(L), [300, 200, 20, 90, 400, 1], 8, extra=0)
     case = SharedCase([9], [9000], [9005 + b for b in range(9)], 2, seed=2)
     attend(L, case, case.cache(L), [5, 4, 3, 5, 1, 2, 5, 5, 3], 8, lse=False)
+
+
+@pytest.mark.parametrize("window,sink", [(2600, 4), (300, 130)])
+def test_attention_windows_in_blocks(L, window, sink):
+    case = SharedCase([5, 2], [4500, 900], [4700, 5100, 4520, 6100, 4801, 1200, 901], 2, dtype=FP, seed=sink)
+    attend(L, case, case.cache(L), [150, 90, 20, 70, 301, 40, 1], 8, window, sink)
 
 
 # ------------------------------------------- graphs, streams, workspaces
