@@ -221,15 +221,35 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
 
 __device__ __forceinline__ int key_tiles(int blocks) { return (blocks + kKeyPages - 1) / kKeyPages; }
 
+// The lowest and the highest position of queries, those of sequence b or none.
+struct Reach {
+  int lo, hi;
+};
+__device__ __forceinline__ Reach reach_of(const AttnParams& p, int b) {
+  const int n = kv16_length(p.c, b, p.q.max_tok);
+  const int nq = p.q.start ? __ldg(p.q.start + b + 1) - __ldg(p.q.start + b) : 1;
+  return n > 0 && nq > 0 ? Reach{max(n - nq, 0), n - 1} : Reach{0x7fffffff, -1};
+}
+// Those of sequences [b0, b1).  A warp.
+__device__ __forceinline__ Reach warp_reach(const AttnParams& p, int b0, int b1) {
+  Reach x{0x7fffffff, -1};
+  for (int b = b0 + (threadIdx.x & 31); b < b1; b += 32) {
+    const Reach y = reach_of(p, b);
+    x = Reach{min(x.lo, y.lo), max(x.hi, y.hi)};
+  }
+  return Reach{__reduce_min_sync(0xffffffffu, x.lo), __reduce_max_sync(0xffffffffu, x.hi)};
+}
+
 // A group's entry of the line: its sequences' queries [r0, r1) against the blocks
-// of `sp`.  One thread looks, or a warp (step 32, one answer).
+// of `sp`.  reach: of its sequences, asked for under a window.
 struct GroupEntry {
   Shared s;
   int r0, r1;
   Span sp;
 };
-__device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, int first, int step,
-                                                  bool report) {
+template <class F>
+__device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, bool report,
+                                                  F&& reach) {
   GroupEntry x;
   x.s = shared_of(p.c, p.line.groups, i, p.q.max_tok, report);
   x.r0 = x.s.lead;
@@ -245,22 +265,13 @@ __device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, in
   x.sp.sink_blocks = x.sp.w0 = 0;
   x.sp.blocks = x.r1 > x.r0 ? x.s.blocks : 0;
   if (p.q.window > 0 && x.sp.blocks > 0) {
-    // what any of the sequences' queries sees
-    int lo = 0x7fffffff, hi = -1;
-    for (int b = x.s.lead + first; b < x.s.end; b += step) {
-      const int n = kv16_length(p.c, b, p.q.max_tok);
-      const int nq = p.q.start ? __ldg(p.q.start + b + 1) - __ldg(p.q.start + b) : 1;
-      if (n <= 0 || nq <= 0) continue;
-      lo = min(lo, max(n - nq, 0));
-      hi = max(hi, n - 1);
-    }
-    if (step > 1) {
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-    }
-    x.sp = Span(lo, hi, p.q.window, p.q.n_sink).below(x.s.blocks);
+    const Reach y = reach(x.s);
+    x.sp = Span(y.lo, y.hi, p.q.window, p.q.n_sink).below(x.s.blocks);
   }
   return x;
+}
+__device__ __forceinline__ GroupEntry warp_group_entry(const AttnParams& p, int i) {
+  return group_entry(p, i, false, [&](const Shared& s) { return warp_reach(p, s.lead, s.end); });
 }
 
 // Kind of a group's rows (kv16_line.h).
@@ -312,18 +323,32 @@ __device__ __forceinline__ int saturate(long long x) { return (int)min(x, 0x7fff
 
 // The entries' first places, first[0 .. groups + B] (no more than the largest int,
 // so that groups that overlap do not wrap around).  All threads of the CTA; ends
-// with a barrier.
-__device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* scan) {
+// with a barrier.  reach: [groups], room that is free until then.  (Under a window a
+// group's span goes by all its sequences, a thread each: 512 of one group 38 us, 54 by
+// a thread a group.)
+__device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* scan, Reach* reach) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int two = 2 * p.tokens, G = p.line.groups.n, entries = G + p.c.B;
   const bool report = blockIdx.x == 0;
+  if (p.q.window > 0) {
+    for (int e = tid; e < G; e += kThreads) reach[e] = Reach{0x7fffffff, -1};
+    __syncthreads();
+    for (int b = tid; b < p.c.B; b += kThreads) {
+      const Reach y = reach_of(p, b);
+      const int i = y.hi < 0 ? -1 : group_of(p.line.groups, b);
+      if (i < 0) continue;
+      atomicMin(&reach[i].lo, y.lo);
+      atomicMax(&reach[i].hi, y.hi);
+    }
+    __syncthreads();
+  }
   unsigned carry = 0;      // sums of two numbers below 2^31
   auto plus = [](unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); };
   for (int e0 = 0; e0 < entries; e0 += kThreads) {
     const int e = e0 + tid;
     unsigned x = 0;
     if (e < G) {
-      const GroupEntry y = group_entry(p, e, 0, 1, report);
+      const GroupEntry y = group_entry(p, e, report, [&](const Shared&) { return reach[e]; });
       const int tiles = key_tiles(y.sp.blocks), rows = y.r1 - y.r0;
       x = (unsigned)saturate((long long)((rows + two - 1) / two) * p.c.Hkv *
                              row_places(tiles, group_kind(p, rows)));
@@ -359,6 +384,8 @@ __device__ __forceinline__ void line_up(const AttnParams& p, int* first, int* sc
     first[entries] = (int)carry;
     if (report) p.line.first[entries] = (int)carry;
   }
+  // (copies may land where `reach` was)
+  if (p.q.window > 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
 }
 
@@ -381,7 +408,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
   int* runs;
   it.clear = false;
   if (lo < G) {
-    const GroupEntry y = group_entry(p, lo, lane, 32, false);
+    const GroupEntry y = warp_group_entry(p, lo);
     const int rows = y.r1 - y.r0, tiles = max(key_tiles(y.sp.blocks), 1);
     kind = group_kind(p, rows);
     to = row_places(tiles, kind);
@@ -641,7 +668,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   if constexpr (PART == kLine) {
     const int entries = p.line.groups.n + p.c.B;
-    line_up(p, first, first + entries + 1);
+    line_up(p, first, first + entries + 1, reinterpret_cast<Reach*>(smem));
     const int total = first[entries];
     share = line_share(total, gridDim.x);
     x0 = (int)min((long long)blockIdx.x * share, (long long)total);

@@ -69,7 +69,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, BATCH ? kBatchCtas : kJoinCta
 kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batch) {
   __shared__ float4 s_o[BATCH ? 1 : kJoinWarps][32];
   __shared__ float2 s_ml[BATCH ? 1 : kJoinWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const SharedParts& s = p.line;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = p.g, two = 2 * p.tokens;
   int first_r, end_r, h, head0 = 0, sub = 0;
@@ -88,10 +87,39 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
     sub = warp % subs;
   }
   const int G = s.groups.n;
+  // the sequence of query r, and its queries
+  int b = -1, seq0 = 0, seq1 = 0;
+  auto find = [&](int r) {
+    b = r;
+    seq0 = r;
+    seq1 = r + 1;
+    if (!p.q.start) return;
+    b = warp_sequence(p.q.start, p.c.B, r);
+    if (b < 0) return;
+    seq0 = __ldg(p.q.start + b);
+    seq1 = __ldg(p.q.start + b + 1);
+    if (seq0 < 0 || seq1 > p.q.total) b = -1;
+  };
+  // A first wave of CTAs waits for the line: it finds its sequence and group meanwhile,
+  // from what the call was given (0.5 to 1.5 us of a call), where later ones load
+  // what the line has found.
+  const bool early = !BATCH && blockIdx.x < kJoinCtas * s.ctas;
+  int2 sq = make_int2(-1, 0);
+  int4 gr = make_int4(0, 0, 0, 0);
+  if (!BATCH) find(first_r);
+  if (early && b >= 0) {
+    sq.x = warp_sequence(s.groups.group, G, b);
+    if (sq.x >= 0) {
+      const GroupEntry y = warp_group_entry(p, sq.x);
+      sq.y = y.s.blocks;
+      gr = make_int4(key_tiles(y.sp.blocks), y.r0, y.r1, 0);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const unsigned per = line_share(__ldcg(s.first + G + p.c.B), s.ctas);
 
   // of the queries [.., same): their sequence, and their rows of the line
-  int same = first_r, b = -1, seq1 = 0, n = 0;
+  int same = first_r, n = 0;
   Runs own{0, 0}, prefix{0, 0};
   int twice_own = 0, twice = 0;     // two records a run
   int in_own = 0, in_prefix = 0;    // the query's place in its chunks
@@ -150,20 +178,9 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
       if ((in == 0 && in_own == p.tokens) || (in == 1 && in_prefix == p.tokens)) off += fix;
     } else {
       same = r + 1;
-      b = r;
-      int seq0 = r;
-      seq1 = r + 1;
-      if (p.q.start) {
-        b = warp_sequence(p.q.start, p.c.B, r);
-        if (b < 0) continue;
-        seq0 = __ldg(p.q.start + b);
-        seq1 = __ldg(p.q.start + b + 1);
-        if (seq0 < 0 || seq1 > p.q.total) {
-          b = -1;
-          continue;
-        }
-      }
-      const int2 sq = __ldcg(s.seq + b);
+      if (BATCH) find(r);
+      if (b < 0) continue;
+      if (!early) sq = __ldcg(s.seq + b);
       const int len = kv16_length(p.c, b, p.q.max_tok), own_chunk = (r - seq0) / two;
       const int row0 = seq0 + own_chunk * two;
       int to = min(seq1, row0 + two);
@@ -175,7 +192,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
         own = runs_from(__ldcg(s.own_runs + (long long)row0 * p.c.Hkv + h), s.ctas);
       blocks = Blocks(0, 1, 0, 1);
       if (sq.x >= 0) {
-        const int4 gr = __ldcg(s.group + sq.x);
+        if (!early) gr = __ldcg(s.group + sq.x);
         const int tiles = gr.x, rows = gr.z - gr.y;
         chunk = (r - gr.y) / two;
         chunks = (rows + two - 1) / two;

@@ -748,7 +748,7 @@ def kv16_shared_decode_attention(cache: KV16Cache, q: torch.Tensor, group: torch
     """kv16_decode_attention of sequences that share prefixes: sequences group[i]
     .. group[i+1] - 1 have their first prefix[i] tokens in common, whose whole
     pages are read once for all of them, from the first one's place in the cache.
-    group int32 [n + 1], prefix int32 [n]."""""
+    group int32 [n + 1], prefix int32 [n]."""
     qp, qs, _, Hq = cache._rows(q, None, cache.B)
     w, wb = _bytes(workspace, cache)
     n = prefix.numel()
@@ -770,7 +770,7 @@ def kv16_shared_attention(cache: KV16Cache, q: torch.Tensor, start: torch.Tensor
                           window: int = 0, n_sink: int = 0, lse: torch.Tensor | None = None,
                           stream=None):
     """kv16_attention of sequences that share prefixes (groups as for
-    kv16_shared_decode_attention)."""""
+    kv16_shared_decode_attention)."""
     qp, qs, total, Hq = cache._rows(q, None)
     w, wb = _bytes(workspace, cache)
     n = prefix.numel()
