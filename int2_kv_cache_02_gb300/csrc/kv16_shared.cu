@@ -453,14 +453,18 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
               : cudaLaunchKernelEx(&cfg, kv16_shared_join_kernel<T, false>, p, subs, 1);
 }
 
-// Is a CTA for each (sequence, KV head) the quicker way?  A wave of them takes 3.6 us
-// and 7.7 for each 1000 tokens of the longest, the line about 15 and 2 for each 100
-// rows.  Measured, that way and by the line (rows, tokens; us): 16 of 533 8.7 and
-// 15.8, 128 of 1021 11.8 and 18.5, 128 of 2001 19.1 and 19.2, 256 of 301 11.6 and
-// 21.4, 512 of 511 24.9 and 25.7, 1024 of 131 27 and 37, 1024 of 511 43 and 42.
-bool short_rows(const Kv16& c, const Kv16Query& q) {
+// Is a CTA for each (sequence, KV head) the quicker way?  A wave of them takes 3.4 us
+// and 7.2 for each 1000 tokens of the longest, the line about 15 and 3 for each 100
+// rows, the groups' among them.  Measured, that way and by the line (rows + rows of
+// groups, tokens; us): 16 + 8 of 533 8.7 and 15.8, 128 + 8 of 1021 11.8 and 18.5, 128 +
+// 8 of 2001 19.1 and 19.2, 512 + 8 of 511 24.9 and 25.7, 1024 + 8 of 511 43 and 42, 1024
+// + 8 of 131 27 and 37, 1024 + 512 of 321 40 and 63, 1024 + 256 of 1089 73 and 66, 2048
+// + 2048 of 309 82 and 159, 4096 + 256 of 577 197 and 159, 8192 + 1024 of 577 392 and
+// 374, 16384 + 8192 of 321 601 and 911.
+bool short_rows(const Kv16& c, const Kv16Query& q, const Kv16Groups& g) {
   const long long rows = (long long)c.B * c.Hkv, sms = sm_count();
-  return !q.start && (rows + sms - 1) / sms * (q.max_tok + 470LL) * 10 <= 19500 + 26 * rows;
+  return !q.start && (rows + sms - 1) / sms * (q.max_tok + 470LL) * 72 <=
+                         150000 + 300 * (rows + (long long)g.n * c.Hkv);
 }
 
 }  // namespace
@@ -489,7 +493,7 @@ cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Grou
   p.scale = std::max(std::fabs(q.scale_log2), std::numeric_limits<float>::denorm_min());
   p.wide = false;
   *launches = 0;
-  if (short_rows(c, q)) {
+  if (short_rows(c, q, g)) {
     *launches = 1;
     return launch_kv16_shared_short(c, q, g, out, s);
   }

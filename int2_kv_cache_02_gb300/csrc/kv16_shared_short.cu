@@ -4,7 +4,7 @@
 // of the CTA's warps; the line of key tiles (kv16_shared.cu) has two launches and
 // records between them.  Measured (GB300): 16 rows of 533 tokens 8.7 us (line 15.8),
 // 128 rows of 1021 tokens 11.8 us (18.5); with all a warp's pages one after another
-// 7.7 us for each 1000 tokens, so long rows are the line's, which cuts them up.
+// 7.2 us for each 1000 tokens, so long rows are the line's, which cuts them up.
 //
 // A warp takes every eighth page, through a slot of shared memory of its own; what
 // it does with a page is the decode's (kv16_page.cuh).
