@@ -623,9 +623,9 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * The work is cut evenly over the GPU, so where a row's sums are cut goes by the
  * whole batch's lengths: the same call gives the same bits, another batch may round
  * differently.
- * B <= 4096, n_groups <= 4096 and, with c = 2 * (128 / (Hq / Hkv)) query tokens in a
- * chunk, (2 * (B / c) + n_groups + B) * Hkv * (22 * ceil(max_tok / 128) + 48) < 2^31 -
- * 128 (else OSCAR_ERR_UNSUPPORTED).
+ * The limits of the decode call hold, n_groups <= 4096 and, with c = 2 * (128 / (Hq /
+ * Hkv)) query tokens in a chunk, (2 * (B / c) + n_groups + B) * Hkv * (22 * ceil(max_tok
+ * / 128) + 48) < 2^31 - 128 (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                                 long long q_stride, int Hq, const int32_t* group,
@@ -641,8 +641,9 @@ size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int H
  * of each: q, start, out, lse, positions and visibility as there, groups as
  * above (a prefix may reach into the new tokens).  workspace:
  * oscar_kv16_shared_attention_workspace_bytes of device memory (no
- * initialisation), asked for with this call's numbers.  The limits of the shared
- * decode hold with total in place of the first B, and total * Hq < 2^31 - 128.
+ * initialisation), asked for with this call's numbers.  B <= 4096, n_groups <= 4096,
+ * total * Hq <= 63000000, and the last limit above with total in place of the first B
+ * (else OSCAR_ERR_UNSUPPORTED).
  */
 oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16_t* q,
                                          long long q_stride, const int32_t* start, int total,

@@ -109,7 +109,7 @@ bool shared_size_ok(const oscar_kv16_cache* c, int Hq, int n_groups, int total, 
   const long long rows = (2 * (total / two) + n_groups + c->B) * c->Hkv;
   const long long places =
       kMostTileCost * ((std::min<long long>(max_tok, capacity(c)) + 127) / 128) + row_cost(3);
-  return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxTokens &&
+  return c->B <= kMaxDecodeBatch && n_groups <= kMaxGroups && (long long)total * Hq <= kMaxSharedRows &&
          rows <= kMaxTokens && rows * places <= kMaxTokens;
 }
 

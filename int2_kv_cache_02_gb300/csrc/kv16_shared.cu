@@ -130,6 +130,7 @@ kv16_shared_join_kernel(const __grid_constant__ AttnParams p, int subs, int batc
   // the lane's record of head 0 in 32-byte steps from the first of all, or none; from a
   // query to the next it moves by `step`, and by `fix` more into a chunk's second tile
   constexpr unsigned kNone = ~0u, kSteps = kPartFloats / 8;
+  static_assert((4 * kMaxSharedRows + kMaxCtas * 512LL) * kSteps < kNone, "records' places");
   const unsigned fix = (128 - p.tokens * g) * kSteps;
   unsigned off = kNone, step = 0;
   int in = -1;                      // 0 own, 1 prefix: which chunk the record's place goes by

@@ -242,6 +242,7 @@ struct Kv16Groups {
   int n;
 };
 constexpr int kMaxGroups = 4096;        // groups of one call
+constexpr long long kMaxSharedRows = 63000000;   // (query, head) rows: records are found in 32 bits
 // q.start nullptr: the decode (lse nullptr).
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
                                uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s);

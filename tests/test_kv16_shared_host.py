@@ -74,6 +74,9 @@ def test_shared_refusals(L):
     assert attention(L, c, out=apart, lse=P(FAKE)) == INVALID
     assert attention(L, c, total=0, q=None, out=None) == OK           # nothing to do
     assert attention(L, c, total=2**30) == UNSUPPORTED
+    # records that 32 bits do not number
+    assert attention(L, c, total=15750001, out=P(1 << 50), ws=None) == UNSUPPORTED
+    assert attention(L, c, total=15750000, out=P(1 << 50), ws=None) == WORKSPACE
     need = L.oscar_kv16_shared_attention_workspace_bytes(ctypes.byref(c), 4, 2, 4, 64, 0, 0)
     assert need > 0
     assert attention(L, c, out=apart, wb=need - 1) == attention(L, c, out=apart, ws=None) == WORKSPACE
