@@ -667,9 +667,13 @@ size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, in
  * Tokens are copied to the pages (contiguous: rows) that dst's block table
  * names, with their weights if dst has any (src then has them too).  No page
  * that the call writes may be one that it reads, except that a block whose page
- * is the parent's own is left as it is.  Shared pages share their weights.
+ * is the parent's own is left as it is.  Shared pages share their weights.  What a
+ * copy goes to has to be the sequence's own: a block that an earlier fork took over
+ * by reference gets another page first.
  * src and dst may be one cache: then a sequence that is forked from is not
  * forked to by the same call, unless from itself, which changes nothing.
+ * A host that keeps copies of dst's table or counts who names a page (an
+ * allocator) has to follow what share 1 writes before it goes by them again.
  * Otherwise their lengths and tables lie apart, and their keys, values and
  * weights too unless they are one pool's.  A parent, a length or a page out of
  * range is recorded in the status word; what cannot be copied stays as it was.

@@ -178,6 +178,19 @@ def _stream(stream) -> c_void_p:
     return c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _capturing(stream, device) -> bool:
+    """Is `stream` (None: the device's current one) being captured into a graph?"""
+    if device.type != "cuda":
+        return False
+    with torch.cuda.device(device):
+        if stream is None:
+            return torch.cuda.is_current_stream_capturing()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+
 def _check(st: int, where: str):
     if st != 0:
         raise OscarError(st, where)
@@ -257,18 +270,45 @@ class KVCache:
 class _PagePool:
     """Host-side page allocator of the paged caches: which pages are free, how
     many table entries name each of the others, and the block table's host copy
-    beside the device's (self.block_table)."""
+    beside the device's (self.block_table).  The table is written by these calls
+    and by kv16_fork (share); entries in tables that a caller makes over the same
+    pages are not counted."""
 
     def _init_pool(self, B: int, max_blocks: int, n_pages: int):
+        self._behind = self._replayed = False
         self._free = list(range(n_pages))
         self._named = [0] * n_pages
         self._table_host = [[-1] * max_blocks for _ in range(B)]
+
+    def _table_written(self, stream):
+        """A call that writes the table has been queued on the stream, or captured:
+        then any replay writes it again."""
+        self._behind = True
+        self._replayed |= _capturing(stream, self.block_table.device)
+
+    def _follow(self):
+        """Where a fork has written the table: waits for the device, and the host's
+        copy, the counts and the free pages go by what the table says now."""
+        if not self._behind:
+            return
+        table, n = self.block_table, len(self._named)
+        if table.is_cuda:
+            torch.cuda.synchronize(table.device)
+        rows, named = [[p if p < n else -1 for p in row] for row in table.tolist()], [0] * n
+        for row in rows:
+            for p in row:
+                if p >= 0:
+                    named[p] += 1
+        self._free = [p for p in self._free if not named[p]] + \
+            [p for p in range(n) if self._named[p] and not named[p]]
+        self._table_host, self._named, self._behind = rows, named, self._replayed
 
     def map_blocks(self, b: int, n_blocks: int, order=None):
         """Gives sequence b pages for its logical blocks 0..n_blocks-1 (those
         not mapped yet), taking free pages in `order` (a permutation of page
         ids, for tests) or in pool order.  A pool with too few of them gives
         none."""
+        self._follow()
         row = self._table_host[b]
         missing = [j for j in range(n_blocks) if row[j] < 0]
         if len(missing) > len(self._free):
@@ -285,6 +325,7 @@ class _PagePool:
         """Lets sequence b's logical blocks 0..n_blocks-1 be the pages of sequence
         parent's; those that b had there are given back.  Whole pages only: what
         is written to a shared page reaches every sequence that has it."""
+        self._follow()
         row, theirs = self._table_host[b], self._table_host[parent]
         if not 0 <= n_blocks <= len(row) or any(p < 0 for p in theirs[:n_blocks]):
             raise OscarError(1, f"{type(self).__name__}.share_blocks: sequence {parent} has no "
@@ -309,6 +350,7 @@ class _PagePool:
         allocator go by the new ids from here on.  Returns (moves, counts) for
         the copies (kv16_copy_pages, paged_copy_pages), which come next on the
         current stream."""
+        self._follow()
         table, n_pages = self.block_table, len(self._named)
         moves = torch.empty((n_pages // 2, 2), dtype=torch.int32, device=table.device)
         counts = torch.empty(2, dtype=torch.int32, device=table.device)
@@ -325,6 +367,7 @@ class _PagePool:
         return moves, counts
 
     def page_of(self, b: int, block: int) -> int:
+        self._follow()
         return self._table_host[b][block]
 
     def release_blocks(self, b: int, n_blocks: int = 0):
@@ -332,6 +375,7 @@ class _PagePool:
         blocks; those that no other sequence shares are free for any sequence
         from then on, so work that reads them has to be queued before what
         writes them."""
+        self._follow()
         row = self._table_host[b]
         for j in range(n_blocks, len(row)):
             self._give_back(row, j)
@@ -787,13 +831,22 @@ def kv16_fork(src: KV16Cache, dst: KV16Cache, parent: torch.Tensor, max_tok: int
     """Sequence b of dst becomes a copy of sequence parent[b] of src (int32
     [dst.B]; negative: stays as it is).  share: its whole pages are the parent's
     own (dst's table is written), the tokens behind them are copied; else every
-    token is copied, to the places that dst's table names.  max_tok bounds the
-    parents' lengths."""
+    token is copied, to the places that dst's table names, which are to be pages of
+    the sequence's own (release_blocks and map_blocks give those again).  max_tok
+    bounds the parents' lengths.
+
+    share and a dst with an allocator (PagedKV16Cache): the pages that dst's
+    sequences had in those places are given back and the parent's are counted, by
+    the next call of the allocator, which waits for the device.  After a fork that
+    was captured into a graph every such call waits.  Where src is not dst, src's
+    allocator does not know of dst's tables."""
     if dst.device != src.device:
         raise ValueError(f"source on {src.device}, destination on {dst.device}")
     _kv16_call(src, "oscar_kv16_fork", _lib.oscar_kv16_fork,
                (src._ref, dst._ref, dst._mine(parent, torch.int32, dst.B), int(share), max_tok),
                stream)
+    if share and isinstance(dst, _PagePool):
+        dst._table_written(stream)
 
 
 def page_compact_workspace_bytes(block_table: torch.Tensor, n_pages: int) -> int:
