@@ -560,7 +560,7 @@ template <class T, bool ACC>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                         int grid, size_t smem, cudaStream_t s) {
   const auto kernel = kv16_decode_kernel<T, ACC>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kernel, kSmemMost);
   if (e != cudaSuccess) return e;
   kernel<<<grid, NW * 32, smem, s>>>(mk, mv, p);
   return cudaGetLastError();
@@ -604,8 +604,7 @@ cudaError_t launch_kv16_decode(const Kv16& c, const Kv16Query& q, bool accumulat
                            : launch_main<Bf16, false>(mk, mv, p, grid, smem, s));
   *launches = 1;
   if (e != cudaSuccess || !accumulate) return e;
-  e = cudaFuncSetAttribute(kv16_decode_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)lines);
+  e = allow_shared(kv16_decode_weights_kernel, (kMaxDecodeBatch + 1) * 4);
   if (e != cudaSuccess) return e;
   const int wgrid = (int)std::max<long long>(
       1, std::min<long long>((pages + 31) / 32, 8LL * sm_count()));

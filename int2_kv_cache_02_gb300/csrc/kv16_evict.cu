@@ -327,8 +327,7 @@ cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int
   const int held = (most / kPage / cluster + 2) * kPage;
   const auto select = held <= kKeysMost ? kv16_select_kernel<true> : kv16_select_kernel<false>;
   const size_t smem = held <= kKeysMost ? (size_t)held * sizeof(uint32_t) : 0;
-  e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  e = allow_shared(select, kKeysMost * sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   if ((long long)rows * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};

@@ -219,8 +219,8 @@ cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long l
                                 int n_pages, int32_t* moves, int32_t* counts, void* ws,
                                 unsigned* status, cudaStream_t s) {
   const int words = compact_words(n_pages), smem = words * (int)sizeof(unsigned);
-  const cudaError_t e = cudaFuncSetAttribute(page_compact_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e =
+      allow_shared(page_compact_kernel, compact_words(kMaxPages) * sizeof(unsigned));
   if (e != cudaSuccess) return e;
   page_compact_kernel<<<kCluster, kThreads, smem, s>>>(table, new_table, entries, n_pages, words,
                                                        reinterpret_cast<int2*>(moves), counts,

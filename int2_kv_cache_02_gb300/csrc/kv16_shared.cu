@@ -422,10 +422,10 @@ cudaError_t launch(const AttnParams& p, int* launches, cudaStream_t s) {
   const auto kernel = kv16_attention_kernel<T, kLine>;
   constexpr int kStages = stages_of(kLine);
   constexpr int fixed = (2 + kStages) * kTileBytes + (int)sizeof(Smem<kLine>);
-  static_assert(fixed + (kMaxGroups + kMaxDecodeBatch + 1 + kThreads / 32) * 4 <= 227 * 1024,
-                "shared memory of a CTA");
+  constexpr int most = fixed + (kMaxGroups + kMaxDecodeBatch + 1 + kThreads / 32) * (int)sizeof(int);
+  static_assert(most <= 227 * 1024, "shared memory of a CTA");
   const int smem = fixed + (p.line.groups.n + p.c.B + 1 + kThreads / 32) * (int)sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared(kernel, most);
   if (e != cudaSuccess) return e;
   kernel<<<p.line.ctas, kThreads, smem, s>>>(mq, mk, mv, p);
   e = cudaGetLastError();

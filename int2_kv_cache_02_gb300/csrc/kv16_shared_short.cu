@@ -139,11 +139,11 @@ kv16_shared_short_kernel(const __grid_constant__ CUtensorMap map_k,
 template <class T>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const ShortParams& p,
                    cudaStream_t s) {
-  const int smem = 1024 + NW * kSlotBytes + NW * p.g * kORow * (int)sizeof(float);
-  static_assert(1024 + NW * kSlotBytes + NW * kMaxGroup * kORow * 4 <= 226 * 1024, "shared memory");
+  constexpr int fixed = 1024 + NW * kSlotBytes, head = NW * kORow * (int)sizeof(float);
+  static_assert(fixed + kMaxGroup * head <= 226 * 1024, "shared memory");
+  const int smem = fixed + p.g * head;
   const auto kernel = kv16_shared_short_kernel<T>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared(kernel, fixed + kMaxGroup * head);
   if (e != cudaSuccess) return e;
   kernel<<<p.c.B * p.c.Hkv, NW * 32, smem, s>>>(mk, mv, p);
   return cudaGetLastError();

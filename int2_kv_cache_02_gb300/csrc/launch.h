@@ -234,6 +234,13 @@ cudaError_t launch_kv16_accumulate(const Kv16& c, const Kv16Query& q, const floa
 cudaError_t launch_kv16_evict(const Kv16& src, const Kv16& dst, int max_tok, int keep_first,
                               int keep_recent, int keep_top, int32_t* kept, void* ws,
                               cudaStream_t s);
+// Lets launches of a kernel ask for up to `most` bytes of dynamic shared memory.  The
+// limit is the process's, so it does not go by a call's own size: a smaller call of
+// another host thread would lower it between this and the launch.
+template <class K>
+cudaError_t allow_shared(K kernel, size_t most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
 // Groups of sequences with a common prefix: group i is the sequences
 // [group[i], group[i+1]), whose first prefix[i] tokens are the same.
 struct Kv16Groups {

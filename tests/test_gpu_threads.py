@@ -1,6 +1,10 @@
 """The 16-bit cache's calls from host threads: one that has never used the GPU,
-and two at once."""
+and several at once."""
+import ctypes
+import os
+import subprocess
 import threading
+from ctypes import c_int, c_size_t, c_void_p
 
 import pytest
 import torch
@@ -10,6 +14,7 @@ from tests._shared_ref import bits, i32
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -56,7 +61,7 @@ def calls_of(L, case, cache, Hq, most):
         L.page_compact_workspace_bytes(cache.block_table, cache.k.shape[0]))]
     row = case.normal(B, case.Hkv).cuda()
     kept = torch.empty((B, case.Hkv, 3), dtype=torch.int32, device="cuda")
-    to = L.KV16Cache.contiguous(B, case.Hkv, most, weights=True)
+    to = L.KV16Cache.contiguous(B, case.Hkv, cache.capacity, weights=True)
     few = L.KV16Cache.contiguous(B, case.Hkv, 3)
     table, moves, counts = torch.empty_like(cache.block_table), i32([[0, 0]] * (cache.k.shape[0] // 2)), i32([0, 0])
     pairs, n_pairs = i32([[0, 0]]), i32([0])
@@ -94,3 +99,132 @@ def test_the_first_call_of_a_thread(L, name):
     assert L.device_status() == 0
     for x, y in zip(outs, want):
         assert torch.equal(bits(x), y)
+
+
+# Host threads in calls at the same time, a large one and small ones, without the
+# interpreter's lock between them.
+HARNESS = r"""
+#include <atomic>
+#include <thread>
+#include "oscar.h"
+struct Call {
+  int kind, large;
+  const oscar_kv16_cache* c;
+  const uint16_t* q;
+  int Hq;
+  const int32_t *group, *prefix;
+  int max_tok;
+  uint16_t* out;
+  const int32_t* table;
+  int32_t *new_table, *moves, *counts;
+  int B, blocks, n_pages;
+  const oscar_kv16_cache* to;
+  void* ws;
+  size_t ws_bytes;
+  void* stream;
+};
+using Compact = decltype(&oscar_page_compact);
+using Shared = decltype(&oscar_kv16_shared_decode_attention);
+using Decode = decltype(&oscar_kv16_decode_attention);
+using Evict = decltype(&oscar_kv16_evict);
+static int call(const void* const* f, const Call& x) {
+  switch (x.kind) {
+    case 0: return ((Compact)f[0])(x.table, x.new_table, x.B, x.blocks, x.n_pages, x.moves, x.counts, x.ws,
+                                   x.ws_bytes, x.stream);
+    case 1: return ((Shared)f[1])(x.c, x.q, (long long)x.Hq * 128, x.Hq, x.group, x.prefix, 1, 0.1f, x.max_tok, 0, 0,
+                                  x.out, x.ws, x.ws_bytes, x.stream);
+    case 2: return ((Evict)f[3])(x.c, x.to, x.max_tok, 1, 1, 1, nullptr, x.ws, x.ws_bytes, x.stream);
+    default: return ((Decode)f[2])(x.c, x.q, (long long)x.Hq * 128, x.Hq, 0.1f, x.max_tok, 0, 0, x.kind == 4, x.out,
+                                   x.ws, x.ws_bytes, x.stream);
+  }
+}
+extern "C" int hammer(const void* const* f, const Call* calls, int n, int times) {
+  std::atomic<int> failed{0}, ready{0};
+  auto run = [&](const Call& x) {
+    for (++ready; ready < n;) {}
+    for (int i = 0; i < times; ++i) failed += call(f, x) != 0;
+  };
+  std::thread t[8];
+  for (int i = 0; i < n; ++i) t[i] = std::thread(run, std::cref(calls[i]));
+  for (int i = 0; i < n; ++i) t[i].join();
+  return failed;
+}
+"""
+FIELDS = [("kind", c_int), ("large", c_int), ("c", c_void_p), ("q", c_void_p), ("Hq", c_int), ("group", c_void_p),
+          ("prefix", c_void_p), ("max_tok", c_int), ("out", c_void_p), ("table", c_void_p), ("new_table", c_void_p),
+          ("moves", c_void_p), ("counts", c_void_p), ("B", c_int), ("blocks", c_int), ("n_pages", c_int),
+          ("to", c_void_p), ("ws", c_void_p), ("ws_bytes", c_size_t), ("stream", c_void_p)]
+
+
+class Call(ctypes.Structure):
+    _fields_ = FIELDS
+
+
+@pytest.fixture(scope="module")
+def hammer(tmp_path_factory):
+    d = tmp_path_factory.mktemp("hammer")
+    src, so = d / "hammer.cpp", d / "hammer.so"
+    src.write_text(HARNESS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"),
+                    str(src), "-o", str(so)], check=True)
+    return ctypes.CDLL(str(so)).hammer
+
+
+KINDS = {"compact": 0, "line": 1, "short": 1, "evict": 2, "decode": 3, "weights": 4}
+
+
+def sized(L, what, large, keep):
+    """A call whose blocks ask for much or for little shared memory, and its outputs."""
+    x = Call(kind=KINDS[what], large=large)
+    if what == "compact":
+        x.B, x.blocks, x.n_pages = 1, 4, 8000000 if large else 16
+        table, moves, counts = i32([[5, 1, -1, 7]]), torch.empty(x.n_pages, dtype=torch.int32, device="cuda"), i32([0, 0])
+        new = torch.empty_like(table)
+        ws = L.alloc_workspace(L.page_compact_workspace_bytes(table, x.n_pages))
+        x.table, x.new_table, x.moves, x.counts = (t.data_ptr() for t in (table, new, moves, counts))
+        outs = [new, counts]
+        keep += [table, moves]
+    else:
+        B = 1500 if large and what in ("line", "decode", "weights") else 2
+        x.Hq = 16 if large and what == "short" else 1
+        case = R.Case([40] * B, 1, weights=True, slack=700 if large and what == "evict" else 1)
+        cache = case.cache(L)
+        x.max_tok = 1 << 20 if what == "line" else cache.capacity
+        q, group, prefix = case.normal(B, x.Hq).cuda(), i32([0, B]), i32([32])
+        out, to = torch.empty_like(q), L.KV16Cache.contiguous(B, 1, 3)
+        if what == "evict":
+            n = L.kv16_evict_workspace_bytes(cache, x.max_tok, 1, 1, 1)
+        elif what in ("line", "short"):
+            n = L.kv16_shared_decode_workspace_bytes(cache, x.Hq, 1, x.max_tok)
+        else:
+            n = L.kv16_decode_workspace_bytes(cache, x.Hq, x.max_tok, accumulate=what == "weights")
+        ws = L.alloc_workspace(n)
+        x.c, x.to = ctypes.addressof(cache.struct), ctypes.addressof(to.struct)
+        x.q, x.group, x.prefix, x.out = (t.data_ptr() for t in (q, group, prefix, out))
+        outs = [to.k, to.n_tok] if what == "evict" else [out]
+        keep += [cache, q, group, prefix, to]
+    stream = torch.cuda.Stream()
+    x.ws, x.ws_bytes, x.stream = ws.data_ptr(), ws.nbytes, stream.cuda_stream
+    keep += [ws, stream]
+    return x, outs
+
+
+@pytest.mark.parametrize("what", KINDS)
+def test_calls_of_unequal_size_at_once(L, hammer, what):
+    """A small call between a large one's preparation and its launch does not fail it."""
+    lib, keep = L.library(), []
+    f = (c_void_p * 4)(*(ctypes.cast(getattr(lib, "oscar_" + n), c_void_p) for n in (
+        "page_compact", "kv16_shared_decode_attention", "kv16_decode_attention", "kv16_evict")))
+    calls = [sized(L, what, large, keep) for large in (True, False, False)]
+    torch.cuda.synchronize()
+    want = []
+    for x, outs in calls:
+        assert hammer(f, (Call * 1)(x), 1, 1) == 0
+        torch.cuda.synchronize()
+        want.append([bits(t).clone() for t in outs])
+    assert hammer(f, (Call * 3)(*(x for x, _ in calls)), 3, 2000) == 0
+    torch.cuda.synchronize()
+    assert L.device_status() == 0
+    for (_, outs), w in zip(calls, want):
+        for t, y in zip(outs, w):
+            assert torch.equal(bits(t), y)
