@@ -272,7 +272,7 @@ class _PagePool:
     many table entries name each of the others, and the block table's host copy
     beside the device's (self.block_table).  The table is written by these calls
     and by kv16_fork (share); entries in tables that a caller makes over the same
-    pages are not counted."""
+    pages are not counted.  Not while the current stream is captured into a graph."""
 
     def _init_pool(self, B: int, max_blocks: int, n_pages: int):
         self._behind = self._replayed = False
@@ -286,9 +286,13 @@ class _PagePool:
         self._behind = True
         self._replayed |= _capturing(stream, self.block_table.device)
 
-    def _follow(self):
+    def _follow(self, changes: bool = True):
         """Where a fork has written the table: waits for the device, and the host's
-        copy, the counts and the free pages go by what the table says now."""
+        copy, the counts and the free pages go by what the table says now.  `changes`:
+        of the calls that change them, which a replayed graph would not repeat."""
+        if (changes or self._behind) and _capturing(None, self.block_table.device):
+            raise RuntimeError(f"{type(self).__name__}: the page allocator works on the host, "
+                               "which a captured graph does not")
         if not self._behind:
             return
         table, n = self.block_table, len(self._named)
@@ -367,7 +371,7 @@ class _PagePool:
         return moves, counts
 
     def page_of(self, b: int, block: int) -> int:
-        self._follow()
+        self._follow(changes=False)
         return self._table_host[b][block]
 
     def release_blocks(self, b: int, n_blocks: int = 0):

@@ -106,3 +106,18 @@ def test_a_captured_fork(L):
         assert_tokens(pool, case, 2, of, n)
         assert pool._table_host[2][:n // 32] == pool._table_host[of][:n // 32]
     assert L.device_status() == 0
+
+
+@pytest.mark.parametrize("call", [lambda p: p.compact(), lambda p: p.map_blocks(0, 6), lambda p: p.release_blocks(0, 2),
+                                  lambda p: p.share_blocks(1, 0, 2)])
+def test_not_in_a_captured_graph(L, call):
+    """What a graph would replay on the device alone is refused, and changes nothing."""
+    _, pool = filled(L, [150, 100], 2)
+    before = ([list(r) for r in pool._table_host], list(pool._free), list(pool._named))
+    with pytest.raises(RuntimeError, match="captured graph"), torch.cuda.graph(torch.cuda.CUDAGraph()):
+        call(pool)
+    torch.cuda.synchronize()
+    assert before == (pool._table_host, pool._free, pool._named)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        assert pool.page_of(0, 0) == before[0][0][0]
+    agrees(pool)
