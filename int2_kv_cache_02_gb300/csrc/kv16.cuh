@@ -60,9 +60,9 @@ __device__ __forceinline__ int ragged_sequence(const int32_t* start, int B, int 
 // the lane's four) asks for is NaN: nothing changes it any more.  The block that
 // it ended with, or -1.
 constexpr int kRowTokens = 8;    // tokens whose loads are in flight together
-template <class T>
+template <class T, class S>
 __device__ __forceinline__ int kv16_warp_row(const Kv16& c, const uint16_t* q, int b, int h,
-                                             int at, const Span& sp, int i0, int i1, int window,
+                                             int at, const S& sp, int i0, int i1, int window,
                                              int n_sink, float scale_log2, unsigned open,
                                              float& m, float& l, float (&o)[4]) {
   const int lane = threadIdx.x & 31;

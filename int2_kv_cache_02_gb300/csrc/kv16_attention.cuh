@@ -134,7 +134,7 @@ struct Item {
   int b, h, split, n;
   int row0, nrow;      // first row of q, tokens (of one or two tiles)
   int at0;             // position of the first token
-  Span sp;
+  WholeSpan sp;
   int k0, k1;          // key tiles
   int cnt[2];          // of them, for each query tile: k0 .. k0 + cnt - 1
   bool clear;          // the last one's last page is the sequence's and lacks tokens
@@ -143,18 +143,21 @@ struct Item {
 struct LineItem : Item {
   int end;             // the sequence behind a group's last (b is its first), -1: b's own
   int first;           // kPair, or the query tile that has the first tile of keys
+  int s0;              // of the span
 };
 template <int PART>
 struct ItemOf {
   using type = Item;
   static __device__ __forceinline__ int end(const Item*) { return -1; }
   static __device__ __forceinline__ int first(const Item*) { return kPair; }
+  static __device__ __forceinline__ const WholeSpan& span(const Item* it) { return it->sp; }
 };
 template <>
 struct ItemOf<kLine> {
   using type = LineItem;
   static __device__ __forceinline__ int end(const LineItem* it) { return it->end; }
   static __device__ __forceinline__ int first(const LineItem* it) { return it->first; }
+  static __device__ __forceinline__ Span span(const LineItem* it) { return Span(it->sp, it->s0); }
 };
 
 template <int PART>
@@ -202,7 +205,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
   it.row0 = r0 + q0;
   it.nrow = min(two, nq - q0);
   it.at0 = it.n - nq + q0;
-  it.sp = Span(it.at0, it.at0 + it.nrow - 1, p.q.window, p.q.n_sink);
+  it.sp = WholeSpan(it.at0, it.at0 + it.nrow - 1, p.q.window, p.q.n_sink);
   const int kt = (it.sp.blocks + kKeyPages - 1) / kKeyPages;
   it.k0 = (int)((long long)kt * it.split / p.splits);
   it.k1 = (int)((long long)kt * (it.split + 1) / p.splits);
@@ -211,7 +214,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int x, Item& it) 
   if (it.nrow > p.tokens) {
     // the first tile's keys end before the second's
     it.cnt[1] = it.cnt[0];
-    const int blocks = Span(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink).blocks;
+    const int blocks = WholeSpan(it.at0, it.at0 + p.tokens - 1, p.q.window, p.q.n_sink).blocks;
     it.cnt[0] = min(it.k1, max(it.k0, (blocks + kKeyPages - 1) / kKeyPages)) - it.k0;
   }
   it.clear = it.k1 > it.k0 && it.k1 == kt && it.n % kPage != 0 &&
@@ -262,7 +265,7 @@ __device__ __forceinline__ GroupEntry group_entry(const AttnParams& p, int i, bo
       x.r0 = x.r1 = 0;
     }
   }
-  x.sp.sink_blocks = x.sp.w0 = 0;
+  x.sp.sink_blocks = x.sp.w0 = x.sp.s0 = 0;
   x.sp.blocks = x.r1 > x.r0 ? x.s.blocks : 0;
   if (p.q.window > 0 && x.sp.blocks > 0) {
     const Reach y = reach(x.s);
@@ -438,6 +441,7 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.row0 = y.r0 + chunk * two;
     it.nrow = min(two, y.r1 - it.row0);
     it.sp = y.sp;
+    it.s0 = 0;
     it.split = from <= row_cost(kind) ? 0 : from > p0 ? 1 : 2;  // where the records go
     runs = p.line.prefix_runs;
   } else {
@@ -478,7 +482,9 @@ __device__ __forceinline__ int find_piece(const AttnParams& p, const int* first,
     it.row0 = y.r0 + chunk * two;
     it.nrow = min(two, y.nq - chunk * two);
     it.at0 = y.at0 + chunk * two;
-    it.sp = y.span(p, chunk * two, it.nrow);
+    const Span sp = y.span(p, chunk * two, it.nrow);
+    it.sp = sp;
+    it.s0 = sp.s0;
     from = max(in, 0);
     kind = y.kind(p, chunk);
     all = key_tiles(it.sp.blocks);
@@ -569,9 +575,9 @@ __device__ __forceinline__ float gather_open(float x, float so_far) {
 // written: its open channels again, from the tokens alone that it sees.  *met is
 // the block in which such a row of this warp has last met its NaN: the others
 // most likely meet it there too, so they look there first.
-template <class T, int PART>
+template <class T, int PART, class S>
 __device__ __forceinline__ void redo_row(const AttnParams& p, int b, int h, int split, int k0,
-                                         int k1, const Span& sp, long long row, int at, int* met,
+                                         int k1, const S& sp, long long row, int at, int* met,
                                          int cut_row, int first_tile, int w) {
   const int lane = threadIdx.x & 31;
   const bool record = PART != kWhole || p.splits > 1;
@@ -816,6 +822,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           __syncwarp();
           ++q_used[w];
         }
+        const auto& sp = ItemOf<PART>::span(&it);
         int row = none;
         auto ask = [&](int kv, unsigned st, uint64_t* bar) {
           uint8_t* dst = ring + st * kTileBytes;
@@ -829,8 +836,8 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         };
         for (int k = it.k0; k < it.k1 && ok; ++k) {
           row = none;
-          if (lane < kKeyPages && k * kKeyPages + lane < it.sp.blocks) {
-            row = kv16_block_row(p.c, it.b, it.h, it.sp.block(k * kKeyPages + lane));
+          if (lane < kKeyPages && k * kKeyPages + lane < sp.blocks) {
+            row = kv16_block_row(p.c, it.b, it.h, sp.block(k * kKeyPages + lane));
             if (row < 0) {
               record_error(p.c.status, kDevErrBadPaged);
               row = none;
@@ -855,9 +862,9 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
           ask(1, st, &sm.tail);
           ++tails;
           kept = used++;
-          const int last = it.sp.blocks - 1;
+          const int last = sp.blocks - 1;
           kept_page = last - (it.k1 - 1) * kKeyPages;
-          kept_at = it.n - it.sp.block(last) * kPage;
+          kept_at = it.n - sp.block(last) * kPage;
           if (PART == kWhole) pass_on(kept_page, kept_at);
         }
       }
@@ -1046,7 +1053,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
       const int b = ip->b, h = ip->h, split = ip->split, k0 = ip->k0, k1 = ip->k1;
       const int seq_end = ItemOf<PART>::end(ip);
       const int at_first = ip->at0 + shift, row_first = ip->row0 + shift;
-      const Span sp = ip->sp;
+      const auto sp = ItemOf<PART>::span(ip);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.i_empty[ni % kItems]);
       if (ntok <= 0) continue;
