@@ -751,6 +751,18 @@ oscar_status oscar_selftest_kv16_decode_timeout(const oscar_kv16_cache* c, const
                                                 int Hq, int max_tok, uint16_t* out,
                                                 void* workspace, size_t ws_bytes, void* stream);
 
+/* Self-test of the waits of the attention over shared prefixes:
+ * oscar_kv16_shared_decode_attention (dense q, no window) whose copies end early.
+ * Where a row is one block's, every wait for a copy gives up at once; else a block's
+ * copies end after `items` pieces of work (0, 1, ..), and what waits for the next one
+ * gives up at its usual limit, two seconds, and takes the rest of the block along.
+ * out is unspecified; the status word reports the time-out, if a block had more pieces. */
+oscar_status oscar_selftest_kv16_shared_timeout(const oscar_kv16_cache* c, const uint16_t* q,
+                                                int Hq, const int32_t* group,
+                                                const int32_t* prefix, int n_groups, int max_tok,
+                                                int items, uint16_t* out, void* workspace,
+                                                size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* oscar_status_string(oscar_status s);
 

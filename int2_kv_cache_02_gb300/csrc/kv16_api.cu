@@ -166,7 +166,7 @@ oscar_status shared(const oscar_kv16_cache* c, const uint16_t* q, long long q_st
                     const int32_t* start, int total, int Hq, const int32_t* group,
                     const int32_t* prefix, int n_groups, float softmax_scale, int max_tok,
                     int window, int n_sink, uint16_t* out, float* lse, void* workspace,
-                    size_t ws_bytes, void* stream) {
+                    size_t ws_bytes, unsigned copied, void* stream) {
   if (total < 0 || !groups_ok(group, prefix, n_groups) ||
       !window_ok(softmax_scale, max_tok, window, n_sink))
     return OSCAR_ERR_INVALID_ARG;
@@ -190,9 +190,21 @@ oscar_status shared(const oscar_kv16_cache* c, const uint16_t* q, long long q_st
   int launches = 0;
   const cudaError_t e = launch_kv16_shared(
       v, query(q, q_stride, start, total, Hq, softmax_scale, max_tok, window, n_sink),
-      Kv16Groups{group, prefix, n_groups}, out, lse, workspace, &launches, as_stream(stream));
+      Kv16Groups{group, prefix, n_groups}, out, lse, workspace, copied, &launches,
+      as_stream(stream));
   count_launches(launches);
   return from_cuda(e);
+}
+
+oscar_status shared_decode(const oscar_kv16_cache* c, const uint16_t* q, long long q_stride,
+                           int Hq, const int32_t* group, const int32_t* prefix, int n_groups,
+                           float softmax_scale, int max_tok, int window, int n_sink, uint16_t* out,
+                           void* workspace, size_t ws_bytes, unsigned copied, void* stream) {
+  const oscar_status st = check(c);
+  if (st != OSCAR_OK) return st;
+  if (max_tok >= 0 && !decode_size_ok(c, max_tok)) return OSCAR_ERR_UNSUPPORTED;
+  return shared(c, q, q_stride, nullptr, c->B, Hq, group, prefix, n_groups, softmax_scale, max_tok,
+                window, n_sink, out, nullptr, workspace, ws_bytes, copied, stream);
 }
 
 oscar_status decode(const oscar_kv16_cache* c, const uint16_t* q, long long q_stride, int Hq,
@@ -403,11 +415,17 @@ oscar_status oscar_kv16_shared_decode_attention(const oscar_kv16_cache* c, const
                                                 float softmax_scale, int max_tok, int window,
                                                 int n_sink, uint16_t* out, void* workspace,
                                                 size_t ws_bytes, void* stream) {
-  const oscar_status st = check(c);
-  if (st != OSCAR_OK) return st;
-  if (max_tok >= 0 && !decode_size_ok(c, max_tok)) return OSCAR_ERR_UNSUPPORTED;
-  return shared(c, q, q_stride, nullptr, c->B, Hq, group, prefix, n_groups, softmax_scale, max_tok,
-                window, n_sink, out, nullptr, workspace, ws_bytes, stream);
+  return shared_decode(c, q, q_stride, Hq, group, prefix, n_groups, softmax_scale, max_tok, window,
+                       n_sink, out, workspace, ws_bytes, kAllItems, stream);
+}
+
+oscar_status oscar_selftest_kv16_shared_timeout(const oscar_kv16_cache* c, const uint16_t* q,
+                                                int Hq, const int32_t* group, const int32_t* prefix,
+                                                int n_groups, int max_tok, int items, uint16_t* out,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+  if (items < 0) return OSCAR_ERR_INVALID_ARG;
+  return shared_decode(c, q, (long long)Hq * kD, Hq, group, prefix, n_groups, 1.0f, max_tok, 0, 0,
+                       out, workspace, ws_bytes, (unsigned)items, stream);
 }
 
 size_t oscar_kv16_shared_attention_workspace_bytes(const oscar_kv16_cache* c, int Hq, int n_groups,
@@ -428,7 +446,7 @@ oscar_status oscar_kv16_shared_attention(const oscar_kv16_cache* c, const uint16
   if (st != OSCAR_OK) return st;
   if (!start) return OSCAR_ERR_INVALID_ARG;
   return shared(c, q, q_stride, start, total, Hq, group, prefix, n_groups, softmax_scale, max_tok,
-                window, n_sink, out, lse, workspace, ws_bytes, stream);
+                window, n_sink, out, lse, workspace, ws_bytes, kAllItems, stream);
 }
 
 oscar_status oscar_kv16_fork(const oscar_kv16_cache* src, const oscar_kv16_cache* dst,

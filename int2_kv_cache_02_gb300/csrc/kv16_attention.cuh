@@ -799,7 +799,7 @@ kv16_attention_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         return ok && tc5_wait(bar, parity, state);
       };
-      for (unsigned ni = 0; ok; ++ni) {
+      for (unsigned ni = 0; ok && (PART != kLine || ni < p.line.copied); ++ni) {
         if (!(ok = settled_wait(&sm.i_full[ni % kItems], (ni / kItems) & 1))) break;
         const It* ip = &sm.item[ni % kItems];
         if (ip->stop) break;

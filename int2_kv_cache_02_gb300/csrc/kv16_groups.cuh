@@ -58,6 +58,7 @@ struct SharedParts {
   int* own_runs;
   int ctas;
   int tokens, g;            // tokens of a query tile, heads of a group
+  unsigned copied;          // items of a CTA that are copied: all but in a self-test
 };
 
 // ragged_sequence by a warp: 32 numbers of `start` at a time, not one.

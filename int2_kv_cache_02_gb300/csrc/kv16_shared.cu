@@ -477,7 +477,8 @@ size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int 
 }
 
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
-                               uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s) {
+                               uint16_t* out, float* lse, void* ws, unsigned copied, int* launches,
+                               cudaStream_t s) {
   size_t n;
   AttnParams p;
   p.c = c;
@@ -486,6 +487,7 @@ cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Grou
   p.lse = lse;
   p.part = nullptr;
   p.line = layout(c, q.Hq, g, q.total, q.max_tok, static_cast<uint8_t*>(ws), &n);
+  p.line.copied = copied;
   p.g = p.line.g;
   p.tokens = p.line.tokens;
   p.tiles = 0;
@@ -496,7 +498,7 @@ cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Grou
   *launches = 0;
   if (short_rows(c, q, g)) {
     *launches = 1;
-    return launch_kv16_shared_short(c, q, g, out, s);
+    return launch_kv16_shared_short(c, q, g, out, copied == kAllItems ? kTcWaitLimit : 0u, s);
   }
   return c.half ? launch<Fp16>(p, launches, s) : launch<Bf16>(p, launches, s);
 }

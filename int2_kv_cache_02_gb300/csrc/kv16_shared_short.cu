@@ -25,6 +25,7 @@ struct ShortParams {
   Kv16Groups groups;
   uint16_t* out;
   int g;
+  unsigned wait_limit;
 };
 
 template <class T>
@@ -80,7 +81,7 @@ kv16_shared_short_kernel(const __grid_constant__ CUtensorMap map_k,
   bool gave_up = false;
   for (int x = warp; x < sp.blocks; x += NW) {
     const int next = place(x + NW);        // (its load passes under the wait)
-    gave_up = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp], phase, kTcWaitLimit));
+    gave_up = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[warp], phase, p.wait_limit));
     if (gave_up) {
       if (lane == 0) record_error(p.c.status, kDevErrWaitTimeout);
       break;
@@ -152,8 +153,8 @@ cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const ShortPara
 }  // namespace
 
 cudaError_t launch_kv16_shared_short(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups,
-                                     uint16_t* out, cudaStream_t s) {
-  const ShortParams p{c, q, groups, out, q.Hq / c.Hkv};
+                                     uint16_t* out, unsigned wait_limit, cudaStream_t s) {
+  const ShortParams p{c, q, groups, out, q.Hq / c.Hkv, wait_limit};
   CUtensorMap mk, mv;
   if (!kv16_row_map(&mk, c, c.k) || !kv16_row_map(&mv, c, c.v)) return cudaErrorNotSupported;
   return c.half ? launch<Fp16>(mk, mv, p, s) : launch<Bf16>(mk, mv, p, s);

@@ -250,13 +250,16 @@ struct Kv16Groups {
 };
 constexpr int kMaxGroups = 4096;        // groups of one call
 constexpr long long kMaxSharedRows = 63000000;   // (query, head) rows: records are found in 32 bits
-// q.start nullptr: the decode (lse nullptr).
+// q.start nullptr: the decode (lse nullptr).  copied: kAllItems, or how many work items
+// of a CTA get their copies (a self-test of the waits behind them).
+constexpr unsigned kAllItems = ~0u;
 cudaError_t launch_kv16_shared(const Kv16& c, const Kv16Query& q, const Kv16Groups& g,
-                               uint16_t* out, float* lse, void* ws, int* launches, cudaStream_t s);
+                               uint16_t* out, float* lse, void* ws, unsigned copied, int* launches,
+                               cudaStream_t s);
 size_t kv16_shared_ws_bytes(const Kv16& c, int Hq, int n_groups, int total, int max_tok);
 // A CTA for each (sequence, KV head): q.start is nullptr.
 cudaError_t launch_kv16_shared_short(const Kv16& c, const Kv16Query& q, const Kv16Groups& groups,
-                                     uint16_t* out, cudaStream_t s);
+                                     uint16_t* out, unsigned wait_limit, cudaStream_t s);
 cudaError_t launch_kv16_fork(const Kv16& src, const Kv16& dst, const int32_t* parent, bool share,
                              bool same, int max_tok, cudaStream_t s);
 cudaError_t launch_page_compact(const int32_t* table, int32_t* new_table, long long entries,

@@ -145,6 +145,9 @@ def _load() -> ctypes.CDLL:
         "oscar_selftest_tc_wait_timeout": (c_int, [c_uint, c_void_p, c_void_p]),
         "oscar_selftest_kv16_decode_timeout": (c_int, [P16, c_void_p, c_int, c_int, c_void_p,
                                                        c_void_p, c_size_t, c_void_p]),
+        "oscar_selftest_kv16_shared_timeout": (c_int, [P16, c_void_p, c_int, c_void_p, c_void_p,
+                                                       c_int, c_int, c_int, c_void_p, c_void_p,
+                                                       c_size_t, c_void_p]),
         "oscar_status_string": (ctypes.c_char_p, [c_int]),
         "oscar_kernel_launches": (c_ulonglong, []),
     }
@@ -935,6 +938,23 @@ def selftest_kv16_decode_timeout(cache: KV16Cache, q: torch.Tensor, max_tok: int
     _kv16_call(cache, "oscar_selftest_kv16_decode_timeout", _lib.oscar_selftest_kv16_decode_timeout,
                (cache._ref, qp, Hq, max_tok, cache._mine(out, cache.dtype, cache.B * Hq * D), w, wb),
                stream)
+
+
+def selftest_kv16_shared_timeout(cache: KV16Cache, q: torch.Tensor, group: torch.Tensor,
+                                 prefix: torch.Tensor, max_tok: int, out: torch.Tensor,
+                                 workspace: torch.Tensor, items: int = 0, stream=None):
+    """kv16_shared_decode_attention (dense q, no window) whose copies end early: what
+    waits for them gives up (at once where a row is one block's, else after two
+    seconds, behind `items` pieces of work), the status word reports it."""
+    qp, _, _, Hq = cache._rows(q, None, cache.B)
+    if not q.is_contiguous():
+        raise ValueError("expected dense queries")
+    w, wb = _bytes(workspace, cache)
+    n = prefix.numel()
+    _kv16_call(cache, "oscar_selftest_kv16_shared_timeout", _lib.oscar_selftest_kv16_shared_timeout,
+               (cache._ref, qp, Hq, cache._mine(group, torch.int32, n + 1),
+                cache._mine(prefix, torch.int32, n), n, max_tok, items,
+                cache._mine(out, cache.dtype, cache.B * Hq * D), w, wb), stream)
 
 
 def device_status(stream=None) -> int:
