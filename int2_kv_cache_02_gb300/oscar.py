@@ -313,8 +313,8 @@ class _PagePool:
     def map_blocks(self, b: int, n_blocks: int, order=None):
         """Gives sequence b pages for its logical blocks 0..n_blocks-1 (those
         not mapped yet), taking free pages in `order` (a permutation of page
-        ids, for tests) or in pool order.  A pool with too few of them gives
-        none."""
+        ids, for tests) or those that have been free longest first.  A pool with
+        too few of them gives none."""
         self._follow()
         row = self._table_host[b]
         missing = [j for j in range(n_blocks) if row[j] < 0]
@@ -846,7 +846,12 @@ def kv16_fork(src: KV16Cache, dst: KV16Cache, parent: torch.Tensor, max_tok: int
     sequences had in those places are given back and the parent's are counted, by
     the next call of the allocator, which waits for the device.  After a fork that
     was captured into a graph every such call waits.  Where src is not dst, src's
-    allocator does not know of dst's tables."""
+    allocator does not know of dst's tables.
+
+    Sequences that continue one another (a step of a beam search) are forked from a
+    KV16Cache over the same k and v with copies of n_tok and block_table, once every
+    sequence of dst has given its last page back and then got one that was free before
+    (release_blocks of all, then map_blocks, in a pool with so many pages free)."""
     if dst.device != src.device:
         raise ValueError(f"source on {src.device}, destination on {dst.device}")
     _kv16_call(src, "oscar_kv16_fork", _lib.oscar_kv16_fork,

@@ -121,3 +121,28 @@ def test_not_in_a_captured_graph(L, call):
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
         assert pool.page_of(0, 0) == before[0][0][0]
     agrees(pool)
+
+
+def test_steps_of_a_beam_search(L):
+    """Beams that continue one another, through the allocator: whole pages by reference,
+    the last one copied to a page that was free, one more token each, and again."""
+    lens, B, rng = [100, 70, 64, 33], 4, torch.Generator().manual_seed(3)
+    case, pool = filled(L, lens, B, blocks=8, n_pages=24)
+    history = [[x[b].clone() for x in (case.k, case.v)] for b in range(B)]
+    for parents in ([1, 0, 0, 2], [3, 3, 1, 0], [0, 1, 2, 3], [2, 2, 2, 2], [1, 0, 3, 2]):
+        n = [history[p][0].shape[1] for p in parents]
+        before = L.KV16Cache(pool.k, pool.v, pool.n_tok.clone(), block_table=pool.block_table.clone())
+        for b in range(B):
+            pool.release_blocks(b, min(n[b], int(before.n_tok[b])) // 32)
+        for b in range(B):
+            pool.map_blocks(b, n[b] // 32 + 1)
+        L.kv16_fork(before, pool, i32(parents), 256)
+        k, v = (torch.randn((B, 2, 128), generator=rng).to(BF) for _ in range(2))
+        L.kv16_write(pool, k.cuda(), v.cuda(), i32([0, 1, 2, 3, 4]), pool.n_tok.clone())
+        history = [[torch.cat((x, y[b][:, None]), 1) for x, y in zip(history[p], (k, v))] for b, p in enumerate(parents)]
+        pool.page_of(0, 0)
+        agrees(pool)
+        assert L.device_status() == 0
+        for b in range(B):
+            for x, want in zip(("k", "v"), history[b]):
+                assert torch.equal(bits(R.tokens(pool, b, n[b] + 1, x).cpu()), bits(want))
