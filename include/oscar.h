@@ -481,7 +481,8 @@ oscar_status oscar_paged_decode_attention(const oscar_paged_cache* c, const floa
  * sequence's own rows.
  *
  * The device that is current is the one that a call runs on and that a
- * workspace's size is planned for: that of the cache's memory.
+ * workspace's size is planned for: that of the cache's memory.  Any host thread may
+ * call, several at once (on workspaces of their own).
  * ----------------------------------------------------------------------
  */
 #define OSCAR_KV16_BF16 0
@@ -609,17 +610,28 @@ size_t oscar_kv16_evict_workspace_bytes(const oscar_kv16_cache* src, int max_tok
  * group[i] .. group[i+1] - 1 are group i, whose first prefix[i] tokens are the
  * same ones.  The prefix's whole pages (tokens below 32 * (prefix[i] / 32)) are
  * read once for the group, from its first sequence's place in the cache, which
- * holds them whatever that sequence's length; the others' table entries
- * (contiguous: rows) for them are not used.  The rest of
+ * holds them whatever that sequence's length (one that is over keeps them for the
+ * others); the others' table entries (contiguous: rows) for them are not used.  The rest of
  * the prefix stands in every sequence's own pages, as oscar_kv16_fork leaves
  * it.  A sequence in no group shares nothing, and one with fewer tokens than
  * the prefix sees those that it has.
  *  group   device int32 [n_groups + 1], not decreasing, within [0, B]
  *  prefix  device int32 [n_groups], within [0, max_tok] and the capacity
  *  q, out, positions and visibility are those of oscar_kv16_decode_attention
+ *  max_tok  as there; it also decides between two ways, a block of the grid a row
+ *           (sequence and KV head) where the rows are few and max_tok small, else the
+ *           rows cut evenly: a bound far above the lengths takes the second, whose
+ *           cost for a few short sequences is about twice the first's.  A window
+ *           does not count here.
  * A group out of range is recorded in the status word and shares nothing.
+ * Rounding: the second way rounds each probability once to the cache's type for the
+ * product with the values, as oscar_kv16_attention does (relative distance of out from
+ * 64 bits 2.3e-3 in bf16, 2.9e-4 in fp16); the first and oscar_kv16_decode_attention
+ * keep what that leaves too (1.7e-3 and 2.1e-4).  Sums are of unrounded ones always.
  * workspace: oscar_kv16_shared_decode_workspace_bytes of device memory (no
- * initialisation).  Calls that use one workspace must not overlap on the GPU.
+ * initialisation): 2176 bytes for every row of out, 8.5 times what the row takes, and
+ * 272 KB for every SM where there is work for all.  Calls that use one workspace must
+ * not overlap on the GPU.
  * The work is cut evenly over the GPU, so where a row's sums are cut goes by the
  * whole batch's lengths: the same call gives the same bits, another batch may round
  * differently.
@@ -641,7 +653,8 @@ size_t oscar_kv16_shared_decode_workspace_bytes(const oscar_kv16_cache* c, int H
  * of each: q, start, out, lse, positions and visibility as there, groups as
  * above (a prefix may reach into the new tokens).  workspace:
  * oscar_kv16_shared_attention_workspace_bytes of device memory (no
- * initialisation), asked for with this call's numbers.  B <= 4096, n_groups <= 4096,
+ * initialisation, as much for a row), asked for with this call's numbers.  Always the
+ * second way.  B <= 4096, n_groups <= 4096,
  * total * Hq <= 63000000, and the last limit above with total in place of the first B
  * (else OSCAR_ERR_UNSUPPORTED).
  */

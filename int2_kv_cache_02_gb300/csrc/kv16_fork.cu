@@ -8,8 +8,8 @@
 // key's 16-byte pieces, lanes 16-31 the value's, eight tokens in flight, and ends:
 // the next unit's loads are another warp's, so none waits for these stores.
 //
-// Measured (GB300): 12 sequences of 6.6K to 16K tokens, 8 heads, with weights,
-// copied whole 177 us, 6.9 TB/s read and written (floor 182 at the rate of a plain
+// Measured (GB300): 12 copies of sequences of 7.8K to 16K tokens, 8 heads, with
+// weights, 178 us, 6.9 TB/s read and written (floor 182 at the rate of a plain
 // copy); 8 samples of an 8190-token prompt by reference 4.7 us, a step of 96 beams 5.6.
 #include <algorithm>
 

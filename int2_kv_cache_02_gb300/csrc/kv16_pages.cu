@@ -9,13 +9,13 @@
 // shared memory (a range of ids each), is set for every entry of the table; the
 // bits' counts, summed over threads and CTAs, give L and every id's rank among
 // the live or the free; a second pass over the table renames.  Latency bounds it:
-// two passes over the table and five barriers of the cluster.  Measured (GB300): 375
-// pages, 8 x 64 entries, with the copies of 95 pages of 4 heads 11.9 us a call among
-// others.  (A map in memory instead of the bits, one CTA that scans it, four
+// two passes over the table and six barriers of the cluster.  Measured (GB300): 344
+// live pages of 382, 8 x 64 entries, with the copies of 34 pages of 4 heads 11.4 to 12 us
+// a call among others.  (A map in memory instead of the bits, one CTA that scans it, four
 // launches: 15.1.)
 //
 // Copies.  A warp takes a (pair, KV head) and ends, so that no load waits for the
-// stores before it.  Bound by HBM: 8.7K pages of 8 heads, 1.14 GB read and written,
+// stores before it.  Bound by HBM: 4.4K pages of 8 heads, 1.14 GB read and written,
 // 165 us, 6.93 TB/s, a little above the rate of a plain copy.  (Warps that walk over
 // the pairs: 180.)
 #include <algorithm>

@@ -9,6 +9,7 @@
 // Probabilities are rounded to the type of V for the product, as in the prompt's
 // attention (the decode's own kernel keeps the remainder too: it has tensor time to
 // spare where 256 rows a key have not): half a step relative, as the output itself.
+// So the two ways of the decode differ in that; what they are off by stands in the header.
 //
 // What bounds it.  256 rows need 256 flops for each byte of keys and values; the GPU
 // has 287 for each byte that HBM delivers (both measured).  A group of fewer rows is
@@ -18,14 +19,14 @@
 // Measured (GB300, in a graph; in brackets the same by the calls that do not know of
 // groups).  Sixteen samples of an 8K prompt, 32/8 heads, 200 to 512 tokens each of
 // their own: 25 us [62] (floor 8.3; of the rest 6 pass before the first product, as
-// many after the last).  128 requests under four prompts of 8K to 16K, 0.2K to 2K
+// many after the last).  128 requests under four prompts of 10K to 16K, 0.2K to 2K
 // tokens each of their own: 158 us [780], 827 MB from HBM (floor 120).  128 requests
-// about two documents of 33K and 65K, 32/4 heads, fp16: 148 us [1590] (floor 65; the
+// about two documents of 54K and 66K, 32/4 heads, fp16: 148 us [1590] (floor 65; the
 // prefixes' 7.5K tiles of two query tiles take 1.65 us each, 0.79 of the measured bf16
 // rate, on 108 of the SMs, while the others read what the requests have of their own).
-// 48 sequences under four instructions of 6K, a window of 4K and 4 sinks, 24/2 heads,
-// fp16: 33 us [40] (floor 13; masked tiles of two query tiles take 3 us each).
-// 951 tokens of 16 questions behind two instructions of 4K to 8K: 127 us [181] (floor
+// 48 sequences under four instructions of 4.3K to 6K, a window of 4K and 4 sinks, 24/2
+// heads, fp16: 33 us [40] (floor 13; masked tiles of two query tiles take 3 us each).
+// 951 tokens of 16 questions behind two instructions of 7.7K and 8.2K: 128 us [181] (floor
 // 64, 20 of it the join of 30K rows).  112 drafted tokens of 32 samples of 32K: 84 us
 // [685] (floor 31).
 //

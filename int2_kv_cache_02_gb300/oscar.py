@@ -185,6 +185,8 @@ def _capturing(stream, device) -> bool:
     """Is `stream` (None: the device's current one) being captured into a graph?"""
     if device.type != "cuda":
         return False
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return torch.cuda.is_current_stream_capturing()
     with torch.cuda.device(device):
         if stream is None:
             return torch.cuda.is_current_stream_capturing()
@@ -798,8 +800,11 @@ def kv16_shared_decode_attention(cache: KV16Cache, q: torch.Tensor, group: torch
                                  n_sink: int = 0, stream=None):
     """kv16_decode_attention of sequences that share prefixes: sequences group[i]
     .. group[i+1] - 1 have their first prefix[i] tokens in common, whose whole
-    pages are read once for all of them, from the first one's place in the cache.
-    group int32 [n + 1], prefix int32 [n]."""
+    pages are read once for all of them, from the first one's place in the cache
+    (which has to keep them: release_blocks takes them from all).  group int32
+    [n + 1], prefix int32 [n].  A max_tok near the lengths lets small batches of
+    short sequences go the quicker way; it keeps more bits of the probabilities too,
+    as kv16_decode_attention does."""
     qp, qs, _, Hq = cache._rows(q, None, cache.B)
     w, wb = _bytes(workspace, cache)
     n = prefix.numel()
